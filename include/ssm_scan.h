@@ -414,6 +414,169 @@ ssm_status ssm_scan_bwd_workspace_size(const ssm_scan_bwd_params* p, size_t* byt
 /* Enqueue the backward pass described by `p` on `hip_stream`. */
 ssm_status ssm_scan_bwd(const ssm_scan_bwd_params* p, void* hip_stream);
 
+/*
+ * Gated delta rule: a matrix state H (dk, dv) per batch row and value head,
+ * with a scalar decay and a rank-one correction toward the new value. For
+ * every step t and value head h (reading key head h / (value_heads / key_heads)):
+ *
+ *   g_t    = A[h] * softplus(dt_raw[b,t,h] + dt_bias[h])      (log decay, A <= 0)
+ *   beta_t = beta_scale * sigmoid(beta_raw[b,t,h])
+ *   H'     = exp(g_t) H_{t-1}          (0 where reset[b,t] != 0)
+ *   u_t    = beta_t (v_t - H'^T k_t)
+ *   H_t    = H' + k_t u_t^T
+ *   out_t  = scale * H_t^T q_t
+ *
+ * with H_{-1} = h0 (zeros when absent). The step is a contraction when
+ * |k_t|^2 beta_t <= 2 (unit keys: ssm_qk_norm_fwd with SSM_NORM_L2 and no
+ * weight); other keys are computed as given.
+ *
+ *   batch, seqlen : B >= 0, 0 <= L < 2^27
+ *   key_heads     : Hk; value_heads : Hv, a multiple of Hk (Hk >= 1 unless Hv = 0)
+ *   dk            : 1 <= dk <= SSM_MAX_DSTATE;  dv : 1 <= dv <= 65536
+ *   in_dtype  : element type of q, k, v, dt_raw, beta_raw
+ *   q, k     (B,L,Hk,dk) required; v (B,L,Hv,dv) required. Heads are dense
+ *            inside a token; q_stride, k_stride, v_stride are the elements from
+ *            one token to the next (at least the token's own size; 0 = dense),
+ *            with batch rows L tokens apart, so slices of one packed projection
+ *            can be passed as they lie.
+ *   dt_raw, beta_raw (B,L,Hv) required; dt_bias (Hv) float32, NULL => 0
+ *   A        (Hv) float32, required; any real value is accepted, A <= 0 decays
+ *   reset    (B,L) uint8, NULL => none
+ *   h0       (B,Hv,dk,dv) float32, NULL => 0
+ *   out      (B,L,Hv,dv) required, out_dtype
+ *   h_last   (B,Hv,dk,dv) float32, NULL => not written
+ *   scale    : factor of the read-out; beta_scale : largest beta (1 for
+ *            sigmoid, 2 for the variant with negative eigenvalues)
+ *   workspace, workspace_bytes : at least ssm_delta_workspace_size() bytes,
+ *            aligned to 256; contents on entry ignored.
+ *   num_segments : 0 = the library chooses how many pieces to split L into;
+ *            k >= 1 asks for k pieces (clamped to what L allows).
+ * Arithmetic is float32 whatever in_dtype is; only out is rounded, to out_dtype.
+ * Outputs must not overlap inputs, each other or the workspace.
+ */
+typedef struct {
+  int64_t batch, seqlen, key_heads, value_heads, dk, dv;
+  int32_t in_dtype, out_dtype;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const void* dt_raw;
+  const void* beta_raw;
+  const float* dt_bias;
+  const float* A;
+  const uint8_t* reset;
+  const float* h0;
+  void* out;
+  float* h_last;
+  void* workspace;
+  size_t workspace_bytes;
+  float scale, beta_scale;
+  int32_t num_segments;
+  int32_t reserved0; /* set to 0 */
+} ssm_delta_params;
+
+/* Bytes of workspace ssm_delta_fwd needs (sizes, dtypes and num_segments are
+ * read; pointers are not). */
+ssm_status ssm_delta_workspace_size(const ssm_delta_params* p, size_t* bytes);
+
+/* Enqueue the whole-sequence gated delta rule described by `p` on `hip_stream`. */
+ssm_status ssm_delta_fwd(const ssm_delta_params* p, void* hip_stream);
+
+/*
+ * The same recurrence over a window of `tokens` steps (one for ordinary
+ * decoding, a few for drafted tokens), with the state updated in place and
+ * held on chip through the window. No workspace.
+ *   h        (B,Hv,dk,dv) float32, required; read as H_{t-1}, overwritten
+ *   q, k     (B,T,Hk,dk), v, out (B,T,Hv,dv), dt_raw, beta_raw (B,T,Hv); strides as
+ *            in ssm_delta_params. T = 0 leaves h as it is.
+ */
+typedef struct {
+  int64_t batch, tokens, key_heads, value_heads, dk, dv;
+  int32_t in_dtype, out_dtype;
+  float* h;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const void* dt_raw;
+  const void* beta_raw;
+  const float* dt_bias;
+  const float* A;
+  void* out;
+  float scale, beta_scale;
+} ssm_delta_update_params;
+
+/* Enqueue the decode window described by `p` on `hip_stream`. */
+ssm_status ssm_delta_update(const ssm_delta_update_params* p, void* hip_stream);
+
+/*
+ * Norms of queries and keys for each head, with the position rotation in the
+ * same pass. For every token and every head x (head_dim entries) of q and k:
+ *
+ *   r = (sum x^2 + eps)^-1/2 (SSM_NORM_L2) or (mean x^2 + eps)^-1/2 (SSM_NORM_RMS)
+ *   y = w * (x r)
+ *   out = y with its first rot_dim entries turned: for pair i < rot_dim / 2,
+ *         (a, b) -> (a c - b s, b c + a s), c = cos[p][i], s = sin[p][i],
+ *         (a, b) = entries (i, i + rot_dim/2), or (2i, 2i+1) with interleaved
+ *
+ * p is the token's position. Sums and factors are float32.
+ *   batch, seqlen, q_heads, k_heads : sizes >= 0
+ *   head_dim  : 1 <= head_dim <= 256; rot_dim : even, 0 <= rot_dim <= head_dim
+ *   q (B,L,q_heads,head_dim), k (B,L,k_heads,head_dim) in_dtype; q_stride,
+ *            k_stride as in ssm_delta_params
+ *   wq, wk   (head_dim) float32, NULL => 1
+ *   cos, sin (rot_positions, rot_dim/2) float32, required when rot_dim > 0
+ *   positions (B,L) int32, NULL => t. A position outside [0, rot_positions)
+ *            makes the turned entries of its token NaN (nothing is read there).
+ *   q_out, k_out : as q and k, dense, out_dtype; ssm_qk_norm_bwd reads them not
+ * ssm_qk_norm_bwd, gradients of  loss = sum dq_out * q_out + sum dk_out * k_out:
+ *   dz = the inverse rotation of the output's gradient,  dw = sum dz * (x r),
+ *   dx = r (w dz - (x r) s (w dz . x r)),  s = 1 (L2) or 1 / head_dim (RMS)
+ *   dq_out, dk_out (dense, in_dtype) required; dq, dk (dense, out_dtype) required;
+ *   dwq, dwk (head_dim) float32, NULL => not written: sums in a fixed order
+ *   workspace, workspace_bytes : at least ssm_qk_norm_bwd_workspace_size() bytes,
+ *            aligned to 16 (the forward needs none)
+ */
+typedef enum { SSM_NORM_RMS = 0, SSM_NORM_L2 = 1 } ssm_norm_kind;
+#define SSM_MAX_HEAD_DIM 256
+
+typedef struct {
+  int64_t batch, seqlen, q_heads, k_heads, head_dim, rot_dim, rot_positions;
+  int32_t in_dtype, out_dtype;
+  const void* q;
+  const void* k;
+  int64_t q_stride, k_stride;
+  const float* wq;
+  const float* wk;
+  const float* cos;
+  const float* sin;
+  const int32_t* positions;
+  void* q_out;
+  void* k_out;
+  const void* dq_out;
+  const void* dk_out;
+  void* dq;
+  void* dk;
+  float* dwq;
+  float* dwk;
+  void* workspace;
+  size_t workspace_bytes;
+  float eps;
+  int32_t norm_kind;   /* ssm_norm_kind */
+  int32_t interleaved; /* 0: halves, 1: neighbours */
+  int32_t reserved0;   /* set to 0 */
+} ssm_qk_norm_params;
+
+/* Enqueue the norms and the rotation described by `p` on `hip_stream`. */
+ssm_status ssm_qk_norm_fwd(const ssm_qk_norm_params* p, void* hip_stream);
+
+/* Bytes of workspace ssm_qk_norm_bwd needs (sizes are read; pointers are not). */
+ssm_status ssm_qk_norm_bwd_workspace_size(const ssm_qk_norm_params* p, size_t* bytes);
+
+/* Enqueue the gradients described by `p` on `hip_stream`. */
+ssm_status ssm_qk_norm_bwd(const ssm_qk_norm_params* p, void* hip_stream);
+
 /* Static, human-readable name of a status code ("unknown status" otherwise). */
 const char* ssm_status_string(int32_t status);
 
@@ -426,7 +589,8 @@ int32_t ssm_version(void);
 
 /* sizeof of the parameter structs as compiled into the library:
  * which = 0 -> ssm_scan_params, 1 -> ssm_update_params,
- * 2 -> ssm_scan_bwd_params; 0 for anything else.
+ * 2 -> ssm_scan_bwd_params, 3 -> ssm_delta_params,
+ * 4 -> ssm_delta_update_params, 6 -> ssm_qk_norm_params; 0 for anything else.
  * Bindings compare these with their own layouts at load time. */
 size_t ssm_abi_struct_size(int32_t which);
 

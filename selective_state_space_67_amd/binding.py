@@ -85,7 +85,9 @@ EXPORTS = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_scan_fwd_noalloc", "s
            "ssm_scan_aggregate_workspace_size",
            "ssm_scan_aggregate",
            "ssm_state_update", "ssm_scan_bwd_workspace_size", "ssm_scan_bwd", "ssm_status_string", "ssm_last_error",
-           "ssm_version", "ssm_abi_struct_size")
+           "ssm_version", "ssm_abi_struct_size",
+           "ssm_delta_workspace_size", "ssm_delta_fwd", "ssm_delta_update", "ssm_qk_norm_fwd",
+           "ssm_qk_norm_bwd_workspace_size", "ssm_qk_norm_bwd")
 
 _lib = None
 
@@ -134,6 +136,9 @@ def load_library():
             lib.ssm_abi_struct_size(1) != ctypes.sizeof(UpdateParams) or \
             lib.ssm_abi_struct_size(2) != ctypes.sizeof(BwdParams):
         raise ImportError("libssmscan.so struct layout does not match this binding")
+    from . import binding_delta
+
+    binding_delta.declare(lib)
     _lib = lib
     return lib
 

@@ -4,7 +4,8 @@
 // touches the HIP runtime until all checks have passed, so invalid calls
 // return their status with no device-side effect (and can be exercised on a
 // machine without a GPU). The launches themselves live in scan_fwd.hip,
-// scan_bwd.hip and state_update.hip.
+// scan_bwd.hip and state_update.hip; the gated delta rule and the head norms
+// have their front end in api_delta.cpp.
 #include "ssm_scan.h"
 
 #include <hip/hip_runtime.h>
@@ -15,11 +16,14 @@
 #include <cstdio>
 #include <limits>
 
+#include "api_checks.h"
 #include "kernels.h"
 
-namespace {
+namespace ssm {
 
+namespace {
 thread_local char g_last_error[512] = "";
+}  // namespace
 
 ssm_status fail(ssm_status s, const char* fmt, ...) {
   va_list ap;
@@ -34,39 +38,27 @@ ssm_status ok() {
   return SSM_OK;
 }
 
-bool valid_dtype(int32_t t) { return t == SSM_F32 || t == SSM_BF16; }
+}  // namespace ssm
+
+namespace {
+
+using ssm::align256;
+using ssm::aligned;
+using ssm::dtype_size;
+using ssm::fail;
+using ssm::mul_ok;
+using ssm::ok;
+using ssm::overlaps;
+using ssm::Range;
+using ssm::range;
+using ssm::valid_dtype;
+
 bool valid_disc(int32_t t) { return t == SSM_DISC_DELTA_B || t == SSM_DISC_ZOH; }
 bool valid_kind(int32_t k) { return k == SSM_STATE_REAL || k == SSM_STATE_COMPLEX; }
 
 ssm_status check_kind(int32_t kind) {
   if (!valid_kind(kind)) return fail(SSM_ERR_UNSUPPORTED, "unknown state_kind %d", kind);
   return SSM_OK;
-}
-size_t dtype_size(int32_t t) { return t == SSM_BF16 ? 2 : 4; }
-
-// a * b without overflow for non-negative operands.
-bool mul_ok(int64_t a, int64_t b, int64_t* r) {
-  if (a != 0 && b > std::numeric_limits<int64_t>::max() / a) return false;
-  *r = a * b;
-  return true;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// A byte range [p, p + n) of one tensor; empty when p is null.
-struct Range {
-  const char* p;
-  size_t n;
-  const char* name;
-};
-
-bool overlaps(const Range& a, const Range& b) {
-  if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-  return a.p < b.p + b.n && b.p < a.p + a.n;
-}
-
-Range range(const void* p, int64_t count, size_t esize, const char* name) {
-  return Range{static_cast<const char*>(p), p ? static_cast<size_t>(count) * esize : 0, name};
 }
 
 // Sizes of a scan, checked for range and overflow.
@@ -269,8 +261,6 @@ struct BwdLayout {
   int64_t n_ck;       // 16-step checkpoints
   size_t off_agg, off_ckpt, off_segP, off_segG, off_part, off_uconv, off_duconv, off_convpart, total;
 };
-
-size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 ssm_status check_bwd_sizes(const ssm_scan_bwd_params* p, ScanSizes* sz) {
   ssm_scan_params f{};
@@ -869,7 +859,7 @@ const char* ssm_status_string(int32_t status) {
   }
 }
 
-const char* ssm_last_error(void) { return g_last_error; }
+const char* ssm_last_error(void) { return ssm::g_last_error; }
 
 int32_t ssm_version(void) { return SSM_SCAN_VERSION; }
 
@@ -877,6 +867,9 @@ size_t ssm_abi_struct_size(int32_t which) {
   if (which == 0) return sizeof(ssm_scan_params);
   if (which == 1) return sizeof(ssm_update_params);
   if (which == 2) return sizeof(ssm_scan_bwd_params);
+  if (which == 3) return sizeof(ssm_delta_params);
+  if (which == 4) return sizeof(ssm_delta_update_params);
+  if (which == 6) return sizeof(ssm_qk_norm_params);
   return 0;
 }
 

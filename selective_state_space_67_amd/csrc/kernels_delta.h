@@ -1,0 +1,68 @@
+// Host-side interface between the front end of the gated delta rule and the
+// head norms (api_delta.cpp) and their kernels (delta_step.hip, qk_norm.hip).
+// Not installed; not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "log.h"
+
+namespace ssm {
+
+// One gated delta rule launch after validation. Pointers are device pointers;
+// optional ones are nullptr. Token strides are in elements.
+struct DeltaPlan {
+  int64_t B, L;
+  int Hk, Hv, dk, dv;
+  int in_bf16, out_bf16;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t qs, ks, vs;
+  const void* dt;
+  const void* br;
+  const float* dt_bias;
+  const float* A;
+  const uint8_t* reset;
+  const float* h0;  // state before the first step, or null
+  void* out;
+  float* h_last;    // state after the last step, or null; may equal h0 in the decode window
+  float scale, beta_scale;
+};
+
+// The recurrence step by step with the state in registers (delta_step.hip).
+hipError_t launch_delta_steps(const DeltaPlan& plan, hipStream_t stream);
+
+// Norms and rotation (qk_norm.hip).
+struct NormPlan {
+  int64_t B, L, P;
+  int Hq, Hk, d, rot;
+  int in_bf16, out_bf16;
+  const void* q;
+  const void* k;
+  int64_t qs, ks;
+  const float* wq;
+  const float* wk;
+  const float* cos;
+  const float* sin;
+  const int32_t* positions;
+  void* q_out;
+  void* k_out;
+  const void* dq_out;  // backward
+  const void* dk_out;
+  void* dq;
+  void* dk;
+  float* dwq;
+  float* dwk;
+  float* part;  // norm_bwd_blocks() rows of 2 * d sums
+  float eps;
+  int l2, interleaved;
+};
+hipError_t launch_qk_norm(const NormPlan& plan, hipStream_t stream);
+// Workgroups of the backward pass: the rows of its partial sums.
+int norm_bwd_blocks(int64_t tokens, int heads, int d);
+hipError_t launch_qk_norm_bwd(const NormPlan& plan, hipStream_t stream);
+
+}  // namespace ssm

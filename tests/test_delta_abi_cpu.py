@@ -1,0 +1,181 @@
+"""Host-side checks of the delta-rule and head-norm entry points; no GPU needed.
+
+Fake, aligned, disjoint addresses: every call fails its checks or is an empty
+problem without outputs, so nothing is launched.
+"""
+import ctypes
+import os
+
+import pytest
+
+from selective_state_space_67_amd import binding as bd
+from selective_state_space_67_amd import binding_delta as bdd
+
+NULL, SHAPE, DTYPE, ALIGN, UNSUP, WORK, ALIAS = 1, 2, 3, 4, 5, 6, 7
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(bd.library_path()):
+        pytest.skip("libssmscan.so not built")
+    return bd.load_library()
+
+
+def fill(p, pointers):
+    """Consecutive megabytes for the named pointers."""
+    for i, name in enumerate(pointers):
+        setattr(p, name, 0x10000000 + (i << 20))
+    return p
+
+
+def delta(**kw):
+    p = bdd.DeltaParams(batch=2, seqlen=70, key_heads=2, value_heads=4, dk=16, dv=24, in_dtype=bd.SSM_BF16,
+                        out_dtype=bd.SSM_F32, scale=1.0, beta_scale=1.0)
+    fill(p, ("q", "k", "v", "dt_raw", "beta_raw", "dt_bias", "A", "reset", "h0", "out", "h_last", "workspace"))
+    p.workspace_bytes = 1 << 20
+    return put(p, kw)
+
+
+def update(**kw):
+    p = bdd.DeltaUpdateParams(batch=2, tokens=3, key_heads=2, value_heads=4, dk=16, dv=24, in_dtype=bd.SSM_BF16,
+                              out_dtype=bd.SSM_F32, scale=1.0, beta_scale=1.0)
+    fill(p, ("h", "q", "k", "v", "dt_raw", "beta_raw", "dt_bias", "A", "out"))
+    return put(p, kw)
+
+
+def norm(**kw):
+    p = bdd.QkNormParams(batch=2, seqlen=5, q_heads=3, k_heads=2, head_dim=32, rot_dim=16, rot_positions=40,
+                         in_dtype=bd.SSM_BF16, out_dtype=bd.SSM_F32, eps=1e-6, norm_kind=bdd.SSM_NORM_L2)
+    fill(p, ("q", "k", "wq", "wk", "cos", "sin", "positions", "q_out", "k_out", "dq_out", "dk_out", "dq", "dk", "dwq",
+             "dwk", "workspace"))
+    p.workspace_bytes = 1 << 20
+    return put(p, kw)
+
+
+def put(p, kw):
+    for k, v in kw.items():
+        assert hasattr(p, k), k
+        setattr(p, k, v)
+    return p
+
+
+def refused(lib, fn, p, status, word=""):
+    assert getattr(lib, fn)(ctypes.byref(p), None) == status, lib.ssm_last_error()
+    assert word.encode() in lib.ssm_last_error()
+
+
+def test_struct_sizes(lib):
+    for which, struct in bdd.STRUCTS.items():
+        assert lib.ssm_abi_struct_size(which) == ctypes.sizeof(struct)
+
+
+@pytest.mark.parametrize("fn,make,names", [
+    ("ssm_delta_fwd", delta, ("q", "k", "v", "dt_raw", "beta_raw", "A", "out")),
+    ("ssm_delta_update", update, ("h", "q", "k", "v", "dt_raw", "beta_raw", "A", "out")),
+    ("ssm_qk_norm_fwd", norm, ("q", "k", "q_out", "k_out", "cos", "sin")),
+    ("ssm_qk_norm_bwd", norm, ("q", "k", "dq_out", "dk_out", "dq", "dk", "cos", "sin")),
+])
+def test_required_pointers(lib, fn, make, names):
+    assert getattr(lib, fn)(None, None) == NULL
+    for name in names:
+        refused(lib, fn, make(**{name: None}), NULL, name)
+
+
+SIZES = [dict(batch=-1), dict(key_heads=3), dict(key_heads=0), dict(value_heads=-4), dict(dk=0), dict(dk=257),
+         dict(dv=0), dict(dv=65537), dict(value_heads=70000, key_heads=70000), dict(batch=2 ** 50), dict(q_stride=31),
+         dict(k_stride=-1), dict(v_stride=95), dict(q_stride=2 ** 60)]
+
+
+@pytest.mark.parametrize("kw", SIZES, ids=str)
+def test_delta_sizes(lib, kw):
+    refused(lib, "ssm_delta_fwd", delta(**kw), SHAPE)
+    refused(lib, "ssm_delta_update", update(**kw), SHAPE)
+    n = ctypes.c_size_t()
+    assert lib.ssm_delta_workspace_size(ctypes.byref(delta(**kw)), ctypes.byref(n)) == SHAPE
+
+
+def test_delta_lengths_and_pieces(lib):
+    refused(lib, "ssm_delta_fwd", delta(seqlen=1 << 27), SHAPE)
+    refused(lib, "ssm_delta_fwd", delta(seqlen=-1), SHAPE)
+    refused(lib, "ssm_delta_fwd", delta(num_segments=-1), SHAPE, "num_segments")
+    refused(lib, "ssm_delta_update", update(tokens=-1), SHAPE)
+
+
+@pytest.mark.parametrize("kw", [dict(head_dim=0), dict(head_dim=257, rot_dim=0), dict(rot_dim=15), dict(rot_dim=34),
+                                dict(rot_dim=-2), dict(batch=-1), dict(seqlen=1 << 27), dict(q_heads=70000),
+                                dict(rot_positions=-1), dict(q_stride=95), dict(k_stride=63), dict(batch=2 ** 50)],
+                         ids=str)
+def test_norm_sizes(lib, kw):
+    refused(lib, "ssm_qk_norm_fwd", norm(**kw), SHAPE)
+    refused(lib, "ssm_qk_norm_bwd", norm(**kw), SHAPE)
+
+
+def test_types_and_kinds(lib):
+    for fn, make in (("ssm_delta_fwd", delta), ("ssm_delta_update", update), ("ssm_qk_norm_fwd", norm),
+                     ("ssm_qk_norm_bwd", norm)):
+        refused(lib, fn, make(in_dtype=2), DTYPE)
+        refused(lib, fn, make(out_dtype=-1), DTYPE)
+    refused(lib, "ssm_qk_norm_fwd", norm(norm_kind=2), UNSUP, "norm_kind")
+
+
+def test_alignment(lib):
+    for name in ("q", "v", "beta_raw"):
+        refused(lib, "ssm_delta_fwd", delta(**{name: 0x50000001}), ALIGN, name)
+    for name in ("A", "dt_bias", "h0", "h_last", "out"):
+        refused(lib, "ssm_delta_fwd", delta(**{name: 0x50000002}), ALIGN, name)
+    refused(lib, "ssm_delta_update", update(h=0x50000002), ALIGN, "h")
+    refused(lib, "ssm_qk_norm_fwd", norm(positions=0x50000002), ALIGN, "positions")
+    refused(lib, "ssm_qk_norm_bwd", norm(workspace=0x50000004), ALIGN, "workspace")
+
+
+def test_overlaps(lib):
+    d = delta()
+    refused(lib, "ssm_delta_fwd", delta(out=d.v), ALIAS, "out overlaps v")
+    refused(lib, "ssm_delta_fwd", delta(h_last=d.h0), ALIAS, "h_last overlaps h0")
+    refused(lib, "ssm_delta_fwd", delta(h_last=d.out), ALIAS)
+    # a strided q reaches past its dense size
+    refused(lib, "ssm_delta_fwd", delta(q_stride=4000, out=d.q + 2 * 139 * 4000), ALIAS, "out overlaps q")
+    refused(lib, "ssm_delta_update", update(out=update().h), ALIAS)
+    refused(lib, "ssm_delta_update", update(h=update().k), ALIAS)
+    refused(lib, "ssm_qk_norm_fwd", norm(q_out=norm().q), ALIAS)
+    refused(lib, "ssm_qk_norm_bwd", norm(dk=norm().dk_out), ALIAS)
+    refused(lib, "ssm_qk_norm_bwd", norm(workspace=norm().dwk), ALIAS)
+
+
+def test_workspace(lib):
+    n = ctypes.c_size_t()
+    assert lib.ssm_qk_norm_bwd_workspace_size(ctypes.byref(norm()), ctypes.byref(n)) == 0 and n.value > 0
+    refused(lib, "ssm_qk_norm_bwd", norm(workspace_bytes=n.value - 1), WORK)
+    refused(lib, "ssm_qk_norm_bwd", norm(workspace=None), WORK)
+
+
+def test_empty_problems_need_no_pointers(lib):
+    none = {n: None for n in ("q", "k", "v", "dt_raw", "beta_raw", "A", "dt_bias", "reset", "h0", "out", "h_last")}
+    for kw in (dict(batch=0), dict(seqlen=0), dict(key_heads=0, value_heads=0)):
+        assert lib.ssm_delta_fwd(ctypes.byref(delta(**none, **kw)), None) == 0
+    none = {n: None for n in ("h", "q", "k", "v", "dt_raw", "beta_raw", "A", "out")}
+    assert lib.ssm_delta_update(ctypes.byref(update(**none, batch=0)), None) == 0
+    none = {n: None for n in ("q", "k", "cos", "sin", "q_out", "k_out", "wq", "wk", "positions")}
+    assert lib.ssm_qk_norm_fwd(ctypes.byref(norm(**none, batch=0)), None) == 0
+
+
+def test_binding_refusals():
+    """What the binding itself checks, before any call: shapes, layout, types."""
+    import torch
+
+    z = torch.zeros
+    q, v, g = z(1, 4, 2, 8), z(1, 4, 2, 6), z(1, 4, 2)
+    ok = dict(q=q, k=q, v=v, dt_raw=g, A=z(2), beta_raw=g)
+    check = lambda **kw: bdd._delta_inputs(**{**ok, "dt_bias": None, **kw})  # noqa: E731
+    check()
+    for bad in (dict(k=z(1, 4, 2, 9)), dict(dt_raw=z(1, 4, 3)), dict(A=z(3)), dict(q=q.transpose(2, 3)),
+                dict(v=z(1, 4, 4, 6)[:, :, ::2])):
+        with pytest.raises(ValueError):
+            check(**bad)
+    for bad in (dict(A=z(2, dtype=torch.float64)), dict(v=v.bfloat16())):
+        with pytest.raises(TypeError):
+            check(**bad)
+    packed = z(2, 4, 40)
+    assert bdd._tokens(packed[..., 3:19].unflatten(-1, (2, 8)), (2, 4, 2, 8), "q", torch.float32) == 40
+    with pytest.raises(ValueError):
+        bdd._norm_params(q, q, None, None, "max", 0.0, None, None, None, False)
