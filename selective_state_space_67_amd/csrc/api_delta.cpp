@@ -1,7 +1,7 @@
 // C-ABI front end of the gated delta rule and of the head norms
 // (include/ssm_scan.h). As in api.cpp, every check is host arithmetic on the
 // parameter struct and precedes the first HIP call. The launches live in
-// delta_step.hip and qk_norm.hip.
+// delta_step.hip, delta_chunk.hip and qk_norm.hip.
 #include <hip/hip_runtime.h>
 
 #include <limits>
@@ -139,8 +139,22 @@ ssm::DeltaPlan delta_plan(const P* p, int64_t len, const DeltaSizes& s) {
   return d;
 }
 
-ssm_status check_segments(const ssm_delta_params* p) {
+// Sequences up to this long go step by step, unless pieces are asked for.
+constexpr int64_t kStepsMax = 32;
+
+// How the forward runs: step by step (no chunks, no workspace) or in chunks.
+ssm_status plan_delta(const ssm_delta_params* p, const DeltaSizes& s, ssm::DeltaChunks* plan) {
   if (p->num_segments < 0) return fail(SSM_ERR_BAD_SHAPE, "num_segments must be >= 0");
+  *plan = ssm::DeltaChunks{};
+  if (s.empty() || (p->seqlen <= kStepsMax && p->num_segments <= 1)) return SSM_OK;
+  // one workgroup for every chunk, and at most four times a state's strips for every piece
+  const int64_t chunks = (p->seqlen + 63) / 64, bh = p->batch * p->value_heads;
+  int64_t blocks;
+  if (!mul_ok(bh, chunks, &blocks) || !mul_ok(blocks, (p->dv + SSM_MAX_DSTATE) / 16 + 2, &blocks) ||
+      blocks > std::numeric_limits<int32_t>::max())
+    return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
+  *plan = ssm::plan_delta_chunks(p->batch, p->seqlen, static_cast<int>(p->value_heads), static_cast<int>(p->dk),
+                                 static_cast<int>(p->dv), p->num_segments);
   return SSM_OK;
 }
 
@@ -221,8 +235,10 @@ ssm_status ssm_delta_workspace_size(const ssm_delta_params* p, size_t* bytes) {
   if (!p || !bytes) return fail(SSM_ERR_NULL_POINTER, "params or bytes is NULL");
   DeltaSizes s;
   ssm_status st = check_delta_sizes(p, p->seqlen, p->out_dtype, &s);
-  if (st != SSM_OK || (st = check_segments(p)) != SSM_OK) return st;
-  *bytes = 0;
+  if (st != SSM_OK) return st;
+  ssm::DeltaChunks plan;
+  if ((st = plan_delta(p, s, &plan)) != SSM_OK) return st;
+  *bytes = plan.bytes;
   return ok();
 }
 
@@ -230,7 +246,9 @@ ssm_status ssm_delta_fwd(const ssm_delta_params* p, void* hip_stream) {
   if (!p) return fail(SSM_ERR_NULL_POINTER, "params is NULL");
   DeltaSizes s;
   ssm_status st = check_delta_sizes(p, p->seqlen, p->out_dtype, &s);
-  if (st != SSM_OK || (st = check_segments(p)) != SSM_OK) return st;
+  if (st != SSM_OK) return st;
+  ssm::DeltaChunks chunks;
+  if ((st = plan_delta(p, s, &chunks)) != SSM_OK) return st;
   const size_t si = dtype_size(p->in_dtype), so = dtype_size(p->out_dtype);
   const Need needs[] = {
       {p->q, s.qk, si, "q", true},         {p->k, s.qk, si, "k", true},
@@ -238,20 +256,28 @@ ssm_status ssm_delta_fwd(const ssm_delta_params* p, void* hip_stream) {
       {p->beta_raw, s.gate, si, "beta_raw", true}, {p->A, s.gate, 4, "A", true},
       {p->out, s.vo, so, "out", true},     {p->dt_bias, 0, 4, "dt_bias", false},
       {p->h0, 0, 4, "h0", false},          {p->h_last, 0, 4, "h_last", false},
+      {p->workspace, 0, 256, "workspace", false},
   };
   if ((st = check_pointers(needs)) != SSM_OK) return st;
+  if (chunks.bytes > 0 && (!p->workspace || p->workspace_bytes < chunks.bytes))
+    return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", chunks.bytes,
+                p->workspace ? p->workspace_bytes : static_cast<size_t>(0));
   const Range in[] = {
       range(p->q, s.q, si, "q"), range(p->k, s.k, si, "k"), range(p->v, s.v, si, "v"),
       range(p->dt_raw, s.gate, si, "dt_raw"), range(p->beta_raw, s.gate, si, "beta_raw"),
       range(p->A, p->value_heads, 4, "A"), range(p->dt_bias, p->value_heads, 4, "dt_bias"),
       range(p->reset, s.tokens, 1, "reset"), range(p->h0, s.state, 4, "h0"),
   };
-  const Range out[] = {range(p->out, s.vo, so, "out"), range(p->h_last, s.state, 4, "h_last")};
+  const Range out[] = {
+      range(p->out, s.vo, so, "out"), range(p->h_last, s.state, 4, "h_last"),
+      Range{chunks.bytes ? static_cast<const char*>(p->workspace) : nullptr, chunks.bytes, "workspace"},
+  };
   if ((st = check_overlaps(in, out)) != SSM_OK) return st;
-  SSM_LOG("ssm_delta_fwd: B %lld L %lld heads %lld / %lld, dk %lld dv %lld, %s in, %s out, resets %d",
+  SSM_LOG("ssm_delta_fwd: B %lld L %lld heads %lld / %lld, dk %lld dv %lld, %s in, %s out, resets %d; %d chunks in %d "
+          "pieces, workspace %zu bytes",
           (long long)p->batch, (long long)p->seqlen, (long long)p->key_heads, (long long)p->value_heads,
           (long long)p->dk, (long long)p->dv, si == 2 ? "bf16" : "f32", so == 2 ? "bf16" : "f32",
-          p->reset != nullptr);
+          p->reset != nullptr, chunks.chunks, chunks.pieces, chunks.bytes);
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   if (s.empty()) {  // the state passes through an empty sequence
     const hipError_t e = ssm::launch_fill(p->h_last, p->h0, 0.0f, 0.0f, s.state, stream);
@@ -264,7 +290,8 @@ ssm_status ssm_delta_fwd(const ssm_delta_params* p, void* hip_stream) {
   plan.h0 = p->h0;
   plan.out = p->out;
   plan.h_last = p->h_last;
-  const hipError_t e = ssm::launch_delta_steps(plan, stream);
+  const hipError_t e = chunks.chunks > 0 ? ssm::launch_delta_chunks(plan, chunks, p->workspace, stream)
+                                         : ssm::launch_delta_steps(plan, stream);
   if (e != hipSuccess) return fail(SSM_ERR_HIP, "delta rule launch failed: %s", hipGetErrorString(e));
   return ok();
 }

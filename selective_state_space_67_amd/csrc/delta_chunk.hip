@@ -1,0 +1,619 @@
+// Gated delta rule in chunks of 64 tokens, forward.
+//
+// Within a chunk that starts from the state H0, with G_i the sum of log decays
+// through token i, M_ij = exp(G_i - G_j) for j <= i of the same document (else 0)
+// and e0, eC, aC the decays from the start, to the end and across (delta_mfma.h):
+//
+//   A_ij = beta_i M_ij (k_i . k_j), j < i        T = (I + A)^-1
+//   U    = T R,    R = beta (V - e0 (K H0))      (the rows u_t of the recurrence)
+//   out  = scale (e0 (Q H0) + P U),   P = M o (Q K^T)
+//   H1   = aC H0 + K^T (eC U)
+//
+// Two launches. delta_chunk_prepare computes T and P of all chunks in parallel
+// (they do not depend on the state). delta_chunk_scan then walks the chunks in
+// order; columns of the state are independent, so a wave owns 16 of them for one
+// head and keeps the state, R and U in registers (delta_mfma.h: a product's result
+// is the next one's operand as it lies). The waves of a workgroup share only the
+// staged tokens of K and Q.
+//
+// A long sequence on few heads is split into pieces: a first walk finds each
+// piece's effect on the state, which is affine, H -> M H + N (the columns of M
+// are a walk from the identity without values); delta_fold carries the state
+// across the pieces, and the full walk starts every piece from its own state.
+#include <algorithm>
+
+#include "delta_chunk.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {  // 16 x 16 x 16 in float32
+#pragma unroll
+  for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
+  return c;
+}
+
+struct ChunkGates {
+  float hi[64], lo[64];  // G in log2 units, as a sum of two floats
+  float beta[64];
+  int seg[64];           // documents started in the chunk up to the token
+};
+
+// One wave, a lane per token. The sums are taken in double and kept in two floats,
+// so that differences of them keep a small decay's precision next to large ones.
+template <typename InT>
+__device__ __forceinline__ void chunk_gates(const ChunkArgs& a, int b, int h, int chunk, int64_t record, int lane,
+                                            ChunkGates* s) {
+  const int64_t t = static_cast<int64_t>(chunk) * kChunk + lane;
+  const bool valid = t < a.L;
+  double g = 0.0;
+  float beta = 0.0f;
+  bool start = false;
+  if (valid) {
+    const int64_t i = (static_cast<int64_t>(b) * a.L + t) * a.Hv + h;
+    const float delta = softplus_f32(load_elem(static_cast<const InT*>(a.dt), i) + (a.dt_bias ? a.dt_bias[h] : 0.0f));
+    beta = a.beta_scale * fast_rcp(1.0f + fast_exp2(-load_elem(static_cast<const InT*>(a.br), i) * kLog2e));
+    start = a.reset && a.reset[static_cast<int64_t>(b) * a.L + t];
+    // a step's decay below 2^-16384 is 0 in float32 whatever its exponent
+    if (!start) g = fmax(static_cast<double>(a.A[h]) * delta * 1.4426950408889634, -16384.0);
+  }
+  const uint64_t starts = __ballot(start);
+  const int seg = __popcll(starts & (~uint64_t{0} >> (63 - lane)));
+  bool cut = start;
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) {
+    const double before = __shfl_up(g, off);
+    const bool cut_before = __shfl_up(static_cast<int>(cut), off);
+    if (lane >= off) {
+      if (!cut) g += before;
+      cut = cut || cut_before;
+    }
+  }
+  const double last = __shfl(g, 63);
+  const int seg_last = __popcll(starts);
+  const float hi = static_cast<float>(g);
+  s->hi[lane] = hi;
+  s->lo[lane] = static_cast<float>(g - hi);
+  s->beta[lane] = beta;
+  s->seg[lane] = seg;
+  float* out = a.gates + record * kGateFloats;
+  out[kE0 + lane] = seg == 0 ? fast_exp2(static_cast<float>(g)) : 0.0f;
+  out[kEC + lane] = seg == seg_last ? fast_exp2(static_cast<float>(last - g)) : 0.0f;
+  out[kBeta + lane] = beta;
+  if (lane == 63) out[kAC] = seg == 0 ? fast_exp2(static_cast<float>(g)) : 0.0f;
+}
+
+__device__ __forceinline__ float pair_decay(const ChunkGates& s, int i, int j) {
+  const float d = (s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j]);
+  return s.seg[i] == s.seg[j] ? fast_exp2(d) : 0.0f;
+}
+
+// T, P (or T^T, P^T) and the scalars of one chunk of one head. Four waves; wave w
+// makes row tile w of the 4 x 4 tiles of 16 tokens (and column tile w for the
+// transposes).
+//
+// The triangular inverse is exact substitution, block by block: each 16 x 16
+// diagonal block by forward substitution in float32, then, down a row,
+//   T_ij = -(sum_{k=j+1..i} T_ik A_kj) T_jj
+// with float32 matrix instructions. All blocks are used in the layout in which
+// they were produced: the transposed products T_ij^T = -T_jj^T sum A_kj^T T_ik^T
+// take A_kj as it came out of K K^T.
+template <typename InT, int NP, int KS, bool VEC, bool BWD>
+__global__ __launch_bounds__(kThreads) void delta_chunk_prepare(const ChunkArgs a) {
+  using Tile = TokenTile<NP, KS>;
+  extern __shared__ uint16_t staged[];
+  uint16_t* sk = staged;
+  uint16_t* sq = staged + NP * Tile::kPart;
+  __shared__ ChunkGates gates;
+  __shared__ float diag[4][16][20];  // A_ii, then T_ii; rows of 16 padded to 20
+  const int lane = threadIdx.x % 64, g4 = (lane >> 4) * 4, col = lane & 15;
+  const int w = wave_index();
+  const int64_t record = blockIdx.x;
+  const int bh = static_cast<int>(record / a.chunks), chunk = static_cast<int>(record - static_cast<int64_t>(bh) * a.chunks);
+  const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / a.group;
+  const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(chunk) * kChunk;
+  const int n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(chunk) * kChunk));
+  const InT* q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
+  const InT* k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
+
+  if (w == 0) chunk_gates<InT>(a, b, h, chunk, record, lane, &gates);
+
+  // S[k][j]: rows k, columns j (j < k <= w, and the diagonal k = j = w); with BWD
+  // also R[k][i]: rows k, columns i (w <= k < i). P[j]: rows j, columns w;
+  // with BWD rows j >= w of Q, columns w of K.
+  f32x4 S[4][4] = {}, R[4][4] = {}, P[4] = {};
+  for (int d0 = 0; d0 < a.dk; d0 += 32 * KS) {
+    if (d0 > 0) __syncthreads();
+    stage_tokens<InT, NP, KS, VEC, kThreads>(sk, k, a.ks, n_tokens, d0, a.dk);
+    stage_tokens<InT, NP, KS, VEC, kThreads>(sq, q, a.qs, n_tokens, d0, a.dk);
+    __syncthreads();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      Frag<NP> kf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kf[i] = Tile::rows(sk, i, ks, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < i; ++j) {
+          if (i <= w) S[i][j] = mma(kf[i], kf[j], S[i][j]);
+          if (BWD && j >= w) R[j][i] = mma(kf[j], kf[i], R[j][i]);
+        }
+        if (i == w) S[i][i] = mma(kf[i], kf[i], S[i][i]);
+      }
+      if constexpr (BWD) {
+        const Frag<NP> kw = Tile::rows(sk, w, ks, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i >= w) P[i] = mma(Tile::rows(sq, i, ks, lane), kw, P[i]);
+      } else {
+        const Frag<NP> qw = Tile::rows(sq, w, ks, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j <= w) P[j] = mma(kf[j], qw, P[j]);
+      }
+    }
+  }
+
+  // Decays and betas.
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j <= i; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if ((j < i && i <= w) || (j == i && i == w)) {
+          const int row = i * 16 + g4 + r, c = j * 16 + col;
+          S[i][j][r] = row > c ? gates.beta[row] * pair_decay(gates, row, c) * S[i][j][r] : 0.0f;
+        }
+        if (BWD && j < i && j >= w) {
+          const int row = j * 16 + g4 + r, c = i * 16 + col;  // A_ci,row of the system, transposed
+          R[j][i][r] = gates.beta[c] * pair_decay(gates, c, row) * R[j][i][r];
+        }
+      }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (BWD ? j < w : j > w) continue;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int x = j * 16 + g4 + r, y = w * 16 + col;
+      const int i = BWD ? x : y, jj = BWD ? y : x;
+      P[j][r] = i >= jj ? pair_decay(gates, i, jj) * P[j][r] : 0.0f;
+    }
+  }
+
+  // The diagonal block: lane c of the first 16 makes column c of its inverse.
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i == w)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) diag[w][g4 + r][col] = S[i][i][r];
+  __syncthreads();
+  float x[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    float v = r == col ? 1.0f : 0.0f;
+#pragma unroll
+    for (int m = 0; m < r; ++m) v = __builtin_fmaf(-diag[w][r][m], x[m], v);
+    x[r] = v;
+  }
+  __syncthreads();
+  if (lane < 16)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) diag[w][r][col] = x[r];
+  __syncthreads();
+
+  // Row w, right to left: Tr[j] = T_wj^T (rows j, columns w).
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 Tr[4] = {zero, zero, zero, zero};
+#pragma unroll
+  for (int j = 3; j >= 0; --j) {
+    if (j == w) Tr[j] = *reinterpret_cast<const f32x4*>(&diag[j][col][g4]);
+    if (j >= w) continue;
+    f32x4 sum = zero;
+#pragma unroll
+    for (int i = j + 1; i < 4; ++i)
+      if (i <= w) sum = mfma4(S[i][j], Tr[i], sum);
+    f32x4 t;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) t[r] = -diag[j][g4 + r][col];
+    Tr[j] = mfma4(t, sum, zero);
+  }
+  uint16_t* T = a.T + record * kTriEntries;
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+    if (ks <= w / 2) store_tri(T, tri_index(w, ks), lane, split8(Tr[2 * ks], Tr[2 * ks + 1]));
+  if constexpr (!BWD) {
+    uint16_t* Pm = a.P + record * kTriEntries;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+      if (ks <= w / 2) store_tri(Pm, tri_index(w, ks), lane, split8(P[2 * ks], P[2 * ks + 1]));
+  } else {
+    // Column w, top to bottom: Tc[i] = T_iw (rows i, columns w).
+    f32x4 Tc[4] = {zero, zero, zero, zero};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i == w)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) Tc[i][r] = diag[i][g4 + r][col];
+      if (i <= w) continue;
+      f32x4 sum = zero;
+#pragma unroll
+      for (int m = 0; m < i; ++m)
+        if (m >= w) sum = mfma4(R[m][i], Tc[m], sum);
+      const f32x4 t = *reinterpret_cast<const f32x4*>(&diag[i][col][g4]);
+      Tc[i] = mfma4(-t, sum, zero);
+    }
+    uint16_t* Tt = a.Tt + record * kTriEntries;
+    uint16_t* Pt = a.Pt + record * kTriEntries;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+      if (ks >= w / 2) {
+        store_tri(Tt, tri_t_index(w, ks), lane, split8(Tc[2 * ks], Tc[2 * ks + 1]));
+        store_tri(Pt, tri_t_index(w, ks), lane, split8(P[2 * ks], P[2 * ks + 1]));
+      }
+  }
+}
+
+template <typename InT, int NP, int KS, bool VEC>
+hipError_t prepare_ks(const ChunkArgs& a, int64_t blocks, bool bwd, hipStream_t stream) {
+  const size_t lds = 2 * TokenTile<NP, KS>::kBytes;
+  SSM_LOG("launch delta_chunk_prepare<%d parts, %d entries a pass>: backward %d; grid %lld x %d threads", NP, 32 * KS,
+          bwd, static_cast<long long>(blocks), kThreads);
+  if (bwd)
+    hipLaunchKernelGGL((delta_chunk_prepare<InT, NP, KS, VEC, true>), dim3(static_cast<unsigned>(blocks)),
+                       dim3(kThreads), lds, stream, a);
+  else
+    hipLaunchKernelGGL((delta_chunk_prepare<InT, NP, KS, VEC, false>), dim3(static_cast<unsigned>(blocks)),
+                       dim3(kThreads), lds, stream, a);
+  return hipGetLastError();
+}
+
+template <typename InT, int NP, bool VEC>
+hipError_t prepare_vec(const ChunkArgs& a, int64_t blocks, bool bwd, hipStream_t stream) {
+  if (a.dk <= 32) return prepare_ks<InT, NP, 1, VEC>(a, blocks, bwd, stream);
+  if (a.dk <= 64 || NP == 3) return prepare_ks<InT, NP, 2, VEC>(a, blocks, bwd, stream);
+  return prepare_ks<InT, NP, NP == 1 ? 4 : 2, VEC>(a, blocks, bwd, stream);
+}
+
+// ---- the walk over the chunks ----
+
+struct ScanArgs {
+  ChunkArgs c;
+  int pieces, chunks_piece;
+  int col_blocks;   // workgroups per (head, piece)
+  int out_bf16;
+  const float* h0;  // (bh, dk, dv) or null
+  const float* starts;  // states of pieces 1 .. (bh, piece, 32 KS, cols), or null
+  float* agg;       // aggregates walk: (bh, piece, 32 KS, 32 KS + cols)
+  int cols;         // dv rounded up to 16
+  void* out;
+  float* h_last;
+};
+
+// One wave's walk over the chunks of a piece with 16 columns of the state.
+// AGG: the aggregates walk (no read-out; the first 32 KS columns start from the identity).
+template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS>
+__global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
+  using Tile = TokenTile<NP, KS>;
+  constexpr int DKT = 2 * KS;  // row tiles of the state
+  extern __shared__ uint16_t staged[];
+  uint16_t* sk = staged;
+  uint16_t* sq = staged + NP * Tile::kPart;
+  __shared__ float gates[kGateFloats];
+  const ChunkArgs& a = s.c;
+  const int lane = threadIdx.x % 64, wave = wave_index(), g4 = (lane >> 4) * 4;
+  const int cb = blockIdx.x % s.col_blocks, rest = blockIdx.x / s.col_blocks;
+  const int piece = rest % s.pieces, bh = rest / s.pieces;
+  const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / a.group;
+  const int strip = cb * (kThreads / 64) + wave;      // 16-column strip
+  const int own = (AGG ? strip - DKT : strip) * 16 + (lane & 15);  // column of v
+  const bool has_v = own >= 0 && own < a.dv;
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+
+  f32x4 H[DKT];
+#pragma unroll
+  for (int m = 0; m < DKT; ++m) {
+    H[m] = zero;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = m * 16 + g4 + r;
+      if (AGG) {
+        if (strip * 16 + (lane & 15) == row) H[m][r] = 1.0f;
+      } else if (piece > 0) {
+        if (own < s.cols)
+          H[m][r] = s.starts[((static_cast<int64_t>(bh) * s.pieces + piece) * (32 * KS) + row) * s.cols + own];
+      } else if (s.h0 && row < a.dk && has_v) {
+        H[m][r] = s.h0[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own];
+      }
+    }
+  }
+
+  const int c1 = min(a.chunks, (piece + 1) * s.chunks_piece);
+  for (int c = piece * s.chunks_piece; c < c1; ++c) {
+    const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk;
+    const int n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(c) * kChunk));
+    const int64_t record = static_cast<int64_t>(bh) * a.chunks + c;
+    const InT* q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
+    const InT* k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
+    const InT* v = static_cast<const InT*>(a.v) + t0 * a.vs + static_cast<int64_t>(h) * a.dv + own;
+    __syncthreads();  // the previous chunk's tiles are read
+    stage_tokens<InT, NP, KS, VEC, kThreads>(sk, k, a.ks, n_tokens, 0, a.dk);
+    if constexpr (!AGG && QLDS) stage_tokens<InT, NP, KS, VEC, kThreads>(sq, q, a.qs, n_tokens, 0, a.dk);
+    gates[threadIdx.x] = a.gates[record * kGateFloats + threadIdx.x];
+    f32x4 V[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int token = m * 16 + g4 + r;
+        V[m][r] = has_v && token < n_tokens ? load_elem(v, token * a.vs) : 0.0f;
+      }
+    __syncthreads();
+
+    f32x4 X[4] = {zero, zero, zero, zero}, Y[4] = {zero, zero, zero, zero};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const Frag<3> hb = split8(H[2 * ks], H[2 * ks + 1]);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        X[m] = mma(Tile::rows(sk, m, ks, lane), hb, X[m]);
+        if constexpr (!AGG) {
+          if constexpr (QLDS)
+            Y[m] = mma(Tile::rows(sq, m, ks, lane), hb, Y[m]);
+          else
+            Y[m] = mma(rows_from_global<InT, NP, VEC>(q, a.qs, n_tokens, a.dk, m, ks, lane), hb, Y[m]);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const f32x4 e0 = *reinterpret_cast<const f32x4*>(gates + kE0 + m * 16 + g4);
+      const f32x4 be = *reinterpret_cast<const f32x4*>(gates + kBeta + m * 16 + g4);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        X[m][r] = be[r] * __builtin_fmaf(-e0[r], X[m][r], V[m][r]);
+        Y[m][r] *= e0[r];
+      }
+    }
+    f32x4 U[4];
+    {
+      const Frag<3> rb[2] = {split8(X[0], X[1]), split8(X[2], X[3])};
+      const uint16_t* T = a.T + record * kTriEntries;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        U[m] = zero;
+#pragma unroll
+        for (int ks = 0; ks <= m / 2; ++ks) U[m] = mma(load_tri(T, tri_index(m, ks), lane), rb[ks], U[m]);
+      }
+    }
+    if constexpr (!AGG) {
+      const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
+      const uint16_t* P = a.P + record * kTriEntries;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+#pragma unroll
+        for (int ks = 0; ks <= m / 2; ++ks) Y[m] = mma(load_tri(P, tri_index(m, ks), lane), ub[ks], Y[m]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int token = m * 16 + g4 + r;
+          if (!has_v || token >= n_tokens) continue;
+          const int64_t o = ((t0 + token) * a.Hv + h) * a.dv + own;
+          if (s.out_bf16)
+            store_elem(static_cast<bf16_t*>(s.out), o, a.scale * Y[m][r]);
+          else
+            store_elem(static_cast<float*>(s.out), o, a.scale * Y[m][r]);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const f32x4 eC = *reinterpret_cast<const f32x4*>(gates + kEC + m * 16 + g4);
+      U[m] *= eC;
+    }
+    const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
+    const float aC = gates[kAC];
+#pragma unroll
+    for (int m = 0; m < DKT; ++m) {
+      H[m] *= aC;
+#pragma unroll
+      for (int ts = 0; ts < 2; ++ts) H[m] = mma(Tile::columns(sk, m, ts, lane), ub[ts], H[m]);
+    }
+  }
+
+  if (AGG) {
+    const int width = 32 * KS + s.cols, at = strip * 16 + (lane & 15);
+    if (at >= width) return;
+    float* dst = s.agg + (static_cast<int64_t>(bh) * s.pieces + piece) * (32 * KS) * width + at;
+#pragma unroll
+    for (int m = 0; m < DKT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dst[static_cast<int64_t>(m * 16 + g4 + r) * width] = H[m][r];
+  } else if (s.h_last && c1 == a.chunks && has_v) {
+#pragma unroll
+    for (int m = 0; m < DKT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = m * 16 + g4 + r;
+        if (row < a.dk) s.h_last[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own] = H[m][r];
+      }
+  }
+}
+
+// The states that pieces 1 .. start from: S <- M S + N over the pieces, 16 columns
+// and all rows a workgroup, its waves sharing the rows. The next piece's
+// operands are loaded before the current ones are used.
+struct FoldArgs {
+  const float* agg;
+  const float* h0;
+  float* starts;
+  int pieces, dk, dv, cols, strips;
+};
+
+template <int KS>
+__global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
+  constexpr int ROWS = 32 * KS;
+  __shared__ u32x4 S[2][KS][3][64];  // the state as B operand, two pieces in turn
+  const int lane = threadIdx.x % 64, w = wave_index(), g4 = (lane >> 4) * 4;  // wave w: rows 16 w ..
+  const int bh = blockIdx.x / a.strips, own = (blockIdx.x - bh * a.strips) * 16 + (lane & 15);
+  const int width = ROWS + a.cols;
+  f32x4 H;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = w * 16 + g4 + r;
+    H[r] = a.h0 && row < a.dk && own < a.dv ? a.h0[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own] : 0.0f;
+  }
+  const float* M = a.agg + static_cast<int64_t>(bh) * a.pieces * ROWS * width;
+  f32x4 m[KS][2], n;
+  const auto fetch = [&](int piece) {
+    const float* p = M + static_cast<int64_t>(piece) * ROWS * width;
+    const float* row = p + static_cast<int64_t>(w * 16 + (lane & 15)) * width + g4;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      m[ks][0] = *reinterpret_cast<const f32x4*>(row + 32 * ks);
+      m[ks][1] = *reinterpret_cast<const f32x4*>(row + 32 * ks + 16);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) n[r] = p[static_cast<int64_t>(w * 16 + g4 + r) * width + ROWS + own];
+  };
+  fetch(0);
+  for (int piece = 0; piece + 1 < a.pieces; ++piece) {
+    // half of operand w / 2: rows 16 w .. are its entries 16 (w % 2) ..
+    uint32_t lo[3], hi[3];
+    split_pair(H.x, H.y, lo);
+    split_pair(H.z, H.w, hi);
+    const int buf = piece & 1;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      reinterpret_cast<u32x2*>(&S[buf][w / 2][i][lane])[w % 2] = u32x2{lo[i], hi[i]};
+    Frag<3> mf[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) mf[ks] = split8(m[ks][0], m[ks][1]);
+    H = n;
+    if (piece + 2 < a.pieces) fetch(piece + 1);
+    __syncthreads();  // one barrier a piece: the other buffer was last read before the previous one
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      Frag<3> sb;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) sb.p[i] = S[buf][ks][i][lane];
+      H = mma(mf[ks], sb, H);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      a.starts[((static_cast<int64_t>(bh) * a.pieces + piece + 1) * ROWS + w * 16 + g4 + r) * a.cols + own] = H[r];
+  }
+}
+
+int padded_ks(int dk) { return dk <= 32 ? 1 : dk <= 64 ? 2 : dk <= 128 ? 4 : 8; }
+
+template <typename InT, int NP, int KS, bool VEC>
+hipError_t launch_scan_ks(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs s, hipStream_t stream) {
+  constexpr int kWaves = kThreads / 64;
+  // K and Q of a chunk side by side fit in LDS except for float32 past 128 entries
+  constexpr bool QLDS = 2 * TokenTile<NP, KS>::kBytes <= 128 * 1024;
+  const int64_t heads = p.B * p.Hv;
+  if (plan.pieces > 1) {
+    const int strips = 2 * KS + s.cols / 16;
+    s.col_blocks = (strips + kWaves - 1) / kWaves;
+    const int64_t blocks = heads * plan.pieces * s.col_blocks;
+    constexpr size_t agg_lds = TokenTile<NP, KS>::kBytes;
+    SSM_LOG("launch delta_chunk_scan<%d parts, %d rows, aggregates>: %d pieces; grid %lld x %d threads", NP, 32 * KS,
+            plan.pieces, static_cast<long long>(blocks), kThreads);
+    hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, VEC, true, false>), dim3(static_cast<unsigned>(blocks)),
+                       dim3(kThreads), agg_lds, stream, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    FoldArgs f{s.agg, s.h0, const_cast<float*>(s.starts), plan.pieces, p.dk, p.dv, s.cols, s.cols / 16};
+    SSM_LOG("launch delta_fold<%d rows>: grid %lld x %d threads", 32 * KS, static_cast<long long>(heads * f.strips),
+            2 * KS * 64);
+    hipLaunchKernelGGL((delta_fold<KS>), dim3(static_cast<unsigned>(heads * f.strips)), dim3(2 * KS * 64), 0, stream, f);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  const int strips = s.cols / 16;
+  s.col_blocks = (strips + kWaves - 1) / kWaves;
+  const int64_t blocks = heads * plan.pieces * s.col_blocks;
+  const size_t lds = (QLDS ? 2 : 1) * TokenTile<NP, KS>::kBytes;
+  SSM_LOG("launch delta_chunk_scan<%d parts, %d rows>: %d pieces of %d chunks; grid %lld x %d threads", NP, 32 * KS,
+          plan.pieces, plan.chunks_piece, static_cast<long long>(blocks), kThreads);
+  hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, VEC, false, QLDS>), dim3(static_cast<unsigned>(blocks)),
+                     dim3(kThreads), lds, stream, s);
+  return hipGetLastError();
+}
+
+template <typename InT, int NP, bool VEC>
+hipError_t launch_scan_vec(const DeltaPlan& p, const DeltaChunks& plan, const ScanArgs& s, hipStream_t stream) {
+  switch (padded_ks(p.dk)) {
+    case 1: return launch_scan_ks<InT, NP, 1, VEC>(p, plan, s, stream);
+    case 2: return launch_scan_ks<InT, NP, 2, VEC>(p, plan, s, stream);
+    case 4: return launch_scan_ks<InT, NP, 4, VEC>(p, plan, s, stream);
+    default: return launch_scan_ks<InT, NP, 8, VEC>(p, plan, s, stream);
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd, hipStream_t stream) {
+  const int64_t blocks = p.B * p.Hv * a.chunks;
+  const bool vec = delta_vec(p);
+  if (p.in_bf16)
+    return vec ? prepare_vec<bf16_t, 1, true>(a, blocks, bwd, stream) : prepare_vec<bf16_t, 1, false>(a, blocks, bwd, stream);
+  return vec ? prepare_vec<float, 3, true>(a, blocks, bwd, stream) : prepare_vec<float, 3, false>(a, blocks, bwd, stream);
+}
+
+DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int requested) {
+  DeltaChunks d{};
+  d.chunks = static_cast<int>((L + kChunk - 1) / kChunk);
+  d.pieces = 1;
+  if (requested > 0) d.pieces = std::min(requested, d.chunks);
+  d.chunks_piece = (d.chunks + d.pieces - 1) / d.pieces;
+  d.pieces = (d.chunks + d.chunks_piece - 1) / d.chunks_piece;
+  const size_t records = static_cast<size_t>(B) * Hv * d.chunks;
+  const size_t rows = 32 * static_cast<size_t>(padded_ks(dk)), cols = (static_cast<size_t>(dv) + 15) / 16 * 16;
+  const size_t piece_heads = static_cast<size_t>(B) * Hv * d.pieces;
+  size_t off = 0;
+  d.off_gates = off;
+  off += align256(records * kGateFloats * sizeof(float));
+  d.off_T = off;
+  off += align256(records * kTriEntries * sizeof(uint16_t));
+  d.off_P = off;
+  off += align256(records * kTriEntries * sizeof(uint16_t));
+  d.off_agg = off;
+  if (d.pieces > 1) off += align256(piece_heads * rows * (rows + cols) * sizeof(float));
+  d.off_starts = off;
+  if (d.pieces > 1) off += align256(piece_heads * rows * cols * sizeof(float));
+  d.bytes = off;
+  return d;
+}
+
+hipError_t launch_delta_chunks(const DeltaPlan& p, const DeltaChunks& plan, void* workspace, hipStream_t stream) {
+  char* ws = static_cast<char*>(workspace);
+  ScanArgs s{};
+  s.c = chunk_args(p, plan.chunks);
+  s.c.gates = reinterpret_cast<float*>(ws + plan.off_gates);
+  s.c.T = reinterpret_cast<uint16_t*>(ws + plan.off_T);
+  s.c.P = reinterpret_cast<uint16_t*>(ws + plan.off_P);
+  hipError_t e = launch_chunk_prepare(p, s.c, false, stream);
+  if (e != hipSuccess) return e;
+  s.pieces = plan.pieces;
+  s.chunks_piece = plan.chunks_piece;
+  s.out_bf16 = p.out_bf16;
+  s.h0 = p.h0;
+  s.cols = (p.dv + 15) / 16 * 16;
+  if (plan.pieces > 1) {
+    s.agg = reinterpret_cast<float*>(ws + plan.off_agg);
+    s.starts = reinterpret_cast<float*>(ws + plan.off_starts);
+  }
+  s.out = p.out;
+  s.h_last = p.h_last;
+  const bool vec = delta_vec(p);
+  if (p.in_bf16)
+    return vec ? launch_scan_vec<bf16_t, 1, true>(p, plan, s, stream) : launch_scan_vec<bf16_t, 1, false>(p, plan, s, stream);
+  return vec ? launch_scan_vec<float, 3, true>(p, plan, s, stream) : launch_scan_vec<float, 3, false>(p, plan, s, stream);
+}
+
+}  // namespace ssm

@@ -1,0 +1,248 @@
+// Matrix-core building blocks of the chunked gated delta rule (gfx950).
+//
+// Every product is v_mfma_f32_16x16x32_bf16 with float32 sums. A float32
+// operand goes in as three bfloat16 parts that add up to it exactly (8 bits of
+// the significand each); a bfloat16 input is its own single part. Products of
+// parts below 2^-24 of the whole are left out, so an operand costs 3 products
+// against an input part and 6 against another split operand, and results carry
+// float32's precision. (The float32 matrix instructions run at 1/16 of the
+// bfloat16 rate.)
+//
+// Lane layouts (lane l, g = l / 16): A holds row l % 16 and 8 entries of the
+// summed index, B column l % 16 and the same 8; D holds column l % 16 and rows
+// 4 g .. 4 g + 3. The order of the summed index is free as long as A and B agree,
+// and it is chosen so that two D tiles are a B operand as they stand: within 32
+// entries, slots 0..3 of lane group g are entries 4 g .. and slots 4..7 are
+// entries 16 + 4 g ... A chain of products on one 16-column strip therefore never
+// leaves the registers.
+#pragma once
+
+#include "device_math.h"
+
+namespace ssm {
+
+constexpr int kChunk = 64;  // tokens per chunk
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// The wave's place in its workgroup as a scalar. Matrix instructions run whatever
+// the lane mask says, so a product under a condition on the wave needs a branch the
+// compiler knows to be uniform; a mask would not keep it from running.
+__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
+
+// An operand of one product: NP parts of 8 entries.
+template <int NP>
+struct Frag {
+  u32x4 p[NP];
+};
+
+// The upper halves of two floats as one word (lo in the low half).
+__device__ __forceinline__ uint32_t upper_pair(float lo, float hi) {
+  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+__device__ __forceinline__ float below(float x) {  // x without its upper half: exact
+  return x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+}
+
+// Two floats in three parts.
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[3]) {
+  w[0] = upper_pair(a, b);
+  a = below(a);
+  b = below(b);
+  w[1] = upper_pair(a, b);
+  w[2] = upper_pair(below(a), below(b));
+}
+
+// Two D tiles (or any two runs of four) as a split operand.
+__device__ __forceinline__ Frag<3> split8(f32x4 a, f32x4 b) {
+  Frag<3> f;
+  uint32_t w[3];
+  split_pair(a.x, a.y, w);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) f.p[i].x = w[i];
+  split_pair(a.z, a.w, w);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) f.p[i].y = w[i];
+  split_pair(b.x, b.y, w);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) f.p[i].z = w[i];
+  split_pair(b.z, b.w, w);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) f.p[i].w = w[i];
+  return f;
+}
+
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                 0);
+}
+
+// c += a b, smallest parts first.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4 c) {
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB) c = mfma(a.p[i], b.p[s - i], c);
+  return c;
+}
+
+// Rows of tokens staged in LDS as A operands: parts x (64 / 16 tiles of rows) x
+// (KS tiles of 32 entries) x 64 lanes x 8 entries.
+template <int NP, int KS>
+struct TokenTile {
+  static constexpr int kFrags = 4 * KS;
+  static constexpr int kPart = kFrags * 64 * 8;  // entries of one part
+  static constexpr int kBytes = NP * kPart * 2;
+
+  // Offset, in entries, of the run of four entries 4 * run .. of a token.
+  __device__ __forceinline__ static int at(int token, int run) {
+    return (((token >> 4) * KS + (run >> 3)) * 64 + (run & 3) * 16 + (token & 15)) * 8 + ((run >> 2) & 1) * 4;
+  }
+  // A operand with the tokens of tile mi as rows, summed over entries 32 ks ..
+  __device__ __forceinline__ static Frag<NP> rows(const uint16_t* s, int mi, int ks, int lane) {
+    Frag<NP> f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+      f.p[i] = *reinterpret_cast<const u32x4*>(s + i * kPart + ((mi * KS + ks) * 64 + lane) * 8);
+    return f;
+  }
+  // A operand with the 16 entries of tile m0 as rows, summed over tokens 32 ts ..:
+  // transposing reads, where each group of 16 lanes names 4 tokens x 16 entries
+  // (lane i: token i / 4, run i % 4) and lane i receives entry i of the 4 tokens.
+  __device__ __forceinline__ static Frag<NP> columns(const uint16_t* s, int m0, int ts, int lane) {
+    const int token = ts * 32 + (lane >> 4) * 4 + ((lane & 15) >> 2), run = m0 * 4 + (lane & 3);
+    Frag<NP> f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const u32x2 lo = transposed(s + i * kPart + at(token, run)), hi = transposed(s + i * kPart + at(token + 16, run));
+      f.p[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
+    }
+    return f;
+  }
+  __device__ __forceinline__ static u32x2 transposed(const uint16_t* p) {
+    using lds_t = __attribute__((address_space(3))) s16x4*;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(p)));
+  }
+};
+
+// Eight consecutive entries of a token from global memory; entries at or past
+// `left` are 0. VEC: whole and aligned.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* p, int left, float (&x)[8]) {
+  if constexpr (VEC) {
+    constexpr int per = 16 / static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int i = 0; i < 8; i += per) {
+      const typename Run<T, per>::raw w = Run<T, per>::load(p + i);
+#pragma unroll
+      for (int j = 0; j < per; ++j) x[i + j] = Run<T, per>::at(w, j);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < left ? load_elem(p, i) : 0.0f;
+  }
+}
+
+// Stage tokens 0 .. n_tokens - 1 (0 beyond) and entries d0 .. d0 + 32 KS - 1 (0 at or
+// past d) of a token-strided tensor. All threads of the workgroup call it.
+template <typename T, int NP, int KS, bool VEC, int THREADS>
+__device__ __forceinline__ void stage_tokens(uint16_t* s, const T* src, int64_t stride, int n_tokens, int d0, int d) {
+  using Tile = TokenTile<NP, KS>;
+  constexpr int kOct = KS * 4;  // runs of 8 entries per token
+#pragma unroll
+  for (int i = threadIdx.x; i < 64 * kOct; i += THREADS) {
+    // a wave takes 16 tokens x 4 runs: 64 or 128 bytes of each token's row
+    const int token = (i & 15) | ((i / (16 * kOct)) << 4), oct = (i >> 4) % kOct;
+    const int left = d - d0 - oct * 8;
+    const T* p = src + token * stride + d0 + oct * 8;
+    if constexpr (NP == 1) {
+      u32x4 w = {0, 0, 0, 0};
+      if (token < n_tokens && left > 0) {
+        if constexpr (VEC) {
+          w = *reinterpret_cast<const u32x4*>(p);
+        } else {
+          uint32_t e[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = j < left ? p[j].bits : 0u;
+          w = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+        }
+      }
+      *reinterpret_cast<u32x2*>(s + Tile::at(token, oct * 2)) = u32x2{w.x, w.y};
+      *reinterpret_cast<u32x2*>(s + Tile::at(token, oct * 2 + 1)) = u32x2{w.z, w.w};
+    } else {
+      float x[8] = {};
+      if (token < n_tokens && left > 0) load8<T, VEC>(p, left, x);
+      const Frag<3> f = split8(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        *reinterpret_cast<u32x2*>(s + k * Tile::kPart + Tile::at(token, oct * 2)) = u32x2{f.p[k].x, f.p[k].y};
+        *reinterpret_cast<u32x2*>(s + k * Tile::kPart + Tile::at(token, oct * 2 + 1)) = u32x2{f.p[k].z, f.p[k].w};
+      }
+    }
+  }
+}
+
+// A operand like TokenTile::rows, straight from global memory and split on the
+// way (where the tile does not fit in LDS). `src`: the chunk's first token.
+template <typename T, int NP, bool VEC>
+__device__ __forceinline__ Frag<NP> rows_from_global(const T* src, int64_t stride, int n_tokens, int d, int mi, int ks,
+                                                     int lane) {
+  const int token = mi * 16 + (lane & 15), at = ks * 32 + (lane >> 4) * 4;
+  float x[8] = {};
+  if (token < n_tokens) {
+    const T* p = src + token * stride + at;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (VEC) {
+        if (at + 16 * h < d) {
+          const typename Run<T, 4>::raw w = Run<T, 4>::load(p + 16 * h);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[4 * h + j] = Run<T, 4>::at(w, j);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[4 * h + j] = at + 16 * h + j < d ? load_elem(p, 16 * h + j) : 0.0f;
+      }
+    }
+  }
+  const Frag<3> f = split8(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
+  Frag<NP> r;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) r.p[i] = f.p[i];
+  return r;
+}
+
+// A chunk's triangular 64 x 64 matrix as split A operands in global memory: for
+// row tile mi the summed tiles ks <= mi / 2 (mi, ks) -> 6 operands, or for its
+// transpose ks >= mi / 2; each 3 parts x 64 lanes x 8 entries.
+constexpr int kTriFrags = 6;
+constexpr int kTriEntries = kTriFrags * 3 * 64 * 8;
+__host__ __device__ constexpr int tri_index(int mi, int ks) { return mi < 2 ? mi : 2 + (mi - 2) * 2 + ks; }
+// transposed: row tiles 0 and 1 sum over both halves, 2 and 3 over the second
+__host__ __device__ constexpr int tri_t_index(int mi, int ks) { return mi < 2 ? mi * 2 + ks : mi + 2; }
+
+__device__ __forceinline__ Frag<3> load_tri(const uint16_t* m, int index, int lane) {
+  Frag<3> f;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) f.p[i] = *reinterpret_cast<const u32x4*>(m + ((index * 3 + i) * 64 + lane) * 8);
+  return f;
+}
+__device__ __forceinline__ void store_tri(uint16_t* m, int index, int lane, const Frag<3>& f) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(m + ((index * 3 + i) * 64 + lane) * 8) = f.p[i];
+}
+
+// Per-chunk scalars in global memory: e0, eC and beta of the 64 tokens, aC.
+//   e0 = exp(sum of log decays from the chunk's start through the token), 0 after a reset
+//   eC = exp(sum after the token to the chunk's end), 0 before a reset
+//   aC = e0 of the last token: the whole chunk's decay
+constexpr int kGateFloats = 256;
+constexpr int kE0 = 0, kEC = 64, kBeta = 128, kAC = 192;
+
+}  // namespace ssm

@@ -1,6 +1,6 @@
 // Host-side interface between the front end of the gated delta rule and the
-// head norms (api_delta.cpp) and their kernels (delta_step.hip, qk_norm.hip).
-// Not installed; not part of the ABI.
+// head norms (api_delta.cpp) and their kernels (delta_step.hip,
+// delta_chunk.hip, qk_norm.hip). Not installed; not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -34,6 +34,16 @@ struct DeltaPlan {
 
 // The recurrence step by step with the state in registers (delta_step.hip).
 hipError_t launch_delta_steps(const DeltaPlan& plan, hipStream_t stream);
+
+// The recurrence in chunks of 64 tokens on the matrix cores (delta_chunk.hip): how
+// many chunks, the pieces the sequence is split into, and the workspace layout.
+struct DeltaChunks {
+  int chunks, pieces, chunks_piece;
+  size_t off_gates, off_T, off_P, off_agg, off_starts, bytes;
+};
+// requested = 0: automatic. Pure host arithmetic.
+DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int requested);
+hipError_t launch_delta_chunks(const DeltaPlan& plan, const DeltaChunks& chunks, void* workspace, hipStream_t stream);
 
 // Norms and rotation (qk_norm.hip).
 struct NormPlan {
