@@ -103,9 +103,9 @@ __device__ __forceinline__ float pair_decay(const ChunkGates& s, int i, int j) {
 template <typename InT, int NP, int KS, bool VEC, bool BWD>
 __global__ __launch_bounds__(kThreads) void delta_chunk_prepare(const ChunkArgs a) {
   using Tile = TokenTile<NP, KS>;
-  extern __shared__ uint16_t staged[];
-  uint16_t* sk = staged;
-  uint16_t* sq = staged + NP * Tile::kPart;
+  extern __shared__ __align__(16) uint16_t staged_tokens[];
+  uint16_t* sk = staged_tokens;
+  uint16_t* sq = staged_tokens + NP * Tile::kPart;
   __shared__ ChunkGates gates;
   __shared__ float diag[4][16][20];  // A_ii, then T_ii; rows of 16 padded to 20
   const int lane = threadIdx.x % 64, g4 = (lane >> 4) * 4, col = lane & 15;
@@ -284,7 +284,7 @@ struct ScanArgs {
   ChunkArgs c;
   int pieces, chunks_piece;
   int col_blocks;   // workgroups per (head, piece)
-  int out_bf16;
+  int out_bf16, out_runs;  // out_runs: rows of out take whole 16-byte runs
   const float* h0;  // (bh, dk, dv) or null
   const float* starts;  // states of pieces 1 .. (bh, piece, 32 KS, cols), or null
   float* agg;       // aggregates walk: (bh, piece, 32 KS, 32 KS + cols)
@@ -293,23 +293,120 @@ struct ScanArgs {
   float* h_last;
 };
 
-// One wave's walk over the chunks of a piece with 16 columns of the state.
-// AGG: the aggregates walk (no read-out; the first 32 KS columns start from the identity).
+constexpr int kWaves = kThreads / 64;
+constexpr int kBlockCols = 16 * kWaves;  // columns of the state per workgroup
+
+// What a workgroup stages of one chunk, in bytes from the stage's start.
+template <typename InT, int NP, int KS, bool AGG, bool QLDS>
+struct Stage {
+  static constexpr int kK = 0;
+  static constexpr int kQ = kK + TokenTile<NP, KS>::kBytes;
+  static constexpr int kT = kQ + (!AGG && QLDS ? TokenTile<NP, KS>::kBytes : 0);
+  static constexpr int kP = kT + kTriEntries * 2;
+  static constexpr int kGates = kP + (AGG ? 0 : kTriEntries * 2);
+  static constexpr int kV = kGates + kGateFloats * 4;  // (64, kBlockCols) of InT
+  static constexpr int kBytes = kV + kChunk * kBlockCols * static_cast<int>(sizeof(InT));
+};
+
+// Where the staging of a chunk reads.
+template <typename InT>
+struct ChunkSource {
+  const InT* q;
+  const InT* k;
+  const InT* v;  // the chunk's first token, column 0 of the head
+  const uint16_t* T;
+  const uint16_t* P;
+  const float* gates;
+  int n_tokens;
+};
+
+template <typename InT>
+__device__ __forceinline__ ChunkSource<InT> chunk_source(const ChunkArgs& a, int bh, int b, int h, int c) {
+  ChunkSource<InT> s;
+  const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk;
+  const int64_t record = static_cast<int64_t>(bh) * a.chunks + c;
+  const int hk = h / a.group;
+  s.q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
+  s.k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
+  s.v = static_cast<const InT*>(a.v) + t0 * a.vs + static_cast<int64_t>(h) * a.dv;
+  s.T = a.T + record * kTriEntries;
+  s.P = a.P + record * kTriEntries;
+  s.gates = a.gates + record * kGateFloats;
+  s.n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(c) * kChunk));
+  return s;
+}
+
+// ASYNC staging: whole 16-byte runs straight into LDS, 1 KB a wave and instruction.
+// Tokens past the end repeat the last one (their beta is 0, so they change
+// nothing), columns past dv repeat the last ones (never stored).
+template <typename InT, int KS, bool AGG>
+__device__ __forceinline__ void stage_async(char* st, const ChunkArgs& a, const ChunkSource<InT>& s, int col0, int lane,
+                                            int wave) {
+  using S = Stage<InT, 1, KS, AGG, true>;
+  const int last = s.n_tokens - 1;
+#pragma unroll
+  for (int i = 0; i < 4 * KS / kWaves; ++i) {  // wave w: row tile w
+    const int token = min(wave * 16 + (lane & 15), last), d = i * 32 + (lane >> 4) * 8, f = wave * KS + i;
+    load_to_lds(s.k + token * a.ks + d, st + S::kK + f * 1024);
+    if constexpr (!AGG) load_to_lds(s.q + token * a.qs + d, st + S::kQ + f * 1024);
+  }
+#pragma unroll
+  for (int i = 0; i < (kTriFrags * 3 + kWaves - 1) / kWaves; ++i) {
+    const int f = wave + i * kWaves;
+    if (f < kTriFrags * 3) {
+      load_to_lds(s.T + f * 512 + lane * 8, st + S::kT + f * 1024);
+      if constexpr (!AGG) load_to_lds(s.P + f * 512 + lane * 8, st + S::kP + f * 1024);
+    }
+  }
+  if (wave == 0) load_to_lds(s.gates + lane * 4, st + S::kGates);
+#pragma unroll
+  for (int i = 0; i < 8 / kWaves; ++i) {  // 8 tokens of 64 columns
+    const int f = wave + i * kWaves, token = min(f * 8 + lane / 8, last);
+    const int col = max(0, min(col0 + (lane & 7) * 8, a.dv - 8));
+    load_to_lds(s.v + token * a.vs + col, st + S::kV + f * 1024);
+  }
+}
+
+// Staging through registers, for float32 and for rows that are not whole runs.
 template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS>
+__device__ __forceinline__ void stage_sync(char* st, const ChunkArgs& a, const ChunkSource<InT>& s, int col0) {
+  using S = Stage<InT, NP, KS, AGG, QLDS>;
+  stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kK), s.k, a.ks, s.n_tokens, 0, a.dk);
+  if constexpr (!AGG && QLDS)
+    stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kQ), s.q, a.qs, s.n_tokens, 0, a.dk);
+  constexpr int kRuns = kTriEntries / 8;
+  for (int i = threadIdx.x; i < kRuns; i += kThreads) {
+    reinterpret_cast<u32x4*>(st + S::kT)[i] = reinterpret_cast<const u32x4*>(s.T)[i];
+    if constexpr (!AGG) reinterpret_cast<u32x4*>(st + S::kP)[i] = reinterpret_cast<const u32x4*>(s.P)[i];
+  }
+  reinterpret_cast<float*>(st + S::kGates)[threadIdx.x] = s.gates[threadIdx.x];
+  InT* v = reinterpret_cast<InT*>(st + S::kV);
+#pragma unroll
+  for (int i = 0; i < kChunk * kBlockCols / kThreads; ++i) {
+    const int e = threadIdx.x + i * kThreads, token = e / kBlockCols, col = col0 + e % kBlockCols;
+    InT x{};
+    if (token < s.n_tokens && col >= 0 && col < a.dv) x = s.v[token * a.vs + col];
+    v[e] = x;
+  }
+}
+
+// One wave's walk over the chunks of a piece with 16 columns of the state.
+// AGG: the aggregates walk (no read-out; the first 32 KS columns start from the
+// identity). With two stages the next chunk is loaded while this one is worked on.
+template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS, bool ASYNC, int STAGES>
 __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
   using Tile = TokenTile<NP, KS>;
+  using S = Stage<InT, NP, KS, AGG, QLDS>;
   constexpr int DKT = 2 * KS;  // row tiles of the state
-  extern __shared__ uint16_t staged[];
-  uint16_t* sk = staged;
-  uint16_t* sq = staged + NP * Tile::kPart;
-  __shared__ float gates[kGateFloats];
+  extern __shared__ __align__(16) char staged[];
   const ChunkArgs& a = s.c;
   const int lane = threadIdx.x % 64, wave = wave_index(), g4 = (lane >> 4) * 4;
   const int cb = blockIdx.x % s.col_blocks, rest = blockIdx.x / s.col_blocks;
   const int piece = rest % s.pieces, bh = rest / s.pieces;
-  const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / a.group;
-  const int strip = cb * (kThreads / 64) + wave;      // 16-column strip
-  const int own = (AGG ? strip - DKT : strip) * 16 + (lane & 15);  // column of v
+  const int b = bh / a.Hv, h = bh - b * a.Hv;
+  const int strip = cb * kWaves + wave;                            // 16-column strip
+  const int col0 = (cb * kWaves - (AGG ? DKT : 0)) * 16;           // the workgroup's first column of v
+  const int own = col0 + wave * 16 + (lane & 15);                  // the lane's
   const bool has_v = own >= 0 && own < a.dv;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
@@ -319,7 +416,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
     H[m] = zero;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int row = m * 16 + g4 + r;
+      const int row = state_row(m, g4, r);
       if (AGG) {
         if (strip * 16 + (lane & 15) == row) H[m][r] = 1.0f;
       } else if (piece > 0) {
@@ -331,95 +428,127 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
     }
   }
 
-  const int c1 = min(a.chunks, (piece + 1) * s.chunks_piece);
-  for (int c = piece * s.chunks_piece; c < c1; ++c) {
-    const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk;
-    const int n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(c) * kChunk));
-    const int64_t record = static_cast<int64_t>(bh) * a.chunks + c;
-    const InT* q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
-    const InT* k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
-    const InT* v = static_cast<const InT*>(a.v) + t0 * a.vs + static_cast<int64_t>(h) * a.dv + own;
-    __syncthreads();  // the previous chunk's tiles are read
-    stage_tokens<InT, NP, KS, VEC, kThreads>(sk, k, a.ks, n_tokens, 0, a.dk);
-    if constexpr (!AGG && QLDS) stage_tokens<InT, NP, KS, VEC, kThreads>(sq, q, a.qs, n_tokens, 0, a.dk);
-    gates[threadIdx.x] = a.gates[record * kGateFloats + threadIdx.x];
-    f32x4 V[4];
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int token = m * 16 + g4 + r;
-        V[m][r] = has_v && token < n_tokens ? load_elem(v, token * a.vs) : 0.0f;
-      }
-    __syncthreads();
+  const int c0 = piece * s.chunks_piece, c1 = min(a.chunks, c0 + s.chunks_piece);
+  if constexpr (STAGES == 2) stage_async<InT, KS, AGG>(staged, a, chunk_source<InT>(a, bh, b, h, c0), col0, lane, wave);
+  for (int c = c0; c < c1; ++c) {
+    char* st = staged + (STAGES == 2 ? ((c - c0) & 1) * S::kBytes : 0);
+    const ChunkSource<InT> src = chunk_source<InT>(a, bh, b, h, c);
+    if constexpr (STAGES == 2) {
+      wait_loads();
+      __syncthreads();  // this stage is loaded, and the other one is no longer read
+      if (c + 1 < c1)
+        stage_async<InT, KS, AGG>(staged + ((c + 1 - c0) & 1) * S::kBytes, a, chunk_source<InT>(a, bh, b, h, c + 1),
+                                  col0, lane, wave);
+    } else {
+      __syncthreads();  // the previous chunk is no longer read
+      if constexpr (ASYNC)
+        stage_async<InT, KS, AGG>(st, a, src, col0, lane, wave);
+      else
+        stage_sync<InT, NP, KS, VEC, AGG, QLDS>(st, a, src, col0);
+      wait_loads();
+      __syncthreads();
+    }
+    const uint16_t* sk = reinterpret_cast<const uint16_t*>(st + S::kK);
+    const uint16_t* sq = reinterpret_cast<const uint16_t*>(st + S::kQ);
+    const float* gates = reinterpret_cast<const float*>(st + S::kGates);
 
     f32x4 X[4] = {zero, zero, zero, zero}, Y[4] = {zero, zero, zero, zero};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const Frag<3> hb = split8(H[2 * ks], H[2 * ks + 1]);
+      Frag<NP> kf[4], qf[4];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        X[m] = mma(Tile::rows(sk, m, ks, lane), hb, X[m]);
+        kf[m] = Tile::rows(sk, m, ks, lane);
         if constexpr (!AGG) {
           if constexpr (QLDS)
-            Y[m] = mma(Tile::rows(sq, m, ks, lane), hb, Y[m]);
+            qf[m] = Tile::rows(sq, m, ks, lane);
           else
-            Y[m] = mma(rows_from_global<InT, NP, VEC>(q, a.qs, n_tokens, a.dk, m, ks, lane), hb, Y[m]);
+            qf[m] = rows_from_global<InT, VEC>(src.q, a.qs, src.n_tokens, a.dk, m, ks, lane);
         }
       }
+      mma_n(kf, hb, X);
+      if constexpr (!AGG) mma_n(qf, hb, Y);
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
+      f32x4 V = zero;
+      if constexpr (sizeof(InT) == 2) {
+        // the lane's column of tokens 16 m + g4 ..
+        const u32x2 w = read_transposed(reinterpret_cast<const uint16_t*>(st + S::kV) +
+                                        (m * 16 + g4 + ((lane & 15) >> 2)) * kBlockCols + wave * 16 + (lane & 3) * 4);
+        V = f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                  __uint_as_float(w.y & 0xFFFF0000u)};
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          V[r] = reinterpret_cast<const float*>(st + S::kV)[(m * 16 + g4 + r) * kBlockCols + wave * 16 + (lane & 15)];
+      }
+      if (AGG && !has_v) V = zero;
       const f32x4 e0 = *reinterpret_cast<const f32x4*>(gates + kE0 + m * 16 + g4);
       const f32x4 be = *reinterpret_cast<const f32x4*>(gates + kBeta + m * 16 + g4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        X[m][r] = be[r] * __builtin_fmaf(-e0[r], X[m][r], V[m][r]);
+        X[m][r] = be[r] * __builtin_fmaf(-e0[r], X[m][r], V[r]);
         Y[m][r] *= e0[r];
       }
     }
-    f32x4 U[4];
+    f32x4 U[4] = {zero, zero, zero, zero};
     {
       const Frag<3> rb[2] = {split8(X[0], X[1]), split8(X[2], X[3])};
-      const uint16_t* T = a.T + record * kTriEntries;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        U[m] = zero;
-#pragma unroll
-        for (int ks = 0; ks <= m / 2; ++ks) U[m] = mma(load_tri(T, tri_index(m, ks), lane), rb[ks], U[m]);
-      }
+      mma_tri(reinterpret_cast<const uint16_t*>(st + S::kT), rb, lane, U);
     }
     if constexpr (!AGG) {
       const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
-      const uint16_t* P = a.P + record * kTriEntries;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-#pragma unroll
-        for (int ks = 0; ks <= m / 2; ++ks) Y[m] = mma(load_tri(P, tri_index(m, ks), lane), ub[ks], Y[m]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int token = m * 16 + g4 + r;
-          if (!has_v || token >= n_tokens) continue;
-          const int64_t o = ((t0 + token) * a.Hv + h) * a.dv + own;
-          if (s.out_bf16)
-            store_elem(static_cast<bf16_t*>(s.out), o, a.scale * Y[m][r]);
-          else
-            store_elem(static_cast<float*>(s.out), o, a.scale * Y[m][r]);
-        }
-      }
+      mma_tri(reinterpret_cast<const uint16_t*>(st + S::kP), ub, lane, Y);
     }
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const f32x4 eC = *reinterpret_cast<const f32x4*>(gates + kEC + m * 16 + g4);
-      U[m] *= eC;
-    }
+    for (int m = 0; m < 4; ++m) U[m] *= *reinterpret_cast<const f32x4*>(gates + kEC + m * 16 + g4);
     const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
     const float aC = gates[kAC];
 #pragma unroll
-    for (int m = 0; m < DKT; ++m) {
-      H[m] *= aC;
+    for (int m = 0; m < DKT; ++m) H[m] *= aC;
 #pragma unroll
-      for (int ts = 0; ts < 2; ++ts) H[m] = mma(Tile::columns(sk, m, ts, lane), ub[ts], H[m]);
+    for (int ts = 0; ts < 2; ++ts) {
+      Frag<NP> kc[DKT];
+#pragma unroll
+      for (int m = 0; m < DKT; ++m) kc[m] = Tile::columns(sk, m, ts, lane);
+      mma_n(kc, ub[ts], H);
+    }
+
+    if constexpr (!AGG) {
+      const int64_t row0 = (static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk) * a.Hv + h;  // x dv
+      if (sizeof(InT) == 2 && s.out_bf16 && s.out_runs) {
+        // The strip's place among the staged values is this wave's alone and has been
+        // read: the outputs turn there from columns to rows, 16 bytes a lane.
+        uint16_t* o = reinterpret_cast<uint16_t*>(st + S::kV) + wave * 16;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            store_elem(reinterpret_cast<bf16_t*>(o), (m * 16 + g4 + r) * kBlockCols + (lane & 15), a.scale * Y[m][r]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int token = i * 32 + lane / 2, half = (lane & 1) * 8;
+          const u32x4 w = *reinterpret_cast<const u32x4*>(o + token * kBlockCols + half);
+          const int col = col0 + wave * 16 + half;
+          if (token < src.n_tokens && col < a.dv)
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(s.out) + (row0 + static_cast<int64_t>(token) * a.Hv) * a.dv + col) = w;
+        }
+      } else {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int token = m * 16 + g4 + r;
+            if (!has_v || token >= src.n_tokens) continue;
+            const int64_t o = (row0 + static_cast<int64_t>(token) * a.Hv) * a.dv + own;
+            if (s.out_bf16)
+              store_elem(static_cast<bf16_t*>(s.out), o, a.scale * Y[m][r]);
+            else
+              store_elem(static_cast<float*>(s.out), o, a.scale * Y[m][r]);
+          }
+      }
     }
   }
 
@@ -430,13 +559,13 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
 #pragma unroll
     for (int m = 0; m < DKT; ++m)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) dst[static_cast<int64_t>(m * 16 + g4 + r) * width] = H[m][r];
+      for (int r = 0; r < 4; ++r) dst[static_cast<int64_t>(state_row(m, g4, r)) * width] = H[m][r];
   } else if (s.h_last && c1 == a.chunks && has_v) {
 #pragma unroll
     for (int m = 0; m < DKT; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = m * 16 + g4 + r;
+        const int row = state_row(m, g4, r);
         if (row < a.dk) s.h_last[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own] = H[m][r];
       }
   }
@@ -456,31 +585,31 @@ template <int KS>
 __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
   constexpr int ROWS = 32 * KS;
   __shared__ u32x4 S[2][KS][3][64];  // the state as B operand, two pieces in turn
-  const int lane = threadIdx.x % 64, w = wave_index(), g4 = (lane >> 4) * 4;  // wave w: rows 16 w ..
+  const int lane = threadIdx.x % 64, w = wave_index(), g4 = (lane >> 4) * 4;  // wave w: row tile w
   const int bh = blockIdx.x / a.strips, own = (blockIdx.x - bh * a.strips) * 16 + (lane & 15);
   const int width = ROWS + a.cols;
   f32x4 H;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    const int row = w * 16 + g4 + r;
+    const int row = state_row(w, g4, r);
     H[r] = a.h0 && row < a.dk && own < a.dv ? a.h0[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own] : 0.0f;
   }
   const float* M = a.agg + static_cast<int64_t>(bh) * a.pieces * ROWS * width;
   f32x4 m[KS][2], n;
   const auto fetch = [&](int piece) {
     const float* p = M + static_cast<int64_t>(piece) * ROWS * width;
-    const float* row = p + static_cast<int64_t>(w * 16 + (lane & 15)) * width + g4;
+    const float* row = p + static_cast<int64_t>(state_row(w, lane & 12, lane & 3)) * width + 2 * g4;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       m[ks][0] = *reinterpret_cast<const f32x4*>(row + 32 * ks);
-      m[ks][1] = *reinterpret_cast<const f32x4*>(row + 32 * ks + 16);
+      m[ks][1] = *reinterpret_cast<const f32x4*>(row + 32 * ks + 4);
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) n[r] = p[static_cast<int64_t>(w * 16 + g4 + r) * width + ROWS + own];
+    for (int r = 0; r < 4; ++r) n[r] = p[static_cast<int64_t>(state_row(w, g4, r)) * width + ROWS + own];
   };
   fetch(0);
   for (int piece = 0; piece + 1 < a.pieces; ++piece) {
-    // half of operand w / 2: rows 16 w .. are its entries 16 (w % 2) ..
+    // half of operand w / 2: the wave's rows are its slots 4 (w % 2) ..
     uint32_t lo[3], hi[3];
     split_pair(H.x, H.y, lo);
     split_pair(H.z, H.w, hi);
@@ -503,28 +632,40 @@ __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      a.starts[((static_cast<int64_t>(bh) * a.pieces + piece + 1) * ROWS + w * 16 + g4 + r) * a.cols + own] = H[r];
+      a.starts[((static_cast<int64_t>(bh) * a.pieces + piece + 1) * ROWS + state_row(w, g4, r)) * a.cols + own] = H[r];
   }
 }
 
-int padded_ks(int dk) { return dk <= 32 ? 1 : dk <= 64 ? 2 : dk <= 128 ? 4 : 8; }
+// Row tiles of 32 that hold dk: 1, 2, 3, 4, 6 or 8.
+int padded_ks(int dk) {
+  const int ks = (dk + 31) / 32;
+  return ks <= 4 ? ks : ks <= 6 ? 6 : 8;
+}
 
-template <typename InT, int NP, int KS, bool VEC>
+constexpr int kMaxLds = 160 * 1024;
+
+template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS, bool ASYNC>
+hipError_t launch_walk(const ScanArgs& s, int64_t blocks, hipStream_t stream) {
+  constexpr int kBytes = Stage<InT, NP, KS, AGG, QLDS>::kBytes;
+  constexpr int STAGES = ASYNC && 2 * kBytes <= kMaxLds ? 2 : 1;
+  static_assert(kBytes <= kMaxLds, "a chunk's stage exceeds LDS");
+  SSM_LOG("launch delta_chunk_scan<%d parts, %d rows, aggregates %d>: %d pieces of %d chunks, %d stages of %d bytes; "
+          "grid %lld x %d threads",
+          NP, 32 * KS, AGG, s.pieces, s.chunks_piece, STAGES, kBytes, static_cast<long long>(blocks), kThreads);
+  hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, VEC, AGG, QLDS, ASYNC, STAGES>),
+                     dim3(static_cast<unsigned>(blocks)), dim3(kThreads), STAGES * kBytes, stream, s);
+  return hipGetLastError();
+}
+
+template <typename InT, int NP, int KS, bool VEC, bool ASYNC>
 hipError_t launch_scan_ks(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs s, hipStream_t stream) {
-  constexpr int kWaves = kThreads / 64;
   // K and Q of a chunk side by side fit in LDS except for float32 past 128 entries
-  constexpr bool QLDS = 2 * TokenTile<NP, KS>::kBytes <= 128 * 1024;
+  constexpr bool QLDS = Stage<InT, NP, KS, false, true>::kBytes <= kMaxLds;
   const int64_t heads = p.B * p.Hv;
   if (plan.pieces > 1) {
     const int strips = 2 * KS + s.cols / 16;
     s.col_blocks = (strips + kWaves - 1) / kWaves;
-    const int64_t blocks = heads * plan.pieces * s.col_blocks;
-    constexpr size_t agg_lds = TokenTile<NP, KS>::kBytes;
-    SSM_LOG("launch delta_chunk_scan<%d parts, %d rows, aggregates>: %d pieces; grid %lld x %d threads", NP, 32 * KS,
-            plan.pieces, static_cast<long long>(blocks), kThreads);
-    hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, VEC, true, false>), dim3(static_cast<unsigned>(blocks)),
-                       dim3(kThreads), agg_lds, stream, s);
-    hipError_t e = hipGetLastError();
+    hipError_t e = launch_walk<InT, NP, KS, VEC, true, QLDS, ASYNC>(s, heads * plan.pieces * s.col_blocks, stream);
     if (e != hipSuccess) return e;
     FoldArgs f{s.agg, s.h0, const_cast<float*>(s.starts), plan.pieces, p.dk, p.dv, s.cols, s.cols / 16};
     SSM_LOG("launch delta_fold<%d rows>: grid %lld x %d threads", 32 * KS, static_cast<long long>(heads * f.strips),
@@ -532,24 +673,19 @@ hipError_t launch_scan_ks(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs 
     hipLaunchKernelGGL((delta_fold<KS>), dim3(static_cast<unsigned>(heads * f.strips)), dim3(2 * KS * 64), 0, stream, f);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const int strips = s.cols / 16;
-  s.col_blocks = (strips + kWaves - 1) / kWaves;
-  const int64_t blocks = heads * plan.pieces * s.col_blocks;
-  const size_t lds = (QLDS ? 2 : 1) * TokenTile<NP, KS>::kBytes;
-  SSM_LOG("launch delta_chunk_scan<%d parts, %d rows>: %d pieces of %d chunks; grid %lld x %d threads", NP, 32 * KS,
-          plan.pieces, plan.chunks_piece, static_cast<long long>(blocks), kThreads);
-  hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, VEC, false, QLDS>), dim3(static_cast<unsigned>(blocks)),
-                     dim3(kThreads), lds, stream, s);
-  return hipGetLastError();
+  s.col_blocks = (s.cols / 16 + kWaves - 1) / kWaves;
+  return launch_walk<InT, NP, KS, VEC, false, QLDS, ASYNC>(s, heads * plan.pieces * s.col_blocks, stream);
 }
 
-template <typename InT, int NP, bool VEC>
+template <typename InT, int NP, bool VEC, bool ASYNC>
 hipError_t launch_scan_vec(const DeltaPlan& p, const DeltaChunks& plan, const ScanArgs& s, hipStream_t stream) {
   switch (padded_ks(p.dk)) {
-    case 1: return launch_scan_ks<InT, NP, 1, VEC>(p, plan, s, stream);
-    case 2: return launch_scan_ks<InT, NP, 2, VEC>(p, plan, s, stream);
-    case 4: return launch_scan_ks<InT, NP, 4, VEC>(p, plan, s, stream);
-    default: return launch_scan_ks<InT, NP, 8, VEC>(p, plan, s, stream);
+    case 1: return launch_scan_ks<InT, NP, 1, VEC, ASYNC>(p, plan, s, stream);
+    case 2: return launch_scan_ks<InT, NP, 2, VEC, ASYNC>(p, plan, s, stream);
+    case 3: return launch_scan_ks<InT, NP, 3, VEC, ASYNC>(p, plan, s, stream);
+    case 4: return launch_scan_ks<InT, NP, 4, VEC, ASYNC>(p, plan, s, stream);
+    case 6: return launch_scan_ks<InT, NP, 6, VEC, ASYNC>(p, plan, s, stream);
+    default: return launch_scan_ks<InT, NP, 8, VEC, ASYNC>(p, plan, s, stream);
   }
 }
 
@@ -610,10 +746,16 @@ hipError_t launch_delta_chunks(const DeltaPlan& p, const DeltaChunks& plan, void
   }
   s.out = p.out;
   s.h_last = p.h_last;
+  s.out_runs = p.dv % 8 == 0 && delta_aligned(p.out, 16);
   const bool vec = delta_vec(p);
-  if (p.in_bf16)
-    return vec ? launch_scan_vec<bf16_t, 1, true>(p, plan, s, stream) : launch_scan_vec<bf16_t, 1, false>(p, plan, s, stream);
-  return vec ? launch_scan_vec<float, 3, true>(p, plan, s, stream) : launch_scan_vec<float, 3, false>(p, plan, s, stream);
+  if (!p.in_bf16)
+    return vec ? launch_scan_vec<float, 3, true, false>(p, plan, s, stream)
+               : launch_scan_vec<float, 3, false, false>(p, plan, s, stream);
+  // Straight loads to LDS: rows that fill the padded tile, values in whole runs.
+  const bool async = vec && p.dk == 32 * padded_ks(p.dk) && p.dv % 8 == 0 && p.vs % 8 == 0 && delta_aligned(p.v, 16);
+  if (async) return launch_scan_vec<bf16_t, 1, true, true>(p, plan, s, stream);
+  return vec ? launch_scan_vec<bf16_t, 1, true, false>(p, plan, s, stream)
+             : launch_scan_vec<bf16_t, 1, false, false>(p, plan, s, stream);
 }
 
 }  // namespace ssm

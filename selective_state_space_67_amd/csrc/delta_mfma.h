@@ -11,10 +11,14 @@
 // Lane layouts (lane l, g = l / 16): A holds row l % 16 and 8 entries of the
 // summed index, B column l % 16 and the same 8; D holds column l % 16 and rows
 // 4 g .. 4 g + 3. The order of the summed index is free as long as A and B agree,
-// and it is chosen so that two D tiles are a B operand as they stand: within 32
-// entries, slots 0..3 of lane group g are entries 4 g .. and slots 4..7 are
-// entries 16 + 4 g ... A chain of products on one 16-column strip therefore never
-// leaves the registers.
+// and it is chosen so that two D tiles are a B operand as they stand: slots 0..3
+// of lane group g are rows 4 g .. of the first, slots 4..7 those of the second.
+// A chain of products on one 16-column strip therefore never leaves the
+// registers. Rows of a D tile stand for
+//   tokens:  row 4 g + r of tile m is token 16 m + 4 g + r;
+//   entries of k and q (rows of the state): row 4 g + r of tile 2 s + t is entry
+//            32 s + 8 g + 4 t + r, so that a lane's 8 slots are 8 neighbours and a
+//            token's row is staged in 16-byte runs.
 #pragma once
 
 #include "device_math.h"
@@ -81,6 +85,13 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                  0);
 }
 
+// Four entries a lane from a 4 x 16 block of 16-bit entries that a group of 16 lanes
+// names in runs of four (lane i: row i / 4, run i % 4): lane i receives column i.
+__device__ __forceinline__ u32x2 read_transposed(const uint16_t* p) {
+  using lds_t = __attribute__((address_space(3))) s16x4*;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(p)));
+}
+
 // c += a b, smallest parts first.
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4 c) {
@@ -92,6 +103,22 @@ __device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4
   return c;
 }
 
+// Entry of k (row of the state) that row 4 g + r of tile m stands for; g4 = 4 g.
+__device__ __forceinline__ int state_row(int m, int g4, int r) { return (m >> 1) * 32 + g4 * 2 + (m & 1) * 4 + r; }
+
+// c[n] += a[n] b for N independent sums, in turns: a sum's next product waits for
+// its last one, the others' do not.
+template <int N, int NA, int NB>
+__device__ __forceinline__ void mma_n(const Frag<NA> (&a)[N], const Frag<NB>& b, f32x4 (&c)[N]) {
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB)
+#pragma unroll
+        for (int n = 0; n < N; ++n) c[n] = mfma(a[n].p[i], b.p[s - i], c[n]);
+}
+
 // Rows of tokens staged in LDS as A operands: parts x (64 / 16 tiles of rows) x
 // (KS tiles of 32 entries) x 64 lanes x 8 entries.
 template <int NP, int KS>
@@ -100,9 +127,9 @@ struct TokenTile {
   static constexpr int kPart = kFrags * 64 * 8;  // entries of one part
   static constexpr int kBytes = NP * kPart * 2;
 
-  // Offset, in entries, of the run of four entries 4 * run .. of a token.
-  __device__ __forceinline__ static int at(int token, int run) {
-    return (((token >> 4) * KS + (run >> 3)) * 64 + (run & 3) * 16 + (token & 15)) * 8 + ((run >> 2) & 1) * 4;
+  // Offset, in entries, of the run of eight entries 8 * oct .. of a token.
+  __device__ __forceinline__ static int at(int token, int oct) {
+    return (((token >> 4) * KS + (oct >> 2)) * 64 + (oct & 3) * 16 + (token & 15)) * 8;
   }
   // A operand with the tokens of tile mi as rows, summed over entries 32 ks ..
   __device__ __forceinline__ static Frag<NP> rows(const uint16_t* s, int mi, int ks, int lane) {
@@ -112,22 +139,19 @@ struct TokenTile {
       f.p[i] = *reinterpret_cast<const u32x4*>(s + i * kPart + ((mi * KS + ks) * 64 + lane) * 8);
     return f;
   }
-  // A operand with the 16 entries of tile m0 as rows, summed over tokens 32 ts ..:
-  // transposing reads, where each group of 16 lanes names 4 tokens x 16 entries
-  // (lane i: token i / 4, run i % 4) and lane i receives entry i of the 4 tokens.
+  // A operand with the entries of state tile m0 as rows, summed over tokens 32 ts ..:
+  // transposing reads, where each group of 16 lanes names 4 tokens x 4 runs of four
+  // entries (lane i: token i / 4, run i % 4) and lane i receives entry i of the 4 tokens.
   __device__ __forceinline__ static Frag<NP> columns(const uint16_t* s, int m0, int ts, int lane) {
-    const int token = ts * 32 + (lane >> 4) * 4 + ((lane & 15) >> 2), run = m0 * 4 + (lane & 3);
+    const int token = ts * 32 + (lane >> 4) * 4 + ((lane & 15) >> 2), oct = (m0 >> 1) * 4 + (lane & 3);
     Frag<NP> f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const u32x2 lo = transposed(s + i * kPart + at(token, run)), hi = transposed(s + i * kPart + at(token + 16, run));
+      const uint16_t* p = s + i * kPart + (m0 & 1) * 4;
+      const u32x2 lo = read_transposed(p + at(token, oct)), hi = read_transposed(p + at(token + 16, oct));
       f.p[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
     }
     return f;
-  }
-  __device__ __forceinline__ static u32x2 transposed(const uint16_t* p) {
-    using lds_t = __attribute__((address_space(3))) s16x4*;
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(p)));
   }
 };
 
@@ -161,6 +185,7 @@ __device__ __forceinline__ void stage_tokens(uint16_t* s, const T* src, int64_t 
     const int token = (i & 15) | ((i / (16 * kOct)) << 4), oct = (i >> 4) % kOct;
     const int left = d - d0 - oct * 8;
     const T* p = src + token * stride + d0 + oct * 8;
+    uint16_t* to = s + Tile::at(token, oct);
     if constexpr (NP == 1) {
       u32x4 w = {0, 0, 0, 0};
       if (token < n_tokens && left > 0) {
@@ -173,50 +198,37 @@ __device__ __forceinline__ void stage_tokens(uint16_t* s, const T* src, int64_t 
           w = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
         }
       }
-      *reinterpret_cast<u32x2*>(s + Tile::at(token, oct * 2)) = u32x2{w.x, w.y};
-      *reinterpret_cast<u32x2*>(s + Tile::at(token, oct * 2 + 1)) = u32x2{w.z, w.w};
+      *reinterpret_cast<u32x4*>(to) = w;
     } else {
       float x[8] = {};
       if (token < n_tokens && left > 0) load8<T, VEC>(p, left, x);
       const Frag<3> f = split8(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        *reinterpret_cast<u32x2*>(s + k * Tile::kPart + Tile::at(token, oct * 2)) = u32x2{f.p[k].x, f.p[k].y};
-        *reinterpret_cast<u32x2*>(s + k * Tile::kPart + Tile::at(token, oct * 2 + 1)) = u32x2{f.p[k].z, f.p[k].w};
-      }
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4*>(to + k * Tile::kPart) = f.p[k];
     }
   }
 }
 
 // A operand like TokenTile::rows, straight from global memory and split on the
 // way (where the tile does not fit in LDS). `src`: the chunk's first token.
-template <typename T, int NP, bool VEC>
-__device__ __forceinline__ Frag<NP> rows_from_global(const T* src, int64_t stride, int n_tokens, int d, int mi, int ks,
-                                                     int lane) {
-  const int token = mi * 16 + (lane & 15), at = ks * 32 + (lane >> 4) * 4;
+template <typename T, bool VEC>
+__device__ __forceinline__ Frag<3> rows_from_global(const T* src, int64_t stride, int n_tokens, int d, int mi, int ks,
+                                                    int lane) {
+  const int token = mi * 16 + (lane & 15), at = ks * 32 + (lane >> 4) * 8;
   float x[8] = {};
-  if (token < n_tokens) {
-    const T* p = src + token * stride + at;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (VEC) {
-        if (at + 16 * h < d) {
-          const typename Run<T, 4>::raw w = Run<T, 4>::load(p + 16 * h);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[4 * h + j] = Run<T, 4>::at(w, j);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[4 * h + j] = at + 16 * h + j < d ? load_elem(p, 16 * h + j) : 0.0f;
-      }
-    }
-  }
-  const Frag<3> f = split8(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
-  Frag<NP> r;
-#pragma unroll
-  for (int i = 0; i < NP; ++i) r.p[i] = f.p[i];
-  return r;
+  if (token < n_tokens && at < d) load8<T, VEC>(src + token * stride + at, d - at, x);
+  return split8(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
 }
+
+// 16 bytes a lane from global memory straight into LDS: lane l's go to dst + 16 l
+// (dst the same in the whole wave). Done when the wave's loads are waited for.
+__device__ __forceinline__ void load_to_lds(const void* src, void* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+// Everything this wave has loaded has arrived.
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
 
 // A chunk's triangular 64 x 64 matrix as split A operands in global memory: for
 // row tile mi the summed tiles ks <= mi / 2 (mi, ks) -> 6 operands, or for its
@@ -232,6 +244,27 @@ __device__ __forceinline__ Frag<3> load_tri(const uint16_t* m, int index, int la
 #pragma unroll
   for (int i = 0; i < 3; ++i) f.p[i] = *reinterpret_cast<const u32x4*>(m + ((index * 3 + i) * 64 + lane) * 8);
   return f;
+}
+// c[m] += M[m][.] b for the four row tiles of a staged triangle M (rows m sum over
+// the halves ks <= m / 2): six independent sums in turns.
+__device__ __forceinline__ void mma_tri(const uint16_t* m, const Frag<3> (&b)[2], int lane, f32x4 (&c)[4]) {
+  Frag<3> a[6];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) a[i] = load_tri(m, i, lane);
+  f32x4 d[2] = {};
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i <= s; ++i) {
+      c[0] = mfma(a[0].p[i], b[0].p[s - i], c[0]);
+      c[1] = mfma(a[1].p[i], b[0].p[s - i], c[1]);
+      c[2] = mfma(a[2].p[i], b[0].p[s - i], c[2]);
+      c[3] = mfma(a[4].p[i], b[0].p[s - i], c[3]);
+      d[0] = mfma(a[3].p[i], b[1].p[s - i], d[0]);
+      d[1] = mfma(a[5].p[i], b[1].p[s - i], d[1]);
+    }
+  c[2] += d[0];
+  c[3] += d[1];
 }
 __device__ __forceinline__ void store_tri(uint16_t* m, int index, int lane, const Frag<3>& f) {
 #pragma unroll
