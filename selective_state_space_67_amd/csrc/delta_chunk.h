@@ -7,9 +7,14 @@
 
 namespace ssm {
 
-// Per (batch row, value head) and chunk the preparation leaves in the workspace:
-// the chunk's scalars, T = (I + A)^-1 and, for the forward, P = M o QK^T; for
-// the backward T^T and P^T.
+// Per (batch row, value head) and chunk the preparation leaves a record in the
+// workspace: T = (I + A)^-1, P = M o QK^T and the chunk's scalars; for the backward
+// T, T^T, P^T and the scalars.
+constexpr int kRecT = 0, kRecP = kTriBytes, kRecGates = 2 * kTriBytes;
+constexpr int kRecBytes = kRecGates + kGateFloats * 4;
+constexpr int kRecTt = kTriBytes, kRecPt = 2 * kTriBytes, kRecGatesBwd = 3 * kTriBytes;
+constexpr int kRecBytesBwd = kRecGatesBwd + kGateFloats * 4;
+
 struct ChunkArgs {
   int64_t L;
   int Hk, Hv, dk, dv, group;
@@ -24,11 +29,7 @@ struct ChunkArgs {
   const float* A;
   const uint8_t* reset;
   float scale, beta_scale;
-  float* gates;   // (bh, chunk, kGateFloats)
-  uint16_t* T;    // (bh, chunk, kTriEntries)
-  uint16_t* P;    // forward
-  uint16_t* Tt;   // backward
-  uint16_t* Pt;
+  char* records;  // (bh, chunk)
 };
 
 inline ChunkArgs chunk_args(const DeltaPlan& p, int chunks) {
@@ -64,7 +65,7 @@ inline bool delta_vec(const DeltaPlan& p) {
   return p.dk % 8 == 0 && p.qs % per == 0 && p.ks % per == 0 && delta_aligned(p.q, 16) && delta_aligned(p.k, 16);
 }
 
-// Prepare every chunk (delta_chunk.hip). bwd: leave T^T and P^T in place of P.
+// Prepare every chunk (delta_chunk.hip); bwd: the backward's records.
 hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd, hipStream_t stream);
 
 }  // namespace ssm

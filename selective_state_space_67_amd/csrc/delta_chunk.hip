@@ -44,7 +44,7 @@ struct ChunkGates {
 // One wave, a lane per token. The sums are taken in double and kept in two floats,
 // so that differences of them keep a small decay's precision next to large ones.
 template <typename InT>
-__device__ __forceinline__ void chunk_gates(const ChunkArgs& a, int b, int h, int chunk, int64_t record, int lane,
+__device__ __forceinline__ void chunk_gates(const ChunkArgs& a, int b, int h, int chunk, float* out, int lane,
                                             ChunkGates* s) {
   const int64_t t = static_cast<int64_t>(chunk) * kChunk + lane;
   const bool valid = t < a.L;
@@ -78,7 +78,6 @@ __device__ __forceinline__ void chunk_gates(const ChunkArgs& a, int b, int h, in
   s->lo[lane] = static_cast<float>(g - hi);
   s->beta[lane] = beta;
   s->seg[lane] = seg;
-  float* out = a.gates + record * kGateFloats;
   out[kE0 + lane] = seg == 0 ? fast_exp2(static_cast<float>(g)) : 0.0f;
   out[kEC + lane] = seg == seg_last ? fast_exp2(static_cast<float>(last - g)) : 0.0f;
   out[kBeta + lane] = beta;
@@ -118,7 +117,9 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_prepare(const ChunkArgs 
   const InT* q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
   const InT* k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
 
-  if (w == 0) chunk_gates<InT>(a, b, h, chunk, record, lane, &gates);
+  char* rec = a.records + record * (BWD ? kRecBytesBwd : kRecBytes);
+  if (w == 0)
+    chunk_gates<InT>(a, b, h, chunk, reinterpret_cast<float*>(rec + (BWD ? kRecGatesBwd : kRecGates)), lane, &gates);
 
   // S[k][j]: rows k, columns j (j < k <= w, and the diagonal k = j = w); with BWD
   // also R[k][i]: rows k, columns i (w <= k < i). P[j]: rows j, columns w;
@@ -221,12 +222,12 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_prepare(const ChunkArgs 
     for (int r = 0; r < 4; ++r) t[r] = -diag[j][g4 + r][col];
     Tr[j] = mfma4(t, sum, zero);
   }
-  uint16_t* T = a.T + record * kTriEntries;
+  uint16_t* T = reinterpret_cast<uint16_t*>(rec + kRecT);
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks)
     if (ks <= w / 2) store_tri(T, tri_index(w, ks), lane, split8(Tr[2 * ks], Tr[2 * ks + 1]));
   if constexpr (!BWD) {
-    uint16_t* Pm = a.P + record * kTriEntries;
+    uint16_t* Pm = reinterpret_cast<uint16_t*>(rec + kRecP);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
       if (ks <= w / 2) store_tri(Pm, tri_index(w, ks), lane, split8(P[2 * ks], P[2 * ks + 1]));
@@ -246,8 +247,8 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_prepare(const ChunkArgs 
       const f32x4 t = *reinterpret_cast<const f32x4*>(&diag[i][col][g4]);
       Tc[i] = mfma4(-t, sum, zero);
     }
-    uint16_t* Tt = a.Tt + record * kTriEntries;
-    uint16_t* Pt = a.Pt + record * kTriEntries;
+    uint16_t* Tt = reinterpret_cast<uint16_t*>(rec + kRecTt);
+    uint16_t* Pt = reinterpret_cast<uint16_t*>(rec + kRecPt);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
       if (ks >= w / 2) {
@@ -296,14 +297,15 @@ struct ScanArgs {
 constexpr int kWaves = kThreads / 64;
 constexpr int kBlockCols = 16 * kWaves;  // columns of the state per workgroup
 
-// What a workgroup stages of one chunk, in bytes from the stage's start.
-template <typename InT, int NP, int KS, bool AGG, bool QLDS>
+// What a workgroup stages of one chunk, in bytes from the stage's start. T, the
+// first OP parts of P and the scalars keep the record's order.
+template <typename InT, int NP, int KS, bool AGG, bool QLDS, int OP>
 struct Stage {
   static constexpr int kK = 0;
   static constexpr int kQ = kK + TokenTile<NP, KS>::kBytes;
   static constexpr int kT = kQ + (!AGG && QLDS ? TokenTile<NP, KS>::kBytes : 0);
-  static constexpr int kP = kT + kTriEntries * 2;
-  static constexpr int kGates = kP + (AGG ? 0 : kTriEntries * 2);
+  static constexpr int kP = kT + kTriBytes;
+  static constexpr int kGates = kP + (AGG ? 0 : kTriBytes / 3 * OP);
   static constexpr int kV = kGates + kGateFloats * 4;  // (64, kBlockCols) of InT
   static constexpr int kBytes = kV + kChunk * kBlockCols * static_cast<int>(sizeof(InT));
 };
@@ -314,9 +316,7 @@ struct ChunkSource {
   const InT* q;
   const InT* k;
   const InT* v;  // the chunk's first token, column 0 of the head
-  const uint16_t* T;
-  const uint16_t* P;
-  const float* gates;
+  const char* record;
   int n_tokens;
 };
 
@@ -324,62 +324,70 @@ template <typename InT>
 __device__ __forceinline__ ChunkSource<InT> chunk_source(const ChunkArgs& a, int bh, int b, int h, int c) {
   ChunkSource<InT> s;
   const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk;
-  const int64_t record = static_cast<int64_t>(bh) * a.chunks + c;
   const int hk = h / a.group;
   s.q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
   s.k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
   s.v = static_cast<const InT*>(a.v) + t0 * a.vs + static_cast<int64_t>(h) * a.dv;
-  s.T = a.T + record * kTriEntries;
-  s.P = a.P + record * kTriEntries;
-  s.gates = a.gates + record * kGateFloats;
+  s.record = a.records + (static_cast<int64_t>(bh) * a.chunks + c) * kRecBytes;
   s.n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(c) * kChunk));
   return s;
 }
 
 // ASYNC staging: whole 16-byte runs straight into LDS, 1 KB a wave and instruction.
 // Tokens past the end repeat the last one (their beta is 0, so they change
-// nothing), columns past dv repeat the last ones (never stored).
-template <typename InT, int KS, bool AGG>
-__device__ __forceinline__ void stage_async(char* st, const ChunkArgs& a, const ChunkSource<InT>& s, int col0, int lane,
+// nothing), columns past dv repeat the last ones (never stored). A lane's byte
+// offsets from the chunk's first token are the same for every whole chunk.
+struct LaneOffsets {
+  uint32_t k, q, v[2];
+};
+
+__device__ __forceinline__ LaneOffsets lane_offsets(const ChunkArgs& a, int n_tokens, int col0, int lane, int wave) {
+  LaneOffsets o;
+  const int last = n_tokens - 1, row = min(wave * 16 + (lane & 15), last);  // wave w: row tile w
+  o.k = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ks) * 2 + (lane >> 4) * 16;
+  o.q = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.qs) * 2 + (lane >> 4) * 16;
+  const int col = max(0, min(col0 + (lane & 7) * 8, a.dv - 8));
+#pragma unroll
+  for (int i = 0; i < 2; ++i)  // 8 tokens of 64 columns
+    o.v[i] = static_cast<uint32_t>(min((wave * 2 + i) * 8 + lane / 8, last)) * static_cast<uint32_t>(a.vs) * 2 + col * 2;
+  return o;
+}
+
+template <typename InT, int KS, bool AGG, int OP>
+__device__ __forceinline__ void stage_async(char* st, const ChunkSource<InT>& s, const LaneOffsets& o, int lane,
                                             int wave) {
-  using S = Stage<InT, 1, KS, AGG, true>;
-  const int last = s.n_tokens - 1;
+  using S = Stage<InT, 1, KS, AGG, true, OP>;
+  static_assert(kWaves == 4, "row tile w and values 16 w .. of wave w");
+  const char *k = reinterpret_cast<const char*>(s.k), *q = reinterpret_cast<const char*>(s.q);
+  const char* v = reinterpret_cast<const char*>(s.v);
 #pragma unroll
-  for (int i = 0; i < 4 * KS / kWaves; ++i) {  // wave w: row tile w
-    const int token = min(wave * 16 + (lane & 15), last), d = i * 32 + (lane >> 4) * 8, f = wave * KS + i;
-    load_to_lds(s.k + token * a.ks + d, st + S::kK + f * 1024);
-    if constexpr (!AGG) load_to_lds(s.q + token * a.qs + d, st + S::kQ + f * 1024);
+  for (int i = 0; i < KS; ++i) {
+    load_to_lds(k + i * 64 + o.k, st + S::kK + (wave * KS + i) * 1024);
+    if constexpr (!AGG) load_to_lds(q + i * 64 + o.q, st + S::kQ + (wave * KS + i) * 1024);
   }
+  const uint32_t own = lane * 16;
+  constexpr int kTri = (AGG ? kTriBytes : kTriBytes + kTriBytes / 3 * OP) / 1024;
 #pragma unroll
-  for (int i = 0; i < (kTriFrags * 3 + kWaves - 1) / kWaves; ++i) {
+  for (int i = 0; i < (kTri + kWaves - 1) / kWaves; ++i) {
     const int f = wave + i * kWaves;
-    if (f < kTriFrags * 3) {
-      load_to_lds(s.T + f * 512 + lane * 8, st + S::kT + f * 1024);
-      if constexpr (!AGG) load_to_lds(s.P + f * 512 + lane * 8, st + S::kP + f * 1024);
-    }
+    if (f < kTri) load_to_lds(s.record + f * 1024 + own, st + S::kT + f * 1024);
   }
-  if (wave == 0) load_to_lds(s.gates + lane * 4, st + S::kGates);
+  if (wave == 3) load_to_lds(s.record + kRecGates + own, st + S::kGates);
 #pragma unroll
-  for (int i = 0; i < 8 / kWaves; ++i) {  // 8 tokens of 64 columns
-    const int f = wave + i * kWaves, token = min(f * 8 + lane / 8, last);
-    const int col = max(0, min(col0 + (lane & 7) * 8, a.dv - 8));
-    load_to_lds(s.v + token * a.vs + col, st + S::kV + f * 1024);
-  }
+  for (int i = 0; i < 2; ++i) load_to_lds(v + o.v[i], st + S::kV + (wave * 2 + i) * 1024);
 }
 
 // Staging through registers, for float32 and for rows that are not whole runs.
-template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS>
+template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS, int OP>
 __device__ __forceinline__ void stage_sync(char* st, const ChunkArgs& a, const ChunkSource<InT>& s, int col0) {
-  using S = Stage<InT, NP, KS, AGG, QLDS>;
+  using S = Stage<InT, NP, KS, AGG, QLDS, OP>;
   stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kK), s.k, a.ks, s.n_tokens, 0, a.dk);
   if constexpr (!AGG && QLDS)
     stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kQ), s.q, a.qs, s.n_tokens, 0, a.dk);
-  constexpr int kRuns = kTriEntries / 8;
-  for (int i = threadIdx.x; i < kRuns; i += kThreads) {
-    reinterpret_cast<u32x4*>(st + S::kT)[i] = reinterpret_cast<const u32x4*>(s.T)[i];
-    if constexpr (!AGG) reinterpret_cast<u32x4*>(st + S::kP)[i] = reinterpret_cast<const u32x4*>(s.P)[i];
-  }
-  reinterpret_cast<float*>(st + S::kGates)[threadIdx.x] = s.gates[threadIdx.x];
+  constexpr int kRuns = (AGG ? kTriBytes : kTriBytes + kTriBytes / 3 * OP) / 16;
+  for (int i = threadIdx.x; i < kRuns; i += kThreads)
+    reinterpret_cast<u32x4*>(st + S::kT)[i] = reinterpret_cast<const u32x4*>(s.record)[i];
+  reinterpret_cast<float*>(st + S::kGates)[threadIdx.x] = reinterpret_cast<const float*>(s.record + kRecGates)[threadIdx.x];
   InT* v = reinterpret_cast<InT*>(st + S::kV);
 #pragma unroll
   for (int i = 0; i < kChunk * kBlockCols / kThreads; ++i) {
@@ -393,10 +401,12 @@ __device__ __forceinline__ void stage_sync(char* st, const ChunkArgs& a, const C
 // One wave's walk over the chunks of a piece with 16 columns of the state.
 // AGG: the aggregates walk (no read-out; the first 32 KS columns start from the
 // identity). With two stages the next chunk is loaded while this one is worked on.
-template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS, bool ASYNC, int STAGES>
+// OP: parts of the products that only the output sees; two (2^-17) where it is
+// rounded to bfloat16 (2^-9).
+template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS, bool ASYNC, int STAGES, int OP>
 __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
   using Tile = TokenTile<NP, KS>;
-  using S = Stage<InT, NP, KS, AGG, QLDS>;
+  using S = Stage<InT, NP, KS, AGG, QLDS, OP>;
   constexpr int DKT = 2 * KS;  // row tiles of the state
   extern __shared__ __align__(16) char staged[];
   const ChunkArgs& a = s.c;
@@ -429,22 +439,31 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
   }
 
   const int c0 = piece * s.chunks_piece, c1 = min(a.chunks, c0 + s.chunks_piece);
-  if constexpr (STAGES == 2) stage_async<InT, KS, AGG>(staged, a, chunk_source<InT>(a, bh, b, h, c0), col0, lane, wave);
+  ChunkSource<InT> src = chunk_source<InT>(a, bh, b, h, c0);
+  const LaneOffsets whole = lane_offsets(a, kChunk, col0, lane, wave);
+  const auto stage = [&](char* st, const ChunkSource<InT>& from) {
+    if constexpr (ASYNC)
+      stage_async<InT, KS, AGG, OP>(
+          st, from, from.n_tokens == kChunk ? whole : lane_offsets(a, from.n_tokens, col0, lane, wave), lane, wave);
+    else
+      stage_sync<InT, NP, KS, VEC, AGG, QLDS, OP>(st, a, from, col0);
+  };
+  if constexpr (STAGES == 2) stage(staged, src);
   for (int c = c0; c < c1; ++c) {
     char* st = staged + (STAGES == 2 ? ((c - c0) & 1) * S::kBytes : 0);
-    const ChunkSource<InT> src = chunk_source<InT>(a, bh, b, h, c);
+    ChunkSource<InT> next = src;
+    next.q += kChunk * a.qs;
+    next.k += kChunk * a.ks;
+    next.v += kChunk * a.vs;
+    next.record += kRecBytes;
+    next.n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(c + 1) * kChunk));
     if constexpr (STAGES == 2) {
       wait_loads();
       __syncthreads();  // this stage is loaded, and the other one is no longer read
-      if (c + 1 < c1)
-        stage_async<InT, KS, AGG>(staged + ((c + 1 - c0) & 1) * S::kBytes, a, chunk_source<InT>(a, bh, b, h, c + 1),
-                                  col0, lane, wave);
+      if (c + 1 < c1) stage(staged + ((c + 1 - c0) & 1) * S::kBytes, next);
     } else {
       __syncthreads();  // the previous chunk is no longer read
-      if constexpr (ASYNC)
-        stage_async<InT, KS, AGG>(st, a, src, col0, lane, wave);
-      else
-        stage_sync<InT, NP, KS, VEC, AGG, QLDS>(st, a, src, col0);
+      stage(st, src);
       wait_loads();
       __syncthreads();
     }
@@ -468,7 +487,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
         }
       }
       mma_n(kf, hb, X);
-      if constexpr (!AGG) mma_n(qf, hb, Y);
+      if constexpr (!AGG) mma_n<OP>(qf, hb, Y);
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -500,7 +519,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
     }
     if constexpr (!AGG) {
       const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
-      mma_tri(reinterpret_cast<const uint16_t*>(st + S::kP), ub, lane, Y);
+      mma_tri<OP>(reinterpret_cast<const uint16_t*>(st + S::kP), ub, lane, Y);
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) U[m] *= *reinterpret_cast<const f32x4*>(gates + kEC + m * 16 + g4);
@@ -518,38 +537,43 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
 
     if constexpr (!AGG) {
       const int64_t row0 = (static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk) * a.Hv + h;  // x dv
-      if (sizeof(InT) == 2 && s.out_bf16 && s.out_runs) {
+      if (OP == 2 && (ASYNC || s.out_runs)) {  // ASYNC has whole runs everywhere
         // The strip's place among the staged values is this wave's alone and has been
         // read: the outputs turn there from columns to rows, 16 bytes a lane.
         uint16_t* o = reinterpret_cast<uint16_t*>(st + S::kV) + wave * 16;
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            store_elem(reinterpret_cast<bf16_t*>(o), (m * 16 + g4 + r) * kBlockCols + (lane & 15), a.scale * Y[m][r]);
+          for (int r = 0; r < 4; r += 2) {
+            const uint32_t w = bf16_words(a.scale * Y[m][r], a.scale * Y[m][r + 1]);
+            uint16_t* p = o + (m * 16 + g4 + r) * kBlockCols + (lane & 15);
+            p[0] = static_cast<uint16_t>(w);
+            p[kBlockCols] = static_cast<uint16_t>(w >> 16);
+          }
+        char* dst = static_cast<char*>(s.out) + (row0 * a.dv + col0 + wave * 16) * 2;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int token = i * 32 + lane / 2, half = (lane & 1) * 8;
           const u32x4 w = *reinterpret_cast<const u32x4*>(o + token * kBlockCols + half);
-          const int col = col0 + wave * 16 + half;
-          if (token < src.n_tokens && col < a.dv)
-            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(s.out) + (row0 + static_cast<int64_t>(token) * a.Hv) * a.dv + col) = w;
+          if (token < src.n_tokens && col0 + wave * 16 + half < a.dv)
+            *reinterpret_cast<u32x4*>(dst + static_cast<uint32_t>(token * a.Hv * a.dv + half) * 2) = w;
         }
       } else {
+        const int64_t step = static_cast<int64_t>(a.Hv) * a.dv;  // elements between tokens
+        const int64_t lane0 = row0 * a.dv + g4 * step + own;
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int token = m * 16 + g4 + r;
-            if (!has_v || token >= src.n_tokens) continue;
-            const int64_t o = (row0 + static_cast<int64_t>(token) * a.Hv) * a.dv + own;
-            if (s.out_bf16)
-              store_elem(static_cast<bf16_t*>(s.out), o, a.scale * Y[m][r]);
+            if (!has_v || m * 16 + g4 + r >= src.n_tokens) continue;
+            if (OP == 2 || s.out_bf16)
+              store_elem(static_cast<bf16_t*>(s.out) + (m * 16 + r) * step, lane0, a.scale * Y[m][r]);
             else
-              store_elem(static_cast<float*>(s.out), o, a.scale * Y[m][r]);
+              store_elem(static_cast<float*>(s.out) + (m * 16 + r) * step, lane0, a.scale * Y[m][r]);
           }
       }
     }
+    src = next;
   }
 
   if (AGG) {
@@ -644,15 +668,15 @@ int padded_ks(int dk) {
 
 constexpr int kMaxLds = 160 * 1024;
 
-template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS, bool ASYNC>
+template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS, bool ASYNC, int OP>
 hipError_t launch_walk(const ScanArgs& s, int64_t blocks, hipStream_t stream) {
-  constexpr int kBytes = Stage<InT, NP, KS, AGG, QLDS>::kBytes;
+  constexpr int kBytes = Stage<InT, NP, KS, AGG, QLDS, OP>::kBytes;
   constexpr int STAGES = ASYNC && 2 * kBytes <= kMaxLds ? 2 : 1;
   static_assert(kBytes <= kMaxLds, "a chunk's stage exceeds LDS");
   SSM_LOG("launch delta_chunk_scan<%d parts, %d rows, aggregates %d>: %d pieces of %d chunks, %d stages of %d bytes; "
           "grid %lld x %d threads",
           NP, 32 * KS, AGG, s.pieces, s.chunks_piece, STAGES, kBytes, static_cast<long long>(blocks), kThreads);
-  hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, VEC, AGG, QLDS, ASYNC, STAGES>),
+  hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, VEC, AGG, QLDS, ASYNC, STAGES, OP>),
                      dim3(static_cast<unsigned>(blocks)), dim3(kThreads), STAGES * kBytes, stream, s);
   return hipGetLastError();
 }
@@ -660,12 +684,12 @@ hipError_t launch_walk(const ScanArgs& s, int64_t blocks, hipStream_t stream) {
 template <typename InT, int NP, int KS, bool VEC, bool ASYNC>
 hipError_t launch_scan_ks(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs s, hipStream_t stream) {
   // K and Q of a chunk side by side fit in LDS except for float32 past 128 entries
-  constexpr bool QLDS = Stage<InT, NP, KS, false, true>::kBytes <= kMaxLds;
+  constexpr bool QLDS = Stage<InT, NP, KS, false, true, 3>::kBytes <= kMaxLds;
   const int64_t heads = p.B * p.Hv;
   if (plan.pieces > 1) {
     const int strips = 2 * KS + s.cols / 16;
     s.col_blocks = (strips + kWaves - 1) / kWaves;
-    hipError_t e = launch_walk<InT, NP, KS, VEC, true, QLDS, ASYNC>(s, heads * plan.pieces * s.col_blocks, stream);
+    hipError_t e = launch_walk<InT, NP, KS, VEC, true, QLDS, ASYNC, 3>(s, heads * plan.pieces * s.col_blocks, stream);
     if (e != hipSuccess) return e;
     FoldArgs f{s.agg, s.h0, const_cast<float*>(s.starts), plan.pieces, p.dk, p.dv, s.cols, s.cols / 16};
     SSM_LOG("launch delta_fold<%d rows>: grid %lld x %d threads", 32 * KS, static_cast<long long>(heads * f.strips),
@@ -674,7 +698,9 @@ hipError_t launch_scan_ks(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs 
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   s.col_blocks = (s.cols / 16 + kWaves - 1) / kWaves;
-  return launch_walk<InT, NP, KS, VEC, false, QLDS, ASYNC>(s, heads * plan.pieces * s.col_blocks, stream);
+  const int64_t blocks = heads * plan.pieces * s.col_blocks;
+  if (NP == 1 && s.out_bf16) return launch_walk<InT, NP, KS, VEC, false, QLDS, ASYNC, NP == 1 ? 2 : 3>(s, blocks, stream);
+  return launch_walk<InT, NP, KS, VEC, false, QLDS, ASYNC, 3>(s, blocks, stream);
 }
 
 template <typename InT, int NP, bool VEC, bool ASYNC>
@@ -712,12 +738,8 @@ DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int 
   const size_t rows = 32 * static_cast<size_t>(padded_ks(dk)), cols = (static_cast<size_t>(dv) + 15) / 16 * 16;
   const size_t piece_heads = static_cast<size_t>(B) * Hv * d.pieces;
   size_t off = 0;
-  d.off_gates = off;
-  off += align256(records * kGateFloats * sizeof(float));
-  d.off_T = off;
-  off += align256(records * kTriEntries * sizeof(uint16_t));
-  d.off_P = off;
-  off += align256(records * kTriEntries * sizeof(uint16_t));
+  d.off_records = off;
+  off += records * kRecBytes;
   d.off_agg = off;
   if (d.pieces > 1) off += align256(piece_heads * rows * (rows + cols) * sizeof(float));
   d.off_starts = off;
@@ -730,9 +752,7 @@ hipError_t launch_delta_chunks(const DeltaPlan& p, const DeltaChunks& plan, void
   char* ws = static_cast<char*>(workspace);
   ScanArgs s{};
   s.c = chunk_args(p, plan.chunks);
-  s.c.gates = reinterpret_cast<float*>(ws + plan.off_gates);
-  s.c.T = reinterpret_cast<uint16_t*>(ws + plan.off_T);
-  s.c.P = reinterpret_cast<uint16_t*>(ws + plan.off_P);
+  s.c.records = ws + plan.off_records;
   hipError_t e = launch_chunk_prepare(p, s.c, false, stream);
   if (e != hipSuccess) return e;
   s.pieces = plan.pieces;
@@ -746,13 +766,16 @@ hipError_t launch_delta_chunks(const DeltaPlan& p, const DeltaChunks& plan, void
   }
   s.out = p.out;
   s.h_last = p.h_last;
-  s.out_runs = p.dv % 8 == 0 && delta_aligned(p.out, 16);
+  // a chunk's rows of out lie within 2^31 bytes (for 32-bit offsets)
+  const int64_t reach = int64_t{1} << 24;  // elements a token
+  s.out_runs = p.dv % 8 == 0 && delta_aligned(p.out, 16) && static_cast<int64_t>(p.Hv) * p.dv < reach;
   const bool vec = delta_vec(p);
   if (!p.in_bf16)
     return vec ? launch_scan_vec<float, 3, true, false>(p, plan, s, stream)
                : launch_scan_vec<float, 3, false, false>(p, plan, s, stream);
   // Straight loads to LDS: rows that fill the padded tile, values in whole runs.
-  const bool async = vec && p.dk == 32 * padded_ks(p.dk) && p.dv % 8 == 0 && p.vs % 8 == 0 && delta_aligned(p.v, 16);
+  const bool async = vec && p.dk == 32 * padded_ks(p.dk) && p.dv % 8 == 0 && p.vs % 8 == 0 && delta_aligned(p.v, 16) &&
+                     p.qs < reach && p.ks < reach && p.vs < reach && (s.out_runs || !p.out_bf16);
   if (async) return launch_scan_vec<bf16_t, 1, true, true>(p, plan, s, stream);
   return vec ? launch_scan_vec<bf16_t, 1, true, false>(p, plan, s, stream)
              : launch_scan_vec<bf16_t, 1, false, false>(p, plan, s, stream);

@@ -3,7 +3,7 @@
 // Every product is v_mfma_f32_16x16x32_bf16 with float32 sums. A float32
 // operand goes in as three bfloat16 parts that add up to it exactly (8 bits of
 // the significand each); a bfloat16 input is its own single part. Products of
-// parts below 2^-24 of the whole are left out, so an operand costs 3 products
+// parts below 2^-26 of the whole are left out, so an operand costs 3 products
 // against an input part and 6 against another split operand, and results carry
 // float32's precision. (The float32 matrix instructions run at 1/16 of the
 // bfloat16 rate.)
@@ -44,21 +44,23 @@ struct Frag {
   u32x4 p[NP];
 };
 
-// The upper halves of two floats as one word (lo in the low half).
-__device__ __forceinline__ uint32_t upper_pair(float lo, float hi) {
-  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
-}
-__device__ __forceinline__ float below(float x) {  // x without its upper half: exact
-  return x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+// Two floats rounded to bfloat16 (nearest even), lo in the low half: one conversion.
+__device__ __forceinline__ uint32_t bf16_words(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
-// Two floats in three parts.
+// Two floats in three parts, each the rest rounded to bfloat16: the rest after two
+// roundings to 8 bits has at most 8 left, so the three add up exactly, and a part is
+// at most 2^-9 of the one before it.
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[3]) {
-  w[0] = upper_pair(a, b);
-  a = below(a);
-  b = below(b);
-  w[1] = upper_pair(a, b);
-  w[2] = upper_pair(below(a), below(b));
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    w[i] = bf16_words(a, b);
+    a -= __uint_as_float(w[i] << 16);
+    b -= __uint_as_float(w[i] & 0xFFFF0000u);
+  }
 }
 
 // Two D tiles (or any two runs of four) as a split operand.
@@ -108,10 +110,12 @@ __device__ __forceinline__ int state_row(int m, int g4, int r) { return (m >> 1)
 
 // c[n] += a[n] b for N independent sums, in turns: a sum's next product waits for
 // its last one, the others' do not.
-template <int N, int NA, int NB>
+// PARTS: 3 for float32's precision, 2 for 2^-17 of the operands (products of parts
+// whose places add up to less than PARTS are kept).
+template <int PARTS = 3, int N, int NA, int NB>
 __device__ __forceinline__ void mma_n(const Frag<NA> (&a)[N], const Frag<NB>& b, f32x4 (&c)[N]) {
 #pragma unroll
-  for (int s = 2; s >= 0; --s)
+  for (int s = PARTS - 1; s >= 0; --s)
 #pragma unroll
     for (int i = 0; i < NA; ++i)
       if (s - i >= 0 && s - i < NB)
@@ -232,28 +236,38 @@ __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70
 
 // A chunk's triangular 64 x 64 matrix as split A operands in global memory: for
 // row tile mi the summed tiles ks <= mi / 2 (mi, ks) -> 6 operands, or for its
-// transpose ks >= mi / 2; each 3 parts x 64 lanes x 8 entries.
+// transpose ks >= mi / 2; three parts x 6 operands x 64 lanes x 8 entries.
 constexpr int kTriFrags = 6;
 constexpr int kTriEntries = kTriFrags * 3 * 64 * 8;
+constexpr int kTriBytes = kTriEntries * 2;
 __host__ __device__ constexpr int tri_index(int mi, int ks) { return mi < 2 ? mi : 2 + (mi - 2) * 2 + ks; }
 // transposed: row tiles 0 and 1 sum over both halves, 2 and 3 over the second
 __host__ __device__ constexpr int tri_t_index(int mi, int ks) { return mi < 2 ? mi * 2 + ks : mi + 2; }
 
-__device__ __forceinline__ Frag<3> load_tri(const uint16_t* m, int index, int lane) {
-  Frag<3> f;
+// `parts` of operand `index`; parts lie one after another.
+template <int PARTS>
+__device__ __forceinline__ Frag<PARTS> load_tri(const uint16_t* m, int index, int lane) {
+  Frag<PARTS> f;
 #pragma unroll
-  for (int i = 0; i < 3; ++i) f.p[i] = *reinterpret_cast<const u32x4*>(m + ((index * 3 + i) * 64 + lane) * 8);
+  for (int i = 0; i < PARTS; ++i)
+    f.p[i] = *reinterpret_cast<const u32x4*>(m + ((i * kTriFrags + index) * 64 + lane) * 8);
   return f;
 }
+__device__ __forceinline__ void store_tri(uint16_t* m, int index, int lane, const Frag<3>& f) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(m + ((i * kTriFrags + index) * 64 + lane) * 8) = f.p[i];
+}
+
 // c[m] += M[m][.] b for the four row tiles of a staged triangle M (rows m sum over
 // the halves ks <= m / 2): six independent sums in turns.
+template <int PARTS = 3>
 __device__ __forceinline__ void mma_tri(const uint16_t* m, const Frag<3> (&b)[2], int lane, f32x4 (&c)[4]) {
-  Frag<3> a[6];
+  Frag<PARTS> a[6];
 #pragma unroll
-  for (int i = 0; i < 6; ++i) a[i] = load_tri(m, i, lane);
+  for (int i = 0; i < 6; ++i) a[i] = load_tri<PARTS>(m, i, lane);
   f32x4 d[2] = {};
 #pragma unroll
-  for (int s = 2; s >= 0; --s)
+  for (int s = PARTS - 1; s >= 0; --s)
 #pragma unroll
     for (int i = 0; i <= s; ++i) {
       c[0] = mfma(a[0].p[i], b[0].p[s - i], c[0]);
@@ -266,12 +280,8 @@ __device__ __forceinline__ void mma_tri(const uint16_t* m, const Frag<3> (&b)[2]
   c[2] += d[0];
   c[3] += d[1];
 }
-__device__ __forceinline__ void store_tri(uint16_t* m, int index, int lane, const Frag<3>& f) {
-#pragma unroll
-  for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(m + ((index * 3 + i) * 64 + lane) * 8) = f.p[i];
-}
 
-// Per-chunk scalars in global memory: e0, eC and beta of the 64 tokens, aC.
+// Per-chunk scalars: e0, eC and beta of the 64 tokens, aC.
 //   e0 = exp(sum of log decays from the chunk's start through the token), 0 after a reset
 //   eC = exp(sum after the token to the chunk's end), 0 before a reset
 //   aC = e0 of the last token: the whole chunk's decay

@@ -39,7 +39,7 @@ hipError_t launch_delta_steps(const DeltaPlan& plan, hipStream_t stream);
 // many chunks, the pieces the sequence is split into, and the workspace layout.
 struct DeltaChunks {
   int chunks, pieces, chunks_piece;
-  size_t off_gates, off_T, off_P, off_agg, off_starts, bytes;
+  size_t off_records, off_agg, off_starts, bytes;
 };
 // requested = 0: automatic. Pure host arithmetic.
 DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int requested);
