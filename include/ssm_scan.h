@@ -431,7 +431,7 @@ ssm_status ssm_scan_bwd(const ssm_scan_bwd_params* p, void* hip_stream);
  * weight); other keys are computed as given.
  *
  *   batch, seqlen : B >= 0, 0 <= L < 2^27
- *   key_heads     : Hk; value_heads : Hv, a multiple of Hk (Hk >= 1 unless Hv = 0)
+ *   key_heads     : Hk; value_heads : Hv, a multiple of Hk (both 0, or neither)
  *   dk            : 1 <= dk <= SSM_MAX_DSTATE;  dv : 1 <= dv <= 65536
  *   in_dtype  : element type of q, k, v, dt_raw, beta_raw
  *   q, k     (B,L,Hk,dk) required; v (B,L,Hv,dv) required. Heads are dense
@@ -451,8 +451,11 @@ ssm_status ssm_scan_bwd(const ssm_scan_bwd_params* p, void* hip_stream);
  *            aligned to 256; contents on entry ignored.
  *   num_segments : 0 = the library chooses how many pieces to split L into;
  *            k >= 1 asks for k pieces (clamped to what L allows).
- * Arithmetic is float32 whatever in_dtype is; only out is rounded, to out_dtype.
- * Outputs must not overlap inputs, each other or the workspace.
+ * Arithmetic has float32's precision whatever in_dtype is (products on the matrix
+ * cores carry each operand in three bfloat16 parts, 24 bits, with float32 sums); only
+ * out is rounded, to out_dtype. Outputs must not overlap inputs, each other or the
+ * workspace. A non-finite input may make every output of its head NaN from the start
+ * of its 64-step chunk on, also past a reset.
  */
 typedef struct {
   int64_t batch, seqlen, key_heads, value_heads, dk, dv;
@@ -509,6 +512,69 @@ typedef struct {
 
 /* Enqueue the decode window described by `p` on `hip_stream`. */
 ssm_status ssm_delta_update(const ssm_delta_update_params* p, void* hip_stream);
+
+/*
+ * Backward pass of ssm_delta_fwd: the gradients of
+ *
+ *   loss = sum dout * out + sum dh_last * h_last
+ *
+ * with respect to every input, for the forward's inputs (no intermediate of
+ * the forward is needed). Per step, in reverse time, with dH the adjoint of H_t:
+ *
+ *   dH += scale q_t dout_t^T;  dq_t = scale H_t dout_t
+ *   dr = beta_t dH^T k_t;  dv_t = dr;  dk_t = dH u_t - H' dr
+ *   d beta_raw_t = (dH^T k_t . u_t) (1 - beta_t / beta_scale)
+ *   dH' = dH - k_t dr^T;  dg_t = <dH', H'>;  dH_{t-1} = exp(g_t) dH'
+ *   d dt_raw_t = dg_t A sigmoid(dt_raw_t + dt_bias);  dA = sum dg_t softplus(..)
+ *
+ * (dg_t and dH_{t-1} are 0 where reset[b,t] is set). Gradients of a key head
+ * are the sums over its value heads.
+ *   batch .. h0, strides : the forward's
+ *   grad_dtype : element type of dq, dk, dv, d_dt_raw, dbeta_raw (all dense)
+ *   dout     (B,L,Hv,dv) required, in_dtype, dense
+ *   dh_last  (B,Hv,dk,dv) float32, NULL => 0
+ *   dq, dk   (B,L,Hk,dk), dv (B,L,Hv,dv), d_dt_raw, dbeta_raw (B,L,Hv) required outputs
+ *   dA       (Hv) float32, required output; d_dt_bias (Hv), dh0 (B,Hv,dk,dv)
+ *            float32 outputs, NULL => not written
+ *   workspace, workspace_bytes : at least ssm_delta_bwd_workspace_size() bytes,
+ *            aligned to 256. The states and adjoints at every 64-token chunk are
+ *            kept there (8 dk dv bytes per chunk and value head, dk rounded up to
+ *            a multiple of 32 and dv to 16, and 57 KB + 512 dv bytes besides).
+ * dA and d_dt_bias are sums in a fixed order, so repeated calls give identical bits.
+ */
+typedef struct {
+  int64_t batch, seqlen, key_heads, value_heads, dk, dv;
+  int32_t in_dtype, grad_dtype;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const void* dt_raw;
+  const void* beta_raw;
+  const float* dt_bias;
+  const float* A;
+  const uint8_t* reset;
+  const float* h0;
+  const void* dout;
+  const float* dh_last;
+  void* dq;
+  void* dk_out; /* gradient of k */
+  void* dv_out; /* gradient of v */
+  void* d_dt_raw;
+  void* dbeta_raw;
+  float* dA;
+  float* d_dt_bias;
+  float* dh0;
+  void* workspace;
+  size_t workspace_bytes;
+  float scale, beta_scale;
+} ssm_delta_bwd_params;
+
+/* Bytes of workspace ssm_delta_bwd needs (only sizes and dtypes of `p` are read). */
+ssm_status ssm_delta_bwd_workspace_size(const ssm_delta_bwd_params* p, size_t* bytes);
+
+/* Enqueue the backward pass described by `p` on `hip_stream`. */
+ssm_status ssm_delta_bwd(const ssm_delta_bwd_params* p, void* hip_stream);
 
 /*
  * Norms of queries and keys for each head, with the position rotation in the
@@ -590,7 +656,8 @@ int32_t ssm_version(void);
 /* sizeof of the parameter structs as compiled into the library:
  * which = 0 -> ssm_scan_params, 1 -> ssm_update_params,
  * 2 -> ssm_scan_bwd_params, 3 -> ssm_delta_params,
- * 4 -> ssm_delta_update_params, 6 -> ssm_qk_norm_params; 0 for anything else.
+ * 4 -> ssm_delta_update_params, 5 -> ssm_delta_bwd_params,
+ * 6 -> ssm_qk_norm_params; 0 for anything else.
  * Bindings compare these with their own layouts at load time. */
 size_t ssm_abi_struct_size(int32_t which);
 

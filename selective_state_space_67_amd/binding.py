@@ -86,7 +86,8 @@ EXPORTS = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_scan_fwd_noalloc", "s
            "ssm_scan_aggregate",
            "ssm_state_update", "ssm_scan_bwd_workspace_size", "ssm_scan_bwd", "ssm_status_string", "ssm_last_error",
            "ssm_version", "ssm_abi_struct_size",
-           "ssm_delta_workspace_size", "ssm_delta_fwd", "ssm_delta_update", "ssm_qk_norm_fwd",
+           "ssm_delta_workspace_size", "ssm_delta_fwd", "ssm_delta_update", "ssm_delta_bwd_workspace_size",
+           "ssm_delta_bwd", "ssm_qk_norm_fwd",
            "ssm_qk_norm_bwd_workspace_size", "ssm_qk_norm_bwd")
 
 _lib = None

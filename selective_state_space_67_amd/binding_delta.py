@@ -34,6 +34,13 @@ class DeltaUpdateParams(ctypes.Structure):
         ("out", _vp), ("scale", _f32), ("beta_scale", _f32)]
 
 
+class DeltaBwdParams(ctypes.Structure):
+    _fields_ = _HEAD + [("grad_dtype", _i32)] + _QKV + [
+        ("reset", _vp), ("h0", _vp), ("dout", _vp), ("dh_last", _vp), ("dq", _vp), ("dk_out", _vp), ("dv_out", _vp),
+        ("d_dt_raw", _vp), ("dbeta_raw", _vp), ("dA", _vp), ("d_dt_bias", _vp), ("dh0", _vp), ("workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t), ("scale", _f32), ("beta_scale", _f32)]
+
+
 class QkNormParams(ctypes.Structure):
     _fields_ = [("batch", _i64), ("seqlen", _i64), ("q_heads", _i64), ("k_heads", _i64), ("head_dim", _i64),
                 ("rot_dim", _i64), ("rot_positions", _i64), ("in_dtype", _i32), ("out_dtype", _i32),
@@ -44,17 +51,19 @@ class QkNormParams(ctypes.Structure):
                 ("reserved0", _i32)]
 
 
-STRUCTS = {3: DeltaParams, 4: DeltaUpdateParams, 6: QkNormParams}
+STRUCTS = {3: DeltaParams, 4: DeltaUpdateParams, 5: DeltaBwdParams, 6: QkNormParams}
 
 
 def declare(lib):
     """Prototypes of this module's entry points (called when the library is loaded)."""
     size = ctypes.POINTER(ctypes.c_size_t)
     for name, struct in (("ssm_delta_fwd", DeltaParams), ("ssm_delta_update", DeltaUpdateParams),
+                         ("ssm_delta_bwd", DeltaBwdParams),
                          ("ssm_qk_norm_fwd", QkNormParams), ("ssm_qk_norm_bwd", QkNormParams)):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = [ctypes.POINTER(struct), _vp], ctypes.c_int
     for name, struct in (("ssm_delta_workspace_size", DeltaParams),
+                         ("ssm_delta_bwd_workspace_size", DeltaBwdParams),
                          ("ssm_qk_norm_bwd_workspace_size", QkNormParams)):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = [ctypes.POINTER(struct), size], ctypes.c_int
@@ -196,6 +205,45 @@ def prepare_delta_update(h, q, k, v, dt_raw, A, beta_raw, *, dt_bias=None, out=N
 
     call.keep = ((h, q, k, v, dt_raw, A, beta_raw, dt_bias, out), p)
     return call
+
+
+def ssm_delta_bwd(q, k, v, dt_raw, A, beta_raw, dout, *, dt_bias=None, reset=None, h0=None, dh_last=None,
+                  grad_dtype=None, scale=None, beta_scale=1.0, want_d_dt_bias=True, want_dh0=True, workspace=None,
+                  stream=None):
+    """Backward pass of ssm_delta_fwd for the same inputs and the output gradient
+    dout (B, L, Hv, dv).
+
+    Returns a dict with dq, dk, dv, d_dt_raw, dbeta_raw in ``grad_dtype`` (float32 by
+    default) and float32 dA, d_dt_bias (Hv,), dh0 (B, Hv, dk, dv) (the last two None
+    when not asked for). dh_last is the gradient reaching h_last (None = 0). The
+    workspace is allocated when not given or too small.
+    """
+    import torch
+
+    lib = _b.load_library()
+    sizes, strides = _delta_inputs(q, k, v, dt_raw, A, beta_raw, dt_bias)
+    B, L, Hk, Hv, dk, dv = sizes
+    _b._need(dout, (B, L, Hv, dv), "dout", q.dtype)
+    if reset is not None:
+        _b._need(reset, (B, L), "reset", torch.uint8)
+    for t, name in ((h0, "h0"), (dh_last, "dh_last")):
+        if t is not None:
+            _b._need(t, (B, Hv, dk, dv), name, torch.float32)
+    gd, dev = grad_dtype or torch.float32, q.device
+    g = dict(dq=torch.empty((B, L, Hk, dk), dtype=gd, device=dev), dk=torch.empty((B, L, Hk, dk), dtype=gd, device=dev),
+             dv=torch.empty((B, L, Hv, dv), dtype=gd, device=dev), d_dt_raw=torch.empty((B, L, Hv), dtype=gd, device=dev),
+             dbeta_raw=torch.empty((B, L, Hv), dtype=gd, device=dev),
+             dA=torch.empty((Hv,), dtype=torch.float32, device=dev),
+             d_dt_bias=torch.empty((Hv,), dtype=torch.float32, device=dev) if want_d_dt_bias else None,
+             dh0=torch.empty((B, Hv, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None)
+    p = DeltaBwdParams(*sizes, _b._dtype_code(q), _b._dtype_code(g["dq"]), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                       *strides, dt_raw.data_ptr(), beta_raw.data_ptr(), _addr(dt_bias), A.data_ptr(), _addr(reset),
+                       _addr(h0), dout.data_ptr(), _addr(dh_last), g["dq"].data_ptr(), g["dk"].data_ptr(),
+                       g["dv"].data_ptr(), g["d_dt_raw"].data_ptr(), g["dbeta_raw"].data_ptr(), g["dA"].data_ptr(),
+                       _addr(g["d_dt_bias"]), _addr(g["dh0"]), None, 0, dk ** -0.5 if scale is None else scale, beta_scale)
+    workspace = _workspace(lib.ssm_delta_bwd_workspace_size, p, workspace, dev)
+    _b._check(lib.ssm_delta_bwd(ctypes.byref(p), _b._stream(stream, dev)))
+    return g
 
 
 def _norm_params(q, k, wq, wk, kind, eps, cos, sin, positions, interleaved):

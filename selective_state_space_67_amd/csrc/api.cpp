@@ -869,6 +869,7 @@ size_t ssm_abi_struct_size(int32_t which) {
   if (which == 2) return sizeof(ssm_scan_bwd_params);
   if (which == 3) return sizeof(ssm_delta_params);
   if (which == 4) return sizeof(ssm_delta_update_params);
+  if (which == 5) return sizeof(ssm_delta_bwd_params);
   if (which == 6) return sizeof(ssm_qk_norm_params);
   return 0;
 }

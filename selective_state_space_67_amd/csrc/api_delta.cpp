@@ -1,7 +1,7 @@
 // C-ABI front end of the gated delta rule and of the head norms
 // (include/ssm_scan.h). As in api.cpp, every check is host arithmetic on the
 // parameter struct and precedes the first HIP call. The launches live in
-// delta_step.hip, delta_chunk.hip and qk_norm.hip.
+// delta_step.hip, delta_chunk.hip, delta_chunk_bwd.hip and qk_norm.hip.
 #include <hip/hip_runtime.h>
 
 #include <limits>
@@ -59,7 +59,7 @@ ssm_status check_delta_sizes(const P* p, int64_t len, int32_t other_dtype, Delta
     return fail(SSM_ERR_BAD_SHAPE, "dv must be in [1, %lld] (got %lld)", (long long)kMaxColumns, (long long)p->dv);
   if (p->value_heads > kMaxHeads || p->key_heads > kMaxHeads)
     return fail(SSM_ERR_BAD_SHAPE, "at most %lld heads", (long long)kMaxHeads);
-  if (p->key_heads == 0 ? p->value_heads != 0 : p->value_heads % p->key_heads != 0)
+  if (p->key_heads == 0 ? p->value_heads != 0 : p->value_heads == 0 || p->value_heads % p->key_heads != 0)
     return fail(SSM_ERR_BAD_SHAPE, "value_heads (%lld) must be a multiple of key_heads (%lld)",
                 (long long)p->value_heads, (long long)p->key_heads);
   if (!valid_dtype(p->in_dtype) || !valid_dtype(other_dtype))
@@ -142,19 +142,41 @@ ssm::DeltaPlan delta_plan(const P* p, int64_t len, const DeltaSizes& s) {
 // Sequences up to this long go step by step, unless pieces are asked for.
 constexpr int64_t kStepsMax = 32;
 
+// One workgroup for every chunk, and at most a workgroup for every 16 columns.
+ssm_status check_grid(int64_t batch, int64_t seqlen, int64_t heads, int64_t dv) {
+  const int64_t chunks = (seqlen + 63) / 64;
+  int64_t blocks;
+  if (!mul_ok(batch * heads, chunks, &blocks) || !mul_ok(blocks, (dv + SSM_MAX_DSTATE) / 16 + 2, &blocks) ||
+      blocks > std::numeric_limits<int32_t>::max())
+    return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
+  return SSM_OK;
+}
+
 // How the forward runs: step by step (no chunks, no workspace) or in chunks.
 ssm_status plan_delta(const ssm_delta_params* p, const DeltaSizes& s, ssm::DeltaChunks* plan) {
   if (p->num_segments < 0) return fail(SSM_ERR_BAD_SHAPE, "num_segments must be >= 0");
   *plan = ssm::DeltaChunks{};
   if (s.empty() || (p->seqlen <= kStepsMax && p->num_segments <= 1)) return SSM_OK;
-  // one workgroup for every chunk, and at most four times a state's strips for every piece
-  const int64_t chunks = (p->seqlen + 63) / 64, bh = p->batch * p->value_heads;
-  int64_t blocks;
-  if (!mul_ok(bh, chunks, &blocks) || !mul_ok(blocks, (p->dv + SSM_MAX_DSTATE) / 16 + 2, &blocks) ||
-      blocks > std::numeric_limits<int32_t>::max())
-    return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
+  const ssm_status st = check_grid(p->batch, p->seqlen, p->value_heads, p->dv);
+  if (st != SSM_OK) return st;
   *plan = ssm::plan_delta_chunks(p->batch, p->seqlen, static_cast<int>(p->value_heads), static_cast<int>(p->dk),
                                  static_cast<int>(p->dv), p->num_segments);
+  return SSM_OK;
+}
+
+ssm_status plan_delta_bwd(const ssm_delta_bwd_params* p, DeltaSizes* s, ssm::DeltaBwdLayout* lay) {
+  ssm_status st = check_delta_sizes(p, p->seqlen, p->grad_dtype, s);
+  if (st != SSM_OK) return st;
+  *lay = ssm::DeltaBwdLayout{};
+  if (s->empty()) return SSM_OK;
+  if ((st = check_grid(p->batch, p->seqlen, p->value_heads, p->dv)) != SSM_OK) return st;
+  // per chunk and head: two states of up to (dk + 31) x (dv + 15), U and dR, the record
+  const int64_t chunks = (p->seqlen + 63) / 64;
+  int64_t bytes;
+  if (!mul_ok(p->batch * p->value_heads * chunks, 8 * (p->dk + 127) * (p->dv + 15) + 65536, &bytes) || bytes > kLim)
+    return fail(SSM_ERR_BAD_SHAPE, "backward workspace size overflows");
+  *lay = ssm::plan_delta_bwd(p->batch, p->seqlen, static_cast<int>(p->value_heads), static_cast<int>(p->dk),
+                             static_cast<int>(p->dv));
   return SSM_OK;
 }
 
@@ -328,6 +350,87 @@ ssm_status ssm_delta_update(const ssm_delta_update_params* p, void* hip_stream) 
   plan.out = p->out;
   const hipError_t e = ssm::launch_delta_steps(plan, static_cast<hipStream_t>(hip_stream));
   if (e != hipSuccess) return fail(SSM_ERR_HIP, "delta window launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+ssm_status ssm_delta_bwd_workspace_size(const ssm_delta_bwd_params* p, size_t* bytes) {
+  if (!p || !bytes) return fail(SSM_ERR_NULL_POINTER, "params or bytes is NULL");
+  DeltaSizes s;
+  ssm::DeltaBwdLayout lay;
+  const ssm_status st = plan_delta_bwd(p, &s, &lay);
+  if (st != SSM_OK) return st;
+  *bytes = lay.bytes;
+  return ok();
+}
+
+ssm_status ssm_delta_bwd(const ssm_delta_bwd_params* p, void* hip_stream) {
+  if (!p) return fail(SSM_ERR_NULL_POINTER, "params is NULL");
+  DeltaSizes s;
+  ssm::DeltaBwdLayout lay;
+  ssm_status st = plan_delta_bwd(p, &s, &lay);
+  if (st != SSM_OK) return st;
+  const size_t si = dtype_size(p->in_dtype), sg = dtype_size(p->grad_dtype);
+  const Need needs[] = {
+      {p->q, s.qk, si, "q", true},          {p->k, s.qk, si, "k", true},
+      {p->v, s.vo, si, "v", true},          {p->dt_raw, s.gate, si, "dt_raw", true},
+      {p->beta_raw, s.gate, si, "beta_raw", true}, {p->A, s.gate, 4, "A", true},
+      {p->dout, s.vo, si, "dout", true},    {p->dq, s.qk, sg, "dq", true},
+      {p->dk_out, s.qk, sg, "dk_out", true}, {p->dv_out, s.vo, sg, "dv_out", true},
+      {p->d_dt_raw, s.gate, sg, "d_dt_raw", true}, {p->dbeta_raw, s.gate, sg, "dbeta_raw", true},
+      {p->dA, p->value_heads, 4, "dA", true}, {p->dt_bias, 0, 4, "dt_bias", false},
+      {p->h0, 0, 4, "h0", false},           {p->dh_last, 0, 4, "dh_last", false},
+      {p->d_dt_bias, 0, 4, "d_dt_bias", false}, {p->dh0, 0, 4, "dh0", false},
+      {p->workspace, 0, 256, "workspace", false},
+  };
+  if ((st = check_pointers(needs)) != SSM_OK) return st;
+  if (lay.bytes > 0 && (!p->workspace || p->workspace_bytes < lay.bytes))
+    return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", lay.bytes,
+                p->workspace ? p->workspace_bytes : static_cast<size_t>(0));
+  const Range in[] = {
+      range(p->q, s.q, si, "q"), range(p->k, s.k, si, "k"), range(p->v, s.v, si, "v"),
+      range(p->dt_raw, s.gate, si, "dt_raw"), range(p->beta_raw, s.gate, si, "beta_raw"),
+      range(p->A, p->value_heads, 4, "A"), range(p->dt_bias, p->value_heads, 4, "dt_bias"),
+      range(p->reset, s.tokens, 1, "reset"), range(p->h0, s.state, 4, "h0"),
+      range(p->dout, s.vo, si, "dout"), range(p->dh_last, s.state, 4, "dh_last"),
+  };
+  const Range out[] = {
+      range(p->dq, s.qk, sg, "dq"), range(p->dk_out, s.qk, sg, "dk_out"), range(p->dv_out, s.vo, sg, "dv_out"),
+      range(p->d_dt_raw, s.gate, sg, "d_dt_raw"), range(p->dbeta_raw, s.gate, sg, "dbeta_raw"),
+      range(p->dA, p->value_heads, 4, "dA"), range(p->d_dt_bias, p->value_heads, 4, "d_dt_bias"),
+      range(p->dh0, s.state, 4, "dh0"),
+      Range{lay.bytes ? static_cast<const char*>(p->workspace) : nullptr, lay.bytes, "workspace"},
+  };
+  if ((st = check_overlaps(in, out)) != SSM_OK) return st;
+  SSM_LOG("ssm_delta_bwd: B %lld L %lld heads %lld / %lld, dk %lld dv %lld, %s in, %s gradients; %d chunks, workspace "
+          "%zu bytes",
+          (long long)p->batch, (long long)p->seqlen, (long long)p->key_heads, (long long)p->value_heads,
+          (long long)p->dk, (long long)p->dv, si == 2 ? "bf16" : "f32", sg == 2 ? "bf16" : "f32", lay.chunks,
+          lay.bytes);
+  const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  if (s.empty()) {  // no token: sums over nothing, and the adjoint passes through
+    hipError_t e = ssm::launch_fill(p->dA, nullptr, 0.0f, 0.0f, p->value_heads, stream);
+    if (e == hipSuccess) e = ssm::launch_fill(p->d_dt_bias, nullptr, 0.0f, 0.0f, p->value_heads, stream);
+    if (e == hipSuccess) e = ssm::launch_fill(p->dh0, p->dh_last, 0.0f, 0.0f, s.state, stream);
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "fill launch failed: %s", hipGetErrorString(e));
+    return ok();
+  }
+  ssm::DeltaPlan plan = delta_plan(p, p->seqlen, s);
+  plan.reset = p->reset;
+  plan.h0 = p->h0;
+  ssm::DeltaBwdPlan g{};
+  g.grad_bf16 = p->grad_dtype == SSM_BF16;
+  g.dout = p->dout;
+  g.dh_last = p->dh_last;
+  g.dq = p->dq;
+  g.dk = p->dk_out;
+  g.dv = p->dv_out;
+  g.ddt = p->d_dt_raw;
+  g.dbr = p->dbeta_raw;
+  g.dA = p->dA;
+  g.dbias = p->d_dt_bias;
+  g.dh0 = p->dh0;
+  const hipError_t e = ssm::launch_delta_bwd(plan, g, lay, p->workspace, stream);
+  if (e != hipSuccess) return fail(SSM_ERR_HIP, "delta rule backward launch failed: %s", hipGetErrorString(e));
   return ok();
 }
 

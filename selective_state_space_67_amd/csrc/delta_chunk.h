@@ -32,6 +32,62 @@ struct ChunkArgs {
   char* records;  // (bh, chunk)
 };
 
+struct ChunkGates {
+  float hi[64], lo[64];  // G in log2 units, as a sum of two floats
+  float beta[64];
+  int seg[64];           // documents started in the chunk up to the token
+  float delta[64];       // softplus(dt_raw + dt_bias)
+};
+
+// One wave, a lane per token; the chunk's scalars (kE0 ..) go to `out`. The sums are taken in double and kept in two floats,
+// so that differences of them keep a small decay's precision next to large ones.
+template <typename InT>
+__device__ __forceinline__ void chunk_gates(const ChunkArgs& a, int b, int h, int chunk, float* out, int lane,
+                                            ChunkGates* s) {
+  const int64_t t = static_cast<int64_t>(chunk) * kChunk + lane;
+  const bool valid = t < a.L;
+  double g = 0.0;
+  float beta = 0.0f, delta = 0.0f;
+  bool start = false;
+  if (valid) {
+    const int64_t i = (static_cast<int64_t>(b) * a.L + t) * a.Hv + h;
+    delta = softplus_f32(load_elem(static_cast<const InT*>(a.dt), i) + (a.dt_bias ? a.dt_bias[h] : 0.0f));
+    beta = a.beta_scale * fast_rcp(1.0f + fast_exp2(-load_elem(static_cast<const InT*>(a.br), i) * kLog2e));
+    start = a.reset && a.reset[static_cast<int64_t>(b) * a.L + t];
+    // a step's decay below 2^-16384 is 0 in float32 whatever its exponent
+    if (!start) g = fmax(static_cast<double>(a.A[h]) * delta * 1.4426950408889634, -16384.0);
+  }
+  const uint64_t starts = __ballot(start);
+  const int seg = __popcll(starts & (~uint64_t{0} >> (63 - lane)));
+  bool cut = start;
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) {
+    const double before = __shfl_up(g, off);
+    const bool cut_before = __shfl_up(static_cast<int>(cut), off);
+    if (lane >= off) {
+      if (!cut) g += before;
+      cut = cut || cut_before;
+    }
+  }
+  const double last = __shfl(g, 63);
+  const int seg_last = __popcll(starts);
+  const float hi = static_cast<float>(g);
+  s->hi[lane] = hi;
+  s->lo[lane] = static_cast<float>(g - hi);
+  s->beta[lane] = beta;
+  s->seg[lane] = seg;
+  s->delta[lane] = delta;
+  out[kE0 + lane] = seg == 0 ? fast_exp2(static_cast<float>(g)) : 0.0f;
+  out[kEC + lane] = seg == seg_last ? fast_exp2(static_cast<float>(last - g)) : 0.0f;
+  out[kBeta + lane] = beta;
+  if (lane == 63) out[kAC] = seg == 0 ? fast_exp2(static_cast<float>(g)) : 0.0f;
+}
+
+__device__ __forceinline__ float pair_decay(const ChunkGates& s, int i, int j) {
+  const float d = (s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j]);
+  return s.seg[i] == s.seg[j] ? fast_exp2(d) : 0.0f;
+}
+
 inline ChunkArgs chunk_args(const DeltaPlan& p, int chunks) {
   ChunkArgs a{};
   a.L = p.L;
@@ -57,6 +113,14 @@ inline ChunkArgs chunk_args(const DeltaPlan& p, int chunks) {
   return a;
 }
 
+// Row tiles of 32 that hold dk: 1, 2, 3, 4, 6 or 8.
+inline int padded_ks(int dk) {
+  const int ks = (dk + 31) / 32;
+  return ks <= 4 ? ks : ks <= 6 ? 6 : 8;
+}
+
+constexpr int kMaxLds = 160 * 1024;
+
 inline bool delta_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 // Token rows of q and k come as whole 16-byte runs of 8 entries (two of them for float32).
@@ -67,5 +131,10 @@ inline bool delta_vec(const DeltaPlan& p) {
 
 // Prepare every chunk (delta_chunk.hip); bwd: the backward's records.
 hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd, hipStream_t stream);
+
+// The forward walk over prepared backward records that keeps every chunk's first
+// state (bh, chunk, 32 padded_ks(dk), cols) and U (bh, chunk, 64, cols), cols = dv
+// rounded up to 16; columns at or past dv and rows of padding are finite.
+hipError_t launch_delta_states(const DeltaPlan& p, const ChunkArgs& c, float* states, float* U, hipStream_t stream);
 
 }  // namespace ssm

@@ -35,60 +35,6 @@ __device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {  // 16 x 16 
   return c;
 }
 
-struct ChunkGates {
-  float hi[64], lo[64];  // G in log2 units, as a sum of two floats
-  float beta[64];
-  int seg[64];           // documents started in the chunk up to the token
-};
-
-// One wave, a lane per token. The sums are taken in double and kept in two floats,
-// so that differences of them keep a small decay's precision next to large ones.
-template <typename InT>
-__device__ __forceinline__ void chunk_gates(const ChunkArgs& a, int b, int h, int chunk, float* out, int lane,
-                                            ChunkGates* s) {
-  const int64_t t = static_cast<int64_t>(chunk) * kChunk + lane;
-  const bool valid = t < a.L;
-  double g = 0.0;
-  float beta = 0.0f;
-  bool start = false;
-  if (valid) {
-    const int64_t i = (static_cast<int64_t>(b) * a.L + t) * a.Hv + h;
-    const float delta = softplus_f32(load_elem(static_cast<const InT*>(a.dt), i) + (a.dt_bias ? a.dt_bias[h] : 0.0f));
-    beta = a.beta_scale * fast_rcp(1.0f + fast_exp2(-load_elem(static_cast<const InT*>(a.br), i) * kLog2e));
-    start = a.reset && a.reset[static_cast<int64_t>(b) * a.L + t];
-    // a step's decay below 2^-16384 is 0 in float32 whatever its exponent
-    if (!start) g = fmax(static_cast<double>(a.A[h]) * delta * 1.4426950408889634, -16384.0);
-  }
-  const uint64_t starts = __ballot(start);
-  const int seg = __popcll(starts & (~uint64_t{0} >> (63 - lane)));
-  bool cut = start;
-#pragma unroll
-  for (int off = 1; off < 64; off *= 2) {
-    const double before = __shfl_up(g, off);
-    const bool cut_before = __shfl_up(static_cast<int>(cut), off);
-    if (lane >= off) {
-      if (!cut) g += before;
-      cut = cut || cut_before;
-    }
-  }
-  const double last = __shfl(g, 63);
-  const int seg_last = __popcll(starts);
-  const float hi = static_cast<float>(g);
-  s->hi[lane] = hi;
-  s->lo[lane] = static_cast<float>(g - hi);
-  s->beta[lane] = beta;
-  s->seg[lane] = seg;
-  out[kE0 + lane] = seg == 0 ? fast_exp2(static_cast<float>(g)) : 0.0f;
-  out[kEC + lane] = seg == seg_last ? fast_exp2(static_cast<float>(last - g)) : 0.0f;
-  out[kBeta + lane] = beta;
-  if (lane == 63) out[kAC] = seg == 0 ? fast_exp2(static_cast<float>(g)) : 0.0f;
-}
-
-__device__ __forceinline__ float pair_decay(const ChunkGates& s, int i, int j) {
-  const float d = (s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j]);
-  return s.seg[i] == s.seg[j] ? fast_exp2(d) : 0.0f;
-}
-
 // T, P (or T^T, P^T) and the scalars of one chunk of one head. Four waves; wave w
 // makes row tile w of the 4 x 4 tiles of 16 tokens (and column tile w for the
 // transposes).
@@ -281,6 +227,10 @@ hipError_t prepare_vec(const ChunkArgs& a, int64_t blocks, bool bwd, hipStream_t
 
 // ---- the walk over the chunks ----
 
+// What a walk leaves: the outputs, a piece's effect on the state, or every chunk's
+// first state and U (for the backward).
+enum Walk { kOutputs, kAggregates, kStates };
+
 struct ScanArgs {
   ChunkArgs c;
   int pieces, chunks_piece;
@@ -292,6 +242,9 @@ struct ScanArgs {
   int cols;         // dv rounded up to 16
   void* out;
   float* h_last;
+  float* states;    // states walk: (bh, chunk, 32 KS, cols)
+  float* U;         // states walk: (bh, chunk, 64, cols)
+  int64_t record_bytes, record_gates;
 };
 
 constexpr int kWaves = kThreads / 64;
@@ -299,13 +252,13 @@ constexpr int kBlockCols = 16 * kWaves;  // columns of the state per workgroup
 
 // What a workgroup stages of one chunk, in bytes from the stage's start. T, the
 // first OP parts of P and the scalars keep the record's order.
-template <typename InT, int NP, int KS, bool AGG, bool QLDS, int OP>
+template <typename InT, int NP, int KS, Walk MODE, bool QLDS, int OP>
 struct Stage {
   static constexpr int kK = 0;
   static constexpr int kQ = kK + TokenTile<NP, KS>::kBytes;
-  static constexpr int kT = kQ + (!AGG && QLDS ? TokenTile<NP, KS>::kBytes : 0);
+  static constexpr int kT = kQ + (MODE == kOutputs && QLDS ? TokenTile<NP, KS>::kBytes : 0);
   static constexpr int kP = kT + kTriBytes;
-  static constexpr int kGates = kP + (AGG ? 0 : kTriBytes / 3 * OP);
+  static constexpr int kGates = kP + (MODE == kOutputs ? kTriBytes / 3 * OP : 0);
   static constexpr int kV = kGates + kGateFloats * 4;  // (64, kBlockCols) of InT
   static constexpr int kBytes = kV + kChunk * kBlockCols * static_cast<int>(sizeof(InT));
 };
@@ -317,18 +270,21 @@ struct ChunkSource {
   const InT* k;
   const InT* v;  // the chunk's first token, column 0 of the head
   const char* record;
+  const char* gates;
   int n_tokens;
 };
 
 template <typename InT>
-__device__ __forceinline__ ChunkSource<InT> chunk_source(const ChunkArgs& a, int bh, int b, int h, int c) {
+__device__ __forceinline__ ChunkSource<InT> chunk_source(const ScanArgs& w, int bh, int b, int h, int c) {
+  const ChunkArgs& a = w.c;
   ChunkSource<InT> s;
   const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk;
   const int hk = h / a.group;
   s.q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
   s.k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
   s.v = static_cast<const InT*>(a.v) + t0 * a.vs + static_cast<int64_t>(h) * a.dv;
-  s.record = a.records + (static_cast<int64_t>(bh) * a.chunks + c) * kRecBytes;
+  s.record = a.records + (static_cast<int64_t>(bh) * a.chunks + c) * w.record_bytes;
+  s.gates = s.record + w.record_gates;
   s.n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(c) * kChunk));
   return s;
 }
@@ -353,41 +309,41 @@ __device__ __forceinline__ LaneOffsets lane_offsets(const ChunkArgs& a, int n_to
   return o;
 }
 
-template <typename InT, int KS, bool AGG, int OP>
+template <typename InT, int KS, Walk MODE, int OP>
 __device__ __forceinline__ void stage_async(char* st, const ChunkSource<InT>& s, const LaneOffsets& o, int lane,
                                             int wave) {
-  using S = Stage<InT, 1, KS, AGG, true, OP>;
+  using S = Stage<InT, 1, KS, MODE, true, OP>;
   static_assert(kWaves == 4, "row tile w and values 16 w .. of wave w");
   const char *k = reinterpret_cast<const char*>(s.k), *q = reinterpret_cast<const char*>(s.q);
   const char* v = reinterpret_cast<const char*>(s.v);
 #pragma unroll
   for (int i = 0; i < KS; ++i) {
     load_to_lds(k + i * 64 + o.k, st + S::kK + (wave * KS + i) * 1024);
-    if constexpr (!AGG) load_to_lds(q + i * 64 + o.q, st + S::kQ + (wave * KS + i) * 1024);
+    if constexpr (MODE == kOutputs) load_to_lds(q + i * 64 + o.q, st + S::kQ + (wave * KS + i) * 1024);
   }
   const uint32_t own = lane * 16;
-  constexpr int kTri = (AGG ? kTriBytes : kTriBytes + kTriBytes / 3 * OP) / 1024;
+  constexpr int kTri = (MODE == kOutputs ? kTriBytes + kTriBytes / 3 * OP : kTriBytes) / 1024;
 #pragma unroll
   for (int i = 0; i < (kTri + kWaves - 1) / kWaves; ++i) {
     const int f = wave + i * kWaves;
     if (f < kTri) load_to_lds(s.record + f * 1024 + own, st + S::kT + f * 1024);
   }
-  if (wave == 3) load_to_lds(s.record + kRecGates + own, st + S::kGates);
+  if (wave == 3) load_to_lds(s.gates + own, st + S::kGates);
 #pragma unroll
   for (int i = 0; i < 2; ++i) load_to_lds(v + o.v[i], st + S::kV + (wave * 2 + i) * 1024);
 }
 
 // Staging through registers, for float32 and for rows that are not whole runs.
-template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS, int OP>
+template <typename InT, int NP, int KS, bool VEC, Walk MODE, bool QLDS, int OP>
 __device__ __forceinline__ void stage_sync(char* st, const ChunkArgs& a, const ChunkSource<InT>& s, int col0) {
-  using S = Stage<InT, NP, KS, AGG, QLDS, OP>;
+  using S = Stage<InT, NP, KS, MODE, QLDS, OP>;
   stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kK), s.k, a.ks, s.n_tokens, 0, a.dk);
-  if constexpr (!AGG && QLDS)
+  if constexpr (MODE == kOutputs && QLDS)
     stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kQ), s.q, a.qs, s.n_tokens, 0, a.dk);
-  constexpr int kRuns = (AGG ? kTriBytes : kTriBytes + kTriBytes / 3 * OP) / 16;
+  constexpr int kRuns = (MODE == kOutputs ? kTriBytes + kTriBytes / 3 * OP : kTriBytes) / 16;
   for (int i = threadIdx.x; i < kRuns; i += kThreads)
     reinterpret_cast<u32x4*>(st + S::kT)[i] = reinterpret_cast<const u32x4*>(s.record)[i];
-  reinterpret_cast<float*>(st + S::kGates)[threadIdx.x] = reinterpret_cast<const float*>(s.record + kRecGates)[threadIdx.x];
+  reinterpret_cast<float*>(st + S::kGates)[threadIdx.x] = reinterpret_cast<const float*>(s.gates)[threadIdx.x];
   InT* v = reinterpret_cast<InT*>(st + S::kV);
 #pragma unroll
   for (int i = 0; i < kChunk * kBlockCols / kThreads; ++i) {
@@ -403,11 +359,12 @@ __device__ __forceinline__ void stage_sync(char* st, const ChunkArgs& a, const C
 // identity). With two stages the next chunk is loaded while this one is worked on.
 // OP: parts of the products that only the output sees; two (2^-17) where it is
 // rounded to bfloat16 (2^-9).
-template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS, bool ASYNC, int STAGES, int OP>
+template <typename InT, int NP, int KS, bool VEC, Walk MODE, bool QLDS, bool ASYNC, int STAGES, int OP>
 __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
   using Tile = TokenTile<NP, KS>;
-  using S = Stage<InT, NP, KS, AGG, QLDS, OP>;
+  using S = Stage<InT, NP, KS, MODE, QLDS, OP>;
   constexpr int DKT = 2 * KS;  // row tiles of the state
+  constexpr bool AGG = MODE == kAggregates, OUT = MODE == kOutputs;
   extern __shared__ __align__(16) char staged[];
   const ChunkArgs& a = s.c;
   const int lane = threadIdx.x % 64, wave = wave_index(), g4 = (lane >> 4) * 4;
@@ -439,14 +396,14 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
   }
 
   const int c0 = piece * s.chunks_piece, c1 = min(a.chunks, c0 + s.chunks_piece);
-  ChunkSource<InT> src = chunk_source<InT>(a, bh, b, h, c0);
+  ChunkSource<InT> src = chunk_source<InT>(s, bh, b, h, c0);
   const LaneOffsets whole = lane_offsets(a, kChunk, col0, lane, wave);
   const auto stage = [&](char* st, const ChunkSource<InT>& from) {
     if constexpr (ASYNC)
-      stage_async<InT, KS, AGG, OP>(
+      stage_async<InT, KS, MODE, OP>(
           st, from, from.n_tokens == kChunk ? whole : lane_offsets(a, from.n_tokens, col0, lane, wave), lane, wave);
     else
-      stage_sync<InT, NP, KS, VEC, AGG, QLDS, OP>(st, a, from, col0);
+      stage_sync<InT, NP, KS, VEC, MODE, QLDS, OP>(st, a, from, col0);
   };
   if constexpr (STAGES == 2) stage(staged, src);
   for (int c = c0; c < c1; ++c) {
@@ -455,7 +412,8 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
     next.q += kChunk * a.qs;
     next.k += kChunk * a.ks;
     next.v += kChunk * a.vs;
-    next.record += kRecBytes;
+    next.record += s.record_bytes;
+    next.gates += s.record_bytes;
     next.n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(c + 1) * kChunk));
     if constexpr (STAGES == 2) {
       wait_loads();
@@ -471,6 +429,14 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
     const uint16_t* sq = reinterpret_cast<const uint16_t*>(st + S::kQ);
     const float* gates = reinterpret_cast<const float*>(st + S::kGates);
 
+    if constexpr (MODE == kStates) {  // in the waves' own layout: columns of the strips are 16 neighbours
+      float* to = s.states + (static_cast<int64_t>(bh) * a.chunks + c) * (32 * KS) * s.cols + own;
+#pragma unroll
+      for (int m = 0; m < DKT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (own < s.cols) to[static_cast<int64_t>(state_row(m, g4, r)) * s.cols] = H[m][r];
+    }
     f32x4 X[4] = {zero, zero, zero, zero}, Y[4] = {zero, zero, zero, zero};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -479,7 +445,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         kf[m] = Tile::rows(sk, m, ks, lane);
-        if constexpr (!AGG) {
+        if constexpr (OUT) {
           if constexpr (QLDS)
             qf[m] = Tile::rows(sq, m, ks, lane);
           else
@@ -487,7 +453,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
         }
       }
       mma_n(kf, hb, X);
-      if constexpr (!AGG) mma_n<OP>(qf, hb, Y);
+      if constexpr (OUT) mma_n<OP>(qf, hb, Y);
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -517,9 +483,17 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
       const Frag<3> rb[2] = {split8(X[0], X[1]), split8(X[2], X[3])};
       mma_tri(reinterpret_cast<const uint16_t*>(st + S::kT), rb, lane, U);
     }
-    if constexpr (!AGG) {
+    if constexpr (OUT) {
       const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
       mma_tri<OP>(reinterpret_cast<const uint16_t*>(st + S::kP), ub, lane, Y);
+    }
+    if constexpr (MODE == kStates) {
+      float* to = s.U + (static_cast<int64_t>(bh) * a.chunks + c) * kChunk * s.cols + own;
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (own < s.cols) to[(m * 16 + g4 + r) * s.cols] = U[m][r];
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) U[m] *= *reinterpret_cast<const f32x4*>(gates + kEC + m * 16 + g4);
@@ -535,7 +509,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
       mma_n(kc, ub[ts], H);
     }
 
-    if constexpr (!AGG) {
+    if constexpr (OUT) {
       const int64_t row0 = (static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk) * a.Hv + h;  // x dv
       if (OP == 2 && (ASYNC || s.out_runs)) {  // ASYNC has whole runs everywhere
         // The strip's place among the staged values is this wave's alone and has been
@@ -584,7 +558,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
     for (int m = 0; m < DKT; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) dst[static_cast<int64_t>(state_row(m, g4, r)) * width] = H[m][r];
-  } else if (s.h_last && c1 == a.chunks && has_v) {
+  } else if (OUT && s.h_last && c1 == a.chunks && has_v) {
 #pragma unroll
     for (int m = 0; m < DKT; ++m)
 #pragma unroll
@@ -660,23 +634,15 @@ __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
   }
 }
 
-// Row tiles of 32 that hold dk: 1, 2, 3, 4, 6 or 8.
-int padded_ks(int dk) {
-  const int ks = (dk + 31) / 32;
-  return ks <= 4 ? ks : ks <= 6 ? 6 : 8;
-}
-
-constexpr int kMaxLds = 160 * 1024;
-
-template <typename InT, int NP, int KS, bool VEC, bool AGG, bool QLDS, bool ASYNC, int OP>
+template <typename InT, int NP, int KS, bool VEC, Walk MODE, bool QLDS, bool ASYNC, int OP>
 hipError_t launch_walk(const ScanArgs& s, int64_t blocks, hipStream_t stream) {
-  constexpr int kBytes = Stage<InT, NP, KS, AGG, QLDS, OP>::kBytes;
+  constexpr int kBytes = Stage<InT, NP, KS, MODE, QLDS, OP>::kBytes;
   constexpr int STAGES = ASYNC && 2 * kBytes <= kMaxLds ? 2 : 1;
   static_assert(kBytes <= kMaxLds, "a chunk's stage exceeds LDS");
-  SSM_LOG("launch delta_chunk_scan<%d parts, %d rows, aggregates %d>: %d pieces of %d chunks, %d stages of %d bytes; "
+  SSM_LOG("launch delta_chunk_scan<%d parts, %d rows, walk %d>: %d pieces of %d chunks, %d stages of %d bytes; "
           "grid %lld x %d threads",
-          NP, 32 * KS, AGG, s.pieces, s.chunks_piece, STAGES, kBytes, static_cast<long long>(blocks), kThreads);
-  hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, VEC, AGG, QLDS, ASYNC, STAGES, OP>),
+          NP, 32 * KS, MODE, s.pieces, s.chunks_piece, STAGES, kBytes, static_cast<long long>(blocks), kThreads);
+  hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, VEC, MODE, QLDS, ASYNC, STAGES, OP>),
                      dim3(static_cast<unsigned>(blocks)), dim3(kThreads), STAGES * kBytes, stream, s);
   return hipGetLastError();
 }
@@ -684,12 +650,12 @@ hipError_t launch_walk(const ScanArgs& s, int64_t blocks, hipStream_t stream) {
 template <typename InT, int NP, int KS, bool VEC, bool ASYNC>
 hipError_t launch_scan_ks(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs s, hipStream_t stream) {
   // K and Q of a chunk side by side fit in LDS except for float32 past 128 entries
-  constexpr bool QLDS = Stage<InT, NP, KS, false, true, 3>::kBytes <= kMaxLds;
+  constexpr bool QLDS = Stage<InT, NP, KS, kOutputs, true, 3>::kBytes <= kMaxLds;
   const int64_t heads = p.B * p.Hv;
   if (plan.pieces > 1) {
     const int strips = 2 * KS + s.cols / 16;
     s.col_blocks = (strips + kWaves - 1) / kWaves;
-    hipError_t e = launch_walk<InT, NP, KS, VEC, true, QLDS, ASYNC, 3>(s, heads * plan.pieces * s.col_blocks, stream);
+    hipError_t e = launch_walk<InT, NP, KS, VEC, kAggregates, QLDS, ASYNC, 3>(s, heads * plan.pieces * s.col_blocks, stream);
     if (e != hipSuccess) return e;
     FoldArgs f{s.agg, s.h0, const_cast<float*>(s.starts), plan.pieces, p.dk, p.dv, s.cols, s.cols / 16};
     SSM_LOG("launch delta_fold<%d rows>: grid %lld x %d threads", 32 * KS, static_cast<long long>(heads * f.strips),
@@ -699,8 +665,9 @@ hipError_t launch_scan_ks(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs 
   }
   s.col_blocks = (s.cols / 16 + kWaves - 1) / kWaves;
   const int64_t blocks = heads * plan.pieces * s.col_blocks;
-  if (NP == 1 && s.out_bf16) return launch_walk<InT, NP, KS, VEC, false, QLDS, ASYNC, NP == 1 ? 2 : 3>(s, blocks, stream);
-  return launch_walk<InT, NP, KS, VEC, false, QLDS, ASYNC, 3>(s, blocks, stream);
+  if (s.states) return launch_walk<InT, NP, KS, VEC, kStates, QLDS, ASYNC, 3>(s, blocks, stream);
+  if (NP == 1 && s.out_bf16) return launch_walk<InT, NP, KS, VEC, kOutputs, QLDS, ASYNC, NP == 1 ? 2 : 3>(s, blocks, stream);
+  return launch_walk<InT, NP, KS, VEC, kOutputs, QLDS, ASYNC, 3>(s, blocks, stream);
 }
 
 template <typename InT, int NP, bool VEC, bool ASYNC>
@@ -748,25 +715,14 @@ DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int 
   return d;
 }
 
-hipError_t launch_delta_chunks(const DeltaPlan& p, const DeltaChunks& plan, void* workspace, hipStream_t stream) {
-  char* ws = static_cast<char*>(workspace);
-  ScanArgs s{};
-  s.c = chunk_args(p, plan.chunks);
-  s.c.records = ws + plan.off_records;
-  hipError_t e = launch_chunk_prepare(p, s.c, false, stream);
-  if (e != hipSuccess) return e;
+namespace {
+
+hipError_t launch_scan(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs& s, hipStream_t stream) {
   s.pieces = plan.pieces;
   s.chunks_piece = plan.chunks_piece;
-  s.out_bf16 = p.out_bf16;
   s.h0 = p.h0;
   s.cols = (p.dv + 15) / 16 * 16;
-  if (plan.pieces > 1) {
-    s.agg = reinterpret_cast<float*>(ws + plan.off_agg);
-    s.starts = reinterpret_cast<float*>(ws + plan.off_starts);
-  }
-  s.out = p.out;
-  s.h_last = p.h_last;
-  // a chunk's rows of out lie within 2^31 bytes (for 32-bit offsets)
+  // a chunk's rows lie within 2^31 bytes (for 32-bit offsets)
   const int64_t reach = int64_t{1} << 24;  // elements a token
   s.out_runs = p.dv % 8 == 0 && delta_aligned(p.out, 16) && static_cast<int64_t>(p.Hv) * p.dv < reach;
   const bool vec = delta_vec(p);
@@ -779,6 +735,40 @@ hipError_t launch_delta_chunks(const DeltaPlan& p, const DeltaChunks& plan, void
   if (async) return launch_scan_vec<bf16_t, 1, true, true>(p, plan, s, stream);
   return vec ? launch_scan_vec<bf16_t, 1, true, false>(p, plan, s, stream)
              : launch_scan_vec<bf16_t, 1, false, false>(p, plan, s, stream);
+}
+
+}  // namespace
+
+hipError_t launch_delta_chunks(const DeltaPlan& p, const DeltaChunks& plan, void* workspace, hipStream_t stream) {
+  char* ws = static_cast<char*>(workspace);
+  ScanArgs s{};
+  s.c = chunk_args(p, plan.chunks);
+  s.c.records = ws + plan.off_records;
+  s.record_bytes = kRecBytes;
+  s.record_gates = kRecGates;
+  const hipError_t e = launch_chunk_prepare(p, s.c, false, stream);
+  if (e != hipSuccess) return e;
+  if (plan.pieces > 1) {
+    s.agg = reinterpret_cast<float*>(ws + plan.off_agg);
+    s.starts = reinterpret_cast<float*>(ws + plan.off_starts);
+  }
+  s.out_bf16 = p.out_bf16;
+  s.out = p.out;
+  s.h_last = p.h_last;
+  return launch_scan(p, plan, s, stream);
+}
+
+hipError_t launch_delta_states(const DeltaPlan& p, const ChunkArgs& c, float* states, float* U, hipStream_t stream) {
+  DeltaChunks one{};
+  one.chunks = one.chunks_piece = c.chunks;
+  one.pieces = 1;
+  ScanArgs s{};
+  s.c = c;
+  s.record_bytes = kRecBytesBwd;
+  s.record_gates = kRecGatesBwd;
+  s.states = states;
+  s.U = U;
+  return launch_scan(p, one, s, stream);
 }
 
 }  // namespace ssm

@@ -1,0 +1,796 @@
+// Gated delta rule in chunks of 64 tokens, backward.
+//
+// With the forward's chunk quantities (delta_chunk.hip), dO the gradient of the
+// output times scale, dH1 the adjoint of the state after the chunk:
+//
+//   dU = P^T dO + eC (K dH1)            dR = T^T dU          dV = beta dR
+//   dH0 = aC dH1 + Q^T (e0 dO) - K^T (beta e0 dR)
+//   dP = M o (dO U^T) (j <= i),  dS = -beta M o (dR U^T) (j < i)
+//   dQ = e0 (dO H0^T) + dP K
+//   dK = [eC (U dH1^T) + dP^T Q + dS^T K] + [dS K - beta e0 (dR H0^T)]
+//   d beta_raw_i = (dR_i . U_i) (1 - beta_i / beta_scale)
+//   d g_t = sum over i >= t of q_i . dQ_i + k_i . (second bracket - first without eC)_i
+//         + sum over j < t of k_j . (eC (U dH1^T))_j + aC <dH1, H0>
+//
+// (M carries exp(G_i - G_j): the first bracket holds k as the j side of every decay,
+// the second as its i side, and what has its sides before and from step t on crosses
+// its decay. Pairs i = j cross nothing: their products are left out of the sum and
+// added to dQ and dK afterwards, so that they need not cancel.)
+//
+// Four launches: the chunks' matrices (delta_chunk.hip, with transposes); the
+// forward walk again, keeping each chunk's first state and U; the reverse walk
+// below, which mirrors the forward one (a wave owns 16 columns of dH in registers)
+// and keeps each chunk's dH1 and dR; and the gradients, every chunk of every key
+// head in parallel, with the value heads of a key head added up in one workgroup.
+#include <algorithm>
+
+#include "delta_chunk.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kBlockCols = 16 * kWaves;
+
+struct BwdArgs {
+  ChunkArgs c;
+  int col_blocks, cols;
+  int grad_bf16;
+  const void* dout;
+  const float* dh_last;
+  const float* states;   // (bh, chunk, 32 KS, cols)
+  const float* U;        // (bh, chunk, 64, cols)
+  float* dstates;        // as states: dH1
+  float* dR;             // as U
+  float* part;           // (bh, chunk, 2): dA, d dt_bias
+  void* dq;
+  void* dk;
+  void* dv;
+  void* ddt;
+  void* dbr;
+  float* dh0;
+};
+
+template <typename InT, int NP, int KS, bool BOTH>
+struct RevStage {
+  static constexpr int kK = 0;
+  static constexpr int kQ = BOTH ? TokenTile<NP, KS>::kBytes : 0;  // else Q takes K's place after it
+  static constexpr int kTt = kQ + TokenTile<NP, KS>::kBytes;
+  static constexpr int kPt = kTt + kTriBytes;
+  static constexpr int kGates = kPt + kTriBytes;
+  static constexpr int kdO = kGates + kGateFloats * 4;  // (64, kBlockCols) of InT
+  static constexpr int kBytes = kdO + kChunk * kBlockCols * static_cast<int>(sizeof(InT));
+};
+
+template <typename InT>
+struct RevSource {
+  const InT* q;
+  const InT* k;
+  const InT* dout;  // the chunk's first token, column 0 of the head
+  const char* record;
+  int n_tokens;
+};
+
+struct RevOffsets {
+  uint32_t k, q, o[2];
+};
+
+__device__ __forceinline__ RevOffsets rev_offsets(const ChunkArgs& a, int n_tokens, int col0, int lane, int wave) {
+  RevOffsets o;
+  const int last = n_tokens - 1, row = min(wave * 16 + (lane & 15), last);
+  o.k = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ks) * 2 + (lane >> 4) * 16;
+  o.q = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.qs) * 2 + (lane >> 4) * 16;
+  const int col = min(col0 + (lane & 7) * 8, a.dv - 8);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    o.o[i] = static_cast<uint32_t>(min((wave * 2 + i) * 8 + lane / 8, last)) * static_cast<uint32_t>(a.Hv * a.dv) * 2 + col * 2;
+  return o;
+}
+
+// Straight into LDS; rows past the end repeat the last token (masked when used).
+template <typename InT, int KS>
+__device__ __forceinline__ void rev_stage_async(char* st, const RevSource<InT>& s, const RevOffsets& o, int lane,
+                                                int wave) {
+  using S = RevStage<InT, 1, KS, true>;
+  const char *k = reinterpret_cast<const char*>(s.k), *q = reinterpret_cast<const char*>(s.q);
+  const char* d = reinterpret_cast<const char*>(s.dout);
+#pragma unroll
+  for (int i = 0; i < KS; ++i) {
+    load_to_lds(k + i * 64 + o.k, st + S::kK + (wave * KS + i) * 1024);
+    load_to_lds(q + i * 64 + o.q, st + S::kQ + (wave * KS + i) * 1024);
+  }
+  constexpr int kRec = (2 * kTriBytes + kGateFloats * 4) / 1024;  // T^T, P^T and the scalars follow each other
+#pragma unroll
+  for (int i = 0; i < (kRec + kWaves - 1) / kWaves; ++i) {
+    const int f = wave + i * kWaves;
+    if (f < kRec) load_to_lds(s.record + kRecTt + f * 1024 + static_cast<uint32_t>(lane * 16), st + S::kTt + f * 1024);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) load_to_lds(d + o.o[i], st + S::kdO + (wave * 2 + i) * 1024);
+}
+
+template <typename InT, int NP, int KS, bool VEC, bool BOTH>
+__device__ __forceinline__ void rev_stage_sync(char* st, const ChunkArgs& a, const RevSource<InT>& s, int col0) {
+  using S = RevStage<InT, NP, KS, BOTH>;
+  stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kK), s.k, a.ks, s.n_tokens, 0, a.dk);
+  if constexpr (BOTH)
+    stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kQ), s.q, a.qs, s.n_tokens, 0, a.dk);
+  constexpr int kRuns = (2 * kTriBytes + kGateFloats * 4) / 16;
+  for (int i = threadIdx.x; i < kRuns; i += kThreads)
+    reinterpret_cast<u32x4*>(st + S::kTt)[i] = reinterpret_cast<const u32x4*>(s.record + kRecTt)[i];
+  InT* o = reinterpret_cast<InT*>(st + S::kdO);
+#pragma unroll
+  for (int i = 0; i < kChunk * kBlockCols / kThreads; ++i) {
+    const int e = threadIdx.x + i * kThreads, token = e / kBlockCols, col = col0 + e % kBlockCols;
+    InT x{};
+    if (token < s.n_tokens && col < a.dv) x = s.dout[static_cast<int64_t>(token) * a.Hv * a.dv + col];
+    o[e] = x;
+  }
+}
+
+template <typename InT, int NP, int KS, bool VEC, bool BOTH, bool ASYNC, int STAGES>
+__global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s) {
+  using Tile = TokenTile<NP, KS>;
+  using S = RevStage<InT, NP, KS, BOTH>;
+  constexpr int DKT = 2 * KS;
+  extern __shared__ __align__(16) char staged[];
+  const ChunkArgs& a = s.c;
+  const int lane = threadIdx.x % 64, wave = wave_index(), g4 = (lane >> 4) * 4;
+  const int cb = blockIdx.x % s.col_blocks, bh = blockIdx.x / s.col_blocks;
+  const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / a.group;
+  const int col0 = cb * kBlockCols, own = col0 + wave * 16 + (lane & 15);
+  const bool has_v = own < a.dv;
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+
+  f32x4 H[DKT];  // dH
+#pragma unroll
+  for (int m = 0; m < DKT; ++m) {
+    H[m] = zero;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = state_row(m, g4, r);
+      if (s.dh_last && row < a.dk && has_v) H[m][r] = s.dh_last[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own];
+    }
+  }
+  const int64_t token_v = static_cast<int64_t>(a.Hv) * a.dv;
+  RevSource<InT> src;
+  {
+    const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(a.chunks - 1) * kChunk;
+    src.q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
+    src.k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
+    src.dout = static_cast<const InT*>(s.dout) + t0 * token_v + static_cast<int64_t>(h) * a.dv;
+    src.record = a.records + (static_cast<int64_t>(bh) * a.chunks + a.chunks - 1) * kRecBytesBwd;
+    src.n_tokens = static_cast<int>(a.L - static_cast<int64_t>(a.chunks - 1) * kChunk);
+  }
+  const RevOffsets whole = rev_offsets(a, kChunk, col0, lane, wave);
+  const auto stage = [&](char* st, const RevSource<InT>& from) {
+    if constexpr (ASYNC)
+      rev_stage_async<InT, KS>(st, from,
+                               from.n_tokens == kChunk ? whole : rev_offsets(a, from.n_tokens, col0, lane, wave), lane,
+                               wave);
+    else
+      rev_stage_sync<InT, NP, KS, VEC, BOTH>(st, a, from, col0);
+  };
+  if constexpr (STAGES == 2) stage(staged, src);
+  for (int c = a.chunks - 1; c >= 0; --c) {
+    char* st = staged + (STAGES == 2 ? ((a.chunks - 1 - c) & 1) * S::kBytes : 0);
+    RevSource<InT> next = src;
+    next.q -= kChunk * a.qs;
+    next.k -= kChunk * a.ks;
+    next.dout -= kChunk * token_v;
+    next.record -= kRecBytesBwd;
+    next.n_tokens = kChunk;
+    if constexpr (STAGES == 2) {
+      wait_loads();
+      __syncthreads();  // this stage is loaded, and the other one is no longer read
+      if (c > 0) stage(staged + ((a.chunks - c) & 1) * S::kBytes, next);
+    } else {
+      __syncthreads();  // the previous chunk is no longer read
+      stage(st, src);
+      wait_loads();
+      __syncthreads();
+    }
+    const uint16_t* sk = reinterpret_cast<const uint16_t*>(st + S::kK);
+    const uint16_t* sq = reinterpret_cast<const uint16_t*>(st + S::kQ);
+    const float* gates = reinterpret_cast<const float*>(st + S::kGates);
+    const int64_t record = static_cast<int64_t>(bh) * a.chunks + c;
+
+    if (own < s.cols) {
+      float* to = s.dstates + record * (32 * KS) * s.cols + own;
+#pragma unroll
+      for (int m = 0; m < DKT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[static_cast<int64_t>(state_row(m, g4, r)) * s.cols] = H[m][r];
+    }
+
+    // K dH1, and the lane's column of dO
+    f32x4 X[4] = {zero, zero, zero, zero};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const Frag<3> hb = split8(H[2 * ks], H[2 * ks + 1]);
+      Frag<NP> kf[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) kf[m] = Tile::rows(sk, m, ks, lane);
+      mma_n(kf, hb, X);
+    }
+    f32x4 dO[4];
+    Frag<NP> ob[2];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if constexpr (sizeof(InT) == 2) {
+        u32x2 w = read_transposed(reinterpret_cast<const uint16_t*>(st + S::kdO) +
+                                  (m * 16 + g4 + ((lane & 15) >> 2)) * kBlockCols + wave * 16 + (lane & 3) * 4);
+        if (src.n_tokens < kChunk) {
+          const int left = src.n_tokens - (m * 16 + g4);  // tokens of the four that exist
+          w.x = left >= 2 ? w.x : left == 1 ? w.x & 0xFFFFu : 0u;
+          w.y = left >= 4 ? w.y : left == 3 ? w.y & 0xFFFFu : 0u;
+        }
+        dO[m] = f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                      __uint_as_float(w.y & 0xFFFF0000u)};
+        if (m & 1) {
+          ob[m / 2].p[0].z = w.x;
+          ob[m / 2].p[0].w = w.y;
+        } else {
+          ob[m / 2].p[0].x = w.x;
+          ob[m / 2].p[0].y = w.y;
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          dO[m][r] = reinterpret_cast<const float*>(st + S::kdO)[(m * 16 + g4 + r) * kBlockCols + wave * 16 + (lane & 15)];
+      }
+    }
+    if constexpr (NP == 3) {
+      ob[0] = split8(dO[0], dO[1]);
+      ob[1] = split8(dO[2], dO[3]);
+    }
+    f32x4 dU[4] = {zero, zero, zero, zero};
+    mma_tri_t(reinterpret_cast<const uint16_t*>(st + S::kPt), ob, lane, dU);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const f32x4 eC = *reinterpret_cast<const f32x4*>(gates + kEC + m * 16 + g4);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dU[m][r] = __builtin_fmaf(eC[r], X[m][r], a.scale * dU[m][r]);
+    }
+    f32x4 dR[4] = {zero, zero, zero, zero};
+    {
+      const Frag<3> ub[2] = {split8(dU[0], dU[1]), split8(dU[2], dU[3])};
+      mma_tri_t(reinterpret_cast<const uint16_t*>(st + S::kTt), ub, lane, dR);
+    }
+    if (own < s.cols) {
+      float* to = s.dR + record * kChunk * s.cols + own;
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[(m * 16 + g4 + r) * s.cols] = dR[m][r];
+    }
+    const float aC = gates[kAC];
+    f32x4 dV[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const f32x4 e0 = *reinterpret_cast<const f32x4*>(gates + kE0 + m * 16 + g4);
+      const f32x4 be = *reinterpret_cast<const f32x4*>(gates + kBeta + m * 16 + g4);
+      dV[m] = be * dR[m];
+      dR[m] = -e0 * dV[m];
+      dO[m] *= a.scale * e0;
+    }
+#pragma unroll
+    for (int m = 0; m < DKT; ++m) H[m] *= aC;
+    {
+      const Frag<3> rb[2] = {split8(dR[0], dR[1]), split8(dR[2], dR[3])};
+#pragma unroll
+      for (int ts = 0; ts < 2; ++ts) {
+        Frag<NP> kc[DKT];
+#pragma unroll
+        for (int m = 0; m < DKT; ++m) kc[m] = Tile::columns(sk, m, ts, lane);
+        mma_n(kc, rb[ts], H);
+      }
+    }
+    if constexpr (!BOTH) {
+      __syncthreads();
+      stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kQ), src.q, a.qs, src.n_tokens, 0, a.dk);
+      __syncthreads();
+    }
+    {
+      const Frag<3> qb[2] = {split8(dO[0], dO[1]), split8(dO[2], dO[3])};
+#pragma unroll
+      for (int ts = 0; ts < 2; ++ts) {
+        Frag<NP> qc[DKT];
+#pragma unroll
+        for (int m = 0; m < DKT; ++m) qc[m] = Tile::columns(sq, m, ts, lane);
+        mma_n(qc, qb[ts], H);
+      }
+    }
+
+    const int64_t row0 = (static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk) * a.Hv + h;  // x dv
+    if (ASYNC && s.grad_bf16) {
+      // turned to rows in the place of the strip's dO, as the forward's outputs
+      uint16_t* o = reinterpret_cast<uint16_t*>(st + S::kdO) + wave * 16;
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+          const uint32_t w = bf16_words(dV[m][r], dV[m][r + 1]);
+          uint16_t* p = o + (m * 16 + g4 + r) * kBlockCols + (lane & 15);
+          p[0] = static_cast<uint16_t>(w);
+          p[kBlockCols] = static_cast<uint16_t>(w >> 16);
+        }
+      char* dst = static_cast<char*>(s.dv) + (row0 * a.dv + col0 + wave * 16) * 2;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int token = i * 32 + lane / 2, half = (lane & 1) * 8;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(o + token * kBlockCols + half);
+        if (token < src.n_tokens && col0 + wave * 16 + half < a.dv)
+          *reinterpret_cast<u32x4*>(dst + static_cast<uint32_t>(token * a.Hv * a.dv + half) * 2) = w;
+      }
+    } else {
+      const int64_t lane0 = row0 * a.dv + g4 * token_v + own;
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (!has_v || m * 16 + g4 + r >= src.n_tokens) continue;
+          if (s.grad_bf16)
+            store_elem(static_cast<bf16_t*>(s.dv) + (m * 16 + r) * token_v, lane0, dV[m][r]);
+          else
+            store_elem(static_cast<float*>(s.dv) + (m * 16 + r) * token_v, lane0, dV[m][r]);
+        }
+    }
+    src = next;
+  }
+  if (s.dh0 && has_v) {
+#pragma unroll
+    for (int m = 0; m < DKT; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = state_row(m, g4, r);
+        if (row < a.dk) s.dh0[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own] = H[m][r];
+      }
+  }
+}
+
+// ---- the gradients of a chunk ----
+
+// Stage a (rows, 32) slab of a float32 matrix as split operands, 8 columns a thread;
+// columns at or past `limit` (dv rounded up to 8: the walks may leave copies of other
+// columns beyond it) are 0. STATE: rows go to the tiles that state_row names.
+template <int TILES, bool STATE>
+__device__ __forceinline__ void stage_slab(uint16_t* s, const float* src, int ld, int col, int limit, f32x4* lo,
+                                           f32x4* hi, int i) {
+  const int row = i >> 2, oct = i & 3;
+  int at = row;
+  if (STATE) at = ((row >> 5) * 2 + ((row >> 2) & 1)) * 16 + ((row >> 3) & 3) * 4 + (row & 3);
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  *lo = *hi = zero;
+  const float* p = src + static_cast<int64_t>(row) * ld + col + oct * 8;
+  if (col + oct * 8 < limit) {
+    *lo = *reinterpret_cast<const f32x4*>(p);
+    *hi = *reinterpret_cast<const f32x4*>(p + 4);
+  }
+  const Frag<3> f = split8(*lo, *hi);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    *reinterpret_cast<u32x4*>(s + k * TILES * 512 + ((at >> 4) * 64 + oct * 16 + (at & 15)) * 8) = f.p[k];
+}
+
+template <int NP, int TILES>
+__device__ __forceinline__ Frag<NP> slab_rows(const uint16_t* s, int tile, int lane) {
+  Frag<NP> f;
+#pragma unroll
+  for (int k = 0; k < NP; ++k) f.p[k] = *reinterpret_cast<const u32x4*>(s + k * TILES * 512 + (tile * 64 + lane) * 8);
+  return f;
+}
+
+template <typename InT, int NP, int KS>
+struct GradLds {
+  static constexpr int kdO = 0;
+  static constexpr int kU = kdO + NP * 4096;
+  static constexpr int kdR = kU + 3 * 4096;
+  static constexpr int kH = kdR + 3 * 4096;
+  static constexpr int kdH = kH + 3 * 2 * KS * 1024;
+  static constexpr int kSlab = kdH + 3 * 2 * KS * 1024;
+  static constexpr int kBytes = std::max(kSlab, TokenTile<NP, KS>::kBytes);
+};
+
+// One workgroup: a chunk of one key head, its value heads in turn; wave w has the
+// tokens of tile w as rows of dQ and dK.
+template <typename InT, int NP, int KS, bool VEC>
+__global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
+  using Tile = TokenTile<NP, KS>;
+  using Lds = GradLds<InT, NP, KS>;
+  constexpr int DKT = 2 * KS, ROWS = 32 * KS;
+  extern __shared__ __align__(16) char staged[];
+  __shared__ ChunkGates gates;
+  __shared__ float scalars[kGateFloats];
+  __shared__ float own_sum[64], end_sum[64], beta_sum[64], diag_dP[64], waves_sum[kWaves];
+  const ChunkArgs& a = s.c;
+  const int lane = threadIdx.x % 64, w = wave_index(), g4 = (lane >> 4) * 4, col = lane & 15;
+  const int chunk = blockIdx.x % a.chunks, bhk = blockIdx.x / a.chunks;
+  const int b = bhk / a.Hk, hk = bhk - b * a.Hk;
+  const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(chunk) * kChunk;
+  const int n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(chunk) * kChunk));
+  const InT* q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
+  const InT* k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
+  uint16_t* sdO = reinterpret_cast<uint16_t*>(staged + Lds::kdO);
+  uint16_t* sU = reinterpret_cast<uint16_t*>(staged + Lds::kU);
+  uint16_t* sdR = reinterpret_cast<uint16_t*>(staged + Lds::kdR);
+  uint16_t* sH = reinterpret_cast<uint16_t*>(staged + Lds::kH);
+  uint16_t* sdH = reinterpret_cast<uint16_t*>(staged + Lds::kdH);
+  uint16_t* stok = reinterpret_cast<uint16_t*>(staged);
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int limit = (a.dv + 7) / 8 * 8;
+
+  f32x4 dq_sum[DKT], dk_sum[DKT];
+#pragma unroll
+  for (int m = 0; m < DKT; ++m) dq_sum[m] = dk_sum[m] = zero;
+
+  for (int gi = 0; gi < a.group; ++gi) {
+    const int h = hk * a.group + gi, bh = b * a.Hv + h;
+    const int64_t record = static_cast<int64_t>(bh) * a.chunks + chunk;
+    const float* U = s.U + record * kChunk * s.cols;
+    const float* dR = s.dR + record * kChunk * s.cols;
+    const float* H0 = s.states + record * ROWS * s.cols;
+    const float* dH1 = s.dstates + record * ROWS * s.cols;
+    const InT* dout = static_cast<const InT*>(s.dout) + (t0 * a.Hv + h) * a.dv;
+    __syncthreads();  // the previous head's scalars are used
+    if (w == 0) chunk_gates<InT>(a, b, h, chunk, scalars, lane, &gates);
+
+    f32x4 E1[DKT], E2[DKT], E3[DKT];  // dO H0^T, dR H0^T, U dH1^T: rows of tile w, columns of state tile m
+#pragma unroll
+    for (int m = 0; m < DKT; ++m) E1[m] = E2[m] = E3[m] = zero;
+    // U dO^T and U dR^T (rows of tile j <= w, columns w); dO U^T and dR U^T (rows of tile i >= w, columns w)
+    f32x4 Pc[4] = {zero, zero, zero, zero}, Sc[4] = {zero, zero, zero, zero};
+    f32x4 Pr[4] = {zero, zero, zero, zero}, Sr[4] = {zero, zero, zero, zero};
+    float hh = 0.0f;  // the thread's part of <dH1, H0>
+    for (int d0 = 0; d0 < a.dv; d0 += 32) {
+      __syncthreads();
+      stage_tokens<InT, NP, 1, VEC, kThreads>(sdO, dout, static_cast<int64_t>(a.Hv) * a.dv, n_tokens, d0, a.dv);
+      {
+        f32x4 x, y;
+        stage_slab<4, false>(sU, U, s.cols, d0, limit, &x, &y, threadIdx.x);
+        stage_slab<4, false>(sdR, dR, s.cols, d0, limit, &x, &y, threadIdx.x);
+      }
+#pragma unroll
+      for (int i = threadIdx.x; i < ROWS * 4; i += kThreads) {
+        f32x4 x, y, dx, dy;
+        stage_slab<DKT, true>(sH, H0, s.cols, d0, limit, &x, &y, i);
+        stage_slab<DKT, true>(sdH, dH1, s.cols, d0, limit, &dx, &dy, i);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) hh = __builtin_fmaf(x[r], dx[r], __builtin_fmaf(y[r], dy[r], hh));
+      }
+      __syncthreads();
+      const Frag<NP> dOw = slab_rows<NP, 4>(sdO, w, lane);
+      const Frag<3> Uw = slab_rows<3, 4>(sU, w, lane), dRw = slab_rows<3, 4>(sdR, w, lane);
+#pragma unroll
+      for (int m = 0; m < DKT; ++m) {
+        const Frag<3> hb = slab_rows<3, DKT>(sH, m, lane), gb = slab_rows<3, DKT>(sdH, m, lane);
+        E1[m] = mma(dOw, hb, E1[m]);
+        E2[m] = mma(dRw, hb, E2[m]);
+        E3[m] = mma(Uw, gb, E3[m]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j <= w) {
+          const Frag<3> Uj = slab_rows<3, 4>(sU, j, lane);
+          Pc[j] = mma(Uj, dOw, Pc[j]);
+          Sc[j] = mma(Uj, dRw, Sc[j]);
+        }
+        if (j >= w) {
+          Pr[j] = mma(slab_rows<NP, 4>(sdO, j, lane), Uw, Pr[j]);
+          Sr[j] = mma(slab_rows<3, 4>(sdR, j, lane), Uw, Sr[j]);
+        }
+      }
+    }
+
+    // d beta comes from the diagonal of dR U^T, and dP's is set aside; then the decays and masks.
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j == w && (col >> 2) == (lane >> 4)) {
+        const int r = col & 3;
+        beta_sum[w * 16 + col] = r == 0 ? Sc[j].x : r == 1 ? Sc[j].y : r == 2 ? Sc[j].z : Sc[j].w;
+        diag_dP[w * 16 + col] = a.scale * (r == 0 ? Pc[j].x : r == 1 ? Pc[j].y : r == 2 ? Pc[j].z : Pc[j].w);
+      }
+      if (j <= w) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int jj = j * 16 + g4 + r, i = w * 16 + col;
+          const float d = i > jj ? pair_decay(gates, i, jj) : 0.0f;
+          Pc[j][r] = i > jj ? a.scale * d * Pc[j][r] : 0.0f;
+          Sc[j][r] = i > jj ? -gates.beta[i] * d * Sc[j][r] : 0.0f;
+        }
+      }
+      if (j >= w) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = j * 16 + g4 + r, jj = w * 16 + col;
+          const float d = i > jj ? pair_decay(gates, i, jj) : 0.0f;
+          Pr[j][r] = i > jj ? a.scale * d * Pr[j][r] : 0.0f;
+          Sr[j][r] = i > jj ? -gates.beta[i] * d * Sr[j][r] : 0.0f;
+        }
+      }
+    }
+    const f32x4 e0 = *reinterpret_cast<const f32x4*>(scalars + kE0 + w * 16 + g4);
+    const f32x4 eC = *reinterpret_cast<const f32x4*>(scalars + kEC + w * 16 + g4);
+    const f32x4 be = *reinterpret_cast<const f32x4*>(scalars + kBeta + w * 16 + g4);
+    // of the lane's four tokens, its columns' part: q . dq + k . (i side - j side), and k . eC (U dH1^T)
+    f32x4 own = zero, ku = zero;
+    const Frag<3> ap[2] = {split8(Pc[0], Pc[1]), split8(Pc[2], Pc[3])};
+    const Frag<3> as[2] = {split8(Sc[0], Sc[1]), split8(Sc[2], Sc[3])};
+    const Frag<3> bp[2] = {split8(Pr[0], Pr[1]), split8(Pr[2], Pr[3])};
+    const Frag<3> bs[2] = {split8(Sr[0], Sr[1]), split8(Sr[2], Sr[3])};
+    __syncthreads();  // the slabs are read
+    stage_tokens<InT, NP, KS, VEC, kThreads>(stok, k, a.ks, n_tokens, 0, a.dk);
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < DKT; ++m) {
+      const int d = state_row(m, col & 12, col & 3);
+      f32x4 kv, qv;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int token = w * 16 + g4 + r;
+        const bool there = token < n_tokens && d < a.dk;
+        kv[r] = there ? load_elem(k + d, token * a.ks) : 0.0f;
+        qv[r] = there ? load_elem(q + d, token * a.qs) : 0.0f;
+      }
+      E1[m] *= a.scale * e0;
+      E2[m] *= -be * e0;
+      E3[m] *= eC;
+      ku += kv * E3[m];
+      f32x4 x = zero;
+#pragma unroll
+      for (int ts = 0; ts < 2; ++ts) {
+        const Frag<NP> kc = Tile::columns(stok, m, ts, lane);
+        if (ts <= w / 2) {
+          E1[m] = mma(ap[ts], kc, E1[m]);
+          E2[m] = mma(as[ts], kc, E2[m]);
+        }
+        if (ts >= w / 2) x = mma(bs[ts], kc, x);
+      }
+      own += qv * E1[m] + kv * (E2[m] - x);
+      const f32x4 dp = *reinterpret_cast<const f32x4*>(&diag_dP[w * 16 + g4]);
+      dq_sum[m] += E1[m] + dp * kv;
+      dk_sum[m] += (E2[m] + E3[m]) + (x + dp * qv);
+    }
+    __syncthreads();
+    stage_tokens<InT, NP, KS, VEC, kThreads>(stok, q, a.qs, n_tokens, 0, a.dk);
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < DKT; ++m) {
+      const int d = state_row(m, col & 12, col & 3);
+      f32x4 x = zero, kv;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int token = w * 16 + g4 + r;
+        kv[r] = token < n_tokens && d < a.dk ? load_elem(k + d, token * a.ks) : 0.0f;
+      }
+#pragma unroll
+      for (int ts = 0; ts < 2; ++ts)
+        if (ts >= w / 2) x = mma(bp[ts], Tile::columns(stok, m, ts, lane), x);
+      dk_sum[m] += x;
+      own -= kv * x;
+    }
+    // sums over the 16 columns' lanes, and over the workgroup
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      own[r] = lanes_sum<16>(own[r]);
+      ku[r] = lanes_sum<16>(ku[r]);
+    }
+    if (col == 0) {
+      *reinterpret_cast<f32x4*>(&own_sum[w * 16 + g4]) = own;
+      *reinterpret_cast<f32x4*>(&end_sum[w * 16 + g4]) = ku;
+    }
+    const float total = lanes_sum<64>(hh);
+    if (lane == 0) waves_sum[w] = total;
+    __syncthreads();
+    if (w == 0) {
+      // a lane per token, sums within its document: from it on, and (eC is 0 before the last document) up to it
+      const int seg = gates.seg[lane];
+      double from = own_sum[lane], upto = end_sum[lane];
+#pragma unroll
+      for (int off = 1; off < 64; off *= 2) {
+        const double after = __shfl_down(from, off), before = __shfl_up(upto, off);
+        const int seg_after = __shfl_down(seg, off), seg_up = __shfl_up(seg, off);
+        if (lane + off < 64 && seg_after == seg) from += after;
+        if (lane >= off && seg_up == seg) upto += before;
+      }
+      const double hh_all = (static_cast<double>(waves_sum[0]) + waves_sum[1]) + (static_cast<double>(waves_sum[2]) + waves_sum[3]);
+      const double sum = from + (upto - end_sum[lane]) + scalars[kAC] * hh_all;
+      const int seg_before = __shfl_up(seg, 1);
+      const bool cut = lane == 0 ? seg > 0 : seg != seg_before;
+      const bool there = lane < n_tokens;
+      const float dg = cut || !there ? 0.0f : static_cast<float>(sum);
+      const float delta = gates.delta[lane];
+      float d_dt = 0.0f;
+      if (there) {
+        const int64_t at = (t0 + lane) * a.Hv + h;
+        const float raw = load_elem(static_cast<const InT*>(a.dt), at) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
+        d_dt = dg * a.A[h] * fast_rcp(1.0f + fast_exp2(-raw * kLog2e));
+        const float d_beta = beta_sum[lane] * (1.0f - gates.beta[lane] / a.beta_scale);
+        if (s.grad_bf16) {
+          store_elem(static_cast<bf16_t*>(s.ddt), at, d_dt);
+          store_elem(static_cast<bf16_t*>(s.dbr), at, d_beta);
+        } else {
+          store_elem(static_cast<float*>(s.ddt), at, d_dt);
+          store_elem(static_cast<float*>(s.dbr), at, d_beta);
+        }
+      }
+      const float dA = lanes_sum<64>(dg * delta), dbias = lanes_sum<64>(d_dt);
+      if (lane == 0) {
+        s.part[record * 2] = dA;
+        s.part[record * 2 + 1] = dbias;
+      }
+    }
+  }
+
+  const int64_t token_k = static_cast<int64_t>(a.Hk) * a.dk;
+#pragma unroll
+  for (int m = 0; m < DKT; ++m) {
+    const int d = state_row(m, col & 12, col & 3);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int token = w * 16 + g4 + r;
+      if (token >= n_tokens || d >= a.dk) continue;
+      const int64_t at = (t0 + token) * token_k + static_cast<int64_t>(hk) * a.dk + d;
+      if (s.grad_bf16) {
+        store_elem(static_cast<bf16_t*>(s.dq), at, dq_sum[m][r]);
+        store_elem(static_cast<bf16_t*>(s.dk), at, dk_sum[m][r]);
+      } else {
+        store_elem(static_cast<float*>(s.dq), at, dq_sum[m][r]);
+        store_elem(static_cast<float*>(s.dk), at, dk_sum[m][r]);
+      }
+    }
+  }
+}
+
+// dA and d dt_bias of a head: its chunks' parts over all batch rows, in a fixed order.
+__global__ __launch_bounds__(kThreads) void delta_head_sums(const float* __restrict__ part, float* dA, float* dbias,
+                                                            int B, int Hv, int chunks) {
+  __shared__ float2 t[kThreads];
+  const int h = blockIdx.x;
+  const int64_t n = static_cast<int64_t>(B) * chunks;
+  float2 x = make_float2(0.0f, 0.0f);
+  for (int64_t i = threadIdx.x; i < n; i += kThreads) {
+    const int64_t b = i / chunks, c = i - b * chunks;
+    const float* p = part + ((b * Hv + h) * chunks + c) * 2;
+    x.x += p[0];
+    x.y += p[1];
+  }
+  t[threadIdx.x] = x;
+  for (int off = kThreads / 2; off > 0; off /= 2) {
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < off) {
+      t[threadIdx.x].x += t[threadIdx.x + off].x;
+      t[threadIdx.x].y += t[threadIdx.x + off].y;
+    }
+  }
+  if (threadIdx.x == 0) {
+    dA[h] = t[0].x;
+    if (dbias) dbias[h] = t[0].y;
+  }
+}
+
+template <typename InT, int NP, int KS, bool VEC, bool ASYNC>
+hipError_t launch_reverse(const BwdArgs& s, int64_t heads, hipStream_t stream) {
+  constexpr bool BOTH = RevStage<InT, NP, KS, true>::kBytes <= kMaxLds;
+  constexpr int kBytes = RevStage<InT, NP, KS, BOTH>::kBytes;
+  constexpr int STAGES = ASYNC && 2 * kBytes <= kMaxLds ? 2 : 1;
+  static_assert(kBytes <= kMaxLds && (BOTH || !ASYNC), "a chunk's stage exceeds LDS");
+  const int64_t blocks = heads * s.col_blocks;
+  SSM_LOG("launch delta_chunk_reverse<%d parts, %d rows>: %d chunks, %d stages of %d bytes; grid %lld x %d threads", NP,
+          32 * KS, s.c.chunks, STAGES, kBytes, static_cast<long long>(blocks), kThreads);
+  hipLaunchKernelGGL((delta_chunk_reverse<InT, NP, KS, VEC, BOTH, ASYNC, STAGES>), dim3(static_cast<unsigned>(blocks)),
+                     dim3(kThreads), STAGES * kBytes, stream, s);
+  return hipGetLastError();
+}
+
+template <typename InT, int NP, int KS, bool VEC>
+hipError_t launch_grads(const BwdArgs& s, int64_t B, hipStream_t stream) {
+  constexpr int kBytes = GradLds<InT, NP, KS>::kBytes;
+  static_assert(kBytes + 4096 <= kMaxLds, "a slab exceeds LDS");
+  const int64_t blocks = B * s.c.Hk * s.c.chunks;
+  SSM_LOG("launch delta_chunk_grads<%d parts, %d rows>: grid %lld x %d threads", NP, 32 * KS,
+          static_cast<long long>(blocks), kThreads);
+  hipLaunchKernelGGL((delta_chunk_grads<InT, NP, KS, VEC>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), kBytes,
+                     stream, s);
+  return hipGetLastError();
+}
+
+template <typename InT, int NP, int KS>
+hipError_t launch_both(const BwdArgs& s, int64_t B, bool vec, bool async, bool vec_out, hipStream_t stream) {
+  const int64_t heads = B * s.c.Hv;
+  hipError_t e;
+  if constexpr (NP == 1) {
+    if (async)
+      e = launch_reverse<InT, NP, KS, true, true>(s, heads, stream);
+    else
+      e = vec ? launch_reverse<InT, NP, KS, true, false>(s, heads, stream)
+              : launch_reverse<InT, NP, KS, false, false>(s, heads, stream);
+  } else {
+    e = vec ? launch_reverse<InT, NP, KS, true, false>(s, heads, stream)
+            : launch_reverse<InT, NP, KS, false, false>(s, heads, stream);
+  }
+  if (e != hipSuccess) return e;
+  return vec && vec_out ? launch_grads<InT, NP, KS, true>(s, B, stream) : launch_grads<InT, NP, KS, false>(s, B, stream);
+}
+
+template <typename InT, int NP>
+hipError_t launch_ks(const BwdArgs& s, int64_t B, bool vec, bool async, bool vec_out, hipStream_t stream) {
+  switch (padded_ks(s.c.dk)) {
+    case 1: return launch_both<InT, NP, 1>(s, B, vec, async, vec_out, stream);
+    case 2: return launch_both<InT, NP, 2>(s, B, vec, async, vec_out, stream);
+    case 3: return launch_both<InT, NP, 3>(s, B, vec, async, vec_out, stream);
+    case 4: return launch_both<InT, NP, 4>(s, B, vec, async, vec_out, stream);
+    case 6: return launch_both<InT, NP, 6>(s, B, vec, async, vec_out, stream);
+    default: return launch_both<InT, NP, 8>(s, B, vec, async, vec_out, stream);
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+DeltaBwdLayout plan_delta_bwd(int64_t B, int64_t L, int Hv, int dk, int dv) {
+  DeltaBwdLayout d{};
+  d.chunks = static_cast<int>((L + kChunk - 1) / kChunk);
+  const size_t n = static_cast<size_t>(B) * Hv * d.chunks;
+  const size_t rows = 32 * static_cast<size_t>(padded_ks(dk)), cols = (static_cast<size_t>(dv) + 15) / 16 * 16;
+  size_t off = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  d.off_records = take(n * kRecBytesBwd);
+  d.off_states = take(n * rows * cols * 4);
+  d.off_U = take(n * kChunk * cols * 4);
+  d.off_dstates = take(n * rows * cols * 4);
+  d.off_dR = take(n * kChunk * cols * 4);
+  d.off_part = take(n * 2 * 4);
+  d.bytes = off;
+  return d;
+}
+
+hipError_t launch_delta_bwd(const DeltaPlan& p, const DeltaBwdPlan& g, const DeltaBwdLayout& lay, void* workspace,
+                            hipStream_t stream) {
+  char* ws = static_cast<char*>(workspace);
+  BwdArgs s{};
+  s.c = chunk_args(p, lay.chunks);
+  s.c.records = ws + lay.off_records;
+  hipError_t e = launch_chunk_prepare(p, s.c, true, stream);
+  if (e != hipSuccess) return e;
+  float* states = reinterpret_cast<float*>(ws + lay.off_states);
+  float* U = reinterpret_cast<float*>(ws + lay.off_U);
+  if ((e = launch_delta_states(p, s.c, states, U, stream)) != hipSuccess) return e;
+  s.states = states;
+  s.U = U;
+  s.dstates = reinterpret_cast<float*>(ws + lay.off_dstates);
+  s.dR = reinterpret_cast<float*>(ws + lay.off_dR);
+  s.part = reinterpret_cast<float*>(ws + lay.off_part);
+  s.cols = (p.dv + 15) / 16 * 16;
+  s.col_blocks = (p.dv + kBlockCols - 1) / kBlockCols;
+  s.grad_bf16 = g.grad_bf16;
+  s.dout = g.dout;
+  s.dh_last = g.dh_last;
+  s.dq = g.dq;
+  s.dk = g.dk;
+  s.dv = g.dv;
+  s.ddt = g.ddt;
+  s.dbr = g.dbr;
+  s.dh0 = g.dh0;
+  const int64_t reach = int64_t{1} << 24;  // elements a token, for 32-bit offsets inside a chunk
+  const bool vec = delta_vec(p);
+  // rows of dout (and, for straight loads, of dv) as whole 16-byte runs
+  const bool vec_out = p.dv % 8 == 0 && delta_aligned(g.dout, 16);
+  const bool async = vec && vec_out && p.in_bf16 && p.dk == 32 * padded_ks(p.dk) && p.qs < reach && p.ks < reach &&
+                     static_cast<int64_t>(p.Hv) * p.dv < reach && delta_aligned(g.dv, 16);
+  e = p.in_bf16 ? launch_ks<bf16_t, 1>(s, p.B, vec, async, vec_out, stream)
+                : launch_ks<float, 3>(s, p.B, vec, false, vec_out, stream);
+  if (e != hipSuccess) return e;
+  SSM_LOG("launch delta_head_sums: grid %d x %d threads", p.Hv, kThreads);
+  hipLaunchKernelGGL(delta_head_sums, dim3(p.Hv), dim3(kThreads), 0, stream, s.part, g.dA, g.dbias,
+                     static_cast<int>(p.B), p.Hv, lay.chunks);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

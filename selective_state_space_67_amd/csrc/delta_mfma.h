@@ -281,6 +281,29 @@ __device__ __forceinline__ void mma_tri(const uint16_t* m, const Frag<3> (&b)[2]
   c[3] += d[1];
 }
 
+// The same for a transposed triangle (rows m sum over the halves ks >= m / 2).
+template <int NB>
+__device__ __forceinline__ void mma_tri_t(const uint16_t* m, const Frag<NB> (&b)[2], int lane, f32x4 (&c)[4]) {
+  Frag<3> a[6];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) a[i] = load_tri<3>(m, i, lane);
+  f32x4 d[2] = {};
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i <= s; ++i) {
+      if (s - i >= NB) continue;
+      c[0] = mfma(a[0].p[i], b[0].p[s - i], c[0]);
+      c[1] = mfma(a[2].p[i], b[0].p[s - i], c[1]);
+      c[2] = mfma(a[4].p[i], b[1].p[s - i], c[2]);
+      c[3] = mfma(a[5].p[i], b[1].p[s - i], c[3]);
+      d[0] = mfma(a[1].p[i], b[1].p[s - i], d[0]);
+      d[1] = mfma(a[3].p[i], b[1].p[s - i], d[1]);
+    }
+  c[0] += d[0];
+  c[1] += d[1];
+}
+
 // Per-chunk scalars: e0, eC and beta of the 64 tokens, aC.
 //   e0 = exp(sum of log decays from the chunk's start through the token), 0 after a reset
 //   eC = exp(sum after the token to the chunk's end), 0 before a reset

@@ -1,6 +1,6 @@
 // Host-side interface between the front end of the gated delta rule and the
 // head norms (api_delta.cpp) and their kernels (delta_step.hip,
-// delta_chunk.hip, qk_norm.hip). Not installed; not part of the ABI.
+// delta_chunk.hip, delta_chunk_bwd.hip, qk_norm.hip). Not installed; not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -44,6 +44,28 @@ struct DeltaChunks {
 // requested = 0: automatic. Pure host arithmetic.
 DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int requested);
 hipError_t launch_delta_chunks(const DeltaPlan& plan, const DeltaChunks& chunks, void* workspace, hipStream_t stream);
+
+// The backward pass (delta_chunk_bwd.hip). DeltaPlan gives the forward's inputs.
+struct DeltaBwdPlan {
+  int grad_bf16;
+  const void* dout;
+  const float* dh_last;
+  void* dq;
+  void* dk;
+  void* dv;
+  void* ddt;
+  void* dbr;
+  float* dA;
+  float* dbias;
+  float* dh0;
+};
+struct DeltaBwdLayout {  // workspace byte offsets
+  int chunks;
+  size_t off_records, off_states, off_U, off_dstates, off_dR, off_part, bytes;
+};
+DeltaBwdLayout plan_delta_bwd(int64_t B, int64_t L, int Hv, int dk, int dv);
+hipError_t launch_delta_bwd(const DeltaPlan& plan, const DeltaBwdPlan& grads, const DeltaBwdLayout& layout,
+                            void* workspace, hipStream_t stream);
 
 // Norms and rotation (qk_norm.hip).
 struct NormPlan {

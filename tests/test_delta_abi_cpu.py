@@ -179,3 +179,44 @@ def test_binding_refusals():
     assert bdd._tokens(packed[..., 3:19].unflatten(-1, (2, 8)), (2, 4, 2, 8), "q", torch.float32) == 40
     with pytest.raises(ValueError):
         bdd._norm_params(q, q, None, None, "max", 0.0, None, None, None, False)
+
+
+def backward(**kw):
+    p = bdd.DeltaBwdParams(batch=2, seqlen=70, key_heads=2, value_heads=4, dk=16, dv=24, in_dtype=bd.SSM_BF16,
+                           grad_dtype=bd.SSM_F32, scale=1.0, beta_scale=1.0)
+    fill(p, ("q", "k", "v", "dt_raw", "beta_raw", "dt_bias", "A", "reset", "h0", "dout", "dh_last", "dq", "dk_out",
+             "dv_out", "d_dt_raw", "dbeta_raw", "dA", "d_dt_bias", "dh0", "workspace"))
+    p.workspace_bytes = 16 << 20
+    return put(p, kw)
+
+
+def test_backward_refusals(lib):
+    n = ctypes.c_size_t()
+    assert lib.ssm_delta_bwd(None, None) == NULL
+    assert lib.ssm_delta_bwd_workspace_size(ctypes.byref(backward()), ctypes.byref(n)) == 0
+    assert 8 * 2 * 4 * 2 * 16 * 24 < n.value < 16 << 20  # more than both states of 2 chunks
+    for name in ("q", "k", "v", "dt_raw", "beta_raw", "A", "dout", "dq", "dk_out", "dv_out", "d_dt_raw", "dbeta_raw",
+                 "dA"):
+        refused(lib, "ssm_delta_bwd", backward(**{name: None}), NULL, name)
+    for kw in SIZES + [dict(seqlen=1 << 27), dict(seqlen=-2), dict(batch=2 ** 20, seqlen=2 ** 26)]:
+        refused(lib, "ssm_delta_bwd", backward(**kw), SHAPE)
+        assert lib.ssm_delta_bwd_workspace_size(ctypes.byref(backward(**kw)), ctypes.byref(n)) == SHAPE
+    refused(lib, "ssm_delta_bwd", backward(grad_dtype=3), DTYPE)
+    refused(lib, "ssm_delta_bwd", backward(dA=0x50000002), ALIGN, "dA")
+    refused(lib, "ssm_delta_bwd", backward(workspace=0x50000080), ALIGN, "workspace")
+    refused(lib, "ssm_delta_bwd", backward(workspace_bytes=1024), WORK)
+    refused(lib, "ssm_delta_bwd", backward(workspace=None), WORK)
+    refused(lib, "ssm_delta_bwd", backward(dq=backward().q), ALIAS, "dq overlaps q")
+    refused(lib, "ssm_delta_bwd", backward(dv_out=backward().dout), ALIAS)
+    refused(lib, "ssm_delta_bwd", backward(dh0=backward().dh_last), ALIAS)
+    refused(lib, "ssm_delta_bwd", backward(dq=backward().dk_out), ALIAS)
+
+
+def test_forward_workspace(lib):
+    """One token needs none; a chunked sequence does, and is refused with too little."""
+    n = ctypes.c_size_t(7)
+    assert lib.ssm_delta_workspace_size(ctypes.byref(delta(seqlen=1)), ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.ssm_delta_workspace_size(ctypes.byref(delta(seqlen=1000)), ctypes.byref(n)) == 0 and n.value > 0
+    refused(lib, "ssm_delta_fwd", delta(seqlen=1000, workspace_bytes=n.value - 1), WORK)
+    refused(lib, "ssm_delta_fwd", delta(seqlen=1000, workspace=None), WORK)
+    refused(lib, "ssm_delta_fwd", delta(batch=2 ** 20, seqlen=2 ** 26), SHAPE)
