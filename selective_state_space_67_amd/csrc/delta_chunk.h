@@ -32,7 +32,7 @@ struct ChunkArgs {
   char* records;  // (bh, chunk)
 };
 
-struct ChunkGates {
+struct alignas(16) ChunkGates {
   float hi[64], lo[64];  // G in log2 units, as a sum of two floats
   float beta[64];
   int seg[64];           // documents started in the chunk up to the token
@@ -83,9 +83,36 @@ __device__ __forceinline__ void chunk_gates(const ChunkArgs& a, int b, int h, in
   if (lane == 63) out[kAC] = seg == 0 ? fast_exp2(static_cast<float>(g)) : 0.0f;
 }
 
-__device__ __forceinline__ float pair_decay(const ChunkGates& s, int i, int j) {
-  const float d = (s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j]);
-  return s.seg[i] == s.seg[j] ? fast_exp2(d) : 0.0f;
+// A lane's share of the sums for elements of 16 x 16 tiles in the D layout: of the four
+// tokens that its rows are, or of the one that its column is.
+struct RowDecay {
+  f32x4 hi, lo, beta;
+  int seg[4];
+};
+struct ColDecay {
+  float hi, lo, beta;
+  int seg;
+};
+__device__ __forceinline__ RowDecay row_decay(const ChunkGates& s, int first) {
+  RowDecay d;
+  d.hi = *reinterpret_cast<const f32x4*>(&s.hi[first]);
+  d.lo = *reinterpret_cast<const f32x4*>(&s.lo[first]);
+  d.beta = *reinterpret_cast<const f32x4*>(&s.beta[first]);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) d.seg[r] = s.seg[first + r];
+  return d;
+}
+__device__ __forceinline__ ColDecay col_decay(const ChunkGates& s, int token) {
+  return ColDecay{s.hi[token], s.lo[token], s.beta[token], s.seg[token]};
+}
+// exp(G_row - G_col), for a row at or after the column, or the reverse; 0 across documents.
+__device__ __forceinline__ float decay_down(const RowDecay& a, int r, const ColDecay& b) {
+  const float e = fast_exp2((a.hi[r] - b.hi) + (a.lo[r] - b.lo));
+  return a.seg[r] == b.seg ? e : 0.0f;
+}
+__device__ __forceinline__ float decay_up(const RowDecay& a, int r, const ColDecay& b) {
+  const float e = fast_exp2((b.hi - a.hi[r]) + (b.lo - a.lo[r]));
+  return a.seg[r] == b.seg ? e : 0.0f;
 }
 
 inline ChunkArgs chunk_args(const DeltaPlan& p, int chunks) {

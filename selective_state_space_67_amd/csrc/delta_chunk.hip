@@ -44,9 +44,11 @@ __device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {  // 16 x 16 
 //   T_ij = -(sum_{k=j+1..i} T_ik A_kj) T_jj
 // with float32 matrix instructions. All blocks are used in the layout in which
 // they were produced: the transposed products T_ij^T = -T_jj^T sum A_kj^T T_ik^T
-// take A_kj as it came out of K K^T.
-template <typename InT, int NP, int KS, bool VEC, bool BWD>
-__global__ __launch_bounds__(kThreads) void delta_chunk_prepare(const ChunkArgs a) {
+// take A_kj as it came out of K K^T. Two workgroups a CU: the second hides the serial
+// parts (3072 chunks of 128 entries in 54 us; one workgroup 73, three 53, four, which
+// spill, 104).
+template <typename InT, int NP, int KS, bool VEC, bool BWD, bool ASYNC>
+__global__ __launch_bounds__(kThreads, 2) void delta_chunk_prepare(const ChunkArgs a) {
   using Tile = TokenTile<NP, KS>;
   extern __shared__ __align__(16) uint16_t staged_tokens[];
   uint16_t* sk = staged_tokens;
@@ -64,6 +66,10 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_prepare(const ChunkArgs 
   const InT* k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
 
   char* rec = a.records + record * (BWD ? kRecBytesBwd : kRecBytes);
+  if constexpr (ASYNC) {  // on their way while the first wave works out the decays
+    stage_tokens_async<KS>(sk, k, a.ks, n_tokens, lane, w);
+    stage_tokens_async<KS>(sq, q, a.qs, n_tokens, lane, w);
+  }
   if (w == 0)
     chunk_gates<InT>(a, b, h, chunk, reinterpret_cast<float*>(rec + (BWD ? kRecGatesBwd : kRecGates)), lane, &gates);
 
@@ -72,9 +78,13 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_prepare(const ChunkArgs 
   // with BWD rows j >= w of Q, columns w of K.
   f32x4 S[4][4] = {}, R[4][4] = {}, P[4] = {};
   for (int d0 = 0; d0 < a.dk; d0 += 32 * KS) {
-    if (d0 > 0) __syncthreads();
-    stage_tokens<InT, NP, KS, VEC, kThreads>(sk, k, a.ks, n_tokens, d0, a.dk);
-    stage_tokens<InT, NP, KS, VEC, kThreads>(sq, q, a.qs, n_tokens, d0, a.dk);
+    if constexpr (ASYNC) {
+      wait_loads();
+    } else {
+      if (d0 > 0) __syncthreads();
+      stage_tokens<InT, NP, KS, VEC, kThreads>(sk, k, a.ks, n_tokens, d0, a.dk);
+      stage_tokens<InT, NP, KS, VEC, kThreads>(sq, q, a.qs, n_tokens, d0, a.dk);
+    }
     __syncthreads();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -105,29 +115,28 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_prepare(const ChunkArgs 
   }
 
   // Decays and betas.
+  {
+    RowDecay rows[4];
+    ColDecay cols[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+      rows[i] = row_decay(gates, i * 16 + g4);
+      cols[i] = col_decay(gates, i * 16 + col);
+    }
+    const ColDecay cw = col_decay(gates, w * 16 + col);
 #pragma unroll
-    for (int j = 0; j <= i; ++j)
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        if ((j < i && i <= w) || (j == i && i == w)) {
-          const int row = i * 16 + g4 + r, c = j * 16 + col;
-          S[i][j][r] = row > c ? gates.beta[row] * pair_decay(gates, row, c) * S[i][j][r] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < i; ++j) {
+          if (i <= w) S[i][j][r] *= rows[i].beta[r] * decay_down(rows[i], r, cols[j]);
+          if (BWD && j >= w) R[j][i][r] *= cols[i].beta * decay_up(rows[j], r, cols[i]);  // transposed: A_ij of the system
         }
-        if (BWD && j < i && j >= w) {
-          const int row = j * 16 + g4 + r, c = i * 16 + col;  // A_ci,row of the system, transposed
-          R[j][i][r] = gates.beta[c] * pair_decay(gates, c, row) * R[j][i][r];
-        }
+        if (i == w) S[i][i][r] *= g4 + r > col ? rows[i].beta[r] * decay_down(rows[i], r, cw) : 0.0f;
+        if (BWD && i >= w) P[i][r] *= i * 16 + g4 + r >= w * 16 + col ? decay_down(rows[i], r, cw) : 0.0f;
+        if (!BWD && i <= w) P[i][r] *= i * 16 + g4 + r <= w * 16 + col ? decay_up(rows[i], r, cw) : 0.0f;
       }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (BWD ? j < w : j > w) continue;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int x = j * 16 + g4 + r, y = w * 16 + col;
-      const int i = BWD ? x : y, jj = BWD ? y : x;
-      P[j][r] = i >= jj ? pair_decay(gates, i, jj) * P[j][r] : 0.0f;
     }
   }
 
@@ -204,25 +213,37 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_prepare(const ChunkArgs 
   }
 }
 
-template <typename InT, int NP, int KS, bool VEC>
+template <typename InT, int NP, int KS, bool VEC, bool ASYNC>
 hipError_t prepare_ks(const ChunkArgs& a, int64_t blocks, bool bwd, hipStream_t stream) {
   const size_t lds = 2 * TokenTile<NP, KS>::kBytes;
   SSM_LOG("launch delta_chunk_prepare<%d parts, %d entries a pass>: backward %d; grid %lld x %d threads", NP, 32 * KS,
           bwd, static_cast<long long>(blocks), kThreads);
   if (bwd)
-    hipLaunchKernelGGL((delta_chunk_prepare<InT, NP, KS, VEC, true>), dim3(static_cast<unsigned>(blocks)),
+    hipLaunchKernelGGL((delta_chunk_prepare<InT, NP, KS, VEC, true, ASYNC>), dim3(static_cast<unsigned>(blocks)),
                        dim3(kThreads), lds, stream, a);
   else
-    hipLaunchKernelGGL((delta_chunk_prepare<InT, NP, KS, VEC, false>), dim3(static_cast<unsigned>(blocks)),
+    hipLaunchKernelGGL((delta_chunk_prepare<InT, NP, KS, VEC, false, ASYNC>), dim3(static_cast<unsigned>(blocks)),
                        dim3(kThreads), lds, stream, a);
   return hipGetLastError();
 }
 
-template <typename InT, int NP, bool VEC>
-hipError_t prepare_vec(const ChunkArgs& a, int64_t blocks, bool bwd, hipStream_t stream) {
-  if (a.dk <= 32) return prepare_ks<InT, NP, 1, VEC>(a, blocks, bwd, stream);
-  if (a.dk <= 64 || NP == 3) return prepare_ks<InT, NP, 2, VEC>(a, blocks, bwd, stream);
-  return prepare_ks<InT, NP, NP == 1 ? 4 : 2, VEC>(a, blocks, bwd, stream);
+// bfloat16 rows in one pass; float32, three times as large, 64 entries a pass.
+template <bool VEC, bool ASYNC>
+hipError_t prepare_bf16(const ChunkArgs& a, int64_t blocks, bool bwd, hipStream_t stream) {
+  switch (padded_ks(a.dk)) {
+    case 1: return prepare_ks<bf16_t, 1, 1, VEC, ASYNC>(a, blocks, bwd, stream);
+    case 2: return prepare_ks<bf16_t, 1, 2, VEC, ASYNC>(a, blocks, bwd, stream);
+    case 3: return prepare_ks<bf16_t, 1, 3, VEC, ASYNC>(a, blocks, bwd, stream);
+    case 4: return prepare_ks<bf16_t, 1, 4, VEC, ASYNC>(a, blocks, bwd, stream);
+    case 6: return prepare_ks<bf16_t, 1, 6, VEC, ASYNC>(a, blocks, bwd, stream);
+    default: return prepare_ks<bf16_t, 1, 8, VEC, ASYNC>(a, blocks, bwd, stream);
+  }
+}
+
+template <bool VEC>
+hipError_t prepare_f32(const ChunkArgs& a, int64_t blocks, bool bwd, hipStream_t stream) {
+  if (a.dk <= 32) return prepare_ks<float, 3, 1, VEC, false>(a, blocks, bwd, stream);
+  return prepare_ks<float, 3, 2, VEC, false>(a, blocks, bwd, stream);
 }
 
 // ---- the walk over the chunks ----
@@ -689,9 +710,9 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd, hipStream_t stream) {
   const int64_t blocks = p.B * p.Hv * a.chunks;
   const bool vec = delta_vec(p);
-  if (p.in_bf16)
-    return vec ? prepare_vec<bf16_t, 1, true>(a, blocks, bwd, stream) : prepare_vec<bf16_t, 1, false>(a, blocks, bwd, stream);
-  return vec ? prepare_vec<float, 3, true>(a, blocks, bwd, stream) : prepare_vec<float, 3, false>(a, blocks, bwd, stream);
+  if (!p.in_bf16) return vec ? prepare_f32<true>(a, blocks, bwd, stream) : prepare_f32<false>(a, blocks, bwd, stream);
+  if (vec && p.dk == 32 * padded_ks(p.dk)) return prepare_bf16<true, true>(a, blocks, bwd, stream);
+  return vec ? prepare_bf16<true, false>(a, blocks, bwd, stream) : prepare_bf16<false, false>(a, blocks, bwd, stream);
 }
 
 DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int requested) {

@@ -491,23 +491,16 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
         beta_sum[w * 16 + col] = r == 0 ? Sc[j].x : r == 1 ? Sc[j].y : r == 2 ? Sc[j].z : Sc[j].w;
         diag_dP[w * 16 + col] = a.scale * (r == 0 ? Pc[j].x : r == 1 ? Pc[j].y : r == 2 ? Pc[j].z : Pc[j].w);
       }
-      if (j <= w) {
+      const RowDecay rows = row_decay(gates, j * 16 + g4);
+      const ColDecay cw = col_decay(gates, w * 16 + col);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int jj = j * 16 + g4 + r, i = w * 16 + col;
-          const float d = i > jj ? pair_decay(gates, i, jj) : 0.0f;
-          Pc[j][r] = i > jj ? a.scale * d * Pc[j][r] : 0.0f;
-          Sc[j][r] = i > jj ? -gates.beta[i] * d * Sc[j][r] : 0.0f;
-        }
-      }
-      if (j >= w) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = j * 16 + g4 + r, jj = w * 16 + col;
-          const float d = i > jj ? pair_decay(gates, i, jj) : 0.0f;
-          Pr[j][r] = i > jj ? a.scale * d * Pr[j][r] : 0.0f;
-          Sr[j][r] = i > jj ? -gates.beta[i] * d * Sr[j][r] : 0.0f;
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int x = j * 16 + g4 + r, y = w * 16 + col;
+        const float up = x < y ? decay_up(rows, r, cw) : 0.0f, down = x > y ? decay_down(rows, r, cw) : 0.0f;
+        Pc[j][r] *= a.scale * up;
+        Sc[j][r] *= -cw.beta * up;
+        Pr[j][r] *= a.scale * down;
+        Sr[j][r] *= -rows.beta[r] * down;
       }
     }
     const f32x4 e0 = *reinterpret_cast<const f32x4*>(scalars + kE0 + w * 16 + g4);

@@ -231,6 +231,17 @@ __device__ __forceinline__ void load_to_lds(const void* src, void* dst) {
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
 
+// Stage 64 tokens like stage_tokens, straight into LDS: bfloat16 rows of 32 KS whole
+// entries, by four waves (wave w: row tile w); tokens past the end repeat the last.
+template <int KS>
+__device__ __forceinline__ void stage_tokens_async(uint16_t* s, const bf16_t* src, int64_t stride, int n_tokens,
+                                                   int lane, int wave) {
+  const int row = min(wave * 16 + (lane & 15), n_tokens - 1);
+  const char* p = reinterpret_cast<const char*>(src + row * stride) + (lane >> 4) * 16;
+#pragma unroll
+  for (int i = 0; i < KS; ++i) load_to_lds(p + i * 64, s + (wave * KS + i) * 512);
+}
+
 // Everything this wave has loaded has arrived.
 __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
 
