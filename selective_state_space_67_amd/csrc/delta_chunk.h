@@ -29,6 +29,7 @@ struct ChunkArgs {
   const float* A;
   const uint8_t* reset;
   float scale, beta_scale;
+  bool vec;       // rows of q and k come as whole 16-byte runs of 8 entries
   char* records;  // (bh, chunk)
 };
 
@@ -115,6 +116,14 @@ __device__ __forceinline__ float decay_up(const RowDecay& a, int r, const ColDec
   return a.seg[r] == b.seg ? e : 0.0f;
 }
 
+inline bool delta_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// Token rows of q and k come as whole 16-byte runs of 8 entries (two of them for float32).
+inline bool delta_vec(const DeltaPlan& p) {
+  const int64_t per = p.in_bf16 ? 8 : 4;
+  return p.dk % 8 == 0 && p.qs % per == 0 && p.ks % per == 0 && delta_aligned(p.q, 16) && delta_aligned(p.k, 16);
+}
+
 inline ChunkArgs chunk_args(const DeltaPlan& p, int chunks) {
   ChunkArgs a{};
   a.L = p.L;
@@ -137,6 +146,7 @@ inline ChunkArgs chunk_args(const DeltaPlan& p, int chunks) {
   a.reset = p.reset;
   a.scale = p.scale;
   a.beta_scale = p.beta_scale;
+  a.vec = delta_vec(p);
   return a;
 }
 
@@ -147,14 +157,6 @@ inline int padded_ks(int dk) {
 }
 
 constexpr int kMaxLds = 160 * 1024;
-
-inline bool delta_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-// Token rows of q and k come as whole 16-byte runs of 8 entries (two of them for float32).
-inline bool delta_vec(const DeltaPlan& p) {
-  const int64_t per = p.in_bf16 ? 8 : 4;
-  return p.dk % 8 == 0 && p.qs % per == 0 && p.ks % per == 0 && delta_aligned(p.q, 16) && delta_aligned(p.k, 16);
-}
 
 // Prepare every chunk (delta_chunk.hip); bwd: the backward's records.
 hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd, hipStream_t stream);

@@ -22,12 +22,10 @@
 // across the pieces, and the full walk starts every piece from its own state.
 #include <algorithm>
 
-#include "delta_chunk.h"
+#include "delta_walk.h"
 
 namespace ssm {
 namespace {
-
-constexpr int kThreads = 256;
 
 __device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {  // 16 x 16 x 16 in float32
 #pragma unroll
@@ -246,350 +244,6 @@ hipError_t prepare_f32(const ChunkArgs& a, int64_t blocks, bool bwd, hipStream_t
   return prepare_ks<float, 3, 2, VEC, false>(a, blocks, bwd, stream);
 }
 
-// ---- the walk over the chunks ----
-
-// What a walk leaves: the outputs, a piece's effect on the state, or every chunk's
-// first state and U (for the backward).
-enum Walk { kOutputs, kAggregates, kStates };
-
-struct ScanArgs {
-  ChunkArgs c;
-  int pieces, chunks_piece;
-  int col_blocks;   // workgroups per (head, piece)
-  int out_bf16, out_runs;  // out_runs: rows of out take whole 16-byte runs
-  const float* h0;  // (bh, dk, dv) or null
-  const float* starts;  // states of pieces 1 .. (bh, piece, 32 KS, cols), or null
-  float* agg;       // aggregates walk: (bh, piece, 32 KS, 32 KS + cols)
-  int cols;         // dv rounded up to 16
-  void* out;
-  float* h_last;
-  float* states;    // states walk: (bh, chunk, 32 KS, cols)
-  float* U;         // states walk: (bh, chunk, 64, cols)
-  int64_t record_bytes, record_gates;
-};
-
-constexpr int kWaves = kThreads / 64;
-constexpr int kBlockCols = 16 * kWaves;  // columns of the state per workgroup
-
-// What a workgroup stages of one chunk, in bytes from the stage's start. T, the
-// first OP parts of P and the scalars keep the record's order.
-template <typename InT, int NP, int KS, Walk MODE, bool QLDS, int OP>
-struct Stage {
-  static constexpr int kK = 0;
-  static constexpr int kQ = kK + TokenTile<NP, KS>::kBytes;
-  static constexpr int kT = kQ + (MODE == kOutputs && QLDS ? TokenTile<NP, KS>::kBytes : 0);
-  static constexpr int kP = kT + kTriBytes;
-  static constexpr int kGates = kP + (MODE == kOutputs ? kTriBytes / 3 * OP : 0);
-  static constexpr int kV = kGates + kGateFloats * 4;  // (64, kBlockCols) of InT
-  static constexpr int kBytes = kV + kChunk * kBlockCols * static_cast<int>(sizeof(InT));
-};
-
-// Where the staging of a chunk reads.
-template <typename InT>
-struct ChunkSource {
-  const InT* q;
-  const InT* k;
-  const InT* v;  // the chunk's first token, column 0 of the head
-  const char* record;
-  const char* gates;
-  int n_tokens;
-};
-
-template <typename InT>
-__device__ __forceinline__ ChunkSource<InT> chunk_source(const ScanArgs& w, int bh, int b, int h, int c) {
-  const ChunkArgs& a = w.c;
-  ChunkSource<InT> s;
-  const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk;
-  const int hk = h / a.group;
-  s.q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
-  s.k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
-  s.v = static_cast<const InT*>(a.v) + t0 * a.vs + static_cast<int64_t>(h) * a.dv;
-  s.record = a.records + (static_cast<int64_t>(bh) * a.chunks + c) * w.record_bytes;
-  s.gates = s.record + w.record_gates;
-  s.n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(c) * kChunk));
-  return s;
-}
-
-// ASYNC staging: whole 16-byte runs straight into LDS, 1 KB a wave and instruction.
-// Tokens past the end repeat the last one (their beta is 0, so they change
-// nothing), columns past dv repeat the last ones (never stored). A lane's byte
-// offsets from the chunk's first token are the same for every whole chunk.
-struct LaneOffsets {
-  uint32_t k, q, v[2];
-};
-
-__device__ __forceinline__ LaneOffsets lane_offsets(const ChunkArgs& a, int n_tokens, int col0, int lane, int wave) {
-  LaneOffsets o;
-  const int last = n_tokens - 1, row = min(wave * 16 + (lane & 15), last);  // wave w: row tile w
-  o.k = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ks) * 2 + (lane >> 4) * 16;
-  o.q = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.qs) * 2 + (lane >> 4) * 16;
-  const int col = max(0, min(col0 + (lane & 7) * 8, a.dv - 8));
-#pragma unroll
-  for (int i = 0; i < 2; ++i)  // 8 tokens of 64 columns
-    o.v[i] = static_cast<uint32_t>(min((wave * 2 + i) * 8 + lane / 8, last)) * static_cast<uint32_t>(a.vs) * 2 + col * 2;
-  return o;
-}
-
-template <typename InT, int KS, Walk MODE, int OP>
-__device__ __forceinline__ void stage_async(char* st, const ChunkSource<InT>& s, const LaneOffsets& o, int lane,
-                                            int wave) {
-  using S = Stage<InT, 1, KS, MODE, true, OP>;
-  static_assert(kWaves == 4, "row tile w and values 16 w .. of wave w");
-  const char *k = reinterpret_cast<const char*>(s.k), *q = reinterpret_cast<const char*>(s.q);
-  const char* v = reinterpret_cast<const char*>(s.v);
-#pragma unroll
-  for (int i = 0; i < KS; ++i) {
-    load_to_lds(k + i * 64 + o.k, st + S::kK + (wave * KS + i) * 1024);
-    if constexpr (MODE == kOutputs) load_to_lds(q + i * 64 + o.q, st + S::kQ + (wave * KS + i) * 1024);
-  }
-  const uint32_t own = lane * 16;
-  constexpr int kTri = (MODE == kOutputs ? kTriBytes + kTriBytes / 3 * OP : kTriBytes) / 1024;
-#pragma unroll
-  for (int i = 0; i < (kTri + kWaves - 1) / kWaves; ++i) {
-    const int f = wave + i * kWaves;
-    if (f < kTri) load_to_lds(s.record + f * 1024 + own, st + S::kT + f * 1024);
-  }
-  if (wave == 3) load_to_lds(s.gates + own, st + S::kGates);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) load_to_lds(v + o.v[i], st + S::kV + (wave * 2 + i) * 1024);
-}
-
-// Staging through registers, for float32 and for rows that are not whole runs.
-template <typename InT, int NP, int KS, bool VEC, Walk MODE, bool QLDS, int OP>
-__device__ __forceinline__ void stage_sync(char* st, const ChunkArgs& a, const ChunkSource<InT>& s, int col0) {
-  using S = Stage<InT, NP, KS, MODE, QLDS, OP>;
-  stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kK), s.k, a.ks, s.n_tokens, 0, a.dk);
-  if constexpr (MODE == kOutputs && QLDS)
-    stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kQ), s.q, a.qs, s.n_tokens, 0, a.dk);
-  constexpr int kRuns = (MODE == kOutputs ? kTriBytes + kTriBytes / 3 * OP : kTriBytes) / 16;
-  for (int i = threadIdx.x; i < kRuns; i += kThreads)
-    reinterpret_cast<u32x4*>(st + S::kT)[i] = reinterpret_cast<const u32x4*>(s.record)[i];
-  reinterpret_cast<float*>(st + S::kGates)[threadIdx.x] = reinterpret_cast<const float*>(s.gates)[threadIdx.x];
-  InT* v = reinterpret_cast<InT*>(st + S::kV);
-#pragma unroll
-  for (int i = 0; i < kChunk * kBlockCols / kThreads; ++i) {
-    const int e = threadIdx.x + i * kThreads, token = e / kBlockCols, col = col0 + e % kBlockCols;
-    InT x{};
-    if (token < s.n_tokens && col >= 0 && col < a.dv) x = s.v[token * a.vs + col];
-    v[e] = x;
-  }
-}
-
-// One wave's walk over the chunks of a piece with 16 columns of the state.
-// AGG: the aggregates walk (no read-out; the first 32 KS columns start from the
-// identity). With two stages the next chunk is loaded while this one is worked on.
-// OP: parts of the products that only the output sees; two (2^-17) where it is
-// rounded to bfloat16 (2^-9).
-template <typename InT, int NP, int KS, bool VEC, Walk MODE, bool QLDS, bool ASYNC, int STAGES, int OP>
-__global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
-  using Tile = TokenTile<NP, KS>;
-  using S = Stage<InT, NP, KS, MODE, QLDS, OP>;
-  constexpr int DKT = 2 * KS;  // row tiles of the state
-  constexpr bool AGG = MODE == kAggregates, OUT = MODE == kOutputs;
-  extern __shared__ __align__(16) char staged[];
-  const ChunkArgs& a = s.c;
-  const int lane = threadIdx.x % 64, wave = wave_index(), g4 = (lane >> 4) * 4;
-  const int cb = blockIdx.x % s.col_blocks, rest = blockIdx.x / s.col_blocks;
-  const int piece = rest % s.pieces, bh = rest / s.pieces;
-  const int b = bh / a.Hv, h = bh - b * a.Hv;
-  const int strip = cb * kWaves + wave;                            // 16-column strip
-  const int col0 = (cb * kWaves - (AGG ? DKT : 0)) * 16;           // the workgroup's first column of v
-  const int own = col0 + wave * 16 + (lane & 15);                  // the lane's
-  const bool has_v = own >= 0 && own < a.dv;
-  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-
-  f32x4 H[DKT];
-#pragma unroll
-  for (int m = 0; m < DKT; ++m) {
-    H[m] = zero;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = state_row(m, g4, r);
-      if (AGG) {
-        if (strip * 16 + (lane & 15) == row) H[m][r] = 1.0f;
-      } else if (piece > 0) {
-        if (own < s.cols)
-          H[m][r] = s.starts[((static_cast<int64_t>(bh) * s.pieces + piece) * (32 * KS) + row) * s.cols + own];
-      } else if (s.h0 && row < a.dk && has_v) {
-        H[m][r] = s.h0[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own];
-      }
-    }
-  }
-
-  const int c0 = piece * s.chunks_piece, c1 = min(a.chunks, c0 + s.chunks_piece);
-  ChunkSource<InT> src = chunk_source<InT>(s, bh, b, h, c0);
-  const LaneOffsets whole = lane_offsets(a, kChunk, col0, lane, wave);
-  const auto stage = [&](char* st, const ChunkSource<InT>& from) {
-    if constexpr (ASYNC)
-      stage_async<InT, KS, MODE, OP>(
-          st, from, from.n_tokens == kChunk ? whole : lane_offsets(a, from.n_tokens, col0, lane, wave), lane, wave);
-    else
-      stage_sync<InT, NP, KS, VEC, MODE, QLDS, OP>(st, a, from, col0);
-  };
-  if constexpr (STAGES == 2) stage(staged, src);
-  for (int c = c0; c < c1; ++c) {
-    char* st = staged + (STAGES == 2 ? ((c - c0) & 1) * S::kBytes : 0);
-    ChunkSource<InT> next = src;
-    next.q += kChunk * a.qs;
-    next.k += kChunk * a.ks;
-    next.v += kChunk * a.vs;
-    next.record += s.record_bytes;
-    next.gates += s.record_bytes;
-    next.n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(c + 1) * kChunk));
-    if constexpr (STAGES == 2) {
-      wait_loads();
-      __syncthreads();  // this stage is loaded, and the other one is no longer read
-      if (c + 1 < c1) stage(staged + ((c + 1 - c0) & 1) * S::kBytes, next);
-    } else {
-      __syncthreads();  // the previous chunk is no longer read
-      stage(st, src);
-      wait_loads();
-      __syncthreads();
-    }
-    const uint16_t* sk = reinterpret_cast<const uint16_t*>(st + S::kK);
-    const uint16_t* sq = reinterpret_cast<const uint16_t*>(st + S::kQ);
-    const float* gates = reinterpret_cast<const float*>(st + S::kGates);
-
-    if constexpr (MODE == kStates) {  // in the waves' own layout: columns of the strips are 16 neighbours
-      float* to = s.states + (static_cast<int64_t>(bh) * a.chunks + c) * (32 * KS) * s.cols + own;
-#pragma unroll
-      for (int m = 0; m < DKT; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (own < s.cols) to[static_cast<int64_t>(state_row(m, g4, r)) * s.cols] = H[m][r];
-    }
-    f32x4 X[4] = {zero, zero, zero, zero}, Y[4] = {zero, zero, zero, zero};
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const Frag<3> hb = split8(H[2 * ks], H[2 * ks + 1]);
-      Frag<NP> kf[4], qf[4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        kf[m] = Tile::rows(sk, m, ks, lane);
-        if constexpr (OUT) {
-          if constexpr (QLDS)
-            qf[m] = Tile::rows(sq, m, ks, lane);
-          else
-            qf[m] = rows_from_global<InT, VEC>(src.q, a.qs, src.n_tokens, a.dk, m, ks, lane);
-        }
-      }
-      mma_n(kf, hb, X);
-      if constexpr (OUT) mma_n<OP>(qf, hb, Y);
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      f32x4 V = zero;
-      if constexpr (sizeof(InT) == 2) {
-        // the lane's column of tokens 16 m + g4 ..
-        const u32x2 w = read_transposed(reinterpret_cast<const uint16_t*>(st + S::kV) +
-                                        (m * 16 + g4 + ((lane & 15) >> 2)) * kBlockCols + wave * 16 + (lane & 3) * 4);
-        V = f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                  __uint_as_float(w.y & 0xFFFF0000u)};
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          V[r] = reinterpret_cast<const float*>(st + S::kV)[(m * 16 + g4 + r) * kBlockCols + wave * 16 + (lane & 15)];
-      }
-      if (AGG && !has_v) V = zero;
-      const f32x4 e0 = *reinterpret_cast<const f32x4*>(gates + kE0 + m * 16 + g4);
-      const f32x4 be = *reinterpret_cast<const f32x4*>(gates + kBeta + m * 16 + g4);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        X[m][r] = be[r] * __builtin_fmaf(-e0[r], X[m][r], V[r]);
-        Y[m][r] *= e0[r];
-      }
-    }
-    f32x4 U[4] = {zero, zero, zero, zero};
-    {
-      const Frag<3> rb[2] = {split8(X[0], X[1]), split8(X[2], X[3])};
-      mma_tri(reinterpret_cast<const uint16_t*>(st + S::kT), rb, lane, U);
-    }
-    if constexpr (OUT) {
-      const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
-      mma_tri<OP>(reinterpret_cast<const uint16_t*>(st + S::kP), ub, lane, Y);
-    }
-    if constexpr (MODE == kStates) {
-      float* to = s.U + (static_cast<int64_t>(bh) * a.chunks + c) * kChunk * s.cols + own;
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (own < s.cols) to[(m * 16 + g4 + r) * s.cols] = U[m][r];
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) U[m] *= *reinterpret_cast<const f32x4*>(gates + kEC + m * 16 + g4);
-    const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
-    const float aC = gates[kAC];
-#pragma unroll
-    for (int m = 0; m < DKT; ++m) H[m] *= aC;
-#pragma unroll
-    for (int ts = 0; ts < 2; ++ts) {
-      Frag<NP> kc[DKT];
-#pragma unroll
-      for (int m = 0; m < DKT; ++m) kc[m] = Tile::columns(sk, m, ts, lane);
-      mma_n(kc, ub[ts], H);
-    }
-
-    if constexpr (OUT) {
-      const int64_t row0 = (static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk) * a.Hv + h;  // x dv
-      if (OP == 2 && (ASYNC || s.out_runs)) {  // ASYNC has whole runs everywhere
-        // The strip's place among the staged values is this wave's alone and has been
-        // read: the outputs turn there from columns to rows, 16 bytes a lane.
-        uint16_t* o = reinterpret_cast<uint16_t*>(st + S::kV) + wave * 16;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int r = 0; r < 4; r += 2) {
-            const uint32_t w = bf16_words(a.scale * Y[m][r], a.scale * Y[m][r + 1]);
-            uint16_t* p = o + (m * 16 + g4 + r) * kBlockCols + (lane & 15);
-            p[0] = static_cast<uint16_t>(w);
-            p[kBlockCols] = static_cast<uint16_t>(w >> 16);
-          }
-        char* dst = static_cast<char*>(s.out) + (row0 * a.dv + col0 + wave * 16) * 2;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int token = i * 32 + lane / 2, half = (lane & 1) * 8;
-          const u32x4 w = *reinterpret_cast<const u32x4*>(o + token * kBlockCols + half);
-          if (token < src.n_tokens && col0 + wave * 16 + half < a.dv)
-            *reinterpret_cast<u32x4*>(dst + static_cast<uint32_t>(token * a.Hv * a.dv + half) * 2) = w;
-        }
-      } else {
-        const int64_t step = static_cast<int64_t>(a.Hv) * a.dv;  // elements between tokens
-        const int64_t lane0 = row0 * a.dv + g4 * step + own;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if (!has_v || m * 16 + g4 + r >= src.n_tokens) continue;
-            if (OP == 2 || s.out_bf16)
-              store_elem(static_cast<bf16_t*>(s.out) + (m * 16 + r) * step, lane0, a.scale * Y[m][r]);
-            else
-              store_elem(static_cast<float*>(s.out) + (m * 16 + r) * step, lane0, a.scale * Y[m][r]);
-          }
-      }
-    }
-    src = next;
-  }
-
-  if (AGG) {
-    const int width = 32 * KS + s.cols, at = strip * 16 + (lane & 15);
-    if (at >= width) return;
-    float* dst = s.agg + (static_cast<int64_t>(bh) * s.pieces + piece) * (32 * KS) * width + at;
-#pragma unroll
-    for (int m = 0; m < DKT; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) dst[static_cast<int64_t>(state_row(m, g4, r)) * width] = H[m][r];
-  } else if (OUT && s.h_last && c1 == a.chunks && has_v) {
-#pragma unroll
-    for (int m = 0; m < DKT; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = state_row(m, g4, r);
-        if (row < a.dk) s.h_last[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own] = H[m][r];
-      }
-  }
-}
-
 // The states that pieces 1 .. start from: S <- M S + N over the pieces, 16 columns
 // and all rows a workgroup, its waves sharing the rows. The next piece's
 // operands are loaded before the current ones are used.
@@ -655,57 +309,30 @@ __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
   }
 }
 
-template <typename InT, int NP, int KS, bool VEC, Walk MODE, bool QLDS, bool ASYNC, int OP>
-hipError_t launch_walk(const ScanArgs& s, int64_t blocks, hipStream_t stream) {
-  constexpr int kBytes = Stage<InT, NP, KS, MODE, QLDS, OP>::kBytes;
-  constexpr int STAGES = ASYNC && 2 * kBytes <= kMaxLds ? 2 : 1;
-  static_assert(kBytes <= kMaxLds, "a chunk's stage exceeds LDS");
-  SSM_LOG("launch delta_chunk_scan<%d parts, %d rows, walk %d>: %d pieces of %d chunks, %d stages of %d bytes; "
-          "grid %lld x %d threads",
-          NP, 32 * KS, MODE, s.pieces, s.chunks_piece, STAGES, kBytes, static_cast<long long>(blocks), kThreads);
-  hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, VEC, MODE, QLDS, ASYNC, STAGES, OP>),
-                     dim3(static_cast<unsigned>(blocks)), dim3(kThreads), STAGES * kBytes, stream, s);
+template <int KS>
+hipError_t fold_ks(const FoldArgs& f, int64_t heads, hipStream_t stream) {
+  SSM_LOG("launch delta_fold<%d rows>: %d pieces; grid %lld x %d threads", 32 * KS, f.pieces,
+          static_cast<long long>(heads * f.strips), 2 * KS * 64);
+  hipLaunchKernelGGL((delta_fold<KS>), dim3(static_cast<unsigned>(heads * f.strips)), dim3(2 * KS * 64), 0, stream, f);
   return hipGetLastError();
-}
-
-template <typename InT, int NP, int KS, bool VEC, bool ASYNC>
-hipError_t launch_scan_ks(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs s, hipStream_t stream) {
-  // K and Q of a chunk side by side fit in LDS except for float32 past 128 entries
-  constexpr bool QLDS = Stage<InT, NP, KS, kOutputs, true, 3>::kBytes <= kMaxLds;
-  const int64_t heads = p.B * p.Hv;
-  if (plan.pieces > 1) {
-    const int strips = 2 * KS + s.cols / 16;
-    s.col_blocks = (strips + kWaves - 1) / kWaves;
-    hipError_t e = launch_walk<InT, NP, KS, VEC, kAggregates, QLDS, ASYNC, 3>(s, heads * plan.pieces * s.col_blocks, stream);
-    if (e != hipSuccess) return e;
-    FoldArgs f{s.agg, s.h0, const_cast<float*>(s.starts), plan.pieces, p.dk, p.dv, s.cols, s.cols / 16};
-    SSM_LOG("launch delta_fold<%d rows>: grid %lld x %d threads", 32 * KS, static_cast<long long>(heads * f.strips),
-            2 * KS * 64);
-    hipLaunchKernelGGL((delta_fold<KS>), dim3(static_cast<unsigned>(heads * f.strips)), dim3(2 * KS * 64), 0, stream, f);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  s.col_blocks = (s.cols / 16 + kWaves - 1) / kWaves;
-  const int64_t blocks = heads * plan.pieces * s.col_blocks;
-  if (s.states) return launch_walk<InT, NP, KS, VEC, kStates, QLDS, ASYNC, 3>(s, blocks, stream);
-  if (NP == 1 && s.out_bf16) return launch_walk<InT, NP, KS, VEC, kOutputs, QLDS, ASYNC, NP == 1 ? 2 : 3>(s, blocks, stream);
-  return launch_walk<InT, NP, KS, VEC, kOutputs, QLDS, ASYNC, 3>(s, blocks, stream);
-}
-
-template <typename InT, int NP, bool VEC, bool ASYNC>
-hipError_t launch_scan_vec(const DeltaPlan& p, const DeltaChunks& plan, const ScanArgs& s, hipStream_t stream) {
-  switch (padded_ks(p.dk)) {
-    case 1: return launch_scan_ks<InT, NP, 1, VEC, ASYNC>(p, plan, s, stream);
-    case 2: return launch_scan_ks<InT, NP, 2, VEC, ASYNC>(p, plan, s, stream);
-    case 3: return launch_scan_ks<InT, NP, 3, VEC, ASYNC>(p, plan, s, stream);
-    case 4: return launch_scan_ks<InT, NP, 4, VEC, ASYNC>(p, plan, s, stream);
-    case 6: return launch_scan_ks<InT, NP, 6, VEC, ASYNC>(p, plan, s, stream);
-    default: return launch_scan_ks<InT, NP, 8, VEC, ASYNC>(p, plan, s, stream);
-  }
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
+
+hipError_t launch_delta_fold(const DeltaPlan& p, const DeltaChunks& plan, const ScanArgs& s, hipStream_t stream) {
+  const FoldArgs f{s.agg, s.h0, const_cast<float*>(s.starts), plan.pieces, p.dk, p.dv, s.cols, s.cols / 16};
+  const int64_t heads = p.B * p.Hv;
+  switch (padded_ks(p.dk)) {
+    case 1: return fold_ks<1>(f, heads, stream);
+    case 2: return fold_ks<2>(f, heads, stream);
+    case 3: return fold_ks<3>(f, heads, stream);
+    case 4: return fold_ks<4>(f, heads, stream);
+    case 6: return fold_ks<6>(f, heads, stream);
+    default: return fold_ks<8>(f, heads, stream);
+  }
+}
 
 hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd, hipStream_t stream) {
   const int64_t blocks = p.B * p.Hv * a.chunks;
@@ -746,16 +373,11 @@ hipError_t launch_scan(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs& s,
   // a chunk's rows lie within 2^31 bytes (for 32-bit offsets)
   const int64_t reach = int64_t{1} << 24;  // elements a token
   s.out_runs = p.dv % 8 == 0 && delta_aligned(p.out, 16) && static_cast<int64_t>(p.Hv) * p.dv < reach;
-  const bool vec = delta_vec(p);
-  if (!p.in_bf16)
-    return vec ? launch_scan_vec<float, 3, true, false>(p, plan, s, stream)
-               : launch_scan_vec<float, 3, false, false>(p, plan, s, stream);
+  if (!p.in_bf16) return launch_walk_f32(p, plan, s, stream);
   // Straight loads to LDS: rows that fill the padded tile, values in whole runs.
-  const bool async = vec && p.dk == 32 * padded_ks(p.dk) && p.dv % 8 == 0 && p.vs % 8 == 0 && delta_aligned(p.v, 16) &&
+  const bool direct = s.c.vec && p.dk == 32 * padded_ks(p.dk) && p.dv % 8 == 0 && p.vs % 8 == 0 && delta_aligned(p.v, 16) &&
                      p.qs < reach && p.ks < reach && p.vs < reach && (s.out_runs || !p.out_bf16);
-  if (async) return launch_scan_vec<bf16_t, 1, true, true>(p, plan, s, stream);
-  return vec ? launch_scan_vec<bf16_t, 1, true, false>(p, plan, s, stream)
-             : launch_scan_vec<bf16_t, 1, false, false>(p, plan, s, stream);
+  return direct ? launch_walk_bf16_direct(p, plan, s, stream) : launch_walk_bf16(p, plan, s, stream);
 }
 
 }  // namespace

@@ -37,6 +37,7 @@ struct BwdArgs {
   ChunkArgs c;
   int col_blocks, cols;
   int grad_bf16;
+  bool vec_out;          // rows of dout come as whole 16-byte runs
   const void* dout;
   const float* dh_last;
   const float* states;   // (bh, chunk, 32 KS, cols)
@@ -110,12 +111,13 @@ __device__ __forceinline__ void rev_stage_async(char* st, const RevSource<InT>& 
   for (int i = 0; i < 2; ++i) load_to_lds(d + o.o[i], st + S::kdO + (wave * 2 + i) * 1024);
 }
 
-template <typename InT, int NP, int KS, bool VEC, bool BOTH>
+template <typename InT, int NP, int KS, bool BOTH>
 __device__ __forceinline__ void rev_stage_sync(char* st, const ChunkArgs& a, const RevSource<InT>& s, int col0) {
   using S = RevStage<InT, NP, KS, BOTH>;
-  stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kK), s.k, a.ks, s.n_tokens, 0, a.dk);
-  if constexpr (BOTH)
-    stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kQ), s.q, a.qs, s.n_tokens, 0, a.dk);
+  uint16_t* sk = reinterpret_cast<uint16_t*>(st + S::kK);
+  uint16_t* sq = reinterpret_cast<uint16_t*>(st + S::kQ);
+  stage_rows<InT, NP, KS, kThreads>(sk, s.k, a.ks, s.n_tokens, a.dk, a.vec);
+  if constexpr (BOTH) stage_rows<InT, NP, KS, kThreads>(sq, s.q, a.qs, s.n_tokens, a.dk, a.vec);
   constexpr int kRuns = (2 * kTriBytes + kGateFloats * 4) / 16;
   for (int i = threadIdx.x; i < kRuns; i += kThreads)
     reinterpret_cast<u32x4*>(st + S::kTt)[i] = reinterpret_cast<const u32x4*>(s.record + kRecTt)[i];
@@ -129,7 +131,7 @@ __device__ __forceinline__ void rev_stage_sync(char* st, const ChunkArgs& a, con
   }
 }
 
-template <typename InT, int NP, int KS, bool VEC, bool BOTH, bool ASYNC, int STAGES>
+template <typename InT, int NP, int KS, bool BOTH, bool ASYNC, int STAGES>
 __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s) {
   using Tile = TokenTile<NP, KS>;
   using S = RevStage<InT, NP, KS, BOTH>;
@@ -170,7 +172,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
                                from.n_tokens == kChunk ? whole : rev_offsets(a, from.n_tokens, col0, lane, wave), lane,
                                wave);
     else
-      rev_stage_sync<InT, NP, KS, VEC, BOTH>(st, a, from, col0);
+      rev_stage_sync<InT, NP, KS, BOTH>(st, a, from, col0);
   };
   if constexpr (STAGES == 2) stage(staged, src);
   for (int c = a.chunks - 1; c >= 0; --c) {
@@ -289,7 +291,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
     }
     if constexpr (!BOTH) {
       __syncthreads();
-      stage_tokens<InT, NP, KS, VEC, kThreads>(reinterpret_cast<uint16_t*>(st + S::kQ), src.q, a.qs, src.n_tokens, 0, a.dk);
+      stage_rows<InT, NP, KS, kThreads>(reinterpret_cast<uint16_t*>(st + S::kQ), src.q, a.qs, src.n_tokens, a.dk, a.vec);
       __syncthreads();
     }
     {
@@ -395,7 +397,7 @@ struct GradLds {
 
 // One workgroup: a chunk of one key head, its value heads in turn; wave w has the
 // tokens of tile w as rows of dQ and dK.
-template <typename InT, int NP, int KS, bool VEC>
+template <typename InT, int NP, int KS>
 __global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
   using Tile = TokenTile<NP, KS>;
   using Lds = GradLds<InT, NP, KS>;
@@ -445,7 +447,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
     float hh = 0.0f;  // the thread's part of <dH1, H0>
     for (int d0 = 0; d0 < a.dv; d0 += 32) {
       __syncthreads();
-      stage_tokens<InT, NP, 1, VEC, kThreads>(sdO, dout, static_cast<int64_t>(a.Hv) * a.dv, n_tokens, d0, a.dv);
+      stage_rows<InT, NP, 1, kThreads>(sdO, dout + d0, static_cast<int64_t>(a.Hv) * a.dv, n_tokens, a.dv - d0, s.vec_out);
       {
         f32x4 x, y;
         stage_slab<4, false>(sU, U, s.cols, d0, limit, &x, &y, threadIdx.x);
@@ -513,7 +515,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
     const Frag<3> bp[2] = {split8(Pr[0], Pr[1]), split8(Pr[2], Pr[3])};
     const Frag<3> bs[2] = {split8(Sr[0], Sr[1]), split8(Sr[2], Sr[3])};
     __syncthreads();  // the slabs are read
-    stage_tokens<InT, NP, KS, VEC, kThreads>(stok, k, a.ks, n_tokens, 0, a.dk);
+    stage_rows<InT, NP, KS, kThreads>(stok, k, a.ks, n_tokens, a.dk, a.vec);
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < DKT; ++m) {
@@ -546,7 +548,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
       dk_sum[m] += (E2[m] + E3[m]) + (x + dp * qv);
     }
     __syncthreads();
-    stage_tokens<InT, NP, KS, VEC, kThreads>(stok, q, a.qs, n_tokens, 0, a.dk);
+    stage_rows<InT, NP, KS, kThreads>(stok, q, a.qs, n_tokens, a.dk, a.vec);
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < DKT; ++m) {
@@ -663,7 +665,7 @@ __global__ __launch_bounds__(kThreads) void delta_head_sums(const float* __restr
   }
 }
 
-template <typename InT, int NP, int KS, bool VEC, bool ASYNC>
+template <typename InT, int NP, int KS, bool ASYNC>
 hipError_t launch_reverse(const BwdArgs& s, int64_t heads, hipStream_t stream) {
   constexpr bool BOTH = RevStage<InT, NP, KS, true>::kBytes <= kMaxLds;
   constexpr int kBytes = RevStage<InT, NP, KS, BOTH>::kBytes;
@@ -672,50 +674,43 @@ hipError_t launch_reverse(const BwdArgs& s, int64_t heads, hipStream_t stream) {
   const int64_t blocks = heads * s.col_blocks;
   SSM_LOG("launch delta_chunk_reverse<%d parts, %d rows>: %d chunks, %d stages of %d bytes; grid %lld x %d threads", NP,
           32 * KS, s.c.chunks, STAGES, kBytes, static_cast<long long>(blocks), kThreads);
-  hipLaunchKernelGGL((delta_chunk_reverse<InT, NP, KS, VEC, BOTH, ASYNC, STAGES>), dim3(static_cast<unsigned>(blocks)),
+  hipLaunchKernelGGL((delta_chunk_reverse<InT, NP, KS, BOTH, ASYNC, STAGES>), dim3(static_cast<unsigned>(blocks)),
                      dim3(kThreads), STAGES * kBytes, stream, s);
   return hipGetLastError();
 }
 
-template <typename InT, int NP, int KS, bool VEC>
+template <typename InT, int NP, int KS>
 hipError_t launch_grads(const BwdArgs& s, int64_t B, hipStream_t stream) {
   constexpr int kBytes = GradLds<InT, NP, KS>::kBytes;
   static_assert(kBytes + 4096 <= kMaxLds, "a slab exceeds LDS");
   const int64_t blocks = B * s.c.Hk * s.c.chunks;
   SSM_LOG("launch delta_chunk_grads<%d parts, %d rows>: grid %lld x %d threads", NP, 32 * KS,
           static_cast<long long>(blocks), kThreads);
-  hipLaunchKernelGGL((delta_chunk_grads<InT, NP, KS, VEC>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), kBytes,
+  hipLaunchKernelGGL((delta_chunk_grads<InT, NP, KS>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), kBytes,
                      stream, s);
   return hipGetLastError();
 }
 
 template <typename InT, int NP, int KS>
-hipError_t launch_both(const BwdArgs& s, int64_t B, bool vec, bool async, bool vec_out, hipStream_t stream) {
+hipError_t launch_both(const BwdArgs& s, int64_t B, bool direct, hipStream_t stream) {
   const int64_t heads = B * s.c.Hv;
   hipError_t e;
-  if constexpr (NP == 1) {
-    if (async)
-      e = launch_reverse<InT, NP, KS, true, true>(s, heads, stream);
-    else
-      e = vec ? launch_reverse<InT, NP, KS, true, false>(s, heads, stream)
-              : launch_reverse<InT, NP, KS, false, false>(s, heads, stream);
-  } else {
-    e = vec ? launch_reverse<InT, NP, KS, true, false>(s, heads, stream)
-            : launch_reverse<InT, NP, KS, false, false>(s, heads, stream);
-  }
-  if (e != hipSuccess) return e;
-  return vec && vec_out ? launch_grads<InT, NP, KS, true>(s, B, stream) : launch_grads<InT, NP, KS, false>(s, B, stream);
+  if constexpr (NP == 1)
+    e = direct ? launch_reverse<InT, NP, KS, true>(s, heads, stream) : launch_reverse<InT, NP, KS, false>(s, heads, stream);
+  else
+    e = launch_reverse<InT, NP, KS, false>(s, heads, stream);
+  return e == hipSuccess ? launch_grads<InT, NP, KS>(s, B, stream) : e;
 }
 
 template <typename InT, int NP>
-hipError_t launch_ks(const BwdArgs& s, int64_t B, bool vec, bool async, bool vec_out, hipStream_t stream) {
+hipError_t launch_ks(const BwdArgs& s, int64_t B, bool direct, hipStream_t stream) {
   switch (padded_ks(s.c.dk)) {
-    case 1: return launch_both<InT, NP, 1>(s, B, vec, async, vec_out, stream);
-    case 2: return launch_both<InT, NP, 2>(s, B, vec, async, vec_out, stream);
-    case 3: return launch_both<InT, NP, 3>(s, B, vec, async, vec_out, stream);
-    case 4: return launch_both<InT, NP, 4>(s, B, vec, async, vec_out, stream);
-    case 6: return launch_both<InT, NP, 6>(s, B, vec, async, vec_out, stream);
-    default: return launch_both<InT, NP, 8>(s, B, vec, async, vec_out, stream);
+    case 1: return launch_both<InT, NP, 1>(s, B, direct, stream);
+    case 2: return launch_both<InT, NP, 2>(s, B, direct, stream);
+    case 3: return launch_both<InT, NP, 3>(s, B, direct, stream);
+    case 4: return launch_both<InT, NP, 4>(s, B, direct, stream);
+    case 6: return launch_both<InT, NP, 6>(s, B, direct, stream);
+    default: return launch_both<InT, NP, 8>(s, B, direct, stream);
   }
 }
 
@@ -772,13 +767,10 @@ hipError_t launch_delta_bwd(const DeltaPlan& p, const DeltaBwdPlan& g, const Del
   s.dbr = g.dbr;
   s.dh0 = g.dh0;
   const int64_t reach = int64_t{1} << 24;  // elements a token, for 32-bit offsets inside a chunk
-  const bool vec = delta_vec(p);
-  // rows of dout (and, for straight loads, of dv) as whole 16-byte runs
-  const bool vec_out = p.dv % 8 == 0 && delta_aligned(g.dout, 16);
-  const bool async = vec && vec_out && p.in_bf16 && p.dk == 32 * padded_ks(p.dk) && p.qs < reach && p.ks < reach &&
-                     static_cast<int64_t>(p.Hv) * p.dv < reach && delta_aligned(g.dv, 16);
-  e = p.in_bf16 ? launch_ks<bf16_t, 1>(s, p.B, vec, async, vec_out, stream)
-                : launch_ks<float, 3>(s, p.B, vec, false, vec_out, stream);
+  s.vec_out = p.dv % 8 == 0 && delta_aligned(g.dout, 16);
+  const bool direct = s.c.vec && s.vec_out && p.in_bf16 && p.dk == 32 * padded_ks(p.dk) && p.qs < reach && p.ks < reach &&
+                      static_cast<int64_t>(p.Hv) * p.dv < reach && delta_aligned(g.dv, 16);
+  e = p.in_bf16 ? launch_ks<bf16_t, 1>(s, p.B, direct, stream) : launch_ks<float, 3>(s, p.B, false, stream);
   if (e != hipSuccess) return e;
   SSM_LOG("launch delta_head_sums: grid %d x %d threads", p.Hv, kThreads);
   hipLaunchKernelGGL(delta_head_sums, dim3(p.Hv), dim3(kThreads), 0, stream, s.part, g.dA, g.dbias,

@@ -213,14 +213,28 @@ __device__ __forceinline__ void stage_tokens(uint16_t* s, const T* src, int64_t 
   }
 }
 
+// All 32 KS entries, whole runs or not as `vec` says.
+template <typename T, int NP, int KS, int THREADS>
+__device__ __forceinline__ void stage_rows(uint16_t* s, const T* src, int64_t stride, int n_tokens, int d, bool vec) {
+  if (vec)
+    stage_tokens<T, NP, KS, true, THREADS>(s, src, stride, n_tokens, 0, d);
+  else
+    stage_tokens<T, NP, KS, false, THREADS>(s, src, stride, n_tokens, 0, d);
+}
+
 // A operand like TokenTile::rows, straight from global memory and split on the
 // way (where the tile does not fit in LDS). `src`: the chunk's first token.
-template <typename T, bool VEC>
-__device__ __forceinline__ Frag<3> rows_from_global(const T* src, int64_t stride, int n_tokens, int d, int mi, int ks,
-                                                    int lane) {
+template <typename T>
+__device__ __forceinline__ Frag<3> rows_from_global(const T* src, int64_t stride, int n_tokens, int d, bool vec, int mi,
+                                                    int ks, int lane) {
   const int token = mi * 16 + (lane & 15), at = ks * 32 + (lane >> 4) * 8;
   float x[8] = {};
-  if (token < n_tokens && at < d) load8<T, VEC>(src + token * stride + at, d - at, x);
+  if (token < n_tokens && at < d) {
+    if (vec)
+      load8<T, true>(src + token * stride + at, d - at, x);
+    else
+      load8<T, false>(src + token * stride + at, d - at, x);
+  }
   return split8(f32x4{x[0], x[1], x[2], x[3]}, f32x4{x[4], x[5], x[6], x[7]});
 }
 
