@@ -354,27 +354,19 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
 
 // ---- the gradients of a chunk ----
 
-// Stage a (rows, 32) slab of a float32 matrix as split operands, 8 columns a thread;
-// columns at or past `limit` (dv rounded up to 8: the walks may leave copies of other
-// columns beyond it) are 0. STATE: rows go to the tiles that state_row names.
-template <int TILES, bool STATE>
-__device__ __forceinline__ void stage_slab(uint16_t* s, const float* src, int ld, int col, int limit, f32x4* lo,
-                                           f32x4* hi, int i) {
-  const int row = i >> 2, oct = i & 3;
-  int at = row;
-  if (STATE) at = ((row >> 5) * 2 + ((row >> 2) & 1)) * 16 + ((row >> 3) & 3) * 4 + (row & 3);
-  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  *lo = *hi = zero;
-  const float* p = src + static_cast<int64_t>(row) * ld + col + oct * 8;
-  if (col + oct * 8 < limit) {
-    *lo = *reinterpret_cast<const f32x4*>(p);
-    *hi = *reinterpret_cast<const f32x4*>(p + 4);
-  }
-  const Frag<3> f = split8(*lo, *hi);
-#pragma unroll
-  for (int k = 0; k < 3; ++k)
-    *reinterpret_cast<u32x4*>(s + k * TILES * 512 + ((at >> 4) * 64 + oct * 16 + (at & 15)) * 8) = f.p[k];
+constexpr int kGradThreads = 512;
+
+// Tile row that a state row is staged at, so that column n of tile m is state_row(m, ..).
+__device__ __forceinline__ int staged_row(int row) {
+  return ((row >> 5) * 2 + ((row >> 2) & 1)) * 16 + ((row >> 3) & 3) * 4 + (row & 3);
 }
+
+// One thread's part of a 32-column slab: eight columns of one row of U, dR (the lower
+// and upper half of the threads), of dO, and of ITEMS rows of H0 and dH1.
+template <int ITEMS>
+struct SlabLoads {
+  f32x4 u[2], h[ITEMS][2], g[ITEMS][2];
+};
 
 template <int NP, int TILES>
 __device__ __forceinline__ Frag<NP> slab_rows(const uint16_t* s, int tile, int lane) {
@@ -383,31 +375,64 @@ __device__ __forceinline__ Frag<NP> slab_rows(const uint16_t* s, int tile, int l
   for (int k = 0; k < NP; ++k) f.p[k] = *reinterpret_cast<const u32x4*>(s + k * TILES * 512 + (tile * 64 + lane) * 8);
   return f;
 }
+template <int TILES>
+__device__ __forceinline__ void store_slab(uint16_t* s, int at, int oct, const f32x4 (&x)[2]) {
+  const Frag<3> f = split8(x[0], x[1]);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    *reinterpret_cast<u32x4*>(s + k * TILES * 512 + ((at >> 4) * 64 + oct * 16 + (at & 15)) * 8) = f.p[k];
+}
 
-template <typename InT, int NP, int KS>
+// LDS of a workgroup: the slab, and the staged tokens of K and Q, KSL tiles of 32
+// entries at a time, beside it for the whole call or in its place after each head.
+template <int NP, int KS>
 struct GradLds {
+  static constexpr int kLimit = kMaxLds - 6 * 1024;
   static constexpr int kdO = 0;
   static constexpr int kU = kdO + NP * 4096;
   static constexpr int kdR = kU + 3 * 4096;
   static constexpr int kH = kdR + 3 * 4096;
   static constexpr int kdH = kH + 3 * 2 * KS * 1024;
   static constexpr int kSlab = kdH + 3 * 2 * KS * 1024;
-  static constexpr int kBytes = std::max(kSlab, TokenTile<NP, KS>::kBytes);
+  static constexpr int KSL = 2 * TokenTile<NP, KS>::kBytes <= kLimit ? KS : KS / 2;
+  static constexpr int kTile = TokenTile<NP, KSL>::kBytes;
+  static constexpr bool kBeside = KSL == KS && kSlab + 2 * kTile <= kLimit;
+  static constexpr int kK = kBeside ? kSlab : 0;
+  static constexpr int kQ = kK + kTile;
+  static constexpr int kBytes = kBeside ? kSlab + 2 * kTile : std::max(kSlab, 2 * kTile);
 };
 
-// One workgroup: a chunk of one key head, its value heads in turn; wave w has the
-// tokens of tile w as rows of dQ and dK.
+// The lane's column of the four tokens 16 w + g4 .. of a staged tile, from the operand
+// that holds the tokens 32 (w / 2) ..
+template <int NP>
+__device__ __forceinline__ f32x4 column_values(const Frag<NP>& f, int w) {
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = NP - 1; i >= 0; --i) {
+    const uint32_t lo = (w & 1) ? f.p[i].z : f.p[i].x, hi = (w & 1) ? f.p[i].w : f.p[i].y;
+    v += f32x4{__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi << 16),
+               __uint_as_float(hi & 0xFFFF0000u)};
+  }
+  return v;
+}
+
+// One workgroup: a chunk of one key head, its value heads in turn. Eight waves: wave
+// w + 4 * half has the tokens of tile w as rows of dQ and dK and half of their columns.
+// The sums over dv go in slabs of 32 columns, the next one's loads under way while one
+// is multiplied.
 template <typename InT, int NP, int KS>
-__global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
-  using Tile = TokenTile<NP, KS>;
-  using Lds = GradLds<InT, NP, KS>;
-  constexpr int DKT = 2 * KS, ROWS = 32 * KS;
+__global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs s) {
+  using Lds = GradLds<NP, KS>;
+  constexpr int DKT = 2 * KS, ROWS = 32 * KS, MT = KS;  // MT: a wave's state tiles
+  constexpr int KSL = Lds::KSL, ITEMS = (ROWS * 4 + kGradThreads - 1) / kGradThreads;
+  using Tile = TokenTile<NP, KSL>;
   extern __shared__ __align__(16) char staged[];
   __shared__ ChunkGates gates;
-  __shared__ float scalars[kGateFloats];
-  __shared__ float own_sum[64], end_sum[64], beta_sum[64], diag_dP[64], waves_sum[kWaves];
+  __shared__ __align__(16) float scalars[kGateFloats];
+  __shared__ __align__(16) float own_sum[2][64], end_sum[2][64], beta_sum[64], diag_dP[64], waves_sum[8];
   const ChunkArgs& a = s.c;
-  const int lane = threadIdx.x % 64, w = wave_index(), g4 = (lane >> 4) * 4, col = lane & 15;
+  const int lane = threadIdx.x % 64, wave = wave_index(), w = wave & 3, half = wave >> 2;
+  const int g4 = (lane >> 4) * 4, col = lane & 15;
   const int chunk = blockIdx.x % a.chunks, bhk = blockIdx.x / a.chunks;
   const int b = bhk / a.Hk, hk = bhk - b * a.Hk;
   const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(chunk) * kChunk;
@@ -419,54 +444,82 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
   uint16_t* sdR = reinterpret_cast<uint16_t*>(staged + Lds::kdR);
   uint16_t* sH = reinterpret_cast<uint16_t*>(staged + Lds::kH);
   uint16_t* sdH = reinterpret_cast<uint16_t*>(staged + Lds::kdH);
-  uint16_t* stok = reinterpret_cast<uint16_t*>(staged);
+  uint16_t* sk = reinterpret_cast<uint16_t*>(staged + Lds::kK);
+  uint16_t* sq = reinterpret_cast<uint16_t*>(staged + Lds::kQ);
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  // columns at or past dv (rounded up to 8) may hold copies of others: read as 0
   const int limit = (a.dv + 7) / 8 * 8;
+  const auto stage_qk = [&](int d0) {
+    stage_rows<InT, NP, KSL, kGradThreads>(sk, k + d0, a.ks, n_tokens, a.dk - d0, a.vec);
+    stage_rows<InT, NP, KSL, kGradThreads>(sq, q + d0, a.qs, n_tokens, a.dk - d0, a.vec);
+  };
+  if constexpr (Lds::kBeside) stage_qk(0);
 
-  f32x4 dq_sum[DKT], dk_sum[DKT];
+  f32x4 dq_sum[MT], dk_sum[MT];
 #pragma unroll
-  for (int m = 0; m < DKT; ++m) dq_sum[m] = dk_sum[m] = zero;
+  for (int m = 0; m < MT; ++m) dq_sum[m] = dk_sum[m] = zero;
 
   for (int gi = 0; gi < a.group; ++gi) {
     const int h = hk * a.group + gi, bh = b * a.Hv + h;
     const int64_t record = static_cast<int64_t>(bh) * a.chunks + chunk;
-    const float* U = s.U + record * kChunk * s.cols;
-    const float* dR = s.dR + record * kChunk * s.cols;
     const float* H0 = s.states + record * ROWS * s.cols;
     const float* dH1 = s.dstates + record * ROWS * s.cols;
     const InT* dout = static_cast<const InT*>(s.dout) + (t0 * a.Hv + h) * a.dv;
-    __syncthreads();  // the previous head's scalars are used
-    if (w == 0) chunk_gates<InT>(a, b, h, chunk, scalars, lane, &gates);
-
-    f32x4 E1[DKT], E2[DKT], E3[DKT];  // dO H0^T, dR H0^T, U dH1^T: rows of tile w, columns of state tile m
+    // this thread's rows and columns of a slab
+    const int oct = threadIdx.x & 3, row = (threadIdx.x >> 2) & 63;
+    const float* uv = (threadIdx.x < 256 ? s.U : s.dR) + record * kChunk * s.cols + row * s.cols;
+    const auto fetch = [&](SlabLoads<ITEMS>& x, int d0) {
+      const int c = d0 + oct * 8;
+      const bool in = c < limit;
+      const int at = in ? c : 0;
 #pragma unroll
-    for (int m = 0; m < DKT; ++m) E1[m] = E2[m] = E3[m] = zero;
+      for (int i = 0; i < 2; ++i) x.u[i] = in ? *reinterpret_cast<const f32x4*>(uv + at + 4 * i) : zero;
+#pragma unroll
+      for (int n = 0; n < ITEMS; ++n) {
+        const int r = min(static_cast<int>(threadIdx.x >> 2) + n * (kGradThreads / 4), ROWS - 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          x.h[n][i] = in ? *reinterpret_cast<const f32x4*>(H0 + static_cast<int64_t>(r) * s.cols + at + 4 * i) : zero;
+          x.g[n][i] = in ? *reinterpret_cast<const f32x4*>(dH1 + static_cast<int64_t>(r) * s.cols + at + 4 * i) : zero;
+        }
+      }
+    };
+    SlabLoads<ITEMS> loads;
+    fetch(loads, 0);
+    __syncthreads();  // the previous head's scalars and tiles are used
+    if (wave == 0) chunk_gates<InT>(a, b, h, chunk, scalars, lane, &gates);
+
+    f32x4 E1[MT], E2[MT], E3[MT];  // dO H0^T, dR H0^T, U dH1^T: rows of tile w, columns of the wave's state tiles
+#pragma unroll
+    for (int m = 0; m < MT; ++m) E1[m] = E2[m] = E3[m] = zero;
     // U dO^T and U dR^T (rows of tile j <= w, columns w); dO U^T and dR U^T (rows of tile i >= w, columns w)
     f32x4 Pc[4] = {zero, zero, zero, zero}, Sc[4] = {zero, zero, zero, zero};
     f32x4 Pr[4] = {zero, zero, zero, zero}, Sr[4] = {zero, zero, zero, zero};
     float hh = 0.0f;  // the thread's part of <dH1, H0>
     for (int d0 = 0; d0 < a.dv; d0 += 32) {
-      __syncthreads();
-      stage_rows<InT, NP, 1, kThreads>(sdO, dout + d0, static_cast<int64_t>(a.Hv) * a.dv, n_tokens, a.dv - d0, s.vec_out);
-      {
-        f32x4 x, y;
-        stage_slab<4, false>(sU, U, s.cols, d0, limit, &x, &y, threadIdx.x);
-        stage_slab<4, false>(sdR, dR, s.cols, d0, limit, &x, &y, threadIdx.x);
-      }
+      if (d0 > 0) __syncthreads();  // the last slab is read
+      stage_rows<InT, NP, 1, kGradThreads>(sdO, dout + d0, static_cast<int64_t>(a.Hv) * a.dv, n_tokens, a.dv - d0,
+                                           s.vec_out);
+      store_slab<4>(threadIdx.x < 256 ? sU : sdR, row, oct, loads.u);
 #pragma unroll
-      for (int i = threadIdx.x; i < ROWS * 4; i += kThreads) {
-        f32x4 x, y, dx, dy;
-        stage_slab<DKT, true>(sH, H0, s.cols, d0, limit, &x, &y, i);
-        stage_slab<DKT, true>(sdH, dH1, s.cols, d0, limit, &dx, &dy, i);
+      for (int n = 0; n < ITEMS; ++n) {
+        const int r = static_cast<int>(threadIdx.x >> 2) + n * (kGradThreads / 4);
+        if (r < ROWS) {
+          store_slab<DKT>(sH, staged_row(r), oct, loads.h[n]);
+          store_slab<DKT>(sdH, staged_row(r), oct, loads.g[n]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) hh = __builtin_fmaf(x[r], dx[r], __builtin_fmaf(y[r], dy[r], hh));
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) hh = __builtin_fmaf(loads.h[n][i][j], loads.g[n][i][j], hh);
+        }
       }
+      if (d0 + 32 < a.dv) fetch(loads, d0 + 32);
       __syncthreads();
       const Frag<NP> dOw = slab_rows<NP, 4>(sdO, w, lane);
       const Frag<3> Uw = slab_rows<3, 4>(sU, w, lane), dRw = slab_rows<3, 4>(sdR, w, lane);
 #pragma unroll
-      for (int m = 0; m < DKT; ++m) {
-        const Frag<3> hb = slab_rows<3, DKT>(sH, m, lane), gb = slab_rows<3, DKT>(sdH, m, lane);
+      for (int m = 0; m < MT; ++m) {
+        const Frag<3> hb = slab_rows<3, DKT>(sH, half * MT + m, lane), gb = slab_rows<3, DKT>(sdH, half * MT + m, lane);
         E1[m] = mma(dOw, hb, E1[m]);
         E2[m] = mma(dRw, hb, E2[m]);
         E3[m] = mma(Uw, gb, E3[m]);
@@ -486,15 +539,15 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
     }
 
     // d beta comes from the diagonal of dR U^T, and dP's is set aside; then the decays and masks.
+    const ColDecay cw = col_decay(gates, w * 16 + col);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (j == w && (col >> 2) == (lane >> 4)) {
+      if (j == w && half == 0 && (col >> 2) == (lane >> 4)) {
         const int r = col & 3;
         beta_sum[w * 16 + col] = r == 0 ? Sc[j].x : r == 1 ? Sc[j].y : r == 2 ? Sc[j].z : Sc[j].w;
         diag_dP[w * 16 + col] = a.scale * (r == 0 ? Pc[j].x : r == 1 ? Pc[j].y : r == 2 ? Pc[j].z : Pc[j].w);
       }
       const RowDecay rows = row_decay(gates, j * 16 + g4);
-      const ColDecay cw = col_decay(gates, w * 16 + col);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int x = j * 16 + g4 + r, y = w * 16 + col;
@@ -514,56 +567,50 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
     const Frag<3> as[2] = {split8(Sc[0], Sc[1]), split8(Sc[2], Sc[3])};
     const Frag<3> bp[2] = {split8(Pr[0], Pr[1]), split8(Pr[2], Pr[3])};
     const Frag<3> bs[2] = {split8(Sr[0], Sr[1]), split8(Sr[2], Sr[3])};
-    __syncthreads();  // the slabs are read
-    stage_rows<InT, NP, KS, kThreads>(stok, k, a.ks, n_tokens, a.dk, a.vec);
-    __syncthreads();
-#pragma unroll
-    for (int m = 0; m < DKT; ++m) {
-      const int d = state_row(m, col & 12, col & 3);
-      f32x4 kv, qv;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int token = w * 16 + g4 + r;
-        const bool there = token < n_tokens && d < a.dk;
-        kv[r] = there ? load_elem(k + d, token * a.ks) : 0.0f;
-        qv[r] = there ? load_elem(q + d, token * a.qs) : 0.0f;
-      }
+    __syncthreads();  // the slab is read, the diagonals are set
+    const f32x4 dp = *reinterpret_cast<const f32x4*>(&diag_dP[w * 16 + g4]);
+    const auto finish = [&](int m, int local) {  // the wave's tile m, staged as tile `local`
       E1[m] *= a.scale * e0;
       E2[m] *= -be * e0;
       E3[m] *= eC;
-      ku += kv * E3[m];
-      f32x4 x = zero;
+      f32x4 x = zero, y = zero, kv = zero, qv = zero;
 #pragma unroll
       for (int ts = 0; ts < 2; ++ts) {
-        const Frag<NP> kc = Tile::columns(stok, m, ts, lane);
+        const Frag<NP> kc = Tile::columns(sk, local, ts, lane), qc = Tile::columns(sq, local, ts, lane);
+        if (ts == w / 2) {
+          kv = column_values(kc, w);
+          qv = column_values(qc, w);
+        }
         if (ts <= w / 2) {
           E1[m] = mma(ap[ts], kc, E1[m]);
           E2[m] = mma(as[ts], kc, E2[m]);
         }
-        if (ts >= w / 2) x = mma(bs[ts], kc, x);
+        if (ts >= w / 2) {
+          x = mma(bs[ts], kc, x);
+          y = mma(bp[ts], qc, y);
+        }
       }
-      own += qv * E1[m] + kv * (E2[m] - x);
-      const f32x4 dp = *reinterpret_cast<const f32x4*>(&diag_dP[w * 16 + g4]);
+      ku += kv * E3[m];
+      own += qv * E1[m] + kv * ((E2[m] - x) - y);
       dq_sum[m] += E1[m] + dp * kv;
-      dk_sum[m] += (E2[m] + E3[m]) + (x + dp * qv);
-    }
-    __syncthreads();
-    stage_rows<InT, NP, KS, kThreads>(stok, q, a.qs, n_tokens, a.dk, a.vec);
-    __syncthreads();
-#pragma unroll
-    for (int m = 0; m < DKT; ++m) {
-      const int d = state_row(m, col & 12, col & 3);
-      f32x4 x = zero, kv;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int token = w * 16 + g4 + r;
-        kv[r] = token < n_tokens && d < a.dk ? load_elem(k + d, token * a.ks) : 0.0f;
+      dk_sum[m] += ((E2[m] + E3[m]) + x) + (y + dp * qv);
+    };
+    if constexpr (KSL == KS) {
+      if constexpr (!Lds::kBeside) {
+        stage_qk(0);
+        __syncthreads();
       }
 #pragma unroll
-      for (int ts = 0; ts < 2; ++ts)
-        if (ts >= w / 2) x = mma(bp[ts], Tile::columns(stok, m, ts, lane), x);
-      dk_sum[m] += x;
-      own -= kv * x;
+      for (int m = 0; m < MT; ++m) finish(m, half * MT + m);
+    } else {
+      for (int pass = 0; pass < 2; ++pass) {  // the entries of each half's tiles in turn
+        if (pass > 0) __syncthreads();
+        stage_qk(pass * 32 * KSL);
+        __syncthreads();
+        if (pass == half)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) finish(m, m);
+      }
     }
     // sums over the 16 columns' lanes, and over the workgroup
 #pragma unroll
@@ -572,16 +619,18 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
       ku[r] = lanes_sum<16>(ku[r]);
     }
     if (col == 0) {
-      *reinterpret_cast<f32x4*>(&own_sum[w * 16 + g4]) = own;
-      *reinterpret_cast<f32x4*>(&end_sum[w * 16 + g4]) = ku;
+      *reinterpret_cast<f32x4*>(&own_sum[half][w * 16 + g4]) = own;
+      *reinterpret_cast<f32x4*>(&end_sum[half][w * 16 + g4]) = ku;
     }
     const float total = lanes_sum<64>(hh);
-    if (lane == 0) waves_sum[w] = total;
+    if (lane == 0) waves_sum[wave] = total;
     __syncthreads();
-    if (w == 0) {
+    if (wave == 0) {
       // a lane per token, sums within its document: from it on, and (eC is 0 before the last document) up to it
       const int seg = gates.seg[lane];
-      double from = own_sum[lane], upto = end_sum[lane];
+      const double own_all = static_cast<double>(own_sum[0][lane]) + own_sum[1][lane];
+      const double end_all = static_cast<double>(end_sum[0][lane]) + end_sum[1][lane];
+      double from = own_all, upto = end_all;
 #pragma unroll
       for (int off = 1; off < 64; off *= 2) {
         const double after = __shfl_down(from, off), before = __shfl_up(upto, off);
@@ -589,8 +638,10 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
         if (lane + off < 64 && seg_after == seg) from += after;
         if (lane >= off && seg_up == seg) upto += before;
       }
-      const double hh_all = (static_cast<double>(waves_sum[0]) + waves_sum[1]) + (static_cast<double>(waves_sum[2]) + waves_sum[3]);
-      const double sum = from + (upto - end_sum[lane]) + scalars[kAC] * hh_all;
+      double hh_all = 0.0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hh_all += waves_sum[i];
+      const double sum = from + (upto - end_all) + scalars[kAC] * hh_all;
       const int seg_before = __shfl_up(seg, 1);
       const bool cut = lane == 0 ? seg > 0 : seg != seg_before;
       const bool there = lane < n_tokens;
@@ -620,19 +671,19 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_grads(const BwdArgs s) {
 
   const int64_t token_k = static_cast<int64_t>(a.Hk) * a.dk;
 #pragma unroll
-  for (int m = 0; m < DKT; ++m) {
-    const int d = state_row(m, col & 12, col & 3);
+  for (int m = 0; m < MT; ++m) {
+    const int d = state_row(half * MT + m, col & 12, col & 3);
+    if (d >= a.dk) continue;
+    const int64_t at = (t0 + w * 16 + g4) * token_k + static_cast<int64_t>(hk) * a.dk + d;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int token = w * 16 + g4 + r;
-      if (token >= n_tokens || d >= a.dk) continue;
-      const int64_t at = (t0 + token) * token_k + static_cast<int64_t>(hk) * a.dk + d;
+      if (w * 16 + g4 + r >= n_tokens) continue;
       if (s.grad_bf16) {
-        store_elem(static_cast<bf16_t*>(s.dq), at, dq_sum[m][r]);
-        store_elem(static_cast<bf16_t*>(s.dk), at, dk_sum[m][r]);
+        store_elem(static_cast<bf16_t*>(s.dq) + r * token_k, at, dq_sum[m][r]);
+        store_elem(static_cast<bf16_t*>(s.dk) + r * token_k, at, dk_sum[m][r]);
       } else {
-        store_elem(static_cast<float*>(s.dq), at, dq_sum[m][r]);
-        store_elem(static_cast<float*>(s.dk), at, dk_sum[m][r]);
+        store_elem(static_cast<float*>(s.dq) + r * token_k, at, dq_sum[m][r]);
+        store_elem(static_cast<float*>(s.dk) + r * token_k, at, dk_sum[m][r]);
       }
     }
   }
@@ -681,12 +732,12 @@ hipError_t launch_reverse(const BwdArgs& s, int64_t heads, hipStream_t stream) {
 
 template <typename InT, int NP, int KS>
 hipError_t launch_grads(const BwdArgs& s, int64_t B, hipStream_t stream) {
-  constexpr int kBytes = GradLds<InT, NP, KS>::kBytes;
-  static_assert(kBytes + 4096 <= kMaxLds, "a slab exceeds LDS");
+  constexpr int kBytes = GradLds<NP, KS>::kBytes;
+  static_assert(kBytes <= GradLds<NP, KS>::kLimit, "a slab exceeds LDS");
   const int64_t blocks = B * s.c.Hk * s.c.chunks;
   SSM_LOG("launch delta_chunk_grads<%d parts, %d rows>: grid %lld x %d threads", NP, 32 * KS,
-          static_cast<long long>(blocks), kThreads);
-  hipLaunchKernelGGL((delta_chunk_grads<InT, NP, KS>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), kBytes,
+          static_cast<long long>(blocks), kGradThreads);
+  hipLaunchKernelGGL((delta_chunk_grads<InT, NP, KS>), dim3(static_cast<unsigned>(blocks)), dim3(kGradThreads), kBytes,
                      stream, s);
   return hipGetLastError();
 }
