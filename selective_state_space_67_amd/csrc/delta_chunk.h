@@ -13,7 +13,7 @@ namespace ssm {
 constexpr int kRecT = 0, kRecP = kTriBytes, kRecGates = 2 * kTriBytes;
 constexpr int kRecBytes = kRecGates + kGateFloats * 4;
 constexpr int kRecTt = kTriBytes, kRecPt = 2 * kTriBytes, kRecGatesBwd = 3 * kTriBytes;
-constexpr int kRecBytesBwd = kRecGatesBwd + kGateFloats * 4;
+constexpr int kRecBytesBwd = kRecGatesBwd + kGateFloatsBwd * 4;
 
 struct ChunkArgs {
   int64_t L;
@@ -33,26 +33,21 @@ struct ChunkArgs {
   char* records;  // (bh, chunk)
 };
 
-struct alignas(16) ChunkGates {
-  float hi[64], lo[64];  // G in log2 units, as a sum of two floats
-  float beta[64];
-  int seg[64];           // documents started in the chunk up to the token
-  float delta[64];       // softplus(dt_raw + dt_bias)
-};
-
-// One wave, a lane per token; the chunk's scalars (kE0 ..) go to `out`. The sums are taken in double and kept in two floats,
-// so that differences of them keep a small decay's precision next to large ones.
+// The chunk's scalars by one wave, a lane per token, into `out` (LDS). The sums are taken
+// in double and kept in two floats, so that differences of them keep a small decay's
+// precision next to large ones.
 template <typename InT>
-__device__ __forceinline__ void chunk_gates(const ChunkArgs& a, int b, int h, int chunk, float* out, int lane,
-                                            ChunkGates* s) {
+__device__ __forceinline__ void chunk_gates(const ChunkArgs& a, int b, int h, int chunk, float* out, int lane) {
   const int64_t t = static_cast<int64_t>(chunk) * kChunk + lane;
   const bool valid = t < a.L;
   double g = 0.0;
-  float beta = 0.0f, delta = 0.0f;
+  float beta = 0.0f, delta = 0.0f, slope = 0.0f;
   bool start = false;
   if (valid) {
     const int64_t i = (static_cast<int64_t>(b) * a.L + t) * a.Hv + h;
-    delta = softplus_f32(load_elem(static_cast<const InT*>(a.dt), i) + (a.dt_bias ? a.dt_bias[h] : 0.0f));
+    const float raw = load_elem(static_cast<const InT*>(a.dt), i) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
+    delta = softplus_f32(raw);
+    slope = fast_rcp(1.0f + fast_exp2(-raw * kLog2e));
     beta = a.beta_scale * fast_rcp(1.0f + fast_exp2(-load_elem(static_cast<const InT*>(a.br), i) * kLog2e));
     start = a.reset && a.reset[static_cast<int64_t>(b) * a.L + t];
     // a step's decay below 2^-16384 is 0 in float32 whatever its exponent
@@ -71,40 +66,31 @@ __device__ __forceinline__ void chunk_gates(const ChunkArgs& a, int b, int h, in
     }
   }
   const double last = __shfl(g, 63);
-  const int seg_last = __popcll(starts);
   const float hi = static_cast<float>(g);
-  s->hi[lane] = hi;
-  s->lo[lane] = static_cast<float>(g - hi);
-  s->beta[lane] = beta;
-  s->seg[lane] = seg;
-  s->delta[lane] = delta;
-  out[kE0 + lane] = seg == 0 ? fast_exp2(static_cast<float>(g)) : 0.0f;
-  out[kEC + lane] = seg == seg_last ? fast_exp2(static_cast<float>(last - g)) : 0.0f;
+  out[kE0 + lane] = seg == 0 ? fast_exp2(hi) : 0.0f;
+  out[kEC + lane] = seg == __popcll(starts) ? fast_exp2(static_cast<float>(last - g)) : 0.0f;
   out[kBeta + lane] = beta;
-  if (lane == 63) out[kAC] = seg == 0 ? fast_exp2(static_cast<float>(g)) : 0.0f;
+  out[kSlope + lane] = slope;
+  out[kSumHi + lane] = hi;
+  out[kSumLo + lane] = static_cast<float>(g - hi);
+  out[kSeg + lane] = static_cast<float>(seg);
+  out[kDelta + lane] = delta;
 }
 
 // A lane's share of the sums for elements of 16 x 16 tiles in the D layout: of the four
 // tokens that its rows are, or of the one that its column is.
 struct RowDecay {
-  f32x4 hi, lo, beta;
-  int seg[4];
+  f32x4 hi, lo, beta, seg;
 };
 struct ColDecay {
-  float hi, lo, beta;
-  int seg;
+  float hi, lo, beta, seg;
 };
-__device__ __forceinline__ RowDecay row_decay(const ChunkGates& s, int first) {
-  RowDecay d;
-  d.hi = *reinterpret_cast<const f32x4*>(&s.hi[first]);
-  d.lo = *reinterpret_cast<const f32x4*>(&s.lo[first]);
-  d.beta = *reinterpret_cast<const f32x4*>(&s.beta[first]);
-#pragma unroll
-  for (int r = 0; r < 4; ++r) d.seg[r] = s.seg[first + r];
-  return d;
+__device__ __forceinline__ RowDecay row_decay(const float* s, int first) {
+  return RowDecay{*reinterpret_cast<const f32x4*>(s + kSumHi + first), *reinterpret_cast<const f32x4*>(s + kSumLo + first),
+                  *reinterpret_cast<const f32x4*>(s + kBeta + first), *reinterpret_cast<const f32x4*>(s + kSeg + first)};
 }
-__device__ __forceinline__ ColDecay col_decay(const ChunkGates& s, int token) {
-  return ColDecay{s.hi[token], s.lo[token], s.beta[token], s.seg[token]};
+__device__ __forceinline__ ColDecay col_decay(const float* s, int token) {
+  return ColDecay{s[kSumHi + token], s[kSumLo + token], s[kBeta + token], s[kSeg + token]};
 }
 // exp(G_row - G_col), for a row at or after the column, or the reverse; 0 across documents.
 __device__ __forceinline__ float decay_down(const RowDecay& a, int r, const ColDecay& b) {

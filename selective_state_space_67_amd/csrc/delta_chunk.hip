@@ -51,7 +51,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chunk_prepare(const ChunkAr
   extern __shared__ __align__(16) uint16_t staged_tokens[];
   uint16_t* sk = staged_tokens;
   uint16_t* sq = staged_tokens + NP * Tile::kPart;
-  __shared__ ChunkGates gates;
+  __shared__ __align__(16) float gates[kGateFloatsBwd];
   __shared__ float diag[4][16][20];  // A_ii, then T_ii; rows of 16 padded to 20
   const int lane = threadIdx.x % 64, g4 = (lane >> 4) * 4, col = lane & 15;
   const int w = wave_index();
@@ -68,8 +68,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chunk_prepare(const ChunkAr
     stage_tokens_async<KS>(sk, k, a.ks, n_tokens, lane, w);
     stage_tokens_async<KS>(sq, q, a.qs, n_tokens, lane, w);
   }
-  if (w == 0)
-    chunk_gates<InT>(a, b, h, chunk, reinterpret_cast<float*>(rec + (BWD ? kRecGatesBwd : kRecGates)), lane, &gates);
+  if (w == 0) chunk_gates<InT>(a, b, h, chunk, gates, lane);
 
   // S[k][j]: rows k, columns j (j < k <= w, and the diagonal k = j = w); with BWD
   // also R[k][i]: rows k, columns i (w <= k < i). P[j]: rows j, columns w;
@@ -112,6 +111,11 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chunk_prepare(const ChunkAr
     }
   }
 
+  {  // the record's scalars
+    float* to = reinterpret_cast<float*>(rec + (BWD ? kRecGatesBwd : kRecGates));
+    to[threadIdx.x] = gates[threadIdx.x];
+    if (BWD) to[kThreads + threadIdx.x] = gates[kThreads + threadIdx.x];
+  }
   // Decays and betas.
   {
     RowDecay rows[4];

@@ -363,8 +363,9 @@ __device__ __forceinline__ int staged_row(int row) {
 
 // One thread's part of a 32-column slab: eight columns of one row of U, dR (the lower
 // and upper half of the threads), of dO, and of ITEMS rows of H0 and dH1.
-template <int ITEMS>
+template <int NP, int ITEMS>
 struct SlabLoads {
+  u32x4 o[NP == 1 ? 1 : 2];  // of dO, as they lie in memory (the lower half of the threads)
   f32x4 u[2], h[ITEMS][2], g[ITEMS][2];
 };
 
@@ -393,7 +394,7 @@ struct GradLds {
   static constexpr int kdR = kU + 3 * 4096;
   static constexpr int kH = kdR + 3 * 4096;
   static constexpr int kdH = kH + 3 * 2 * KS * 1024;
-  static constexpr int kSlab = kdH + 3 * 2 * KS * 1024;
+  static constexpr int kSlab = std::max(kdH + 3 * 2 * KS * 1024, 64 * 1024);  // at least the exchange of P and S
   static constexpr int KSL = 2 * TokenTile<NP, KS>::kBytes <= kLimit ? KS : KS / 2;
   static constexpr int kTile = TokenTile<NP, KSL>::kBytes;
   static constexpr bool kBeside = KSL == KS && kSlab + 2 * kTile <= kLimit;
@@ -416,6 +417,9 @@ __device__ __forceinline__ f32x4 column_values(const Frag<NP>& f, int w) {
   return v;
 }
 
+// Keeps the compiler from reading the operands of many tiles ahead, which spills.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
 // One workgroup: a chunk of one key head, its value heads in turn. Eight waves: wave
 // w + 4 * half has the tokens of tile w as rows of dQ and dK and half of their columns.
 // The sums over dv go in slabs of 32 columns, the next one's loads under way while one
@@ -427,8 +431,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
   constexpr int KSL = Lds::KSL, ITEMS = (ROWS * 4 + kGradThreads - 1) / kGradThreads;
   using Tile = TokenTile<NP, KSL>;
   extern __shared__ __align__(16) char staged[];
-  __shared__ ChunkGates gates;
-  __shared__ __align__(16) float scalars[kGateFloats];
+  __shared__ __align__(16) float scalars[kGateFloatsBwd];
   __shared__ __align__(16) float own_sum[2][64], end_sum[2][64], beta_sum[64], diag_dP[64], waves_sum[8];
   const ChunkArgs& a = s.c;
   const int lane = threadIdx.x % 64, wave = wave_index(), w = wave & 3, half = wave >> 2;
@@ -449,6 +452,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   // columns at or past dv (rounded up to 8) may hold copies of others: read as 0
   const int limit = (a.dv + 7) / 8 * 8;
+  const int64_t token_v = static_cast<int64_t>(a.Hv) * a.dv;
   const auto stage_qk = [&](int d0) {
     stage_rows<InT, NP, KSL, kGradThreads>(sk, k + d0, a.ks, n_tokens, a.dk - d0, a.vec);
     stage_rows<InT, NP, KSL, kGradThreads>(sq, q + d0, a.qs, n_tokens, a.dk - d0, a.vec);
@@ -468,7 +472,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
     // this thread's rows and columns of a slab
     const int oct = threadIdx.x & 3, row = (threadIdx.x >> 2) & 63;
     const float* uv = (threadIdx.x < 256 ? s.U : s.dR) + record * kChunk * s.cols + row * s.cols;
-    const auto fetch = [&](SlabLoads<ITEMS>& x, int d0) {
+    const auto fetch = [&](SlabLoads<NP, ITEMS>& x, int d0) {
       const int c = d0 + oct * 8;
       const bool in = c < limit;
       const int at = in ? c : 0;
@@ -483,23 +487,48 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
           x.g[n][i] = in ? *reinterpret_cast<const f32x4*>(dH1 + static_cast<int64_t>(r) * s.cols + at + 4 * i) : zero;
         }
       }
+      if (threadIdx.x < 256) {
+        const InT* p = dout + row * token_v + c;
+        const int left = row < n_tokens ? a.dv - c : 0;
+        const u32x4 none = {0, 0, 0, 0};
+        if (s.vec_out) {
+#pragma unroll
+          for (int i = 0; i < (NP == 1 ? 1 : 2); ++i) x.o[i] = left > 0 ? reinterpret_cast<const u32x4*>(p)[i] : none;
+        } else if constexpr (NP == 1) {
+          uint32_t e[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = j < left ? p[j].bits : 0u;
+          x.o[0] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x.o[j / 4][j % 4] = j < left ? __float_as_uint(p[j]) : 0u;
+        }
+      }
     };
-    SlabLoads<ITEMS> loads;
+    SlabLoads<NP, ITEMS> loads;
     fetch(loads, 0);
     __syncthreads();  // the previous head's scalars and tiles are used
-    if (wave == 0) chunk_gates<InT>(a, b, h, chunk, scalars, lane, &gates);
+    scalars[threadIdx.x] = reinterpret_cast<const float*>(a.records + record * kRecBytesBwd + kRecGatesBwd)[threadIdx.x];
 
     f32x4 E1[MT], E2[MT], E3[MT];  // dO H0^T, dR H0^T, U dH1^T: rows of tile w, columns of the wave's state tiles
 #pragma unroll
     for (int m = 0; m < MT; ++m) E1[m] = E2[m] = E3[m] = zero;
-    // U dO^T and U dR^T (rows of tile j <= w, columns w); dO U^T and dR U^T (rows of tile i >= w, columns w)
-    f32x4 Pc[4] = {zero, zero, zero, zero}, Sc[4] = {zero, zero, zero, zero};
-    f32x4 Pr[4] = {zero, zero, zero, zero}, Sr[4] = {zero, zero, zero, zero};
+    // the lower waves: U dO^T and U dR^T (rows of tile j <= w, columns w); the upper ones: dO U^T and
+    // dR U^T (rows of tile j >= w, columns w)
+    f32x4 P[4] = {zero, zero, zero, zero}, S[4] = {zero, zero, zero, zero};
     float hh = 0.0f;  // the thread's part of <dH1, H0>
     for (int d0 = 0; d0 < a.dv; d0 += 32) {
       if (d0 > 0) __syncthreads();  // the last slab is read
-      stage_rows<InT, NP, 1, kGradThreads>(sdO, dout + d0, static_cast<int64_t>(a.Hv) * a.dv, n_tokens, a.dv - d0,
-                                           s.vec_out);
+      if (threadIdx.x < 256) {
+        uint16_t* to = sdO + ((row >> 4) * 64 + oct * 16 + (row & 15)) * 8;
+        if constexpr (NP == 1) {
+          *reinterpret_cast<u32x4*>(to) = loads.o[0];
+        } else {
+          const Frag<3> f = split8(__builtin_bit_cast(f32x4, loads.o[0]), __builtin_bit_cast(f32x4, loads.o[1]));
+#pragma unroll
+          for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(to + i * 2048) = f.p[i];
+        }
+      }
       store_slab<4>(threadIdx.x < 256 ? sU : sdR, row, oct, loads.u);
 #pragma unroll
       for (int n = 0; n < ITEMS; ++n) {
@@ -521,41 +550,41 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
       for (int m = 0; m < MT; ++m) {
         const Frag<3> hb = slab_rows<3, DKT>(sH, half * MT + m, lane), gb = slab_rows<3, DKT>(sdH, half * MT + m, lane);
         E1[m] = mma(dOw, hb, E1[m]);
-        E2[m] = mma(dRw, hb, E2[m]);
-        E3[m] = mma(Uw, gb, E3[m]);
+        mma_pair(dRw, hb, E2[m], Uw, gb, E3[m]);
+        keep_order();
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (j <= w) {
+        if (half == 0 && j <= w) {
           const Frag<3> Uj = slab_rows<3, 4>(sU, j, lane);
-          Pc[j] = mma(Uj, dOw, Pc[j]);
-          Sc[j] = mma(Uj, dRw, Sc[j]);
+          P[j] = mma(Uj, dOw, P[j]);
+          S[j] = mma(Uj, dRw, S[j]);
         }
-        if (j >= w) {
-          Pr[j] = mma(slab_rows<NP, 4>(sdO, j, lane), Uw, Pr[j]);
-          Sr[j] = mma(slab_rows<3, 4>(sdR, j, lane), Uw, Sr[j]);
+        if (half == 1 && j >= w) {
+          P[j] = mma(slab_rows<NP, 4>(sdO, j, lane), Uw, P[j]);
+          S[j] = mma(slab_rows<3, 4>(sdR, j, lane), Uw, S[j]);
         }
+        keep_order();
       }
     }
 
     // d beta comes from the diagonal of dR U^T, and dP's is set aside; then the decays and masks.
-    const ColDecay cw = col_decay(gates, w * 16 + col);
+    const ColDecay cw = col_decay(scalars, w * 16 + col);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j == w && half == 0 && (col >> 2) == (lane >> 4)) {
         const int r = col & 3;
-        beta_sum[w * 16 + col] = r == 0 ? Sc[j].x : r == 1 ? Sc[j].y : r == 2 ? Sc[j].z : Sc[j].w;
-        diag_dP[w * 16 + col] = a.scale * (r == 0 ? Pc[j].x : r == 1 ? Pc[j].y : r == 2 ? Pc[j].z : Pc[j].w);
+        beta_sum[w * 16 + col] = r == 0 ? S[j].x : r == 1 ? S[j].y : r == 2 ? S[j].z : S[j].w;
+        diag_dP[w * 16 + col] = a.scale * (r == 0 ? P[j].x : r == 1 ? P[j].y : r == 2 ? P[j].z : P[j].w);
       }
-      const RowDecay rows = row_decay(gates, j * 16 + g4);
+      const RowDecay rows = row_decay(scalars, j * 16 + g4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int x = j * 16 + g4 + r, y = w * 16 + col;
-        const float up = x < y ? decay_up(rows, r, cw) : 0.0f, down = x > y ? decay_down(rows, r, cw) : 0.0f;
-        Pc[j][r] *= a.scale * up;
-        Sc[j][r] *= -cw.beta * up;
-        Pr[j][r] *= a.scale * down;
-        Sr[j][r] *= -rows.beta[r] * down;
+        // half 0: row token x before column token y; half 1: after it
+        const float d = half == 0 ? (x < y ? decay_up(rows, r, cw) : 0.0f) : (x > y ? decay_down(rows, r, cw) : 0.0f);
+        P[j][r] *= a.scale * d;
+        S[j][r] *= -(half == 0 ? cw.beta : rows.beta[r]) * d;
       }
     }
     const f32x4 e0 = *reinterpret_cast<const f32x4*>(scalars + kE0 + w * 16 + g4);
@@ -563,11 +592,26 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
     const f32x4 be = *reinterpret_cast<const f32x4*>(scalars + kBeta + w * 16 + g4);
     // of the lane's four tokens, its columns' part: q . dq + k . (i side - j side), and k . eC (U dH1^T)
     f32x4 own = zero, ku = zero;
-    const Frag<3> ap[2] = {split8(Pc[0], Pc[1]), split8(Pc[2], Pc[3])};
-    const Frag<3> as[2] = {split8(Sc[0], Sc[1]), split8(Sc[2], Sc[3])};
-    const Frag<3> bp[2] = {split8(Pr[0], Pr[1]), split8(Pr[2], Pr[3])};
-    const Frag<3> bs[2] = {split8(Sr[0], Sr[1]), split8(Sr[2], Sr[3])};
-    __syncthreads();  // the slab is read, the diagonals are set
+    __syncthreads();  // the slab is read
+    // the waves w and w + 4 exchange what they made: (8 waves, 2 matrices, 4 tiles, 64 lanes)
+    f32x4* swap = reinterpret_cast<f32x4*>(staged);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      swap[((wave * 2 + 0) * 4 + j) * 64 + lane] = P[j];
+      swap[((wave * 2 + 1) * 4 + j) * 64 + lane] = S[j];
+    }
+    __syncthreads();
+    Frag<3> ap[2], as[2], bp[2], bs[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4* lo = swap + (w * 8 + 2 * i) * 64 + lane;        // of wave w
+      const f32x4* hi = swap + ((w + 4) * 8 + 2 * i) * 64 + lane;  // of wave w + 4
+      ap[i] = split8(lo[0], lo[64]);
+      as[i] = split8(lo[256], lo[320]);
+      bp[i] = split8(hi[0], hi[64]);
+      bs[i] = split8(hi[256], hi[320]);
+    }
+    if constexpr (!Lds::kBeside) __syncthreads();
     const f32x4 dp = *reinterpret_cast<const f32x4*>(&diag_dP[w * 16 + g4]);
     const auto finish = [&](int m, int local) {  // the wave's tile m, staged as tile `local`
       E1[m] *= a.scale * e0;
@@ -581,19 +625,14 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
           kv = column_values(kc, w);
           qv = column_values(qc, w);
         }
-        if (ts <= w / 2) {
-          E1[m] = mma(ap[ts], kc, E1[m]);
-          E2[m] = mma(as[ts], kc, E2[m]);
-        }
-        if (ts >= w / 2) {
-          x = mma(bs[ts], kc, x);
-          y = mma(bp[ts], qc, y);
-        }
+        if (ts <= w / 2) mma_pair(ap[ts], kc, E1[m], as[ts], kc, E2[m]);
+        if (ts >= w / 2) mma_pair(bs[ts], kc, x, bp[ts], qc, y);
       }
       ku += kv * E3[m];
       own += qv * E1[m] + kv * ((E2[m] - x) - y);
       dq_sum[m] += E1[m] + dp * kv;
       dk_sum[m] += ((E2[m] + E3[m]) + x) + (y + dp * qv);
+      keep_order();
     };
     if constexpr (KSL == KS) {
       if constexpr (!Lds::kBeside) {
@@ -627,14 +666,14 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
     __syncthreads();
     if (wave == 0) {
       // a lane per token, sums within its document: from it on, and (eC is 0 before the last document) up to it
-      const int seg = gates.seg[lane];
+      const float seg = scalars[kSeg + lane];
       const double own_all = static_cast<double>(own_sum[0][lane]) + own_sum[1][lane];
       const double end_all = static_cast<double>(end_sum[0][lane]) + end_sum[1][lane];
       double from = own_all, upto = end_all;
 #pragma unroll
       for (int off = 1; off < 64; off *= 2) {
         const double after = __shfl_down(from, off), before = __shfl_up(upto, off);
-        const int seg_after = __shfl_down(seg, off), seg_up = __shfl_up(seg, off);
+        const float seg_after = __shfl_down(seg, off), seg_up = __shfl_up(seg, off);
         if (lane + off < 64 && seg_after == seg) from += after;
         if (lane >= off && seg_up == seg) upto += before;
       }
@@ -642,17 +681,14 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
 #pragma unroll
       for (int i = 0; i < 8; ++i) hh_all += waves_sum[i];
       const double sum = from + (upto - end_all) + scalars[kAC] * hh_all;
-      const int seg_before = __shfl_up(seg, 1);
-      const bool cut = lane == 0 ? seg > 0 : seg != seg_before;
+      const float seg_before = __shfl_up(seg, 1);
+      const bool cut = lane == 0 ? seg > 0.0f : seg != seg_before;
       const bool there = lane < n_tokens;
       const float dg = cut || !there ? 0.0f : static_cast<float>(sum);
-      const float delta = gates.delta[lane];
-      float d_dt = 0.0f;
+      const float d_dt = dg * a.A[h] * scalars[kSlope + lane];
       if (there) {
         const int64_t at = (t0 + lane) * a.Hv + h;
-        const float raw = load_elem(static_cast<const InT*>(a.dt), at) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
-        d_dt = dg * a.A[h] * fast_rcp(1.0f + fast_exp2(-raw * kLog2e));
-        const float d_beta = beta_sum[lane] * (1.0f - gates.beta[lane] / a.beta_scale);
+        const float d_beta = beta_sum[lane] * (1.0f - scalars[kBeta + lane] / a.beta_scale);
         if (s.grad_bf16) {
           store_elem(static_cast<bf16_t*>(s.ddt), at, d_dt);
           store_elem(static_cast<bf16_t*>(s.dbr), at, d_beta);
@@ -661,7 +697,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
           store_elem(static_cast<float*>(s.dbr), at, d_beta);
         }
       }
-      const float dA = lanes_sum<64>(dg * delta), dbias = lanes_sum<64>(d_dt);
+      const float dA = lanes_sum<64>(dg * scalars[kDelta + lane]), dbias = lanes_sum<64>(d_dt);
       if (lane == 0) {
         s.part[record * 2] = dA;
         s.part[record * 2 + 1] = dbias;

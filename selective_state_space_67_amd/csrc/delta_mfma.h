@@ -123,6 +123,32 @@ __device__ __forceinline__ void mma_n(const Frag<NA> (&a)[N], const Frag<NB>& b,
         for (int n = 0; n < N; ++n) c[n] = mfma(a[n].p[i], b.p[s - i], c[n]);
 }
 
+// c[n] += a b[n] for two independent sums, in turns.
+template <int NA, int NB>
+__device__ __forceinline__ void mma_b(const Frag<NA>& a, const Frag<NB> (&b)[2], f32x4* c) {
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB) {
+        c[0] = mfma(a.p[i], b[0].p[s - i], c[0]);
+        c[1] = mfma(a.p[i], b[1].p[s - i], c[1]);
+      }
+}
+// c += a b and d += e f, in turns.
+template <int NA, int NB>
+__device__ __forceinline__ void mma_pair(const Frag<NA>& a, const Frag<NB>& b, f32x4& c, const Frag<NA>& e,
+                                         const Frag<NB>& f, f32x4& d) {
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB) {
+        c = mfma(a.p[i], b.p[s - i], c);
+        d = mfma(e.p[i], f.p[s - i], d);
+      }
+}
+
 // Rows of tokens staged in LDS as A operands: parts x (64 / 16 tiles of rows) x
 // (KS tiles of 32 entries) x 64 lanes x 8 entries.
 template <int NP, int KS>
@@ -329,11 +355,16 @@ __device__ __forceinline__ void mma_tri_t(const uint16_t* m, const Frag<NB> (&b)
   c[1] += d[1];
 }
 
-// Per-chunk scalars: e0, eC and beta of the 64 tokens, aC.
-//   e0 = exp(sum of log decays from the chunk's start through the token), 0 after a reset
+// Per-chunk scalars, eight rows of 64 tokens:
+//   e0 = exp(sum of log decays from the chunk's start through the token), 0 after a reset;
+//        the last token's, aC, is the whole chunk's decay
 //   eC = exp(sum after the token to the chunk's end), 0 before a reset
-//   aC = e0 of the last token: the whole chunk's decay
-constexpr int kGateFloats = 256;
-constexpr int kE0 = 0, kEC = 64, kBeta = 128, kAC = 192;
+//   beta; the derivative of softplus at the token's step size
+// and for the backward the sums themselves (in log2 units, as two floats), the number
+// of documents started in the chunk up to the token, and the step size.
+constexpr int kE0 = 0, kAC = 63, kEC = 64, kBeta = 128, kSlope = 192;
+constexpr int kSumHi = 256, kSumLo = 320, kSeg = 384, kDelta = 448;
+constexpr int kGateFloats = 256;     // what the walks read
+constexpr int kGateFloatsBwd = 512;
 
 }  // namespace ssm
