@@ -346,11 +346,38 @@ hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd
   return vec ? prepare_bf16<true, false>(a, blocks, bwd, stream) : prepare_bf16<false, false>(a, blocks, bwd, stream);
 }
 
+namespace {
+
+// Pieces that cost least, in units of a chunk's step of the full walk (4.2 us at 128 x
+// 128): rounds of one workgroup a CU times the chunks of a piece, where a step of the
+// aggregates' walk, which has a workgroup for every 64 of dk + dv columns, takes 0.7;
+// a piece's fold takes 0.7; and two more launches. Measured at 128 x 128: 2 heads of 131072
+// steps 9356 us in one piece, 16 heads x 2 of 4096 310 us, 12 x 8 of 2048 211 us (406 in
+// two: the grid is full as it is).
+int choose_pieces(int64_t heads, int chunks, int dk, int dv) {
+  constexpr int64_t kCUs = 256;
+  const int64_t strips = (dv + 15) / 16, state_strips = 2 * padded_ks(dk);
+  const int64_t walk = heads * ((strips + 3) / 4), agg = heads * ((strips + state_strips + 3) / 4);
+  int best = 1;
+  double least = static_cast<double>(chunks) * static_cast<double>((walk + kCUs - 1) / kCUs);
+  for (int n = 2; n <= std::min(chunks / 2, 256); ++n) {
+    const int steps = (chunks + n - 1) / n;
+    const double cost = steps * (static_cast<double>((walk * n + kCUs - 1) / kCUs) +
+                                 0.7 * static_cast<double>((agg * n + kCUs - 1) / kCUs)) + 0.7 * n + 3.0;
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
 DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int requested) {
   DeltaChunks d{};
   d.chunks = static_cast<int>((L + kChunk - 1) / kChunk);
-  d.pieces = 1;
-  if (requested > 0) d.pieces = std::min(requested, d.chunks);
+  d.pieces = requested > 0 ? std::min(requested, d.chunks) : choose_pieces(B * Hv, d.chunks, dk, dv);
   d.chunks_piece = (d.chunks + d.pieces - 1) / d.pieces;
   d.pieces = (d.chunks + d.chunks_piece - 1) / d.chunks_piece;
   const size_t records = static_cast<size_t>(B) * Hv * d.chunks;
