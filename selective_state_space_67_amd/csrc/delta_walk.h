@@ -211,7 +211,6 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
     char* st_next = staged + (STAGES == 2 ? ((c + 1 - c0) & 1) * S::kBytes : 0);
     const bool more = c + 1 < c1;
     ChunkSource<InT> next = src;
-    LaneOffsets next_off = whole;
     if (more) {
       next.q += kChunk * a.qs;
       next.k += kChunk * a.ks;
@@ -219,12 +218,12 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
       next.record += s.record_bytes;
       next.gates += s.record_bytes;
       next.n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(c + 1) * kChunk));
-      if (next.n_tokens < kChunk) next_off = lane_offsets(a, next.n_tokens, col0, lane, wave);
     }
+    const LaneOffsets next_off = offsets(next.n_tokens);  // the next chunk may be the last, with fewer tokens
     if constexpr (STAGES == 2) {
       wait_loads();
       __syncthreads();  // this stage is loaded, and the other one is no longer read
-      stage_async<InT, KS, MODE, OP, 0>(st_next, next, next_off, lane, wave);  // past the end: this chunk again
+      if (more) stage_async<InT, KS, MODE, OP, 0>(st_next, next, next_off, lane, wave);
     } else {
       __syncthreads();  // the previous chunk is no longer read
       if constexpr (ASYNC)
@@ -282,7 +281,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
         }
       }
     }
-    if constexpr (STAGES == 2) stage_async<InT, KS, MODE, OP, 1>(st_next, next, next_off, lane, wave);
+    if (STAGES == 2 && more) stage_async<InT, KS, MODE, OP, 1>(st_next, next, next_off, lane, wave);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       f32x4 V = zero;
@@ -311,7 +310,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
       const Frag<3> rb[2] = {split8(X[0], X[1]), split8(X[2], X[3])};
       mma_tri(reinterpret_cast<const uint16_t*>(st + S::kT), rb, lane, U);
     }
-    if constexpr (STAGES == 2) stage_async<InT, KS, MODE, OP, 2>(st_next, next, next_off, lane, wave);
+    if (STAGES == 2 && more) stage_async<InT, KS, MODE, OP, 2>(st_next, next, next_off, lane, wave);
     if constexpr (OUT) {
       const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
       mma_tri<OP>(reinterpret_cast<const uint16_t*>(st + S::kP), ub, lane, Y);
@@ -324,7 +323,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
         for (int r = 0; r < 4; ++r)
           if (own < s.cols) to[(m * 16 + g4 + r) * s.cols] = U[m][r];
     }
-    if constexpr (STAGES == 2) stage_async<InT, KS, MODE, OP, 3>(st_next, next, next_off, lane, wave);
+    if (STAGES == 2 && more) stage_async<InT, KS, MODE, OP, 3>(st_next, next, next_off, lane, wave);
 #pragma unroll
     for (int m = 0; m < 4; ++m) U[m] *= *reinterpret_cast<const f32x4*>(gates + kEC + m * 16 + g4);
     const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
