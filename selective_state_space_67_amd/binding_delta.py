@@ -72,13 +72,28 @@ def declare(lib):
             raise ImportError("libssmscan.so struct layout does not match this binding")
 
 
+def _need(t, shape, name, dtype):
+    """t is a contiguous tensor of this shape and type (these checks are most of a small call's time)."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        _b._need(t, shape, name, dtype)
+
+
+def _stream(stream, device):
+    """The stream's address; without one, torch's current stream of the device."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
 def _tokens(t, shape, name, dtype):
     """Elements between consecutive tokens of t (B, L, heads, entries); 0 where there is at most one."""
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
     if t.dtype != dtype:
         raise TypeError("%s must be %s" % (name, dtype))
@@ -115,11 +130,11 @@ def _delta_inputs(q, k, v, dt_raw, A, beta_raw, dt_bias):
     qs = _tokens(q, (B, L, Hk, dk), "q", q.dtype)
     ks = _tokens(k, (B, L, Hk, dk), "k", q.dtype)
     vs = _tokens(v, (B, L, Hv, dv), "v", q.dtype)
-    _b._need(dt_raw, (B, L, Hv), "dt_raw", q.dtype)
-    _b._need(beta_raw, (B, L, Hv), "beta_raw", q.dtype)
-    _b._need(A, (Hv,), "A", torch.float32)
+    _need(dt_raw, (B, L, Hv), "dt_raw", q.dtype)
+    _need(beta_raw, (B, L, Hv), "beta_raw", q.dtype)
+    _need(A, (Hv,), "A", torch.float32)
     if dt_bias is not None:
-        _b._need(dt_bias, (Hv,), "dt_bias", torch.float32)
+        _need(dt_bias, (Hv,), "dt_bias", torch.float32)
     return (B, L, Hk, Hv, dk, dv), (qs, ks, vs)
 
 
@@ -128,12 +143,12 @@ def _delta_params(q, k, v, dt_raw, A, beta_raw, dt_bias, reset, h0, h_last, out,
 
     sizes, strides = _delta_inputs(q, k, v, dt_raw, A, beta_raw, dt_bias)
     B, L, _, Hv, dk, dv = sizes
-    _b._need(out, (B, L, Hv, dv), "out")
+    _need(out, (B, L, Hv, dv), "out", out.dtype)
     if reset is not None:
-        _b._need(reset, (B, L), "reset", torch.uint8)
+        _need(reset, (B, L), "reset", torch.uint8)
     for t, name in ((h0, "h0"), (h_last, "h_last")):
         if t is not None:
-            _b._need(t, (B, Hv, dk, dv), name, torch.float32)
+            _need(t, (B, Hv, dk, dv), name, torch.float32)
     return DeltaParams(*sizes, _b._dtype_code(q), _b._dtype_code(out), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                        *strides, dt_raw.data_ptr(), beta_raw.data_ptr(), _addr(dt_bias), A.data_ptr(), _addr(reset),
                        _addr(h0), out.data_ptr(), _addr(h_last), None, 0,
@@ -157,7 +172,7 @@ def ssm_delta_fwd(q, k, v, dt_raw, A, beta_raw, *, dt_bias=None, reset=None, h0=
         out = torch.empty(v.shape, dtype=out_dtype or torch.float32, device=v.device)
     p = _delta_params(q, k, v, dt_raw, A, beta_raw, dt_bias, reset, h0, h_last, out, scale, beta_scale, num_segments)
     workspace = _workspace(lib.ssm_delta_workspace_size, p, workspace, v.device)
-    _b._check(lib.ssm_delta_fwd(ctypes.byref(p), _b._stream(stream, v.device)))
+    _b._check(lib.ssm_delta_fwd(ctypes.byref(p), _stream(stream, v.device)))
     return out
 
 
@@ -166,8 +181,8 @@ def _delta_update_params(h, q, k, v, dt_raw, A, beta_raw, dt_bias, out, scale, b
 
     sizes, strides = _delta_inputs(q, k, v, dt_raw, A, beta_raw, dt_bias)
     B, T, _, Hv, dk, dv = sizes
-    _b._need(h, (B, Hv, dk, dv), "h", torch.float32)
-    _b._need(out, (B, T, Hv, dv), "out")
+    _need(h, (B, Hv, dk, dv), "h", torch.float32)
+    _need(out, (B, T, Hv, dv), "out", out.dtype)
     return DeltaUpdateParams(*sizes, _b._dtype_code(q), _b._dtype_code(out), h.data_ptr(), q.data_ptr(), k.data_ptr(),
                              v.data_ptr(), *strides, dt_raw.data_ptr(), beta_raw.data_ptr(), _addr(dt_bias),
                              A.data_ptr(), out.data_ptr(), dk ** -0.5 if scale is None else scale, beta_scale)
@@ -183,7 +198,7 @@ def ssm_delta_update(h, q, k, v, dt_raw, A, beta_raw, *, dt_bias=None, out=None,
     if out is None:
         out = torch.empty(v.shape, dtype=out_dtype or torch.float32, device=v.device)
     p = _delta_update_params(h, q, k, v, dt_raw, A, beta_raw, dt_bias, out, scale, beta_scale)
-    _b._check(lib.ssm_delta_update(ctypes.byref(p), _b._stream(stream, v.device)))
+    _b._check(lib.ssm_delta_update(ctypes.byref(p), _stream(stream, v.device)))
     return out
 
 
@@ -197,7 +212,7 @@ def prepare_delta_update(h, q, k, v, dt_raw, A, beta_raw, *, dt_bias=None, out=N
     if out is None:
         out = torch.empty(v.shape, dtype=out_dtype or torch.float32, device=v.device)
     p = _delta_update_params(h, q, k, v, dt_raw, A, beta_raw, dt_bias, out, scale, beta_scale)
-    st, fn, pref = _b._stream(stream, v.device), lib.ssm_delta_update, ctypes.byref(p)
+    st, fn, pref = _stream(stream, v.device), lib.ssm_delta_update, ctypes.byref(p)
 
     def call():
         _b._check(fn(pref, st))
@@ -223,12 +238,12 @@ def ssm_delta_bwd(q, k, v, dt_raw, A, beta_raw, dout, *, dt_bias=None, reset=Non
     lib = _b.load_library()
     sizes, strides = _delta_inputs(q, k, v, dt_raw, A, beta_raw, dt_bias)
     B, L, Hk, Hv, dk, dv = sizes
-    _b._need(dout, (B, L, Hv, dv), "dout", q.dtype)
+    _need(dout, (B, L, Hv, dv), "dout", q.dtype)
     if reset is not None:
-        _b._need(reset, (B, L), "reset", torch.uint8)
+        _need(reset, (B, L), "reset", torch.uint8)
     for t, name in ((h0, "h0"), (dh_last, "dh_last")):
         if t is not None:
-            _b._need(t, (B, Hv, dk, dv), name, torch.float32)
+            _need(t, (B, Hv, dk, dv), name, torch.float32)
     gd, dev = grad_dtype or torch.float32, q.device
     g = dict(dq=torch.empty((B, L, Hk, dk), dtype=gd, device=dev), dk=torch.empty((B, L, Hk, dk), dtype=gd, device=dev),
              dv=torch.empty((B, L, Hv, dv), dtype=gd, device=dev), d_dt_raw=torch.empty((B, L, Hv), dtype=gd, device=dev),
@@ -242,7 +257,7 @@ def ssm_delta_bwd(q, k, v, dt_raw, A, beta_raw, dout, *, dt_bias=None, reset=Non
                        g["dv"].data_ptr(), g["d_dt_raw"].data_ptr(), g["dbeta_raw"].data_ptr(), g["dA"].data_ptr(),
                        _addr(g["d_dt_bias"]), _addr(g["dh0"]), None, 0, dk ** -0.5 if scale is None else scale, beta_scale)
     workspace = _workspace(lib.ssm_delta_bwd_workspace_size, p, workspace, dev)
-    _b._check(lib.ssm_delta_bwd(ctypes.byref(p), _b._stream(stream, dev)))
+    _b._check(lib.ssm_delta_bwd(ctypes.byref(p), _stream(stream, dev)))
     return g
 
 
@@ -255,17 +270,17 @@ def _norm_params(q, k, wq, wk, kind, eps, cos, sin, positions, interleaved):
     ks = _tokens(k, (B, L, Hk, d), "k", q.dtype)
     for t, name in ((wq, "wq"), (wk, "wk")):
         if t is not None:
-            _b._need(t, (d,), name, torch.float32)
+            _need(t, (d,), name, torch.float32)
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     rot = P = 0
     if cos is not None:
         P, half = cos.shape
         rot = 2 * half
-        _b._need(cos, (P, half), "cos", torch.float32)
-        _b._need(sin, (P, half), "sin", torch.float32)
+        _need(cos, (P, half), "cos", torch.float32)
+        _need(sin, (P, half), "sin", torch.float32)
     if positions is not None:
-        _b._need(positions, (B, L), "positions", torch.int32)
+        _need(positions, (B, L), "positions", torch.int32)
     p = QkNormParams(B, L, Hq, Hk, d, rot, P, _b._dtype_code(q), 0, q.data_ptr(), k.data_ptr(), qs, ks, _addr(wq),
                      _addr(wk), _addr(cos), _addr(sin), _addr(positions))
     p.eps = eps
@@ -295,10 +310,10 @@ def ssm_qk_norm_fwd(q, k, *, wq=None, wk=None, kind="rms", eps=1e-6, cos=None, s
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=q_out.dtype, device=k.device)
     p = _norm_params(q, k, wq, wk, kind, eps, cos, sin, positions, interleaved)
-    _b._need(q_out, q.shape, "q_out")
-    _b._need(k_out, k.shape, "k_out", q_out.dtype)
+    _need(q_out, q.shape, "q_out", q_out.dtype)
+    _need(k_out, k.shape, "k_out", q_out.dtype)
     p.out_dtype, p.q_out, p.k_out = _b._dtype_code(q_out), q_out.data_ptr(), k_out.data_ptr()
-    _b._check(lib.ssm_qk_norm_fwd(ctypes.byref(p), _b._stream(stream, q.device)))
+    _b._check(lib.ssm_qk_norm_fwd(ctypes.byref(p), _stream(stream, q.device)))
     return q_out, k_out
 
 
@@ -315,11 +330,11 @@ def ssm_qk_norm_bwd(q, k, dq_out, dk_out, *, wq=None, wk=None, kind="rms", eps=1
     for name in ("dwq", "dwk"):
         g[name] = torch.empty(q.shape[3], dtype=torch.float32, device=q.device) if want_dw else None
     p = _norm_params(q, k, wq, wk, kind, eps, cos, sin, positions, interleaved)
-    _b._need(dq_out, q.shape, "dq_out", q.dtype)
-    _b._need(dk_out, k.shape, "dk_out", q.dtype)
+    _need(dq_out, q.shape, "dq_out", q.dtype)
+    _need(dk_out, k.shape, "dk_out", q.dtype)
     p.out_dtype = _b._dtype_code(g["dq"])
     p.dq_out, p.dk_out, p.dq, p.dk = dq_out.data_ptr(), dk_out.data_ptr(), g["dq"].data_ptr(), g["dk"].data_ptr()
     p.dwq, p.dwk = _addr(g["dwq"]), _addr(g["dwk"])
     workspace = _workspace(lib.ssm_qk_norm_bwd_workspace_size, p, workspace, q.device)
-    _b._check(lib.ssm_qk_norm_bwd(ctypes.byref(p), _b._stream(stream, q.device)))
+    _b._check(lib.ssm_qk_norm_bwd(ctypes.byref(p), _stream(stream, q.device)))
     return g
