@@ -17,11 +17,12 @@
 // its decay. Pairs i = j cross nothing: their products are left out of the sum and
 // added to dQ and dK afterwards, so that they need not cancel.)
 //
-// Four launches: the chunks' matrices (delta_chunk.hip, with transposes); the
+// Five launches and a sum: the chunks' matrices (delta_chunk.hip, with transposes); the
 // forward walk again, keeping each chunk's first state and U; the reverse walk
 // below, which mirrors the forward one (a wave owns 16 columns of dH in registers)
-// and keeps each chunk's dH1 and dR; and the gradients, every chunk of every key
-// head in parallel, with the value heads of a key head added up in one workgroup.
+// and keeps each chunk's dH1 and dR; the gradients of q and k, every chunk of every
+// key head in parallel, with the value heads of a key head added up in one workgroup;
+// and those of the gates, a wave for every chunk of every value head.
 #include <algorithm>
 
 #include "delta_chunk.h"
@@ -36,6 +37,7 @@ constexpr int kBlockCols = 16 * kWaves;
 struct BwdArgs {
   ChunkArgs c;
   int col_blocks, cols;
+  int items;             // chunks of all key heads
   int grad_bf16;
   bool vec_out;          // rows of dout come as whole 16-byte runs
   const void* dout;
@@ -44,6 +46,7 @@ struct BwdArgs {
   const float* U;        // (bh, chunk, 64, cols)
   float* dstates;        // as states: dH1
   float* dR;             // as U
+  float* sums;           // (bh, chunk, split, kSumFloats): what the gates' gradients are made of
   float* part;           // (bh, chunk, 2): dA, d dt_bias
   void* dq;
   void* dk;
@@ -354,19 +357,26 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
 
 // ---- the gradients of a chunk ----
 
-constexpr int kGradThreads = 512;
+// A workgroup takes up to 64 entries of q and k (SL tiles of 32): its accumulators then
+// fit 256 registers, so that two workgroups share a CU and one multiplies while the
+// other waits for its operands (all 128 entries in one workgroup of eight waves
+// spilled and took twice as long). P and S are made anew for every split.
+__host__ __device__ constexpr int split_tiles(int ks) { return ks % 2 == 0 ? 2 : ks == 3 ? 3 : 1; }
+constexpr int grad_splits(int ks) { return ks / split_tiles(ks); }
+// A split's sums: own, end, the diagonal of dR U^T (64 tokens each), <dH1, H0>.
+constexpr int kSumOwn = 0, kSumEnd = 64, kSumBeta = 128, kSumState = 192, kSumFloats = 256;
 
 // Tile row that a state row is staged at, so that column n of tile m is state_row(m, ..).
 __device__ __forceinline__ int staged_row(int row) {
   return ((row >> 5) * 2 + ((row >> 2) & 1)) * 16 + ((row >> 3) & 3) * 4 + (row & 3);
 }
 
-// One thread's part of a 32-column slab: eight columns of one row of U, dR (the lower
-// and upper half of the threads), of dO, and of ITEMS rows of H0 and dH1.
+// One thread's part of a 32-column slab: eight columns of one row of dO, U and dR, and of
+// ITEMS rows of H0 and dH1.
 template <int NP, int ITEMS>
 struct SlabLoads {
-  u32x4 o[NP == 1 ? 1 : 2];  // of dO, as they lie in memory (the lower half of the threads)
-  f32x4 u[2], h[ITEMS][2], g[ITEMS][2];
+  u32x4 o[NP == 1 ? 1 : 2];  // as they lie in memory
+  f32x4 u[2], r[2], h[ITEMS][2], g[ITEMS][2];
 };
 
 template <int NP, int TILES>
@@ -384,20 +394,18 @@ __device__ __forceinline__ void store_slab(uint16_t* s, int at, int oct, const f
     *reinterpret_cast<u32x4*>(s + k * TILES * 512 + ((at >> 4) * 64 + oct * 16 + (at & 15)) * 8) = f.p[k];
 }
 
-// LDS of a workgroup: the slab, and the staged tokens of K and Q, KSL tiles of 32
-// entries at a time, beside it for the whole call or in its place after each head.
-template <int NP, int KS>
+// LDS of a workgroup: the slab, and its entries of the staged tokens of K and Q, beside it
+// for the whole call where two workgroups still fit a CU, else in its place after each head.
+template <int NP, int SL>
 struct GradLds {
-  static constexpr int kLimit = kMaxLds - 6 * 1024;
   static constexpr int kdO = 0;
   static constexpr int kU = kdO + NP * 4096;
   static constexpr int kdR = kU + 3 * 4096;
   static constexpr int kH = kdR + 3 * 4096;
-  static constexpr int kdH = kH + 3 * 2 * KS * 1024;
-  static constexpr int kSlab = std::max(kdH + 3 * 2 * KS * 1024, 64 * 1024);  // at least the exchange of P and S
-  static constexpr int KSL = 2 * TokenTile<NP, KS>::kBytes <= kLimit ? KS : KS / 2;
-  static constexpr int kTile = TokenTile<NP, KSL>::kBytes;
-  static constexpr bool kBeside = KSL == KS && kSlab + 2 * kTile <= kLimit;
+  static constexpr int kdH = kH + 3 * 2 * SL * 1024;
+  static constexpr int kSlab = kdH + 3 * 2 * SL * 1024;
+  static constexpr int kTile = TokenTile<NP, SL>::kBytes;
+  static constexpr bool kBeside = kSlab + 2 * kTile <= 76 * 1024;
   static constexpr int kK = kBeside ? kSlab : 0;
   static constexpr int kQ = kK + kTile;
   static constexpr int kBytes = kBeside ? kSlab + 2 * kTile : std::max(kSlab, 2 * kTile);
@@ -420,28 +428,32 @@ __device__ __forceinline__ f32x4 column_values(const Frag<NP>& f, int w) {
 // Keeps the compiler from reading the operands of many tiles ahead, which spills.
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
-// One workgroup: a chunk of one key head, its value heads in turn. Eight waves: wave
-// w + 4 * half has the tokens of tile w as rows of dQ and dK and half of their columns.
-// The sums over dv go in slabs of 32 columns, the next one's loads under way while one
-// is multiplied.
-template <typename InT, int NP, int KS>
-__global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs s) {
-  using Lds = GradLds<NP, KS>;
-  constexpr int DKT = 2 * KS, ROWS = 32 * KS, MT = KS;  // MT: a wave's state tiles
-  constexpr int KSL = Lds::KSL, ITEMS = (ROWS * 4 + kGradThreads - 1) / kGradThreads;
-  using Tile = TokenTile<NP, KSL>;
+// One workgroup: 32 SL entries of a chunk of one key head, its value heads in turn; wave w
+// has the tokens of tile w as rows of dQ and dK. The sums over dv go in slabs of 32
+// columns, the next one's loads under way while one is multiplied.
+template <typename InT, int NP, int SL>
+__global__ __launch_bounds__(kThreads, 2) void delta_chunk_grads(const BwdArgs s, int splits) {
+  using Lds = GradLds<NP, SL>;
+  using Tile = TokenTile<NP, SL>;
+  constexpr int MT = 2 * SL, ROWS = 32 * SL, ITEMS = ROWS * 4 / kThreads > 0 ? (ROWS * 4 + kThreads - 1) / kThreads : 1;
   extern __shared__ __align__(16) char staged[];
   __shared__ __align__(16) float scalars[kGateFloatsBwd];
-  __shared__ __align__(16) float own_sum[2][64], end_sum[2][64], beta_sum[64], diag_dP[64], waves_sum[8];
+  __shared__ __align__(16) float diag_dP[64], waves_sum[kWaves];
   const ChunkArgs& a = s.c;
-  const int lane = threadIdx.x % 64, wave = wave_index(), w = wave & 3, half = wave >> 2;
+  const int lane = threadIdx.x % 64, w = wave_index();
   const int g4 = (lane >> 4) * 4, col = lane & 15;
-  const int chunk = blockIdx.x % a.chunks, bhk = blockIdx.x / a.chunks;
+  // The splits of a chunk, which read the same U, dR and dO, are 8 workgroups apart: workgroups
+  // go round the 8 dies in turn, so they share a die's L2.
+  const int eights = blockIdx.x / (8 * splits), in = blockIdx.x - eights * 8 * splits;
+  const int split = in / 8, item = eights * 8 + in % 8;
+  if (item >= s.items) return;
+  const int chunk = item % a.chunks, bhk = item / a.chunks;
   const int b = bhk / a.Hk, hk = bhk - b * a.Hk;
+  const int first = split * ROWS, all_rows = splits * ROWS;  // the workgroup's entries, and the states' rows
   const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(chunk) * kChunk;
   const int n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(chunk) * kChunk));
-  const InT* q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
-  const InT* k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
+  const InT* q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk + first;
+  const InT* k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk + first;
   uint16_t* sdO = reinterpret_cast<uint16_t*>(staged + Lds::kdO);
   uint16_t* sU = reinterpret_cast<uint16_t*>(staged + Lds::kU);
   uint16_t* sdR = reinterpret_cast<uint16_t*>(staged + Lds::kdR);
@@ -453,11 +465,12 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
   // columns at or past dv (rounded up to 8) may hold copies of others: read as 0
   const int limit = (a.dv + 7) / 8 * 8;
   const int64_t token_v = static_cast<int64_t>(a.Hv) * a.dv;
-  const auto stage_qk = [&](int d0) {
-    stage_rows<InT, NP, KSL, kGradThreads>(sk, k + d0, a.ks, n_tokens, a.dk - d0, a.vec);
-    stage_rows<InT, NP, KSL, kGradThreads>(sq, q + d0, a.qs, n_tokens, a.dk - d0, a.vec);
+  const int oct = threadIdx.x & 3, row = threadIdx.x >> 2;  // this thread's rows and columns of a slab
+  const auto stage_qk = [&]() {
+    stage_rows<InT, NP, SL, kThreads>(sk, k, a.ks, n_tokens, a.dk - first, a.vec);
+    stage_rows<InT, NP, SL, kThreads>(sq, q, a.qs, n_tokens, a.dk - first, a.vec);
   };
-  if constexpr (Lds::kBeside) stage_qk(0);
+  if constexpr (Lds::kBeside) stage_qk();
 
   f32x4 dq_sum[MT], dk_sum[MT];
 #pragma unroll
@@ -466,76 +479,78 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
   for (int gi = 0; gi < a.group; ++gi) {
     const int h = hk * a.group + gi, bh = b * a.Hv + h;
     const int64_t record = static_cast<int64_t>(bh) * a.chunks + chunk;
-    const float* H0 = s.states + record * ROWS * s.cols;
-    const float* dH1 = s.dstates + record * ROWS * s.cols;
-    const InT* dout = static_cast<const InT*>(s.dout) + (t0 * a.Hv + h) * a.dv;
-    // this thread's rows and columns of a slab
-    const int oct = threadIdx.x & 3, row = (threadIdx.x >> 2) & 63;
-    const float* uv = (threadIdx.x < 256 ? s.U : s.dR) + record * kChunk * s.cols + row * s.cols;
+    const float* H0 = s.states + (record * all_rows + first) * s.cols;
+    const float* dH1 = s.dstates + (record * all_rows + first) * s.cols;
+    const float* U = s.U + (record * kChunk + row) * s.cols;
+    const float* dR = s.dR + (record * kChunk + row) * s.cols;
+    const InT* dout = static_cast<const InT*>(s.dout) + (t0 * a.Hv + h) * a.dv + row * token_v;
     const auto fetch = [&](SlabLoads<NP, ITEMS>& x, int d0) {
       const int c = d0 + oct * 8;
-      const bool in = c < limit;
-      const int at = in ? c : 0;
+      const bool inside = c < limit;
+      const int at = inside ? c : 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) x.u[i] = in ? *reinterpret_cast<const f32x4*>(uv + at + 4 * i) : zero;
+      for (int i = 0; i < 2; ++i) {
+        x.u[i] = inside ? *reinterpret_cast<const f32x4*>(U + at + 4 * i) : zero;
+        x.r[i] = inside ? *reinterpret_cast<const f32x4*>(dR + at + 4 * i) : zero;
+      }
 #pragma unroll
       for (int n = 0; n < ITEMS; ++n) {
-        const int r = min(static_cast<int>(threadIdx.x >> 2) + n * (kGradThreads / 4), ROWS - 1);
+        const int r = min(row + n * (kThreads / 4), ROWS - 1);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          x.h[n][i] = in ? *reinterpret_cast<const f32x4*>(H0 + static_cast<int64_t>(r) * s.cols + at + 4 * i) : zero;
-          x.g[n][i] = in ? *reinterpret_cast<const f32x4*>(dH1 + static_cast<int64_t>(r) * s.cols + at + 4 * i) : zero;
+          x.h[n][i] = inside ? *reinterpret_cast<const f32x4*>(H0 + r * s.cols + at + 4 * i) : zero;
+          x.g[n][i] = inside ? *reinterpret_cast<const f32x4*>(dH1 + r * s.cols + at + 4 * i) : zero;
         }
       }
-      if (threadIdx.x < 256) {
-        const InT* p = dout + row * token_v + c;
-        const int left = row < n_tokens ? a.dv - c : 0;
-        const u32x4 none = {0, 0, 0, 0};
-        if (s.vec_out) {
+      const int left = row < n_tokens ? a.dv - c : 0;
+      const u32x4 none = {0, 0, 0, 0};
+      if (s.vec_out) {
 #pragma unroll
-          for (int i = 0; i < (NP == 1 ? 1 : 2); ++i) x.o[i] = left > 0 ? reinterpret_cast<const u32x4*>(p)[i] : none;
-        } else if constexpr (NP == 1) {
-          uint32_t e[8];
+        for (int i = 0; i < (NP == 1 ? 1 : 2); ++i)
+          x.o[i] = left > 0 ? reinterpret_cast<const u32x4*>(dout + c)[i] : none;
+      } else if constexpr (NP == 1) {
+        uint32_t e[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) e[j] = j < left ? p[j].bits : 0u;
-          x.o[0] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
-        } else {
+        for (int j = 0; j < 8; ++j) e[j] = j < left ? dout[c + j].bits : 0u;
+        x.o[0] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+      } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x.o[j / 4][j % 4] = j < left ? __float_as_uint(p[j]) : 0u;
-        }
+        for (int j = 0; j < 8; ++j) x.o[j / 4][j % 4] = j < left ? __float_as_uint(dout[c + j]) : 0u;
       }
     };
     SlabLoads<NP, ITEMS> loads;
     fetch(loads, 0);
     __syncthreads();  // the previous head's scalars and tiles are used
-    scalars[threadIdx.x] = reinterpret_cast<const float*>(a.records + record * kRecBytesBwd + kRecGatesBwd)[threadIdx.x];
+#pragma unroll
+    for (int i = 0; i < kGateFloatsBwd / kThreads; ++i)
+      scalars[i * kThreads + threadIdx.x] =
+          reinterpret_cast<const float*>(a.records + record * kRecBytesBwd + kRecGatesBwd)[i * kThreads + threadIdx.x];
 
-    f32x4 E1[MT], E2[MT], E3[MT];  // dO H0^T, dR H0^T, U dH1^T: rows of tile w, columns of the wave's state tiles
+    f32x4 E1[MT], E2[MT], E3[MT];  // dO H0^T, dR H0^T, U dH1^T: rows of tile w, columns of the state tiles
 #pragma unroll
     for (int m = 0; m < MT; ++m) E1[m] = E2[m] = E3[m] = zero;
-    // the lower waves: U dO^T and U dR^T (rows of tile j <= w, columns w); the upper ones: dO U^T and
-    // dR U^T (rows of tile j >= w, columns w)
-    f32x4 P[4] = {zero, zero, zero, zero}, S[4] = {zero, zero, zero, zero};
+    // U dO^T and U dR^T (rows of tile j <= w, columns w); dO U^T and dR U^T (rows of tile j >= w, columns w)
+    f32x4 Pc[4] = {zero, zero, zero, zero}, Sc[4] = {zero, zero, zero, zero};
+    f32x4 Pr[4] = {zero, zero, zero, zero}, Sr[4] = {zero, zero, zero, zero};
     float hh = 0.0f;  // the thread's part of <dH1, H0>
     for (int d0 = 0; d0 < a.dv; d0 += 32) {
       if (d0 > 0) __syncthreads();  // the last slab is read
-      if (threadIdx.x < 256) {
-        uint16_t* to = sdO + ((row >> 4) * 64 + oct * 16 + (row & 15)) * 8;
-        if constexpr (NP == 1) {
-          *reinterpret_cast<u32x4*>(to) = loads.o[0];
-        } else {
-          const Frag<3> f = split8(__builtin_bit_cast(f32x4, loads.o[0]), __builtin_bit_cast(f32x4, loads.o[1]));
+      uint16_t* to = sdO + ((row >> 4) * 64 + oct * 16 + (row & 15)) * 8;
+      if constexpr (NP == 1) {
+        *reinterpret_cast<u32x4*>(to) = loads.o[0];
+      } else {
+        const Frag<3> f = split8(__builtin_bit_cast(f32x4, loads.o[0]), __builtin_bit_cast(f32x4, loads.o[1]));
 #pragma unroll
-          for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(to + i * 2048) = f.p[i];
-        }
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(to + i * 2048) = f.p[i];
       }
-      store_slab<4>(threadIdx.x < 256 ? sU : sdR, row, oct, loads.u);
+      store_slab<4>(sU, row, oct, loads.u);
+      store_slab<4>(sdR, row, oct, loads.r);
 #pragma unroll
       for (int n = 0; n < ITEMS; ++n) {
-        const int r = static_cast<int>(threadIdx.x >> 2) + n * (kGradThreads / 4);
+        const int r = row + n * (kThreads / 4);
         if (r < ROWS) {
-          store_slab<DKT>(sH, staged_row(r), oct, loads.h[n]);
-          store_slab<DKT>(sdH, staged_row(r), oct, loads.g[n]);
+          store_slab<MT>(sH, staged_row(r), oct, loads.h[n]);
+          store_slab<MT>(sdH, staged_row(r), oct, loads.g[n]);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -548,43 +563,45 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
       const Frag<3> Uw = slab_rows<3, 4>(sU, w, lane), dRw = slab_rows<3, 4>(sdR, w, lane);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const Frag<3> hb = slab_rows<3, DKT>(sH, half * MT + m, lane), gb = slab_rows<3, DKT>(sdH, half * MT + m, lane);
+        const Frag<3> hb = slab_rows<3, MT>(sH, m, lane), gb = slab_rows<3, MT>(sdH, m, lane);
         E1[m] = mma(dOw, hb, E1[m]);
         mma_pair(dRw, hb, E2[m], Uw, gb, E3[m]);
         keep_order();
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (half == 0 && j <= w) {
+        if (j <= w) {
           const Frag<3> Uj = slab_rows<3, 4>(sU, j, lane);
-          P[j] = mma(Uj, dOw, P[j]);
-          S[j] = mma(Uj, dRw, S[j]);
+          Pc[j] = mma(Uj, dOw, Pc[j]);
+          Sc[j] = mma(Uj, dRw, Sc[j]);
         }
-        if (half == 1 && j >= w) {
-          P[j] = mma(slab_rows<NP, 4>(sdO, j, lane), Uw, P[j]);
-          S[j] = mma(slab_rows<3, 4>(sdR, j, lane), Uw, S[j]);
+        if (j >= w) {
+          Pr[j] = mma(slab_rows<NP, 4>(sdO, j, lane), Uw, Pr[j]);
+          Sr[j] = mma(slab_rows<3, 4>(sdR, j, lane), Uw, Sr[j]);
         }
         keep_order();
       }
     }
 
     // d beta comes from the diagonal of dR U^T, and dP's is set aside; then the decays and masks.
+    float* sums = s.sums + (record * splits + split) * kSumFloats;
     const ColDecay cw = col_decay(scalars, w * 16 + col);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (j == w && half == 0 && (col >> 2) == (lane >> 4)) {
+      if (j == w && (col >> 2) == (lane >> 4)) {
         const int r = col & 3;
-        beta_sum[w * 16 + col] = r == 0 ? S[j].x : r == 1 ? S[j].y : r == 2 ? S[j].z : S[j].w;
-        diag_dP[w * 16 + col] = a.scale * (r == 0 ? P[j].x : r == 1 ? P[j].y : r == 2 ? P[j].z : P[j].w);
+        sums[kSumBeta + w * 16 + col] = r == 0 ? Sc[j].x : r == 1 ? Sc[j].y : r == 2 ? Sc[j].z : Sc[j].w;
+        diag_dP[w * 16 + col] = a.scale * (r == 0 ? Pc[j].x : r == 1 ? Pc[j].y : r == 2 ? Pc[j].z : Pc[j].w);
       }
       const RowDecay rows = row_decay(scalars, j * 16 + g4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int x = j * 16 + g4 + r, y = w * 16 + col;
-        // half 0: row token x before column token y; half 1: after it
-        const float d = half == 0 ? (x < y ? decay_up(rows, r, cw) : 0.0f) : (x > y ? decay_down(rows, r, cw) : 0.0f);
-        P[j][r] *= a.scale * d;
-        S[j][r] *= -(half == 0 ? cw.beta : rows.beta[r]) * d;
+        const float up = x < y ? decay_up(rows, r, cw) : 0.0f, down = x > y ? decay_down(rows, r, cw) : 0.0f;
+        Pc[j][r] *= a.scale * up;
+        Sc[j][r] *= -cw.beta * up;
+        Pr[j][r] *= a.scale * down;
+        Sr[j][r] *= -rows.beta[r] * down;
       }
     }
     const f32x4 e0 = *reinterpret_cast<const f32x4*>(scalars + kE0 + w * 16 + g4);
@@ -592,35 +609,25 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
     const f32x4 be = *reinterpret_cast<const f32x4*>(scalars + kBeta + w * 16 + g4);
     // of the lane's four tokens, its columns' part: q . dq + k . (i side - j side), and k . eC (U dH1^T)
     f32x4 own = zero, ku = zero;
-    __syncthreads();  // the slab is read
-    // the waves w and w + 4 exchange what they made: (8 waves, 2 matrices, 4 tiles, 64 lanes)
-    f32x4* swap = reinterpret_cast<f32x4*>(staged);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      swap[((wave * 2 + 0) * 4 + j) * 64 + lane] = P[j];
-      swap[((wave * 2 + 1) * 4 + j) * 64 + lane] = S[j];
+    const Frag<3> ap[2] = {split8(Pc[0], Pc[1]), split8(Pc[2], Pc[3])};
+    const Frag<3> as[2] = {split8(Sc[0], Sc[1]), split8(Sc[2], Sc[3])};
+    const Frag<3> bp[2] = {split8(Pr[0], Pr[1]), split8(Pr[2], Pr[3])};
+    const Frag<3> bs[2] = {split8(Sr[0], Sr[1]), split8(Sr[2], Sr[3])};
+    __syncthreads();  // the slab is read, the diagonal is set
+    if constexpr (!Lds::kBeside) {
+      stage_qk();
+      __syncthreads();
     }
-    __syncthreads();
-    Frag<3> ap[2], as[2], bp[2], bs[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const f32x4* lo = swap + (w * 8 + 2 * i) * 64 + lane;        // of wave w
-      const f32x4* hi = swap + ((w + 4) * 8 + 2 * i) * 64 + lane;  // of wave w + 4
-      ap[i] = split8(lo[0], lo[64]);
-      as[i] = split8(lo[256], lo[320]);
-      bp[i] = split8(hi[0], hi[64]);
-      bs[i] = split8(hi[256], hi[320]);
-    }
-    if constexpr (!Lds::kBeside) __syncthreads();
     const f32x4 dp = *reinterpret_cast<const f32x4*>(&diag_dP[w * 16 + g4]);
-    const auto finish = [&](int m, int local) {  // the wave's tile m, staged as tile `local`
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
       E1[m] *= a.scale * e0;
       E2[m] *= -be * e0;
       E3[m] *= eC;
       f32x4 x = zero, y = zero, kv = zero, qv = zero;
 #pragma unroll
       for (int ts = 0; ts < 2; ++ts) {
-        const Frag<NP> kc = Tile::columns(sk, local, ts, lane), qc = Tile::columns(sq, local, ts, lane);
+        const Frag<NP> kc = Tile::columns(sk, m, ts, lane), qc = Tile::columns(sq, m, ts, lane);
         if (ts == w / 2) {
           kv = column_values(kc, w);
           qv = column_values(qc, w);
@@ -633,23 +640,6 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
       dq_sum[m] += E1[m] + dp * kv;
       dk_sum[m] += ((E2[m] + E3[m]) + x) + (y + dp * qv);
       keep_order();
-    };
-    if constexpr (KSL == KS) {
-      if constexpr (!Lds::kBeside) {
-        stage_qk(0);
-        __syncthreads();
-      }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) finish(m, half * MT + m);
-    } else {
-      for (int pass = 0; pass < 2; ++pass) {  // the entries of each half's tiles in turn
-        if (pass > 0) __syncthreads();
-        stage_qk(pass * 32 * KSL);
-        __syncthreads();
-        if (pass == half)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) finish(m, m);
-      }
     }
     // sums over the 16 columns' lanes, and over the workgroup
 #pragma unroll
@@ -658,57 +648,19 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
       ku[r] = lanes_sum<16>(ku[r]);
     }
     if (col == 0) {
-      *reinterpret_cast<f32x4*>(&own_sum[half][w * 16 + g4]) = own;
-      *reinterpret_cast<f32x4*>(&end_sum[half][w * 16 + g4]) = ku;
+      *reinterpret_cast<f32x4*>(&sums[kSumOwn + w * 16 + g4]) = own;
+      *reinterpret_cast<f32x4*>(&sums[kSumEnd + w * 16 + g4]) = ku;
     }
     const float total = lanes_sum<64>(hh);
-    if (lane == 0) waves_sum[wave] = total;
+    if (lane == 0) waves_sum[w] = total;
     __syncthreads();
-    if (wave == 0) {
-      // a lane per token, sums within its document: from it on, and (eC is 0 before the last document) up to it
-      const float seg = scalars[kSeg + lane];
-      const double own_all = static_cast<double>(own_sum[0][lane]) + own_sum[1][lane];
-      const double end_all = static_cast<double>(end_sum[0][lane]) + end_sum[1][lane];
-      double from = own_all, upto = end_all;
-#pragma unroll
-      for (int off = 1; off < 64; off *= 2) {
-        const double after = __shfl_down(from, off), before = __shfl_up(upto, off);
-        const float seg_after = __shfl_down(seg, off), seg_up = __shfl_up(seg, off);
-        if (lane + off < 64 && seg_after == seg) from += after;
-        if (lane >= off && seg_up == seg) upto += before;
-      }
-      double hh_all = 0.0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) hh_all += waves_sum[i];
-      const double sum = from + (upto - end_all) + scalars[kAC] * hh_all;
-      const float seg_before = __shfl_up(seg, 1);
-      const bool cut = lane == 0 ? seg > 0.0f : seg != seg_before;
-      const bool there = lane < n_tokens;
-      const float dg = cut || !there ? 0.0f : static_cast<float>(sum);
-      const float d_dt = dg * a.A[h] * scalars[kSlope + lane];
-      if (there) {
-        const int64_t at = (t0 + lane) * a.Hv + h;
-        const float d_beta = beta_sum[lane] * (1.0f - scalars[kBeta + lane] / a.beta_scale);
-        if (s.grad_bf16) {
-          store_elem(static_cast<bf16_t*>(s.ddt), at, d_dt);
-          store_elem(static_cast<bf16_t*>(s.dbr), at, d_beta);
-        } else {
-          store_elem(static_cast<float*>(s.ddt), at, d_dt);
-          store_elem(static_cast<float*>(s.dbr), at, d_beta);
-        }
-      }
-      const float dA = lanes_sum<64>(dg * scalars[kDelta + lane]), dbias = lanes_sum<64>(d_dt);
-      if (lane == 0) {
-        s.part[record * 2] = dA;
-        s.part[record * 2 + 1] = dbias;
-      }
-    }
+    if (threadIdx.x == 0) sums[kSumState] = (waves_sum[0] + waves_sum[1]) + (waves_sum[2] + waves_sum[3]);
   }
 
   const int64_t token_k = static_cast<int64_t>(a.Hk) * a.dk;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int d = state_row(half * MT + m, col & 12, col & 3);
+    const int d = first + state_row(m, col & 12, col & 3);
     if (d >= a.dk) continue;
     const int64_t at = (t0 + w * 16 + g4) * token_k + static_cast<int64_t>(hk) * a.dk + d;
 #pragma unroll
@@ -722,6 +674,58 @@ __global__ __launch_bounds__(kGradThreads) void delta_chunk_grads(const BwdArgs 
         store_elem(static_cast<float*>(s.dk) + r * token_k, at, dk_sum[m][r]);
       }
     }
+  }
+}
+
+// The gates' gradients: a wave for a chunk of a value head, a lane per token.
+template <typename InT>
+__global__ __launch_bounds__(kThreads) void delta_gate_grads(const BwdArgs s, int splits, int64_t records) {
+  const ChunkArgs& a = s.c;
+  const int lane = threadIdx.x % 64;
+  const int64_t record = static_cast<int64_t>(blockIdx.x) * kWaves + wave_index();
+  if (record >= records) return;
+  const int bh = static_cast<int>(record / a.chunks), chunk = static_cast<int>(record - static_cast<int64_t>(bh) * a.chunks);
+  const int b = bh / a.Hv, h = bh - b * a.Hv;
+  const int n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(chunk) * kChunk));
+  const float* scalars = reinterpret_cast<const float*>(a.records + record * kRecBytesBwd + kRecGatesBwd);
+  const float* sums = s.sums + record * splits * kSumFloats;
+  double from = 0.0, end = 0.0, state = 0.0;
+  for (int i = 0; i < splits; ++i) {
+    from += sums[i * kSumFloats + kSumOwn + lane];
+    end += sums[i * kSumFloats + kSumEnd + lane];
+    state += sums[i * kSumFloats + kSumState];
+  }
+  // sums within the token's document: from it on, and (eC is 0 before the last document) up to it
+  const float seg = scalars[kSeg + lane];
+  double upto = end;
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) {
+    const double after = __shfl_down(from, off), before = __shfl_up(upto, off);
+    const float seg_after = __shfl_down(seg, off), seg_up = __shfl_up(seg, off);
+    if (lane + off < 64 && seg_after == seg) from += after;
+    if (lane >= off && seg_up == seg) upto += before;
+  }
+  const double sum = from + (upto - end) + scalars[kAC] * state;
+  const float seg_before = __shfl_up(seg, 1);
+  const bool cut = lane == 0 ? seg > 0.0f : seg != seg_before;
+  const bool there = lane < n_tokens;
+  const float dg = cut || !there ? 0.0f : static_cast<float>(sum);
+  const float d_dt = dg * a.A[h] * scalars[kSlope + lane];
+  if (there) {
+    const int64_t at = (static_cast<int64_t>(b) * a.L + static_cast<int64_t>(chunk) * kChunk + lane) * a.Hv + h;
+    const float d_beta = sums[kSumBeta + lane] * (1.0f - scalars[kBeta + lane] / a.beta_scale);
+    if (s.grad_bf16) {
+      store_elem(static_cast<bf16_t*>(s.ddt), at, d_dt);
+      store_elem(static_cast<bf16_t*>(s.dbr), at, d_beta);
+    } else {
+      store_elem(static_cast<float*>(s.ddt), at, d_dt);
+      store_elem(static_cast<float*>(s.dbr), at, d_beta);
+    }
+  }
+  const float dA = lanes_sum<64>(dg * scalars[kDelta + lane]), dbias = lanes_sum<64>(d_dt);
+  if (lane == 0) {
+    s.part[record * 2] = dA;
+    s.part[record * 2 + 1] = dbias;
   }
 }
 
@@ -768,13 +772,20 @@ hipError_t launch_reverse(const BwdArgs& s, int64_t heads, hipStream_t stream) {
 
 template <typename InT, int NP, int KS>
 hipError_t launch_grads(const BwdArgs& s, int64_t B, hipStream_t stream) {
-  constexpr int kBytes = GradLds<NP, KS>::kBytes;
-  static_assert(kBytes <= GradLds<NP, KS>::kLimit, "a slab exceeds LDS");
-  const int64_t blocks = B * s.c.Hk * s.c.chunks;
-  SSM_LOG("launch delta_chunk_grads<%d parts, %d rows>: grid %lld x %d threads", NP, 32 * KS,
-          static_cast<long long>(blocks), kGradThreads);
-  hipLaunchKernelGGL((delta_chunk_grads<InT, NP, KS>), dim3(static_cast<unsigned>(blocks)), dim3(kGradThreads), kBytes,
-                     stream, s);
+  constexpr int SL = split_tiles(KS), splits = grad_splits(KS);
+  constexpr int kBytes = GradLds<NP, SL>::kBytes;
+  static_assert(kBytes + 4096 <= kMaxLds, "a slab exceeds LDS");
+  const int64_t blocks = (static_cast<int64_t>(s.items) + 7) / 8 * 8 * splits;
+  SSM_LOG("launch delta_chunk_grads<%d parts, %d entries>: %d splits; grid %lld x %d threads", NP, 32 * SL, splits,
+          static_cast<long long>(blocks), kThreads);
+  hipLaunchKernelGGL((delta_chunk_grads<InT, NP, SL>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), kBytes,
+                     stream, s, splits);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t records = B * s.c.Hv * s.c.chunks, grid = (records + kWaves - 1) / kWaves;
+  SSM_LOG("launch delta_gate_grads: grid %lld x %d threads", static_cast<long long>(grid), kThreads);
+  hipLaunchKernelGGL((delta_gate_grads<InT>), dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, s, splits,
+                     records);
   return hipGetLastError();
 }
 
@@ -821,6 +832,7 @@ DeltaBwdLayout plan_delta_bwd(int64_t B, int64_t L, int Hv, int dk, int dv) {
   d.off_U = take(n * kChunk * cols * 4);
   d.off_dstates = take(n * rows * cols * 4);
   d.off_dR = take(n * kChunk * cols * 4);
+  d.off_sums = take(n * grad_splits(padded_ks(dk)) * kSumFloats * 4);
   d.off_part = take(n * 2 * 4);
   d.bytes = off;
   return d;
@@ -841,7 +853,9 @@ hipError_t launch_delta_bwd(const DeltaPlan& p, const DeltaBwdPlan& g, const Del
   s.U = U;
   s.dstates = reinterpret_cast<float*>(ws + lay.off_dstates);
   s.dR = reinterpret_cast<float*>(ws + lay.off_dR);
+  s.sums = reinterpret_cast<float*>(ws + lay.off_sums);
   s.part = reinterpret_cast<float*>(ws + lay.off_part);
+  s.items = static_cast<int>(p.B * p.Hk * lay.chunks);
   s.cols = (p.dv + 15) / 16 * 16;
   s.col_blocks = (p.dv + kBlockCols - 1) / kBlockCols;
   s.grad_bf16 = g.grad_bf16;

@@ -61,7 +61,7 @@ struct DeltaBwdPlan {
 };
 struct DeltaBwdLayout {  // workspace byte offsets
   int chunks;
-  size_t off_records, off_states, off_U, off_dstates, off_dR, off_part, bytes;
+  size_t off_records, off_states, off_U, off_dstates, off_dR, off_sums, off_part, bytes;
 };
 DeltaBwdLayout plan_delta_bwd(int64_t B, int64_t L, int Hv, int dk, int dv);
 hipError_t launch_delta_bwd(const DeltaPlan& plan, const DeltaBwdPlan& grads, const DeltaBwdLayout& layout,
