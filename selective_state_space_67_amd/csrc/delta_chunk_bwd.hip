@@ -82,7 +82,7 @@ struct RevOffsets {
 
 __device__ __forceinline__ RevOffsets rev_offsets(const ChunkArgs& a, int n_tokens, int col0, int lane, int wave) {
   RevOffsets o;
-  const int last = n_tokens - 1, row = min(wave * 16 + (lane & 15), last);
+  const int last = n_tokens - 1, row = min(wave * 16 + (swizzled(lane) & 15), last);
   o.k = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ks) * 2 + (lane >> 4) * 16;
   o.q = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.qs) * 2 + (lane >> 4) * 16;
   const int col = min(col0 + (lane & 7) * 8, a.dv - 8);
@@ -383,7 +383,7 @@ template <int NP, int TILES>
 __device__ __forceinline__ Frag<NP> slab_rows(const uint16_t* s, int tile, int lane) {
   Frag<NP> f;
 #pragma unroll
-  for (int k = 0; k < NP; ++k) f.p[k] = *reinterpret_cast<const u32x4*>(s + k * TILES * 512 + (tile * 64 + lane) * 8);
+  for (int k = 0; k < NP; ++k) f.p[k] = *reinterpret_cast<const u32x4*>(s + k * TILES * 512 + (tile * 64 + swizzled(lane)) * 8);
   return f;
 }
 template <int TILES>
@@ -391,7 +391,7 @@ __device__ __forceinline__ void store_slab(uint16_t* s, int at, int oct, const f
   const Frag<3> f = split8(x[0], x[1]);
 #pragma unroll
   for (int k = 0; k < 3; ++k)
-    *reinterpret_cast<u32x4*>(s + k * TILES * 512 + ((at >> 4) * 64 + oct * 16 + (at & 15)) * 8) = f.p[k];
+    *reinterpret_cast<u32x4*>(s + k * TILES * 512 + ((at >> 4) * 64 + swizzled(oct * 16 + (at & 15))) * 8) = f.p[k];
 }
 
 // LDS of a workgroup: the slab, and its entries of the staged tokens of K and Q, beside it
@@ -431,7 +431,8 @@ __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0)
 // One workgroup: 32 SL entries of a chunk of one key head, its value heads in turn; wave w
 // has the tokens of tile w as rows of dQ and dK. The sums over dv go in slabs of 32
 // columns, the next one's loads under way while one is multiplied.
-template <typename InT, int NP, int SL>
+// VEC: rows of dout come as whole 16-byte runs.
+template <typename InT, int NP, int SL, bool VEC>
 __global__ __launch_bounds__(kThreads, 2) void delta_chunk_grads(const BwdArgs s, int splits) {
   using Lds = GradLds<NP, SL>;
   using Tile = TokenTile<NP, SL>;
@@ -479,35 +480,34 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chunk_grads(const BwdArgs s
   for (int gi = 0; gi < a.group; ++gi) {
     const int h = hk * a.group + gi, bh = b * a.Hv + h;
     const int64_t record = static_cast<int64_t>(bh) * a.chunks + chunk;
-    const float* H0 = s.states + (record * all_rows + first) * s.cols;
-    const float* dH1 = s.dstates + (record * all_rows + first) * s.cols;
-    const float* U = s.U + (record * kChunk + row) * s.cols;
-    const float* dR = s.dR + (record * kChunk + row) * s.cols;
-    const InT* dout = static_cast<const InT*>(s.dout) + (t0 * a.Hv + h) * a.dv + row * token_v;
+    const char* H0 = reinterpret_cast<const char*>(s.states + (record * all_rows + first) * s.cols);
+    const char* dH1 = reinterpret_cast<const char*>(s.dstates + (record * all_rows + first) * s.cols);
+    const char* U = reinterpret_cast<const char*>(s.U + record * kChunk * s.cols);
+    const char* dR = reinterpret_cast<const char*>(s.dR + record * kChunk * s.cols);
+    const InT* dout_first = static_cast<const InT*>(s.dout) + (t0 * a.Hv + h) * a.dv;
+    const InT* dout = dout_first + row * token_v;
     const auto fetch = [&](SlabLoads<NP, ITEMS>& x, int d0) {
-      const int c = d0 + oct * 8;
-      const bool inside = c < limit;
-      const int at = inside ? c : 0;
+      const int c = d0 + oct * 8, from = c < limit ? c : 0;
+      const uint32_t at = static_cast<uint32_t>(row * s.cols + from) * 4;  // bytes from a uniform base
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        x.u[i] = inside ? *reinterpret_cast<const f32x4*>(U + at + 4 * i) : zero;
-        x.r[i] = inside ? *reinterpret_cast<const f32x4*>(dR + at + 4 * i) : zero;
+        x.u[i] = *reinterpret_cast<const f32x4*>(U + at + 16 * i);
+        x.r[i] = *reinterpret_cast<const f32x4*>(dR + at + 16 * i);
       }
 #pragma unroll
       for (int n = 0; n < ITEMS; ++n) {
-        const int r = min(row + n * (kThreads / 4), ROWS - 1);
+        const uint32_t at = static_cast<uint32_t>(min(row + n * (kThreads / 4), ROWS - 1) * s.cols + from) * 4;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          x.h[n][i] = inside ? *reinterpret_cast<const f32x4*>(H0 + r * s.cols + at + 4 * i) : zero;
-          x.g[n][i] = inside ? *reinterpret_cast<const f32x4*>(dH1 + r * s.cols + at + 4 * i) : zero;
+          x.h[n][i] = *reinterpret_cast<const f32x4*>(H0 + at + 16 * i);
+          x.g[n][i] = *reinterpret_cast<const f32x4*>(dH1 + at + 16 * i);
         }
       }
       const int left = row < n_tokens ? a.dv - c : 0;
-      const u32x4 none = {0, 0, 0, 0};
-      if (s.vec_out) {
+      if constexpr (VEC) {
+        const u32x4* o = reinterpret_cast<const u32x4*>(left > 0 ? dout + c : dout_first);
 #pragma unroll
-        for (int i = 0; i < (NP == 1 ? 1 : 2); ++i)
-          x.o[i] = left > 0 ? reinterpret_cast<const u32x4*>(dout + c)[i] : none;
+        for (int i = 0; i < (NP == 1 ? 1 : 2); ++i) x.o[i] = o[i];
       } else if constexpr (NP == 1) {
         uint32_t e[8];
 #pragma unroll
@@ -520,7 +520,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chunk_grads(const BwdArgs s
     };
     SlabLoads<NP, ITEMS> loads;
     fetch(loads, 0);
-    __syncthreads();  // the previous head's scalars and tiles are used
+    __syncthreads();  // the previous head's scalars are used
 #pragma unroll
     for (int i = 0; i < kGateFloatsBwd / kThreads; ++i)
       scalars[i * kThreads + threadIdx.x] =
@@ -529,13 +529,24 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chunk_grads(const BwdArgs s
     f32x4 E1[MT], E2[MT], E3[MT];  // dO H0^T, dR H0^T, U dH1^T: rows of tile w, columns of the state tiles
 #pragma unroll
     for (int m = 0; m < MT; ++m) E1[m] = E2[m] = E3[m] = zero;
-    // U dO^T and U dR^T (rows of tile j <= w, columns w); dO U^T and dR U^T (rows of tile j >= w, columns w)
-    f32x4 Pc[4] = {zero, zero, zero, zero}, Sc[4] = {zero, zero, zero, zero};
-    f32x4 Pr[4] = {zero, zero, zero, zero}, Sr[4] = {zero, zero, zero, zero};
+    // Columns of tile w: rows of tile j < w of U dO^T and U dR^T, rows of tile j >= w of dO U^T
+    // and dR U^T; and, apart, tile w of the first two
+    f32x4 P[4] = {zero, zero, zero, zero}, S[4] = {zero, zero, zero, zero}, Pw = zero, Sw = zero;
     float hh = 0.0f;  // the thread's part of <dH1, H0>
+#pragma unroll 1
     for (int d0 = 0; d0 < a.dv; d0 += 32) {
-      if (d0 > 0) __syncthreads();  // the last slab is read
-      uint16_t* to = sdO + ((row >> 4) * 64 + oct * 16 + (row & 15)) * 8;
+      __syncthreads();  // the last slab is read, or the previous head's tiles
+      // Rows past the chunk's and columns past the head's were loaded from the first ones.
+      const bool inside = d0 + oct * 8 < limit;
+      if (!inside || row >= n_tokens) {
+        for (u32x4& x : loads.o) x = u32x4{0, 0, 0, 0};
+      }
+      if (!inside) {
+        loads.u[0] = loads.u[1] = loads.r[0] = loads.r[1] = zero;
+#pragma unroll
+        for (int n = 0; n < ITEMS; ++n) loads.h[n][0] = loads.h[n][1] = loads.g[n][0] = loads.g[n][1] = zero;
+      }
+      uint16_t* to = sdO + ((row >> 4) * 64 + swizzled(oct * 16 + (row & 15))) * 8;
       if constexpr (NP == 1) {
         *reinterpret_cast<u32x4*>(to) = loads.o[0];
       } else {
@@ -570,38 +581,41 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chunk_grads(const BwdArgs s
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (j <= w) {
+        if (j < w) {
           const Frag<3> Uj = slab_rows<3, 4>(sU, j, lane);
-          Pc[j] = mma(Uj, dOw, Pc[j]);
-          Sc[j] = mma(Uj, dRw, Sc[j]);
-        }
-        if (j >= w) {
-          Pr[j] = mma(slab_rows<NP, 4>(sdO, j, lane), Uw, Pr[j]);
-          Sr[j] = mma(slab_rows<3, 4>(sdR, j, lane), Uw, Sr[j]);
+          P[j] = mma(Uj, dOw, P[j]);
+          S[j] = mma(Uj, dRw, S[j]);
+        } else {
+          P[j] = mma(slab_rows<NP, 4>(sdO, j, lane), Uw, P[j]);
+          S[j] = mma(slab_rows<3, 4>(sdR, j, lane), Uw, S[j]);
         }
         keep_order();
       }
+      Pw = mma(Uw, dOw, Pw);
+      Sw = mma(Uw, dRw, Sw);
     }
 
     // d beta comes from the diagonal of dR U^T, and dP's is set aside; then the decays and masks.
     float* sums = s.sums + (record * splits + split) * kSumFloats;
     const ColDecay cw = col_decay(scalars, w * 16 + col);
+    if ((col >> 2) == (lane >> 4)) {
+      const int r = col & 3;
+      sums[kSumBeta + w * 16 + col] = r == 0 ? Sw.x : r == 1 ? Sw.y : r == 2 ? Sw.z : Sw.w;
+      diag_dP[w * 16 + col] = a.scale * (r == 0 ? Pw.x : r == 1 ? Pw.y : r == 2 ? Pw.z : Pw.w);
+    }
+    // of rows of tile j: those before the columns (up), and those after them, which stay in P and S
+    f32x4 Pc[4], Sc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (j == w && (col >> 2) == (lane >> 4)) {
-        const int r = col & 3;
-        sums[kSumBeta + w * 16 + col] = r == 0 ? Sc[j].x : r == 1 ? Sc[j].y : r == 2 ? Sc[j].z : Sc[j].w;
-        diag_dP[w * 16 + col] = a.scale * (r == 0 ? Pc[j].x : r == 1 ? Pc[j].y : r == 2 ? Pc[j].z : Pc[j].w);
-      }
       const RowDecay rows = row_decay(scalars, j * 16 + g4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int x = j * 16 + g4 + r, y = w * 16 + col;
         const float up = x < y ? decay_up(rows, r, cw) : 0.0f, down = x > y ? decay_down(rows, r, cw) : 0.0f;
-        Pc[j][r] *= a.scale * up;
-        Sc[j][r] *= -cw.beta * up;
-        Pr[j][r] *= a.scale * down;
-        Sr[j][r] *= -rows.beta[r] * down;
+        Pc[j][r] = (j == w ? Pw[r] : P[j][r]) * (a.scale * up);
+        Sc[j][r] = (j == w ? Sw[r] : S[j][r]) * (-cw.beta * up);
+        P[j][r] *= a.scale * down;
+        S[j][r] *= -rows.beta[r] * down;
       }
     }
     const f32x4 e0 = *reinterpret_cast<const f32x4*>(scalars + kE0 + w * 16 + g4);
@@ -609,37 +623,55 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chunk_grads(const BwdArgs s
     const f32x4 be = *reinterpret_cast<const f32x4*>(scalars + kBeta + w * 16 + g4);
     // of the lane's four tokens, its columns' part: q . dq + k . (i side - j side), and k . eC (U dH1^T)
     f32x4 own = zero, ku = zero;
-    const Frag<3> ap[2] = {split8(Pc[0], Pc[1]), split8(Pc[2], Pc[3])};
-    const Frag<3> as[2] = {split8(Sc[0], Sc[1]), split8(Sc[2], Sc[3])};
-    const Frag<3> bp[2] = {split8(Pr[0], Pr[1]), split8(Pr[2], Pr[3])};
-    const Frag<3> bs[2] = {split8(Sr[0], Sr[1]), split8(Sr[2], Sr[3])};
     __syncthreads();  // the slab is read, the diagonal is set
     if constexpr (!Lds::kBeside) {
       stage_qk();
       __syncthreads();
     }
     const f32x4 dp = *reinterpret_cast<const f32x4*>(&diag_dP[w * 16 + g4]);
+    {  // what the tokens take from those before them, and the state's end
+      const Frag<3> ap[2] = {split8(Pc[0], Pc[1]), split8(Pc[2], Pc[3])};
+      const Frag<3> as[2] = {split8(Sc[0], Sc[1]), split8(Sc[2], Sc[3])};
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      E1[m] *= a.scale * e0;
-      E2[m] *= -be * e0;
-      E3[m] *= eC;
-      f32x4 x = zero, y = zero, kv = zero, qv = zero;
+      for (int m = 0; m < MT; ++m) {
+        E1[m] *= a.scale * e0;
+        E2[m] *= -be * e0;
+        E3[m] *= eC;
+        f32x4 kv = zero, qv = zero;
 #pragma unroll
-      for (int ts = 0; ts < 2; ++ts) {
-        const Frag<NP> kc = Tile::columns(sk, m, ts, lane), qc = Tile::columns(sq, m, ts, lane);
-        if (ts == w / 2) {
-          kv = column_values(kc, w);
-          qv = column_values(qc, w);
+        for (int ts = 0; ts < 2; ++ts) {
+          if (ts > w / 2) continue;
+          const Frag<NP> kc = Tile::columns(sk, m, ts, lane);
+          if (ts == w / 2) {
+            kv = column_values(kc, w);
+            qv = column_values(Tile::columns(sq, m, ts, lane), w);
+          }
+          mma_pair(ap[ts], kc, E1[m], as[ts], kc, E2[m]);
         }
-        if (ts <= w / 2) mma_pair(ap[ts], kc, E1[m], as[ts], kc, E2[m]);
-        if (ts >= w / 2) mma_pair(bs[ts], kc, x, bp[ts], qc, y);
+        ku += kv * E3[m];
+        own += qv * E1[m] + kv * E2[m];
+        dq_sum[m] += E1[m] + dp * kv;
+        dk_sum[m] += (E2[m] + E3[m]) + dp * qv;
+        keep_order();
       }
-      ku += kv * E3[m];
-      own += qv * E1[m] + kv * ((E2[m] - x) - y);
-      dq_sum[m] += E1[m] + dp * kv;
-      dk_sum[m] += ((E2[m] + E3[m]) + x) + (y + dp * qv);
-      keep_order();
+    }
+    {  // what they give to those after them
+      const Frag<3> bp[2] = {split8(P[0], P[1]), split8(P[2], P[3])};
+      const Frag<3> bs[2] = {split8(S[0], S[1]), split8(S[2], S[3])};
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x4 x = zero, y = zero, kv = zero;
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts) {
+          if (ts < w / 2) continue;
+          const Frag<NP> kc = Tile::columns(sk, m, ts, lane);
+          if (ts == w / 2) kv = column_values(kc, w);
+          mma_pair(bs[ts], kc, x, bp[ts], Tile::columns(sq, m, ts, lane), y);
+        }
+        own -= kv * (x + y);
+        dk_sum[m] += x + y;
+        keep_order();
+      }
     }
     // sums over the 16 columns' lanes, and over the workgroup
 #pragma unroll
@@ -778,8 +810,11 @@ hipError_t launch_grads(const BwdArgs& s, int64_t B, hipStream_t stream) {
   const int64_t blocks = (static_cast<int64_t>(s.items) + 7) / 8 * 8 * splits;
   SSM_LOG("launch delta_chunk_grads<%d parts, %d entries>: %d splits; grid %lld x %d threads", NP, 32 * SL, splits,
           static_cast<long long>(blocks), kThreads);
-  hipLaunchKernelGGL((delta_chunk_grads<InT, NP, SL>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), kBytes,
-                     stream, s, splits);
+  const dim3 grid_dim(static_cast<unsigned>(blocks));
+  if (s.vec_out)
+    hipLaunchKernelGGL((delta_chunk_grads<InT, NP, SL, true>), grid_dim, dim3(kThreads), kBytes, stream, s, splits);
+  else
+    hipLaunchKernelGGL((delta_chunk_grads<InT, NP, SL, false>), grid_dim, dim3(kThreads), kBytes, stream, s, splits);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t records = B * s.c.Hv * s.c.chunks, grid = (records + kWaves - 1) / kWaves;

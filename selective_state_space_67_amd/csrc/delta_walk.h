@@ -90,7 +90,7 @@ struct LaneOffsets {
 
 __device__ __forceinline__ LaneOffsets lane_offsets(const ChunkArgs& a, int n_tokens, int col0, int lane, int wave) {
   LaneOffsets o;
-  const int last = n_tokens - 1, row = min(wave * 16 + (lane & 15), last);  // wave w: row tile w
+  const int last = n_tokens - 1, row = min(wave * 16 + (swizzled(lane) & 15), last);  // wave w: row tile w
   o.k = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ks) * 2 + (lane >> 4) * 16;
   o.q = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.qs) * 2 + (lane >> 4) * 16;
   const int col = max(0, min(col0 + (lane & 7) * 8, a.dv - 8));
