@@ -139,8 +139,14 @@ ssm::DeltaPlan delta_plan(const P* p, int64_t len, const DeltaSizes& s) {
   return d;
 }
 
-// Sequences up to this long go step by step, unless pieces are asked for.
-constexpr int64_t kStepsMax = 32;
+// Sequences up to this long go step by step, unless pieces are asked for. The steps take
+// the longer the more there are, a chunk about the same time however few of its 64 tokens
+// are there. bfloat16, 128 x 128 states, 1 x 16 heads: 13.6, 17.4, 21.0 us at 12, 16, 20
+// steps against 17.7 in chunks (8 x 12 heads: 14.4, 18.1, 21.8 against 20.0; 64 x 16: 58.5,
+// 73.2, 89.0 against 104). float32, whose chunks take three times the products: 23.6 and
+// 30.8 us at 24 and 32 steps against 31.6 (8 x 12: 24.5, 31.2 against 38; 64 x 16: 101, 132
+// against 243).
+constexpr int64_t steps_max(int in_dtype) { return in_dtype == SSM_BF16 ? 16 : 32; }
 
 // One workgroup for every chunk, and at most a workgroup for every 16 columns.
 ssm_status check_grid(int64_t batch, int64_t seqlen, int64_t heads, int64_t dv) {
@@ -156,7 +162,7 @@ ssm_status check_grid(int64_t batch, int64_t seqlen, int64_t heads, int64_t dv) 
 ssm_status plan_delta(const ssm_delta_params* p, const DeltaSizes& s, ssm::DeltaChunks* plan) {
   if (p->num_segments < 0) return fail(SSM_ERR_BAD_SHAPE, "num_segments must be >= 0");
   *plan = ssm::DeltaChunks{};
-  if (s.empty() || (p->seqlen <= kStepsMax && p->num_segments <= 1)) return SSM_OK;
+  if (s.empty() || (p->seqlen <= steps_max(p->in_dtype) && p->num_segments <= 1)) return SSM_OK;
   const ssm_status st = check_grid(p->batch, p->seqlen, p->value_heads, p->dv);
   if (st != SSM_OK) return st;
   *plan = ssm::plan_delta_chunks(p->batch, p->seqlen, static_cast<int>(p->value_heads), static_cast<int>(p->dk),
