@@ -159,6 +159,14 @@ __device__ __forceinline__ void stage_sync(char* st, const ChunkArgs& a, const C
 }
 
 // One wave's walk over the chunks of a piece with 16 columns of the state.
+//
+// Bound by the chain of dependent steps of a chunk: K H0, R, T R, P U and K^T U follow
+// one another, and a workgroup has a wave for every SIMD of its CU and no second one to
+// fill its waits (8 x 2048 x 12 heads of 128 x 128 give 192 workgroups for 256 CUs, and the
+// two staged chunks of one take 142 KB of LDS). A chunk takes 4.2 us, about 10000 cycles,
+// 2900 of them matrix instructions: 155 us for that call, 1.6 TB/s of inputs, records and
+// outputs. The 16 columns a wave are what one operand of the matrix instruction holds: more
+// of them would share the operands of K, Q, T and P, but leave fewer waves than SIMDs.
 // AGG: the aggregates walk (no read-out; the first 32 KS columns start from the
 // identity). With two stages the next chunk is loaded while this one is worked on.
 // OP: parts of the products that only the output sees; two (2^-17) where it is
