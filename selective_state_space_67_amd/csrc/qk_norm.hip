@@ -291,14 +291,23 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd(const NormArgs a) {
 }
 
 // dwq and dwk from the workgroups' rows: 16 entries a workgroup, 16 threads an
-// entry, each adding every 16th row in order, then the 16 sums in order.
+// entry, each adding every 16th row in order, then the 16 sums in order. A thread has
+// eight rows under way: one at a time, 1024 rows took 20 us, a fifth of the backward.
 __global__ __launch_bounds__(kThreads) void qk_norm_reduce(const float* __restrict__ part, float* dwq, float* dwk,
                                                            int rows, int d) {
+  constexpr int kAhead = 8;
   __shared__ float t[16][17];
   const int col = threadIdx.x % 16, by = threadIdx.x / 16, e = blockIdx.x * 16 + col;
   float x = 0.0f;
   if (e < 2 * d)
-    for (int r = by; r < rows; r += 16) x += part[static_cast<int64_t>(r) * 2 * d + e];
+    for (int r = by; r < rows; r += 16 * kAhead) {
+      float row[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        row[i] = r + 16 * i < rows ? part[static_cast<int64_t>(r + 16 * i) * 2 * d + e] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) x += row[i];
+    }
   t[by][col] = x;
   __syncthreads();
   if (by != 0 || e >= 2 * d) return;
