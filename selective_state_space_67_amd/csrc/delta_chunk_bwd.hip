@@ -37,6 +37,7 @@ constexpr int kBlockCols = 16 * kWaves;
 struct BwdArgs {
   ChunkArgs c;
   int col_blocks, cols;
+  int heads;             // batch rows x value heads
   int items;             // chunks of all key heads
   int grad_bf16;
   bool vec_out;          // rows of dout come as whole 16-byte runs
@@ -148,7 +149,9 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
   extern __shared__ __align__(16) char staged[];
   const ChunkArgs& a = s.c;
   const int lane = threadIdx.x % 64, wave = wave_index(), g4 = (lane >> 4) * 4;
-  const int cb = blockIdx.x % s.col_blocks, bh = blockIdx.x / s.col_blocks;
+  const Place place = place_of(blockIdx.x, s.col_blocks);
+  const int cb = place.part, bh = place.item;
+  if (bh >= s.heads) return;
   const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / a.group;
   const int col0 = cb * kBlockCols, own = col0 + wave * 16 + (lane & 15);
   const bool has_v = own < a.dv;
@@ -453,10 +456,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chunk_grads(const BwdArgs s
   const ChunkArgs& a = s.c;
   const int lane = threadIdx.x % 64, w = wave_index();
   const int g4 = (lane >> 4) * 4, col = lane & 15;
-  // The splits of a chunk, which read the same U, dR and dO, are 8 workgroups apart: workgroups
-  // go round the 8 dies in turn, so they share a die's L2.
-  const int eights = blockIdx.x / (8 * splits), in = blockIdx.x - eights * 8 * splits;
-  const int split = in / 8, item = eights * 8 + in % 8;
+  const Place place = place_of(blockIdx.x, splits);  // the splits of a chunk read the same U, dR and dO
+  const int split = place.part, item = place.item;
   if (item >= s.items) return;
   const int chunk = item % a.chunks, bhk = item / a.chunks;
   const int b = bhk / a.Hk, hk = bhk - b * a.Hk;
@@ -799,12 +800,12 @@ __global__ __launch_bounds__(kThreads) void delta_head_sums(const float* __restr
 }
 
 template <typename InT, int NP, int KS, bool ASYNC>
-hipError_t launch_reverse(const BwdArgs& s, int64_t heads, hipStream_t stream) {
+hipError_t launch_reverse(const BwdArgs& s, hipStream_t stream) {
   constexpr bool BOTH = RevStage<InT, NP, KS, true>::kBytes <= kMaxLds;
   constexpr int kBytes = RevStage<InT, NP, KS, BOTH>::kBytes;
   constexpr int STAGES = ASYNC && 2 * kBytes <= kMaxLds ? 2 : 1;
   static_assert(kBytes <= kMaxLds && (BOTH || !ASYNC), "a chunk's stage exceeds LDS");
-  const int64_t blocks = heads * s.col_blocks;
+  const int64_t blocks = placed_blocks(s.heads, s.col_blocks);
   SSM_LOG("launch delta_chunk_reverse<%d parts, %d rows>: %d chunks, %d stages of %d bytes; grid %lld x %d threads", NP,
           32 * KS, s.c.chunks, STAGES, kBytes, static_cast<long long>(blocks), kThreads);
   hipLaunchKernelGGL((delta_chunk_reverse<InT, NP, KS, BOTH, ASYNC, STAGES>), dim3(static_cast<unsigned>(blocks)),
@@ -817,7 +818,7 @@ hipError_t launch_grads(const BwdArgs& s, int64_t B, hipStream_t stream) {
   constexpr int SL = split_tiles(KS), splits = grad_splits(KS);
   constexpr int kBytes = GradLds<NP, SL>::kBytes;
   static_assert(kBytes + 4096 <= kMaxLds, "a slab exceeds LDS");
-  const int64_t blocks = (static_cast<int64_t>(s.items) + 7) / 8 * 8 * splits;
+  const int64_t blocks = placed_blocks(s.items, splits);
   SSM_LOG("launch delta_chunk_grads<%d parts, %d entries>: %d splits; grid %lld x %d threads", NP, 32 * SL, splits,
           static_cast<long long>(blocks), kThreads);
   const dim3 grid_dim(static_cast<unsigned>(blocks));
@@ -836,12 +837,11 @@ hipError_t launch_grads(const BwdArgs& s, int64_t B, hipStream_t stream) {
 
 template <typename InT, int NP, int KS>
 hipError_t launch_both(const BwdArgs& s, int64_t B, bool direct, hipStream_t stream) {
-  const int64_t heads = B * s.c.Hv;
   hipError_t e;
   if constexpr (NP == 1)
-    e = direct ? launch_reverse<InT, NP, KS, true>(s, heads, stream) : launch_reverse<InT, NP, KS, false>(s, heads, stream);
+    e = direct ? launch_reverse<InT, NP, KS, true>(s, stream) : launch_reverse<InT, NP, KS, false>(s, stream);
   else
-    e = launch_reverse<InT, NP, KS, false>(s, heads, stream);
+    e = launch_reverse<InT, NP, KS, false>(s, stream);
   return e == hipSuccess ? launch_grads<InT, NP, KS>(s, B, stream) : e;
 }
 
@@ -900,6 +900,7 @@ hipError_t launch_delta_bwd(const DeltaPlan& p, const DeltaBwdPlan& g, const Del
   s.dR = reinterpret_cast<float*>(ws + lay.off_dR);
   s.sums = reinterpret_cast<float*>(ws + lay.off_sums);
   s.part = reinterpret_cast<float*>(ws + lay.off_part);
+  s.heads = static_cast<int>(p.B * p.Hv);
   s.items = static_cast<int>(p.B * p.Hk * lay.chunks);
   s.cols = (p.dv + 15) / 16 * 16;
   s.col_blocks = (p.dv + kBlockCols - 1) / kBlockCols;

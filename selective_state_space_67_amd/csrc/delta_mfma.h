@@ -38,6 +38,20 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // compiler knows to be uniform; a mask would not keep it from running.
 __device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
+// Workgroups go round the 8 dies in turn, each with an L2 of its own: the parts of an
+// item, which read the same tokens and records, are 8 apart and share one. (With the parts
+// next to each other the walk of 8 x 2048 x 12 heads fetched 426 MB, so 237; its reverse 462
+// and 255.)
+constexpr int kDies = 8;
+struct Place {
+  int item, part;  // item: may be past the last one
+};
+__device__ __forceinline__ Place place_of(int block, int parts) {
+  const int round = block / (kDies * parts), in = block - round * kDies * parts;
+  return {round * kDies + in % kDies, in / kDies};
+}
+inline int64_t placed_blocks(int64_t items, int parts) { return (items + kDies - 1) / kDies * kDies * parts; }
+
 // An operand of one product: NP parts of 8 entries.
 template <int NP>
 struct Frag {

@@ -15,7 +15,8 @@ enum Walk { kOutputs, kAggregates, kStates };
 struct ScanArgs {
   ChunkArgs c;
   int pieces, chunks_piece;
-  int col_blocks;   // workgroups per (head, piece)
+  int items;        // heads x pieces
+  int col_blocks;   // workgroups per item
   int out_bf16, out_runs;  // out_runs: rows of out take whole 16-byte runs
   const float* h0;  // (bh, dk, dv) or null
   const float* starts;  // states of pieces 1 .. (bh, piece, 32 KS, cols), or null
@@ -180,8 +181,9 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
   extern __shared__ __align__(16) char staged[];
   const ChunkArgs& a = s.c;
   const int lane = threadIdx.x % 64, wave = wave_index(), g4 = (lane >> 4) * 4;
-  const int cb = blockIdx.x % s.col_blocks, rest = blockIdx.x / s.col_blocks;
-  const int piece = rest % s.pieces, bh = rest / s.pieces;
+  const Place place = place_of(blockIdx.x, s.col_blocks);
+  if (place.item >= s.items) return;
+  const int cb = place.part, piece = place.item % s.pieces, bh = place.item / s.pieces;
   const int b = bh / a.Hv, h = bh - b * a.Hv;
   const int strip = cb * kWaves + wave;                            // 16-column strip
   const int col0 = (cb * kWaves - (AGG ? DKT : 0)) * 16;           // the workgroup's first column of v
@@ -423,16 +425,17 @@ template <typename InT, int NP, int KS, bool ASYNC>
 hipError_t launch_scan_ks(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs s, hipStream_t stream) {
   // K and Q of a chunk side by side fit in LDS except for float32 past 128 entries
   constexpr bool QLDS = Stage<InT, NP, KS, kOutputs, true, 3>::kBytes <= kMaxLds;
-  const int64_t heads = p.B * p.Hv;
+  const int64_t items = p.B * p.Hv * plan.pieces;
+  s.items = static_cast<int>(items);
   if (plan.pieces > 1) {
     const int strips = 2 * KS + s.cols / 16;
     s.col_blocks = (strips + kWaves - 1) / kWaves;
-    hipError_t e = launch_walk<InT, NP, KS, kAggregates, QLDS, ASYNC, 3>(s, heads * plan.pieces * s.col_blocks, stream);
+    hipError_t e = launch_walk<InT, NP, KS, kAggregates, QLDS, ASYNC, 3>(s, placed_blocks(items, s.col_blocks), stream);
     if (e != hipSuccess) return e;
     if ((e = launch_delta_fold(p, plan, s, stream)) != hipSuccess) return e;
   }
   s.col_blocks = (s.cols / 16 + kWaves - 1) / kWaves;
-  const int64_t blocks = heads * plan.pieces * s.col_blocks;
+  const int64_t blocks = placed_blocks(items, s.col_blocks);
   if (s.states) return launch_walk<InT, NP, KS, kStates, QLDS, ASYNC, 3>(s, blocks, stream);
   if (NP == 1 && s.out_bf16) return launch_walk<InT, NP, KS, kOutputs, QLDS, ASYNC, NP == 1 ? 2 : 3>(s, blocks, stream);
   return launch_walk<InT, NP, KS, kOutputs, QLDS, ASYNC, 3>(s, blocks, stream);
