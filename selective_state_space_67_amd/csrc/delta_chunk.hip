@@ -21,6 +21,7 @@
 // are a walk from the identity without values); delta_fold carries the state
 // across the pieces, and the full walk starts every piece from its own state.
 #include <algorithm>
+#include <cmath>
 
 #include "delta_walk.h"
 
@@ -253,27 +254,42 @@ hipError_t prepare_f32(const ChunkArgs& a, int64_t blocks, bool bwd, hipStream_t
 // The states that pieces 1 .. start from: S <- M S + N over the pieces, 16 columns
 // and all rows a workgroup, its waves sharing the rows. The next piece's
 // operands are loaded before the current ones are used. A chain over the pieces, bound by
-// reading M: 2.4 us a piece of 128 x 128 (64 pieces on 2 heads 152 us, of a call of
-// 600). Loads two pieces ahead changed nothing.
+// reading M: 2.4 us a piece of 128 x 128 (64 pieces on 2 heads 152 us). Loads two pieces
+// ahead changed nothing.
+//
+// Many pieces are therefore folded in groups: COMPOSE makes each group's (M, N) from its
+// pieces', from the identity for M and zero for N; the fold over the groups gives the
+// states that they start from; and a fold inside every group the pieces'. (64 pieces on 2
+// heads in 8 groups: 19 + 17 + 19 us; the call 591 -> 490.)
 struct FoldArgs {
-  const float* agg;
-  const float* h0;
-  float* starts;
-  int pieces, dk, dv, cols, strips;
+  const float* agg;     // (bh, pieces, ROWS, ROWS + cols)
+  const float* h0;      // of group 0, (bh, dk, dv) or null
+  const float* from;    // of groups 1 .., (bh, groups, ROWS, cols)
+  float* out;           // (bh, pieces, ROWS, cols); COMPOSE: (bh, groups, ROWS, ROWS + cols)
+  int pieces, groups, group_pieces;
+  int dk, dv, cols, strips;
 };
 
-template <int KS>
+template <int KS, bool COMPOSE>
 __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
   constexpr int ROWS = 32 * KS;
   __shared__ u32x4 S[2][KS][3][64];  // the state as B operand, two pieces in turn
   const int lane = threadIdx.x % 64, w = wave_index(), g4 = (lane >> 4) * 4;  // wave w: row tile w
-  const int bh = blockIdx.x / a.strips, own = (blockIdx.x - bh * a.strips) * 16 + (lane & 15);
+  const int strip = blockIdx.x % a.strips, chain = blockIdx.x / a.strips;
+  const int group = chain % a.groups, bh = chain / a.groups;
+  const int first = group * a.group_pieces, last = min(first + a.group_pieces, a.pieces);
   const int width = ROWS + a.cols;
+  const int at = strip * 16 + (lane & 15) + (COMPOSE ? 0 : ROWS), own = at - ROWS;  // own < 0: a column of M
   f32x4 H;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int row = state_row(w, g4, r);
-    H[r] = a.h0 && row < a.dk && own < a.dv ? a.h0[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own] : 0.0f;
+    if (COMPOSE)
+      H[r] = row == at ? 1.0f : 0.0f;
+    else if (group > 0)
+      H[r] = a.from[((static_cast<int64_t>(bh) * a.groups + group) * ROWS + row) * a.cols + own];
+    else
+      H[r] = a.h0 && row < a.dk && own < a.dv ? a.h0[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own] : 0.0f;
   }
   const float* M = a.agg + static_cast<int64_t>(bh) * a.pieces * ROWS * width;
   f32x4 m[KS][2], n;
@@ -286,10 +302,17 @@ __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
       m[ks][1] = *reinterpret_cast<const f32x4*>(row + 32 * ks + 4);
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) n[r] = p[static_cast<int64_t>(state_row(w, g4, r)) * width + ROWS + own];
+    for (int r = 0; r < 4; ++r) n[r] = own >= 0 ? p[static_cast<int64_t>(state_row(w, g4, r)) * width + at] : 0.0f;
   };
-  fetch(0);
-  for (int piece = 0; piece + 1 < a.pieces; ++piece) {
+  const auto store = [&](int piece) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      a.out[((static_cast<int64_t>(bh) * a.pieces + piece) * ROWS + state_row(w, g4, r)) * a.cols + own] = H[r];
+  };
+  if (!COMPOSE && group > 0) store(first);
+  const int end = COMPOSE ? last : last - 1;  // the last piece's own effect is the full walk's
+  if (first < end) fetch(first);
+  for (int piece = first; piece < end; ++piece) {
     // half of operand w / 2: the wave's rows are its slots 4 (w % 2) ..
     uint32_t lo[3], hi[3];
     split_pair(H.x, H.y, lo);
@@ -302,7 +325,7 @@ __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) mf[ks] = split8(m[ks][0], m[ks][1]);
     H = n;
-    if (piece + 2 < a.pieces) fetch(piece + 1);
+    if (piece + 1 < end) fetch(piece + 1);
     __syncthreads();  // one barrier a piece: the other buffer was last read before the previous one
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -311,18 +334,40 @@ __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
       for (int i = 0; i < 3; ++i) sb.p[i] = S[buf][ks][i][lane];
       H = mma(mf[ks], sb, H);
     }
+    if (!COMPOSE) store(piece + 1);
+  }
+  if (COMPOSE) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      a.starts[((static_cast<int64_t>(bh) * a.pieces + piece + 1) * ROWS + state_row(w, g4, r)) * a.cols + own] = H[r];
+      a.out[((static_cast<int64_t>(bh) * a.groups + group) * ROWS + state_row(w, g4, r)) * width + at] = H[r];
   }
 }
 
-template <int KS>
-hipError_t fold_ks(const FoldArgs& f, int64_t heads, hipStream_t stream) {
-  SSM_LOG("launch delta_fold<%d rows>: %d pieces; grid %lld x %d threads", 32 * KS, f.pieces,
-          static_cast<long long>(heads * f.strips), 2 * KS * 64);
-  hipLaunchKernelGGL((delta_fold<KS>), dim3(static_cast<unsigned>(heads * f.strips)), dim3(2 * KS * 64), 0, stream, f);
+template <int KS, bool COMPOSE>
+hipError_t launch_fold(FoldArgs f, int64_t heads, hipStream_t stream) {
+  f.strips = f.cols / 16 + (COMPOSE ? 2 * KS : 0);
+  const int64_t blocks = heads * f.groups * f.strips;
+  SSM_LOG("launch delta_fold<%d rows, compose %d>: %d pieces in %d groups; grid %lld x %d threads", 32 * KS, COMPOSE,
+          f.pieces, f.groups, static_cast<long long>(blocks), 2 * KS * 64);
+  hipLaunchKernelGGL((delta_fold<KS, COMPOSE>), dim3(static_cast<unsigned>(blocks)), dim3(2 * KS * 64), 0, stream, f);
   return hipGetLastError();
+}
+
+template <int KS>
+hipError_t fold_ks(const FoldArgs& all, float* group_agg, float* group_starts, int64_t heads, hipStream_t stream) {
+  if (all.groups > 1) {
+    FoldArgs f = all;
+    f.out = group_agg;
+    hipError_t e = launch_fold<KS, true>(f, heads, stream);
+    if (e != hipSuccess) return e;
+    f = all;
+    f.agg = group_agg;
+    f.out = group_starts;
+    f.pieces = f.group_pieces = all.groups;
+    f.groups = 1;
+    if ((e = launch_fold<KS, false>(f, heads, stream)) != hipSuccess) return e;
+  }
+  return launch_fold<KS, false>(all, heads, stream);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -330,15 +375,25 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 hipError_t launch_delta_fold(const DeltaPlan& p, const DeltaChunks& plan, const ScanArgs& s, hipStream_t stream) {
-  const FoldArgs f{s.agg, s.h0, const_cast<float*>(s.starts), plan.pieces, p.dk, p.dv, s.cols, s.cols / 16};
+  FoldArgs f{};
+  f.agg = s.agg;
+  f.h0 = s.h0;
+  f.from = s.group_starts;
+  f.out = const_cast<float*>(s.starts);
+  f.pieces = plan.pieces;
+  f.groups = plan.groups;
+  f.group_pieces = plan.group_pieces;
+  f.dk = p.dk;
+  f.dv = p.dv;
+  f.cols = s.cols;
   const int64_t heads = p.B * p.Hv;
   switch (padded_ks(p.dk)) {
-    case 1: return fold_ks<1>(f, heads, stream);
-    case 2: return fold_ks<2>(f, heads, stream);
-    case 3: return fold_ks<3>(f, heads, stream);
-    case 4: return fold_ks<4>(f, heads, stream);
-    case 6: return fold_ks<6>(f, heads, stream);
-    default: return fold_ks<8>(f, heads, stream);
+    case 1: return fold_ks<1>(f, s.group_agg, s.group_starts, heads, stream);
+    case 2: return fold_ks<2>(f, s.group_agg, s.group_starts, heads, stream);
+    case 3: return fold_ks<3>(f, s.group_agg, s.group_starts, heads, stream);
+    case 4: return fold_ks<4>(f, s.group_agg, s.group_starts, heads, stream);
+    case 6: return fold_ks<6>(f, s.group_agg, s.group_starts, heads, stream);
+    default: return fold_ks<8>(f, s.group_agg, s.group_starts, heads, stream);
   }
 }
 
@@ -352,11 +407,15 @@ hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd
 
 namespace {
 
+// Up to this many pieces are folded one after another, more in groups.
+constexpr int kFoldAlone = 16;
+
 // Pieces that cost least, in units of a chunk's step of the full walk (4.2 us at 128 x
 // 128): rounds of one workgroup a CU times the chunks of a piece, where a step of the
 // aggregates' walk, which has a workgroup for every 64 of dk + dv columns, takes 0.7;
-// a piece's fold takes 0.7; and two more launches. Measured at 128 x 128: 2 heads of 131072
-// steps 9356 us in one piece, 16 heads x 2 of 4096 310 us, 12 x 8 of 2048 211 us (406 in
+// a piece's fold takes 0.7 (of three folds over the root of the pieces, where there are
+// groups); and two more launches. Measured at 128 x 128: 2 heads of 131072
+// steps 9356 us in one piece, 490 in 64; 16 heads x 2 of 4096 310 us, 244 in 4; 12 x 8 of 2048 211 us (406 in
 // two: the grid is full as it is).
 int choose_pieces(int64_t heads, int chunks, int dk, int dv) {
   constexpr int64_t kCUs = 256;
@@ -366,8 +425,9 @@ int choose_pieces(int64_t heads, int chunks, int dk, int dv) {
   double least = static_cast<double>(chunks) * static_cast<double>((walk + kCUs - 1) / kCUs);
   for (int n = 2; n <= std::min(chunks / 2, 256); ++n) {
     const int steps = (chunks + n - 1) / n;
+    const double fold = 0.7 * (n > kFoldAlone ? 3.0 * std::sqrt(static_cast<double>(n)) : n) + (n > kFoldAlone ? 2.0 : 0.0);
     const double cost = steps * (static_cast<double>((walk * n + kCUs - 1) / kCUs) +
-                                 0.7 * static_cast<double>((agg * n + kCUs - 1) / kCUs)) + 0.7 * n + 3.0;
+                                 0.7 * static_cast<double>((agg * n + kCUs - 1) / kCUs)) + fold + 3.0;
     if (cost < least) {
       least = cost;
       best = n;
@@ -394,6 +454,19 @@ DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int 
   if (d.pieces > 1) off += align256(piece_heads * rows * (rows + cols) * sizeof(float));
   d.off_starts = off;
   if (d.pieces > 1) off += align256(piece_heads * rows * cols * sizeof(float));
+  // groups of about the root of the pieces, from where three folds are shorter than one
+  d.groups = 1;
+  d.group_pieces = d.pieces;
+  if (d.pieces > kFoldAlone) {
+    d.group_pieces = 1;
+    while (d.group_pieces * d.group_pieces < d.pieces) ++d.group_pieces;
+    d.groups = (d.pieces + d.group_pieces - 1) / d.group_pieces;
+  }
+  const size_t group_heads = static_cast<size_t>(B) * Hv * d.groups;
+  d.off_group_agg = off;
+  if (d.groups > 1) off += align256(group_heads * rows * (rows + cols) * sizeof(float));
+  d.off_group_starts = off;
+  if (d.groups > 1) off += align256(group_heads * rows * cols * sizeof(float));
   d.bytes = off;
   return d;
 }
@@ -429,6 +502,8 @@ hipError_t launch_delta_chunks(const DeltaPlan& p, const DeltaChunks& plan, void
   if (plan.pieces > 1) {
     s.agg = reinterpret_cast<float*>(ws + plan.off_agg);
     s.starts = reinterpret_cast<float*>(ws + plan.off_starts);
+    s.group_agg = reinterpret_cast<float*>(ws + plan.off_group_agg);
+    s.group_starts = reinterpret_cast<float*>(ws + plan.off_group_starts);
   }
   s.out_bf16 = p.out_bf16;
   s.out = p.out;

@@ -21,6 +21,8 @@ struct ScanArgs {
   const float* h0;  // (bh, dk, dv) or null
   const float* starts;  // states of pieces 1 .. (bh, piece, 32 KS, cols), or null
   float* agg;       // aggregates walk: (bh, piece, 32 KS, 32 KS + cols)
+  float* group_agg;     // of groups of pieces, as agg
+  float* group_starts;  // and the states that they start from, as starts
   int cols;         // dv rounded up to 16
   void* out;
   float* h_last;

@@ -39,7 +39,8 @@ hipError_t launch_delta_steps(const DeltaPlan& plan, hipStream_t stream);
 // many chunks, the pieces the sequence is split into, and the workspace layout.
 struct DeltaChunks {
   int chunks, pieces, chunks_piece;
-  size_t off_records, off_agg, off_starts, bytes;
+  int groups, group_pieces;  // of pieces, where their states are folded
+  size_t off_records, off_agg, off_starts, off_group_agg, off_group_starts, bytes;
 };
 // requested = 0: automatic. Pure host arithmetic.
 DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int requested);

@@ -65,6 +65,21 @@ def test_long_sequence_on_one_head():
     check(hl, rh, STATE, "h_last")
 
 
+@pytest.mark.parametrize("dk,dv", [(48, 40), (128, 64), (200, 16)])
+@pytest.mark.parametrize("pieces", [16, 17, 25, 40])
+def test_many_pieces_agree(pieces, dk, dv):
+    """Pieces whose states are folded in groups (more than 16), the last group ragged or not;
+    one document crosses all of them, another begins inside a group."""
+    x = delta_inputs(1, 2600, 1, 2, dk, dv, wl.F32, seed=pieces + dk, resets=[(0, 1500)] if pieces == 25 else None,
+                     state=True)
+    x["A"][:] = -0.002
+    ref, rh = od.delta_fwd(**wide(x), reset=x["reset"], scale=dk ** -0.5)
+    print(pieces, dk, dv, flush=True)
+    out, hl = run(x, num_segments=pieces)
+    check(out, ref, STATE, "out")
+    check(hl, rh, STATE, "h_last")
+
+
 @pytest.mark.parametrize("beta_scale,scale", [(2.0, 0.3), (1.0, 1.0)])
 def test_scales_and_large_keys(beta_scale, scale):
     x = delta_inputs(1, 100, 1, 2, 32, 32, wl.F32, seed=4)
