@@ -415,8 +415,8 @@ constexpr int kFoldAlone = 16;
 // aggregates' walk, which has a workgroup for every 64 of dk + dv columns, takes 0.7;
 // a piece's fold takes 0.7 (of three folds over the root of the pieces, where there are
 // groups); and two more launches. Measured at 128 x 128: 2 heads of 131072
-// steps 9356 us in one piece, 490 in 64; 16 heads x 2 of 4096 310 us, 244 in 4; 12 x 8 of 2048 211 us (406 in
-// two: the grid is full as it is).
+// steps 9356 us in one piece, 490 in 64; 16 heads x 2 of 4096 310 us, 244 in 4; 12 x 8 of
+// 2048 211 us (406 in two: the grid is full as it is).
 int choose_pieces(int64_t heads, int chunks, int dk, int dv) {
   constexpr int64_t kCUs = 256;
   const int64_t strips = (dv + 15) / 16, state_strips = 2 * padded_ks(dk);
