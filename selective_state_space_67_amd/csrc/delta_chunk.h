@@ -150,6 +150,7 @@ hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd
 // The forward walk over prepared backward records that keeps every chunk's first
 // state (bh, chunk, 32 padded_ks(dk), cols) and U (bh, chunk, 64, cols), cols = dv
 // rounded up to 16; columns at or past dv and rows of padding are finite.
-hipError_t launch_delta_states(const DeltaPlan& p, const ChunkArgs& c, float* states, float* U, hipStream_t stream);
+hipError_t launch_delta_states(const DeltaPlan& p, const ChunkArgs& c, const DeltaChunks& plan, char* ws, float* states,
+                               float* U, hipStream_t stream);
 
 }  // namespace ssm

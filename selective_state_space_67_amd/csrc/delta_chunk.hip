@@ -45,7 +45,7 @@ __device__ __forceinline__ f32x4 mfma4(f32x4 a, f32x4 b, f32x4 c) {  // 16 x 16 
 // they were produced: the transposed products T_ij^T = -T_jj^T sum A_kj^T T_ik^T
 // take A_kj as it came out of K K^T. Bound by the latency of that chain of small
 // dependent products (the vector pipe is busy 18% of a wave's cycles); two workgroups a
-// CU, one of which hides the serial parts of the other: 3072 chunks of 128 entries in
+// CU, one of which hides the serial parts of the other: 8 x 2048 x 12 heads of 128 entries in
 // 48 us, 2.4 TB/s of records written (in an earlier form 54 us; one workgroup 73, three
 // 53, four, which spill, 104).
 template <typename InT, int NP, int KS, bool VEC, bool BWD, bool ASYNC>
@@ -473,6 +473,14 @@ DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int 
 
 namespace {
 
+void piece_args(const DeltaChunks& plan, char* ws, ScanArgs& s) {
+  if (plan.pieces <= 1) return;
+  s.agg = reinterpret_cast<float*>(ws + plan.off_agg);
+  s.starts = reinterpret_cast<float*>(ws + plan.off_starts);
+  s.group_agg = reinterpret_cast<float*>(ws + plan.off_group_agg);
+  s.group_starts = reinterpret_cast<float*>(ws + plan.off_group_starts);
+}
+
 hipError_t launch_scan(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs& s, hipStream_t stream) {
   s.pieces = plan.pieces;
   s.chunks_piece = plan.chunks_piece;
@@ -499,29 +507,23 @@ hipError_t launch_delta_chunks(const DeltaPlan& p, const DeltaChunks& plan, void
   s.record_gates = kRecGates;
   const hipError_t e = launch_chunk_prepare(p, s.c, false, stream);
   if (e != hipSuccess) return e;
-  if (plan.pieces > 1) {
-    s.agg = reinterpret_cast<float*>(ws + plan.off_agg);
-    s.starts = reinterpret_cast<float*>(ws + plan.off_starts);
-    s.group_agg = reinterpret_cast<float*>(ws + plan.off_group_agg);
-    s.group_starts = reinterpret_cast<float*>(ws + plan.off_group_starts);
-  }
+  piece_args(plan, ws, s);
   s.out_bf16 = p.out_bf16;
   s.out = p.out;
   s.h_last = p.h_last;
   return launch_scan(p, plan, s, stream);
 }
 
-hipError_t launch_delta_states(const DeltaPlan& p, const ChunkArgs& c, float* states, float* U, hipStream_t stream) {
-  DeltaChunks one{};
-  one.chunks = one.chunks_piece = c.chunks;
-  one.pieces = 1;
+hipError_t launch_delta_states(const DeltaPlan& p, const ChunkArgs& c, const DeltaChunks& plan, char* ws, float* states,
+                               float* U, hipStream_t stream) {
   ScanArgs s{};
   s.c = c;
   s.record_bytes = kRecBytesBwd;
   s.record_gates = kRecGatesBwd;
+  piece_args(plan, ws, s);
   s.states = states;
   s.U = U;
-  return launch_scan(p, one, s, stream);
+  return launch_scan(p, plan, s, stream);
 }
 
 }  // namespace ssm

@@ -879,6 +879,11 @@ DeltaBwdLayout plan_delta_bwd(int64_t B, int64_t L, int Hv, int dk, int dv) {
   d.off_dR = take(n * kChunk * cols * 4);
   d.off_sums = take(n * grad_splits(padded_ks(dk)) * kSumFloats * 4);
   d.off_part = take(n * 2 * 4);
+  // the forward's pieces, behind the records that they have here
+  d.walk = plan_delta_chunks(B, L, Hv, dk, dv, 0);
+  const size_t records = d.walk.off_agg, at = take(d.walk.bytes - records);
+  for (size_t* o : {&d.walk.off_agg, &d.walk.off_starts, &d.walk.off_group_agg, &d.walk.off_group_starts})
+    *o += at - records;
   d.bytes = off;
   return d;
 }
@@ -893,7 +898,7 @@ hipError_t launch_delta_bwd(const DeltaPlan& p, const DeltaBwdPlan& g, const Del
   if (e != hipSuccess) return e;
   float* states = reinterpret_cast<float*>(ws + lay.off_states);
   float* U = reinterpret_cast<float*>(ws + lay.off_U);
-  if ((e = launch_delta_states(p, s.c, states, U, stream)) != hipSuccess) return e;
+  if ((e = launch_delta_states(p, s.c, lay.walk, ws, states, U, stream)) != hipSuccess) return e;
   s.states = states;
   s.U = U;
   s.dstates = reinterpret_cast<float*>(ws + lay.off_dstates);

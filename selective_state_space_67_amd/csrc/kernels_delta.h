@@ -62,6 +62,7 @@ struct DeltaBwdPlan {
 };
 struct DeltaBwdLayout {  // workspace byte offsets
   int chunks;
+  DeltaChunks walk;  // the pieces of the forward walk, with offsets in this workspace
   size_t off_records, off_states, off_U, off_dstates, off_dR, off_sums, off_part, bytes;
 };
 DeltaBwdLayout plan_delta_bwd(int64_t B, int64_t L, int Hv, int dk, int dv);

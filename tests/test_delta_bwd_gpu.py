@@ -50,6 +50,18 @@ def test_gradients(shape, dtype, resets):
     compare(run(x, grad_dtype=torch.bfloat16 if bf16 else None), reference(x, scale=shape[4] ** -0.5), bf16)
 
 
+@pytest.mark.parametrize("dtype", [wl.F32, wl.BF16])
+@pytest.mark.parametrize("shape", [(1, 1500, 1, 1, 64, 32), (1, 2500, 1, 2, 48, 40), (2, 1300, 1, 1, 128, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_long_sequences_on_few_heads(shape, dtype):
+    """Walks that are split into pieces, with a decay slow enough that states and their
+    gradients cross them; a document begins inside a piece."""
+    x = delta_inputs(*shape, dtype, seed=sum(shape), resets=[(0, shape[1] - 333)], state=True)
+    x["A"][:] = -0.01
+    print(shape, dtype, flush=True)
+    compare(run(x), reference(x, scale=shape[4] ** -0.5))
+
+
 @pytest.mark.parametrize("beta_scale,scale", [(2.0, 0.3), (1.0, 1.0)])
 def test_scales(beta_scale, scale):
     x = delta_inputs(1, 100, 1, 2, 32, 32, wl.F32, seed=4, state=True)
