@@ -147,6 +147,10 @@ constexpr int kMaxLds = 160 * 1024;
 // Prepare every chunk (delta_chunk.hip); bwd: the backward's records.
 hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd, hipStream_t stream);
 
+// dH at the ends of the pieces (in the starts' place), from the aggregates whose N the
+// reverse walk left.
+hipError_t launch_delta_fold_back(const DeltaPlan& p, const DeltaChunks& plan, char* ws, const float* dh_last,
+                                  hipStream_t stream);
 // The forward walk over prepared backward records that keeps every chunk's first
 // state (bh, chunk, 32 padded_ks(dk), cols) and U (bh, chunk, 64, cols), cols = dv
 // rounded up to 16; columns at or past dv and rows of padding are finite.

@@ -270,7 +270,9 @@ struct FoldArgs {
   int dk, dv, cols, strips;
 };
 
-template <int KS, bool COMPOSE>
+// BACK: of the adjoint, from the last piece to the first (piece numbers count from the end):
+// dH at a piece's start = M^T (dH at its end) + N, N from the reverse walk.
+template <int KS, bool COMPOSE, bool BACK>
 __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
   constexpr int ROWS = 32 * KS;
   __shared__ u32x4 S[2][KS][3][64];  // the state as B operand, two pieces in turn
@@ -294,17 +296,26 @@ __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
   const float* M = a.agg + static_cast<int64_t>(bh) * a.pieces * ROWS * width;
   f32x4 m[KS][2], n;
   const auto fetch = [&](int piece) {
-    const float* p = M + static_cast<int64_t>(piece) * ROWS * width;
-    const float* row = p + static_cast<int64_t>(state_row(w, lane & 12, lane & 3)) * width + 2 * g4;
+    const float* p = M + static_cast<int64_t>(BACK ? a.pieces - 1 - piece : piece) * ROWS * width;
+    const int own_row = state_row(w, lane & 12, lane & 3);
+    if constexpr (BACK) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      m[ks][0] = *reinterpret_cast<const f32x4*>(row + 32 * ks);
-      m[ks][1] = *reinterpret_cast<const f32x4*>(row + 32 * ks + 4);
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[ks][i / 4][i % 4] = p[static_cast<int64_t>(32 * ks + 2 * g4 + i) * width + own_row];
+    } else {
+      const float* row = p + static_cast<int64_t>(own_row) * width + 2 * g4;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        m[ks][0] = *reinterpret_cast<const f32x4*>(row + 32 * ks);
+        m[ks][1] = *reinterpret_cast<const f32x4*>(row + 32 * ks + 4);
+      }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) n[r] = own >= 0 ? p[static_cast<int64_t>(state_row(w, g4, r)) * width + at] : 0.0f;
   };
-  const auto store = [&](int piece) {
+  const auto store = [&](int counted) {
+    const int piece = BACK ? a.pieces - 1 - counted : counted;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       a.out[((static_cast<int64_t>(bh) * a.pieces + piece) * ROWS + state_row(w, g4, r)) * a.cols + own] = H[r];
@@ -343,41 +354,41 @@ __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
   }
 }
 
-template <int KS, bool COMPOSE>
+template <int KS, bool COMPOSE, bool BACK>
 hipError_t launch_fold(FoldArgs f, int64_t heads, hipStream_t stream) {
   f.strips = f.cols / 16 + (COMPOSE ? 2 * KS : 0);
   const int64_t blocks = heads * f.groups * f.strips;
-  SSM_LOG("launch delta_fold<%d rows, compose %d>: %d pieces in %d groups; grid %lld x %d threads", 32 * KS, COMPOSE,
-          f.pieces, f.groups, static_cast<long long>(blocks), 2 * KS * 64);
-  hipLaunchKernelGGL((delta_fold<KS, COMPOSE>), dim3(static_cast<unsigned>(blocks)), dim3(2 * KS * 64), 0, stream, f);
+  SSM_LOG("launch delta_fold<%d rows, compose %d, back %d>: %d pieces in %d groups; grid %lld x %d threads", 32 * KS,
+          COMPOSE, BACK, f.pieces, f.groups, static_cast<long long>(blocks), 2 * KS * 64);
+  hipLaunchKernelGGL((delta_fold<KS, COMPOSE, BACK>), dim3(static_cast<unsigned>(blocks)), dim3(2 * KS * 64), 0, stream, f);
   return hipGetLastError();
 }
 
-template <int KS>
+template <int KS, bool BACK>
 hipError_t fold_ks(const FoldArgs& all, float* group_agg, float* group_starts, int64_t heads, hipStream_t stream) {
   if (all.groups > 1) {
     FoldArgs f = all;
     f.out = group_agg;
-    hipError_t e = launch_fold<KS, true>(f, heads, stream);
+    hipError_t e = launch_fold<KS, true, BACK>(f, heads, stream);
     if (e != hipSuccess) return e;
     f = all;
     f.agg = group_agg;
     f.out = group_starts;
     f.pieces = f.group_pieces = all.groups;
     f.groups = 1;
-    if ((e = launch_fold<KS, false>(f, heads, stream)) != hipSuccess) return e;
+    if ((e = launch_fold<KS, false, false>(f, heads, stream)) != hipSuccess) return e;
   }
-  return launch_fold<KS, false>(all, heads, stream);
+  return launch_fold<KS, false, BACK>(all, heads, stream);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-}  // namespace
-
-hipError_t launch_delta_fold(const DeltaPlan& p, const DeltaChunks& plan, const ScanArgs& s, hipStream_t stream) {
+template <bool BACK>
+hipError_t fold_any(const DeltaPlan& p, const DeltaChunks& plan, const ScanArgs& s, const float* first,
+                    hipStream_t stream) {
   FoldArgs f{};
   f.agg = s.agg;
-  f.h0 = s.h0;
+  f.h0 = first;
   f.from = s.group_starts;
   f.out = const_cast<float*>(s.starts);
   f.pieces = plan.pieces;
@@ -385,16 +396,37 @@ hipError_t launch_delta_fold(const DeltaPlan& p, const DeltaChunks& plan, const 
   f.group_pieces = plan.group_pieces;
   f.dk = p.dk;
   f.dv = p.dv;
-  f.cols = s.cols;
+  f.cols = (p.dv + 15) / 16 * 16;
   const int64_t heads = p.B * p.Hv;
   switch (padded_ks(p.dk)) {
-    case 1: return fold_ks<1>(f, s.group_agg, s.group_starts, heads, stream);
-    case 2: return fold_ks<2>(f, s.group_agg, s.group_starts, heads, stream);
-    case 3: return fold_ks<3>(f, s.group_agg, s.group_starts, heads, stream);
-    case 4: return fold_ks<4>(f, s.group_agg, s.group_starts, heads, stream);
-    case 6: return fold_ks<6>(f, s.group_agg, s.group_starts, heads, stream);
-    default: return fold_ks<8>(f, s.group_agg, s.group_starts, heads, stream);
+    case 1: return fold_ks<1, BACK>(f, s.group_agg, s.group_starts, heads, stream);
+    case 2: return fold_ks<2, BACK>(f, s.group_agg, s.group_starts, heads, stream);
+    case 3: return fold_ks<3, BACK>(f, s.group_agg, s.group_starts, heads, stream);
+    case 4: return fold_ks<4, BACK>(f, s.group_agg, s.group_starts, heads, stream);
+    case 6: return fold_ks<6, BACK>(f, s.group_agg, s.group_starts, heads, stream);
+    default: return fold_ks<8, BACK>(f, s.group_agg, s.group_starts, heads, stream);
   }
+}
+
+void piece_args(const DeltaChunks& plan, char* ws, ScanArgs& s) {
+  if (plan.pieces <= 1) return;
+  s.agg = reinterpret_cast<float*>(ws + plan.off_agg);
+  s.starts = reinterpret_cast<float*>(ws + plan.off_starts);
+  s.group_agg = reinterpret_cast<float*>(ws + plan.off_group_agg);
+  s.group_starts = reinterpret_cast<float*>(ws + plan.off_group_starts);
+}
+
+}  // namespace
+
+hipError_t launch_delta_fold(const DeltaPlan& p, const DeltaChunks& plan, const ScanArgs& s, hipStream_t stream) {
+  return fold_any<false>(p, plan, s, s.h0, stream);
+}
+
+hipError_t launch_delta_fold_back(const DeltaPlan& p, const DeltaChunks& plan, char* ws, const float* dh_last,
+                                  hipStream_t stream) {
+  ScanArgs s{};
+  piece_args(plan, ws, s);
+  return fold_any<true>(p, plan, s, dh_last, stream);
 }
 
 hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd, hipStream_t stream) {
@@ -472,14 +504,6 @@ DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int 
 }
 
 namespace {
-
-void piece_args(const DeltaChunks& plan, char* ws, ScanArgs& s) {
-  if (plan.pieces <= 1) return;
-  s.agg = reinterpret_cast<float*>(ws + plan.off_agg);
-  s.starts = reinterpret_cast<float*>(ws + plan.off_starts);
-  s.group_agg = reinterpret_cast<float*>(ws + plan.off_group_agg);
-  s.group_starts = reinterpret_cast<float*>(ws + plan.off_group_starts);
-}
 
 hipError_t launch_scan(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs& s, hipStream_t stream) {
   s.pieces = plan.pieces;

@@ -38,6 +38,10 @@ struct BwdArgs {
   ChunkArgs c;
   int col_blocks, cols;
   int heads;             // batch rows x value heads
+  int pieces, chunks_piece;  // of the reverse walk
+  const float* ends;     // dH at the ends of pieces 0 .. pieces - 2 (bh, piece, 32 KS, cols)
+  float* agg;            // not null: from dH = 0 at every piece's end, only what its start has, to
+                         // the last cols columns of (bh, piece, 32 KS, 32 KS + cols)
   int items;             // chunks of all key heads
   int grad_bf16;
   bool vec_out;          // rows of dout come as whole 16-byte runs
@@ -138,6 +142,10 @@ __device__ __forceinline__ void rev_stage_sync(char* st, const ChunkArgs& a, con
 // The walk from the last chunk to the first: 16 columns of dH a wave, as in the forward,
 //   dU = P^T dO + eC (K dH1),  dR = T^T dU,  dV = beta dR,
 //   dH0 = aC dH1 + Q^T (e0 dO) - K^T (beta e0 dR).
+// On few heads it goes in the forward's pieces: a first pass finds what every piece adds to
+// dH at its start, the fold carries dH back over them by the transposes of the forward's M,
+// and the full pass starts every piece from its own dH (1 x 4096 x 2 heads: the
+// whole backward 489 -> 223 us).
 // Bound like the forward's walk by the chain of a chunk's products, one wave a SIMD, and
 // it writes dH1 and dR for the gradients' kernel besides: 260 us for 8 x 2048 x 12 heads of
 // 128 x 128 (1.8 TB/s), against 186 for the walk that leaves H0 and U.
@@ -150,8 +158,10 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
   const ChunkArgs& a = s.c;
   const int lane = threadIdx.x % 64, wave = wave_index(), g4 = (lane >> 4) * 4;
   const Place place = place_of(blockIdx.x, s.col_blocks);
-  const int cb = place.part, bh = place.item;
+  const int cb = place.part, bh = place.item / s.pieces, piece = place.item - bh * s.pieces;
   if (bh >= s.heads) return;
+  const int c0 = piece * s.chunks_piece, c1 = min(a.chunks, c0 + s.chunks_piece);
+  const bool all = s.agg == nullptr;
   const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / a.group;
   const int col0 = cb * kBlockCols, own = col0 + wave * 16 + (lane & 15);
   const bool has_v = own < a.dv;
@@ -164,18 +174,24 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = state_row(m, g4, r);
-      if (s.dh_last && row < a.dk && has_v) H[m][r] = s.dh_last[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own];
+      if (!all) continue;
+      if (piece + 1 < s.pieces) {
+        if (own < s.cols)
+          H[m][r] = s.ends[((static_cast<int64_t>(bh) * s.pieces + piece) * (32 * KS) + row) * s.cols + own];
+      } else if (s.dh_last && row < a.dk && has_v) {
+        H[m][r] = s.dh_last[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own];
+      }
     }
   }
   const int64_t token_v = static_cast<int64_t>(a.Hv) * a.dv;
   RevSource<InT> src;
   {
-    const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(a.chunks - 1) * kChunk;
+    const int64_t t0 = static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c1 - 1) * kChunk;
     src.q = static_cast<const InT*>(a.q) + t0 * a.qs + static_cast<int64_t>(hk) * a.dk;
     src.k = static_cast<const InT*>(a.k) + t0 * a.ks + static_cast<int64_t>(hk) * a.dk;
     src.dout = static_cast<const InT*>(s.dout) + t0 * token_v + static_cast<int64_t>(h) * a.dv;
-    src.record = a.records + (static_cast<int64_t>(bh) * a.chunks + a.chunks - 1) * kRecBytesBwd;
-    src.n_tokens = static_cast<int>(a.L - static_cast<int64_t>(a.chunks - 1) * kChunk);
+    src.record = a.records + (static_cast<int64_t>(bh) * a.chunks + c1 - 1) * kRecBytesBwd;
+    src.n_tokens = static_cast<int>(min(static_cast<int64_t>(kChunk), a.L - static_cast<int64_t>(c1 - 1) * kChunk));
   }
   const RevOffsets whole = rev_offsets(a, kChunk, col0, lane, wave);
   const auto stage = [&](char* st, const RevSource<InT>& from) {
@@ -187,8 +203,8 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
       rev_stage_sync<InT, NP, KS, BOTH>(st, a, from, col0);
   };
   if constexpr (STAGES == 2) stage(staged, src);
-  for (int c = a.chunks - 1; c >= 0; --c) {
-    char* st = staged + (STAGES == 2 ? ((a.chunks - 1 - c) & 1) * S::kBytes : 0);
+  for (int c = c1 - 1; c >= c0; --c) {
+    char* st = staged + (STAGES == 2 ? ((c1 - 1 - c) & 1) * S::kBytes : 0);
     RevSource<InT> next = src;
     next.q -= kChunk * a.qs;
     next.k -= kChunk * a.ks;
@@ -198,7 +214,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
     if constexpr (STAGES == 2) {
       wait_loads();
       __syncthreads();  // this stage is loaded, and the other one is no longer read
-      if (c > 0) stage(staged + ((a.chunks - c) & 1) * S::kBytes, next);
+      if (c > c0) stage(staged + ((c1 - c) & 1) * S::kBytes, next);
     } else {
       __syncthreads();  // the previous chunk is no longer read
       stage(st, src);
@@ -210,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
     const float* gates = reinterpret_cast<const float*>(st + S::kGates);
     const int64_t record = static_cast<int64_t>(bh) * a.chunks + c;
 
-    if (own < s.cols) {
+    if (all && own < s.cols) {
       float* to = s.dstates + record * (32 * KS) * s.cols + own;
 #pragma unroll
       for (int m = 0; m < DKT; ++m)
@@ -272,7 +288,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
       const Frag<3> ub[2] = {split8(dU[0], dU[1]), split8(dU[2], dU[3])};
       mma_tri_t(reinterpret_cast<const uint16_t*>(st + S::kTt), ub, lane, dR);
     }
-    if (own < s.cols) {
+    if (all && own < s.cols) {
       float* to = s.dR + record * kChunk * s.cols + own;
 #pragma unroll
       for (int m = 0; m < 4; ++m)
@@ -318,7 +334,9 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
     }
 
     const int64_t row0 = (static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk) * a.Hv + h;  // x dv
-    if (ASYNC && s.grad_bf16) {
+    if (!all) {
+      // the piece's start alone is wanted
+    } else if (ASYNC && s.grad_bf16) {
       // turned to rows in the place of the strip's dO, as the forward's outputs
       uint16_t* o = reinterpret_cast<uint16_t*>(st + S::kdO) + wave * 16;
 #pragma unroll
@@ -353,7 +371,16 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
     }
     src = next;
   }
-  if (s.dh0 && has_v) {
+  if (!all) {
+    const int width = 32 * KS + s.cols;
+    float* to = s.agg + (static_cast<int64_t>(bh) * s.pieces + piece) * (32 * KS) * width + 32 * KS + own;
+    if (own < s.cols) {
+#pragma unroll
+      for (int m = 0; m < DKT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[static_cast<int64_t>(state_row(m, g4, r)) * width] = H[m][r];
+    }
+  } else if (piece == 0 && s.dh0 && has_v) {
 #pragma unroll
     for (int m = 0; m < DKT; ++m)
 #pragma unroll
@@ -805,7 +832,7 @@ hipError_t launch_reverse(const BwdArgs& s, hipStream_t stream) {
   constexpr int kBytes = RevStage<InT, NP, KS, BOTH>::kBytes;
   constexpr int STAGES = ASYNC && 2 * kBytes <= kMaxLds ? 2 : 1;
   static_assert(kBytes <= kMaxLds && (BOTH || !ASYNC), "a chunk's stage exceeds LDS");
-  const int64_t blocks = placed_blocks(s.heads, s.col_blocks);
+  const int64_t blocks = placed_blocks(static_cast<int64_t>(s.heads) * s.pieces, s.col_blocks);
   SSM_LOG("launch delta_chunk_reverse<%d parts, %d rows>: %d chunks, %d stages of %d bytes; grid %lld x %d threads", NP,
           32 * KS, s.c.chunks, STAGES, kBytes, static_cast<long long>(blocks), kThreads);
   hipLaunchKernelGGL((delta_chunk_reverse<InT, NP, KS, BOTH, ASYNC, STAGES>), dim3(static_cast<unsigned>(blocks)),
@@ -835,25 +862,40 @@ hipError_t launch_grads(const BwdArgs& s, int64_t B, hipStream_t stream) {
   return hipGetLastError();
 }
 
+struct Pieces {  // what the fold between the reverse walks needs
+  const DeltaPlan& p;
+  const DeltaChunks& plan;
+  char* ws;
+  float* agg;
+};
+
 template <typename InT, int NP, int KS>
-hipError_t launch_both(const BwdArgs& s, int64_t B, bool direct, hipStream_t stream) {
+hipError_t launch_both(const BwdArgs& s, const Pieces& cut, bool direct, hipStream_t stream) {
+  const auto reverse = [&](const BwdArgs& args) {
+    if constexpr (NP == 1)
+      if (direct) return launch_reverse<InT, NP, KS, true>(args, stream);
+    return launch_reverse<InT, NP, KS, false>(args, stream);
+  };
   hipError_t e;
-  if constexpr (NP == 1)
-    e = direct ? launch_reverse<InT, NP, KS, true>(s, stream) : launch_reverse<InT, NP, KS, false>(s, stream);
-  else
-    e = launch_reverse<InT, NP, KS, false>(s, stream);
-  return e == hipSuccess ? launch_grads<InT, NP, KS>(s, B, stream) : e;
+  if (s.pieces > 1) {
+    BwdArgs ends = s;
+    ends.agg = cut.agg;
+    if ((e = reverse(ends)) != hipSuccess) return e;
+    if ((e = launch_delta_fold_back(cut.p, cut.plan, cut.ws, s.dh_last, stream)) != hipSuccess) return e;
+  }
+  e = reverse(s);
+  return e == hipSuccess ? launch_grads<InT, NP, KS>(s, cut.p.B, stream) : e;
 }
 
 template <typename InT, int NP>
-hipError_t launch_ks(const BwdArgs& s, int64_t B, bool direct, hipStream_t stream) {
+hipError_t launch_ks(const BwdArgs& s, const Pieces& cut, bool direct, hipStream_t stream) {
   switch (padded_ks(s.c.dk)) {
-    case 1: return launch_both<InT, NP, 1>(s, B, direct, stream);
-    case 2: return launch_both<InT, NP, 2>(s, B, direct, stream);
-    case 3: return launch_both<InT, NP, 3>(s, B, direct, stream);
-    case 4: return launch_both<InT, NP, 4>(s, B, direct, stream);
-    case 6: return launch_both<InT, NP, 6>(s, B, direct, stream);
-    default: return launch_both<InT, NP, 8>(s, B, direct, stream);
+    case 1: return launch_both<InT, NP, 1>(s, cut, direct, stream);
+    case 2: return launch_both<InT, NP, 2>(s, cut, direct, stream);
+    case 3: return launch_both<InT, NP, 3>(s, cut, direct, stream);
+    case 4: return launch_both<InT, NP, 4>(s, cut, direct, stream);
+    case 6: return launch_both<InT, NP, 6>(s, cut, direct, stream);
+    default: return launch_both<InT, NP, 8>(s, cut, direct, stream);
   }
 }
 
@@ -906,6 +948,10 @@ hipError_t launch_delta_bwd(const DeltaPlan& p, const DeltaBwdPlan& g, const Del
   s.sums = reinterpret_cast<float*>(ws + lay.off_sums);
   s.part = reinterpret_cast<float*>(ws + lay.off_part);
   s.heads = static_cast<int>(p.B * p.Hv);
+  s.pieces = lay.walk.pieces;
+  s.chunks_piece = lay.walk.chunks_piece;
+  s.ends = reinterpret_cast<const float*>(ws + lay.walk.off_starts);
+  const Pieces cut{p, lay.walk, ws, reinterpret_cast<float*>(ws + lay.walk.off_agg)};
   s.items = static_cast<int>(p.B * p.Hk * lay.chunks);
   s.cols = (p.dv + 15) / 16 * 16;
   s.col_blocks = (p.dv + kBlockCols - 1) / kBlockCols;
@@ -922,7 +968,7 @@ hipError_t launch_delta_bwd(const DeltaPlan& p, const DeltaBwdPlan& g, const Del
   s.vec_out = p.dv % 8 == 0 && delta_aligned(g.dout, 16);
   const bool direct = s.c.vec && s.vec_out && p.in_bf16 && p.dk == 32 * padded_ks(p.dk) && p.qs < reach && p.ks < reach &&
                       static_cast<int64_t>(p.Hv) * p.dv < reach && delta_aligned(g.dv, 16);
-  e = p.in_bf16 ? launch_ks<bf16_t, 1>(s, p.B, direct, stream) : launch_ks<float, 3>(s, p.B, false, stream);
+  e = p.in_bf16 ? launch_ks<bf16_t, 1>(s, cut, direct, stream) : launch_ks<float, 3>(s, cut, false, stream);
   if (e != hipSuccess) return e;
   SSM_LOG("launch delta_head_sums: grid %d x %d threads", p.Hv, kThreads);
   hipLaunchKernelGGL(delta_head_sums, dim3(p.Hv), dim3(kThreads), 0, stream, s.part, g.dA, g.dbias,
