@@ -263,6 +263,7 @@ hipError_t prepare_f32(const ChunkArgs& a, int64_t blocks, bool bwd, hipStream_t
 // heads in 8 groups: 19 + 17 + 19 us; the call 591 -> 490.)
 struct FoldArgs {
   const float* agg;     // (bh, pieces, ROWS, ROWS + cols)
+  const float* turned;  // BACK: M^T (bh, pieces, ROWS, ROWS)
   const float* h0;      // of group 0, (bh, dk, dv) or null
   const float* from;    // of groups 1 .., (bh, groups, ROWS, cols)
   float* out;           // (bh, pieces, ROWS, cols); COMPOSE: (bh, groups, ROWS, ROWS + cols)
@@ -271,7 +272,8 @@ struct FoldArgs {
 };
 
 // BACK: of the adjoint, from the last piece to the first (piece numbers count from the end):
-// dH at a piece's start = M^T (dH at its end) + N, N from the reverse walk.
+// dH at a piece's start = M^T (dH at its end) + N, N from the reverse walk. M^T is written
+// by the aggregates' walk (gathered from M instead, 16 heads of 192 x 128 took 84 us, so 29).
 template <int KS, bool COMPOSE, bool BACK>
 __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
   constexpr int ROWS = 32 * KS;
@@ -298,18 +300,13 @@ __global__ __launch_bounds__(2 * KS * 64) void delta_fold(const FoldArgs a) {
   const auto fetch = [&](int piece) {
     const float* p = M + static_cast<int64_t>(BACK ? a.pieces - 1 - piece : piece) * ROWS * width;
     const int own_row = state_row(w, lane & 12, lane & 3);
-    if constexpr (BACK) {
+    const float* row =
+        (BACK ? a.turned + ((static_cast<int64_t>(bh) * a.pieces + a.pieces - 1 - piece) * ROWS + own_row) * ROWS
+              : p + static_cast<int64_t>(own_row) * width) + 2 * g4;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m[ks][i / 4][i % 4] = p[static_cast<int64_t>(32 * ks + 2 * g4 + i) * width + own_row];
-    } else {
-      const float* row = p + static_cast<int64_t>(own_row) * width + 2 * g4;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        m[ks][0] = *reinterpret_cast<const f32x4*>(row + 32 * ks);
-        m[ks][1] = *reinterpret_cast<const f32x4*>(row + 32 * ks + 4);
-      }
+    for (int ks = 0; ks < KS; ++ks) {
+      m[ks][0] = *reinterpret_cast<const f32x4*>(row + 32 * ks);
+      m[ks][1] = *reinterpret_cast<const f32x4*>(row + 32 * ks + 4);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) n[r] = own >= 0 ? p[static_cast<int64_t>(state_row(w, g4, r)) * width + at] : 0.0f;
@@ -388,6 +385,7 @@ hipError_t fold_any(const DeltaPlan& p, const DeltaChunks& plan, const ScanArgs&
                     hipStream_t stream) {
   FoldArgs f{};
   f.agg = s.agg;
+  f.turned = s.turned;
   f.h0 = first;
   f.from = s.group_starts;
   f.out = const_cast<float*>(s.starts);
@@ -414,6 +412,7 @@ void piece_args(const DeltaChunks& plan, char* ws, ScanArgs& s) {
   s.starts = reinterpret_cast<float*>(ws + plan.off_starts);
   s.group_agg = reinterpret_cast<float*>(ws + plan.off_group_agg);
   s.group_starts = reinterpret_cast<float*>(ws + plan.off_group_starts);
+  if (plan.off_turned) s.turned = reinterpret_cast<float*>(ws + plan.off_turned);
 }
 
 }  // namespace

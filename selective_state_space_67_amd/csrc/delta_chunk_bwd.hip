@@ -926,6 +926,7 @@ DeltaBwdLayout plan_delta_bwd(int64_t B, int64_t L, int Hv, int dk, int dv) {
   const size_t records = d.walk.off_agg, at = take(d.walk.bytes - records);
   for (size_t* o : {&d.walk.off_agg, &d.walk.off_starts, &d.walk.off_group_agg, &d.walk.off_group_starts})
     *o += at - records;
+  if (d.walk.pieces > 1) d.walk.off_turned = take(static_cast<size_t>(B) * Hv * d.walk.pieces * rows * rows * 4);
   d.bytes = off;
   return d;
 }

@@ -21,6 +21,7 @@ struct ScanArgs {
   const float* h0;  // (bh, dk, dv) or null
   const float* starts;  // states of pieces 1 .. (bh, piece, 32 KS, cols), or null
   float* agg;       // aggregates walk: (bh, piece, 32 KS, 32 KS + cols)
+  float* turned;    // M^T as well: (bh, piece, 32 KS, 32 KS), or null
   float* group_agg;     // of groups of pieces, as agg
   float* group_starts;  // and the states that they start from, as starts
   int cols;         // dv rounded up to 16
@@ -399,6 +400,11 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
     for (int m = 0; m < DKT; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) dst[static_cast<int64_t>(state_row(m, g4, r)) * width] = H[m][r];
+    if (s.turned && strip < DKT) {
+      float* row = s.turned + ((static_cast<int64_t>(bh) * s.pieces + piece) * (32 * KS) + at) * (32 * KS);
+#pragma unroll
+      for (int m = 0; m < DKT; ++m) *reinterpret_cast<f32x4*>(row + state_row(m, g4, 0)) = H[m];
+    }
   } else if (OUT && s.h_last && c1 == a.chunks && has_v) {
 #pragma unroll
     for (int m = 0; m < DKT; ++m)

@@ -41,6 +41,7 @@ struct DeltaChunks {
   int chunks, pieces, chunks_piece;
   int groups, group_pieces;  // of pieces, where their states are folded
   size_t off_records, off_agg, off_starts, off_group_agg, off_group_starts, bytes;
+  size_t off_turned;  // M^T of the pieces, which the backward keeps
 };
 // requested = 0: automatic. Pure host arithmetic.
 DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int requested);
