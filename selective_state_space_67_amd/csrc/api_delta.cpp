@@ -180,7 +180,8 @@ ssm_status plan_delta_bwd(const ssm_delta_bwd_params* p, DeltaSizes* s, ssm::Del
   // what a piece and a group of pieces need (at most one of each for two chunks)
   const int64_t chunks = (p->seqlen + 63) / 64;
   int64_t bytes;
-  if (!mul_ok(p->batch * p->value_heads * chunks, 4 * (p->dk + 127) * (2 * p->dk + 4 * p->dv + 314) + 98304, &bytes) || bytes > kLim)
+  if (!mul_ok(p->batch * p->value_heads * chunks, 4 * (p->dk + 127) * (2 * p->dk + 4 * p->dv + 314) + 98304, &bytes) ||
+      bytes > kLim)
     return fail(SSM_ERR_BAD_SHAPE, "backward workspace size overflows");
   *lay = ssm::plan_delta_bwd(p->batch, p->seqlen, static_cast<int>(p->value_heads), static_cast<int>(p->dk),
                              static_cast<int>(p->dv));
