@@ -62,6 +62,15 @@ def test_long_sequences_on_few_heads(shape, dtype):
     compare(run(x), reference(x, scale=shape[4] ** -0.5))
 
 
+@pytest.mark.parametrize("shape", [(1, 4160, 1, 1, 32, 24), (1, 5100, 1, 1, 40, 16)], ids=lambda s: "x".join(map(str, s)))
+def test_many_pieces(shape):
+    """More than 16 pieces, whose adjoints are folded in groups from the last to the first."""
+    x = delta_inputs(*shape, wl.F32, seed=sum(shape), state=True)
+    x["A"][:] = -0.003
+    print(shape, flush=True)
+    compare(run(x), reference(x, scale=shape[4] ** -0.5))
+
+
 @pytest.mark.parametrize("beta_scale,scale", [(2.0, 0.3), (1.0, 1.0)])
 def test_scales(beta_scale, scale):
     x = delta_inputs(1, 100, 1, 2, 32, 32, wl.F32, seed=4, state=True)
