@@ -50,8 +50,11 @@ __device__ __forceinline__ void chunk_gates(const ChunkArgs& a, int b, int h, in
     slope = fast_rcp(1.0f + fast_exp2(-raw * kLog2e));
     beta = a.beta_scale * fast_rcp(1.0f + fast_exp2(-load_elem(static_cast<const InT*>(a.br), i) * kLog2e));
     start = a.reset && a.reset[static_cast<int64_t>(b) * a.L + t];
-    // a step's decay below 2^-16384 is 0 in float32 whatever its exponent
-    if (!start) g = fmax(static_cast<double>(a.A[h]) * delta * 1.4426950408889634, -16384.0);
+    // a step's decay below 2^-16384 is 0 in float32 whatever its exponent; a NaN stays one
+    if (!start) {
+      g = static_cast<double>(a.A[h]) * delta * 1.4426950408889634;
+      if (g < -16384.0) g = -16384.0;
+    }
   }
   const uint64_t starts = __ballot(start);
   const int seg = __popcll(starts & (~uint64_t{0} >> (63 - lane)));
