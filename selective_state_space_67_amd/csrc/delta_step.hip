@@ -120,8 +120,9 @@ __global__ __launch_bounds__(kThreads) void delta_steps(const StepArgs a) {
     const float delta = softplus_f32(load_elem(static_cast<const InT*>(a.dt), gi) + bias);
     const float beta =
         a.beta_scale * fast_rcp(1.0f + fast_exp2(-load_elem(static_cast<const InT*>(a.br), gi) * kLog2e));
-    const float al = fast_exp2(A * delta * kLog2e);
+    float al = fast_exp2(A * delta * kLog2e);
     if (a.reset && a.reset[static_cast<int64_t>(b) * a.L + t]) {
+      al = 0.0f;  // a document's first token carries nothing over, whatever its decay (NaN, infinite)
 #pragma unroll
       for (int r = 0; r < R; ++r) H[r][0] = H[r][1] = H[r][2] = H[r][3] = 0.0f;
     }

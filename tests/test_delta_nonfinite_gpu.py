@@ -64,3 +64,30 @@ def test_a_nan_gate_reaches_its_gradients(name):
         v = host(g[n])
         assert np.isnan(v[1]) and np.isfinite(v[0]), n
     assert np.isnan(host(g["d_dt_raw"])[0, 5, 1]) and np.isfinite(host(g["d_dt_raw"])[0, :, 0]).all()
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("dtype,L,pieces", [(wl.BF16, 12, 0), (wl.F32, 30, 0), (wl.BF16, 90, 0), (wl.F32, 140, 2)])
+def test_a_reset_token_needs_no_decay(dtype, L, pieces, value):
+    """Where a document starts nothing is carried over, whatever the token's decay would be (a
+    growing one that overflows included)."""
+    x = delta_inputs(1, L, 1, 2, 32, 24, dtype, seed=L, resets=[(0, 7)], state=True)
+    ref, rh = od.delta_fwd(**wide(x), reset=x["reset"], scale=1.0)
+    put(x, "dt_raw", (0, 7, 0), value)
+    put(x, "dt_raw", (0, 7, 1), value)
+    print(dtype, L, value, flush=True)
+    out, hl = forward(x, scale=1.0, num_segments=pieces)
+    check(out, ref, STATE, "out")
+    check(hl, rh, STATE, "h_last")
+
+
+def test_a_reset_token_needs_no_decay_in_a_window_that_grows():
+    """A positive A whose exponential overflows at the token that a document starts with."""
+    x = delta_inputs(1, 10, 1, 1, 32, 24, wl.F32, seed=2, resets=[(0, 4)], state=True)
+    x["A"][:] = 1e-3
+    x["dt_raw"][0, 4] = 1e30
+    ref, rh = od.delta_fwd(**wide({**x, "dt_raw": np.where(x["reset"][..., None] != 0, 0, x["dt_raw"])}),
+                           reset=x["reset"], scale=1.0)
+    out, hl = forward(x, scale=1.0)
+    check(out, ref, STATE, "out")
+    check(hl, rh, STATE, "h_last")
