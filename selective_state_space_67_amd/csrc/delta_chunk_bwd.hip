@@ -779,8 +779,10 @@ __global__ __launch_bounds__(kThreads) void delta_gate_grads(const BwdArgs s, in
   const float seg_before = __shfl_up(seg, 1);
   const bool cut = lane == 0 ? seg > 0.0f : seg != seg_before;
   const bool there = lane < n_tokens;
-  const float dg = cut || !there ? 0.0f : static_cast<float>(sum);
-  const float d_dt = dg * a.A[h] * scalars[kSlope + lane];
+  // nothing crosses a document's start: its token's gate has no part in the sums, whatever it is
+  const bool off = cut || !there;
+  const float dg = off ? 0.0f : static_cast<float>(sum);
+  const float d_dt = off ? 0.0f : dg * a.A[h] * scalars[kSlope + lane];
   if (there) {
     const int64_t at = (static_cast<int64_t>(b) * a.L + static_cast<int64_t>(chunk) * kChunk + lane) * a.Hv + h;
     const float d_beta = sums[kSumBeta + lane] * (1.0f - scalars[kBeta + lane] / a.beta_scale);
@@ -792,7 +794,7 @@ __global__ __launch_bounds__(kThreads) void delta_gate_grads(const BwdArgs s, in
       store_elem(static_cast<float*>(s.dbr), at, d_beta);
     }
   }
-  const float dA = lanes_sum<64>(dg * scalars[kDelta + lane]), dbias = lanes_sum<64>(d_dt);
+  const float dA = lanes_sum<64>(off ? 0.0f : dg * scalars[kDelta + lane]), dbias = lanes_sum<64>(d_dt);
   if (lane == 0) {
     s.part[record * 2] = dA;
     s.part[record * 2 + 1] = dbias;

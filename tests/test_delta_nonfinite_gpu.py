@@ -5,7 +5,7 @@ import pytest
 from oracle import delta as od
 from selective_state_space_67_amd import workloads as wl
 
-from delta_helpers import ARGS, STATE, check, delta_inputs, host, on_device, wide
+from delta_helpers import ARGS, GRAD, STATE, check, delta_inputs, host, on_device, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +91,22 @@ def test_a_reset_token_needs_no_decay_in_a_window_that_grows():
     out, hl = forward(x, scale=1.0)
     check(out, ref, STATE, "out")
     check(hl, rh, STATE, "h_last")
+
+
+def test_a_reset_tokens_gate_has_no_gradient():
+    """The decay of a token that starts a document is not used: whatever it is, its gradient is 0
+    and it stays out of the sums for A and dt_bias."""
+    import torch
+
+    from selective_state_space_67_amd import ssm_delta_bwd
+
+    x = delta_inputs(1, 100, 1, 2, 32, 24, wl.F32, seed=4, resets=[(0, 7), (0, 64)], state=True)
+    ref = od.delta_bwd(**wide(x), dout=x["dout"].astype(np.float64), reset=x["reset"],
+                       dh_last=x["dh_last"].astype(np.float64), scale=1.0)
+    x["dt_raw"][0, 7, 0], x["dt_raw"][0, 64, 1] = np.nan, np.inf
+    t = on_device(x)
+    g = ssm_delta_bwd(*(t[n] for n in ARGS), t["dout"], dt_bias=t["dt_bias"], reset=t["reset"], h0=t["h0"],
+                      dh_last=t["dh_last"], scale=1.0)
+    torch.cuda.synchronize()
+    for n, want in ref.items():
+        check(g[n], want, GRAD, n)
