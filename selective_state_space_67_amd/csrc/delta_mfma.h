@@ -124,12 +124,10 @@ __device__ __forceinline__ int state_row(int m, int g4, int r) { return (m >> 1)
 
 // c[n] += a[n] b for N independent sums, in turns: a sum's next product waits for
 // its last one, the others' do not.
-// PARTS: 3 for float32's precision, 2 for 2^-17 of the operands (products of parts
-// whose places add up to less than PARTS are kept).
-template <int PARTS = 3, int N, int NA, int NB>
+template <int N, int NA, int NB>
 __device__ __forceinline__ void mma_n(const Frag<NA> (&a)[N], const Frag<NB>& b, f32x4 (&c)[N]) {
 #pragma unroll
-  for (int s = PARTS - 1; s >= 0; --s)
+  for (int s = 2; s >= 0; --s)
 #pragma unroll
     for (int i = 0; i < NA; ++i)
       if (s - i >= 0 && s - i < NB)
@@ -317,12 +315,11 @@ __host__ __device__ constexpr int tri_index(int mi, int ks) { return mi < 2 ? mi
 // transposed: row tiles 0 and 1 sum over both halves, 2 and 3 over the second
 __host__ __device__ constexpr int tri_t_index(int mi, int ks) { return mi < 2 ? mi * 2 + ks : mi + 2; }
 
-// `parts` of operand `index`; parts lie one after another.
-template <int PARTS>
-__device__ __forceinline__ Frag<PARTS> load_tri(const uint16_t* m, int index, int lane) {
-  Frag<PARTS> f;
+// Operand `index`; its parts lie one after another.
+__device__ __forceinline__ Frag<3> load_tri(const uint16_t* m, int index, int lane) {
+  Frag<3> f;
 #pragma unroll
-  for (int i = 0; i < PARTS; ++i)
+  for (int i = 0; i < 3; ++i)
     f.p[i] = *reinterpret_cast<const u32x4*>(m + ((i * kTriFrags + index) * 64 + lane) * 8);
   return f;
 }
@@ -333,14 +330,13 @@ __device__ __forceinline__ void store_tri(uint16_t* m, int index, int lane, cons
 
 // c[m] += M[m][.] b for the four row tiles of a staged triangle M (rows m sum over
 // the halves ks <= m / 2): six independent sums in turns.
-template <int PARTS = 3>
 __device__ __forceinline__ void mma_tri(const uint16_t* m, const Frag<3> (&b)[2], int lane, f32x4 (&c)[4]) {
-  Frag<PARTS> a[6];
+  Frag<3> a[6];
 #pragma unroll
-  for (int i = 0; i < 6; ++i) a[i] = load_tri<PARTS>(m, i, lane);
+  for (int i = 0; i < 6; ++i) a[i] = load_tri(m, i, lane);
   f32x4 d[2] = {};
 #pragma unroll
-  for (int s = PARTS - 1; s >= 0; --s)
+  for (int s = 2; s >= 0; --s)
 #pragma unroll
     for (int i = 0; i <= s; ++i) {
       c[0] = mfma(a[0].p[i], b[0].p[s - i], c[0]);
@@ -359,7 +355,7 @@ template <int NB>
 __device__ __forceinline__ void mma_tri_t(const uint16_t* m, const Frag<NB> (&b)[2], int lane, f32x4 (&c)[4]) {
   Frag<3> a[6];
 #pragma unroll
-  for (int i = 0; i < 6; ++i) a[i] = load_tri<3>(m, i, lane);
+  for (int i = 0; i < 6; ++i) a[i] = load_tri(m, i, lane);
   f32x4 d[2] = {};
 #pragma unroll
   for (int s = 2; s >= 0; --s)

@@ -45,15 +45,15 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBlockCols = 16 * kWaves;  // columns of the state per workgroup
 
-// What a workgroup stages of one chunk, in bytes from the stage's start. T, the
-// first OP parts of P and the scalars keep the record's order.
-template <typename InT, int NP, int KS, Walk MODE, bool QLDS, int OP>
+// What a workgroup stages of one chunk, in bytes from the stage's start. T, P and the
+// scalars keep the record's order.
+template <typename InT, int NP, int KS, Walk MODE, bool QLDS>
 struct Stage {
   static constexpr int kK = 0;
   static constexpr int kQ = kK + TokenTile<NP, KS>::kBytes;
   static constexpr int kT = kQ + (MODE == kOutputs && QLDS ? TokenTile<NP, KS>::kBytes : 0);
   static constexpr int kP = kT + kTriBytes;
-  static constexpr int kGates = kP + (MODE == kOutputs ? kTriBytes / 3 * OP : 0);
+  static constexpr int kGates = kP + (MODE == kOutputs ? kTriBytes : 0);
   static constexpr int kV = kGates + kGateFloats * 4;  // (64, kBlockCols) of InT
   static constexpr int kBytes = kV + kChunk * kBlockCols * static_cast<int>(sizeof(InT));
 };
@@ -107,10 +107,10 @@ __device__ __forceinline__ LaneOffsets lane_offsets(const ChunkArgs& a, int n_to
 // In four parts (PART < 0: all), which the walk issues between its products: loads
 // enter the memory pipe no faster than 64 bytes a cycle, and a wave that issues them
 // all at once waits for it.
-template <typename InT, int KS, Walk MODE, int OP, int PART>
+template <typename InT, int KS, Walk MODE, int PART>
 __device__ __forceinline__ void stage_async(char* st, const ChunkSource<InT>& s, const LaneOffsets& o, int lane,
                                             int wave) {
-  using S = Stage<InT, 1, KS, MODE, true, OP>;
+  using S = Stage<InT, 1, KS, MODE, true>;
   static_assert(kWaves == 4, "row tile w and values 16 w .. of wave w");
   if constexpr (PART < 0 || PART == 0) {
     const char* k = reinterpret_cast<const char*>(s.k);
@@ -124,7 +124,7 @@ __device__ __forceinline__ void stage_async(char* st, const ChunkSource<InT>& s,
   }
   if constexpr (PART < 0 || PART >= 2) {
     const uint32_t own = lane * 16;
-    constexpr int kTri = (MODE == kOutputs ? kTriBytes + kTriBytes / 3 * OP : kTriBytes) / 1024;
+    constexpr int kTri = (MODE == kOutputs ? 2 * kTriBytes : kTriBytes) / 1024;
     constexpr int kAll = (kTri + kWaves - 1) / kWaves, kHalf = kAll / 2;
 #pragma unroll
     for (int i = PART == 3 ? kHalf : 0; i < (PART == 2 ? kHalf : kAll); ++i) {
@@ -141,14 +141,14 @@ __device__ __forceinline__ void stage_async(char* st, const ChunkSource<InT>& s,
 }
 
 // Staging through registers, for float32 and for rows that are not whole runs.
-template <typename InT, int NP, int KS, Walk MODE, bool QLDS, int OP>
+template <typename InT, int NP, int KS, Walk MODE, bool QLDS>
 __device__ __forceinline__ void stage_sync(char* st, const ChunkArgs& a, const ChunkSource<InT>& s, int col0) {
-  using S = Stage<InT, NP, KS, MODE, QLDS, OP>;
+  using S = Stage<InT, NP, KS, MODE, QLDS>;
   uint16_t* sk = reinterpret_cast<uint16_t*>(st + S::kK);
   uint16_t* sq = reinterpret_cast<uint16_t*>(st + S::kQ);
   stage_rows<InT, NP, KS, kThreads>(sk, s.k, a.ks, s.n_tokens, a.dk, a.vec);
   if constexpr (MODE == kOutputs && QLDS) stage_rows<InT, NP, KS, kThreads>(sq, s.q, a.qs, s.n_tokens, a.dk, a.vec);
-  constexpr int kRuns = (MODE == kOutputs ? kTriBytes + kTriBytes / 3 * OP : kTriBytes) / 16;
+  constexpr int kRuns = (MODE == kOutputs ? 2 * kTriBytes : kTriBytes) / 16;
   for (int i = threadIdx.x; i < kRuns; i += kThreads)
     reinterpret_cast<u32x4*>(st + S::kT)[i] = reinterpret_cast<const u32x4*>(s.record)[i];
   reinterpret_cast<float*>(st + S::kGates)[threadIdx.x] = reinterpret_cast<const float*>(s.gates)[threadIdx.x];
@@ -167,18 +167,20 @@ __device__ __forceinline__ void stage_sync(char* st, const ChunkArgs& a, const C
 // Bound by the chain of dependent steps of a chunk: K H0, R, T R, P U and K^T U follow
 // one another, and a workgroup has a wave for every SIMD of its CU and no second one to
 // fill its waits (8 x 2048 x 12 heads of 128 x 128 give 192 workgroups for 256 CUs, and the
-// two staged chunks of one take 142 KB of LDS). A chunk takes 4.2 us, about 10000 cycles,
+// two staged chunks of one take 158 KB of LDS). A chunk takes 4.2 us, about 10000 cycles,
 // 2900 of them matrix instructions: 155 us for that call, 1.6 TB/s of inputs, records and
 // outputs. The 16 columns a wave are what one operand of the matrix instruction holds: more
 // of them would share the operands of K, Q, T and P, but leave fewer waves than SIMDs.
 // AGG: the aggregates walk (no read-out; the first 32 KS columns start from the
 // identity). With two stages the next chunk is loaded while this one is worked on.
-// OP: parts of the products that only the output sees; two (2^-17) where it is
-// rounded to bfloat16 (2^-9).
-template <typename InT, int NP, int KS, Walk MODE, bool QLDS, bool ASYNC, int STAGES, int OP>
+// OUT16: the output is bfloat16. Its products keep all three parts all the same, since what
+// Q H0 and P U cancel of each other can be many times the output: with two parts, new values
+// over old ones R times as large came out 45 x 2^-24 R off, float32 arithmetic 3 x 2^-24 R
+// (and 8 x 2048 x 12 heads took 201 us, so 212).
+template <typename InT, int NP, int KS, Walk MODE, bool QLDS, bool ASYNC, int STAGES, bool OUT16>
 __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
   using Tile = TokenTile<NP, KS>;
-  using S = Stage<InT, NP, KS, MODE, QLDS, OP>;
+  using S = Stage<InT, NP, KS, MODE, QLDS>;
   constexpr int DKT = 2 * KS;  // row tiles of the state
   constexpr bool AGG = MODE == kAggregates, OUT = MODE == kOutputs;
   extern __shared__ __align__(16) char staged[];
@@ -218,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
   const auto offsets = [&](int n_tokens) {
     return n_tokens == kChunk ? whole : lane_offsets(a, n_tokens, col0, lane, wave);
   };
-  if constexpr (STAGES == 2) stage_async<InT, KS, MODE, OP, -1>(staged, src, offsets(src.n_tokens), lane, wave);
+  if constexpr (STAGES == 2) stage_async<InT, KS, MODE, -1>(staged, src, offsets(src.n_tokens), lane, wave);
   for (int c = c0; c < c1; ++c) {
     char* st = staged + (STAGES == 2 ? ((c - c0) & 1) * S::kBytes : 0);
     char* st_next = staged + (STAGES == 2 ? ((c + 1 - c0) & 1) * S::kBytes : 0);
@@ -236,13 +238,13 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
     if constexpr (STAGES == 2) {
       wait_loads();
       __syncthreads();  // this stage is loaded, and the other one is no longer read
-      if (more) stage_async<InT, KS, MODE, OP, 0>(st_next, next, next_off, lane, wave);
+      if (more) stage_async<InT, KS, MODE, 0>(st_next, next, next_off, lane, wave);
     } else {
       __syncthreads();  // the previous chunk is no longer read
       if constexpr (ASYNC)
-        stage_async<InT, KS, MODE, OP, -1>(st, src, offsets(src.n_tokens), lane, wave);
+        stage_async<InT, KS, MODE, -1>(st, src, offsets(src.n_tokens), lane, wave);
       else
-        stage_sync<InT, NP, KS, MODE, QLDS, OP>(st, a, src, col0);
+        stage_sync<InT, NP, KS, MODE, QLDS>(st, a, src, col0);
       wait_loads();
       __syncthreads();
     }
@@ -284,7 +286,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
         hb_next = split8(H[2 * ks + 2], H[2 * ks + 3]);
       }
       mma_n(kf, hb, X);
-      if constexpr (OUT) mma_n<OP>(qf, hb, Y);
+      if constexpr (OUT) mma_n(qf, hb, Y);
       if (ks + 1 < KS) {
         hb = hb_next;
 #pragma unroll
@@ -294,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
         }
       }
     }
-    if (STAGES == 2 && more) stage_async<InT, KS, MODE, OP, 1>(st_next, next, next_off, lane, wave);
+    if (STAGES == 2 && more) stage_async<InT, KS, MODE, 1>(st_next, next, next_off, lane, wave);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       f32x4 V = zero;
@@ -323,10 +325,10 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
       const Frag<3> rb[2] = {split8(X[0], X[1]), split8(X[2], X[3])};
       mma_tri(reinterpret_cast<const uint16_t*>(st + S::kT), rb, lane, U);
     }
-    if (STAGES == 2 && more) stage_async<InT, KS, MODE, OP, 2>(st_next, next, next_off, lane, wave);
+    if (STAGES == 2 && more) stage_async<InT, KS, MODE, 2>(st_next, next, next_off, lane, wave);
     if constexpr (OUT) {
       const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
-      mma_tri<OP>(reinterpret_cast<const uint16_t*>(st + S::kP), ub, lane, Y);
+      mma_tri(reinterpret_cast<const uint16_t*>(st + S::kP), ub, lane, Y);
     }
     if constexpr (MODE == kStates) {
       float* to = s.U + (static_cast<int64_t>(bh) * a.chunks + c) * kChunk * s.cols + own;
@@ -336,7 +338,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
         for (int r = 0; r < 4; ++r)
           if (own < s.cols) to[(m * 16 + g4 + r) * s.cols] = U[m][r];
     }
-    if (STAGES == 2 && more) stage_async<InT, KS, MODE, OP, 3>(st_next, next, next_off, lane, wave);
+    if (STAGES == 2 && more) stage_async<InT, KS, MODE, 3>(st_next, next, next_off, lane, wave);
 #pragma unroll
     for (int m = 0; m < 4; ++m) U[m] *= *reinterpret_cast<const f32x4*>(gates + kEC + m * 16 + g4);
     const Frag<3> ub[2] = {split8(U[0], U[1]), split8(U[2], U[3])};
@@ -353,7 +355,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
 
     if constexpr (OUT) {
       const int64_t row0 = (static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk) * a.Hv + h;  // x dv
-      if (OP == 2 && (ASYNC || s.out_runs)) {  // ASYNC has whole runs everywhere
+      if (OUT16 && (ASYNC || s.out_runs)) {  // ASYNC has whole runs everywhere
         // The strip's place among the staged values is this wave's alone and has been
         // read: the outputs turn there from columns to rows, 16 bytes a lane.
         uint16_t* o = reinterpret_cast<uint16_t*>(st + S::kV) + wave * 16;
@@ -382,7 +384,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             if (!has_v || m * 16 + g4 + r >= src.n_tokens) continue;
-            if (OP == 2 || s.out_bf16)
+            if (OUT16 || s.out_bf16)
               store_elem(static_cast<bf16_t*>(s.out) + (m * 16 + r) * step, lane0, a.scale * Y[m][r]);
             else
               store_elem(static_cast<float*>(s.out) + (m * 16 + r) * step, lane0, a.scale * Y[m][r]);
@@ -416,15 +418,15 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
   }
 }
 
-template <typename InT, int NP, int KS, Walk MODE, bool QLDS, bool ASYNC, int OP>
+template <typename InT, int NP, int KS, Walk MODE, bool QLDS, bool ASYNC, bool OUT16>
 hipError_t launch_walk(const ScanArgs& s, int64_t blocks, hipStream_t stream) {
-  constexpr int kBytes = Stage<InT, NP, KS, MODE, QLDS, OP>::kBytes;
+  constexpr int kBytes = Stage<InT, NP, KS, MODE, QLDS>::kBytes;
   constexpr int STAGES = ASYNC && 2 * kBytes <= kMaxLds ? 2 : 1;
   static_assert(kBytes <= kMaxLds, "a chunk's stage exceeds LDS");
   SSM_LOG("launch delta_chunk_scan<%d parts, %d rows, walk %d>: %d pieces of %d chunks, %d stages of %d bytes; "
           "grid %lld x %d threads",
           NP, 32 * KS, MODE, s.pieces, s.chunks_piece, STAGES, kBytes, static_cast<long long>(blocks), kThreads);
-  hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, MODE, QLDS, ASYNC, STAGES, OP>),
+  hipLaunchKernelGGL((delta_chunk_scan<InT, NP, KS, MODE, QLDS, ASYNC, STAGES, OUT16>),
                      dim3(static_cast<unsigned>(blocks)), dim3(kThreads), STAGES * kBytes, stream, s);
   return hipGetLastError();
 }
@@ -432,21 +434,21 @@ hipError_t launch_walk(const ScanArgs& s, int64_t blocks, hipStream_t stream) {
 template <typename InT, int NP, int KS, bool ASYNC>
 hipError_t launch_scan_ks(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs s, hipStream_t stream) {
   // K and Q of a chunk side by side fit in LDS except for float32 past 128 entries
-  constexpr bool QLDS = Stage<InT, NP, KS, kOutputs, true, 3>::kBytes <= kMaxLds;
+  constexpr bool QLDS = Stage<InT, NP, KS, kOutputs, true>::kBytes <= kMaxLds;
   const int64_t items = p.B * p.Hv * plan.pieces;
   s.items = static_cast<int>(items);
   if (plan.pieces > 1) {
     const int strips = 2 * KS + s.cols / 16;
     s.col_blocks = (strips + kWaves - 1) / kWaves;
-    hipError_t e = launch_walk<InT, NP, KS, kAggregates, QLDS, ASYNC, 3>(s, placed_blocks(items, s.col_blocks), stream);
+    hipError_t e = launch_walk<InT, NP, KS, kAggregates, QLDS, ASYNC, false>(s, placed_blocks(items, s.col_blocks), stream);
     if (e != hipSuccess) return e;
     if ((e = launch_delta_fold(p, plan, s, stream)) != hipSuccess) return e;
   }
   s.col_blocks = (s.cols / 16 + kWaves - 1) / kWaves;
   const int64_t blocks = placed_blocks(items, s.col_blocks);
-  if (s.states) return launch_walk<InT, NP, KS, kStates, QLDS, ASYNC, 3>(s, blocks, stream);
-  if (NP == 1 && s.out_bf16) return launch_walk<InT, NP, KS, kOutputs, QLDS, ASYNC, NP == 1 ? 2 : 3>(s, blocks, stream);
-  return launch_walk<InT, NP, KS, kOutputs, QLDS, ASYNC, 3>(s, blocks, stream);
+  if (s.states) return launch_walk<InT, NP, KS, kStates, QLDS, ASYNC, false>(s, blocks, stream);
+  if (NP == 1 && s.out_bf16) return launch_walk<InT, NP, KS, kOutputs, QLDS, ASYNC, NP == 1>(s, blocks, stream);
+  return launch_walk<InT, NP, KS, kOutputs, QLDS, ASYNC, false>(s, blocks, stream);
 }
 
 template <typename InT, int NP, bool ASYNC>
