@@ -454,8 +454,9 @@ ssm_status ssm_scan_bwd(const ssm_scan_bwd_params* p, void* hip_stream);
  * Arithmetic has float32's precision whatever in_dtype is (products on the matrix
  * cores carry each operand in three bfloat16 parts, 24 bits, with float32 sums); only
  * out is rounded, to out_dtype. Outputs must not overlap inputs, each other or the
- * workspace. A non-finite input may make every output of its head NaN from the start
- * of its 64-step chunk on, also past a reset.
+ * workspace. A non-finite input reaches what the recurrence hands it on to: from its step
+ * to the end of its document, the other columns too unless it is in v or h0. (The 16
+ * columns around one that it reaches are then worked out step by step, about 2 us a step.)
  */
 typedef struct {
   int64_t batch, seqlen, key_heads, value_heads, dk, dv;
@@ -541,6 +542,8 @@ ssm_status ssm_delta_update(const ssm_delta_update_params* p, void* hip_stream);
  *            kept there (8 dk dv bytes per chunk and value head, dk rounded up to
  *            a multiple of 32 and dv to 16, and 57 KB + 512 dv bytes besides).
  * dA and d_dt_bias are sums in a fixed order, so repeated calls give identical bits.
+ * A non-finite input (one that is used: a gate at a reset is not) may make any gradient of
+ * its head and its key head NaN, in other documents of the row and before its step too.
  */
 typedef struct {
   int64_t batch, seqlen, key_heads, value_heads, dk, dv;

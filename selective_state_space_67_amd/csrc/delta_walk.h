@@ -162,6 +162,112 @@ __device__ __forceinline__ void stage_sync(char* st, const ChunkArgs& a, const C
   }
 }
 
+// Sum over the four lanes of a wave that hold the rows of one column.
+__device__ __forceinline__ float column_sum(float x) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// 0 as long as every x that went in was finite, else NaN.
+__device__ __forceinline__ float finite_so_far(float so_far, float x) { return __builtin_fmaf(0.0f, x, so_far); }
+
+// The last token up to `from` of a row at which a document starts; -1 if there is none.
+__device__ __forceinline__ int64_t last_start(const uint8_t* reset, int64_t from, int lane) {
+  for (int64_t t = from; t >= 0; t -= 64) {
+    const uint64_t starts = __ballot(t - lane >= 0 && reset[max(t - lane, int64_t{0})] != 0);
+    if (starts) return t - __builtin_ctzll(starts);
+  }
+  return -1;
+}
+
+// The piece's tokens again, one by one in the step form's arithmetic: a strip's outputs and,
+// in H, its state after them.
+//
+// A chunk's products multiply 0 by whatever stands before a document's start or after a
+// token, and the fold does so with the pieces before, so that a NaN or an infinity among the
+// inputs reaches tokens that the recurrence keeps it from. A strip that has made a non-finite
+// output therefore goes through its piece again here, and what is not finite afterwards is so
+// by the recurrence. About 2 us a token, on such inputs alone.
+//
+// The arguments are read anew from where the kernel was passed them, and the lane's place is
+// hidden from the compiler: it would otherwise work out what it can of this ahead of the walk
+// (1 x 37 x 16 heads: 18.8 us without this, 20.5 with, 19.3 so; 8 x 2048 x 12 heads: 212, 219, 215).
+template <typename InT, int KS>
+__device__ __forceinline__ void piece_again(int bh, int piece, int own, int lane, f32x4 (&H)[2 * KS]) {
+  uint64_t passed = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+  asm volatile("" : "+s"(passed), "+s"(bh), "+s"(piece), "+v"(own), "+v"(lane));
+  const ScanArgs& s = *reinterpret_cast<const ScanArgs*>(passed);
+  const ChunkArgs& a = s.c;
+  const int b = bh / a.Hv, h = bh - b * a.Hv, hk = h / a.group, g4 = (lane >> 4) * 4;
+  const int64_t first = static_cast<int64_t>(piece) * s.chunks_piece * kChunk;
+  const int64_t end = min(a.L, first + static_cast<int64_t>(s.chunks_piece) * kChunk);
+  const bool has_v = own < a.dv;
+  int64_t t = first;
+  float finite = 0.0f;
+#pragma unroll
+  for (int m = 0; m < 2 * KS; ++m)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = state_row(m, g4, r);
+      H[m][r] = 0.0f;
+      if (piece > 0) {
+        if (own < s.cols) H[m][r] = s.starts[((static_cast<int64_t>(bh) * s.pieces + piece) * (32 * KS) + row) * s.cols + own];
+      } else if (s.h0 && row < a.dk && has_v) {
+        H[m][r] = s.h0[(static_cast<int64_t>(bh) * a.dk + row) * a.dv + own];
+      }
+      finite = finite_so_far(finite, H[m][r]);
+    }
+  // Where no document starts up to here, a state that is not finite is so by the recurrence.
+  if (piece > 0 && a.reset && __any(finite != 0.0f)) {
+    const int64_t start = last_start(a.reset + static_cast<int64_t>(b) * a.L, first, lane);
+    if (start >= 0) t = start;
+  }
+  const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+#pragma unroll 1
+  for (; t < end; ++t) {
+    const int64_t row = static_cast<int64_t>(b) * a.L + t, gate = row * a.Hv + h;
+    const InT* q = static_cast<const InT*>(a.q) + row * a.qs + static_cast<int64_t>(hk) * a.dk;
+    const InT* k = static_cast<const InT*>(a.k) + row * a.ks + static_cast<int64_t>(hk) * a.dk;
+    const float v = has_v ? load_elem(static_cast<const InT*>(a.v), row * a.vs + static_cast<int64_t>(h) * a.dv + own) : 0.0f;
+    float al = fast_exp2(A * softplus_f32(load_elem(static_cast<const InT*>(a.dt), gate) + bias) * kLog2e);
+    const float beta = a.beta_scale * fast_rcp(1.0f + fast_exp2(-load_elem(static_cast<const InT*>(a.br), gate) * kLog2e));
+    if (a.reset && a.reset[row]) {
+      al = 0.0f;
+#pragma unroll
+      for (int m = 0; m < 2 * KS; ++m) H[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    f32x4 kv[2 * KS];
+    float kh = 0.0f, qh = 0.0f, kq = 0.0f;
+    int dk = a.dk;
+    asm volatile("" : "+v"(dk));  // or the rows' masks are kept from token to token
+#pragma unroll
+    for (int m = 0; m < 2 * KS; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = state_row(m, g4, r);
+        kv[m][r] = d < dk ? load_elem(k, d) : 0.0f;
+        const float qv = d < dk ? load_elem(q, d) : 0.0f;
+        kh = __builtin_fmaf(kv[m][r], H[m][r], kh);
+        qh = __builtin_fmaf(qv, H[m][r], qh);
+        kq = __builtin_fmaf(kv[m][r], qv, kq);
+      }
+    const float u = beta * __builtin_fmaf(-al, column_sum(kh), v);
+    const float o = a.scale * __builtin_fmaf(al, column_sum(qh), column_sum(kq) * u);
+#pragma unroll
+    for (int m = 0; m < 2 * KS; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) H[m][r] = __builtin_fmaf(al, H[m][r], kv[m][r] * u);
+    if (t >= first && has_v && g4 == 0) {
+      if (s.out_bf16)
+        store_elem(static_cast<bf16_t*>(s.out), gate * a.dv + own, o);
+      else
+        store_elem(static_cast<float*>(s.out), gate * a.dv + own, o);
+    }
+  }
+}
+
 // One wave's walk over the chunks of a piece with 16 columns of the state.
 //
 // Bound by the chain of dependent steps of a chunk: K H0, R, T R, P U and K^T U follow
@@ -213,6 +319,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
       }
     }
   }
+  float finite = 0.0f;  // NaN once an output is not (OUT)
 
   const int c0 = piece * s.chunks_piece, c1 = min(a.chunks, c0 + s.chunks_piece);
   ChunkSource<InT> src = chunk_source<InT>(s, bh, b, h, c0);
@@ -354,6 +461,10 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
     }
 
     if constexpr (OUT) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) finite = finite_so_far(finite, Y[m][r]);
       const int64_t row0 = (static_cast<int64_t>(b) * a.L + static_cast<int64_t>(c) * kChunk) * a.Hv + h;  // x dv
       if (OUT16 && (ASYNC || s.out_runs)) {  // ASYNC has whole runs everywhere
         // The strip's place among the staged values is this wave's alone and has been
@@ -392,6 +503,11 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_scan(const ScanArgs s) {
       }
     }
     src = next;
+  }
+
+  if (OUT && __builtin_expect(__any(finite != 0.0f), 0)) {
+    __threadfence();  // what other lanes have written of the strip's outputs comes before what follows
+    piece_again<InT, KS>(bh, piece, own, lane, H);
   }
 
   if (AGG) {

@@ -110,3 +110,44 @@ def test_a_reset_tokens_gate_has_no_gradient():
     torch.cuda.synchronize()
     for n, want in ref.items():
         check(g[n], want, GRAD, n)
+
+
+RESETS = [(0, 40), (0, 75), (0, 150), (0, 200)]
+PLACES = {"q": (0, 10, 0, 3), "k": (0, 10, 0, 3), "v": (0, 10, 1, 5), "dt_raw": (0, 10, 1), "beta_raw": (0, 10, 1),
+          "h0": (0, 1, 3, 5)}
+
+
+@pytest.mark.parametrize("dtype,L,dk,dv,pieces", [(wl.F32, 30, 32, 24, 0), (wl.F32, 100, 32, 24, 1),
+                                                  (wl.BF16, 230, 64, 40, 1), (wl.BF16, 230, 64, 40, 3),
+                                                  (wl.BF16, 100, 33, 21, 1), (wl.F32, 300, 160, 24, 2),
+                                                  (wl.BF16, 1500, 64, 32, 20)])
+@pytest.mark.parametrize("name,value", [("q", np.nan), ("k", np.nan), ("v", np.nan), ("v", np.inf), ("v", 3.4e38),
+                                        ("dt_raw", np.nan), ("beta_raw", np.nan), ("h0", np.inf), ("h0", np.nan)])
+def test_what_a_non_finite_value_reaches(name, value, dtype, L, dk, dv, pieces):
+    """From its token on, to the end of its document: neither the tokens before it, nor other
+    documents of its row, nor (of v and h0) other columns, whatever the length and the pieces."""
+    if name == "v" and np.isfinite(value) and dtype == wl.BF16:
+        value = 3.38e38  # the largest finite bfloat16 is 3.3895e38
+    x = delta_inputs(1, L, 1, 2, dk, dv, dtype, seed=L + dk, resets=RESETS if L > 40 else [(0, 20)], state=True)
+    ref, rh = od.delta_fwd(**wide(x), reset=x["reset"], scale=1.0)
+    put(x, name, PLACES[name], value)
+    print(name, value, dtype, L, pieces, flush=True)
+    out, hl = forward(x, scale=1.0, num_segments=pieces)
+    hit = np.zeros(out.shape, bool)
+    token = 0 if name == "h0" else 10
+    end = 40 if L > 40 else 20
+    if name == "q":
+        hit[:, 10] = True
+    elif name == "k":
+        hit[:, 10:end] = True
+    else:
+        columns = [PLACES[name][-1]] if name in ("v", "h0") else slice(None)
+        hit[:, token:end, 1, columns] = True
+    if np.isfinite(value):  # very large: float32 may or may not overflow there
+        out = np.where(hit, 0.0, out)
+        ref = np.where(hit, 0.0, ref)
+    else:
+        assert not np.isfinite(out[hit]).any()
+        out, ref = np.where(hit, 0.0, out), np.where(hit, 0.0, ref)
+    check(out, ref, STATE, "out elsewhere")
+    check(hl, rh, STATE, "h_last")
