@@ -3,6 +3,11 @@
 Argument marshalling only, as in binding.py. Tensors q, k, v may be slices of
 one packed projection: heads are dense inside a token, tokens lie a fixed
 stride apart, batch rows follow each other. Everything else is contiguous.
+
+A call runs on ``stream``, by default the device's current one. What it allocates
+belongs to that stream, and results are marked as used on the current one too, so
+that neither is handed out again while work on them is under way. Inputs are the
+caller's: made on another stream, they have to be ready and to stay alive there.
 """
 from __future__ import annotations
 
@@ -108,14 +113,37 @@ def _tokens(t, shape, name, dtype):
     return step
 
 
-def _workspace(size_fn, p, workspace, device):
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor of the stream that the call runs on: its memory goes back to
+    that stream's, where whatever takes it next comes after the call's own work."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(shape, dtype, device, stream):
+    """_empty for what the caller gets, who may use and drop it on the current stream."""
+    t = _empty(shape, dtype, device, stream)
+    if stream is not None:
+        import torch
+
+        current = torch.cuda.current_stream(device)
+        if current != stream:
+            t.record_stream(current)
+    return t
+
+
+def _workspace(size_fn, p, workspace, device, stream):
     import torch
 
     n = ctypes.c_size_t(0)
     _b._check(size_fn(ctypes.byref(p), ctypes.byref(n)))
     if n.value:
         if workspace is None or workspace.numel() * workspace.element_size() < n.value:
-            workspace = torch.empty(int(n.value), dtype=torch.uint8, device=device)
+            workspace = _empty(int(n.value), torch.uint8, device, stream)
         p.workspace = workspace.data_ptr()
         p.workspace_bytes = workspace.numel() * workspace.element_size()
     return workspace
@@ -169,9 +197,10 @@ def ssm_delta_fwd(q, k, v, dt_raw, A, beta_raw, *, dt_bias=None, reset=None, h0=
 
     lib = _b.load_library()
     if out is None:
-        out = torch.empty(v.shape, dtype=out_dtype or torch.float32, device=v.device)
+        dt = out_dtype or torch.float32
+        out = torch.empty(v.shape, dtype=dt, device=v.device) if stream is None else _result(v.shape, dt, v.device, stream)
     p = _delta_params(q, k, v, dt_raw, A, beta_raw, dt_bias, reset, h0, h_last, out, scale, beta_scale, num_segments)
-    workspace = _workspace(lib.ssm_delta_workspace_size, p, workspace, v.device)
+    workspace = _workspace(lib.ssm_delta_workspace_size, p, workspace, v.device, stream)
     _b._check(lib.ssm_delta_fwd(ctypes.byref(p), _stream(stream, v.device)))
     return out
 
@@ -196,7 +225,8 @@ def ssm_delta_update(h, q, k, v, dt_raw, A, beta_raw, *, dt_bias=None, out=None,
 
     lib = _b.load_library()
     if out is None:
-        out = torch.empty(v.shape, dtype=out_dtype or torch.float32, device=v.device)
+        dt = out_dtype or torch.float32
+        out = torch.empty(v.shape, dtype=dt, device=v.device) if stream is None else _result(v.shape, dt, v.device, stream)
     p = _delta_update_params(h, q, k, v, dt_raw, A, beta_raw, dt_bias, out, scale, beta_scale)
     _b._check(lib.ssm_delta_update(ctypes.byref(p), _stream(stream, v.device)))
     return out
@@ -210,7 +240,8 @@ def prepare_delta_update(h, q, k, v, dt_raw, A, beta_raw, *, dt_bias=None, out=N
 
     lib = _b.load_library()
     if out is None:
-        out = torch.empty(v.shape, dtype=out_dtype or torch.float32, device=v.device)
+        dt = out_dtype or torch.float32
+        out = torch.empty(v.shape, dtype=dt, device=v.device) if stream is None else _result(v.shape, dt, v.device, stream)
     p = _delta_update_params(h, q, k, v, dt_raw, A, beta_raw, dt_bias, out, scale, beta_scale)
     st, fn, pref = _stream(stream, v.device), lib.ssm_delta_update, ctypes.byref(p)
 
@@ -244,19 +275,20 @@ def ssm_delta_bwd(q, k, v, dt_raw, A, beta_raw, dout, *, dt_bias=None, reset=Non
     for t, name in ((h0, "h0"), (dh_last, "dh_last")):
         if t is not None:
             _need(t, (B, Hv, dk, dv), name, torch.float32)
-    gd, dev = grad_dtype or torch.float32, q.device
-    g = dict(dq=torch.empty((B, L, Hk, dk), dtype=gd, device=dev), dk=torch.empty((B, L, Hk, dk), dtype=gd, device=dev),
-             dv=torch.empty((B, L, Hv, dv), dtype=gd, device=dev), d_dt_raw=torch.empty((B, L, Hv), dtype=gd, device=dev),
-             dbeta_raw=torch.empty((B, L, Hv), dtype=gd, device=dev),
-             dA=torch.empty((Hv,), dtype=torch.float32, device=dev),
-             d_dt_bias=torch.empty((Hv,), dtype=torch.float32, device=dev) if want_d_dt_bias else None,
-             dh0=torch.empty((B, Hv, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None)
+    gd, f32, dev = grad_dtype or torch.float32, torch.float32, q.device
+
+    def new(shape, dtype):
+        return _result(shape, dtype, dev, stream)
+
+    g = dict(dq=new((B, L, Hk, dk), gd), dk=new((B, L, Hk, dk), gd), dv=new((B, L, Hv, dv), gd),
+             d_dt_raw=new((B, L, Hv), gd), dbeta_raw=new((B, L, Hv), gd), dA=new((Hv,), f32),
+             d_dt_bias=new((Hv,), f32) if want_d_dt_bias else None, dh0=new((B, Hv, dk, dv), f32) if want_dh0 else None)
     p = DeltaBwdParams(*sizes, _b._dtype_code(q), _b._dtype_code(g["dq"]), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                        *strides, dt_raw.data_ptr(), beta_raw.data_ptr(), _addr(dt_bias), A.data_ptr(), _addr(reset),
                        _addr(h0), dout.data_ptr(), _addr(dh_last), g["dq"].data_ptr(), g["dk"].data_ptr(),
                        g["dv"].data_ptr(), g["d_dt_raw"].data_ptr(), g["dbeta_raw"].data_ptr(), g["dA"].data_ptr(),
                        _addr(g["d_dt_bias"]), _addr(g["dh0"]), None, 0, dk ** -0.5 if scale is None else scale, beta_scale)
-    workspace = _workspace(lib.ssm_delta_bwd_workspace_size, p, workspace, dev)
+    workspace = _workspace(lib.ssm_delta_bwd_workspace_size, p, workspace, dev, stream)
     _b._check(lib.ssm_delta_bwd(ctypes.byref(p), _stream(stream, dev)))
     return g
 
@@ -306,9 +338,10 @@ def ssm_qk_norm_fwd(q, k, *, wq=None, wk=None, kind="rms", eps=1e-6, cos=None, s
     lib = _b.load_library()
     dt = out_dtype or torch.float32
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+        q_out = torch.empty(q.shape, dtype=dt, device=q.device) if stream is None else _result(q.shape, dt, q.device, stream)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=q_out.dtype, device=k.device)
+        k_out = (torch.empty(k.shape, dtype=q_out.dtype, device=k.device) if stream is None
+                 else _result(k.shape, q_out.dtype, k.device, stream))
     p = _norm_params(q, k, wq, wk, kind, eps, cos, sin, positions, interleaved)
     _need(q_out, q.shape, "q_out", q_out.dtype)
     _need(k_out, k.shape, "k_out", q_out.dtype)
@@ -326,15 +359,15 @@ def ssm_qk_norm_bwd(q, k, dq_out, dk_out, *, wq=None, wk=None, kind="rms", eps=1
 
     lib = _b.load_library()
     dt = grad_dtype or torch.float32
-    g = dict(dq=torch.empty(q.shape, dtype=dt, device=q.device), dk=torch.empty(k.shape, dtype=dt, device=k.device))
+    g = dict(dq=_result(q.shape, dt, q.device, stream), dk=_result(k.shape, dt, k.device, stream))
     for name in ("dwq", "dwk"):
-        g[name] = torch.empty(q.shape[3], dtype=torch.float32, device=q.device) if want_dw else None
+        g[name] = _result(q.shape[3], torch.float32, q.device, stream) if want_dw else None
     p = _norm_params(q, k, wq, wk, kind, eps, cos, sin, positions, interleaved)
     _need(dq_out, q.shape, "dq_out", q.dtype)
     _need(dk_out, k.shape, "dk_out", q.dtype)
     p.out_dtype = _b._dtype_code(g["dq"])
     p.dq_out, p.dk_out, p.dq, p.dk = dq_out.data_ptr(), dk_out.data_ptr(), g["dq"].data_ptr(), g["dk"].data_ptr()
     p.dwq, p.dwk = _addr(g["dwq"]), _addr(g["dwk"])
-    workspace = _workspace(lib.ssm_qk_norm_bwd_workspace_size, p, workspace, q.device)
+    workspace = _workspace(lib.ssm_qk_norm_bwd_workspace_size, p, workspace, q.device, stream)
     _b._check(lib.ssm_qk_norm_bwd(ctypes.byref(p), _stream(stream, q.device)))
     return g
