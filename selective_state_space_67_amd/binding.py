@@ -5,6 +5,11 @@ pointers and the current HIP stream from torch tensors, fill the C parameter
 structs and call the library. Every step of the computation runs in the
 library's HIP kernels; there is no fallback of any kind. If the library is
 missing (not built) the first call raises.
+
+A call runs on ``stream``, by default the device's current one. What it allocates
+belongs to that stream, and results are marked as used on the current one too, so
+that neither is handed out again while work on them is under way. Inputs are the
+caller's: made on another stream, they have to be ready and to stay alive there.
 """
 from __future__ import annotations
 
@@ -180,6 +185,30 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor of the stream that the call runs on: its memory goes back to
+    that stream's, where whatever takes it next comes after the call's own work."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _result(shape, dtype, device, stream):
+    """_empty for what the caller gets, who may use and drop it on the current stream."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    t = _empty(shape, dtype, device, stream)
+    current = torch.cuda.current_stream(device)
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
 def _scan_params(u, dt_raw, A, Bm, Cm, dt_bias, Dskip, z, reset, h0, out, h_last, out_dtype,
                  num_segments, conv_w=None, conv_b=None, conv_state_in=None, conv_state_out=None, zoh=False,
                  cplx=False):
@@ -245,8 +274,8 @@ def ssm_scan_aggregate(u, dt_raw, A, Bm, *, dt_bias=None, reset=None, conv_w=Non
     Bt, D, _ = u.shape
     N = A.shape[1]
     shape = (Bt, D, N, 2) if complex_state else (Bt, D, N)
-    P = torch.empty(shape, dtype=torch.float32, device=u.device) if P is None else P
-    H = torch.empty(shape, dtype=torch.float32, device=u.device) if H is None else H
+    P = _result(shape, torch.float32, u.device, stream) if P is None else P
+    H = _result(shape, torch.float32, u.device, stream) if H is None else H
     _need(P, shape, "P", torch.float32)
     _need(H, shape, "H", torch.float32)
     p = _scan_params(u, dt_raw, A, Bm, None, dt_bias, None, None, reset, None, None, None, None, num_segments,
@@ -254,7 +283,7 @@ def ssm_scan_aggregate(u, dt_raw, A, Bm, *, dt_bias=None, reset=None, conv_w=Non
     n = ctypes.c_size_t(0)
     _check(lib.ssm_scan_aggregate_workspace_size(ctypes.byref(p), ctypes.byref(n)))
     if n.value and (workspace is None or workspace.numel() * workspace.element_size() < n.value):
-        workspace = torch.empty(int(n.value), dtype=torch.uint8, device=u.device)
+        workspace = _empty(int(n.value), torch.uint8, u.device, stream)
     if n.value:
         p.workspace = _ptr(workspace)
         p.workspace_bytes = workspace.numel() * workspace.element_size()
@@ -272,15 +301,15 @@ def prepare_aggregate(u, dt_raw, A, Bm, *, dt_bias=None, reset=None, conv_w=None
     Bt, D, _ = u.shape
     N = A.shape[1]
     shape = (Bt, D, N, 2) if complex_state else (Bt, D, N)
-    P = torch.empty(shape, dtype=torch.float32, device=u.device) if P is None else P
-    H = torch.empty(shape, dtype=torch.float32, device=u.device) if H is None else H
+    P = _result(shape, torch.float32, u.device, stream) if P is None else P
+    H = _result(shape, torch.float32, u.device, stream) if H is None else H
     _need(P, shape, "P", torch.float32)
     _need(H, shape, "H", torch.float32)
     p = _scan_params(u, dt_raw, A, Bm, None, dt_bias, None, None, reset, None, None, None, None, num_segments,
                      conv_w, conv_b, conv_state_in, None, zoh, complex_state)
     n = ctypes.c_size_t(0)
     _check(lib.ssm_scan_aggregate_workspace_size(ctypes.byref(p), ctypes.byref(n)))
-    ws = torch.empty(max(int(n.value), 1), dtype=torch.uint8, device=u.device)
+    ws = _empty(max(int(n.value), 1), torch.uint8, u.device, stream)
     if n.value:
         p.workspace = _ptr(ws)
         p.workspace_bytes = int(n.value)
@@ -335,14 +364,14 @@ def ssm_scan_fwd(u, dt_raw, A, Bm, Cm, *, dt_bias=None, Dskip=None, z=None, rese
 
     lib = load_library()
     if out is None:
-        out = torch.empty(u.shape, dtype=out_dtype or torch.float32, device=u.device)
+        out = _result(u.shape, out_dtype or torch.float32, u.device, stream)
     p = _scan_params(u, dt_raw, A, Bm, Cm, dt_bias, Dskip, z, reset, h0, out, h_last, out_dtype,
                      num_segments, conv_w, conv_b, conv_state_in, conv_state_out, zoh, complex_state)
     n = ctypes.c_size_t(0)
     _check(lib.ssm_scan_workspace_size(ctypes.byref(p), ctypes.byref(n)))
     if n.value:
         if workspace is None or workspace.numel() * workspace.element_size() < n.value:
-            workspace = torch.empty(int(n.value), dtype=torch.uint8, device=u.device)
+            workspace = _empty(int(n.value), torch.uint8, u.device, stream)
         p.workspace = _ptr(workspace)
         p.workspace_bytes = workspace.numel() * workspace.element_size()
     _check(lib.ssm_scan_fwd(ctypes.byref(p), _stream(stream, u.device)))
@@ -372,7 +401,7 @@ def ssm_scan_fwd_wavefront(u, dt_raw, A, Bm, Cm, *, dt_bias=None, Dskip=None, z=
 
     lib = load_library()
     if out is None:
-        out = torch.empty(u.shape, dtype=out_dtype or torch.float32, device=u.device)
+        out = _result(u.shape, out_dtype or torch.float32, u.device, stream)
     p = _scan_params(u, dt_raw, A, Bm, Cm, dt_bias, Dskip, z, reset, h0, out, h_last, out_dtype,
                      0, None, None, None, None, False, False)
     _check(lib.ssm_scan_fwd_wavefront(ctypes.byref(p), _stream(stream, u.device)))
@@ -390,7 +419,7 @@ def prepare_scan(u, dt_raw, A, Bm, Cm, *, dt_bias=None, Dskip=None, z=None, rese
 
     lib = load_library()
     if out is None:
-        out = torch.empty(u.shape, dtype=out_dtype or torch.float32, device=u.device)
+        out = _result(u.shape, out_dtype or torch.float32, u.device, stream)
     p = _scan_params(u, dt_raw, A, Bm, Cm, dt_bias, Dskip, z, reset, h0, out, h_last, out_dtype,
                      num_segments, conv_w, conv_b, conv_state_in, conv_state_out, zoh, complex_state)
     n = ctypes.c_size_t(0)
@@ -399,7 +428,7 @@ def prepare_scan(u, dt_raw, A, Bm, Cm, *, dt_bias=None, Dskip=None, z=None, rese
     keep = [u, dt_raw, A, Bm, Cm, dt_bias, Dskip, z, reset, h0, out, h_last, conv_w, conv_b, conv_state_in,
             conv_state_out]
     if n.value:
-        ws = torch.empty(int(n.value), dtype=torch.uint8, device=u.device)
+        ws = _empty(int(n.value), torch.uint8, u.device, stream)
         keep.append(ws)
         p.workspace = _ptr(ws)
         p.workspace_bytes = int(n.value)
@@ -425,7 +454,7 @@ def prepare_state_update(h, u, dt_raw, A, Bm, Cm, *, dt_bias=None, Dskip=None, z
     lib = load_library()
     Bt, D, N = h.shape[:3]
     if out is None:
-        out = torch.empty((Bt, D), dtype=out_dtype or torch.float32, device=u.device)
+        out = _result((Bt, D), out_dtype or torch.float32, u.device, stream)
     p = _update_params(h, u, dt_raw, A, Bm, Cm, dt_bias, Dskip, z, out, zoh=zoh, cplx=complex_state)
     st = _stream(stream, u.device)
     fn = lib.ssm_state_update
@@ -490,7 +519,7 @@ def ssm_state_update(h, u, dt_raw, A, Bm, Cm, *, dt_bias=None, Dskip=None, z=Non
     lib = load_library()
     Bt, D, N = h.shape[:3]
     if out is None:
-        out = torch.empty((Bt, D), dtype=out_dtype or torch.float32, device=u.device)
+        out = _result((Bt, D), out_dtype or torch.float32, u.device, stream)
     p = _update_params(h, u, dt_raw, A, Bm, Cm, dt_bias, Dskip, z, out, conv_w, conv_b, conv_state, zoh,
                        complex_state)
     _check(lib.ssm_state_update(ctypes.byref(p), _stream(stream, u.device)))
@@ -541,7 +570,7 @@ def _bwd_params(u, dt_raw, A, Bm, Cm, dout, dt_bias, Dskip, z, reset, h0, dh_las
     return p
 
 
-def _bwd_grads(u, A, Bm, z, grad_dtype, want_dD, want_dbias, want_dh0, cplx=False):
+def _bwd_grads(u, A, Bm, z, grad_dtype, want_dD, want_dbias, want_dh0, cplx=False, stream=None):
     import torch
 
     Bt, D, L = u.shape
@@ -550,15 +579,15 @@ def _bwd_grads(u, A, Bm, z, grad_dtype, want_dD, want_dbias, want_dh0, cplx=Fals
     gd = grad_dtype or torch.float32
     f32 = torch.float32
     c2 = (2,) if cplx else ()
-    return dict(du=torch.empty((Bt, D, L), dtype=gd, device=dev),
-                d_dt_raw=torch.empty((Bt, D, L), dtype=gd, device=dev),
-                dz=torch.empty((Bt, D, L), dtype=gd, device=dev) if z is not None else None,
-                dA=torch.empty((D, N) + c2, dtype=f32, device=dev),
-                dBm=torch.empty((Bt, L, N) + c2, dtype=f32, device=dev),
-                dCm=torch.empty((Bt, L, N) + c2, dtype=f32, device=dev),
-                dDskip=torch.empty((D,), dtype=f32, device=dev) if want_dD else None,
-                d_dt_bias=torch.empty((D,), dtype=f32, device=dev) if want_dbias else None,
-                dh0=torch.empty((Bt, D, N) + c2, dtype=f32, device=dev) if want_dh0 else None)
+    return dict(du=_result((Bt, D, L), gd, dev, stream),
+                d_dt_raw=_result((Bt, D, L), gd, dev, stream),
+                dz=_result((Bt, D, L), gd, dev, stream) if z is not None else None,
+                dA=_result((D, N) + c2, f32, dev, stream),
+                dBm=_result((Bt, L, N) + c2, f32, dev, stream),
+                dCm=_result((Bt, L, N) + c2, f32, dev, stream),
+                dDskip=_result((D,), f32, dev, stream) if want_dD else None,
+                d_dt_bias=_result((D,), f32, dev, stream) if want_dbias else None,
+                dh0=_result((Bt, D, N) + c2, f32, dev, stream) if want_dh0 else None)
 
 
 def ssm_scan_bwd(u, dt_raw, A, Bm, Cm, dout, *, dt_bias=None, Dskip=None, z=None, reset=None, h0=None,
@@ -580,20 +609,20 @@ def ssm_scan_bwd(u, dt_raw, A, Bm, Cm, dout, *, dt_bias=None, Dskip=None, z=None
     import torch
 
     lib = load_library()
-    grads = _bwd_grads(u, A, Bm, z, grad_dtype, want_dDskip, want_d_dt_bias, want_dh0, complex_state)
+    grads = _bwd_grads(u, A, Bm, z, grad_dtype, want_dDskip, want_d_dt_bias, want_dh0, complex_state, stream)
     if conv_w is not None:
         Bt, D, _ = u.shape
         K = conv_w.shape[1]
-        grads["dconv_w"] = torch.empty((D, K), dtype=torch.float32, device=u.device)
-        grads["dconv_b"] = torch.empty((D,), dtype=torch.float32, device=u.device)
-        grads["dconv_state_in"] = (torch.empty((Bt, D, K - 1), dtype=torch.float32, device=u.device)
+        grads["dconv_w"] = _result((D, K), torch.float32, u.device, stream)
+        grads["dconv_b"] = _result((D,), torch.float32, u.device, stream)
+        grads["dconv_state_in"] = (_result((Bt, D, K - 1), torch.float32, u.device, stream)
                                    if K > 1 else None)
     p = _bwd_params(u, dt_raw, A, Bm, Cm, dout, dt_bias, Dskip, z, reset, h0, dh_last, grads,
                     (conv_w, conv_b, conv_state_in), zoh, complex_state)
     n = ctypes.c_size_t(0)
     _check(lib.ssm_scan_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)))
     if workspace is None or workspace.numel() * workspace.element_size() < n.value:
-        workspace = torch.empty(int(n.value), dtype=torch.uint8, device=u.device)
+        workspace = _empty(int(n.value), torch.uint8, u.device, stream)
     p.workspace = _ptr(workspace)
     p.workspace_bytes = workspace.numel() * workspace.element_size()
     _check(lib.ssm_scan_bwd(ctypes.byref(p), _stream(stream, u.device)))
@@ -609,19 +638,19 @@ def prepare_scan_bwd(u, dt_raw, A, Bm, Cm, dout, *, dt_bias=None, Dskip=None, z=
     import torch
 
     lib = load_library()
-    grads = _bwd_grads(u, A, Bm, z, grad_dtype, True, True, True, complex_state)
+    grads = _bwd_grads(u, A, Bm, z, grad_dtype, True, True, True, complex_state, stream)
     if conv_w is not None:
         Bt, D, _ = u.shape
         K = conv_w.shape[1]
-        grads["dconv_w"] = torch.empty((D, K), dtype=torch.float32, device=u.device)
-        grads["dconv_b"] = torch.empty((D,), dtype=torch.float32, device=u.device)
-        grads["dconv_state_in"] = (torch.empty((Bt, D, K - 1), dtype=torch.float32, device=u.device)
+        grads["dconv_w"] = _result((D, K), torch.float32, u.device, stream)
+        grads["dconv_b"] = _result((D,), torch.float32, u.device, stream)
+        grads["dconv_state_in"] = (_result((Bt, D, K - 1), torch.float32, u.device, stream)
                                    if K > 1 else None)
     p = _bwd_params(u, dt_raw, A, Bm, Cm, dout, dt_bias, Dskip, z, reset, h0, dh_last, grads,
                     (conv_w, conv_b, conv_state_in), zoh, complex_state)
     n = ctypes.c_size_t(0)
     _check(lib.ssm_scan_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)))
-    ws = torch.empty(int(n.value), dtype=torch.uint8, device=u.device)
+    ws = _empty(int(n.value), torch.uint8, u.device, stream)
     p.workspace = _ptr(ws)
     p.workspace_bytes = int(n.value)
     st = _stream(stream, u.device)

@@ -4,10 +4,7 @@ Argument marshalling only, as in binding.py. Tensors q, k, v may be slices of
 one packed projection: heads are dense inside a token, tokens lie a fixed
 stride apart, batch rows follow each other. Everything else is contiguous.
 
-A call runs on ``stream``, by default the device's current one. What it allocates
-belongs to that stream, and results are marked as used on the current one too, so
-that neither is handed out again while work on them is under way. Inputs are the
-caller's: made on another stream, they have to be ready and to stay alive there.
+Streams as in binding.py: what a call allocates belongs to the stream that it runs on.
 """
 from __future__ import annotations
 
@@ -113,27 +110,9 @@ def _tokens(t, shape, name, dtype):
     return step
 
 
-def _empty(shape, dtype, device, stream):
-    """An uninitialised tensor of the stream that the call runs on: its memory goes back to
-    that stream's, where whatever takes it next comes after the call's own work."""
-    import torch
-
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _result(shape, dtype, device, stream):
-    """_empty for what the caller gets, who may use and drop it on the current stream."""
-    t = _empty(shape, dtype, device, stream)
-    if stream is not None:
-        import torch
-
-        current = torch.cuda.current_stream(device)
-        if current != stream:
-            t.record_stream(current)
-    return t
+def _out(t, dtype, stream):
+    """An output of t's shape (torch's empty_like would keep t's strides)."""
+    return _b._result(t.shape, dtype, t.device, stream)
 
 
 def _workspace(size_fn, p, workspace, device, stream):
@@ -143,7 +122,7 @@ def _workspace(size_fn, p, workspace, device, stream):
     _b._check(size_fn(ctypes.byref(p), ctypes.byref(n)))
     if n.value:
         if workspace is None or workspace.numel() * workspace.element_size() < n.value:
-            workspace = _empty(int(n.value), torch.uint8, device, stream)
+            workspace = _b._empty(int(n.value), torch.uint8, device, stream)
         p.workspace = workspace.data_ptr()
         p.workspace_bytes = workspace.numel() * workspace.element_size()
     return workspace
@@ -197,8 +176,7 @@ def ssm_delta_fwd(q, k, v, dt_raw, A, beta_raw, *, dt_bias=None, reset=None, h0=
 
     lib = _b.load_library()
     if out is None:
-        dt = out_dtype or torch.float32
-        out = torch.empty(v.shape, dtype=dt, device=v.device) if stream is None else _result(v.shape, dt, v.device, stream)
+        out = _out(v, out_dtype or torch.float32, stream)
     p = _delta_params(q, k, v, dt_raw, A, beta_raw, dt_bias, reset, h0, h_last, out, scale, beta_scale, num_segments)
     workspace = _workspace(lib.ssm_delta_workspace_size, p, workspace, v.device, stream)
     _b._check(lib.ssm_delta_fwd(ctypes.byref(p), _stream(stream, v.device)))
@@ -225,8 +203,7 @@ def ssm_delta_update(h, q, k, v, dt_raw, A, beta_raw, *, dt_bias=None, out=None,
 
     lib = _b.load_library()
     if out is None:
-        dt = out_dtype or torch.float32
-        out = torch.empty(v.shape, dtype=dt, device=v.device) if stream is None else _result(v.shape, dt, v.device, stream)
+        out = _out(v, out_dtype or torch.float32, stream)
     p = _delta_update_params(h, q, k, v, dt_raw, A, beta_raw, dt_bias, out, scale, beta_scale)
     _b._check(lib.ssm_delta_update(ctypes.byref(p), _stream(stream, v.device)))
     return out
@@ -240,8 +217,7 @@ def prepare_delta_update(h, q, k, v, dt_raw, A, beta_raw, *, dt_bias=None, out=N
 
     lib = _b.load_library()
     if out is None:
-        dt = out_dtype or torch.float32
-        out = torch.empty(v.shape, dtype=dt, device=v.device) if stream is None else _result(v.shape, dt, v.device, stream)
+        out = _out(v, out_dtype or torch.float32, stream)
     p = _delta_update_params(h, q, k, v, dt_raw, A, beta_raw, dt_bias, out, scale, beta_scale)
     st, fn, pref = _stream(stream, v.device), lib.ssm_delta_update, ctypes.byref(p)
 
@@ -278,7 +254,7 @@ def ssm_delta_bwd(q, k, v, dt_raw, A, beta_raw, dout, *, dt_bias=None, reset=Non
     gd, f32, dev = grad_dtype or torch.float32, torch.float32, q.device
 
     def new(shape, dtype):
-        return _result(shape, dtype, dev, stream)
+        return _b._result(shape, dtype, dev, stream)
 
     g = dict(dq=new((B, L, Hk, dk), gd), dk=new((B, L, Hk, dk), gd), dv=new((B, L, Hv, dv), gd),
              d_dt_raw=new((B, L, Hv), gd), dbeta_raw=new((B, L, Hv), gd), dA=new((Hv,), f32),
@@ -338,10 +314,9 @@ def ssm_qk_norm_fwd(q, k, *, wq=None, wk=None, kind="rms", eps=1e-6, cos=None, s
     lib = _b.load_library()
     dt = out_dtype or torch.float32
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device) if stream is None else _result(q.shape, dt, q.device, stream)
+        q_out = _out(q, dt, stream)
     if k_out is None:
-        k_out = (torch.empty(k.shape, dtype=q_out.dtype, device=k.device) if stream is None
-                 else _result(k.shape, q_out.dtype, k.device, stream))
+        k_out = _out(k, q_out.dtype, stream)
     p = _norm_params(q, k, wq, wk, kind, eps, cos, sin, positions, interleaved)
     _need(q_out, q.shape, "q_out", q_out.dtype)
     _need(k_out, k.shape, "k_out", q_out.dtype)
@@ -359,9 +334,9 @@ def ssm_qk_norm_bwd(q, k, dq_out, dk_out, *, wq=None, wk=None, kind="rms", eps=1
 
     lib = _b.load_library()
     dt = grad_dtype or torch.float32
-    g = dict(dq=_result(q.shape, dt, q.device, stream), dk=_result(k.shape, dt, k.device, stream))
+    g = dict(dq=_out(q, dt, stream), dk=_out(k, dt, stream))
     for name in ("dwq", "dwk"):
-        g[name] = _result(q.shape[3], torch.float32, q.device, stream) if want_dw else None
+        g[name] = _b._result(q.shape[3], torch.float32, q.device, stream) if want_dw else None
     p = _norm_params(q, k, wq, wk, kind, eps, cos, sin, positions, interleaved)
     _need(dq_out, q.shape, "dq_out", q.dtype)
     _need(dk_out, k.shape, "dk_out", q.dtype)

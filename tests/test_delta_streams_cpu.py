@@ -22,8 +22,8 @@ class Library:
                 return 0
             return size
 
-        def call(params, stream):
-            self.ran.append(stream)
+        def call(params, *rest):
+            self.ran.append(rest[-1])
             return 0
         return call
 
