@@ -78,7 +78,15 @@ ssm_status check_delta_sizes(const P* p, int64_t len, int32_t other_dtype, Delta
       !mul_ok(p->batch, p->value_heads, &bh) || !mul_ok(bh, p->dk * p->dv, &s->state) || s->qk > kLim ||
       s->vo > kLim || s->state > kLim)
     return fail(SSM_ERR_BAD_SHAPE, "element count overflows");
-  if (bh > std::numeric_limits<int32_t>::max() / (kMaxColumns / 16))
+  if (bh > std::numeric_limits<int32_t>::max())
+    return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
+  return SSM_OK;
+}
+
+// Step by step: a workgroup of 256 threads for every 64 columns of a head, and a launch has
+// less than 2^32 threads.
+ssm_status check_steps_grid(int64_t batch, int64_t heads, int64_t dv) {
+  if (batch * heads > ((int64_t{1} << 24) - 1) / ((dv + 63) / 64))
     return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
   return SSM_OK;
 }
@@ -162,7 +170,9 @@ ssm_status check_grid(int64_t batch, int64_t seqlen, int64_t heads, int64_t dv) 
 ssm_status plan_delta(const ssm_delta_params* p, const DeltaSizes& s, ssm::DeltaChunks* plan) {
   if (p->num_segments < 0) return fail(SSM_ERR_BAD_SHAPE, "num_segments must be >= 0");
   *plan = ssm::DeltaChunks{};
-  if (s.empty() || (p->seqlen <= steps_max(p->in_dtype) && p->num_segments <= 1)) return SSM_OK;
+  if (s.empty()) return SSM_OK;
+  if (p->seqlen <= steps_max(p->in_dtype) && p->num_segments <= 1)
+    return check_steps_grid(p->batch, p->value_heads, p->dv);
   const ssm_status st = check_grid(p->batch, p->seqlen, p->value_heads, p->dv);
   if (st != SSM_OK) return st;
   *plan = ssm::plan_delta_chunks(p->batch, p->seqlen, static_cast<int>(p->value_heads), static_cast<int>(p->dk),
@@ -330,6 +340,7 @@ ssm_status ssm_delta_update(const ssm_delta_update_params* p, void* hip_stream) 
   if (!p) return fail(SSM_ERR_NULL_POINTER, "params is NULL");
   DeltaSizes s;
   ssm_status st = check_delta_sizes(p, p->tokens, p->out_dtype, &s);
+  if (st == SSM_OK && !s.empty()) st = check_steps_grid(p->batch, p->value_heads, p->dv);
   if (st != SSM_OK) return st;
   const size_t si = dtype_size(p->in_dtype), so = dtype_size(p->out_dtype);
   const Need needs[] = {
