@@ -26,6 +26,7 @@ constexpr int kThreads = 256;
 
 struct NormArgs {
   int64_t tokens, L, P;
+  int64_t first;                      // lane group that the launch starts with (forward)
   int Hq, Hk, d, rot, slots, turned;  // turned: slots of the rotated part
   int parts, heads_part;              // a token's heads are split over `parts` lane groups
   const void* q;
@@ -170,7 +171,7 @@ __device__ __forceinline__ void load_weights(const float* w, const Slot (&s)[NS]
 
 template <typename InT, typename OutT, int V, int LR, int NS>
 __global__ __launch_bounds__(kThreads) void qk_norm_fwd(const NormArgs a) {
-  const int64_t group = static_cast<int64_t>(blockIdx.x) * (kThreads / LR) + threadIdx.x / LR;
+  const int64_t group = a.first + static_cast<int64_t>(blockIdx.x) * (kThreads / LR) + threadIdx.x / LR;
   const int64_t token = group / a.parts;
   if (token >= a.tokens) return;  // whole groups; the sums stay inside a group
   const int lane = threadIdx.x % LR;
@@ -368,9 +369,15 @@ hipError_t launch(const NormPlan& p, NormArgs a, hipStream_t stream) {
   if constexpr (!BWD) {
     SSM_LOG("launch qk_norm_fwd<%d entries a run, %d lanes a row>: %d heads in %d parts; grid %lld x %d threads", V,
             LR, heads, a.parts, static_cast<long long>(blocks), kThreads);
-    hipLaunchKernelGGL((qk_norm_fwd<InT, OutT, V, LR, NS>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
-                       stream, a);
-    return hipGetLastError();
+    constexpr int64_t kMost = int64_t{1} << 23;  // workgroups a launch, which has less than 2^32 threads
+    for (int64_t at = 0; at < blocks; at += kMost) {
+      a.first = at * kGroups;
+      hipLaunchKernelGGL((qk_norm_fwd<InT, OutT, V, LR, NS>), dim3(static_cast<unsigned>(std::min(kMost, blocks - at))),
+                         dim3(kThreads), 0, stream, a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   } else {
     const int rows = static_cast<int>(std::min<int64_t>(blocks, norm_bwd_blocks(a.tokens, heads, a.d)));
     a.part = p.dwq || p.dwk ? p.part : nullptr;

@@ -5,7 +5,7 @@ import pytest
 from oracle import delta as od
 from selective_state_space_67_amd import workloads as wl
 
-from delta_helpers import ARGS, STATE, check, delta_inputs, on_device, wide
+from delta_helpers import ARGS, NORM, STATE, check, delta_inputs, on_device, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +23,27 @@ def test_decode_of_600000_small_states():
     ref, rh = od.delta_fwd(**wide(x), scale=0.5)
     check(out, ref, STATE, "out")
     check(h, rh, STATE, "h")
+
+
+@pytest.mark.parametrize("d,tokens", [(1, 1 << 28), (33, (1 << 26) + 12)])
+def test_norms_of_more_rows_than_one_launch_has_threads_for(d, tokens):
+    """16 lanes a row of 1 entry, 64 a row of 33: 2^32 threads and a few more."""
+    import torch
+
+    from selective_state_space_67_amd import ssm_qk_norm_fwd
+
+    dev = torch.device("cuda:0")
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(d)
+    q = torch.randn(4, tokens // 4, 1, d, generator=gen, device=dev, dtype=torch.bfloat16)
+    w = torch.linspace(0.5, 1.5, d, device=dev)
+    print(d, tokens, flush=True)
+    out, _ = ssm_qk_norm_fwd(q, q.new_empty(4, tokens // 4, 0, d), wq=w)
+    torch.cuda.synchronize()
+    x, y = q.flatten(0, 2), out.flatten(0, 2)
+    step = 1 << 22
+    for i in range(0, tokens, step):
+        a = x[i:i + step].double()
+        want = a * torch.rsqrt(a.square().mean(-1, keepdim=True) + float(np.float32(1e-6))) * w.double()
+        bound = NORM * (want.square().mean().sqrt() + want.abs())
+        assert bool(((y[i:i + step].double() - want).abs() <= bound).all()), i
