@@ -156,7 +156,8 @@ ssm::DeltaPlan delta_plan(const P* p, int64_t len, const DeltaSizes& s) {
 // against 243).
 constexpr int64_t steps_max(int in_dtype) { return in_dtype == SSM_BF16 ? 16 : 32; }
 
-// One workgroup for every chunk, and at most a workgroup for every 16 columns.
+// One workgroup for every chunk, and at most a workgroup for every 16 columns, in 31 bits: the
+// plans can be made (and then say whether each launch fits).
 ssm_status check_grid(int64_t batch, int64_t seqlen, int64_t heads, int64_t dv) {
   const int64_t chunks = (seqlen + 63) / 64;
   int64_t blocks;
@@ -177,6 +178,8 @@ ssm_status plan_delta(const ssm_delta_params* p, const DeltaSizes& s, ssm::Delta
   if (st != SSM_OK) return st;
   *plan = ssm::plan_delta_chunks(p->batch, p->seqlen, static_cast<int>(p->value_heads), static_cast<int>(p->dk),
                                  static_cast<int>(p->dv), p->num_segments);
+  if (!ssm::delta_grids_fit(p->batch * p->value_heads, static_cast<int>(p->dk), static_cast<int>(p->dv), *plan))
+    return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
   return SSM_OK;
 }
 
@@ -195,6 +198,9 @@ ssm_status plan_delta_bwd(const ssm_delta_bwd_params* p, DeltaSizes* s, ssm::Del
     return fail(SSM_ERR_BAD_SHAPE, "backward workspace size overflows");
   *lay = ssm::plan_delta_bwd(p->batch, p->seqlen, static_cast<int>(p->value_heads), static_cast<int>(p->dk),
                              static_cast<int>(p->dv));
+  if (!ssm::delta_bwd_grids_fit(p->batch * p->value_heads, p->batch * p->key_heads, static_cast<int>(p->dk),
+                                static_cast<int>(p->dv), *lay))
+    return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
   return SSM_OK;
 }
 

@@ -502,6 +502,16 @@ DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int 
   return d;
 }
 
+bool delta_grids_fit(int64_t heads, int dk, int dv, const DeltaChunks& d) {
+  const int64_t strips = (dv + 15) / 16, state_strips = 2 * padded_ks(dk);
+  bool fit = fits_launch(heads * d.chunks, kThreads) &&
+             fits_launch(placed_blocks(heads * d.pieces, (strips + kWaves - 1) / kWaves), kThreads);
+  if (d.pieces > 1)
+    fit = fit && fits_launch(placed_blocks(heads * d.pieces, (strips + state_strips + kWaves - 1) / kWaves), kThreads) &&
+          fits_launch(heads * d.groups * (strips + state_strips), 64 * state_strips);
+  return fit;
+}
+
 namespace {
 
 hipError_t launch_scan(const DeltaPlan& p, const DeltaChunks& plan, ScanArgs& s, hipStream_t stream) {

@@ -933,6 +933,11 @@ DeltaBwdLayout plan_delta_bwd(int64_t B, int64_t L, int Hv, int dk, int dv) {
   return d;
 }
 
+bool delta_bwd_grids_fit(int64_t heads, int64_t key_heads, int dk, int dv, const DeltaBwdLayout& d) {
+  return delta_grids_fit(heads, dk, dv, d.walk) &&
+         fits_launch(placed_blocks(key_heads * d.chunks, grad_splits(padded_ks(dk))), kThreads);
+}
+
 hipError_t launch_delta_bwd(const DeltaPlan& p, const DeltaBwdPlan& g, const DeltaBwdLayout& lay, void* workspace,
                             hipStream_t stream) {
   char* ws = static_cast<char*>(workspace);

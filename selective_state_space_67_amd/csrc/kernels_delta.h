@@ -45,6 +45,9 @@ struct DeltaChunks {
 };
 // requested = 0: automatic. Pure host arithmetic.
 DeltaChunks plan_delta_chunks(int64_t B, int64_t L, int Hv, int dk, int dv, int requested);
+// Whether every launch of a forward call stays below 2^32 threads (heads: B Hv), and of a
+// backward call (key_heads: B Hk).
+bool delta_grids_fit(int64_t heads, int dk, int dv, const DeltaChunks& plan);
 hipError_t launch_delta_chunks(const DeltaPlan& plan, const DeltaChunks& chunks, void* workspace, hipStream_t stream);
 
 // The backward pass (delta_chunk_bwd.hip). DeltaPlan gives the forward's inputs.
@@ -67,6 +70,7 @@ struct DeltaBwdLayout {  // workspace byte offsets
   size_t off_records, off_states, off_U, off_dstates, off_dR, off_sums, off_part, bytes;
 };
 DeltaBwdLayout plan_delta_bwd(int64_t B, int64_t L, int Hv, int dk, int dv);
+bool delta_bwd_grids_fit(int64_t heads, int64_t key_heads, int dk, int dv, const DeltaBwdLayout& layout);
 hipError_t launch_delta_bwd(const DeltaPlan& plan, const DeltaBwdPlan& grads, const DeltaBwdLayout& layout,
                             void* workspace, hipStream_t stream);
 
