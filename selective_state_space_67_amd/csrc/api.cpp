@@ -46,12 +46,15 @@ using ssm::align256;
 using ssm::aligned;
 using ssm::dtype_size;
 using ssm::fail;
+using ssm::fits_launch;
 using ssm::mul_ok;
 using ssm::ok;
 using ssm::overlaps;
 using ssm::Range;
 using ssm::range;
 using ssm::valid_dtype;
+
+constexpr int64_t kThreads = 256;  // of a workgroup, unless scan_block_threads() says otherwise
 
 bool valid_disc(int32_t t) { return t == SSM_DISC_DELTA_B || t == SSM_DISC_ZOH; }
 bool valid_kind(int32_t k) { return k == SSM_STATE_REAL || k == SSM_STATE_COMPLEX; }
@@ -96,14 +99,14 @@ ssm_status plan_scan(const ssm_scan_params* p, int* nseg, int64_t* seg_len, size
   }
   if (p->state_kind == SSM_STATE_COMPLEX) {
     ssm::plan_cplx_segments(p->batch, p->dim, p->seqlen, p->dstate, p->num_segments, nseg, seg_len);
-    if (ssm::cplx_scan_grid_blocks(p->batch, p->dim, *nseg) > std::numeric_limits<int32_t>::max())
+    if (!fits_launch(ssm::cplx_scan_grid_blocks(p->batch, p->dim, *nseg), kThreads))
       return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
     *ws = ssm::cplx_workspace_bytes(p->batch, p->dim, p->dstate, *nseg);
     return SSM_OK;
   }
   const bool plain = !p->conv_w && p->discretization != SSM_DISC_ZOH;
   ssm::plan_segments(p->batch, p->dim, p->seqlen, p->dstate, p->num_segments, nseg, seg_len, plain);
-  if (ssm::scan_grid_blocks(p->batch, p->dim, p->dstate, *nseg) > std::numeric_limits<int32_t>::max())
+  if (!fits_launch(ssm::scan_grid_blocks(p->batch, p->dim, p->dstate, *nseg), ssm::scan_block_threads(p->dstate)))
     return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
   *ws = ssm::scan_workspace_bytes(p->batch, p->dim, p->dstate, *nseg);
   return SSM_OK;
@@ -217,7 +220,9 @@ ssm_status plan_aggregate(const ssm_scan_params* p, int* nseg, int64_t* seg_len,
     ssm::plan_segments(p->batch, p->dim, p->seqlen, p->dstate, p->num_segments, nseg, seg_len, true, 512);
   const int64_t blocks = cplx ? ssm::cplx_scan_grid_blocks(p->batch, p->dim, *nseg)
                               : ssm::scan_grid_blocks(p->batch, p->dim, p->dstate, *nseg);
-  if (blocks > std::numeric_limits<int32_t>::max())
+  const int64_t states = p->batch * p->dim * p->dstate;  // a thread of the fold each
+  if (!fits_launch(blocks, cplx ? kThreads : ssm::scan_block_threads(p->dstate)) ||
+      (*nseg > 1 && !fits_launch((states + kThreads - 1) / kThreads, kThreads)))
     return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
   *ws = *nseg > 1 ? static_cast<size_t>(2) * static_cast<size_t>(*nseg) * static_cast<size_t>(p->batch) *
                         static_cast<size_t>(p->dim) * static_cast<size_t>(p->dstate) * (cplx ? 2 : 1) *
@@ -278,8 +283,9 @@ ssm_status check_bwd_kind(const ssm_scan_bwd_params* p) { return check_kind(p->s
 ssm_status plan_bwd_cplx(const ssm_scan_bwd_params* p, const ScanSizes& sz, BwdLayout* lay) {
   const int64_t B = p->batch, D = p->dim, L = p->seqlen, N = p->dstate;
   ssm::plan_cplx_bwd(B, D, L, N, &lay->nsegb, &lay->seg_steps, &lay->nseg, &lay->seg_len, &lay->n_ck);
-  if (ssm::cplx_scan_grid_blocks(B, D, lay->nseg) > std::numeric_limits<int32_t>::max() ||
-      ssm::cplx_bwd_grid_blocks(B, D, lay->nsegb) > std::numeric_limits<int32_t>::max())
+  if (!fits_launch(ssm::cplx_scan_grid_blocks(B, D, lay->nseg), kThreads) ||
+      !fits_launch(ssm::cplx_bwd_grid_blocks(B, D, lay->nsegb), kThreads) ||
+      (p->conv_w && !fits_launch(ssm::conv_bwd_grid_blocks(B, D, L), kThreads)))
     return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
   int64_t ck, seg, part;
   const int64_t groups = (D + 15) / 16;
@@ -327,8 +333,9 @@ ssm_status plan_bwd(const ssm_scan_bwd_params* p, const ScanSizes& sz, BwdLayout
   lay->seg_len = seg_len;
   lay->nseg = static_cast<int>((L + seg_len - 1) / seg_len);
   lay->n_ck = (L + 15) / 16;
-  if (ssm::scan_grid_blocks(B, D, N, lay->nseg) > std::numeric_limits<int32_t>::max() ||
-      ssm::bwd_grid_blocks(B, D, N, lay->nsegb) > std::numeric_limits<int32_t>::max())
+  if (!fits_launch(ssm::scan_grid_blocks(B, D, N, lay->nseg), ssm::scan_block_threads(N)) ||
+      !fits_launch(ssm::bwd_grid_blocks(B, D, N, lay->nsegb), kThreads) ||
+      (p->conv_w && !fits_launch(ssm::conv_bwd_grid_blocks(B, D, L), kThreads)))
     return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
   int64_t ck, seg, part;
   const int64_t groups = (D + ssm::bwd_channels_per_block(N) - 1) / ssm::bwd_channels_per_block(N);
@@ -395,7 +402,7 @@ ssm_status scan_fwd(const ssm_scan_params* p, void* hip_stream, bool noalloc, bo
     nseg = 1;
     seg_len = p->seqlen;
     ws = 0;
-    if ((p->batch * p->dim + 3) / 4 > std::numeric_limits<int32_t>::max())
+    if (!fits_launch((p->batch * p->dim + 3) / 4, kThreads))
       return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
   }
   const Range outs[] = {out, hl, cso};

@@ -147,9 +147,6 @@ inline int padded_ks(int dk) {
 
 constexpr int kMaxLds = 160 * 1024;
 
-// A launch's threads are counted in 32 bits.
-inline bool fits_launch(int64_t blocks, int64_t threads) { return blocks <= ((int64_t{1} << 32) - 1) / threads; }
-
 // Prepare every chunk (delta_chunk.hip); bwd: the backward's records.
 hipError_t launch_chunk_prepare(const DeltaPlan& p, const ChunkArgs& a, bool bwd, hipStream_t stream);
 

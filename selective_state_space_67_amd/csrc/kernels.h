@@ -6,6 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "launch_limits.h"
 #include "log.h"
 
 namespace ssm {
@@ -89,6 +90,8 @@ size_t scan_workspace_bytes(int64_t B, int64_t D, int64_t N, int nseg);
 
 // Number of workgroups the scan launches use (for grid-limit checks).
 int64_t scan_grid_blocks(int64_t B, int64_t D, int64_t N, int nseg);
+// Threads of each of them.
+int scan_block_threads(int64_t N);
 
 hipError_t launch_scan(const ScanPlan& plan, hipStream_t stream);
 // The forward as a chunked associative scan (scan_fwd_wavefront.hip): N = 16,
@@ -170,6 +173,8 @@ int bwd_channels_per_block(int64_t N);
 size_t bwd_partial_floats(int64_t B, int64_t D, int64_t L, int64_t N, int nsegb);
 // Workgroups of the reverse sweep.
 int64_t bwd_grid_blocks(int64_t B, int64_t D, int64_t N, int nsegb);
+// Workgroups of the conv backward.
+int64_t conv_bwd_grid_blocks(int64_t B, int64_t D, int64_t L);
 // Floats of partial sums of the conv backward (per row tile: 4 taps + bias).
 size_t bwd_conv_partial_floats(int64_t B, int64_t D, int64_t L);
 hipError_t launch_scan_bwd(const BwdPlan& plan, hipStream_t stream);

@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "launch_limits.h"
 #include "log.h"
 
 namespace ssm {

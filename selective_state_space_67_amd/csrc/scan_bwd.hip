@@ -918,6 +918,8 @@ int64_t bwd_grid_blocks(int64_t B, int64_t D, int64_t N, int nsegb) {
   return B * ((D + bwd_channels_per_block(N) - 1) / bwd_channels_per_block(N)) * nsegb;
 }
 
+int64_t conv_bwd_grid_blocks(int64_t B, int64_t D, int64_t L) { return B * D * ((L + kConvTile - 1) / kConvTile); }
+
 hipError_t launch_bwd_reduce(const float* partB, const float* partC, const float* partA, const float* partD,
                              const float* partBias, float* dB, float* dC, float* dA, float* dD, float* dbias,
                              int64_t bln, int64_t dn, int64_t D, int64_t groups, int64_t bs, hipStream_t stream) {
@@ -1052,7 +1054,7 @@ hipError_t launch_conv_bwd(const BwdPlan& pl, hipStream_t stream) {
   c.dx = pl.du;
   c.dstate = pl.dconv_state;
   c.part = pl.conv_part;
-  const dim3 cgrid(static_cast<unsigned>(pl.B * pl.D * c.ntiles));
+  const dim3 cgrid(static_cast<unsigned>(conv_bwd_grid_blocks(pl.B, pl.D, pl.L)));
   SSM_LOG("launch conv_bwd_kernel: width %d, %d tiles of %d steps; grid %u x 256 threads", c.K, c.ntiles, kConvTile,
           cgrid.x);
   if (pl.in_bf16)

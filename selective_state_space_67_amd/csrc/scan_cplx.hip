@@ -706,6 +706,7 @@ hipError_t launch_state_update_cplx(const UpdatePlan& p, hipStream_t stream) {
       constexpr bool Z = decltype(zoh)::value;
       constexpr int kChannels = kThreads / LR * 2;
       a.dtiles = static_cast<int>((p.D + kChannels - 1) / kChannels);
+      if (!fits_launch(a.dtiles * ((p.B + 1) / 2), kThreads)) return hipErrorInvalidConfiguration;
       const dim3 grid(static_cast<unsigned>(a.dtiles * ((p.B + 1) / 2)));
       SSM_LOG("launch cplx_update_tile<%d lanes per row, 2 channels x 2 batch rows per thread>: %s in, zoh %d, "
               "streamed state %d; grid %u x %d threads",
@@ -727,6 +728,7 @@ hipError_t launch_state_update_cplx(const UpdatePlan& p, hipStream_t stream) {
     };
     return p.zoh ? with_lr(std::true_type{}) : with_lr(std::false_type{});
   }
+  if (!fits_launch((p.B * p.D + kCPW - 1) / kCPW, kThreads)) return hipErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>((p.B * p.D + kCPW - 1) / kCPW));
   auto go = [&](auto npl, auto zoh, auto st) {
     constexpr int NPL = decltype(npl)::value;

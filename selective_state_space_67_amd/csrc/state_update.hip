@@ -249,6 +249,7 @@ hipError_t launch_tile(UpdateArgs a, hipStream_t stream) {
   constexpr int kChannels = kThreads / LR * RD;  // channels per workgroup
   a.dtiles = static_cast<int>((a.D + kChannels - 1) / kChannels);
   const int64_t blocks = a.dtiles * ((a.B + RB - 1) / RB);
+  if (!fits_launch(blocks, kThreads)) return hipErrorInvalidConfiguration;
   const bool stream_state = a.rows * a.N * static_cast<int64_t>(sizeof(float)) > kStreamStateBytes;
   SSM_LOG("launch state_update_tile<%d lanes per row, %d channels x %d batch rows per thread>: %s in, streamed "
           "state %d; grid %lld x %d threads",
@@ -280,6 +281,7 @@ template <typename InT, int LR>
 hipError_t launch_scalar(const UpdateArgs& a, hipStream_t stream) {
   const int64_t rows_per_block = kThreads / LR;
   const int64_t blocks = (a.rows + rows_per_block - 1) / rows_per_block;
+  if (!fits_launch(blocks, kThreads)) return hipErrorInvalidConfiguration;
   SSM_LOG("launch state_update_scalar<%d lanes per row>: %s in; grid %lld x %d threads", LR,
           sizeof(InT) == 2 ? "bf16" : "f32", static_cast<long long>(blocks), kThreads);
   hipLaunchKernelGGL((state_update_scalar<InT, LR>), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,

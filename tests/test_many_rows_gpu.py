@@ -47,3 +47,25 @@ def test_norms_of_more_rows_than_one_launch_has_threads_for(d, tokens):
         want = a * torch.rsqrt(a.square().mean(-1, keepdim=True) + float(np.float32(1e-6))) * w.double()
         bound = NORM * (want.square().mean().sqrt() + want.abs())
         assert bool(((y[i:i + step].double() - want).abs() <= bound).all()), i
+
+
+@pytest.mark.parametrize("complex_state", [False, True])
+def test_a_decode_of_more_rows_than_a_launch_has_threads_for_is_refused(complex_state):
+    """Two batch rows a workgroup (one channel, 16 states): 2^25 rows are 2^24 workgroups."""
+    import torch
+
+    from selective_state_space_67_amd import ssm_state_update
+    from selective_state_space_67_amd.binding import SsmError
+
+    B, N = 1 << (28 if complex_state else 25), 1 if complex_state else 16
+    dev, c2 = torch.device("cuda:0"), (2,) if complex_state else ()
+    h = torch.ones((B, 1, N) + c2, device=dev)
+    one = torch.ones(B, 1, device=dev, dtype=torch.bfloat16)
+    Bm = torch.ones((B, N) + c2, device=dev, dtype=torch.bfloat16)
+    out = torch.full((B, 1), 7.0, device=dev, dtype=torch.bfloat16)
+    print(complex_state, flush=True)
+    with pytest.raises(SsmError, match="configuration"):
+        ssm_state_update(h, one, one, -torch.ones((1, N) + c2, device=dev), Bm, Bm, out=out,
+                         complex_state=complex_state)
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all()) and bool((h == 1.0).all())
