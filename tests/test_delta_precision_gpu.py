@@ -2,9 +2,10 @@
 import numpy as np
 import pytest
 
+from oracle import delta as od
 from selective_state_space_67_amd import workloads as wl
 
-from delta_helpers import ARGS, host, on_device
+from delta_helpers import ARGS, GRAD, STATE, check, delta_inputs, host, on_device, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +51,96 @@ def test_new_values_over_large_old_ones(dtype, L, dk, dv, pad, out_bf16):
     torch.cuda.synchronize()
     err = np.sqrt(np.mean((host(out) - wl.widen(x["v"])) ** 2))
     assert err <= 12 * U * R, "root mean square error %.3g, %.1f u R" % (err, err / (U * R))
+
+
+# Root mean square error over the reference's, float32 results. A product's operands are held
+# to 2^-26 (three bfloat16 parts) and its float32 sum of up to 256 terms to about sqrt(256) u / 3 =
+# 3e-7; four such products follow one another: 6e-7, held to 1e-6. Without the third part of one
+# operand it is 2^-17 / sqrt(12) = 2.2e-6 of that product, with two parts everywhere 6e-6. The gates'
+# gradients are sums over a state of terms that cancel to a third or less (4e-6), and over all
+# tokens of terms of either sign (2e-5).
+RMS = dict(out=1e-6, h_last=1e-6, dq=1e-6, dk=1e-6, dv=1e-6, dbeta_raw=1e-6, dh0=1e-6, d_dt_raw=4e-6, dA=2e-5,
+           d_dt_bias=2e-5)
+RESETS = [(0, 0), (0, 5), (0, 6), (0, 63), (0, 64), (0, 130), (1, 1), (1, 129), (1, 191)]
+
+
+def close(got, ref, name):
+    err, size = np.sqrt(np.mean((host(got) - ref) ** 2)), np.sqrt(np.mean(ref ** 2))
+    assert err <= RMS[name] * size, "%s: root mean square error %.3g of %.3g" % (name, err, size)
+
+
+# bfloat16 sizes that go straight into LDS (entries of k that fill tiles of 32, 8 columns at least)
+# with one to eight tiles, sizes that do not, a ragged last chunk
+@pytest.mark.parametrize("dtype", [wl.F32, wl.BF16])
+@pytest.mark.parametrize("resets", [False, True])
+@pytest.mark.parametrize("shape", [(2, 150, 1, 2, 32, 40), (1, 130, 1, 2, 64, 64), (1, 200, 2, 2, 96, 64),
+                                   (1, 165, 1, 3, 128, 128), (1, 170, 1, 2, 192, 128), (1, 140, 1, 1, 256, 48),
+                                   (2, 100, 2, 2, 33, 50), (1, 150, 1, 1, 224, 24)], ids=lambda s: "x".join(map(str, s)))
+def test_three_parts_everywhere(shape, dtype, resets):
+    import torch
+
+    from selective_state_space_67_amd import ssm_delta_bwd, ssm_delta_fwd
+
+    x = delta_inputs(*shape, dtype, seed=sum(shape) + 5, resets=RESETS if resets else None, state=True)
+    t = on_device(x)
+    scale = shape[4] ** -0.5
+    ref, rh = od.delta_fwd(**wide(x), reset=x["reset"], scale=scale)
+    grads = od.delta_bwd(**wide(x), dout=wl.widen(x["dout"]), reset=x["reset"], dh_last=wl.widen(x["dh_last"]), scale=scale)
+    print(shape, dtype, resets, flush=True)
+    a = [t[n] for n in ARGS]
+    hl = torch.empty_like(t["h0"])
+    out = ssm_delta_fwd(*a, dt_bias=t["dt_bias"], reset=t["reset"], h0=t["h0"], h_last=hl)
+    g = ssm_delta_bwd(*a, t["dout"], dt_bias=t["dt_bias"], reset=t["reset"], h0=t["h0"], dh_last=t["dh_last"])
+    low = ssm_delta_fwd(*a, dt_bias=t["dt_bias"], reset=t["reset"], h0=t["h0"], out_dtype=torch.bfloat16)
+    low_g = ssm_delta_bwd(*a, t["dout"], dt_bias=t["dt_bias"], reset=t["reset"], h0=t["h0"], dh_last=t["dh_last"],
+                          grad_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    close(out, ref, "out")
+    close(hl, rh, "h_last")
+    check(low, ref, STATE, "bfloat16 out", bf16=True)
+    for name, want in grads.items():
+        close(g[name], want, name)
+        check(low_g[name], want, GRAD, "bfloat16 " + name, bf16=name not in ("dA", "d_dt_bias", "dh0"))
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [(wl.BF16, 32, 40), (wl.BF16, 96, 64), (wl.BF16, 192, 128), (wl.F32, 160, 24),
+                                         (wl.BF16, 256, 32)])
+@pytest.mark.parametrize("pieces", [3, 20])
+def test_pieces_of_every_state_size(dtype, dk, dv, pieces):
+    """Folds of 1, 3, 6 and 8 row tiles, one after another and in groups."""
+    import torch
+
+    from selective_state_space_67_amd import ssm_delta_fwd
+
+    x = delta_inputs(1, 1290, 1, 2, dk, dv, dtype, seed=dk + pieces, resets=[(0, 700)] if pieces == 3 else None, state=True)
+    x["A"][:] = -0.01
+    ref, rh = od.delta_fwd(**wide(x), reset=x["reset"], scale=dk ** -0.5)
+    t = on_device(x)
+    print(dtype, dk, dv, pieces, flush=True)
+    hl = torch.empty_like(t["h0"])
+    out = ssm_delta_fwd(*(t[n] for n in ARGS), dt_bias=t["dt_bias"], reset=t["reset"], h0=t["h0"], h_last=hl,
+                        num_segments=pieces)
+    torch.cuda.synchronize()
+    check(out, ref, STATE, "out")
+    check(hl, rh, STATE, "h_last")
+
+
+@pytest.mark.parametrize("dtype", [wl.F32, wl.BF16])
+@pytest.mark.parametrize("L,dk,dv", [(1030, 96, 32), (1100, 192, 128), (1030, 256, 16)])
+def test_backward_pieces_of_large_states(L, dk, dv, dtype):
+    """Few heads and a slow decay: the walks go in pieces both ways, with folds of 3, 6 and 8 row tiles."""
+    import torch
+
+    from selective_state_space_67_amd import ssm_delta_bwd
+
+    x = delta_inputs(1, L, 1, 2, dk, dv, dtype, seed=dk + L, resets=[(0, L - 333)], state=True)
+    x["A"][:] = -0.01
+    want = od.delta_bwd(**wide(x), dout=wl.widen(x["dout"]), reset=x["reset"], dh_last=wl.widen(x["dh_last"]),
+                        scale=dk ** -0.5)
+    t = on_device(x)
+    print(L, dk, dv, dtype, flush=True)
+    g = ssm_delta_bwd(*(t[n] for n in ARGS), t["dout"], dt_bias=t["dt_bias"], reset=t["reset"], h0=t["h0"],
+                      dh_last=t["dh_last"])
+    torch.cuda.synchronize()
+    for name, ref in want.items():
+        check(g[name], ref, GRAD, name)
