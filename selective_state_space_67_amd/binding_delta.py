@@ -112,6 +112,10 @@ def _tokens(t, shape, name, dtype):
 
 def _out(t, dtype, stream):
     """An output of t's shape (torch's empty_like would keep t's strides)."""
+    import torch
+
+    if stream is None:
+        return torch.empty(t.shape, dtype=dtype, device=t.device)
     return _b._result(t.shape, dtype, t.device, stream)
 
 

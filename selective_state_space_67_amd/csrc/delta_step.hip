@@ -37,7 +37,7 @@ constexpr int kColsBlock = 64;  // columns per workgroup
 
 struct StepArgs {
   int64_t L;
-  int Hk, Hv, dk, dv, group;  // group: value heads per key head
+  int Hv, dk, dv, group;  // group: value heads per key head
   int col_blocks;             // workgroups per head
   int out_bf16;
   const void* q;
@@ -215,7 +215,6 @@ hipError_t launch_dtype(const DeltaPlan& p, const StepArgs& a, hipStream_t strea
 hipError_t launch_delta_steps(const DeltaPlan& p, hipStream_t stream) {
   StepArgs a{};
   a.L = p.L;
-  a.Hk = p.Hk;
   a.Hv = p.Hv;
   a.dk = p.dk;
   a.dv = p.dv;
