@@ -785,7 +785,9 @@ __global__ __launch_bounds__(kThreads) void delta_gate_grads(const BwdArgs s, in
   const float d_dt = off ? 0.0f : dg * a.A[h] * scalars[kSlope + lane];
   if (there) {
     const int64_t at = (static_cast<int64_t>(b) * a.L + static_cast<int64_t>(chunk) * kChunk + lane) * a.Hv + h;
-    const float d_beta = sums[kSumBeta + lane] * (1.0f - scalars[kBeta + lane] / a.beta_scale);
+    // 1 - beta / beta_scale is the sigmoid of -beta_raw, of which a beta near its limit keeps nothing
+    const float rest = fast_rcp(1.0f + fast_exp2(load_elem(static_cast<const InT*>(a.br), at) * kLog2e));
+    const float d_beta = sums[kSumBeta + lane] * rest;
     if (s.grad_bf16) {
       store_elem(static_cast<bf16_t*>(s.ddt), at, d_dt);
       store_elem(static_cast<bf16_t*>(s.dbr), at, d_beta);

@@ -69,6 +69,37 @@ def close(got, ref, name):
     assert err <= RMS[name] * size, "%s: root mean square error %.3g of %.3g" % (name, err, size)
 
 
+@pytest.mark.parametrize("dtype", [wl.F32, wl.BF16])
+def test_gradients_of_betas_near_their_limit(dtype):
+    """d beta_raw has the factor 1 - sigmoid(beta_raw), 2e-9 at 20: without it, it is as exact as elsewhere."""
+    import torch
+
+    from selective_state_space_67_amd import ssm_delta_bwd
+
+    x = delta_inputs(1, 100, 1, 2, 32, 24, dtype, seed=8, state=True)
+    x["beta_raw"] = wl.store(np.random.default_rng(9).uniform(-3.0, 20.0, x["beta_raw"].shape), dtype)
+    want = od.delta_bwd(**wide(x), dout=wl.widen(x["dout"]), dh_last=wl.widen(x["dh_last"]), scale=1.0)["dbeta_raw"]
+    t = on_device(x)
+    got = ssm_delta_bwd(*(t[n] for n in ARGS), t["dout"], dt_bias=t["dt_bias"], h0=t["h0"], dh_last=t["dh_last"],
+                        scale=1.0)["dbeta_raw"]
+    torch.cuda.synchronize()
+    rest = 1.0 / (1.0 + np.exp(wl.widen(x["beta_raw"])))
+    check(host(got) / rest, want / rest, GRAD, "dbeta_raw")
+
+
+def test_a_beta_scale_of_zero_writes_nothing_and_has_no_beta_gradient():
+    import torch
+
+    from selective_state_space_67_amd import ssm_delta_bwd
+
+    x = delta_inputs(1, 70, 1, 1, 32, 24, wl.F32, seed=10, state=True)
+    t = on_device(x)
+    g = ssm_delta_bwd(*(t[n] for n in ARGS), t["dout"], dt_bias=t["dt_bias"], h0=t["h0"], dh_last=t["dh_last"],
+                      beta_scale=0.0)
+    torch.cuda.synchronize()
+    assert not host(g["dbeta_raw"]).any() and not host(g["dv"]).any() and np.isfinite(host(g["dq"])).all()
+
+
 # bfloat16 sizes that go straight into LDS (entries of k that fill tiles of 32, 8 columns at least)
 # with one to eight tiles, sizes that do not, a ragged last chunk
 @pytest.mark.parametrize("dtype", [wl.F32, wl.BF16])
