@@ -539,8 +539,10 @@ ssm_status ssm_delta_update(const ssm_delta_update_params* p, void* hip_stream);
  *            float32 outputs, NULL => not written
  *   workspace, workspace_bytes : at least ssm_delta_bwd_workspace_size() bytes,
  *            aligned to 256. The states and adjoints at every 64-token chunk are
- *            kept there (8 dk dv bytes per chunk and value head, dk rounded up to
- *            a multiple of 32 and dv to 16, and 57 KB + 512 dv bytes besides).
+ *            kept there: 8 dk dv bytes per chunk and value head, dk rounded up to
+ *            32, 64, 96, 128, 192 or 256 and dv to a multiple of 16, and 512 dv
+ *            bytes and 58 to 62 KB besides; and, where few heads make the library
+ *            split L, 4 dk (2 dk + 2 dv) bytes per piece and value head.
  * dA and d_dt_bias are sums in a fixed order, so repeated calls give identical bits.
  * A non-finite input (one that is used: a gate at a reset is not) may make any gradient of
  * its head and its key head NaN, in other documents of the row and before its step too.

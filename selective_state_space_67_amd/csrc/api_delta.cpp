@@ -149,11 +149,13 @@ ssm::DeltaPlan delta_plan(const P* p, int64_t len, const DeltaSizes& s) {
 
 // Sequences up to this long go step by step, unless pieces are asked for. The steps take
 // the longer the more there are, a chunk about the same time however few of its 64 tokens
-// are there. bfloat16, 128 x 128 states, 1 x 16 heads: 13.6, 17.4, 21.0 us at 12, 16, 20
-// steps against 17.7 in chunks (8 x 12 heads: 14.4, 18.1, 21.8 against 20.0; 64 x 16: 58.5,
-// 73.2, 89.0 against 104). float32, whose chunks take three times the products: 23.6 and
-// 30.8 us at 24 and 32 steps against 31.6 (8 x 12: 24.5, 31.2 against 38; 64 x 16: 101, 132
-// against 243).
+// are there. bfloat16, 128 x 128 states, 1 x 16 heads: 14.3, 18.0, 21.5 us at 12, 16, 20
+// steps against 19.4 in chunks (8 x 12 heads: 15.1, 18.5, 22.3 against 20.4; 64 x 16: 62,
+// 75, 90 against 107; 4 x 8 heads of 64 x 64: 11.6, 14.9, 17.8 against 16.3; 1 x 4 of 256 x
+// 256: 18.5, 23.4, 28.2 against 31.8). float32, whose chunks take three times the products:
+// 23.0, 29.7, 36.6 us at 24, 32, 40 steps against 29.5 (8 x 12: 25.1, 31.2, 37.7 against 30.5;
+// 64 x 16: 102, 129, 158 against 185; 64 x 64: 18.6, 23.9, 28.4 against 22.6; 256 x 256:
+// 33.5, 43.5, 53.4 against 71).
 constexpr int64_t steps_max(int in_dtype) { return in_dtype == SSM_BF16 ? 16 : 32; }
 
 // One workgroup for every chunk, and at most a workgroup for every 16 columns, in 31 bits: the

@@ -441,13 +441,18 @@ namespace {
 // Up to this many pieces are folded one after another, more in groups.
 constexpr int kFoldAlone = 16;
 
-// Pieces that cost least, in units of a chunk's step of the full walk (4.2 us at 128 x
+// Pieces that cost least, in units of a chunk's step of the full walk (about 5 us at 128 x
 // 128): rounds of one workgroup a CU times the chunks of a piece, where a step of the
 // aggregates' walk, which has a workgroup for every 64 of dk + dv columns, takes 0.7;
 // a piece's fold takes 0.7 (of three folds over the root of the pieces, where there are
 // groups); and two more launches. Measured at 128 x 128: 2 heads of 131072
-// steps 9356 us in one piece, 490 in 64; 16 heads x 2 of 4096 310 us, 244 in 4; 12 x 8 of
-// 2048 211 us (406 in two: the grid is full as it is).
+// steps 10212 us in one piece, 502 in 64; 16 heads x 2 of 4096 336 us, 232 in 4; 12 x 8 of
+// 2048 220 us (410 in two: the grid is full as it is). The costs are those of bfloat16 forward;
+// the choice was compared with one piece for 172 sizes (both types; 32 x 32, 64 x 64, 128 x
+// 128, 192 x 128, 256 x 64 and 256 x 256; 2 to 64 heads of 256 to 8192 steps), and for the
+// backward, which uses it too: it splits 70 of them, 3.0 times as fast in the mean (up to 15; the
+// backward 2.5, up to 11), and the worst loses 5% (bfloat16 256 x 64, 24 heads of 2048 steps,
+// 280 us against 267; backward 812 against 763).
 int choose_pieces(int64_t heads, int chunks, int dk, int dv) {
   constexpr int64_t kCUs = 256;
   const int64_t strips = (dv + 15) / 16, state_strips = 2 * padded_ks(dk);

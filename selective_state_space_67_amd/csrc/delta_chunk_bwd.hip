@@ -145,7 +145,7 @@ __device__ __forceinline__ void rev_stage_sync(char* st, const ChunkArgs& a, con
 // On few heads it goes in the forward's pieces: a first pass finds what every piece adds to
 // dH at its start, the fold carries dH back over them by the transposes of the forward's M,
 // and the full pass starts every piece from its own dH (1 x 4096 x 2 heads: the
-// whole backward 489 -> 223 us).
+// whole backward 489 us without, 215 with; this kernel 21 us for the first pass, 35 for the second).
 // Bound like the forward's walk by the chain of a chunk's products, one wave a SIMD, and
 // it writes dH1 and dR for the gradients' kernel besides: 260 us for 8 x 2048 x 12 heads of
 // 128 x 128 (1.8 TB/s), against 186 for the walk that leaves H0 and U.
@@ -393,14 +393,16 @@ __global__ __launch_bounds__(kThreads) void delta_chunk_reverse(const BwdArgs s)
 
 // ---- the gradients of a chunk ----
 
-// A workgroup takes up to 64 entries of q and k (SL tiles of 32): its accumulators then
-// fit 256 registers, and two workgroups share a CU, one multiplying while the other waits
+// A workgroup takes up to 64 entries of q and k (SL tiles of 32; 96 where they are 65 to
+// 96): its accumulators then come near 256 registers, and two workgroups share a CU, one multiplying while the other waits
 // for its operands. P and S are made anew for every split. 8 x 2048 x 12 heads of 128 x 128:
 // 548 us with all entries in one workgroup of eight waves, 417 so split, 360 with the
 // staged tiles turned against bank conflicts and 32-bit offsets from uniform bases; its
 // states, U, dR and dO are 0.65 GB (1.8 TB/s). Half of a wave's cycles are still waits:
 // every slab of 32 columns is split into bfloat16 parts, stored and read back between two
-// barriers. (Split by rows and columns of P instead: 1004 us, spilled.)
+// barriers. Every instance spills some of what it holds through the sums over dv: 13 to 57
+// registers for bfloat16 (174 with 96 entries), 38 to 221 for float32, which is 240 MB written
+// beside the results of that call. (Split by rows and columns of P instead: 1004 us, spilled.)
 __host__ __device__ constexpr int split_tiles(int ks) { return ks % 2 == 0 ? 2 : ks == 3 ? 3 : 1; }
 constexpr int grad_splits(int ks) { return ks / split_tiles(ks); }
 // A split's sums: own, end, the diagonal of dR U^T (64 tokens each), <dH1, H0>.

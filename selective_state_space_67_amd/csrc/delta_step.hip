@@ -19,8 +19,9 @@
 //
 // A decode step is bound by the state's bytes, 8 dk dv per head: 64 sequences of 16 heads of
 // 128 x 128 take 21.1 us, 6.4 TB/s (the state is partly in the last-level cache when the
-// steps follow one another); a small step by the call itself (10.3 us for one sequence of
-// 12 heads). Of several steps each takes 0.9 us, the latency of its arithmetic: the sums over
+// steps follow one another; after a read of 1 GB between them 30 us, events included, 4.5
+// TB/s); a small step by the call itself (10.3 us for one sequence of 12 heads, of which the
+// kernel takes 4.2). Of several steps each takes 0.9 us, the latency of its arithmetic: the sums over
 // the rows, u, and the state's update. (The next token loaded while one is worked on: 16
 // steps 17.4 -> 16.0 us for 1 x 16 heads, 73 -> 80 us for 64 x 16; not kept.)
 #include <algorithm>

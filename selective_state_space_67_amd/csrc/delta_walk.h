@@ -273,8 +273,8 @@ __device__ __forceinline__ void piece_again(int bh, int piece, int own, int lane
 // Bound by the chain of dependent steps of a chunk: K H0, R, T R, P U and K^T U follow
 // one another, and a workgroup has a wave for every SIMD of its CU and no second one to
 // fill its waits (8 x 2048 x 12 heads of 128 x 128 give 192 workgroups for 256 CUs, and the
-// two staged chunks of one take 158 KB of LDS). A chunk takes 4.2 us, about 10000 cycles,
-// 2900 of them matrix instructions: 155 us for that call, 1.6 TB/s of inputs, records and
+// two staged chunks of one take 158 KB of LDS). A chunk takes about 5 us, 12000 cycles,
+// 3450 of them matrix instructions: 172 us for that call, 1.8 TB/s of inputs, records and
 // outputs. The 16 columns a wave are what one operand of the matrix instruction holds: more
 // of them would share the operands of K, Q, T and P, but leave fewer waves than SIMDs.
 // AGG: the aggregates walk (no read-out; the first 32 KS columns start from the
