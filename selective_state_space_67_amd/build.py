@@ -14,8 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["api.cpp", "scan_fwd.hip", "scan_fwd_f32_plain.hip", "scan_fwd_f32_reset.hip", "scan_fwd_bf16_plain.hip",
            "scan_fwd_bf16_reset.hip", "scan_fwd_n16.hip", "scan_fwd_wavefront.hip", "scan_bwd.hip", "state_update.hip",
-           "scan_cplx.hip", "scan_cplx_bwd.hip", "fill.hip", "scan_noalloc.hip", "api_delta.cpp", "delta_step.hip",
-           "delta_chunk.hip", "delta_walk_bf16_direct.hip", "delta_walk_bf16.hip", "delta_walk_f32.hip",
+           "scan_cplx.hip", "scan_cplx_bwd.hip", "fill.hip", "scan_noalloc.hip", "scan_limits.hip", "api_delta.cpp",
+           "delta_step.hip", "delta_chunk.hip", "delta_walk_bf16_direct.hip", "delta_walk_bf16.hip", "delta_walk_f32.hip",
            "delta_chunk_bwd.hip", "qk_norm.hip", "log.cpp"]
 OUT = os.path.join(HERE, "libssmscan.so")
 OBJ = os.path.join(ROOT, "_build")

@@ -26,6 +26,7 @@
 #include <algorithm>
 
 #include "delta_chunk.h"
+#include "lane_sums.h"
 
 namespace ssm {
 namespace {

@@ -18,6 +18,7 @@
 
 #include "device_math.h"
 #include "kernels_delta.h"
+#include "lane_sums.h"
 
 namespace ssm {
 namespace {

@@ -45,8 +45,6 @@ int64_t scan_grid_blocks(int64_t B, int64_t D, int64_t N, int nseg) {
   return static_cast<int64_t>(nseg) * B * ((D + cpw - 1) / cpw);
 }
 
-int scan_block_threads(int64_t N) { return fwd::threads_per_block(N); }
-
 namespace {
 
 fwd::ScanArgs scan_args(const ScanPlan& pl) {

@@ -999,15 +999,6 @@ inline int channels_per_block(int64_t N) {
   return cpw;
 }
 
-inline int threads_per_block(int64_t N) {
-  int threads = 0;
-  (void)with_tile(N, [&](auto tile) {
-    threads = decltype(tile)::THREADS;
-    return hipSuccess;
-  });
-  return threads;
-}
-
 // Workgroups of the full pass that are resident at once on the whole chip
 // (256 CUs x 4 SIMDs x the kernel's waves per SIMD / waves per workgroup);
 // `plain`: the plain full pass (no conv stage, delta B coefficient).
