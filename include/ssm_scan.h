@@ -456,7 +456,7 @@ ssm_status ssm_scan_bwd(const ssm_scan_bwd_params* p, void* hip_stream);
  * out is rounded, to out_dtype. Outputs must not overlap inputs, each other or the
  * workspace. A non-finite input reaches what the recurrence hands it on to: from its step
  * to the end of its document, the other columns too unless it is in v or h0. (The 16
- * columns around one that it reaches are then worked out step by step, about 2 us a step.)
+ * columns around one that it reaches are then worked out step by step, 1 to 4 us a step.)
  */
 typedef struct {
   int64_t batch, seqlen, key_heads, value_heads, dk, dv;

@@ -189,7 +189,8 @@ __device__ __forceinline__ int64_t last_start(const uint8_t* reset, int64_t from
 // token, and the fold does so with the pieces before, so that a NaN or an infinity among the
 // inputs reaches tokens that the recurrence keeps it from. A strip that has made a non-finite
 // output therefore goes through its piece again here, and what is not finite afterwards is so
-// by the recurrence. About 2 us a token, on such inputs alone.
+// by the recurrence. On such inputs alone it takes 2 us a token for 128 entries of k (0.8 for 48,
+// 3.7 for 256; 5.5 with a load for every entry).
 //
 // The arguments are read anew from where the kernel was passed them, and the lane's place is
 // hidden from the compiler: it would otherwise work out what it can of this ahead of the walk
@@ -238,20 +239,38 @@ __device__ __forceinline__ void piece_again(int bh, int piece, int own, int lane
 #pragma unroll
       for (int m = 0; m < 2 * KS; ++m) H[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    f32x4 kv[2 * KS];
+    f32x4 kv[2 * KS], qv[2 * KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      // the lane's eight rows 32 ks + 8 g .. of tiles 2 ks and 2 ks + 1; rows past dk are read
+      // from before it and taken as 0
+      const int row0 = ks * 32 + 2 * g4, last = a.dk - 1;
+      float kx[8], qx[8];
+      if (a.vec) {
+        const int at = min(row0, last - 7);
+        load8<InT, true>(k + at, 8, kx);
+        load8<InT, true>(q + at, 8, qx);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          kx[i] = load_elem(k, min(row0 + i, last));
+          qx[i] = load_elem(q, min(row0 + i, last));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        kv[2 * ks + i / 4][i % 4] = row0 + i < a.dk ? kx[i] : 0.0f;
+        qv[2 * ks + i / 4][i % 4] = row0 + i < a.dk ? qx[i] : 0.0f;
+      }
+    }
     float kh = 0.0f, qh = 0.0f, kq = 0.0f;
-    int dk = a.dk;
-    asm volatile("" : "+v"(dk));  // or the rows' masks are kept from token to token
 #pragma unroll
     for (int m = 0; m < 2 * KS; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int d = state_row(m, g4, r);
-        kv[m][r] = d < dk ? load_elem(k, d) : 0.0f;
-        const float qv = d < dk ? load_elem(q, d) : 0.0f;
         kh = __builtin_fmaf(kv[m][r], H[m][r], kh);
-        qh = __builtin_fmaf(qv, H[m][r], qh);
-        kq = __builtin_fmaf(kv[m][r], qv, kq);
+        qh = __builtin_fmaf(qv[m][r], H[m][r], qh);
+        kq = __builtin_fmaf(kv[m][r], qv[m][r], kq);
       }
     const float u = beta * __builtin_fmaf(-al, column_sum(kh), v);
     const float o = a.scale * __builtin_fmaf(al, column_sum(qh), column_sum(kq) * u);
