@@ -648,6 +648,129 @@ ssm_status ssm_qk_norm_bwd_workspace_size(const ssm_qk_norm_params* p, size_t* b
 /* Enqueue the gradients described by `p` on `hip_stream`. */
 ssm_status ssm_qk_norm_bwd(const ssm_qk_norm_params* p, void* hip_stream);
 
+/*
+ * Gated linear recurrence: one state for each channel, with its own decay and
+ * input gate at every step, channels innermost. For batch row b, channel d:
+ *
+ *   s_t = sigmoid(dt_raw[b,t,d] + dt_bias[d])    (SSM_GLR_SIGMOID)
+ *         softplus(dt_raw[b,t,d] + dt_bias[d])   (SSM_GLR_SOFTPLUS)
+ *   a_t = exp(A[d] * s_t)                        (0 where reset[b,t] != 0)
+ *   i_t = sigmoid(in_raw[b,t,d] + in_bias[d])    (1 without in_raw)
+ *   c_t = sqrt(1 - a_t^2) (SSM_GLR_UNIT), 1 - a_t (SSM_GLR_REST) or 1 (SSM_GLR_ONE)
+ *   h_t = a_t h_{t-1} + c_t i_t u[b,t,d]
+ *   out = h_t silu(z[b,t,d])                     (h_t without z)
+ *
+ * with h_{-1} = h0 (zeros when absent).
+ *
+ *   batch, seqlen, dim : B >= 0, 0 <= L < 2^27, 0 <= D <= 2^24
+ *   in_dtype  : element type of u, dt_raw, in_raw, z (and dout)
+ *   u, dt_raw (B,L,D) required; in_raw, z (B,L,D), NULL => none. Channels are dense;
+ *            the strides are the elements from one token to the next (at least D;
+ *            0 = D), with batch rows L tokens apart, so slices of one packed
+ *            projection can be passed as they lie.
+ *   A        (D) float32, required. Any real value is accepted by SSM_GLR_REST and
+ *            SSM_GLR_ONE; a_t above 1 (A > 0) makes SSM_GLR_UNIT's root NaN.
+ *   dt_bias, in_bias (D) float32, NULL => 0 (in_bias only with in_raw)
+ *   reset    (B,L) uint8, NULL => none; h0 (B,D) float32, NULL => 0
+ * ssm_glr_fwd:
+ *   out      (B,L,D) required, dense, out_dtype; h_last (B,D) float32, NULL => not written
+ *   num_segments : 0 = the library chooses how many pieces to split L into;
+ *            k >= 1 asks for k pieces (clamped to what L allows).
+ *   workspace, workspace_bytes : at least ssm_glr_workspace_size() bytes, aligned to
+ *            256 (none for an unsplit sequence); contents on entry ignored.
+ * ssm_glr_bwd, gradients of  loss = sum dout * out + sum dh_last * h_last  for the
+ * same inputs (no intermediate of the forward is needed). With lam_t the adjoint of h_t:
+ *   dy = dout silu(z),  dz = dout h silu'(z),  lam_t = dy_t + a_{t+1} lam_{t+1}
+ *   du = lam c i,  d in_raw = lam c u i (1 - i)
+ *   dg = lam a (h_{t-1} + i u dc/da),  d dt_raw = dg A s',  dA = sum dg s,  dh0 = a_0 lam_0
+ *   (dg and what goes on to h_{t-1} are 0 where reset is set; where a_t rounds to 1, so
+ *   that SSM_GLR_UNIT's c is 0, the part of dg with dc/da is left out: its limit is 0 for
+ *   d dt_raw and dA)
+ *   dout     (B,L,D) required, dense, in_dtype; dh_last (B,D) float32, NULL => 0
+ *   du, d_dt_raw (B,L,D) required, din_raw with in_raw and dz with z required: dense, out_dtype
+ *   dA       (D) float32, required; d_dt_bias, din_bias (D), dh0 (B,D) float32, NULL => not
+ *            written. Sums go in a fixed order: repeated calls give identical bits.
+ *   workspace, workspace_bytes : at least ssm_glr_bwd_workspace_size() bytes, aligned to
+ *            256: 32 bytes for every 64 steps of a channel. num_segments is not read.
+ * Arithmetic is float32 whatever in_dtype is; only results are rounded. Outputs must not
+ * overlap inputs, each other or the workspace. A non-finite input stays within its
+ * channel and document (the sums over tokens aside).
+ */
+typedef enum { SSM_GLR_SIGMOID = 0, SSM_GLR_SOFTPLUS = 1 } ssm_glr_decay;
+typedef enum { SSM_GLR_UNIT = 0, SSM_GLR_REST = 1, SSM_GLR_ONE = 2 } ssm_glr_mix;
+
+typedef struct {
+  int64_t batch, seqlen, dim;
+  int32_t in_dtype, out_dtype; /* out_dtype: of out, or of the gradients */
+  const void* u;
+  const void* dt_raw;
+  const void* in_raw;
+  const void* z;
+  int64_t u_stride, dt_stride, in_stride, z_stride;
+  const float* A;
+  const float* dt_bias;
+  const float* in_bias;
+  const uint8_t* reset;
+  const float* h0;
+  void* out;
+  float* h_last;
+  const void* dout;
+  const float* dh_last;
+  void* du;
+  void* d_dt_raw;
+  void* din_raw;
+  void* dz;
+  float* dA;
+  float* d_dt_bias;
+  float* din_bias;
+  float* dh0;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t decay; /* ssm_glr_decay */
+  int32_t mix;   /* ssm_glr_mix */
+  int32_t num_segments;
+  int32_t reserved0; /* set to 0 */
+} ssm_glr_params;
+
+/* Bytes of workspace ssm_glr_fwd needs (sizes, dtypes and num_segments are read;
+ * pointers are not). */
+ssm_status ssm_glr_workspace_size(const ssm_glr_params* p, size_t* bytes);
+
+/* Enqueue the whole-sequence recurrence described by `p` on `hip_stream`. */
+ssm_status ssm_glr_fwd(const ssm_glr_params* p, void* hip_stream);
+
+/* Bytes of workspace ssm_glr_bwd needs (only sizes and dtypes of `p` are read). */
+ssm_status ssm_glr_bwd_workspace_size(const ssm_glr_params* p, size_t* bytes);
+
+/* Enqueue the backward pass described by `p` on `hip_stream`. */
+ssm_status ssm_glr_bwd(const ssm_glr_params* p, void* hip_stream);
+
+/*
+ * The same recurrence over a window of `tokens` steps (one for ordinary decoding,
+ * a few for drafted tokens), with the state updated in place. No workspace.
+ *   h        (B,D) float32, required; read as h_{t-1}, overwritten
+ *   u, dt_raw, in_raw, z, out (B,T,D); strides as in ssm_glr_params. T = 0 leaves h
+ *            as it is.
+ */
+typedef struct {
+  int64_t batch, tokens, dim;
+  int32_t in_dtype, out_dtype;
+  float* h;
+  const void* u;
+  const void* dt_raw;
+  const void* in_raw;
+  const void* z;
+  int64_t u_stride, dt_stride, in_stride, z_stride;
+  const float* A;
+  const float* dt_bias;
+  const float* in_bias;
+  void* out;
+  int32_t decay, mix;
+} ssm_glr_update_params;
+
+/* Enqueue the decode window described by `p` on `hip_stream`. */
+ssm_status ssm_glr_update(const ssm_glr_update_params* p, void* hip_stream);
+
 /* Static, human-readable name of a status code ("unknown status" otherwise). */
 const char* ssm_status_string(int32_t status);
 
@@ -662,7 +785,8 @@ int32_t ssm_version(void);
  * which = 0 -> ssm_scan_params, 1 -> ssm_update_params,
  * 2 -> ssm_scan_bwd_params, 3 -> ssm_delta_params,
  * 4 -> ssm_delta_update_params, 5 -> ssm_delta_bwd_params,
- * 6 -> ssm_qk_norm_params; 0 for anything else.
+ * 6 -> ssm_qk_norm_params, 8 -> ssm_glr_params, 9 -> ssm_glr_update_params;
+ * 0 for anything else.
  * Bindings compare these with their own layouts at load time. */
 size_t ssm_abi_struct_size(int32_t which);
 

@@ -878,6 +878,8 @@ size_t ssm_abi_struct_size(int32_t which) {
   if (which == 4) return sizeof(ssm_delta_update_params);
   if (which == 5) return sizeof(ssm_delta_bwd_params);
   if (which == 6) return sizeof(ssm_qk_norm_params);
+  if (which == 8) return sizeof(ssm_glr_params);
+  if (which == 9) return sizeof(ssm_glr_update_params);
   return 0;
 }
 

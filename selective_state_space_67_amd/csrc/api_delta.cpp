@@ -13,30 +13,23 @@
 
 namespace {
 
-using ssm::aligned;
+using ssm::check_overlaps;
+using ssm::check_pointers;
 using ssm::dtype_size;
 using ssm::fail;
+using ssm::kLim;
 using ssm::mul_ok;
+using ssm::Need;
 using ssm::ok;
 using ssm::overlaps;
 using ssm::Range;
 using ssm::range;
+using ssm::span;
 using ssm::valid_dtype;
 
 constexpr int64_t kMaxLen = int64_t{1} << 27;
 constexpr int64_t kMaxHeads = 65536;
 constexpr int64_t kMaxColumns = 65536;
-constexpr int64_t kLim = std::numeric_limits<int64_t>::max() / 16;
-
-// Elements spanned by `tokens` tokens `stride` apart, each `size` long.
-bool span(int64_t tokens, int64_t stride, int64_t size, int64_t* n) {
-  *n = 0;
-  if (tokens == 0 || size == 0) return true;
-  int64_t m;
-  if (!mul_ok(tokens - 1, stride, &m) || m > kLim - size) return false;
-  *n = m + size;
-  return true;
-}
 
 struct DeltaSizes {
   int64_t tokens;              // B L
@@ -88,37 +81,6 @@ ssm_status check_delta_sizes(const P* p, int64_t len, int32_t other_dtype, Delta
 ssm_status check_steps_grid(int64_t batch, int64_t heads, int64_t dv) {
   if (batch * heads > ((int64_t{1} << 24) - 1) / ((dv + 63) / 64))
     return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
-  return SSM_OK;
-}
-
-struct Need {
-  const void* ptr;
-  int64_t count;
-  size_t align;
-  const char* name;
-  bool required;
-};
-
-// Required pointers are there (a pointer to an empty tensor may be NULL) and
-// every pointer is aligned.
-template <int N>
-ssm_status check_pointers(const Need (&needs)[N]) {
-  for (const Need& n : needs)
-    if (n.required && !n.ptr && n.count > 0) return fail(SSM_ERR_NULL_POINTER, "%s is NULL", n.name);
-  for (const Need& n : needs)
-    if (n.ptr && !aligned(n.ptr, n.align))
-      return fail(SSM_ERR_MISALIGNED, "%s is not aligned to %zu bytes", n.name, n.align);
-  return SSM_OK;
-}
-
-template <int NI, int NO>
-ssm_status check_overlaps(const Range (&in)[NI], const Range (&out)[NO]) {
-  for (int i = 0; i < NO; ++i) {
-    for (const Range& r : in)
-      if (overlaps(out[i], r)) return fail(SSM_ERR_ALIAS, "%s overlaps %s", out[i].name, r.name);
-    for (int j = i + 1; j < NO; ++j)
-      if (overlaps(out[i], out[j])) return fail(SSM_ERR_ALIAS, "%s overlaps %s", out[i].name, out[j].name);
-  }
   return SSM_OK;
 }
 

@@ -1,0 +1,225 @@
+// Gradients of the gated linear recurrence.
+//
+// With lam_t the adjoint of h_t,
+//
+//   dy = dout silu(z),  lam_t = dy_t + a_{t+1} lam_{t+1},  dz = dout h silu'(z)
+//   du = lam c i,  d in_raw = lam c u i (1 - i)
+//   dg = lam a (h_{t-1} + i u dc/da),  dc/da = -a/c, -1 or 0
+//   d dt_raw = dg A s',  dA = sum dg s,  dh0 = a_0 lam_0
+//
+// and dg = 0 at a reset, which hands no adjoint on either.
+//
+// Three passes: what every piece of 64 rows does to a state and to an adjoint
+// (glr_aggregate: u, dt_raw, in_raw, z, dout read once), the states and adjoints
+// that enter the pieces (glr_fold), and here the pieces' gradients, all in
+// parallel: a workgroup takes one piece of 64 channels, its waves K rows each,
+// kept in registers. Each wave's rows act on a state as (P, H) and on an adjoint
+// as (P, G); the waves exchange them through LDS once. The parameters' gradients
+// are summed over a wave's rows in registers, over the waves in LDS, and over the
+// pieces by glr_sums, always in the same order.
+#include "glr_device.h"
+#include "glr_launch.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kWaves = 8, kRows = 8, kPiece = kWaves * kRows;
+
+template <typename InT, int DECAY, int MIX, int W, int K>
+__global__ __launch_bounds__(kLanes * W) void glr_grads(const GlrArgs g) {
+  __shared__ float ex[3][W][kLanes];  // P, H, G; then the three sums
+  const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
+  const int tile = blockIdx.x % g.tiles, rest = blockIdx.x / g.tiles;
+  const int piece = rest % g.pieces, batch = rest / g.pieces;
+  const int channel = tile * kLanes + lane, ch = min(channel, g.D - 1);
+  const bool on = channel < g.D;
+  const uint32_t at = static_cast<uint32_t>(ch) * sizeof(InT);
+  const int64_t row0 = batch * g.L, t = static_cast<int64_t>(piece) * (W * K) + w * K;
+  const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{K}, g.L - t)));
+  const int64_t row = row0 + min(t, g.L - 1);
+  const int have = max(rows, 1);
+  uint32_t ru[K], rdt[K], rin[K], rz[K], rdy[K];
+  load_rows<InT, K>(g.dt, row, g.ds, have, at, rdt);
+  load_rows<InT, K>(g.u, row, g.us, have, at, ru);
+  if (g.in) load_rows<InT, K>(g.in, row, g.is, have, at, rin);
+  load_rows<InT, K>(g.dout, row, g.D, have, at, rdy);
+  if (g.z) load_rows<InT, K>(g.z, row, g.zs, have, at, rz);
+  const uint32_t reset = reset_byte<K>(g.reset, row, rows, lane);
+  const int64_t joint = (static_cast<int64_t>(batch) * g.pieces + piece) * g.D + ch;
+  float h = g.starts[joint], m = g.ends[joint];
+  const float A = g.A[ch], dt_bias = g.dt_bias ? g.dt_bias[ch] : 0.0f, in_bias = g.in_bias ? g.in_bias[ch] : 0.0f;
+  const uint32_t cuts = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(reset != 0));
+
+  float a[K], c[K], x[K], i[K], s[K], dy[K];  // x = i u
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const float raw = widen<InT>(rdt[k]) + dt_bias;
+    s[k] = decay_gate<DECAY>(raw);
+    decay_terms<MIX>(A * s[k], a[k], c[k]);
+    if ((cuts >> k) & 1) c[k] = 1.0f;
+    x[k] = widen<InT>(ru[k]);
+    dy[k] = widen<InT>(rdy[k]);
+    i[k] = 1.0f;
+  }
+  if (g.in) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      i[k] = sigmoid_f32(widen<InT>(rin[k]) + in_bias);
+      x[k] *= i[k];
+    }
+  }
+  if (g.z) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) dy[k] *= silu_f32(widen<InT>(rz[k]));
+  }
+  // what the wave's rows do to a state and to an adjoint
+  float P = 1.0f, H = 0.0f, G = 0.0f;
+  bool cut = false;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (k < rows) {
+      const bool here = (cuts >> k) & 1;
+      cut |= here;
+      P *= a[k];
+      H = here ? x[k] : __builtin_fmaf(a[k], H, c[k] * x[k]);
+      if (!cut) G = __builtin_fmaf(P, dy[k], G);
+    }
+  }
+  if (cut) P = kCut;
+  ex[0][w][lane] = P;
+  ex[1][w][lane] = H;
+  ex[2][w][lane] = G;
+  __syncthreads();
+  for (int j = 0; j < w; ++j) h = through(ex[0][j][lane], ex[1][j][lane], h);
+  for (int j = W - 1; j > w; --j) m = through(ex[0][j][lane], ex[2][j][lane], m);
+
+  float before[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    before[k] = h;
+    const float b = c[k] * x[k];
+    h = (cuts >> k) & 1 ? b : __builtin_fmaf(a[k], h, b);
+  }
+  const int size = g.out_bf16 ? 2 : 4;
+  const int64_t first = ((row0 + t) * g.D) * size;
+  float sum_A = 0.0f, sum_dt = 0.0f, sum_in = 0.0f;
+#pragma unroll
+  for (int k = K - 1; k >= 0; --k) {
+    if (k < rows) {
+      const bool here = (cuts >> k) & 1;
+      const int64_t to = first + static_cast<int64_t>(k) * g.D * size;
+      const float lam = dy[k] + m;
+      if (g.z) {
+        const float z = widen<InT>(rz[k]), sz = sigmoid_f32(z), now = here ? c[k] * x[k] : __builtin_fmaf(a[k], before[k], c[k] * x[k]);
+        const float dz = widen<InT>(rdy[k]) * now * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
+        if (on) store_result(static_cast<char*>(g.dz) + to, ch, dz, g.out_bf16);
+      }
+      const float lc = lam * c[k];
+      if (on) store_result(static_cast<char*>(g.du) + to, ch, lc * i[k], g.out_bf16);
+      if (g.in) {
+        const float d = lc * x[k] * (1.0f - i[k]);
+        sum_in += d;
+        if (on) store_result(static_cast<char*>(g.d_in) + to, ch, d, g.out_bf16);
+      }
+      float d_dt = 0.0f;
+      if (here) {
+        m = 0.0f;
+      } else {
+        m = a[k] * lam;
+        // where a rounds to 1, c is 0 and its slope infinite, but what the gate and A get tends to 0
+        float dc = 0.0f;
+        if (MIX == kGlrUnit) dc = c[k] == 0.0f ? 0.0f : -a[k] * fast_rcp(c[k]);
+        if (MIX == kGlrRest) dc = -1.0f;
+        const float dg = m * __builtin_fmaf(x[k], dc, before[k]);
+        sum_A = __builtin_fmaf(dg, s[k], sum_A);
+        const float slope = DECAY == kGlrSigmoid ? s[k] * (1.0f - s[k]) : sigmoid_f32(widen<InT>(rdt[k]) + dt_bias);
+        d_dt = dg * A * slope;
+        sum_dt += d_dt;
+      }
+      if (on) store_result(static_cast<char*>(g.d_dt) + to, ch, d_dt, g.out_bf16);
+    }
+  }
+  __syncthreads();
+  ex[0][w][lane] = sum_A;
+  ex[1][w][lane] = sum_dt;
+  ex[2][w][lane] = sum_in;
+  __syncthreads();
+  if (w < 3 && on) {
+    float v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) v += ex[w][j][lane];
+    g.part[((static_cast<int64_t>(batch) * g.pieces + piece) * 3 + w) * g.D + ch] = v;
+  }
+}
+
+// The pieces' sums, 16 columns a workgroup (of 3 D), 16 threads a column, each adding every
+// 16th piece in order with eight of them under way, then the 16 sums in order.
+__global__ __launch_bounds__(256) void glr_sums(const float* __restrict__ part, float* dA, float* d_dt_bias,
+                                                float* din_bias, int64_t rows, int D) {
+  constexpr int kAhead = 8;
+  __shared__ float t[16][17];
+  const int col = threadIdx.x % 16, by = threadIdx.x / 16;
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 16 + col, width = 3 * static_cast<int64_t>(D);
+  float x = 0.0f;
+  if (e < width)
+    for (int64_t r = by; r < rows; r += 16 * kAhead) {
+      float v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) v[i] = r + 16 * i < rows ? part[(r + 16 * i) * width + e] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) x += v[i];
+    }
+  t[by][col] = x;
+  __syncthreads();
+  if (by != 0 || e >= width) return;
+  x = 0.0f;
+  for (int r = 0; r < 16; ++r) x += t[r][col];
+  const int which = static_cast<int>(e / D);
+  float* dst = which == 0 ? dA : which == 1 ? d_dt_bias : din_bias;
+  if (dst) dst[e - static_cast<int64_t>(which) * D] = x;
+}
+
+struct Grads {
+  template <typename InT, int DECAY, int MIX>
+  static hipError_t run(unsigned blocks, const GlrArgs& g, hipStream_t stream) {
+    hipLaunchKernelGGL((glr_grads<InT, DECAY, MIX, kWaves, kRows>), dim3(blocks), dim3(kWaves * kLanes), 0, stream, g);
+    return hipGetLastError();
+  }
+};
+
+}  // namespace
+
+GlrPieces plan_glr_bwd(int64_t B, int64_t L, int64_t D) {
+  GlrPieces p{};
+  p.rows = kPiece;
+  p.waves = kWaves;
+  p.ways = 2;
+  p.pieces = (L + kPiece - 1) / kPiece;
+  const size_t each = (static_cast<size_t>(B) * p.pieces * D * sizeof(float) + 255) / 256 * 256;
+  p.off_H = each;
+  p.off_G = 2 * each;
+  p.off_starts = 3 * each;
+  p.off_ends = 4 * each;
+  p.off_part = 5 * each;
+  p.bytes = 8 * each;
+  return p;
+}
+
+hipError_t launch_glr_bwd(const GlrPlan& plan, const GlrPieces& pieces, void* workspace, hipStream_t stream) {
+  const GlrArgs g = glr_args(plan, pieces, workspace);
+  hipError_t e = launch_glr_aggregates(plan, g, pieces.pieces, true, stream);
+  if (e == hipSuccess) e = launch_glr_fold(plan, g, pieces.pieces, true, stream);
+  if (e != hipSuccess) return e;
+  const unsigned blocks = static_cast<unsigned>(plan.B * pieces.pieces * g.tiles);
+  SSM_LOG("launch glr_grads: %lld pieces of %d rows; grid %u x %d threads", static_cast<long long>(pieces.pieces),
+          kPiece, blocks, kWaves * kLanes);
+  e = glr_pick<Grads>(plan, blocks, g, stream);
+  if (e != hipSuccess) return e;
+  const unsigned grid = static_cast<unsigned>((3 * plan.D + 15) / 16);
+  SSM_LOG("launch glr_sums: grid %u x 256 threads", grid);
+  hipLaunchKernelGGL(glr_sums, dim3(grid), dim3(256), 0, stream, g.part, plan.dA, plan.d_dt_bias, plan.din_bias,
+                     plan.B * pieces.pieces, g.D);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

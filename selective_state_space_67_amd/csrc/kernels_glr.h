@@ -1,0 +1,77 @@
+// Host-side interface between the front end of the gated linear recurrence
+// (api_glr.cpp) and its kernels (glr_fwd.hip, glr_pieces.hip, glr_bwd.hip). Not
+// installed; not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "launch_limits.h"
+#include "log.h"
+
+namespace ssm {
+
+constexpr int kGlrSigmoid = 0, kGlrSoftplus = 1;         // decay
+constexpr int kGlrUnit = 0, kGlrRest = 1, kGlrOne = 2;   // mix
+
+// One call after validation. Pointers are device pointers; optional ones are
+// nullptr. Token strides are in elements.
+struct GlrPlan {
+  int64_t B, L, D;
+  int in_bf16, out_bf16, decay, mix;  // out_bf16: type of out, or of the gradients
+  const void* u;
+  const void* dt;
+  const void* in;
+  const void* z;
+  int64_t us, ds, is, zs;
+  const float* A;
+  const float* dt_bias;
+  const float* in_bias;
+  const uint8_t* reset;
+  const float* h0;
+  void* out;
+  float* h_last;  // may equal h0 in the decode window
+  // backward
+  const void* dout;
+  const float* dh_last;
+  void* du;
+  void* d_dt;
+  void* d_in;
+  void* dz;
+  float* dA;
+  float* d_dt_bias;
+  float* din_bias;
+  float* dh0;
+};
+
+// How a sequence is cut into pieces, and where the workspace holds what joins them.
+struct GlrPieces {
+  int64_t pieces, rows;  // rows of a piece; forward, pieces = 1: a single walk, no workspace
+  int waves;             // of a workgroup that takes a piece of 64 channels
+  int ways;              // in which the pieces are folded: states (1), adjoints too (2)
+  size_t off_P, off_H, off_G, off_starts, off_ends, off_part, bytes;
+};
+// requested = 0: automatic. Pure host arithmetic, like the others here.
+GlrPieces plan_glr(int64_t B, int64_t L, int64_t D, int requested);
+GlrPieces plan_glr_bwd(int64_t B, int64_t L, int64_t D);
+// Whether every launch of a call stays below 2^32 threads.
+bool glr_grids_fit(int64_t B, int64_t D, const GlrPieces& pieces);
+// Sequences that go step by step, one thread a channel.
+bool glr_by_steps(int64_t L);
+bool glr_steps_fit(int64_t B, int64_t D);
+
+hipError_t launch_glr(const GlrPlan& plan, const GlrPieces& pieces, void* workspace, hipStream_t stream);
+hipError_t launch_glr_steps(const GlrPlan& plan, hipStream_t stream);
+hipError_t launch_glr_bwd(const GlrPlan& plan, const GlrPieces& pieces, void* workspace, hipStream_t stream);
+
+// Between the kernels' files.
+struct GlrArgs;
+GlrArgs glr_args(const GlrPlan& plan, const GlrPieces& pieces, void* workspace);
+// P and H (and G) of the first `count` pieces of every batch row.
+hipError_t launch_glr_aggregates(const GlrPlan& plan, const GlrArgs& args, int64_t count, bool backward,
+                                 hipStream_t stream);
+// The states entering the pieces from h0, and for the backward the adjoints from dh_last (and dh0).
+hipError_t launch_glr_fold(const GlrPlan& plan, const GlrArgs& args, int64_t count, bool backward, hipStream_t stream);
+
+}  // namespace ssm
