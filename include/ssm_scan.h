@@ -771,6 +771,119 @@ typedef struct {
 /* Enqueue the decode window described by `p` on `hip_stream`. */
 ssm_status ssm_glr_update(const ssm_glr_update_params* p, void* hip_stream);
 
+/*
+ * The norm of a mixer's output x with its gate z, for every head (row of head_dim
+ * entries) of every token. With r(v) = (mean v^2 + eps)^-1/2:
+ *
+ *   out = w * (x r(x)) * silu(z)           (gate_first = 0)
+ *   out = w * (v r(v)),  v = x * silu(z)   (gate_first = 1)
+ *
+ *   batch, seqlen, heads : sizes >= 0, seqlen < 2^27, heads <= 65536
+ *   head_dim  : 1 <= head_dim <= SSM_MAX_NORM_DIM (one head of all channels: a layer's norm)
+ *   x, z     (B,L,heads,head_dim) in_dtype, required. Heads are dense inside a token;
+ *            x_stride, z_stride are the elements from one token to the next (at least
+ *            the token's own size; 0 = dense), with batch rows L tokens apart.
+ *   w        float32, NULL => 1: (head_dim), or (heads, head_dim) with w_per_head
+ *   out      as x, dense, out_dtype
+ * ssm_gated_norm_bwd, gradients of  loss = sum dout * out  for the same inputs:
+ *   dout     dense, in_dtype, required; dx, dz dense, out_dtype, required
+ *   dw       as w, float32, NULL => not written: a sum in a fixed order
+ *   workspace, workspace_bytes : at least ssm_gated_norm_bwd_workspace_size() bytes,
+ *            aligned to 16 (the forward needs none)
+ * Sums and factors are float32; only results are rounded.
+ */
+#define SSM_MAX_NORM_DIM 16384
+
+typedef struct {
+  int64_t batch, seqlen, heads, head_dim;
+  int32_t in_dtype, out_dtype; /* out_dtype: of out, or of dx and dz */
+  const void* x;
+  const void* z;
+  int64_t x_stride, z_stride;
+  const float* w;
+  void* out;
+  const void* dout;
+  void* dx;
+  void* dz;
+  float* dw;
+  void* workspace;
+  size_t workspace_bytes;
+  float eps;
+  int32_t gate_first; /* 0 or 1 */
+  int32_t w_per_head; /* 0 or 1 */
+  int32_t reserved0;  /* set to 0 */
+} ssm_gated_norm_params;
+
+/* Enqueue the norm described by `p` on `hip_stream`. */
+ssm_status ssm_gated_norm_fwd(const ssm_gated_norm_params* p, void* hip_stream);
+
+/* Bytes of workspace ssm_gated_norm_bwd needs (sizes are read; pointers are not). */
+ssm_status ssm_gated_norm_bwd_workspace_size(const ssm_gated_norm_params* p, size_t* bytes);
+
+/* Enqueue the gradients described by `p` on `hip_stream`. */
+ssm_status ssm_gated_norm_bwd(const ssm_gated_norm_params* p, void* hip_stream);
+
+/*
+ * Between two blocks: the output y of one joins the residual stream x, and the input
+ * of the next is normed. For every token, r as above:
+ *
+ *   m     = w_post * (y r(y)) with post, else y
+ *   x_out = x + scale * gate * m
+ *   out   = w * (x_out r(x_out))
+ *
+ * out is the norm of x_out before that is rounded to res_dtype.
+ *   batch, seqlen : sizes >= 0, seqlen < 2^27; dim : 1 <= D <= SSM_MAX_NORM_DIM
+ *   y        (B,L,D) in_dtype, required; y_stride elements from token to token (0 = D)
+ *   x        (B,L,D) res_dtype, dense, NULL => 0 (the stream starts here)
+ *   w, w_post (D) float32, NULL => 1 (w_post only with post)
+ *   gate     float32, NULL => 1: (D), or (B,D) with gate_rows (a gate for each sequence)
+ *   out      (B,L,D) dense, out_dtype, required; x_out (B,L,D) dense, res_dtype, NULL =>
+ *            not written
+ * ssm_block_norm_bwd, gradients of  loss = sum dout * out + sum dx_out * x_out  for the
+ * same inputs (x_out itself is not needed):
+ *   dout     dense, in_dtype, required; dx_out dense, res_dtype, NULL => 0
+ *   dy       dense, out_dtype, required; dx dense, res_dtype, NULL => not written
+ *   dw, dw_post (D), dgate (as gate) float32, NULL => not written (dw_post only with post,
+ *            dgate only with gate): sums in a fixed order
+ *   workspace, workspace_bytes : at least ssm_block_norm_bwd_workspace_size() bytes,
+ *            aligned to 16 (the forward needs none)
+ * Sums and factors are float32; only results are rounded.
+ */
+typedef struct {
+  int64_t batch, seqlen, dim;
+  int32_t in_dtype, out_dtype, res_dtype;
+  int32_t gate_rows; /* 0 or 1 */
+  const void* y;
+  int64_t y_stride;
+  const void* x;
+  const float* w;
+  const float* w_post;
+  const float* gate;
+  void* out;
+  void* x_out;
+  const void* dout;
+  const void* dx_out;
+  void* dy;
+  void* dx;
+  float* dw;
+  float* dw_post;
+  float* dgate;
+  void* workspace;
+  size_t workspace_bytes;
+  float eps, scale;
+  int32_t post;      /* 0 or 1 */
+  int32_t reserved0; /* set to 0 */
+} ssm_block_norm_params;
+
+/* Enqueue what `p` describes on `hip_stream`. */
+ssm_status ssm_block_norm_fwd(const ssm_block_norm_params* p, void* hip_stream);
+
+/* Bytes of workspace ssm_block_norm_bwd needs (sizes are read; pointers are not). */
+ssm_status ssm_block_norm_bwd_workspace_size(const ssm_block_norm_params* p, size_t* bytes);
+
+/* Enqueue the gradients described by `p` on `hip_stream`. */
+ssm_status ssm_block_norm_bwd(const ssm_block_norm_params* p, void* hip_stream);
+
 /* Static, human-readable name of a status code ("unknown status" otherwise). */
 const char* ssm_status_string(int32_t status);
 
@@ -785,8 +898,8 @@ int32_t ssm_version(void);
  * which = 0 -> ssm_scan_params, 1 -> ssm_update_params,
  * 2 -> ssm_scan_bwd_params, 3 -> ssm_delta_params,
  * 4 -> ssm_delta_update_params, 5 -> ssm_delta_bwd_params,
- * 6 -> ssm_qk_norm_params, 8 -> ssm_glr_params, 9 -> ssm_glr_update_params;
- * 0 for anything else.
+ * 6 -> ssm_qk_norm_params, 8 -> ssm_glr_params, 9 -> ssm_glr_update_params,
+ * 10 -> ssm_gated_norm_params, 11 -> ssm_block_norm_params; 0 for anything else.
  * Bindings compare these with their own layouts at load time. */
 size_t ssm_abi_struct_size(int32_t which);
 

@@ -94,7 +94,9 @@ EXPORTS = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_scan_fwd_noalloc", "s
            "ssm_delta_workspace_size", "ssm_delta_fwd", "ssm_delta_update", "ssm_delta_bwd_workspace_size",
            "ssm_delta_bwd", "ssm_qk_norm_fwd",
            "ssm_qk_norm_bwd_workspace_size", "ssm_qk_norm_bwd",
-           "ssm_glr_workspace_size", "ssm_glr_fwd", "ssm_glr_update", "ssm_glr_bwd_workspace_size", "ssm_glr_bwd")
+           "ssm_glr_workspace_size", "ssm_glr_fwd", "ssm_glr_update", "ssm_glr_bwd_workspace_size", "ssm_glr_bwd",
+           "ssm_gated_norm_fwd", "ssm_gated_norm_bwd_workspace_size", "ssm_gated_norm_bwd",
+           "ssm_block_norm_fwd", "ssm_block_norm_bwd_workspace_size", "ssm_block_norm_bwd")
 
 _lib = None
 
@@ -143,10 +145,10 @@ def load_library():
             lib.ssm_abi_struct_size(1) != ctypes.sizeof(UpdateParams) or \
             lib.ssm_abi_struct_size(2) != ctypes.sizeof(BwdParams):
         raise ImportError("libssmscan.so struct layout does not match this binding")
-    from . import binding_delta, binding_glr
+    from . import binding_block, binding_delta, binding_glr
 
-    binding_delta.declare(lib)
-    binding_glr.declare(lib)
+    for module in (binding_delta, binding_glr, binding_block):
+        module.declare(lib)
     _lib = lib
     return lib
 

@@ -880,6 +880,8 @@ size_t ssm_abi_struct_size(int32_t which) {
   if (which == 6) return sizeof(ssm_qk_norm_params);
   if (which == 8) return sizeof(ssm_glr_params);
   if (which == 9) return sizeof(ssm_glr_update_params);
+  if (which == 10) return sizeof(ssm_gated_norm_params);
+  if (which == 11) return sizeof(ssm_block_norm_params);
   return 0;
 }
 
