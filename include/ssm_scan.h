@@ -665,8 +665,8 @@ ssm_status ssm_qk_norm_bwd(const ssm_qk_norm_params* p, void* hip_stream);
  *   batch, seqlen, dim : B >= 0, 0 <= L < 2^27, 0 <= D <= 2^24
  *   in_dtype  : element type of u, dt_raw, in_raw, z (and dout)
  *   u, dt_raw (B,L,D) required; in_raw, z (B,L,D), NULL => none. Channels are dense;
- *            the strides are the elements from one token to the next (at least D;
- *            0 = D), with batch rows L tokens apart, so slices of one packed
+ *            the strides are the elements from one token to the next (at least D, at most
+ *            2^24; 0 = D), with batch rows L tokens apart, so slices of one packed
  *            projection can be passed as they lie.
  *   A        (D) float32, required. Any real value is accepted by SSM_GLR_REST and
  *            SSM_GLR_ONE; a_t above 1 (A > 0) makes SSM_GLR_UNIT's root NaN.

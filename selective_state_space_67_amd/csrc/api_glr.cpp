@@ -57,6 +57,8 @@ ssm_status check_glr_sizes(const P* p, int64_t len, GlrSizes* s) {
   for (int j = 0; j < 4; ++j) {
     if (strides[j] != 0 && strides[j] < p->dim)
       return fail(SSM_ERR_BAD_SHAPE, "a token stride is smaller than the token");
+    if (strides[j] > ssm::kGlrMaxStride)
+      return fail(SSM_ERR_BAD_SHAPE, "a token stride is above 2^24 (got %lld)", (long long)strides[j]);
     *steps[j] = strides[j] ? strides[j] : p->dim;
     if (!span(s->tokens, *steps[j], p->dim, spans[j]) || *spans[j] > kLim)
       return fail(SSM_ERR_BAD_SHAPE, "element count overflows");

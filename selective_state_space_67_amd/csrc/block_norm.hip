@@ -38,13 +38,21 @@ struct BlockArgs {
   float eps, scale, share;
 };
 
-template <typename InT, typename ResT, int V, int TR, int NV>
-__global__ __launch_bounds__(TR < 256 ? 256 : TR) void block_norm_fwd(const BlockArgs a) {
-  __shared__ float lds[2][TeamSum<TR>::kWaves];
+template <typename InT, typename ResT, int V, int TR, int NV, int MOST>
+__global__ __launch_bounds__(MOST) void block_norm_fwd(const BlockArgs a) {
+  __shared__ float lds[2][16];
   TeamSum<TR> sum;
   const Columns<V, TR, NV> c(a.D);
   const int group = RowWalk::group(a.g);
   const RowWalk walk = RowWalk::of<TR>(a.g);
+  Raw<V, InT> raw_y[NV];
+  Raw<V, ResT> rx[NV];
+  auto load = [&](int64_t i) {
+    const int64_t row = group * a.g.rows + i;
+    c.load(a.y, row * a.ys, raw_y);
+    if (a.x) c.load(a.x, row * a.D, rx);
+  };
+  if (walk.row < walk.end) load(walk.row);
   float w[NV][V], wp[NV][V], k[NV][V];
   c.weights(a.w, w);
   if (a.post) c.weights(a.w_post, wp);
@@ -52,8 +60,14 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void block_norm_fwd(const Bloc
   for (int64_t i = walk.row; i < walk.end; i += walk.step) {
     const int64_t row = group * a.g.rows + i;
     float y[NV][V], x[NV][V];
-    c.load(static_cast<const InT*>(a.y) + row * a.ys, y);
-    if (a.x) c.load(static_cast<const ResT*>(a.x) + row * a.D, x);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        y[j][e] = raw_y[j].at(e);
+        x[j][e] = a.x ? rx[j].at(e) : 0.0f;
+      }
+    if (i + walk.step < walk.end) load(i + walk.step);
     if (a.post) {
       const float ry = __builtin_amdgcn_rsqf(__builtin_fmaf(sum(dot(y, y), lds), a.share, a.eps));
 #pragma unroll
@@ -66,7 +80,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void block_norm_fwd(const Bloc
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float f = a.scale * k[j][e];
-        y[j][e] = a.x ? __builtin_fmaf(f, y[j][e], x[j][e]) : f * y[j][e];
+        y[j][e] = __builtin_fmaf(f, y[j][e], x[j][e]);
       }
     if (a.x_out) c.store(a.x_out, row * a.D, a.res_bf16, y);
     const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum(dot(y, y), lds), a.share, a.eps));
@@ -78,14 +92,24 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void block_norm_fwd(const Bloc
   }
 }
 
-template <typename InT, typename ResT, int V, int TR, int NV>
-__global__ __launch_bounds__(TR < 256 ? 256 : TR) void block_norm_bwd(const BlockArgs a) {
+template <typename InT, typename ResT, int V, int TR, int NV, int MOST>
+__global__ __launch_bounds__(MOST) void block_norm_bwd(const BlockArgs a) {
   extern __shared__ float sums[];
-  __shared__ float lds[2][TeamSum<TR>::kWaves];
+  __shared__ float lds[2][16];
   TeamSum<TR> sum;
   const Columns<V, TR, NV> c(a.D);
   const int group = RowWalk::group(a.g);
   const RowWalk walk = RowWalk::of<TR>(a.g);
+  Raw<V, InT> raw_y[NV], rdn[NV];
+  Raw<V, ResT> rx[NV], rdx[NV];
+  auto load = [&](int64_t i) {
+    const int64_t row = group * a.g.rows + i;
+    c.load(a.y, row * a.ys, raw_y);
+    if (a.x) c.load(a.x, row * a.D, rx);
+    c.load(a.dout, row * a.D, rdn);
+    if (a.dx_out) c.load(a.dx_out, row * a.D, rdx);
+  };
+  if (walk.row < walk.end) load(walk.row);
   float w[NV][V], wp[NV][V], k[NV][V], dw[NV][V] = {}, dwp[NV][V] = {}, dg[NV][V] = {};
   c.weights(a.w, w);
   if (a.post) c.weights(a.w_post, wp);
@@ -95,10 +119,16 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void block_norm_bwd(const Bloc
   for (int64_t i = walk.row; i < walk.end; i += walk.step) {
     const int64_t row = group * a.g.rows + i;
     float y[NV][V], x[NV][V], dn[NV][V], dX[NV][V];
-    c.load(static_cast<const InT*>(a.y) + row * a.ys, y);
-    if (a.x) c.load(static_cast<const ResT*>(a.x) + row * a.D, x);
-    c.load(static_cast<const InT*>(a.dout) + row * a.D, dn);
-    if (a.dx_out) c.load(static_cast<const ResT*>(a.dx_out) + row * a.D, dX);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        y[j][e] = raw_y[j].at(e);
+        x[j][e] = a.x ? rx[j].at(e) : 0.0f;
+        dn[j][e] = rdn[j].at(e);
+        dX[j][e] = a.dx_out ? rdx[j].at(e) : 0.0f;
+      }
+    if (i + walk.step < walk.end) load(i + walk.step);
     float ry = 1.0f;
     if (a.post) {
       ry = __builtin_amdgcn_rsqf(__builtin_fmaf(sum(dot(y, y), lds), a.share, a.eps));
@@ -112,7 +142,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void block_norm_bwd(const Bloc
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float f = a.scale * k[j][e], m = a.post ? y[j][e] * wp[j][e] : y[j][e];
-        x[j][e] = a.x ? __builtin_fmaf(f, m, x[j][e]) : f * m;
+        x[j][e] = __builtin_fmaf(f, m, x[j][e]);
       }
     const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum(dot(x, x), lds), a.share, a.eps));
 #pragma unroll
@@ -129,7 +159,7 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void block_norm_bwd(const Bloc
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float back = alone ? r * dn[j][e] * (a.eps * r * r) : r * __builtin_fmaf(-x[j][e], along, dn[j][e]);
-        dX[j][e] = a.dx_out ? back + dX[j][e] : back;
+        dX[j][e] += back;
       }
     if (a.dx) c.store(a.dx, row * a.D, a.res_bf16, dX);
 #pragma unroll
@@ -191,34 +221,29 @@ BlockArgs block_args(const BlockPlan& p) {
   return a;
 }
 
-constexpr int64_t kWantThreads = int64_t{1} << 19;
-
 template <typename InT, typename ResT>
 struct Forward {
-  template <int V, int TR, int NV>
-  static hipError_t run(BlockArgs a, hipStream_t stream) {
-    const int threads = workgroup_threads<TR>(a.g.rows * a.g.groups);
-    const int64_t most = (a.g.rows + threads / TR - 1) / (threads / TR);
-    a.g.parts = static_cast<int>(std::min(most, std::max<int64_t>(1, kWantThreads / threads / a.g.groups)));
+  template <int V, int TR, int NV, int MOST>
+  static hipError_t run(int threads, BlockArgs a, hipStream_t stream) {
+    a.g.parts = row_parts(a.g, threads, TR ? threads / (TR ? TR : 1) : 1);
     const unsigned blocks = static_cast<unsigned>(a.g.groups) * a.g.parts;
-    SSM_LOG("launch block_norm_fwd<%d entries a run, %d lanes a row, %d runs a lane>: grid %u x %d threads", V, TR, NV,
-            blocks, threads);
-    hipLaunchKernelGGL((block_norm_fwd<InT, ResT, V, TR, NV>), dim3(blocks), dim3(threads), 0, stream, a);
+    SSM_LOG("launch block_norm_fwd<%d entries a run, %d lanes a row, %d runs a lane>: grid %u x %d threads", V,
+            TR ? TR : threads, NV, blocks, threads);
+    hipLaunchKernelGGL((block_norm_fwd<InT, ResT, V, TR, NV, MOST>), dim3(blocks), dim3(threads), 0, stream, a);
     return hipGetLastError();
   }
 };
 
 template <typename InT, typename ResT>
 struct Backward {
-  template <int V, int TR, int NV>
-  static hipError_t run(BlockArgs a, int parts, hipStream_t stream) {
-    const int threads = TR < 256 ? 256 : TR;
+  template <int V, int TR, int NV, int MOST>
+  static hipError_t run(int threads, BlockArgs a, int parts, hipStream_t stream) {
     a.g.parts = parts;
     const unsigned blocks = static_cast<unsigned>(a.g.groups) * parts;
-    const size_t lds = TR < 256 ? static_cast<size_t>(threads / TR) * a.D * sizeof(float) : 0;
-    SSM_LOG("launch block_norm_bwd<%d entries a run, %d lanes a row, %d runs a lane>: grid %u x %d threads", V, TR, NV,
-            blocks, threads);
-    hipLaunchKernelGGL((block_norm_bwd<InT, ResT, V, TR, NV>), dim3(blocks), dim3(threads), lds, stream, a);
+    const size_t lds = TR ? static_cast<size_t>(threads / (TR ? TR : 1)) * a.D * sizeof(float) : 0;
+    SSM_LOG("launch block_norm_bwd<%d entries a run, %d lanes a row, %d runs a lane>: grid %u x %d threads", V,
+            TR ? TR : threads, NV, blocks, threads);
+    hipLaunchKernelGGL((block_norm_bwd<InT, ResT, V, TR, NV, MOST>), dim3(blocks), dim3(threads), lds, stream, a);
     return hipGetLastError();
   }
 };
@@ -232,10 +257,10 @@ hipError_t pick_types(const BlockPlan& p, X&&... x) {
                         static_cast<const void*>(p.dx)})
     runs = runs && aligned_to(q, 16);
   if (p.in_bf16)
-    return p.res_bf16 ? pick_team<F<bf16_t, bf16_t>>(runs, p.D, std::forward<X>(x)...)
-                      : pick_team<F<bf16_t, float>>(runs, p.D, std::forward<X>(x)...);
-  return p.res_bf16 ? pick_team<F<float, bf16_t>>(runs, p.D, std::forward<X>(x)...)
-                    : pick_team<F<float, float>>(runs, p.D, std::forward<X>(x)...);
+    return p.res_bf16 ? pick_team<F<bf16_t, bf16_t>>(runs, p.D, p.B * p.L, std::forward<X>(x)...)
+                      : pick_team<F<bf16_t, float>>(runs, p.D, p.B * p.L, std::forward<X>(x)...);
+  return p.res_bf16 ? pick_team<F<float, bf16_t>>(runs, p.D, p.B * p.L, std::forward<X>(x)...)
+                    : pick_team<F<float, float>>(runs, p.D, p.B * p.L, std::forward<X>(x)...);
 }
 
 }  // namespace
@@ -245,22 +270,18 @@ hipError_t launch_block_norm(const BlockPlan& p, hipStream_t stream) {
 }
 
 int64_t block_norm_bwd_blocks(int64_t B, int64_t L, int D, bool gate_rows) {
-  const int64_t groups = gate_rows ? B : 1, rows = gate_rows ? L : B * L;
-  const int64_t want = std::min<int64_t>((rows * D + 16383) / 16384, std::max<int64_t>(1, 1024 / groups));
-  return groups * std::max<int64_t>(1, std::min(want, rows));
+  return row_sum_blocks(gate_rows ? B : 1, gate_rows ? L : B * L, D);
 }
 
 hipError_t launch_block_norm_bwd(const BlockPlan& p, float* workspace, hipStream_t stream) {
   BlockArgs a = block_args(p);
-  const bool sums = p.dw || (p.post && p.dw_post) || (p.gate && p.dgate);
-  a.part = sums ? workspace : nullptr;
-  const int64_t blocks = block_norm_bwd_blocks(p.B, p.L, p.D, p.gate_rows), width = 3 * static_cast<int64_t>(p.D);
-  hipError_t e = pick_types<Backward>(p, a, static_cast<int>(blocks / a.g.groups), stream);
-  if (e == hipSuccess) e = launch_row_sums(workspace, blocks, 1, width, 0, p.D, p.dw, stream);
-  if (e == hipSuccess && p.post) e = launch_row_sums(workspace, blocks, 1, width, p.D, p.D, p.dw_post, stream);
-  if (e == hipSuccess && p.gate)
-    e = launch_row_sums(workspace, blocks / a.g.groups, a.g.groups, width, 2 * p.D, p.D, p.dgate, stream);
-  return e;
+  const int64_t blocks = block_norm_bwd_blocks(p.B, p.L, p.D, p.gate_rows), D = p.D;
+  const RowSum sums[3] = {{p.dw, 0, blocks, 1},
+                          {p.post ? p.dw_post : nullptr, D, blocks, 1},
+                          {p.gate ? p.dgate : nullptr, 2 * D, blocks / a.g.groups, a.g.groups}};
+  a.part = sums[0].to || sums[1].to || sums[2].to ? workspace : nullptr;
+  const hipError_t e = pick_types<Backward>(p, a, static_cast<int>(blocks / a.g.groups), stream);
+  return e != hipSuccess ? e : launch_row_sums(workspace, 3 * D, p.D, sums, stream);
 }
 
 }  // namespace ssm

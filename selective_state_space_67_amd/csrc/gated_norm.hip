@@ -40,65 +40,79 @@ struct GatedRow {
   }
 };
 
-template <typename InT, int V, int TR, int NV>
-__global__ __launch_bounds__(TR < 256 ? 256 : TR) void gated_norm_fwd(const GatedArgs a) {
-  __shared__ float lds[2][TeamSum<TR>::kWaves];
+template <typename InT, int V, int TR, int NV, int MOST>
+__global__ __launch_bounds__(MOST) void gated_norm_fwd(const GatedArgs a) {
+  __shared__ float lds[2][16];
   TeamSum<TR> sum;
   const Columns<V, TR, NV> c(a.d);
   const int group = RowWalk::group(a.g);
   const RowWalk walk = RowWalk::of<TR>(a.g);
+  Raw<V, InT> rx[NV], rz[NV];
+  auto load = [&](int64_t i) {
+    const GatedRow row(a, i, group);
+    c.load(a.x, row.x, rx);
+    c.load(a.z, row.z, rz);
+  };
+  if (walk.row < walk.end) load(walk.row);
   float w[NV][V];
   c.weights(a.w ? a.w + (a.w_per_head ? static_cast<int64_t>(group) * a.d : 0) : nullptr, w);
   for (int64_t i = walk.row; i < walk.end; i += walk.step) {
-    const GatedRow row(a, i, group);
     float x[NV][V], z[NV][V];
-    c.load(static_cast<const InT*>(a.x) + row.x, x);
-    c.load(static_cast<const InT*>(a.z) + row.z, z);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        z[j][e] = silu_f32(z[j][e]);
+        x[j][e] = rx[j].at(e);
+        z[j][e] = silu_f32(rz[j].at(e));
         if (a.gate_first) {
           x[j][e] *= z[j][e];
           z[j][e] = 1.0f;
         }
       }
+    if (i + walk.step < walk.end) load(i + walk.step);
     const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum(dot(x, x), lds), a.share, a.eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < V; ++e) x[j][e] = x[j][e] * r * w[j][e] * z[j][e];
-    c.store(a.out, row.dense, a.out_bf16, x);
+    c.store(a.out, GatedRow(a, i, group).dense, a.out_bf16, x);
   }
 }
 
-template <typename InT, int V, int TR, int NV>
-__global__ __launch_bounds__(TR < 256 ? 256 : TR) void gated_norm_bwd(const GatedArgs a) {
+template <typename InT, int V, int TR, int NV, int MOST>
+__global__ __launch_bounds__(MOST) void gated_norm_bwd(const GatedArgs a) {
   extern __shared__ float sums[];
-  __shared__ float lds[2][TeamSum<TR>::kWaves];
+  __shared__ float lds[2][16];
   TeamSum<TR> sum;
   const Columns<V, TR, NV> c(a.d);
   const int group = RowWalk::group(a.g);
   const RowWalk walk = RowWalk::of<TR>(a.g);
+  Raw<V, InT> rx[NV], rz[NV], rdy[NV];
+  auto load = [&](int64_t i) {
+    const GatedRow row(a, i, group);
+    c.load(a.x, row.x, rx);
+    c.load(a.z, row.z, rz);
+    c.load(a.dout, row.dense, rdy);
+  };
+  if (walk.row < walk.end) load(walk.row);
   float w[NV][V], dw[NV][V] = {};
   c.weights(a.w ? a.w + (a.w_per_head ? static_cast<int64_t>(group) * a.d : 0) : nullptr, w);
   for (int64_t i = walk.row; i < walk.end; i += walk.step) {
-    const GatedRow row(a, i, group);
     float x[NV][V], z[NV][V], dy[NV][V], n[NV][V];
-    c.load(static_cast<const InT*>(a.x) + row.x, x);
-    c.load(static_cast<const InT*>(a.z) + row.z, z);
-    c.load(static_cast<const InT*>(a.dout) + row.dense, dy);
     float slope[NV][V];  // of silu at z, whose value replaces z
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
+        x[j][e] = rx[j].at(e);
+        z[j][e] = rz[j].at(e);
+        dy[j][e] = rdy[j].at(e);
         const float s = fast_rcp(1.0f + fast_exp2(-z[j][e] * kLog2e));
         slope[j][e] = s * __builtin_fmaf(z[j][e], 1.0f - s, 1.0f);
         z[j][e] *= s;
         n[j][e] = a.gate_first ? x[j][e] * z[j][e] : x[j][e];
       }
+    if (i + walk.step < walk.end) load(i + walk.step);
     const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum(dot(n, n), lds), a.share, a.eps));
     // dy becomes the gradient of the normed row, and with the norm first the gate's is taken on the way
 #pragma unroll
@@ -132,8 +146,9 @@ __global__ __launch_bounds__(TR < 256 ? 256 : TR) void gated_norm_bwd(const Gate
           dy[j][e] = dv;
         }
       }
-    c.store(a.dx, row.dense, a.out_bf16, dy);
-    c.store(a.dz, row.dense, a.out_bf16, slope);
+    const int64_t at = GatedRow(a, i, group).dense;
+    c.store(a.dx, at, a.out_bf16, dy);
+    c.store(a.dz, at, a.out_bf16, slope);
   }
   if (a.part) store_sums(c, dw, sums, a.part + static_cast<int64_t>(blockIdx.x) * a.d);
 }
@@ -161,35 +176,29 @@ GatedArgs gated_args(const GatedPlan& p) {
   return a;
 }
 
-// Workgroups of the forward: enough for 2048 threads a CU.
-constexpr int64_t kWantThreads = int64_t{1} << 19;
-
 template <typename InT>
 struct Forward {
-  template <int V, int TR, int NV>
-  static hipError_t run(GatedArgs a, hipStream_t stream) {
-    const int threads = workgroup_threads<TR>(a.g.rows * a.g.groups);
-    const int64_t most = (a.g.rows + threads / TR - 1) / (threads / TR);
-    a.g.parts = static_cast<int>(std::min(most, std::max<int64_t>(1, kWantThreads / threads / a.g.groups)));
+  template <int V, int TR, int NV, int MOST>
+  static hipError_t run(int threads, GatedArgs a, hipStream_t stream) {
+    a.g.parts = row_parts(a.g, threads, TR ? threads / (TR ? TR : 1) : 1);
     const unsigned blocks = static_cast<unsigned>(a.g.groups) * a.g.parts;
-    SSM_LOG("launch gated_norm_fwd<%d entries a run, %d lanes a row, %d runs a lane>: grid %u x %d threads", V, TR, NV,
-            blocks, threads);
-    hipLaunchKernelGGL((gated_norm_fwd<InT, V, TR, NV>), dim3(blocks), dim3(threads), 0, stream, a);
+    SSM_LOG("launch gated_norm_fwd<%d entries a run, %d lanes a row, %d runs a lane>: grid %u x %d threads", V,
+            TR ? TR : threads, NV, blocks, threads);
+    hipLaunchKernelGGL((gated_norm_fwd<InT, V, TR, NV, MOST>), dim3(blocks), dim3(threads), 0, stream, a);
     return hipGetLastError();
   }
 };
 
 template <typename InT>
 struct Backward {
-  template <int V, int TR, int NV>
-  static hipError_t run(GatedArgs a, int parts, hipStream_t stream) {
-    const int threads = TR < 256 ? 256 : TR;
+  template <int V, int TR, int NV, int MOST>
+  static hipError_t run(int threads, GatedArgs a, int parts, hipStream_t stream) {
     a.g.parts = parts;
     const unsigned blocks = static_cast<unsigned>(a.g.groups) * parts;
-    const size_t lds = TR < 256 ? static_cast<size_t>(threads / TR) * a.d * sizeof(float) : 0;
-    SSM_LOG("launch gated_norm_bwd<%d entries a run, %d lanes a row, %d runs a lane>: grid %u x %d threads", V, TR, NV,
-            blocks, threads);
-    hipLaunchKernelGGL((gated_norm_bwd<InT, V, TR, NV>), dim3(blocks), dim3(threads), lds, stream, a);
+    const size_t lds = TR ? static_cast<size_t>(threads / (TR ? TR : 1)) * a.d * sizeof(float) : 0;
+    SSM_LOG("launch gated_norm_bwd<%d entries a run, %d lanes a row, %d runs a lane>: grid %u x %d threads", V,
+            TR ? TR : threads, NV, blocks, threads);
+    hipLaunchKernelGGL((gated_norm_bwd<InT, V, TR, NV, MOST>), dim3(blocks), dim3(threads), lds, stream, a);
     return hipGetLastError();
   }
 };
@@ -204,24 +213,24 @@ bool in_runs(const GatedPlan& p) {
 
 hipError_t launch_gated_norm(const GatedPlan& p, hipStream_t stream) {
   const GatedArgs a = gated_args(p);
-  if (p.in_bf16) return pick_team<Forward<bf16_t>>(in_runs(p), p.d, a, stream);
-  return pick_team<Forward<float>>(in_runs(p), p.d, a, stream);
+  const int64_t rows = p.tokens * p.H;
+  if (p.in_bf16) return pick_team<Forward<bf16_t>>(in_runs(p), p.d, rows, a, stream);
+  return pick_team<Forward<float>>(in_runs(p), p.d, rows, a, stream);
 }
 
 int64_t gated_norm_bwd_blocks(int64_t tokens, int H, int d, bool w_per_head) {
-  const int64_t groups = w_per_head ? H : 1, rows = w_per_head ? tokens : tokens * H;
-  const int64_t want = std::min<int64_t>((rows * d + 16383) / 16384, std::max<int64_t>(1, 1024 / groups));
-  return groups * std::max<int64_t>(1, std::min(want, rows));
+  return row_sum_blocks(w_per_head ? H : 1, w_per_head ? tokens : tokens * H, d);
 }
 
 hipError_t launch_gated_norm_bwd(const GatedPlan& p, float* workspace, hipStream_t stream) {
   GatedArgs a = gated_args(p);
   a.part = p.dw ? workspace : nullptr;
   const int parts = static_cast<int>(gated_norm_bwd_blocks(p.tokens, p.H, p.d, p.w_per_head) / a.g.groups);
-  const hipError_t e = p.in_bf16 ? pick_team<Backward<bf16_t>>(in_runs(p), p.d, a, parts, stream)
-                                 : pick_team<Backward<float>>(in_runs(p), p.d, a, parts, stream);
+  const int64_t rows = p.tokens * p.H;
+  const hipError_t e = p.in_bf16 ? pick_team<Backward<bf16_t>>(in_runs(p), p.d, rows, a, parts, stream)
+                                 : pick_team<Backward<float>>(in_runs(p), p.d, rows, a, parts, stream);
   if (e != hipSuccess) return e;
-  return launch_row_sums(workspace, parts, a.g.groups, p.d, 0, p.d, p.dw, stream);
+  return launch_row_sums(workspace, p.d, p.d, {{p.dw, 0, parts, a.g.groups}, {}, {}}, stream);
 }
 
 }  // namespace ssm

@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kWaves = 8, kRows = 8, kPiece = kWaves * kRows;
 
-template <typename InT, int DECAY, int MIX, int W, int K>
+template <typename InT, int DECAY, int MIX, bool IN, bool Z, int W, int K>
 __global__ __launch_bounds__(kLanes * W) void glr_grads(const GlrArgs g) {
   __shared__ float ex[3][W][kLanes];  // P, H, G; then the three sums
   const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
@@ -40,103 +40,118 @@ __global__ __launch_bounds__(kLanes * W) void glr_grads(const GlrArgs g) {
   const int have = max(rows, 1);
   uint32_t ru[K], rdt[K], rin[K], rz[K], rdy[K];
   load_rows<InT, K>(g.dt, row, g.ds, have, at, rdt);
+  if (IN) load_rows<InT, K>(g.in, row, g.is, have, at, rin);
   load_rows<InT, K>(g.u, row, g.us, have, at, ru);
-  if (g.in) load_rows<InT, K>(g.in, row, g.is, have, at, rin);
   load_rows<InT, K>(g.dout, row, g.D, have, at, rdy);
-  if (g.z) load_rows<InT, K>(g.z, row, g.zs, have, at, rz);
+  if (Z) load_rows<InT, K>(g.z, row, g.zs, have, at, rz);
   const uint32_t reset = reset_byte<K>(g.reset, row, rows, lane);
   const int64_t joint = (static_cast<int64_t>(batch) * g.pieces + piece) * g.D + ch;
   float h = g.starts[joint], m = g.ends[joint];
-  const float A = g.A[ch], dt_bias = g.dt_bias ? g.dt_bias[ch] : 0.0f, in_bias = g.in_bias ? g.in_bias[ch] : 0.0f;
+  const Channel<DECAY> chn(g, ch);
   const uint32_t cuts = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(reset != 0));
 
-  float a[K], c[K], x[K], i[K], s[K], dy[K];  // x = i u
+  float a[K], c[K], x[K], i[K], s[K], dy[K], b[K];  // x = i u, b = c x
+  decays<InT, DECAY, MIX, K>(chn, rdt, s, a, c);
+  if (cuts) {
+    keep_branch();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if ((cuts >> k) & 1) c[k] = 1.0f;
+  }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const float raw = widen<InT>(rdt[k]) + dt_bias;
-    s[k] = decay_gate<DECAY>(raw);
-    decay_terms<MIX>(A * s[k], a[k], c[k]);
-    if ((cuts >> k) & 1) c[k] = 1.0f;
     x[k] = widen<InT>(ru[k]);
-    dy[k] = widen<InT>(rdy[k]);
     i[k] = 1.0f;
-  }
-  if (g.in) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      i[k] = sigmoid_f32(widen<InT>(rin[k]) + in_bias);
+    if (IN) {
+      i[k] = biased_sigmoid(widen<InT>(rin[k]), chn.in);
       x[k] *= i[k];
     }
-  }
-  if (g.z) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) dy[k] *= silu_f32(widen<InT>(rz[k]));
+    b[k] = MIX == kGlrOne ? x[k] : c[k] * x[k];
+    dy[k] = Z ? widen<InT>(rdy[k]) * silu_f32(widen<InT>(rz[k])) : widen<InT>(rdy[k]);
   }
   // what the wave's rows do to a state and to an adjoint
   float P = 1.0f, H = 0.0f, G = 0.0f;
-  bool cut = false;
+  if (rows == K && cuts == 0) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (k < rows) {
-      const bool here = (cuts >> k) & 1;
-      cut |= here;
+    for (int k = 0; k < K; ++k) {
       P *= a[k];
-      H = here ? x[k] : __builtin_fmaf(a[k], H, c[k] * x[k]);
-      if (!cut) G = __builtin_fmaf(P, dy[k], G);
+      H = __builtin_fmaf(a[k], H, b[k]);
+      G = __builtin_fmaf(P, dy[k], G);
     }
+  } else {
+    keep_branch();
+    bool cut = false;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k < rows) {
+        const bool here = (cuts >> k) & 1;
+        cut |= here;
+        P *= a[k];
+        H = here ? b[k] : __builtin_fmaf(a[k], H, b[k]);
+        if (!cut) G = __builtin_fmaf(P, dy[k], G);
+      }
+    }
+    if (cut) P = kCut;
   }
-  if (cut) P = kCut;
   ex[0][w][lane] = P;
   ex[1][w][lane] = H;
   ex[2][w][lane] = G;
   __syncthreads();
   for (int j = 0; j < w; ++j) h = through(ex[0][j][lane], ex[1][j][lane], h);
   for (int j = W - 1; j > w; --j) m = through(ex[0][j][lane], ex[2][j][lane], m);
-
-  float before[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    before[k] = h;
-    const float b = c[k] * x[k];
-    h = (cuts >> k) & 1 ? b : __builtin_fmaf(a[k], h, b);
-  }
-  const int size = g.out_bf16 ? 2 : 4;
-  const int64_t first = ((row0 + t) * g.D) * size;
   float sum_A = 0.0f, sum_dt = 0.0f, sum_in = 0.0f;
+  if (rows > 0) {
+    float before[K];
 #pragma unroll
-  for (int k = K - 1; k >= 0; --k) {
-    if (k < rows) {
-      const bool here = (cuts >> k) & 1;
-      const int64_t to = first + static_cast<int64_t>(k) * g.D * size;
-      const float lam = dy[k] + m;
-      if (g.z) {
-        const float z = widen<InT>(rz[k]), sz = sigmoid_f32(z), now = here ? c[k] * x[k] : __builtin_fmaf(a[k], before[k], c[k] * x[k]);
-        const float dz = widen<InT>(rdy[k]) * now * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
-        if (on) store_result(static_cast<char*>(g.dz) + to, ch, dz, g.out_bf16);
+    for (int k = 0; k < K; ++k) {
+      before[k] = h;
+      h = __builtin_fmaf(a[k], h, b[k]);
+      if (cuts) {
+        keep_branch();
+        if ((cuts >> k) & 1) h = b[k];
       }
-      const float lc = lam * c[k];
-      if (on) store_result(static_cast<char*>(g.du) + to, ch, lc * i[k], g.out_bf16);
-      if (g.in) {
-        const float d = lc * x[k] * (1.0f - i[k]);
-        sum_in += d;
-        if (on) store_result(static_cast<char*>(g.d_in) + to, ch, d, g.out_bf16);
+      if (Z) {  // b becomes dz
+        const float z = widen<InT>(rz[k]), sz = sigmoid_f32(z);
+        b[k] = widen<InT>(rdy[k]) * h * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
       }
-      float d_dt = 0.0f;
+    }
+    if (Z && on) store_rows<K>(g.dz, row, g.D, rows, ch, g.out_bf16, b);
+    float d_in[K];
+    auto back = [&](int k, bool here) {
+      const float lam = dy[k] + m, lc = MIX == kGlrOne ? lam : lam * c[k];
+      b[k] = IN ? lc * i[k] : lc;  // du
+      if (IN) {
+        d_in[k] = lc * x[k] * (1.0f - i[k]);
+        sum_in += d_in[k];
+      }
       if (here) {
-        m = 0.0f;
-      } else {
-        m = a[k] * lam;
-        // where a rounds to 1, c is 0 and its slope infinite, but what the gate and A get tends to 0
-        float dc = 0.0f;
-        if (MIX == kGlrUnit) dc = c[k] == 0.0f ? 0.0f : -a[k] * fast_rcp(c[k]);
-        if (MIX == kGlrRest) dc = -1.0f;
-        const float dg = m * __builtin_fmaf(x[k], dc, before[k]);
-        sum_A = __builtin_fmaf(dg, s[k], sum_A);
-        const float slope = DECAY == kGlrSigmoid ? s[k] * (1.0f - s[k]) : sigmoid_f32(widen<InT>(rdt[k]) + dt_bias);
-        d_dt = dg * A * slope;
-        sum_dt += d_dt;
+        m = dy[k] = 0.0f;
+        return;
       }
-      if (on) store_result(static_cast<char*>(g.d_dt) + to, ch, d_dt, g.out_bf16);
+      m = a[k] * lam;
+      // where a rounds to 1, c is 0 and its slope infinite, but what the gate and A get tends to 0
+      float dc = 0.0f;
+      if (MIX == kGlrUnit) dc = c[k] == 0.0f ? 0.0f : -a[k] * fast_rcp(c[k]);
+      if (MIX == kGlrRest) dc = -1.0f;
+      const float dg = m * (MIX == kGlrOne ? before[k] : __builtin_fmaf(x[k], dc, before[k]));
+      sum_A = __builtin_fmaf(dg, s[k], sum_A);
+      const float slope = DECAY == kGlrSigmoid ? s[k] * (1.0f - s[k]) : sigmoid_f32(widen<InT>(rdt[k]) + chn.dt);
+      dy[k] = dg * chn.A * slope;  // d dt_raw
+      sum_dt += dy[k];
+    };
+    if (rows == K && cuts == 0) {
+#pragma unroll
+      for (int k = K - 1; k >= 0; --k) back(k, false);
+    } else {
+      keep_branch();
+#pragma unroll
+      for (int k = K - 1; k >= 0; --k)
+        if (k < rows) back(k, (cuts >> k) & 1);
+    }
+    if (on) {
+      store_rows<K>(g.du, row, g.D, rows, ch, g.out_bf16, b);
+      if (IN) store_rows<K>(g.d_in, row, g.D, rows, ch, g.out_bf16, d_in);
+      store_rows<K>(g.d_dt, row, g.D, rows, ch, g.out_bf16, dy);
     }
   }
   __syncthreads();
@@ -180,9 +195,10 @@ __global__ __launch_bounds__(256) void glr_sums(const float* __restrict__ part, 
 }
 
 struct Grads {
-  template <typename InT, int DECAY, int MIX>
+  template <typename InT, int DECAY, int MIX, bool IN, bool Z>
   static hipError_t run(unsigned blocks, const GlrArgs& g, hipStream_t stream) {
-    hipLaunchKernelGGL((glr_grads<InT, DECAY, MIX, kWaves, kRows>), dim3(blocks), dim3(kWaves * kLanes), 0, stream, g);
+    hipLaunchKernelGGL((glr_grads<InT, DECAY, MIX, IN, Z, kWaves, kRows>), dim3(blocks), dim3(kWaves * kLanes), 0,
+                       stream, g);
     return hipGetLastError();
   }
 };

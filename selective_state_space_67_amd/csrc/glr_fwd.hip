@@ -15,61 +15,41 @@
 namespace ssm {
 namespace {
 
-constexpr int kWaves = 16, kRows = 8, kTile = kWaves * kRows;
+constexpr int kWaves = 8, kRows = 8, kTile = kWaves * kRows;
 
-template <typename InT, int K>
+// Rows of the four inputs, K a wave.
+template <typename InT, bool IN, bool Z, int K>
 struct Rows {
   uint32_t u[K], dt[K], in[K], z[K], reset;
-  __device__ __forceinline__ void load(const GlrArgs& g, int64_t row0, int64_t t, int64_t end, int lane, uint32_t at) {
+  __device__ __forceinline__ void load(const GlrArgs& g, int64_t row0, int t, int end, int lane, uint32_t at) {
     // a wave whose rows are all past the end reads the last row
-    const int64_t row = row0 + (t < end ? t : end - 1);
-    const int rows = t < end ? static_cast<int>(end - t < K ? end - t : K) : 1;
-    load_rows<InT, K>(g.u, row, g.us, rows, at, u);
+    const int64_t row = row0 + min(t, end - 1);
+    const int rows = max(1, min(end - t, K));
     load_rows<InT, K>(g.dt, row, g.ds, rows, at, dt);
-    if (g.in) load_rows<InT, K>(g.in, row, g.is, rows, at, in);
-    if (g.z) load_rows<InT, K>(g.z, row, g.zs, rows, at, z);
+    if (IN) load_rows<InT, K>(g.in, row, g.is, rows, at, in);
+    load_rows<InT, K>(g.u, row, g.us, rows, at, u);
+    if (Z) load_rows<InT, K>(g.z, row, g.zs, rows, at, z);
     reset = reset_byte<K>(g.reset, row, t < end ? rows : 0, lane);
   }
+  // which of the rows start a document
+  __device__ __forceinline__ uint32_t cuts() const {
+    return static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(reset != 0));
+  }
 };
 
-// A channel's constants.
-struct Channel {
-  float A, dt_bias, in_bias;
-  __device__ __forceinline__ Channel(const GlrArgs& g, int ch)
-      : A(g.A[ch]), dt_bias(g.dt_bias ? g.dt_bias[ch] : 0.0f), in_bias(g.in_bias ? g.in_bias[ch] : 0.0f) {}
-};
-
-// Decays a and inputs b of K rows; cuts: the rows that start a document.
-template <typename InT, int DECAY, int MIX, int K>
-__device__ __forceinline__ void terms(const GlrArgs& g, const Channel& c, const Rows<InT, K>& x, uint32_t cuts,
-                                      float (&a)[K], float (&b)[K]) {
-#pragma unroll
-  for (int k = 0; k < K; ++k) b[k] = widen<InT>(x.u[k]);
-  if (g.in) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) b[k] *= sigmoid_f32(widen<InT>(x.in[k]) + c.in_bias);
-  }
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    float m;
-    decay_terms<MIX>(c.A * decay_gate<DECAY>(widen<InT>(x.dt[k]) + c.dt_bias), a[k], m);
-    if (MIX != kGlrOne) b[k] *= (cuts >> k) & 1 ? 1.0f : m;
-  }
-}
-
-template <int K, bool CUTS>
+template <int K>
 __device__ __forceinline__ void run_rows(const float (&a)[K], const float (&b)[K], uint32_t cuts, float& P, float& H) {
-  P = 1.0f;
-  H = 0.0f;
+  P = a[0];
+  H = b[0];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
+  for (int k = 1; k < K; ++k) {
     P *= a[k];
-    H = CUTS && ((cuts >> k) & 1) ? b[k] : __builtin_fmaf(a[k], H, b[k]);
+    H = (cuts >> k) & 1 ? b[k] : __builtin_fmaf(a[k], H, b[k]);
   }
-  if (CUTS) P = kCut;
+  if (cuts) P = kCut;
 }
 
-template <typename InT, int DECAY, int MIX, int W, int K>
+template <typename InT, int DECAY, int MIX, bool IN, bool Z, int W, int K>
 __global__ __launch_bounds__(kLanes * W) void glr_walk(const GlrArgs g) {
   __shared__ float2 pairs[2][W][kLanes];
   const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
@@ -78,28 +58,34 @@ __global__ __launch_bounds__(kLanes * W) void glr_walk(const GlrArgs g) {
   const int channel = tile * kLanes + lane, ch = min(channel, g.D - 1);
   const bool on = channel < g.D;
   const uint32_t at = static_cast<uint32_t>(ch) * sizeof(InT);
-  const Channel c(g, ch);
   const int64_t state = static_cast<int64_t>(batch) * g.D + ch, row0 = batch * g.L;
+  // rows are counted in 32 bits (L < 2^27)
+  const int begin = static_cast<int>(piece * g.piece_rows);
+  const int end = static_cast<int>(min(g.L, begin + g.piece_rows));
+  Channel<DECAY> c(g, ch);
   float h = g.pieces > 1 ? g.starts[(static_cast<int64_t>(batch) * g.pieces + piece) * g.D + ch]
             : g.h0       ? g.h0[state]
                          : 0.0f;
-  const int64_t begin = piece * g.piece_rows, end = min(g.L, begin + g.piece_rows);
-  const int out_size = g.out_bf16 ? 2 : 4;
-  Rows<InT, K> x;
+  Rows<InT, IN, Z, K> x;
   x.load(g, row0, begin + w * K, end, lane, at);
+  arrived(h);
+  arrived(c.A);
+  arrived(c.dt);
+  arrived(c.in);
   int buf = 0;
-  for (int64_t t0 = begin; t0 < end; t0 += W * K, buf ^= 1) {
-    const int64_t t = t0 + w * K;
-    const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{K}, end - t)));
-    const uint32_t cuts = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(x.reset != 0));
+  for (int t0 = begin; t0 < end; t0 += W * K, buf ^= 1) {
+    const int t = t0 + w * K;
+    const int rows = max(0, min(K, end - t));
+    const uint32_t cuts = x.cuts();
     float a[K], b[K], gate[K];
-    terms<InT, DECAY, MIX, K>(g, c, x, cuts, a, b);
-    if (g.z) {
+    terms<InT, DECAY, MIX, IN, K>(c, x.u, x.dt, x.in, cuts, a, b);
+    if (Z) {
 #pragma unroll
       for (int k = 0; k < K; ++k) gate[k] = silu_f32(widen<InT>(x.z[k]));
     }
     if (t0 + W * K < end) x.load(g, row0, t + W * K, end, lane, at);
     if (rows < K) {  // rows past the end do nothing
+      keep_branch();
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         a[k] = k < rows ? a[k] : 1.0f;
@@ -108,9 +94,9 @@ __global__ __launch_bounds__(kLanes * W) void glr_walk(const GlrArgs g) {
     }
     float P, H;
     if (cuts)
-      run_rows<K, true>(a, b, cuts, P, H);
+      run_rows<K>(a, b, cuts, P, H);
     else
-      run_rows<K, false>(a, b, cuts, P, H);
+      run_rows<K>(a, b, 0, P, H);
     pairs[buf][w][lane] = make_float2(P, H);
     __syncthreads();
     float mine = h;
@@ -142,24 +128,17 @@ __global__ __launch_bounds__(kLanes * W) void glr_walk(const GlrArgs g) {
         b[k] = mine;
       }
     }
-    if (g.z) {
+    if (Z) {
 #pragma unroll
       for (int k = 0; k < K; ++k) b[k] *= gate[k];
     }
-    if (on) {
-      char* out = static_cast<char*>(g.out) + (row0 + t) * g.D * out_size;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (k < rows) store_result(out, ch, b[k], g.out_bf16);
-        out += static_cast<int64_t>(g.D) * out_size;
-      }
-    }
+    if (on && rows > 0) store_rows<K>(g.out, row0 + t, g.D, rows, ch, g.out_bf16, b);
   }
   if (g.h_last && piece == g.pieces - 1 && w == 0 && on) g.h_last[state] = h;
 }
 
 // One thread a channel, token by token; the next tokens are loaded ahead, K at a time.
-template <typename InT, int DECAY, int MIX, int K>
+template <typename InT, int DECAY, int MIX, bool IN, bool Z, int K>
 __global__ __launch_bounds__(kLanes) void glr_steps(const GlrArgs g) {
   const int lane = threadIdx.x;
   const int tile = blockIdx.x % g.tiles, batch = blockIdx.x / g.tiles;
@@ -167,49 +146,63 @@ __global__ __launch_bounds__(kLanes) void glr_steps(const GlrArgs g) {
   const bool on = channel < g.D;
   const uint32_t at = static_cast<uint32_t>(ch) * sizeof(InT);
   const int64_t state = static_cast<int64_t>(batch) * g.D + ch, row0 = batch * g.L;
-  Rows<InT, K> x;
-  x.load(g, row0, 0, g.L, lane, at);
-  const Channel c(g, ch);
+  Rows<InT, IN, Z, K> x;
+  const int L = static_cast<int>(g.L);
+  x.load(g, row0, 0, L, lane, at);
+  const Channel<DECAY> c(g, ch);
   float h = g.h0 ? g.h0[state] : 0.0f;
-  const int out_size = g.out_bf16 ? 2 : 4;
-  for (int64_t t = 0; t < g.L; t += K) {
-    const uint32_t cuts = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(x.reset != 0));
-    const int rows = static_cast<int>(min(int64_t{K}, g.L - t));
+  for (int t = 0; t < L; t += K) {
+    const uint32_t cuts = x.cuts();
+    const int rows = min(K, L - t);
     float a[K], b[K], gate[K];
-    terms<InT, DECAY, MIX, K>(g, c, x, cuts, a, b);
-    if (g.z) {
+    terms<InT, DECAY, MIX, IN, K>(c, x.u, x.dt, x.in, cuts, a, b);
+    if (Z) {
 #pragma unroll
       for (int k = 0; k < K; ++k) gate[k] = silu_f32(widen<InT>(x.z[k]));
     }
-    if (t + K < g.L) x.load(g, row0, t + K, g.L, lane, at);
-    char* out = static_cast<char*>(g.out) + (row0 + t) * g.D * out_size;
+    if (t + K < L) x.load(g, row0, t + K, L, lane, at);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; k < K; ++k)
       if (k < rows) {
         h = (cuts >> k) & 1 ? b[k] : __builtin_fmaf(a[k], h, b[k]);
-        if (on) store_result(out, ch, g.z ? h * gate[k] : h, g.out_bf16);
-        out += static_cast<int64_t>(g.D) * out_size;
+        b[k] = Z ? h * gate[k] : h;
       }
-    }
+    if (on) store_rows<K>(g.out, row0 + t, g.D, rows, ch, g.out_bf16, b);
   }
   if (g.h_last && on) g.h_last[state] = h;
 }
 
+// Few workgroups, none of which shares its CU with another, take 16 rows a wave: with half the
+// barriers and folds an element their waves wait less (8 x 2048 x 1536 channels, 192 workgroups:
+// 65 us, with 8 rows 71; with 16 waves of 16 rows 63). Many take 8: 1 x 131072 x 256 in 512
+// pieces 58 us, with 16 rows 63, with 16 waves 81. So does what 8 rows a wave cover in a few tiles:
+// 1 x 37 x 1536 4.8 us, with 16 rows 6.7.
+bool wide_tiles(int64_t blocks, int64_t rows) { return blocks <= 384 && rows >= 8 * kTile; }
+
 struct Walk {
-  template <typename InT, int DECAY, int MIX>
-  static hipError_t run(unsigned blocks, const GlrArgs& g, hipStream_t stream) {
-    hipLaunchKernelGGL((glr_walk<InT, DECAY, MIX, kWaves, kRows>), dim3(blocks), dim3(kWaves * kLanes), 0, stream, g);
+  template <typename InT, int DECAY, int MIX, bool IN, bool Z>
+  static hipError_t run(const GlrPlan& plan, const GlrArgs& g, hipStream_t stream) {
+    const int64_t blocks = plan.B * g.pieces * g.tiles;
+    const bool wide = wide_tiles(blocks, g.piece_rows);
+    SSM_LOG("launch glr_walk<%d waves of %d rows>: %d pieces of %lld rows; grid %lld x %d threads", kWaves,
+            wide ? 2 * kRows : kRows, g.pieces, static_cast<long long>(g.piece_rows), static_cast<long long>(blocks),
+            kWaves * kLanes);
+    const dim3 grid(static_cast<unsigned>(blocks)), block(kWaves * kLanes);
+    if (wide)
+      hipLaunchKernelGGL((glr_walk<InT, DECAY, MIX, IN, Z, kWaves, 2 * kRows>), grid, block, 0, stream, g);
+    else
+      hipLaunchKernelGGL((glr_walk<InT, DECAY, MIX, IN, Z, kWaves, kRows>), grid, block, 0, stream, g);
     return hipGetLastError();
   }
 };
 
 struct Steps {
-  template <typename InT, int DECAY, int MIX>
+  template <typename InT, int DECAY, int MIX, bool IN, bool Z>
   static hipError_t run(unsigned blocks, const GlrArgs& g, hipStream_t stream) {
     if (g.L == 1)
-      hipLaunchKernelGGL((glr_steps<InT, DECAY, MIX, 1>), dim3(blocks), dim3(kLanes), 0, stream, g);
+      hipLaunchKernelGGL((glr_steps<InT, DECAY, MIX, IN, Z, 1>), dim3(blocks), dim3(kLanes), 0, stream, g);
     else
-      hipLaunchKernelGGL((glr_steps<InT, DECAY, MIX, 4>), dim3(blocks), dim3(kLanes), 0, stream, g);
+      hipLaunchKernelGGL((glr_steps<InT, DECAY, MIX, IN, Z, 4>), dim3(blocks), dim3(kLanes), 0, stream, g);
     return hipGetLastError();
   }
 };
@@ -254,10 +247,7 @@ hipError_t launch_glr(const GlrPlan& plan, const GlrPieces& pieces, void* worksp
     if (e == hipSuccess) e = launch_glr_fold(plan, g, pieces.pieces - 1, false, stream);
     if (e != hipSuccess) return e;
   }
-  const unsigned blocks = static_cast<unsigned>(plan.B * pieces.pieces * g.tiles);
-  SSM_LOG("launch glr_walk<%d waves of %d rows>: %lld pieces of %lld rows; grid %u x %d threads", kWaves, kRows,
-          static_cast<long long>(pieces.pieces), static_cast<long long>(pieces.rows), blocks, kWaves * kLanes);
-  return glr_pick<Walk>(plan, blocks, g, stream);
+  return glr_pick<Walk>(plan, plan, g, stream);
 }
 
 hipError_t launch_glr_steps(const GlrPlan& plan, hipStream_t stream) {

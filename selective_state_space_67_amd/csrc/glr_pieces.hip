@@ -16,7 +16,7 @@ namespace {
 constexpr int kAggWaves = 4, kAggRows = 8;
 constexpr int kFoldWaves = 16, kFoldRows = 8;
 
-template <typename InT, int DECAY, int MIX, bool BWD, int K>
+template <typename InT, int DECAY, int MIX, bool IN, bool Z, bool BWD, int K>
 __global__ __launch_bounds__(kAggWaves * kLanes) void glr_aggregate(const GlrArgs g, const int64_t count,
                                                                     const int64_t waves) {
   const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
@@ -27,54 +27,49 @@ __global__ __launch_bounds__(kAggWaves * kLanes) void glr_aggregate(const GlrArg
   const int channel = tile * kLanes + lane, ch = min(channel, g.D - 1);
   const uint32_t at = static_cast<uint32_t>(ch) * sizeof(InT);
   const int64_t row0 = batch * g.L, begin = piece * g.piece_rows, end = min(g.L, begin + g.piece_rows);
-  const float A = g.A[ch], dt_bias = g.dt_bias ? g.dt_bias[ch] : 0.0f, in_bias = g.in_bias ? g.in_bias[ch] : 0.0f;
   uint32_t u[K], dt[K], in[K], z[K], dy[K], reset;
   auto load = [&](int64_t t) {
     const int rows = static_cast<int>(min(int64_t{K}, end - t));
-    load_rows<InT, K>(g.u, row0 + t, g.us, rows, at, u);
     load_rows<InT, K>(g.dt, row0 + t, g.ds, rows, at, dt);
-    if (g.in) load_rows<InT, K>(g.in, row0 + t, g.is, rows, at, in);
-    if (BWD && g.z) load_rows<InT, K>(g.z, row0 + t, g.zs, rows, at, z);
+    if (IN) load_rows<InT, K>(g.in, row0 + t, g.is, rows, at, in);
+    load_rows<InT, K>(g.u, row0 + t, g.us, rows, at, u);
+    if (BWD && Z) load_rows<InT, K>(g.z, row0 + t, g.zs, rows, at, z);
     if (BWD) load_rows<InT, K>(g.dout, row0 + t, g.D, rows, at, dy);
     reset = reset_byte<K>(g.reset, row0 + t, rows, lane);
   };
+  load(begin);
+  const Channel<DECAY> c(g, ch);
   float P = 1.0f, H = 0.0f, G = 0.0f;
   bool cut = false;
-  load(begin);
   for (int64_t t = begin; t < end; t += K) {
     const int rows = static_cast<int>(min(int64_t{K}, end - t));
     const uint32_t cuts = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(reset != 0));
     float a[K], b[K], y[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) b[k] = widen<InT>(u[k]);
-    if (g.in) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) b[k] *= sigmoid_f32(widen<InT>(in[k]) + in_bias);
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float m;
-      decay_terms<MIX>(A * decay_gate<DECAY>(widen<InT>(dt[k]) + dt_bias), a[k], m);
-      if (MIX != kGlrOne) b[k] *= (cuts >> k) & 1 ? 1.0f : m;
-    }
+    terms<InT, DECAY, MIX, IN, K>(c, u, dt, in, cuts, a, b);
     if (BWD) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) y[k] = widen<InT>(dy[k]);
-      if (g.z) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) y[k] *= silu_f32(widen<InT>(z[k]));
-      }
+      for (int k = 0; k < K; ++k) y[k] = Z ? widen<InT>(dy[k]) * silu_f32(widen<InT>(z[k])) : widen<InT>(dy[k]);
     }
     if (t + K < end) load(t + K);
+    if (rows == K && cuts == 0) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (k < rows) {
-        const bool here = (cuts >> k) & 1;
-        cut |= here;
+      for (int k = 0; k < K; ++k) {
         P *= a[k];
-        H = here ? b[k] : __builtin_fmaf(a[k], H, b[k]);
-        // what lies behind a document's start is out of the adjoint's sight
+        H = __builtin_fmaf(a[k], H, b[k]);
         if (BWD && !cut) G = __builtin_fmaf(P, y[k], G);
+      }
+    } else {
+      keep_branch();
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (k < rows) {
+          const bool here = (cuts >> k) & 1;
+          cut |= here;
+          P *= a[k];
+          H = here ? b[k] : __builtin_fmaf(a[k], H, b[k]);
+          // what lies behind a document's start is out of the adjoint's sight
+          if (BWD && !cut) G = __builtin_fmaf(P, y[k], G);
+        }
       }
     }
   }
@@ -152,15 +147,15 @@ __global__ __launch_bounds__(kFoldWaves * kLanes) void glr_fold(const GlrArgs g,
 }
 
 struct Aggregate {
-  template <typename InT, int DECAY, int MIX>
+  template <typename InT, int DECAY, int MIX, bool IN, bool Z>
   static hipError_t run(unsigned blocks, const GlrArgs& g, int64_t count, int64_t waves, bool backward,
                         hipStream_t stream) {
     if (backward)
-      hipLaunchKernelGGL((glr_aggregate<InT, DECAY, MIX, true, kAggRows>), dim3(blocks), dim3(kAggWaves * kLanes), 0,
-                         stream, g, count, waves);
+      hipLaunchKernelGGL((glr_aggregate<InT, DECAY, MIX, IN, Z, true, kAggRows>), dim3(blocks),
+                         dim3(kAggWaves * kLanes), 0, stream, g, count, waves);
     else
-      hipLaunchKernelGGL((glr_aggregate<InT, DECAY, MIX, false, kAggRows>), dim3(blocks), dim3(kAggWaves * kLanes), 0,
-                         stream, g, count, waves);
+      hipLaunchKernelGGL((glr_aggregate<InT, DECAY, MIX, IN, false, false, kAggRows>), dim3(blocks),
+                         dim3(kAggWaves * kLanes), 0, stream, g, count, waves);
     return hipGetLastError();
   }
 };

@@ -65,9 +65,13 @@ hipError_t launch_block_norm(const BlockPlan& plan, hipStream_t stream);
 int64_t block_norm_bwd_blocks(int64_t B, int64_t L, int D, bool gate_rows);
 hipError_t launch_block_norm_bwd(const BlockPlan& plan, float* workspace, hipStream_t stream);
 
-// to[g, e] = sum over the rows of group g of part[row, offset + e], in a fixed order: rows_group
-// rows a group, `width` sums a row (row_sums.hip).
-hipError_t launch_row_sums(const float* part, int64_t rows_group, int groups, int64_t width, int64_t offset, int size,
-                           float* to, hipStream_t stream);
+// Sums over the rows of a backward's workspace, `width` floats each, in a fixed order
+// (row_sums.hip): to[g, e] = sum over the rows of group g of part[row, offset + e].
+struct RowSum {
+  float* to;  // null: nothing
+  int64_t offset, rows_group;
+  int groups;
+};
+hipError_t launch_row_sums(const float* part, int64_t width, int size, const RowSum (&sums)[3], hipStream_t stream);
 
 }  // namespace ssm

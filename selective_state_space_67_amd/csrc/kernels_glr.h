@@ -15,6 +15,9 @@ namespace ssm {
 constexpr int kGlrSigmoid = 0, kGlrSoftplus = 1;         // decay
 constexpr int kGlrUnit = 0, kGlrRest = 1, kGlrOne = 2;   // mix
 
+// Elements between tokens stay below this, so that a wave's rows can be reached by 32-bit offsets.
+constexpr int64_t kGlrMaxStride = int64_t{1} << 24;
+
 // One call after validation. Pointers are device pointers; optional ones are
 // nullptr. Token strides are in elements.
 struct GlrPlan {

@@ -1,10 +1,13 @@
 // Rows for the norms around a block (gated_norm.hip, block_norm.hip): a team of
-// TR lanes holds a row in registers, NV runs of V elements a lane, run j of lane
-// i at element (j TR + i) V. The only exchange is the sum over the row, by DPP
-// within a wave and through LDS between the waves of a larger team.
+// lanes holds a row in registers, NV runs of V elements a lane, run j of lane i at
+// element (j team + i) V. A team is TR = 8 to 64 lanes of a wave, or (TR = 0) a
+// whole workgroup of as many waves as the row needs. The only exchange is the sum
+// over the row, by DPP within a wave and through LDS between waves.
 //
 // V = 8 (16 bytes of bfloat16) needs sizes and addresses in multiples of a run;
-// V = 1 takes everything else.
+// V = 1 takes everything else. A team goes through its rows in strides, and the
+// next row is loaded (as it lies in memory, half the registers of bfloat16) while
+// one is worked on.
 #pragma once
 
 #include <algorithm>
@@ -15,29 +18,50 @@
 
 namespace ssm {
 
-// V elements as floats from / to memory of type T.
+// V elements as they lie in memory, and as floats.
 template <int V, typename T>
-__device__ __forceinline__ void load_run(const T* p, float (&x)[V]) {
-  if constexpr (V == 1) {
-    x[0] = load_elem(p, 0);
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
+struct Raw {
+  static constexpr int kWords = V == 1 ? 1 : V * static_cast<int>(sizeof(T)) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (V == 1) {
+      if constexpr (sizeof(T) == 2)
+        w[0] = reinterpret_cast<const uint16_t*>(p)[0];
+      else
+        w[0] = reinterpret_cast<const uint32_t*>(p)[0];
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t q = word(r, i >> 1);
-      x[i] = __uint_as_float((i & 1) ? (q & 0xFFFF0000u) : (q << 16));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 r = *reinterpret_cast<const float4*>(p + i);
-      x[i] = r.x;
-      x[i + 1] = r.y;
-      x[i + 2] = r.z;
-      x[i + 3] = r.w;
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 r = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+        w[i] = r.x;
+        w[i + 1] = r.y;
+        w[i + 2] = r.z;
+        w[i + 3] = r.w;
+      }
     }
   }
-}
+  // from a buffer: zeros past its end
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, uint32_t offset) {
+    if constexpr (V == 1) {
+      if constexpr (sizeof(T) == 2)
+        w[0] = __builtin_amdgcn_raw_buffer_load_b16(b, offset, 0, 0);
+      else
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, offset, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const auto r = __builtin_amdgcn_raw_buffer_load_b128(b, offset + 4 * i, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[i + k] = r[k];
+      }
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    if constexpr (V == 1) return __uint_as_float(w[0] << 16);
+    return __uint_as_float((i & 1) ? (w[i / 2] & 0xFFFF0000u) : (w[i / 2] << 16));
+  }
+};
 
 // Two floats as bfloat16, nearest even, by the hardware's conversion (a NaN stays one).
 __device__ __forceinline__ uint32_t bf16_two(float lo, float hi) {
@@ -46,82 +70,122 @@ __device__ __forceinline__ uint32_t bf16_two(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
+// A row of `bytes` bytes as a buffer: what is read past its end is 0, what is written there is dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void* row, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(row), 0, bytes, 0x00020000);
+}
+
+typedef uint32_t words4 __attribute__((ext_vector_type(4)));
+
+// V results as the words that bfloat16 or float32 takes.
 template <int V>
-__device__ __forceinline__ void store_run(void* base, int64_t at, bool bf16, const float (&x)[V]) {
-  if (bf16) {
-    uint16_t* p = static_cast<uint16_t*>(base) + at;
-    if constexpr (V == 1)
-      *p = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x[0]));
+__device__ __forceinline__ words4 bf16_words4(const float (&x)[V]) {
+  return words4{bf16_two(x[0], x[1]), bf16_two(x[2], x[3]), bf16_two(x[4], x[5]), bf16_two(x[6], x[7])};
+}
+__device__ __forceinline__ words4 float_words4(const float* x) {
+  return words4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+}
+
+template <int V>
+__device__ __forceinline__ void store_run(char* p, bool bf16, const float (&x)[V]) {
+  if constexpr (V == 1) {
+    if (bf16)
+      *reinterpret_cast<uint16_t*>(p) = __builtin_bit_cast(uint16_t, static_cast<__bf16>(x[0]));
     else
-      *reinterpret_cast<uint4*>(p) = make_uint4(bf16_two(x[0], x[1]), bf16_two(x[2], x[3]), bf16_two(x[4], x[5]),
-                                                bf16_two(x[6], x[7]));
+      *reinterpret_cast<float*>(p) = x[0];
+  } else if (bf16) {
+    *reinterpret_cast<words4*>(p) = bf16_words4(x);
   } else {
-    float* p = static_cast<float*>(base) + at;
-    if constexpr (V == 1) {
-      *p = x[0];
-    } else {
-      *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-    }
+    *reinterpret_cast<words4*>(p) = float_words4(x);
+    *reinterpret_cast<words4*>(p + 16) = float_words4(x + 4);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_run(__amdgpu_buffer_rsrc_t b, uint32_t offset, bool bf16, const float (&x)[V]) {
+  if constexpr (V == 1) {
+    if (bf16)
+      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<__bf16>(x[0])), b, offset, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[0]), b, offset, 0, 0);
+  } else if (bf16) {
+    __builtin_amdgcn_raw_buffer_store_b128(bf16_words4(x), b, offset, 0, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b128(float_words4(x), b, offset, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(float_words4(x + 4), b, offset + 16, 0, 0);
   }
 }
 
 // Where a lane's runs lie in a row of `size` elements.
 template <int V, int TR, int NV>
 struct Columns {
-  int lane, size;
-  __device__ __forceinline__ Columns(int size) : lane(threadIdx.x % TR), size(size) {}
-  __device__ __forceinline__ int at(int j) const { return (j * TR + lane) * V; }
+  int lane, team, size;
+  __device__ __forceinline__ Columns(int size)
+      : lane(TR ? threadIdx.x % TR : threadIdx.x), team(TR ? TR : blockDim.x), size(size) {}
+  __device__ __forceinline__ int at(int j) const { return (j * team + lane) * V; }
   __device__ __forceinline__ bool on(int j) const { return at(j) < size; }
 
+  // A row as it lies in memory; runs past its end are zeros. A workgroup's row goes through a
+  // buffer, so that its runs need neither addresses nor masks.
   template <typename T>
-  __device__ __forceinline__ void load(const T* row, float (&x)[NV][V]) const {
+  __device__ __forceinline__ void load(const void* base, int64_t row, Raw<V, T> (&x)[NV]) const {
+    const T* p = static_cast<const T*>(base) + row;
+    if constexpr (TR == 0) {
+      const auto b = row_buffer(p, size * static_cast<int>(sizeof(T)));
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (on(j)) {
-        load_run<V>(row + at(j), x[j]);
-      } else {
+      for (int j = 0; j < NV; ++j) x[j].load(b, static_cast<uint32_t>(at(j)) * sizeof(T));
+    } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[j][i] = 0.0f;
+      for (int j = 0; j < NV; ++j) {
+        x[j] = Raw<V, T>{};
+        if (on(j)) x[j].load(p + at(j));
       }
     }
   }
   // a weight row: 1 where there is none
   __device__ __forceinline__ void weights(const float* w, float (&x)[NV][V]) const {
-    if (w) {
-      load(w, x);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[j][i] = 1.0f;
+    if (!w) return;
+    Raw<V, float> r[NV];
+    load(w, 0, r);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[j][i] = r[j].at(i);
+  }
+  __device__ __forceinline__ void store(void* base, int64_t row, bool bf16, const float (&x)[NV][V]) const {
+    const int bytes = bf16 ? 2 : 4;
+    char* p = static_cast<char*>(base) + row * bytes;
+    if constexpr (TR == 0) {
+      const auto b = row_buffer(p, size * bytes);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) store_run<V>(b, static_cast<uint32_t>(at(j)) * bytes, bf16, x[j]);
     } else {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[j][i] = 1.0f;
+        if (on(j)) store_run<V>(p + at(j) * bytes, bf16, x[j]);
     }
-  }
-  __device__ __forceinline__ void store(void* base, int64_t row, bool bf16, const float (&x)[NV][V]) const {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (on(j)) store_run<V>(base, row + at(j), bf16, x[j]);
   }
 };
 
-// Sum over the row's team, in all of its lanes. A team of several waves is the whole
-// workgroup; its sums take turns in two halves of LDS, so that one barrier serves each.
+// Sum over the row's team, in all of its lanes. The sums of a team of several waves take
+// turns in two halves of LDS, so that one barrier serves each.
 template <int TR>
 class TeamSum {
  public:
-  static constexpr int kWaves = TR > 64 ? TR / 64 : 1;
-  __device__ __forceinline__ float operator()(float x, float (&lds)[2][kWaves]) {
-    if constexpr (TR <= 64) {
+  __device__ __forceinline__ float operator()(float x, float (&lds)[2][16]) {
+    if constexpr (TR != 0) {
       return lanes_sum<TR>(x);
     } else {
       x = lanes_sum<64>(x);
       if (threadIdx.x % 64 == 0) lds[half_][threadIdx.x / 64] = x;
       __syncthreads();
-      float t = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) t += lds[half_][i];
+      const int i = threadIdx.x % 16;
+      x = i < static_cast<int>(blockDim.x / 64) ? lds[half_][i] : 0.0f;
       half_ ^= 1;
-      return t;
+      return lanes_sum<16>(x);
     }
   }
 
@@ -145,68 +209,76 @@ struct RowWalk {
   int64_t row, end, step;
   template <int TR>
   __device__ __forceinline__ static RowWalk of(const RowGroups& g) {
-    const int teams = blockDim.x / TR, part = blockIdx.x % g.parts;
-    const int64_t first = static_cast<int64_t>(part) * teams + threadIdx.x / TR;
+    const int teams = TR ? blockDim.x / (TR ? TR : 1) : 1, part = blockIdx.x % g.parts;
+    const int64_t first = static_cast<int64_t>(part) * teams + (TR ? threadIdx.x / (TR ? TR : 1) : 0);
     return {first, g.rows, static_cast<int64_t>(g.parts) * teams};
   }
   __device__ __forceinline__ static int group(const RowGroups& g) { return blockIdx.x / g.parts; }
 };
 
-// A workgroup's sums over its teams' rows: added up in LDS in the teams' order, one row of
-// `count` x size sums a workgroup. `lds` holds size floats for each team.
+// A workgroup's sums over its rows: its teams' are added up in LDS (`lds` holds `size` floats
+// for each) in their order.
 template <int V, int TR, int NV>
 __device__ __forceinline__ void store_sums(const Columns<V, TR, NV>& c, const float (&x)[NV][V], float* lds, float* to) {
-  const int teams = blockDim.x / TR;
-  if (teams == 1) {
+  if constexpr (TR == 0) {
+    c.store(to, 0, false, x);
+  } else {
+    __syncthreads();
+    float* mine = lds + (threadIdx.x / TR) * c.size;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (c.on(j)) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) to[c.at(j) + i] = x[j][i];
+        for (int i = 0; i < V; ++i) mine[c.at(j) + i] = x[j][i];
       }
-    return;
-  }
-  __syncthreads();
-  float* mine = lds + (threadIdx.x / TR) * c.size;
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (c.on(j)) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) mine[c.at(j) + i] = x[j][i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < c.size; e += blockDim.x) {
+      float t = 0.0f;
+      for (int k = 0; k < static_cast<int>(blockDim.x / TR); ++k) t += lds[k * c.size + e];
+      to[e] = t;
     }
-  __syncthreads();
-  for (int e = threadIdx.x; e < c.size; e += blockDim.x) {
-    float t = 0.0f;
-    for (int k = 0; k < teams; ++k) t += lds[k * c.size + e];
-    to[e] = t;
   }
 }
 
-// Team shapes for a row of `size` elements: F::run<V, TR, NV>(...). Up to 16 elements a lane.
+// Team shapes for a row of `size` elements, and the threads of a workgroup: 256 of several
+// teams (64 where that would leave CUs idle: `rows` rows in all), or as many as a row needs.
+// F::run<V, TR, NV, most threads>(threads, ...).
 template <typename F, typename... X>
-hipError_t pick_team(bool runs, int size, X&&... x) {
+hipError_t pick_team(bool runs, int size, int64_t rows, X&&... x) {
+  auto several = [&](int team) { return rows >= 256 * (256 / team) ? 256 : 64; };
+  auto whole = [&](int each) { return (size + 64 * each - 1) / (64 * each) * 64; };
   if (runs) {
-    if (size <= 512) return F::template run<8, 64, 1>(std::forward<X>(x)...);
-    if (size <= 1024) return F::template run<8, 64, 2>(std::forward<X>(x)...);
-    if (size <= 2048) return F::template run<8, 256, 1>(std::forward<X>(x)...);
-    if (size <= 4096) return F::template run<8, 256, 2>(std::forward<X>(x)...);
-    if (size <= 8192) return F::template run<8, 512, 2>(std::forward<X>(x)...);
-    return F::template run<8, 1024, 2>(std::forward<X>(x)...);
+    if (size <= 64) return F::template run<8, 8, 1, 256>(several(8), std::forward<X>(x)...);
+    if (size <= 128) return F::template run<8, 16, 1, 256>(several(16), std::forward<X>(x)...);
+    if (size <= 256) return F::template run<8, 32, 1, 256>(several(32), std::forward<X>(x)...);
+    if (size <= 512) return F::template run<8, 64, 1, 256>(several(64), std::forward<X>(x)...);
+    if (size <= 4096) return F::template run<8, 0, 1, 512>(whole(8), std::forward<X>(x)...);
+    if (size <= 8192) return F::template run<8, 0, 1, 1024>(whole(8), std::forward<X>(x)...);
+    return F::template run<8, 0, 2, 1024>(whole(16), std::forward<X>(x)...);
   }
-  if (size <= 256) return F::template run<1, 64, 4>(std::forward<X>(x)...);
-  if (size <= 1024) return F::template run<1, 64, 16>(std::forward<X>(x)...);
-  if (size <= 4096) return F::template run<1, 256, 16>(std::forward<X>(x)...);
-  return F::template run<1, 1024, 16>(std::forward<X>(x)...);
+  if (size <= 256) return F::template run<1, 64, 4, 256>(several(64), std::forward<X>(x)...);
+  if (size <= 4096) return F::template run<1, 0, 8, 512>(whole(8), std::forward<X>(x)...);
+  return F::template run<1, 0, 16, 1024>(whole(16), std::forward<X>(x)...);
+}
+
+// Threads that go through the rows: 2048 a CU.
+constexpr int64_t kWantThreads = int64_t{1} << 19;
+
+// Parts of a group of rows, for a launch of that many threads; `teams` rows at once in a workgroup.
+inline int row_parts(const RowGroups& g, int threads, int teams) {
+  const int64_t most = (g.rows + teams - 1) / teams;
+  return static_cast<int>(std::min(most, std::max<int64_t>(1, kWantThreads / threads / g.groups)));
+}
+
+#ifndef NORM_BLOCKS
+#define NORM_BLOCKS 512
+#endif
+// Workgroups of a backward, each of which leaves a row of sums for the weights.
+inline int64_t row_sum_blocks(int64_t groups, int64_t rows, int size) {
+  const int64_t want = std::min<int64_t>((rows * size + 16383) / 16384, std::max<int64_t>(1, NORM_BLOCKS / groups));
+  return groups * std::max<int64_t>(1, std::min(want, rows));
 }
 
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-// Threads of a workgroup: a team, or 256 of several teams (64 where that leaves CUs idle).
-template <int TR>
-int workgroup_threads(int64_t rows) {
-  if (TR >= 256) return TR;
-  const int64_t teams = 256 / TR;
-  return rows >= teams * 256 || TR > 64 ? 256 : std::max(TR, 64);
-}
 
 }  // namespace ssm
