@@ -11,9 +11,9 @@ from __future__ import annotations
 import ctypes
 
 from . import binding as _b
-from .binding_delta import _addr, _need, _out, _workspace
+from .binding_delta import _need
 from .binding_delta import _tokens as _head_tokens
-from .binding_glr import _call, _one_device, _tokens
+from .binding_glr import _at, _call, _new, _one_device, _space, _tokens, check_layouts, packer
 
 _i64, _i32, _vp, _f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
 
@@ -36,34 +36,33 @@ class BlockNormParams(ctypes.Structure):
 
 
 STRUCTS = {10: GatedNormParams, 11: BlockNormParams}
+_PACKED = {which: packer(fields) for which, fields in STRUCTS.items()}
 
 
 def declare(lib):
     """Prototypes of this module's entry points (called when the library is loaded)."""
     size = ctypes.POINTER(ctypes.c_size_t)
-    for name, struct in (("ssm_gated_norm", GatedNormParams), ("ssm_block_norm", BlockNormParams)):
+    for name in ("ssm_gated_norm", "ssm_block_norm"):
         for end, last in (("_fwd", _vp), ("_bwd", _vp), ("_bwd_workspace_size", size)):
             fn = getattr(lib, name + end)
-            fn.argtypes, fn.restype = [ctypes.POINTER(struct), last], ctypes.c_int
-    for which, struct in STRUCTS.items():
-        if lib.ssm_abi_struct_size(which) != ctypes.sizeof(struct):
-            raise ImportError("libssmscan.so struct layout does not match this binding")
+            fn.argtypes, fn.restype = [_vp, last], ctypes.c_int
+    check_layouts(lib, STRUCTS, _PACKED)
 
 
-def _gated_params(x, z, w, eps, gate_first):
+def _gated(x, z, w):
+    """(sizes and input type, addresses and strides of x and z, address of w, w_per_head), checked."""
     import torch
 
     if x.dim() != 4:
         raise ValueError("x must be (B, L, H, d)")
-    B, L, H, d = x.shape
-    xs = _head_tokens(x, (B, L, H, d), "x", x.dtype)
-    zs = _head_tokens(z, (B, L, H, d), "z", x.dtype)
+    shape, dt = x.shape, x.dtype
+    B, L, H, d = shape
+    xs = H * d if x.is_contiguous() else _head_tokens(x, shape, "x", dt)
+    zs = _head_tokens(z, shape, "z", dt)
     per_head = w is not None and w.dim() == 2
     if w is not None:
         _need(w, (H, d) if per_head else (d,), "w", torch.float32)
-    p = GatedNormParams(B, L, H, d, _b._dtype_code(x), 0, x.data_ptr(), z.data_ptr(), xs, zs, _addr(w))
-    p.eps, p.gate_first, p.w_per_head = eps, int(bool(gate_first)), int(per_head)
-    return p
+    return (B, L, H, d, _b._dtype_code(x)), (x.data_ptr(), z.data_ptr(), xs, zs), _at(w), int(per_head)
 
 
 def ssm_gated_norm_fwd(x, z, *, w=None, eps=1e-6, gate_first=False, out=None, out_dtype=None, stream=None):
@@ -76,13 +75,14 @@ def ssm_gated_norm_fwd(x, z, *, w=None, eps=1e-6, gate_first=False, out=None, ou
     import torch
 
     lib = _b.load_library()
+    sizes, rows, at_w, per_head = _gated(x, z, w)
     if out is None:
-        out = _out(x, out_dtype or torch.float32, stream)
-    p = _gated_params(x, z, w, eps, gate_first)
-    _need(out, x.shape, "out", out.dtype)
+        out = _new(x, out_dtype or torch.float32, stream)
+    else:
+        _need(out, x.shape, "out", out.dtype)
     _one_device(x, z, w, out)
-    p.out_dtype, p.out = _b._dtype_code(out), out.data_ptr()
-    _call(lib.ssm_gated_norm_fwd, p, stream, x.device)
+    _call(lib.ssm_gated_norm_fwd, _PACKED[10].pack(*sizes, _b._dtype_code(out), *rows, at_w, out.data_ptr(), 0, 0, 0, 0,
+                                                   0, 0, eps, bool(gate_first), per_head, 0), stream, x.device)
     return out
 
 
@@ -95,46 +95,51 @@ def ssm_gated_norm_bwd(x, z, dout, *, w=None, eps=1e-6, gate_first=False, grad_d
 
     lib = _b.load_library()
     dt = grad_dtype or torch.float32
-    p = _gated_params(x, z, w, eps, gate_first)
+    sizes, rows, at_w, per_head = _gated(x, z, w)
     _need(dout, x.shape, "dout", x.dtype)
     _one_device(x, z, dout, w, workspace)
-    g = dict(dx=_out(x, dt, stream), dz=_out(z, dt, stream), dw=None)
+    g = dict(dx=_new(x, dt, stream), dz=_new(z, dt, stream), dw=None)
     if want_dw:
         g["dw"] = _b._result(x.shape[3:] if w is None else w.shape, torch.float32, x.device, stream)
-    p.out_dtype = _b._dtype_code(g["dx"])
-    p.dout, p.dx, p.dz, p.dw = dout.data_ptr(), g["dx"].data_ptr(), g["dz"].data_ptr(), _addr(g["dw"])
-    workspace = _workspace(lib.ssm_gated_norm_bwd_workspace_size, p, workspace, x.device, stream)
-    _call(lib.ssm_gated_norm_bwd, p, stream, x.device)
+    head = (*sizes, _b._dtype_code(g["dx"]), *rows, at_w, 0, dout.data_ptr(), *[_at(t) for t in g.values()])
+    tail = (eps, bool(gate_first), per_head, 0)
+    pack = _PACKED[10].pack
+    workspace, at, n = _space(lib.ssm_gated_norm_bwd_workspace_size, pack(*head, 0, 0, *tail), workspace, x.device,
+                              stream)
+    _call(lib.ssm_gated_norm_bwd, pack(*head, at, n, *tail), stream, x.device)
     return g
 
 
-def _block_params(y, x, w, post, w_post, gate, scale, eps, res_dtype):
+def _block(y, x, w, post, w_post, gate, res_dtype):
+    """(sizes, input type, stream type's code, gate_rows, addresses of the inputs, the stream's type), checked."""
     import torch
 
     if y.dim() != 3:
         raise ValueError("y must be (B, L, D)")
-    B, L, D = y.shape
-    ys = _tokens(y, y.shape, "y", y.dtype)
+    f32, shape = torch.float32, y.shape
+    B, L, D = shape
+    ys = D if y.is_contiguous() else _tokens(y, shape, "y", y.dtype)
     if x is not None:
         if res_dtype is not None and res_dtype != x.dtype:
             raise TypeError("res_dtype %s is not the type of x, %s" % (res_dtype, x.dtype))
-        _need(x, y.shape, "x", x.dtype)
         res_dtype = x.dtype
-    if w_post is not None and not post:
-        raise ValueError("w_post comes with post")
-    for t, name in ((w, "w"), (w_post, "w_post")):
-        if t is not None:
-            _need(t, (D,), name, torch.float32)
+        _need(x, shape, "x", res_dtype)
+    elif res_dtype is None:
+        res_dtype = f32
+    if res_dtype is not f32 and res_dtype is not torch.bfloat16:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % res_dtype)
+    if w is not None:
+        _need(w, (D,), "w", f32)
+    if w_post is not None:
+        if not post:
+            raise ValueError("w_post comes with post")
+        _need(w_post, (D,), "w_post", f32)
     rows = gate is not None and gate.dim() == 2
     if gate is not None:
-        _need(gate, (B, D) if rows else (D,), "gate", torch.float32)
-    res_dtype = res_dtype or torch.float32
-    if res_dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % res_dtype)
-    p = BlockNormParams(B, L, D, _b._dtype_code(y), 0, _b.SSM_BF16 if res_dtype == torch.bfloat16 else _b.SSM_F32,
-                        int(rows), y.data_ptr(), ys, _addr(x), _addr(w), _addr(w_post), _addr(gate))
-    p.eps, p.scale, p.post = eps, scale, int(bool(post))
-    return p, res_dtype
+        _need(gate, (B, D) if rows else (D,), "gate", f32)
+    code = _b.SSM_F32 if res_dtype is f32 else _b.SSM_BF16
+    inputs = (code, int(rows), y.data_ptr(), ys, _at(x), _at(w), _at(w_post), _at(gate))
+    return (B, L, D, _b._dtype_code(y)), inputs, res_dtype
 
 
 def ssm_block_norm_fwd(y, x=None, *, w=None, post=False, w_post=None, gate=None, scale=1.0, eps=1e-6, out=None,
@@ -151,17 +156,18 @@ def ssm_block_norm_fwd(y, x=None, *, w=None, post=False, w_post=None, gate=None,
     import torch
 
     lib = _b.load_library()
-    p, res = _block_params(y, x, w, post, w_post, gate, scale, eps, res_dtype)
+    sizes, inputs, res = _block(y, x, w, post, w_post, gate, res_dtype)
     if out is None:
-        out = _out(y, out_dtype or torch.float32, stream)
-    if x_out is None and want_x:
-        x_out = _out(y, res, stream)
-    _need(out, y.shape, "out", out.dtype)
+        out = _new(y, out_dtype or torch.float32, stream)
+    else:
+        _need(out, y.shape, "out", out.dtype)
     if x_out is not None:
         _need(x_out, y.shape, "x_out", res)
+    elif want_x:
+        x_out = _new(y, res, stream)
     _one_device(y, x, w, w_post, gate, out, x_out)
-    p.out_dtype, p.out, p.x_out = _b._dtype_code(out), out.data_ptr(), _addr(x_out)
-    _call(lib.ssm_block_norm_fwd, p, stream, y.device)
+    _call(lib.ssm_block_norm_fwd, _PACKED[11].pack(*sizes, _b._dtype_code(out), *inputs, out.data_ptr(), _at(x_out), 0, 0,
+                                                   0, 0, 0, 0, 0, 0, 0, eps, scale, bool(post), 0), stream, y.device)
     return out, x_out
 
 
@@ -178,23 +184,22 @@ def ssm_block_norm_bwd(y, x, dout, dx_out=None, *, w=None, post=False, w_post=No
     import torch
 
     lib = _b.load_library()
-    p, res = _block_params(y, x, w, post, w_post, gate, scale, eps, dx_out.dtype if x is None and dx_out is not None else None)
+    sizes, inputs, res = _block(y, x, w, post, w_post, gate, dx_out.dtype if x is None and dx_out is not None else None)
     _need(dout, y.shape, "dout", y.dtype)
     if dx_out is not None:
         _need(dx_out, y.shape, "dx_out", res)
     _one_device(y, x, dout, dx_out, w, w_post, gate, workspace)
-    D, dev = y.shape[2], y.device
+    D, dev = sizes[2], y.device
 
     def new(wanted, shape):
         return _b._result(shape, torch.float32, dev, stream) if wanted else None
 
-    g = dict(dy=_out(y, grad_dtype or torch.float32, stream), dx=None if x is None else _out(x, res, stream),
+    g = dict(dy=_new(y, grad_dtype or torch.float32, stream), dx=None if x is None else _new(x, res, stream),
              dw=new(want_dw, (D,)), dw_post=new(want_dw and post, (D,)),
              dgate=new(want_dw and gate is not None, () if gate is None else gate.shape))
-    p.out_dtype = _b._dtype_code(g["dy"])
-    p.dout, p.dx_out = dout.data_ptr(), _addr(dx_out)
-    for name, t in g.items():
-        setattr(p, name, _addr(t))
-    workspace = _workspace(lib.ssm_block_norm_bwd_workspace_size, p, workspace, dev, stream)
-    _call(lib.ssm_block_norm_bwd, p, stream, dev)
+    head = (*sizes, _b._dtype_code(g["dy"]), *inputs, 0, 0, dout.data_ptr(), _at(dx_out), *[_at(t) for t in g.values()])
+    tail = (eps, scale, bool(post), 0)
+    pack = _PACKED[11].pack
+    workspace, at, n = _space(lib.ssm_block_norm_bwd_workspace_size, pack(*head, 0, 0, *tail), workspace, dev, stream)
+    _call(lib.ssm_block_norm_bwd, pack(*head, at, n, *tail), stream, dev)
     return g

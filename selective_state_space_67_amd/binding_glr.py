@@ -5,13 +5,18 @@ slices of one packed projection: channels are dense inside a token, tokens lie a
 fixed stride apart, batch rows follow each other. Everything else is contiguous.
 
 Streams as in binding.py: what a call allocates belongs to the stream that it runs on.
+
+A small call's time is mostly this module's, so its parameter structs are packed into
+bytes in one go (a ctypes structure of twenty fields takes four times as long), and a
+tensor that is as expected is looked at no further.
 """
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from . import binding as _b
-from .binding_delta import _addr, _need, _out, _stream, _workspace
+from .binding_delta import _need, _stream
 
 _i64, _i32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
 
@@ -41,39 +46,80 @@ class GlrUpdateParams(ctypes.Structure):
 
 
 STRUCTS = {8: GlrParams, 9: GlrUpdateParams}
+_CODES = {_i64: "q", _i32: "i", _vp: "Q", ctypes.c_size_t: "Q", ctypes.c_float: "f"}
+
+
+def packer(fields):
+    """Packs a parameter struct's fields, in order and at the places that C gives them."""
+    return struct.Struct("@" + "".join(_CODES[t] for _, t in fields._fields_))
+
+
+_PACKED = {which: packer(fields) for which, fields in STRUCTS.items()}
 
 
 def declare(lib):
-    """Prototypes of this module's entry points (called when the library is loaded)."""
+    """Prototypes of this module's entry points (called when the library is loaded). A
+    parameter struct is passed by reference or as packed bytes."""
     size = ctypes.POINTER(ctypes.c_size_t)
-    for name, struct in (("ssm_glr_fwd", GlrParams), ("ssm_glr_bwd", GlrParams), ("ssm_glr_update", GlrUpdateParams)):
+    for name, last in (("ssm_glr_fwd", _vp), ("ssm_glr_bwd", _vp), ("ssm_glr_update", _vp),
+                       ("ssm_glr_workspace_size", size), ("ssm_glr_bwd_workspace_size", size)):
         fn = getattr(lib, name)
-        fn.argtypes, fn.restype = [ctypes.POINTER(struct), _vp], ctypes.c_int
-    for name in ("ssm_glr_workspace_size", "ssm_glr_bwd_workspace_size"):
-        fn = getattr(lib, name)
-        fn.argtypes, fn.restype = [ctypes.POINTER(GlrParams), size], ctypes.c_int
-    for which, struct in STRUCTS.items():
-        if lib.ssm_abi_struct_size(which) != ctypes.sizeof(struct):
+        fn.argtypes, fn.restype = [_vp, last], ctypes.c_int
+    check_layouts(lib, STRUCTS, _PACKED)
+
+
+def check_layouts(lib, structs, packed):
+    for which, fields in structs.items():
+        if not lib.ssm_abi_struct_size(which) == ctypes.sizeof(fields) == packed[which].size:
             raise ImportError("libssmscan.so struct layout does not match this binding")
 
 
 def _one_device(first, *others):
     """Everything lies where the call runs (an address on another device would fault there)."""
+    d = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != d:
             raise ValueError("tensors on %s and %s in one call" % (first.device, t.device))
 
 
-def _call(fn, p, stream, device):
+def _call(fn, packed, stream, device):
     """Enqueue on the stream, with its device current."""
     import torch
 
     st = _stream(stream, device)
     if device.type != "cuda" or device.index == torch._C._cuda_getDevice():
-        _b._check(fn(ctypes.byref(p), st))
-        return
-    with torch.cuda.device(device):
-        _b._check(fn(ctypes.byref(p), st))
+        status = fn(packed, st)
+    else:
+        with torch.cuda.device(device):
+            status = fn(packed, st)
+    if status != 0:
+        _b._check(status)
+
+
+def _at(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _new(t, dtype, stream):
+    """A contiguous output of t's shape."""
+    import torch
+
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+    return _b._result(t.shape, dtype, t.device, stream)
+
+
+def _space(size_fn, packed, workspace, device, stream):
+    """(workspace, its address and bytes) of what a call needs."""
+    import torch
+
+    n = ctypes.c_size_t(0)
+    _b._check(size_fn(packed, ctypes.byref(n)))
+    if n.value == 0:
+        return workspace, 0, 0
+    if workspace is None or workspace.numel() * workspace.element_size() < n.value:
+        workspace = _b._empty(int(n.value), torch.uint8, device, stream)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _tokens(t, shape, name, dtype):
@@ -93,41 +139,52 @@ def _tokens(t, shape, name, dtype):
 
 
 def _inputs(u, dt_raw, A, dt_bias, in_raw, in_bias, z, decay, mix):
-    """The struct fields _INPUTS and the kinds, checked."""
+    """(sizes and input type, the struct fields _INPUTS, the kinds), checked."""
     import torch
 
-    if decay not in _DECAYS:
+    f32 = torch.float32
+    p_decay, p_mix = _DECAYS.get(decay), _MIXES.get(mix)
+    if p_decay is None:
         raise ValueError("decay is 'sigmoid' or 'softplus' (got %r)" % (decay,))
-    if mix not in _MIXES:
+    if p_mix is None:
         raise ValueError("mix is 'unit', 'rest' or 'one' (got %r)" % (mix,))
-    if in_bias is not None and in_raw is None:
-        raise ValueError("in_bias comes with in_raw")
     if u.dim() != 3:
         raise ValueError("u must be (B, L, D)")
     shape, dt = u.shape, u.dtype
-    D = shape[2]
-    steps = [_tokens(u, shape, "u", dt), _tokens(dt_raw, shape, "dt_raw", dt),
-             0 if in_raw is None else _tokens(in_raw, shape, "in_raw", dt),
-             0 if z is None else _tokens(z, shape, "z", dt)]
-    _need(A, (D,), "A", torch.float32)
+    B, L, D = shape
+    us = D if u.is_contiguous() else _tokens(u, shape, "u", dt)
+    ds = _tokens(dt_raw, shape, "dt_raw", dt)
+    ins = zs = 0
+    if in_raw is not None:
+        ins = _tokens(in_raw, shape, "in_raw", dt)
+    elif in_bias is not None:
+        raise ValueError("in_bias comes with in_raw")
+    if z is not None:
+        zs = _tokens(z, shape, "z", dt)
+    size = (D,)
+    _need(A, size, "A", f32)
     if dt_bias is not None:
-        _need(dt_bias, (D,), "dt_bias", torch.float32)
+        _need(dt_bias, size, "dt_bias", f32)
     if in_bias is not None:
-        _need(in_bias, (D,), "in_bias", torch.float32)
-    fields = (u.data_ptr(), dt_raw.data_ptr(), _addr(in_raw), _addr(z), *steps, A.data_ptr(), _addr(dt_bias),
-              _addr(in_bias))
-    return fields, _DECAYS[decay], _MIXES[mix]
+        _need(in_bias, size, "in_bias", f32)
+    fields = (u.data_ptr(), dt_raw.data_ptr(), _at(in_raw), _at(z), us, ds, ins, zs, A.data_ptr(), _at(dt_bias),
+              _at(in_bias))
+    return (B, L, D, _b._dtype_code(u)), fields, (p_decay, p_mix)
 
 
-def _params(u, fields, reset, h0, out_code):
+def _sequence(sizes, reset, h0):
+    """Addresses of reset and h0, checked."""
     import torch
 
-    B, L, D = u.shape
+    B, L, D, _ = sizes
     if reset is not None:
         _need(reset, (B, L), "reset", torch.uint8)
     if h0 is not None:
         _need(h0, (B, D), "h0", torch.float32)
-    return GlrParams(B, L, D, _b._dtype_code(u), out_code, *fields, _addr(reset), _addr(h0))
+    return _at(reset), _at(h0)
+
+
+_NO_GRADS = (0,) * 10
 
 
 def ssm_glr_fwd(u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=None, z=None, reset=None, h0=None, out=None,
@@ -143,44 +200,43 @@ def ssm_glr_fwd(u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=None, z=None
     import torch
 
     lib = _b.load_library()
-    fields, p_decay, p_mix = _inputs(u, dt_raw, A, dt_bias, in_raw, in_bias, z, decay, mix)
+    sizes, fields, kinds = _inputs(u, dt_raw, A, dt_bias, in_raw, in_bias, z, decay, mix)
     if out is None:
-        out = _out(u, out_dtype or torch.float32, stream)
-    _need(out, u.shape, "out", out.dtype)
-    p = _params(u, fields, reset, h0, _b._dtype_code(out))
+        out = _new(u, out_dtype or torch.float32, stream)
+    else:
+        _need(out, u.shape, "out", out.dtype)
     if h_last is not None:
-        _need(h_last, (p.batch, p.dim), "h_last", torch.float32)
-    p.out, p.h_last = out.data_ptr(), _addr(h_last)
-    p.decay, p.mix, p.num_segments = p_decay, p_mix, num_segments
-    workspace = _workspace(lib.ssm_glr_workspace_size, p, workspace, u.device, stream)
+        _need(h_last, (sizes[0], sizes[2]), "h_last", torch.float32)
     _one_device(u, dt_raw, A, dt_bias, in_raw, in_bias, z, reset, h0, out, h_last, workspace)
-    _call(lib.ssm_glr_fwd, p, stream, u.device)
+    head = (*sizes, _b._dtype_code(out), *fields, *_sequence(sizes, reset, h0), out.data_ptr(), _at(h_last), *_NO_GRADS)
+    pack = _PACKED[8].pack
+    workspace, at, n = _space(lib.ssm_glr_workspace_size, pack(*head, 0, 0, *kinds, num_segments, 0), workspace,
+                              u.device, stream)
+    _call(lib.ssm_glr_fwd, pack(*head, at, n, *kinds, num_segments, 0), stream, u.device)
     return out
 
 
-def _update_params(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, decay, mix):
+def _update(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, out_dtype, decay, mix, stream):
+    """(packed struct, out) of a decode window."""
     import torch
 
-    fields, p_decay, p_mix = _inputs(u, dt_raw, A, dt_bias, in_raw, in_bias, z, decay, mix)
-    B, T, D = u.shape
-    _need(h, (B, D), "h", torch.float32)
-    _need(out, u.shape, "out", out.dtype)
+    sizes, fields, kinds = _inputs(u, dt_raw, A, dt_bias, in_raw, in_bias, z, decay, mix)
+    if out is None:
+        out = _new(u, out_dtype or torch.float32, stream)
+    else:
+        _need(out, u.shape, "out", out.dtype)
+    _need(h, (sizes[0], sizes[2]), "h", torch.float32)
     _one_device(u, h, dt_raw, A, dt_bias, in_raw, in_bias, z, out)
-    return GlrUpdateParams(B, T, D, _b._dtype_code(u), _b._dtype_code(out), h.data_ptr(), *fields, out.data_ptr(),
-                           p_decay, p_mix)
+    return _PACKED[9].pack(*sizes, _b._dtype_code(out), h.data_ptr(), *fields, out.data_ptr(), *kinds), out
 
 
 def ssm_glr_update(h, u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=None, z=None, out=None, out_dtype=None,
                    decay="sigmoid", mix="unit", stream=None):
     """Decode window of T tokens: updates h (B, D) float32 in place and returns out
     (B, T, D). Arguments as for ssm_glr_fwd with L = T."""
-    import torch
-
     lib = _b.load_library()
-    if out is None:
-        out = _out(u, out_dtype or torch.float32, stream)
-    p = _update_params(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, decay, mix)
-    _call(lib.ssm_glr_update, p, stream, u.device)
+    packed, out = _update(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, out_dtype, decay, mix, stream)
+    _call(lib.ssm_glr_update, packed, stream, u.device)
     return out
 
 
@@ -191,18 +247,16 @@ def prepare_glr_update(h, u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=No
     import torch
 
     lib = _b.load_library()
-    if out is None:
-        out = _out(u, out_dtype or torch.float32, stream)
-    p = _update_params(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, decay, mix)
+    packed, out = _update(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, out_dtype, decay, mix, stream)
     fn, dev = lib.ssm_glr_update, u.device
     if stream is None and dev.type == "cuda":
         stream = torch.cuda.current_stream(dev)
 
     def call():
-        _call(fn, p, stream, dev)
+        _call(fn, packed, stream, dev)
         return out
 
-    call.keep = ((h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out), p)
+    call.keep = (h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out)
     return call
 
 
@@ -220,26 +274,20 @@ def ssm_glr_bwd(u, dt_raw, A, dout, *, dt_bias=None, in_raw=None, in_bias=None, 
     import torch
 
     lib = _b.load_library()
-    fields, p_decay, p_mix = _inputs(u, dt_raw, A, dt_bias, in_raw, in_bias, z, decay, mix)
+    sizes, fields, kinds = _inputs(u, dt_raw, A, dt_bias, in_raw, in_bias, z, decay, mix)
     gd, f32, dev = grad_dtype or torch.float32, torch.float32, u.device
-    B, L, D = u.shape
+    B, L, D, _ = sizes
     _need(dout, u.shape, "dout", u.dtype)
     if dh_last is not None:
         _need(dh_last, (B, D), "dh_last", f32)
-
-    def new(wanted, shape, dtype):
-        return _b._result(shape, dtype, dev, stream) if wanted else None
-
-    gate = in_raw is not None
-    g = dict(du=new(True, u.shape, gd), d_dt_raw=new(True, u.shape, gd), din_raw=new(gate, u.shape, gd),
-             dz=new(z is not None, u.shape, gd), dA=new(True, (D,), f32), d_dt_bias=new(True, (D,), f32),
-             din_bias=new(gate, (D,), f32), dh0=new(want_dh0, (B, D), f32))
-    p = _params(u, fields, reset, h0, _b._dtype_code(g["du"]))
-    p.dout, p.dh_last = dout.data_ptr(), _addr(dh_last)
-    for name, t in g.items():
-        setattr(p, name, _addr(t))
-    p.decay, p.mix = p_decay, p_mix
-    workspace = _workspace(lib.ssm_glr_bwd_workspace_size, p, workspace, dev, stream)
     _one_device(u, dt_raw, A, dout, dt_bias, in_raw, in_bias, z, reset, h0, dh_last, workspace)
-    _call(lib.ssm_glr_bwd, p, stream, dev)
+    gate = in_raw is not None
+    g = dict(du=_new(u, gd, stream), d_dt_raw=_new(u, gd, stream), din_raw=_new(u, gd, stream) if gate else None,
+             dz=None if z is None else _new(u, gd, stream), dA=_new(A, f32, stream), d_dt_bias=_new(A, f32, stream),
+             din_bias=_new(A, f32, stream) if gate else None, dh0=_b._result((B, D), f32, dev, stream) if want_dh0 else None)
+    head = (*sizes, _b._dtype_code(g["du"]), *fields, *_sequence(sizes, reset, h0), 0, 0, dout.data_ptr(), _at(dh_last),
+            *[_at(t) for t in g.values()])
+    pack = _PACKED[8].pack
+    workspace, at, n = _space(lib.ssm_glr_bwd_workspace_size, pack(*head, 0, 0, *kinds, 0, 0), workspace, dev, stream)
+    _call(lib.ssm_glr_bwd, pack(*head, at, n, *kinds, 0, 0), stream, dev)
     return g

@@ -141,17 +141,17 @@ def test_binding_refusals():
 
     z = torch.zeros
     x, y = z(2, 3, 2, 8), z(2, 3, 16)
-    bb._gated_params(x, x, z(8), 1e-6, False)
-    assert bb._gated_params(x, x, z(2, 8), 1e-6, True).w_per_head == 1
+    bb._gated(x, x, z(8))
+    assert bb._gated(x, x, z(2, 8))[3] == 1
     for bad in ((x, z(2, 3, 2, 9), None), (x, x, z(9)), (x, x, z(3, 8)), (y, y, None), (x, x.transpose(1, 2), None)):
         with pytest.raises(ValueError):
-            bb._gated_params(*bad, 1e-6, False)
+            bb._gated(*bad)
     with pytest.raises(TypeError):
-        bb._gated_params(x, x.bfloat16(), None, 1e-6, False)
-    ok = dict(y=y, x=y, w=None, post=True, w_post=z(16), gate=None, scale=1.0, eps=1e-6, res_dtype=None)
-    make = lambda **kw: bb._block_params(**{**ok, **kw})  # noqa: E731
+        bb._gated(x, x.bfloat16(), None)
+    ok = dict(y=y, x=y, w=None, post=True, w_post=z(16), gate=None, res_dtype=None)
+    make = lambda **kw: bb._block(**{**ok, **kw})  # noqa: E731
     make()
-    assert make(gate=z(2, 16))[0].gate_rows == 1 and make(x=y.bfloat16())[0].res_dtype == bd.SSM_BF16
+    assert make(gate=z(2, 16))[1][1] == 1 and make(x=y.bfloat16())[1][0] == bd.SSM_BF16
     for bad in (dict(x=z(2, 3, 17)), dict(w=z(15)), dict(gate=z(3, 16)), dict(post=False), dict(y=z(6, 16)),
                 dict(x=z(2, 3, 32)[..., ::2]), dict(y=z(2, 3, 32)[..., ::2])):
         with pytest.raises(ValueError):
@@ -160,3 +160,11 @@ def test_binding_refusals():
                 dict(gate=z(16).half())):
         with pytest.raises(TypeError):
             make(**bad)
+
+
+@pytest.mark.parametrize("which", bb.STRUCTS)
+def test_packed_fields_are_the_structs(which):
+    """Every field in its place, whatever its type."""
+    fields = bb.STRUCTS[which]._fields_
+    got = bb.STRUCTS[which].from_buffer_copy(bb._PACKED[which].pack(*range(1, len(fields) + 1)))
+    assert [getattr(got, n) for n, _ in fields] == list(range(1, len(fields) + 1))

@@ -125,9 +125,9 @@ def test_more_than_a_launch_allows(lib):  # noqa: F811
     assert ok(batch=(1 << 26) - 1, seqlen=1) == 0
     assert ok(batch=1 << 26, seqlen=1) == SHAPE
     refused(lib, "ssm_glr_update", window(batch=1 << 26, tokens=1, dim=1), SHAPE, "workgroups")
-    # 1024 threads a piece, and none of the sizes is multiplied past 64 bits
-    assert ok(batch=1 << 21, seqlen=128) == 0
-    assert ok(batch=1 << 22, seqlen=128) == SHAPE
+    # 512 threads a piece, and none of the sizes is multiplied past 64 bits
+    assert ok(batch=(1 << 23) - 1, seqlen=128) == 0
+    assert ok(batch=1 << 23, seqlen=128) == SHAPE
     assert ok(batch=1 << 20, seqlen=1 << 26, num_segments=1 << 20) == SHAPE
     assert lib.ssm_glr_bwd_workspace_size(ctypes.byref(seq(batch=1 << 20, seqlen=1 << 20, dim=1)), ctypes.byref(n)) == SHAPE
     assert lib.ssm_glr_bwd_workspace_size(ctypes.byref(seq(batch=1 << 57, seqlen=1, dim=1)), ctypes.byref(n)) == SHAPE
@@ -164,4 +164,12 @@ def test_binding_refusals():
     assert bg._tokens(packed[..., 3:11], (2, 5, 8), "u", torch.float32) == 40
     assert bg._tokens(packed[:, :1, 3:11], (2, 1, 8), "u", torch.float32) == 200
     with pytest.raises(ValueError):
-        bg._one_device(u, z(3, device="meta"))
+        bg._one_device(u, type("T", (), dict(get_device=lambda self: 0, device="cuda:0"))())
+
+
+@pytest.mark.parametrize("which", bg.STRUCTS)
+def test_packed_fields_are_the_structs(which):
+    """Every field in its place, whatever its type."""
+    fields = bg.STRUCTS[which]._fields_
+    got = bg.STRUCTS[which].from_buffer_copy(bg._PACKED[which].pack(*range(1, len(fields) + 1)))
+    assert [getattr(got, n) for n, _ in fields] == list(range(1, len(fields) + 1))
