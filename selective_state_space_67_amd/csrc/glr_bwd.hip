@@ -9,27 +9,31 @@
 //
 // and dg = 0 at a reset, which hands no adjoint on either.
 //
-// Three passes: what every piece of 64 rows does to a state and to an adjoint
+// Three passes: what every piece of 32 rows does to a state and to an adjoint
 // (glr_aggregate: u, dt_raw, in_raw, z, dout read once), the states and adjoints
 // that enter the pieces (glr_fold), and here the pieces' gradients, all in
-// parallel: a workgroup takes one piece of 64 channels, its waves K rows each,
+// parallel: a workgroup takes one piece of 64 channels, its waves 8 rows each,
 // kept in registers. Each wave's rows act on a state as (P, H) and on an adjoint
 // as (P, G); the waves exchange them through LDS once. The parameters' gradients
 // are summed over a wave's rows in registers, over the waves in LDS, and over the
 // pieces by glr_sums, always in the same order.
+#include <type_traits>
+
 #include "glr_device.h"
 #include "glr_launch.h"
 
 namespace ssm {
 namespace {
 
-constexpr int kWaves = 8, kRows = 8, kPiece = kWaves * kRows;
+constexpr int kRows = 8, kPiece = kGlrBwdWaves * kRows;
 
 template <typename InT, int DECAY, int MIX, bool IN, bool Z, int W, int K>
 __global__ __launch_bounds__(kLanes * W) void glr_grads(const GlrArgs g) {
   __shared__ float ex[3][W][kLanes];  // P, H, G; then the three sums
   const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
-  const int tile = blockIdx.x % g.tiles, rest = blockIdx.x / g.tiles;
+  // the pieces that were read last come first: some of them are in the last-level cache still
+  const int block = gridDim.x - 1 - blockIdx.x;
+  const int tile = block % g.tiles, rest = block / g.tiles;
   const int piece = rest % g.pieces, batch = rest / g.pieces;
   const int channel = tile * kLanes + lane, ch = min(channel, g.D - 1);
   const bool on = channel < g.D;
@@ -52,6 +56,7 @@ __global__ __launch_bounds__(kLanes * W) void glr_grads(const GlrArgs g) {
 
   float a[K], c[K], x[K], i[K], s[K], dy[K], b[K];  // x = i u, b = c x
   decays<InT, DECAY, MIX, K>(chn, rdt, s, a, c);
+  const bool plain = rows == K && cuts == 0;
   if (cuts) {
     keep_branch();
 #pragma unroll
@@ -69,64 +74,46 @@ __global__ __launch_bounds__(kLanes * W) void glr_grads(const GlrArgs g) {
     b[k] = MIX == kGlrOne ? x[k] : c[k] * x[k];
     dy[k] = Z ? widen<InT>(rdy[k]) * silu_f32(widen<InT>(rz[k])) : widen<InT>(rdy[k]);
   }
-  // what the wave's rows do to a state and to an adjoint
   float P = 1.0f, H = 0.0f, G = 0.0f;
-  if (rows == K && cuts == 0) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      P *= a[k];
-      H = __builtin_fmaf(a[k], H, b[k]);
-      G = __builtin_fmaf(P, dy[k], G);
-    }
-  } else {
-    keep_branch();
-    bool cut = false;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (k < rows) {
-        const bool here = (cuts >> k) & 1;
-        cut |= here;
-        P *= a[k];
-        H = here ? b[k] : __builtin_fmaf(a[k], H, b[k]);
-        if (!cut) G = __builtin_fmaf(P, dy[k], G);
-      }
-    }
-    if (cut) P = kCut;
-  }
-  ex[0][w][lane] = P;
+  bool cut = false;
+  if (plain)
+    run_rows<true, true, K>(a, b, dy, K, 0, P, H, G, cut);
+  else
+    run_rows<false, true, K>(a, b, dy, rows, cuts, P, H, G, cut);
+  ex[0][w][lane] = cut ? kCut : P;
   ex[1][w][lane] = H;
   ex[2][w][lane] = G;
   __syncthreads();
   for (int j = 0; j < w; ++j) h = through(ex[0][j][lane], ex[1][j][lane], h);
   for (int j = W - 1; j > w; --j) m = through(ex[0][j][lane], ex[2][j][lane], m);
+
   float sum_A = 0.0f, sum_dt = 0.0f, sum_in = 0.0f;
-  if (rows > 0) {
+  auto gradients = [&](auto all) {
+    constexpr bool PLAIN = decltype(all)::value;
     float before[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       before[k] = h;
-      h = __builtin_fmaf(a[k], h, b[k]);
-      if (cuts) {
-        keep_branch();
-        if ((cuts >> k) & 1) h = b[k];
-      }
+      h = !PLAIN && ((cuts >> k) & 1) ? b[k] : __builtin_fmaf(a[k], h, b[k]);
       if (Z) {  // b becomes dz
         const float z = widen<InT>(rz[k]), sz = sigmoid_f32(z);
         b[k] = widen<InT>(rdy[k]) * h * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
       }
     }
-    if (Z && on) store_rows<K>(g.dz, row, g.D, rows, ch, g.out_bf16, b);
+    if (Z && on) store_rows<PLAIN, K>(g.dz, row, g.D, rows, ch, g.out_bf16, b);
     float d_in[K];
-    auto back = [&](int k, bool here) {
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+      if (!PLAIN && k >= rows) continue;
       const float lam = dy[k] + m, lc = MIX == kGlrOne ? lam : lam * c[k];
       b[k] = IN ? lc * i[k] : lc;  // du
       if (IN) {
         d_in[k] = lc * x[k] * (1.0f - i[k]);
         sum_in += d_in[k];
       }
-      if (here) {
+      if (!PLAIN && ((cuts >> k) & 1)) {
         m = dy[k] = 0.0f;
-        return;
+        continue;
       }
       m = a[k] * lam;
       // where a rounds to 1, c is 0 and its slope infinite, but what the gate and A get tends to 0
@@ -138,22 +125,17 @@ __global__ __launch_bounds__(kLanes * W) void glr_grads(const GlrArgs g) {
       const float slope = DECAY == kGlrSigmoid ? s[k] * (1.0f - s[k]) : sigmoid_f32(widen<InT>(rdt[k]) + chn.dt);
       dy[k] = dg * chn.A * slope;  // d dt_raw
       sum_dt += dy[k];
-    };
-    if (rows == K && cuts == 0) {
-#pragma unroll
-      for (int k = K - 1; k >= 0; --k) back(k, false);
-    } else {
-      keep_branch();
-#pragma unroll
-      for (int k = K - 1; k >= 0; --k)
-        if (k < rows) back(k, (cuts >> k) & 1);
     }
     if (on) {
-      store_rows<K>(g.du, row, g.D, rows, ch, g.out_bf16, b);
-      if (IN) store_rows<K>(g.d_in, row, g.D, rows, ch, g.out_bf16, d_in);
-      store_rows<K>(g.d_dt, row, g.D, rows, ch, g.out_bf16, dy);
+      store_rows<PLAIN, K>(g.du, row, g.D, rows, ch, g.out_bf16, b);
+      if (IN) store_rows<PLAIN, K>(g.d_in, row, g.D, rows, ch, g.out_bf16, d_in);
+      store_rows<PLAIN, K>(g.d_dt, row, g.D, rows, ch, g.out_bf16, dy);
     }
-  }
+  };
+  if (plain)
+    gradients(std::true_type{});
+  else if (rows > 0)
+    gradients(std::false_type{});
   __syncthreads();
   ex[0][w][lane] = sum_A;
   ex[1][w][lane] = sum_dt;
@@ -197,7 +179,7 @@ __global__ __launch_bounds__(256) void glr_sums(const float* __restrict__ part, 
 struct Grads {
   template <typename InT, int DECAY, int MIX, bool IN, bool Z>
   static hipError_t run(unsigned blocks, const GlrArgs& g, hipStream_t stream) {
-    hipLaunchKernelGGL((glr_grads<InT, DECAY, MIX, IN, Z, kWaves, kRows>), dim3(blocks), dim3(kWaves * kLanes), 0,
+    hipLaunchKernelGGL((glr_grads<InT, DECAY, MIX, IN, Z, kGlrBwdWaves, kRows>), dim3(blocks), dim3(kGlrBwdWaves * kLanes), 0,
                        stream, g);
     return hipGetLastError();
   }
@@ -208,7 +190,7 @@ struct Grads {
 GlrPieces plan_glr_bwd(int64_t B, int64_t L, int64_t D) {
   GlrPieces p{};
   p.rows = kPiece;
-  p.waves = kWaves;
+  p.waves = kGlrBwdWaves;
   p.ways = 2;
   p.pieces = (L + kPiece - 1) / kPiece;
   const size_t each = (static_cast<size_t>(B) * p.pieces * D * sizeof(float) + 255) / 256 * 256;
@@ -228,7 +210,7 @@ hipError_t launch_glr_bwd(const GlrPlan& plan, const GlrPieces& pieces, void* wo
   if (e != hipSuccess) return e;
   const unsigned blocks = static_cast<unsigned>(plan.B * pieces.pieces * g.tiles);
   SSM_LOG("launch glr_grads: %lld pieces of %d rows; grid %u x %d threads", static_cast<long long>(pieces.pieces),
-          kPiece, blocks, kWaves * kLanes);
+          kPiece, blocks, kGlrBwdWaves * kLanes);
   e = glr_pick<Grads>(plan, blocks, g, stream);
   if (e != hipSuccess) return e;
   const unsigned grid = static_cast<unsigned>((3 * plan.D + 15) / 16);

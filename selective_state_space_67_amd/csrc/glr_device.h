@@ -87,9 +87,28 @@ __device__ __forceinline__ void load_rows(const void* base, int64_t row, int64_t
   for (int k = 0; k < K; ++k) x[k] = raw_load<T>(b, at, min(k, rows - 1));
 }
 
-// K rows of results, of which `rows` exist: rounding to bfloat16 is to nearest even, by the
+// What K rows of a wave do to a state that enters them (P, H) and to an adjoint that enters
+// from behind (P, G), as below. `rows` exist; `cuts` start a document. With PLAIN all exist and
+// none does.
+template <bool PLAIN, bool BWD, int K>
+__device__ __forceinline__ void run_rows(const float (&a)[K], const float (&b)[K], const float (&dy)[K], int rows,
+                                         uint32_t cuts, float& P, float& H, float& G, bool& cut) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (PLAIN || k < rows) {
+      const bool here = !PLAIN && ((cuts >> k) & 1);
+      cut |= here;
+      P *= a[k];
+      H = here ? b[k] : __builtin_fmaf(a[k], H, b[k]);
+      // what lies behind a document's start is out of the adjoint's sight
+      if (BWD && !cut) G = __builtin_fmaf(P, dy[k], G);
+    }
+  }
+}
+
+// K rows of results, of which `rows` exist (all with PLAIN): rounding to bfloat16 is to nearest even, by the
 // hardware's conversion (a NaN stays one).
-template <int K>
+template <bool PLAIN, int K>
 __device__ __forceinline__ void store_rows(void* base, int64_t row, int D, int rows, uint32_t channel, bool bf16,
                                            const float (&x)[K]) {
   const RowBuffer b(base, row, D, bf16 ? 2 : 4);
@@ -101,7 +120,7 @@ __device__ __forceinline__ void store_rows(void* base, int64_t row, int D, int r
     else
       __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[k]), b.rsrc, at, k * b.step, 0);
   };
-  if (rows == K) {
+  if (PLAIN || rows == K) {
 #pragma unroll
     for (int k = 0; k < K; ++k) store(k);
   } else {

@@ -37,18 +37,6 @@ struct Rows {
   }
 };
 
-template <int K>
-__device__ __forceinline__ void run_rows(const float (&a)[K], const float (&b)[K], uint32_t cuts, float& P, float& H) {
-  P = a[0];
-  H = b[0];
-#pragma unroll
-  for (int k = 1; k < K; ++k) {
-    P *= a[k];
-    H = (cuts >> k) & 1 ? b[k] : __builtin_fmaf(a[k], H, b[k]);
-  }
-  if (cuts) P = kCut;
-}
-
 template <typename InT, int DECAY, int MIX, bool IN, bool Z, int W, int K>
 __global__ __launch_bounds__(kLanes * W) void glr_walk(const GlrArgs g) {
   __shared__ float2 pairs[2][W][kLanes];
@@ -92,12 +80,13 @@ __global__ __launch_bounds__(kLanes * W) void glr_walk(const GlrArgs g) {
         b[k] = k < rows ? b[k] : 0.0f;
       }
     }
-    float P, H;
+    float P = 1.0f, H = 0.0f, none = 0.0f;
+    bool cut = false;
     if (cuts)
-      run_rows<K>(a, b, cuts, P, H);
+      run_rows<false, false, K>(a, b, b, K, cuts, P, H, none, cut);
     else
-      run_rows<K>(a, b, 0, P, H);
-    pairs[buf][w][lane] = make_float2(P, H);
+      run_rows<true, false, K>(a, b, b, K, 0, P, H, none, cut);
+    pairs[buf][w][lane] = make_float2(cut ? kCut : P, H);
     __syncthreads();
     float mine = h;
     if (g.reset) {
@@ -132,7 +121,7 @@ __global__ __launch_bounds__(kLanes * W) void glr_walk(const GlrArgs g) {
 #pragma unroll
       for (int k = 0; k < K; ++k) b[k] *= gate[k];
     }
-    if (on && rows > 0) store_rows<K>(g.out, row0 + t, g.D, rows, ch, g.out_bf16, b);
+    if (on && rows > 0) store_rows<false, K>(g.out, row0 + t, g.D, rows, ch, g.out_bf16, b);
   }
   if (g.h_last && piece == g.pieces - 1 && w == 0 && on) g.h_last[state] = h;
 }
@@ -167,7 +156,7 @@ __global__ __launch_bounds__(kLanes) void glr_steps(const GlrArgs g) {
         h = (cuts >> k) & 1 ? b[k] : __builtin_fmaf(a[k], h, b[k]);
         b[k] = Z ? h * gate[k] : h;
       }
-    if (on) store_rows<K>(g.out, row0 + t, g.D, rows, ch, g.out_bf16, b);
+    if (on) store_rows<false, K>(g.out, row0 + t, g.D, rows, ch, g.out_bf16, b);
   }
   if (g.h_last && on) g.h_last[state] = h;
 }
@@ -223,7 +212,7 @@ GlrPieces plan_glr(int64_t B, int64_t L, int64_t D, int requested) {
   if (requested > 0)
     pieces = requested;
   else if (groups < 128 && tiles >= 8)
-    pieces = 2048 / groups;
+    pieces = 1024 / groups;
   pieces = pieces < tiles ? pieces : tiles;
   if (pieces < 1) pieces = 1;
   p.rows = (tiles + pieces - 1) / pieces * kTile;

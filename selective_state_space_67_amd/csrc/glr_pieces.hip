@@ -5,79 +5,87 @@
 // adjoint m that enters it from behind to P m + G, with P the product of its
 // decays and
 //   H = the state it leaves from zero,   G = sum_t (prod_{r <= t} a_r) dout_t silu(z_t)
-// One wave makes a piece's three values for 64 channels; the fold runs the same
-// scheme over the pieces that the walk runs over rows.
+// A workgroup makes a piece's three values for 64 channels, its waves those of
+// equal parts of the rows; the fold runs the same scheme over the pieces that the
+// walk runs over rows.
 #include "glr_device.h"
 #include "glr_launch.h"
 
 namespace ssm {
 namespace {
 
-constexpr int kAggWaves = 4, kAggRows = 8;
+constexpr int kAggWaves = 8, kAggRows = 8;
 constexpr int kFoldWaves = 16, kFoldRows = 8;
 
-template <typename InT, int DECAY, int MIX, bool IN, bool Z, bool BWD, int K>
-__global__ __launch_bounds__(kAggWaves * kLanes) void glr_aggregate(const GlrArgs g, const int64_t count,
-                                                                    const int64_t waves) {
+template <typename InT, int DECAY, int MIX, bool IN, bool Z, bool BWD, int W, int K>
+__global__ __launch_bounds__(W * kLanes) void glr_aggregate(const GlrArgs g, const int count) {
+  __shared__ float ex[3][W][kLanes];
   const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
-  const int64_t wave = static_cast<int64_t>(blockIdx.x) * kAggWaves + w;
-  if (wave >= waves) return;
-  const int tile = static_cast<int>(wave % g.tiles);
-  const int64_t rest = wave / g.tiles, piece = rest % count, batch = rest / count;
+  const int tile = blockIdx.x % g.tiles, rest = blockIdx.x / g.tiles;
+  const int piece = rest % count, batch = rest / count;
   const int channel = tile * kLanes + lane, ch = min(channel, g.D - 1);
   const uint32_t at = static_cast<uint32_t>(ch) * sizeof(InT);
-  const int64_t row0 = batch * g.L, begin = piece * g.piece_rows, end = min(g.L, begin + g.piece_rows);
-  uint32_t u[K], dt[K], in[K], z[K], dy[K], reset;
-  auto load = [&](int64_t t) {
-    const int rows = static_cast<int>(min(int64_t{K}, end - t));
-    load_rows<InT, K>(g.dt, row0 + t, g.ds, rows, at, dt);
-    if (IN) load_rows<InT, K>(g.in, row0 + t, g.is, rows, at, in);
-    load_rows<InT, K>(g.u, row0 + t, g.us, rows, at, u);
-    if (BWD && Z) load_rows<InT, K>(g.z, row0 + t, g.zs, rows, at, z);
-    if (BWD) load_rows<InT, K>(g.dout, row0 + t, g.D, rows, at, dy);
-    reset = reset_byte<K>(g.reset, row0 + t, rows, lane);
-  };
-  load(begin);
+  const int64_t row0 = batch * g.L;
+  // the wave's rows (a piece has a multiple of W K; the last one's waves may have none)
+  const int part = static_cast<int>(g.piece_rows) / W;
+  const int begin = static_cast<int>(piece * g.piece_rows) + w * part;
+  const int end = min(static_cast<int>(g.L), begin + part);
   const Channel<DECAY> c(g, ch);
   float P = 1.0f, H = 0.0f, G = 0.0f;
   bool cut = false;
-  for (int64_t t = begin; t < end; t += K) {
-    const int rows = static_cast<int>(min(int64_t{K}, end - t));
+  uint32_t u[K], dt[K], in[K], z[K], rdy[K], reset;
+  auto load = [&](int t) {
+    const int rows = min(K, end - t);
+    load_rows<InT, K>(g.dt, row0 + t, g.ds, rows, at, dt);
+    if (IN) load_rows<InT, K>(g.in, row0 + t, g.is, rows, at, in);
+    load_rows<InT, K>(g.u, row0 + t, g.us, rows, at, u);
+    if (BWD) load_rows<InT, K>(g.dout, row0 + t, g.D, rows, at, rdy);
+    if (BWD && Z) load_rows<InT, K>(g.z, row0 + t, g.zs, rows, at, z);
+    reset = reset_byte<K>(g.reset, row0 + t, rows, lane);
+  };
+  if (begin < end) load(begin);
+  for (int t = begin; t < end; t += K) {
+    const int rows = min(K, end - t);
     const uint32_t cuts = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(reset != 0));
-    float a[K], b[K], y[K];
+    float a[K], b[K], dy[K];
     terms<InT, DECAY, MIX, IN, K>(c, u, dt, in, cuts, a, b);
     if (BWD) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) y[k] = Z ? widen<InT>(dy[k]) * silu_f32(widen<InT>(z[k])) : widen<InT>(dy[k]);
+      for (int k = 0; k < K; ++k) dy[k] = Z ? widen<InT>(rdy[k]) * silu_f32(widen<InT>(z[k])) : widen<InT>(rdy[k]);
     }
     if (t + K < end) load(t + K);
-    if (rows == K && cuts == 0) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        P *= a[k];
-        H = __builtin_fmaf(a[k], H, b[k]);
-        if (BWD && !cut) G = __builtin_fmaf(P, y[k], G);
-      }
-    } else {
-      keep_branch();
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (k < rows) {
-          const bool here = (cuts >> k) & 1;
-          cut |= here;
-          P *= a[k];
-          H = here ? b[k] : __builtin_fmaf(a[k], H, b[k]);
-          // what lies behind a document's start is out of the adjoint's sight
-          if (BWD && !cut) G = __builtin_fmaf(P, y[k], G);
-        }
-      }
-    }
+    if (rows == K && cuts == 0 && !cut)
+      run_rows<true, BWD, K>(a, b, dy, K, 0, P, H, G, cut);
+    else
+      run_rows<false, BWD, K>(a, b, dy, rows, cuts, P, H, G, cut);
   }
-  if (channel >= g.D) return;
-  const int64_t to = (batch * g.pieces + piece) * g.D + ch;
-  g.P[to] = cut ? kCut : P;
-  g.H[to] = H;
-  if (BWD) g.G[to] = G;
+  ex[0][w][lane] = cut ? kCut : P;
+  ex[1][w][lane] = H;
+  if (BWD) ex[2][w][lane] = G;
+  __syncthreads();
+  if (w >= (BWD ? 3 : 2) || channel >= g.D) return;
+  // wave 0 joins the P, wave 1 the H, wave 2 the G
+  const int64_t to = (static_cast<int64_t>(batch) * g.pieces + piece) * g.D + ch;
+  if (w == 0) {
+    P = 1.0f;
+    cut = false;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      cut |= __float_as_int(ex[0][i][lane]) < 0;
+      P *= ex[0][i][lane];
+    }
+    g.P[to] = cut ? kCut : P;
+  } else if (w == 1) {
+    H = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) H = through(ex[0][i][lane], ex[1][i][lane], H);
+    g.H[to] = H;
+  } else {
+    G = 0.0f;
+#pragma unroll
+    for (int i = W - 1; i >= 0; --i) G = through(ex[0][i][lane], ex[2][i][lane], G);
+    g.G[to] = G;
+  }
 }
 
 // States entering the pieces (forward: from h0 on), or adjoints entering them from
@@ -148,14 +156,13 @@ __global__ __launch_bounds__(kFoldWaves * kLanes) void glr_fold(const GlrArgs g,
 
 struct Aggregate {
   template <typename InT, int DECAY, int MIX, bool IN, bool Z>
-  static hipError_t run(unsigned blocks, const GlrArgs& g, int64_t count, int64_t waves, bool backward,
-                        hipStream_t stream) {
+  static hipError_t run(unsigned blocks, const GlrArgs& g, int count, bool backward, hipStream_t stream) {
     if (backward)
-      hipLaunchKernelGGL((glr_aggregate<InT, DECAY, MIX, IN, Z, true, kAggRows>), dim3(blocks),
-                         dim3(kAggWaves * kLanes), 0, stream, g, count, waves);
+      hipLaunchKernelGGL((glr_aggregate<InT, DECAY, MIX, IN, Z, true, kGlrBwdWaves, kAggRows>), dim3(blocks),
+                         dim3(kGlrBwdWaves * kLanes), 0, stream, g, count);
     else
-      hipLaunchKernelGGL((glr_aggregate<InT, DECAY, MIX, IN, false, false, kAggRows>), dim3(blocks),
-                         dim3(kAggWaves * kLanes), 0, stream, g, count, waves);
+      hipLaunchKernelGGL((glr_aggregate<InT, DECAY, MIX, IN, false, false, kAggWaves, kAggRows>), dim3(blocks),
+                         dim3(kAggWaves * kLanes), 0, stream, g, count);
     return hipGetLastError();
   }
 };
@@ -212,11 +219,10 @@ bool glr_grids_fit(int64_t B, int64_t D, const GlrPieces& p) {
 
 hipError_t launch_glr_aggregates(const GlrPlan& plan, const GlrArgs& g, int64_t count, bool backward,
                                  hipStream_t stream) {
-  const int64_t waves = plan.B * count * g.tiles;
-  const unsigned blocks = static_cast<unsigned>((waves + kAggWaves - 1) / kAggWaves);
+  const unsigned blocks = static_cast<unsigned>(plan.B * count * g.tiles);
   SSM_LOG("launch glr_aggregate: %lld pieces; grid %u x %d threads", static_cast<long long>(count), blocks,
-          kAggWaves * kLanes);
-  return glr_pick<Aggregate>(plan, blocks, g, count, waves, backward, stream);
+          (backward ? kGlrBwdWaves : kAggWaves) * kLanes);
+  return glr_pick<Aggregate>(plan, blocks, g, static_cast<int>(count), backward, stream);
 }
 
 hipError_t launch_glr_fold(const GlrPlan& plan, const GlrArgs& g, int64_t count, bool backward, hipStream_t stream) {

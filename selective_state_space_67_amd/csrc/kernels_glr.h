@@ -68,7 +68,8 @@ hipError_t launch_glr(const GlrPlan& plan, const GlrPieces& pieces, void* worksp
 hipError_t launch_glr_steps(const GlrPlan& plan, hipStream_t stream);
 hipError_t launch_glr_bwd(const GlrPlan& plan, const GlrPieces& pieces, void* workspace, hipStream_t stream);
 
-// Between the kernels' files.
+// Between the kernels' files. A piece of the backward is 8 rows for each of this many waves.
+constexpr int kGlrBwdWaves = 4;
 struct GlrArgs;
 GlrArgs glr_args(const GlrPlan& plan, const GlrPieces& pieces, void* workspace);
 // P and H (and G) of the first `count` pieces of every batch row.
