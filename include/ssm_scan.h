@@ -674,10 +674,9 @@ ssm_status ssm_qk_norm_bwd(const ssm_qk_norm_params* p, void* hip_stream);
  *   reset    (B,L) uint8, NULL => none; h0 (B,D) float32, NULL => 0
  * ssm_glr_fwd:
  *   out      (B,L,D) required, dense, out_dtype; h_last (B,D) float32, NULL => not written
- *   num_segments : 0 = the library chooses how many pieces to split L into;
- *            k >= 1 asks for k pieces (clamped to what L allows).
  *   workspace, workspace_bytes : at least ssm_glr_workspace_size() bytes, aligned to
- *            256 (none for an unsplit sequence); contents on entry ignored.
+ *            256 (none where batch rows and channels fill the device by themselves);
+ *            contents on entry ignored. Calls that may run at the same time need one each.
  * ssm_glr_bwd, gradients of  loss = sum dout * out + sum dh_last * h_last  for the
  * same inputs (no intermediate of the forward is needed). With lam_t the adjoint of h_t:
  *   dy = dout silu(z),  dz = dout h silu'(z),  lam_t = dy_t + a_{t+1} lam_{t+1}
@@ -691,7 +690,7 @@ ssm_status ssm_qk_norm_bwd(const ssm_qk_norm_params* p, void* hip_stream);
  *   dA       (D) float32, required; d_dt_bias, din_bias (D), dh0 (B,D) float32, NULL => not
  *            written. Sums go in a fixed order: repeated calls give identical bits.
  *   workspace, workspace_bytes : at least ssm_glr_bwd_workspace_size() bytes, aligned to
- *            256: 32 bytes for every 32 steps of a channel. num_segments is not read.
+ *            256: 32 bytes for every 32 steps of a channel.
  * Arithmetic is float32 whatever in_dtype is; only results are rounded. Outputs must not
  * overlap inputs, each other or the workspace. A non-finite input stays within its
  * channel and document (the sums over tokens aside).
@@ -728,12 +727,9 @@ typedef struct {
   size_t workspace_bytes;
   int32_t decay; /* ssm_glr_decay */
   int32_t mix;   /* ssm_glr_mix */
-  int32_t num_segments;
-  int32_t reserved0; /* set to 0 */
 } ssm_glr_params;
 
-/* Bytes of workspace ssm_glr_fwd needs (sizes, dtypes and num_segments are read;
- * pointers are not). */
+/* Bytes of workspace ssm_glr_fwd needs (sizes and dtypes are read; pointers are not). */
 ssm_status ssm_glr_workspace_size(const ssm_glr_params* p, size_t* bytes);
 
 /* Enqueue the whole-sequence recurrence described by `p` on `hip_stream`. */

@@ -36,8 +36,7 @@ class GlrParams(ctypes.Structure):
     _fields_ = [("batch", _i64), ("seqlen", _i64), ("dim", _i64), ("in_dtype", _i32), ("out_dtype", _i32)] + _INPUTS + [
         ("reset", _vp), ("h0", _vp), ("out", _vp), ("h_last", _vp), ("dout", _vp), ("dh_last", _vp), ("du", _vp),
         ("d_dt_raw", _vp), ("din_raw", _vp), ("dz", _vp), ("dA", _vp), ("d_dt_bias", _vp), ("din_bias", _vp),
-        ("dh0", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("decay", _i32), ("mix", _i32),
-        ("num_segments", _i32), ("reserved0", _i32)]
+        ("dh0", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("decay", _i32), ("mix", _i32)]
 
 
 class GlrUpdateParams(ctypes.Structure):
@@ -188,7 +187,7 @@ _NO_GRADS = (0,) * 10
 
 
 def ssm_glr_fwd(u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=None, z=None, reset=None, h0=None, out=None,
-                h_last=None, out_dtype=None, decay="sigmoid", mix="unit", num_segments=0, workspace=None, stream=None):
+                h_last=None, out_dtype=None, decay="sigmoid", mix="unit", workspace=None, stream=None):
     """Gated linear recurrence over the whole sequence; returns ``out`` (B, L, D).
 
     u, dt_raw, in_raw, z: (B, L, D) float32 or bfloat16 (the last two optional); A,
@@ -210,9 +209,9 @@ def ssm_glr_fwd(u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=None, z=None
     _one_device(u, dt_raw, A, dt_bias, in_raw, in_bias, z, reset, h0, out, h_last, workspace)
     head = (*sizes, _b._dtype_code(out), *fields, *_sequence(sizes, reset, h0), out.data_ptr(), _at(h_last), *_NO_GRADS)
     pack = _PACKED[8].pack
-    workspace, at, n = _space(lib.ssm_glr_workspace_size, pack(*head, 0, 0, *kinds, num_segments, 0), workspace,
+    workspace, at, n = _space(lib.ssm_glr_workspace_size, pack(*head, 0, 0, *kinds), workspace,
                               u.device, stream)
-    _call(lib.ssm_glr_fwd, pack(*head, at, n, *kinds, num_segments, 0), stream, u.device)
+    _call(lib.ssm_glr_fwd, pack(*head, at, n, *kinds), stream, u.device)
     return out
 
 
@@ -288,6 +287,6 @@ def ssm_glr_bwd(u, dt_raw, A, dout, *, dt_bias=None, in_raw=None, in_bias=None, 
     head = (*sizes, _b._dtype_code(g["du"]), *fields, *_sequence(sizes, reset, h0), 0, 0, dout.data_ptr(), _at(dh_last),
             *[_at(t) for t in g.values()])
     pack = _PACKED[8].pack
-    workspace, at, n = _space(lib.ssm_glr_bwd_workspace_size, pack(*head, 0, 0, *kinds, 0, 0), workspace, dev, stream)
-    _call(lib.ssm_glr_bwd, pack(*head, at, n, *kinds, 0, 0), stream, dev)
+    workspace, at, n = _space(lib.ssm_glr_bwd_workspace_size, pack(*head, 0, 0, *kinds), workspace, dev, stream)
+    _call(lib.ssm_glr_bwd, pack(*head, at, n, *kinds), stream, dev)
     return g

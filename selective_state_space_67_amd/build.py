@@ -16,7 +16,7 @@ SOURCES = ["api.cpp", "scan_fwd.hip", "scan_fwd_f32_plain.hip", "scan_fwd_f32_re
            "scan_fwd_bf16_reset.hip", "scan_fwd_n16.hip", "scan_fwd_wavefront.hip", "scan_bwd.hip", "state_update.hip",
            "scan_cplx.hip", "scan_cplx_bwd.hip", "fill.hip", "scan_noalloc.hip", "scan_limits.hip", "api_delta.cpp",
            "delta_step.hip", "delta_chunk.hip", "delta_walk_bf16_direct.hip", "delta_walk_bf16.hip", "delta_walk_f32.hip",
-           "delta_chunk_bwd.hip", "qk_norm.hip", "api_glr.cpp", "glr_fwd.hip", "glr_pieces.hip", "glr_bwd.hip",
+           "delta_chunk_bwd.hip", "qk_norm.hip", "api_glr.cpp", "glr_fwd.hip", "glr_pieces.hip", "glr_chain.hip", "glr_bwd.hip",
            "api_block.cpp", "gated_norm.hip", "block_norm.hip", "row_sums.hip", "log.cpp"]
 OUT = os.path.join(HERE, "libssmscan.so")
 OBJ = os.path.join(ROOT, "_build")

@@ -1,7 +1,7 @@
 // C-ABI front end of the gated linear recurrence (include/ssm_scan.h). As in
 // api.cpp, every check is host arithmetic on the parameter struct and precedes
-// the first HIP call. The launches live in glr_fwd.hip, glr_pieces.hip and
-// glr_bwd.hip.
+// the first HIP call. The launches live in glr_fwd.hip, glr_chain.hip,
+// glr_pieces.hip and glr_bwd.hip.
 #include <hip/hip_runtime.h>
 
 #include "api_checks.h"
@@ -68,14 +68,12 @@ ssm_status check_glr_sizes(const P* p, int64_t len, GlrSizes* s) {
 
 ssm_status no_grid() { return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows"); }
 
-// How the forward runs: step by step (no pieces) or as a walk over pieces.
+// How the forward runs: step by step (no pieces), as one walk or in pieces.
 ssm_status plan_fwd(const ssm_glr_params* p, const GlrSizes& s, ssm::GlrPieces* pieces) {
-  if (p->num_segments < 0) return fail(SSM_ERR_BAD_SHAPE, "num_segments must be >= 0");
   *pieces = ssm::GlrPieces{};
   if (s.empty()) return SSM_OK;
-  if (ssm::glr_by_steps(p->seqlen) && p->num_segments <= 1)
-    return ssm::glr_steps_fit(p->batch, p->dim) ? SSM_OK : no_grid();
-  *pieces = ssm::plan_glr(p->batch, p->seqlen, p->dim, p->num_segments);
+  if (ssm::glr_by_steps(p->seqlen)) return ssm::glr_steps_fit(p->batch, p->dim) ? SSM_OK : no_grid();
+  *pieces = ssm::plan_glr(p->batch, p->seqlen, p->dim);
   return ssm::glr_grids_fit(p->batch, p->dim, *pieces) ? SSM_OK : no_grid();
 }
 

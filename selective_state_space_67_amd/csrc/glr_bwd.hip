@@ -191,7 +191,6 @@ GlrPieces plan_glr_bwd(int64_t B, int64_t L, int64_t D) {
   GlrPieces p{};
   p.rows = kPiece;
   p.waves = kGlrBwdWaves;
-  p.ways = 2;
   p.pieces = (L + kPiece - 1) / kPiece;
   const size_t each = (static_cast<size_t>(B) * p.pieces * D * sizeof(float) + 255) / 256 * 256;
   p.off_H = each;
@@ -204,9 +203,17 @@ GlrPieces plan_glr_bwd(int64_t B, int64_t L, int64_t D) {
 }
 
 hipError_t launch_glr_bwd(const GlrPlan& plan, const GlrPieces& pieces, void* workspace, hipStream_t stream) {
-  const GlrArgs g = glr_args(plan, pieces, workspace);
-  hipError_t e = launch_glr_aggregates(plan, g, pieces.pieces, true, stream);
-  if (e == hipSuccess) e = launch_glr_fold(plan, g, pieces.pieces, true, stream);
+  GlrArgs g = glr_args(plan);
+  char* ws = static_cast<char*>(workspace);
+  g.pieces = static_cast<int>(pieces.pieces);
+  g.P = reinterpret_cast<float*>(ws + pieces.off_P);
+  g.H = reinterpret_cast<float*>(ws + pieces.off_H);
+  g.G = reinterpret_cast<float*>(ws + pieces.off_G);
+  g.starts = reinterpret_cast<float*>(ws + pieces.off_starts);
+  g.ends = reinterpret_cast<float*>(ws + pieces.off_ends);
+  g.part = reinterpret_cast<float*>(ws + pieces.off_part);
+  hipError_t e = launch_glr_aggregates(plan, g, stream);
+  if (e == hipSuccess) e = launch_glr_fold(plan, g, stream);
   if (e != hipSuccess) return e;
   const unsigned blocks = static_cast<unsigned>(plan.B * pieces.pieces * g.tiles);
   SSM_LOG("launch glr_grads: %lld pieces of %d rows; grid %u x %d threads", static_cast<long long>(pieces.pieces),

@@ -1,5 +1,5 @@
 // Device code shared by the gated linear recurrence's kernels (glr_fwd.hip,
-// glr_pieces.hip, glr_bwd.hip): the arguments, a step's gates, decay and
+// glr_chain.hip, glr_pieces.hip, glr_bwd.hip): the arguments, a step's gates, decay and
 // multiplier, and rows of inputs as loaded.
 //
 //   s = sigmoid(dt_raw + dt_bias) or softplus(dt_raw + dt_bias)
@@ -23,8 +23,7 @@ constexpr int kLanes = 64;
 struct GlrArgs {
   int64_t L;
   int D, tiles;        // tiles: groups of 64 channels
-  int pieces;          // of the sequence, piece_rows each
-  int64_t piece_rows;
+  int pieces;          // of the sequence (backward)
   const void* u;
   const void* dt;
   const void* in;  // null: no input gate

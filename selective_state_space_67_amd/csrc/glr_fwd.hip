@@ -1,5 +1,6 @@
-// The gated linear recurrence forward: the walk over a sequence (or over one
-// piece of it), and the decode window.
+// The gated linear recurrence forward: the walk over a sequence, the decode
+// window, and when to take which (calls with few batch rows and channels go
+// through glr_chain.hip).
 //
 // The walk. A workgroup owns 64 channels and goes through its rows in tiles of
 // W K: each of its W waves takes K consecutive rows, works out their decays and
@@ -41,27 +42,22 @@ template <typename InT, int DECAY, int MIX, bool IN, bool Z, int W, int K>
 __global__ __launch_bounds__(kLanes * W) void glr_walk(const GlrArgs g) {
   __shared__ float2 pairs[2][W][kLanes];
   const int lane = threadIdx.x % kLanes, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kLanes);
-  const int tile = blockIdx.x % g.tiles, rest = blockIdx.x / g.tiles;
-  const int piece = rest % g.pieces, batch = rest / g.pieces;
+  const int tile = blockIdx.x % g.tiles, batch = blockIdx.x / g.tiles;
   const int channel = tile * kLanes + lane, ch = min(channel, g.D - 1);
   const bool on = channel < g.D;
   const uint32_t at = static_cast<uint32_t>(ch) * sizeof(InT);
   const int64_t state = static_cast<int64_t>(batch) * g.D + ch, row0 = batch * g.L;
-  // rows are counted in 32 bits (L < 2^27)
-  const int begin = static_cast<int>(piece * g.piece_rows);
-  const int end = static_cast<int>(min(g.L, begin + g.piece_rows));
+  const int end = static_cast<int>(g.L);  // rows are counted in 32 bits (L < 2^27)
   Channel<DECAY> c(g, ch);
-  float h = g.pieces > 1 ? g.starts[(static_cast<int64_t>(batch) * g.pieces + piece) * g.D + ch]
-            : g.h0       ? g.h0[state]
-                         : 0.0f;
+  float h = g.h0 ? g.h0[state] : 0.0f;
   Rows<InT, IN, Z, K> x;
-  x.load(g, row0, begin + w * K, end, lane, at);
+  x.load(g, row0, w * K, end, lane, at);
   arrived(h);
   arrived(c.A);
   arrived(c.dt);
   arrived(c.in);
   int buf = 0;
-  for (int t0 = begin; t0 < end; t0 += W * K, buf ^= 1) {
+  for (int t0 = 0; t0 < end; t0 += W * K, buf ^= 1) {
     const int t = t0 + w * K;
     const int rows = max(0, min(K, end - t));
     const uint32_t cuts = x.cuts();
@@ -123,7 +119,7 @@ __global__ __launch_bounds__(kLanes * W) void glr_walk(const GlrArgs g) {
     }
     if (on && rows > 0) store_rows<false, K>(g.out, row0 + t, g.D, rows, ch, g.out_bf16, b);
   }
-  if (g.h_last && piece == g.pieces - 1 && w == 0 && on) g.h_last[state] = h;
+  if (g.h_last && w == 0 && on) g.h_last[state] = h;
 }
 
 // One thread a channel, token by token; the next tokens are loaded ahead, K at a time.
@@ -163,19 +159,17 @@ __global__ __launch_bounds__(kLanes) void glr_steps(const GlrArgs g) {
 
 // Few workgroups, none of which shares its CU with another, take 16 rows a wave: with half the
 // barriers and folds an element their waves wait less (8 x 2048 x 1536 channels, 192 workgroups:
-// 65 us, with 8 rows 71; with 16 waves of 16 rows 63). Many take 8: 1 x 131072 x 256 in 512
-// pieces 58 us, with 16 rows 63, with 16 waves 81. So does what 8 rows a wave cover in a few tiles:
-// 1 x 37 x 1536 4.8 us, with 16 rows 6.7.
+// 65 us, with 8 rows 71; with 16 waves of 16 rows 63). Many take 8, and so does what 8 rows a
+// wave cover in a few tiles: 1 x 37 x 1536 4.8 us, with 16 rows 6.7.
 bool wide_tiles(int64_t blocks, int64_t rows) { return blocks <= 384 && rows >= 8 * kTile; }
 
 struct Walk {
   template <typename InT, int DECAY, int MIX, bool IN, bool Z>
   static hipError_t run(const GlrPlan& plan, const GlrArgs& g, hipStream_t stream) {
-    const int64_t blocks = plan.B * g.pieces * g.tiles;
-    const bool wide = wide_tiles(blocks, g.piece_rows);
-    SSM_LOG("launch glr_walk<%d waves of %d rows>: %d pieces of %lld rows; grid %lld x %d threads", kWaves,
-            wide ? 2 * kRows : kRows, g.pieces, static_cast<long long>(g.piece_rows), static_cast<long long>(blocks),
-            kWaves * kLanes);
+    const int64_t blocks = plan.B * g.tiles;
+    const bool wide = wide_tiles(blocks, g.L);
+    SSM_LOG("launch glr_walk<%d waves of %d rows>: grid %lld x %d threads", kWaves, wide ? 2 * kRows : kRows,
+            static_cast<long long>(blocks), kWaves * kLanes);
     const dim3 grid(static_cast<unsigned>(blocks)), block(kWaves * kLanes);
     if (wide)
       hipLaunchKernelGGL((glr_walk<InT, DECAY, MIX, IN, Z, kWaves, 2 * kRows>), grid, block, 0, stream, g);
@@ -205,48 +199,64 @@ bool glr_by_steps(int64_t L) { return L <= 8; }
 
 bool glr_steps_fit(int64_t B, int64_t D) { return fits_launch(B * tiles_of(D), kLanes); }
 
-GlrPieces plan_glr(int64_t B, int64_t L, int64_t D, int requested) {
+// The walk gives 64 channels of a batch row to one workgroup, in rounds of one for every CU: 30 ns a
+// row and round, however little of the chip a round fills. The chain fills it whatever the shape
+// is (0.119 ns a row and 64 channels), for a launch and a workspace more. It is taken where that
+// saves 7 us. us of walk and chain, bfloat16 with the sigmoid gates: 1 x 256 x 256 channels 14.0 and
+// 18.3, 1 x 2048 x 1536 65 (by its 30 ns a row) and 18.7, 2 x 4096 x 2048 121 and 41; 8 x 512 x 1536 18.8
+// and 20.5, 8 x 1024 x 1536 34.7 and 32.5, 8 x 2048 x 1536 64.4 and 55.8; 8 x 2048 x 2048 (256
+// workgroups) 68.5 and 71.5; 16 x 2048 x 1280 (320) 121 and 85; 16 x 1024 x 2048 (512) 68.6 and 75.6.
+GlrPieces plan_glr(int64_t B, int64_t L, int64_t D) {
+  const int64_t groups = B * tiles_of(D), rounds = (groups + 255) / 256;
+  if (groups < int64_t{1} << 22 && (30000 * rounds - 119 * groups) * L >= 7000000) return plan_glr_chain(B, L, D);
   GlrPieces p{};
-  const int64_t tiles = (L + kTile - 1) / kTile, groups = B * tiles_of(D);
-  int64_t pieces = 1;
-  if (requested > 0)
-    pieces = requested;
-  else if (groups < 128 && tiles >= 8)
-    pieces = 1024 / groups;
-  pieces = pieces < tiles ? pieces : tiles;
-  if (pieces < 1) pieces = 1;
-  p.rows = (tiles + pieces - 1) / pieces * kTile;
-  p.pieces = (L + p.rows - 1) / p.rows;
+  p.pieces = 1;
+  p.rows = L;
   p.waves = kWaves;
-  p.ways = p.pieces > 1 ? 1 : 0;
-  if (p.pieces > 1) {
-    const size_t each = (static_cast<size_t>(B) * p.pieces * D * sizeof(float) + 255) / 256 * 256;
-    p.off_P = 0;
-    p.off_H = each;
-    p.off_starts = 2 * each;
-    p.bytes = 3 * each;
-  }
   return p;
 }
 
 hipError_t launch_glr(const GlrPlan& plan, const GlrPieces& pieces, void* workspace, hipStream_t stream) {
-  const GlrArgs g = glr_args(plan, pieces, workspace);
-  if (pieces.pieces > 1) {
-    hipError_t e = launch_glr_aggregates(plan, g, pieces.pieces - 1, false, stream);
-    if (e == hipSuccess) e = launch_glr_fold(plan, g, pieces.pieces - 1, false, stream);
-    if (e != hipSuccess) return e;
-  }
-  return glr_pick<Walk>(plan, plan, g, stream);
+  if (pieces.pieces > 1) return launch_glr_chain(plan, pieces, workspace, stream);
+  return glr_pick<Walk>(plan, plan, glr_args(plan), stream);
 }
 
 hipError_t launch_glr_steps(const GlrPlan& plan, hipStream_t stream) {
-  GlrPieces one{};
-  one.pieces = 1;
-  one.rows = plan.L;
-  const GlrArgs g = glr_args(plan, one, nullptr);
+  const GlrArgs g = glr_args(plan);
   const unsigned blocks = static_cast<unsigned>(plan.B * g.tiles);
   SSM_LOG("launch glr_steps: grid %u x %d threads", blocks, kLanes);
   return glr_pick<Steps>(plan, blocks, g, stream);
+}
+
+GlrArgs glr_args(const GlrPlan& p) {
+  GlrArgs g{};
+  g.L = p.L;
+  g.D = static_cast<int>(p.D);
+  g.tiles = static_cast<int>(tiles_of(p.D));
+  g.u = p.u;
+  g.dt = p.dt;
+  g.in = p.in;
+  g.z = p.z;
+  g.us = p.us;
+  g.ds = p.ds;
+  g.is = p.is;
+  g.zs = p.zs;
+  g.A = p.A;
+  g.dt_bias = p.dt_bias;
+  g.in_bias = p.in_bias;
+  g.reset = p.reset;
+  g.h0 = p.h0;
+  g.out = p.out;
+  g.h_last = p.h_last;
+  g.out_bf16 = p.out_bf16;
+  g.dout = p.dout;
+  g.dh_last = p.dh_last;
+  g.du = p.du;
+  g.d_dt = p.d_dt;
+  g.d_in = p.d_in;
+  g.dz = p.dz;
+  g.dh0 = p.dh0;
+  return g;
 }
 
 }  // namespace ssm

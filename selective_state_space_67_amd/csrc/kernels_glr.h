@@ -1,5 +1,6 @@
 // Host-side interface between the front end of the gated linear recurrence
-// (api_glr.cpp) and its kernels (glr_fwd.hip, glr_pieces.hip, glr_bwd.hip). Not
+// (api_glr.cpp) and its kernels (glr_fwd.hip, glr_chain.hip, glr_pieces.hip,
+// glr_bwd.hip). Not
 // installed; not part of the ABI.
 #pragma once
 
@@ -50,13 +51,12 @@ struct GlrPlan {
 
 // How a sequence is cut into pieces, and where the workspace holds what joins them.
 struct GlrPieces {
-  int64_t pieces, rows;  // rows of a piece; forward, pieces = 1: a single walk, no workspace
+  int64_t pieces, rows;  // rows of a piece; forward, pieces = 1: one walk from end to end, no workspace
   int waves;             // of a workgroup that takes a piece of 64 channels
-  int ways;              // in which the pieces are folded: states (1), adjoints too (2)
   size_t off_P, off_H, off_G, off_starts, off_ends, off_part, bytes;
 };
-// requested = 0: automatic. Pure host arithmetic, like the others here.
-GlrPieces plan_glr(int64_t B, int64_t L, int64_t D, int requested);
+// Pure host arithmetic, like the others here.
+GlrPieces plan_glr(int64_t B, int64_t L, int64_t D);
 GlrPieces plan_glr_bwd(int64_t B, int64_t L, int64_t D);
 // Whether every launch of a call stays below 2^32 threads.
 bool glr_grids_fit(int64_t B, int64_t D, const GlrPieces& pieces);
@@ -68,14 +68,15 @@ hipError_t launch_glr(const GlrPlan& plan, const GlrPieces& pieces, void* worksp
 hipError_t launch_glr_steps(const GlrPlan& plan, hipStream_t stream);
 hipError_t launch_glr_bwd(const GlrPlan& plan, const GlrPieces& pieces, void* workspace, hipStream_t stream);
 
-// Between the kernels' files. A piece of the backward is 8 rows for each of this many waves.
-constexpr int kGlrBwdWaves = 4;
+// Between the kernels' files: the forward in pieces that follow each other on the chip
+// (glr_chain.hip), and the backward's first two passes (glr_pieces.hip).
+GlrPieces plan_glr_chain(int64_t B, int64_t L, int64_t D);
+hipError_t launch_glr_chain(const GlrPlan& plan, const GlrPieces& pieces, void* workspace, hipStream_t stream);
 struct GlrArgs;
-GlrArgs glr_args(const GlrPlan& plan, const GlrPieces& pieces, void* workspace);
-// P and H (and G) of the first `count` pieces of every batch row.
-hipError_t launch_glr_aggregates(const GlrPlan& plan, const GlrArgs& args, int64_t count, bool backward,
-                                 hipStream_t stream);
-// The states entering the pieces from h0, and for the backward the adjoints from dh_last (and dh0).
-hipError_t launch_glr_fold(const GlrPlan& plan, const GlrArgs& args, int64_t count, bool backward, hipStream_t stream);
+GlrArgs glr_args(const GlrPlan& plan);
+hipError_t launch_glr_aggregates(const GlrPlan& plan, const GlrArgs& args, hipStream_t stream);
+hipError_t launch_glr_fold(const GlrPlan& plan, const GlrArgs& args, hipStream_t stream);
+// A piece of the backward is 8 rows for each of this many waves.
+constexpr int kGlrBwdWaves = 4;
 
 }  // namespace ssm

@@ -81,17 +81,21 @@ def test_kinds(decay, mix, gate, z):
         compare_bwd(x, t, decay, mix, False)
 
 
-@pytest.mark.parametrize("L,D,pieces", [(129, 64, 2), (1000, 3, 3), (1000, 130, 7), (2049, 65, 100), (70000, 64, 0), (40000, 1, 300)])
-def test_pieces(L, D, pieces):
-    """A split sequence, with documents that start inside pieces and at their ends."""
-    x = glr_inputs(1, L, D, wl.F32, seed=L + D, z=True, state=True, resets=[(0, 128), (0, 255), (0, 700), (0, 896)])
+# lengths at the ends of pieces (64 rows), of groups of them (1024) and of ranges of groups (16384)
+@pytest.mark.parametrize("L,D", [(256, 64), (300, 3), (1000, 130), (1024, 64), (1025, 65), (2049, 65), (16384, 3), (16385, 64),
+                                 (70000, 64), (40000, 1)])
+@pytest.mark.parametrize("cuts", [False, True])
+def test_pieces(L, D, cuts):
+    """Few channels, so that a sequence goes in pieces, with and without documents that start inside them and at their ends."""
+    resets = [(0, 64), (0, 127), (0, 700), (0, 896), (0, 1023), (0, 20000), (0, 32768)] if cuts else None
+    x = glr_inputs(1, L, D, wl.F32, seed=L + D, z=True, state=True, resets=resets)
     t = on_device(x, device())
-    print(L, D, pieces, flush=True)
-    out, last = forward(x, t, "sigmoid", "unit", num_segments=pieces)
+    print(L, D, cuts, flush=True)
+    out, last = forward(x, t, "sigmoid", "unit")
     ref, rh = og.glr_fwd(**wide(x))
     check(out, ref, STATE, "out")
     check(last, rh, STATE, "h_last")
-    if L <= 2049 or D == 1:
+    if L <= 2049 or D <= 3:
         compare_bwd(x, t, "sigmoid", "unit", False)
 
 
@@ -184,19 +188,19 @@ def test_a_non_finite_input_stays_in_its_channel_and_document(name, bad):
 
     from selective_state_space_67_amd import ssm_glr_bwd
 
-    cuts = [70, 71, 140, 290]
-    B, L, D, at = 2, 400, 66, 100
-    for pieces in (1, 3):
+    cuts = [70, 71, 140, 160]
+    B, D, at = 2, 66, 100
+    for L in (200, 400):  # a walk, and pieces
         x = glr_inputs(B, L, D, wl.F32, seed=3, z=True, state=True, resets=[(b, c) for b in range(B) for c in cuts])
         t = on_device(x, device())
-        clean, clean_last = forward(x, t, "sigmoid", "unit", num_segments=pieces)
+        clean, clean_last = forward(x, t, "sigmoid", "unit")
         a, k = call(t)
         kw = dict(reset=t["reset"], h0=t["h0"], dh_last=t["dh_last"], **k)
         g0 = ssm_glr_bwd(*a, t["dout"], **kw)
         where = {"h0": (0, 5), "dh_last": (0, 5)}.get(name, (0, at, 5))
         t[name][where] = bad
-        lo, hi = {"h0": (0, 70), "dh_last": (290, L)}.get(name, (71, 140))
-        out, last = forward(x, t, "sigmoid", "unit", num_segments=pieces)
+        lo, hi = {"h0": (0, 70), "dh_last": (160, L)}.get(name, (71, 140))
+        out, last = forward(x, t, "sigmoid", "unit")
         g = ssm_glr_bwd(*a, t["dout"], **kw)
         torch.cuda.synchronize()
         mask = torch.ones((B, L, D), dtype=torch.bool, device=device())
