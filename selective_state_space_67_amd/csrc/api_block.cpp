@@ -122,7 +122,7 @@ ssm_status check_block(const ssm_block_norm_params* p, BlockSizes* s) {
   if (!p->gate_rows) s->gate = p->dim;
   // a gate for each sequence: a workgroup of up to 1024 threads at least for each
   if (p->gate_rows && !s->empty() &&
-      (!fits_launch(p->batch, 1024) || !fits_launch(p->batch * ((p->dim + 15) / 16), 256)))
+      (!fits_launch(p->batch, 1024) || !fits_launch(p->batch * ((p->dim + 15) / 16), 1024)))
     return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
   return SSM_OK;
 }

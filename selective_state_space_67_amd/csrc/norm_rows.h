@@ -256,10 +256,23 @@ hipError_t pick_team(bool runs, int size, int64_t rows, X&&... x) {
     if (size <= 8192) return F::template run<8, 0, 1, 1024>(whole(8), std::forward<X>(x)...);
     return F::template run<8, 0, 2, 1024>(whole(16), std::forward<X>(x)...);
   }
+  if (size <= 32) return F::template run<1, 8, 4, 256>(several(8), std::forward<X>(x)...);
+  if (size <= 64) return F::template run<1, 16, 4, 256>(several(16), std::forward<X>(x)...);
+  if (size <= 128) return F::template run<1, 32, 4, 256>(several(32), std::forward<X>(x)...);
   if (size <= 256) return F::template run<1, 64, 4, 256>(several(64), std::forward<X>(x)...);
+  if (size <= 512) return F::template run<1, 64, 8, 256>(several(64), std::forward<X>(x)...);
   if (size <= 4096) return F::template run<1, 0, 8, 512>(whole(8), std::forward<X>(x)...);
+  if (size <= 8192) return F::template run<1, 0, 8, 1024>(whole(8), std::forward<X>(x)...);
   return F::template run<1, 0, 16, 1024>(whole(16), std::forward<X>(x)...);
 }
+
+// What a lane's registers hold besides a row: the next one's elements unless its runs are long or
+// (a kernel with many rows of sums) its workgroup so large that it has no more than 128 registers,
+// and the weights unless its runs are long.
+template <int V, int NV, int MOST, bool MANY>
+struct Holds {
+  static constexpr bool kAhead = V * NV <= 8 && (!MANY || MOST <= 512), kWeights = V * NV <= 8;
+};
 
 // Threads that go through the rows: 2048 a CU.
 constexpr int64_t kWantThreads = int64_t{1} << 19;
@@ -270,12 +283,13 @@ inline int row_parts(const RowGroups& g, int threads, int teams) {
   return static_cast<int>(std::min(most, std::max<int64_t>(1, kWantThreads / threads / g.groups)));
 }
 
-#ifndef NORM_BLOCKS
-#define NORM_BLOCKS 512
-#endif
-// Workgroups of a backward, each of which leaves a row of sums for the weights.
-inline int64_t row_sum_blocks(int64_t groups, int64_t rows, int size) {
-  const int64_t want = std::min<int64_t>((rows * size + 16383) / 16384, std::max<int64_t>(1, NORM_BLOCKS / groups));
+// Workgroups of a backward, each of which leaves a row of sums for the weights: the least whole
+// number for every CU that gives it `per_cu` threads (a part more on some CUs makes the others
+// wait: 4096 rows of 5120 of the block norm 85 us with 256 workgroups, 115 with 307).
+inline int64_t row_sum_blocks(int64_t groups, int64_t rows, int size, int64_t per_cu) {
+  const int64_t threads = size <= 512 ? 256 : (size + 511) / 512 * 64;
+  const int64_t most = std::max<int64_t>(1, 256 * ((per_cu + threads - 1) / threads) / groups);
+  const int64_t want = std::min<int64_t>((rows * size + 8191) / 8192, most);
   return groups * std::max<int64_t>(1, std::min(want, rows));
 }
 

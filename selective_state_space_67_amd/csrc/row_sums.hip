@@ -1,6 +1,6 @@
 // Sums over the workgroups' rows of partial sums (weights' gradients of the norms
-// around a block): 16 columns a workgroup, 16 threads a column, each adding every
-// 16th row in order with eight of them under way, then the 16 sums in order. Up to
+// around a block): 16 columns a workgroup, 64 threads a column, each adding every
+// 64th row in order with eight of them under way, then the 64 sums in order. Up to
 // three sums go in one launch.
 #include "kernels_block.h"
 
@@ -14,9 +14,11 @@ struct SumsArgs {
   int size, columns;
 };
 
-__global__ __launch_bounds__(256) void row_sums(const float* __restrict__ part, const SumsArgs a) {
+constexpr int kBy = 64;  // threads a column
+
+__global__ __launch_bounds__(16 * kBy) void row_sums(const float* __restrict__ part, const SumsArgs a) {
   constexpr int kAhead = 8;
-  __shared__ float t[16][17];
+  __shared__ float t[kBy][17];
   const int block = blockIdx.x, which = block >= a.first[2] ? 2 : block >= a.first[1] ? 1 : 0;
   const RowSum& s = a.sum[which];
   const int mine = block - a.first[which], group = mine / a.columns;
@@ -24,10 +26,10 @@ __global__ __launch_bounds__(256) void row_sums(const float* __restrict__ part, 
   const float* from = part + group * s.rows_group * a.width + s.offset + e;
   float x = 0.0f;
   if (e < a.size)
-    for (int64_t r = by; r < s.rows_group; r += 16 * kAhead) {
+    for (int64_t r = by; r < s.rows_group; r += kBy * kAhead) {
       float v[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) v[i] = r + 16 * i < s.rows_group ? from[(r + 16 * i) * a.width] : 0.0f;
+      for (int i = 0; i < kAhead; ++i) v[i] = r + kBy * i < s.rows_group ? from[(r + kBy * i) * a.width] : 0.0f;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) x += v[i];
     }
@@ -35,7 +37,7 @@ __global__ __launch_bounds__(256) void row_sums(const float* __restrict__ part, 
   __syncthreads();
   if (by != 0 || e >= a.size) return;
   x = 0.0f;
-  for (int r = 0; r < 16; ++r) x += t[r][col];
+  for (int r = 0; r < kBy; ++r) x += t[r][col];
   s.to[static_cast<int64_t>(group) * a.size + e] = x;
 }
 
@@ -56,8 +58,8 @@ hipError_t launch_row_sums(const float* part, int64_t width, int size, const Row
     }
   for (int i = n; i < 4; ++i) a.first[i] = 0x7fffffff;
   if (blocks == 0) return hipSuccess;
-  SSM_LOG("launch row_sums: %d sums of rows of %d; grid %u x 256 threads", n, size, blocks);
-  hipLaunchKernelGGL(row_sums, dim3(blocks), dim3(256), 0, stream, part, a);
+  SSM_LOG("launch row_sums: %d sums of rows of %d; grid %u x %d threads", n, size, blocks, 16 * kBy);
+  hipLaunchKernelGGL(row_sums, dim3(blocks), dim3(16 * kBy), 0, stream, part, a);
   return hipGetLastError();
 }
 
