@@ -85,6 +85,8 @@ def _call(fn, packed, stream, device):
     """Enqueue on the stream, with its device current."""
     import torch
 
+    if device.type != "cuda" and isinstance(fn, ctypes._CFuncPtr):  # (a stand-in may have them anywhere)
+        raise ValueError("tensors on %s: the operators run on a GPU" % device)
     st = _stream(stream, device)
     if device.type != "cuda" or device.index == torch._C._cuda_getDevice():
         status = fn(packed, st)
@@ -116,7 +118,7 @@ def _space(size_fn, packed, workspace, device, stream):
     _b._check(size_fn(packed, ctypes.byref(n)))
     if n.value == 0:
         return workspace, 0, 0
-    if workspace is None or workspace.numel() * workspace.element_size() < n.value:
+    if workspace is None or workspace.numel() * workspace.element_size() < n.value or not workspace.is_contiguous():
         workspace = _b._empty(int(n.value), torch.uint8, device, stream)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 

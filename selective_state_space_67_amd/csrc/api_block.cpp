@@ -92,6 +92,13 @@ ssm::GatedPlan gated_plan(const ssm_gated_norm_params* p, const GatedSizes& s) {
   return g;
 }
 
+// The sums over the workgroups' rows: a workgroup of 1024 threads for 16 elements of each weight.
+ssm_status check_gated_bwd(const ssm_gated_norm_params* p, GatedSizes* s) {
+  const ssm_status st = check_gated(p, s);
+  if (st != SSM_OK || !p->w_per_head || s->empty() || fits_launch(p->heads * ((p->head_dim + 15) / 16), 1024)) return st;
+  return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
+}
+
 size_t gated_bytes(const ssm_gated_norm_params* p, const GatedSizes& s) {
   if (s.empty()) return 0;
   return static_cast<size_t>(ssm::gated_norm_bwd_blocks(s.tokens, static_cast<int>(p->heads),
@@ -195,7 +202,7 @@ ssm_status ssm_gated_norm_fwd(const ssm_gated_norm_params* p, void* hip_stream) 
 ssm_status ssm_gated_norm_bwd_workspace_size(const ssm_gated_norm_params* p, size_t* bytes) {
   if (!p || !bytes) return fail(SSM_ERR_NULL_POINTER, "params or bytes is NULL");
   GatedSizes s;
-  const ssm_status st = check_gated(p, &s);
+  const ssm_status st = check_gated_bwd(p, &s);
   if (st != SSM_OK) return st;
   *bytes = gated_bytes(p, s);
   return ok();
@@ -204,7 +211,7 @@ ssm_status ssm_gated_norm_bwd_workspace_size(const ssm_gated_norm_params* p, siz
 ssm_status ssm_gated_norm_bwd(const ssm_gated_norm_params* p, void* hip_stream) {
   if (!p) return fail(SSM_ERR_NULL_POINTER, "params is NULL");
   GatedSizes s;
-  ssm_status st = check_gated(p, &s);
+  ssm_status st = check_gated_bwd(p, &s);
   if (st != SSM_OK) return st;
   const size_t si = dtype_size(p->in_dtype), so = dtype_size(p->out_dtype), ws = gated_bytes(p, s);
   const Need needs[] = {

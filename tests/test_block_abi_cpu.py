@@ -59,13 +59,30 @@ SIZES += [(block, kw) for kw in (dict(batch=-1), dict(seqlen=-1), dict(seqlen=1 
                                  dict(gate_rows=1, batch=1 << 22))]
 
 
-@pytest.mark.parametrize("make,kw", SIZES, ids=str)
+def named(v):
+    return v.__name__ if callable(v) else str(v)
+
+
+@pytest.mark.parametrize("make,kw", SIZES, ids=named)
 def test_sizes(lib, make, kw):  # noqa: F811
     n = ctypes.c_size_t()
     for fn in both(make):
         refused(lib, fn, make(**kw), SHAPE)
     size = getattr(lib, both(make)[1] + "_workspace_size")
     assert size(ctypes.byref(make(**kw)), ctypes.byref(n)) == SHAPE and size(None, ctypes.byref(n)) == NULL
+
+
+def test_sums_of_many_weights(lib):  # noqa: F811
+    """A weight for each head: one launch sums them, 16 a workgroup of 1024 threads; 2^22 of those are refused, one less is not."""
+    n = ctypes.c_size_t()
+    for kw, status in ((dict(heads=4096, head_dim=16384), SHAPE), (dict(heads=4095, head_dim=16384), 0),
+                       (dict(heads=65536, head_dim=1009), SHAPE), (dict(heads=65536, head_dim=1008), 0)):
+        p = gated(w_per_head=1, **kw)
+        assert lib.ssm_gated_norm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)) == status, kw
+        if status != 0:
+            refused(lib, "ssm_gated_norm_bwd", p, SHAPE, "workgroups")
+        p.w_per_head = 0
+        assert lib.ssm_gated_norm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
 
 
 def test_types_and_flags(lib):  # noqa: F811

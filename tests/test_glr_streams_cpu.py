@@ -36,3 +36,17 @@ def test_memory_comes_from_the_stream_that_uses_it(watch, name):  # noqa: F811
     results = got.values() if isinstance(got, dict) else got if isinstance(got, tuple) else (got,)
     for t in results:
         assert (t.data_ptr(), current) in marked
+
+
+class Anywhere:
+    """A stream of whatever device."""
+    cuda_stream = 0
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_tensors_in_host_memory_are_refused(name):
+    """The kernels would be handed addresses that they cannot reach."""
+    with pytest.raises(ValueError, match="cpu"):
+        CALLS[name](None)
+    with pytest.raises(ValueError, match="cpu"):
+        bg.ssm_glr_update(z(2, 8), z(2, 1, 8), z(2, 1, 8), z(8), out=z(2, 1, 8), stream=Anywhere())
