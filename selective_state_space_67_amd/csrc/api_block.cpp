@@ -92,10 +92,10 @@ ssm::GatedPlan gated_plan(const ssm_gated_norm_params* p, const GatedSizes& s) {
   return g;
 }
 
-// The sums over the workgroups' rows: a workgroup of 1024 threads for 16 elements of each weight.
+// The sums over the workgroups' rows: a workgroup of 1024 threads for 32 elements of each weight.
 ssm_status check_gated_bwd(const ssm_gated_norm_params* p, GatedSizes* s) {
   const ssm_status st = check_gated(p, s);
-  if (st != SSM_OK || !p->w_per_head || s->empty() || fits_launch(p->heads * ((p->head_dim + 15) / 16), 1024)) return st;
+  if (st != SSM_OK || !p->w_per_head || s->empty() || fits_launch(p->heads * ((p->head_dim + 31) / 32), 1024)) return st;
   return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
 }
 
@@ -129,7 +129,7 @@ ssm_status check_block(const ssm_block_norm_params* p, BlockSizes* s) {
   if (!p->gate_rows) s->gate = p->dim;
   // a gate for each sequence: a workgroup of up to 1024 threads at least for each
   if (p->gate_rows && !s->empty() &&
-      (!fits_launch(p->batch, 1024) || !fits_launch(p->batch * ((p->dim + 15) / 16), 1024)))
+      (!fits_launch(p->batch, 1024) || !fits_launch(p->batch * ((p->dim + 31) / 32), 1024)))
     return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
   return SSM_OK;
 }

@@ -16,11 +16,12 @@
 // kept in registers. Each wave's rows act on a state as (P, H) and on an adjoint
 // as (P, G); the waves exchange them through LDS once. The parameters' gradients
 // are summed over a wave's rows in registers, over the waves in LDS, and over the
-// pieces by glr_sums, always in the same order.
+// pieces by row_sums, always in the same order.
 #include <type_traits>
 
 #include "glr_device.h"
 #include "glr_launch.h"
+#include "kernels_block.h"
 
 namespace ssm {
 namespace {
@@ -149,33 +150,6 @@ __global__ __launch_bounds__(kLanes * W) void glr_grads(const GlrArgs g) {
   }
 }
 
-// The pieces' sums, 16 columns a workgroup (of 3 D), 16 threads a column, each adding every
-// 16th piece in order with eight of them under way, then the 16 sums in order.
-__global__ __launch_bounds__(256) void glr_sums(const float* __restrict__ part, float* dA, float* d_dt_bias,
-                                                float* din_bias, int64_t rows, int D) {
-  constexpr int kAhead = 8;
-  __shared__ float t[16][17];
-  const int col = threadIdx.x % 16, by = threadIdx.x / 16;
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * 16 + col, width = 3 * static_cast<int64_t>(D);
-  float x = 0.0f;
-  if (e < width)
-    for (int64_t r = by; r < rows; r += 16 * kAhead) {
-      float v[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) v[i] = r + 16 * i < rows ? part[(r + 16 * i) * width + e] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) x += v[i];
-    }
-  t[by][col] = x;
-  __syncthreads();
-  if (by != 0 || e >= width) return;
-  x = 0.0f;
-  for (int r = 0; r < 16; ++r) x += t[r][col];
-  const int which = static_cast<int>(e / D);
-  float* dst = which == 0 ? dA : which == 1 ? d_dt_bias : din_bias;
-  if (dst) dst[e - static_cast<int64_t>(which) * D] = x;
-}
-
 struct Grads {
   template <typename InT, int DECAY, int MIX, bool IN, bool Z>
   static hipError_t run(unsigned blocks, const GlrArgs& g, hipStream_t stream) {
@@ -220,11 +194,11 @@ hipError_t launch_glr_bwd(const GlrPlan& plan, const GlrPieces& pieces, void* wo
           kPiece, blocks, kGlrBwdWaves * kLanes);
   e = glr_pick<Grads>(plan, blocks, g, stream);
   if (e != hipSuccess) return e;
-  const unsigned grid = static_cast<unsigned>((3 * plan.D + 15) / 16);
-  SSM_LOG("launch glr_sums: grid %u x 256 threads", grid);
-  hipLaunchKernelGGL(glr_sums, dim3(grid), dim3(256), 0, stream, g.part, plan.dA, plan.d_dt_bias, plan.din_bias,
-                     plan.B * pieces.pieces, g.D);
-  return hipGetLastError();
+  // (dim <= 2^24: below 2^32 threads)
+  const int64_t sums = plan.B * pieces.pieces;
+  return launch_row_sums(g.part, 3 * plan.D, g.D,
+                         {{plan.dA, 0, sums, 1}, {plan.d_dt_bias, plan.D, sums, 1}, {plan.din_bias, 2 * plan.D, sums, 1}},
+                         stream);
 }
 
 }  // namespace ssm

@@ -73,10 +73,10 @@ def test_sizes(lib, make, kw):  # noqa: F811
 
 
 def test_sums_of_many_weights(lib):  # noqa: F811
-    """A weight for each head: one launch sums them, 16 a workgroup of 1024 threads; 2^22 of those are refused, one less is not."""
+    """A weight for each head: one launch sums them, 32 a workgroup of 1024 threads; 2^22 of those are refused, one less is not."""
     n = ctypes.c_size_t()
-    for kw, status in ((dict(heads=4096, head_dim=16384), SHAPE), (dict(heads=4095, head_dim=16384), 0),
-                       (dict(heads=65536, head_dim=1009), SHAPE), (dict(heads=65536, head_dim=1008), 0)):
+    for kw, status in ((dict(heads=8192, head_dim=16384), SHAPE), (dict(heads=8191, head_dim=16384), 0),
+                       (dict(heads=65536, head_dim=2017), SHAPE), (dict(heads=65536, head_dim=2016), 0)):
         p = gated(w_per_head=1, **kw)
         assert lib.ssm_gated_norm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)) == status, kw
         if status != 0:
