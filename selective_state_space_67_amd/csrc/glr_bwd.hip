@@ -172,7 +172,18 @@ GlrPieces plan_glr_bwd(int64_t B, int64_t L, int64_t D) {
   p.off_starts = 3 * each;
   p.off_ends = 4 * each;
   p.off_part = 5 * each;
-  p.bytes = 8 * each;
+  p.off_segments = 8 * each;
+  p.bytes = p.off_segments;
+  p.segments = 1;
+  p.each = static_cast<int>(p.pieces);
+  // Few columns and many pieces: the fold in segments. us of one fold and of the three launches in
+  // segments, which start some 3 us later: 4 columns 15.6 and 12.5 with 767 and 768 pieces, 88 and 17.6
+  // with 4096; 128 columns, whose one fold reaches every CU, 24 and 52 with 512.
+  if (p.pieces >= 768 && B * ((D + kLanes - 1) / kLanes) < 64) {
+    p.each = kGlrSegment;
+    p.segments = (p.pieces + kGlrSegment - 1) / kGlrSegment;
+    p.bytes += (5 * static_cast<size_t>(B) * p.segments * D * sizeof(float) + 255) / 256 * 256;
+  }
   return p;
 }
 
@@ -187,7 +198,7 @@ hipError_t launch_glr_bwd(const GlrPlan& plan, const GlrPieces& pieces, void* wo
   g.ends = reinterpret_cast<float*>(ws + pieces.off_ends);
   g.part = reinterpret_cast<float*>(ws + pieces.off_part);
   hipError_t e = launch_glr_aggregates(plan, g, stream);
-  if (e == hipSuccess) e = launch_glr_fold(plan, g, stream);
+  if (e == hipSuccess) e = launch_glr_fold(plan, g, pieces, reinterpret_cast<float*>(ws + pieces.off_segments), stream);
   if (e != hipSuccess) return e;
   const unsigned blocks = static_cast<unsigned>(plan.B * pieces.pieces * g.tiles);
   SSM_LOG("launch glr_grads: %lld pieces of %d rows; grid %u x %d threads", static_cast<long long>(pieces.pieces),

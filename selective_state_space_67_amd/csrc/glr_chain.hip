@@ -69,7 +69,7 @@ __device__ __forceinline__ float2 await(const uint64_t* from, uint64_t word, int
 // First (P, H), then (p.x, p.y).
 __device__ __forceinline__ void then(float& P, float& H, float2 p) {
   H = through(p.x, p.y, H);
-  P = __float_as_int(P) < 0 || __float_as_int(p.x) < 0 ? kCut : P * p.x;
+  P = joined(P, p.x);
 }
 
 template <typename InT, int DECAY, int MIX, bool IN, bool Z, int W, int K>

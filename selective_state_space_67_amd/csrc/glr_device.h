@@ -235,5 +235,9 @@ constexpr float kCut = -0.0f;
 __device__ __forceinline__ float through(float P, float H, float h) {
   return __float_as_int(P) < 0 ? H : __builtin_fmaf(P, h, H);
 }
+// P of two runs together.
+__device__ __forceinline__ float joined(float a, float b) {
+  return __float_as_int(a) < 0 || __float_as_int(b) < 0 ? kCut : a * b;
+}
 
 }  // namespace ssm

@@ -53,7 +53,9 @@ struct GlrPlan {
 struct GlrPieces {
   int64_t pieces, rows;  // rows of a piece; forward, pieces = 1: one walk from end to end, no workspace
   int waves;             // of a workgroup that takes a piece of 64 channels
-  size_t off_P, off_H, off_G, off_starts, off_ends, off_part, bytes;
+  int64_t segments;      // of pieces, for the backward's fold
+  int each;              // pieces of a segment
+  size_t off_P, off_H, off_G, off_starts, off_ends, off_part, off_segments, bytes;
 };
 // Pure host arithmetic, like the others here.
 GlrPieces plan_glr(int64_t B, int64_t L, int64_t D);
@@ -75,8 +77,11 @@ hipError_t launch_glr_chain(const GlrPlan& plan, const GlrPieces& pieces, void* 
 struct GlrArgs;
 GlrArgs glr_args(const GlrPlan& plan);
 hipError_t launch_glr_aggregates(const GlrPlan& plan, const GlrArgs& args, hipStream_t stream);
-hipError_t launch_glr_fold(const GlrPlan& plan, const GlrArgs& args, hipStream_t stream);
+hipError_t launch_glr_fold(const GlrPlan& plan, const GlrArgs& args, const GlrPieces& pieces, float* segments,
+                           hipStream_t stream);
 // A piece of the backward is 8 rows for each of this many waves.
 constexpr int kGlrBwdWaves = 4;
+// Pieces of a segment, where the backward's fold goes in segments.
+constexpr int kGlrSegment = 64;
 
 }  // namespace ssm

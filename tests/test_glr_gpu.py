@@ -99,6 +99,16 @@ def test_pieces(L, D, cuts):
         compare_bwd(x, t, "sigmoid", "unit", False)
 
 
+# 768 pieces of 32 rows and more are joined in segments of 64 (2048 rows)
+@pytest.mark.parametrize("B,L,D", [(1, 24544, 64), (1, 24545, 3), (2, 28700, 66)])
+@pytest.mark.parametrize("cuts", [False, True])
+def test_gradients_of_long_sequences(B, L, D, cuts):
+    resets = [(0, 4096), (0, 8191), (0, 20000), (1, 0), (1, 4095), (1, 24576)] if cuts else None
+    x = glr_inputs(B, L, D, wl.F32, seed=L + D, state=True, resets=resets)
+    print(B, L, D, cuts, flush=True)
+    compare_bwd(x, on_device(x, device()), "sigmoid", "unit", False)
+
+
 @pytest.mark.parametrize("B,T,D", [(1, 1, 1), (1, 1, 1536), (5, 1, 100), (64, 1, 64), (3, 2, 65), (2, 5, 70), (1, 33, 64)])
 @pytest.mark.parametrize("dtype", [wl.F32, wl.BF16])
 def test_decode_window(B, T, D, dtype):
