@@ -13,7 +13,7 @@ import ctypes
 from . import binding as _b
 from .binding_delta import _need
 from .binding_delta import _tokens as _head_tokens
-from .binding_glr import _at, _call, _new, _one_device, _space, _tokens, check_layouts, packer
+from .binding_glr import _at, _call, _new, _one_device, _space, _sum, _tokens, check_layouts, packer
 
 _i64, _i32, _vp, _f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
 
@@ -100,7 +100,7 @@ def ssm_gated_norm_bwd(x, z, dout, *, w=None, eps=1e-6, gate_first=False, grad_d
     _one_device(x, z, dout, w, workspace)
     g = dict(dx=_new(x, dt, stream), dz=_new(z, dt, stream), dw=None)
     if want_dw:
-        g["dw"] = _b._result(x.shape[3:] if w is None else w.shape, torch.float32, x.device, stream)
+        g["dw"] = _sum(w, x.shape[3:], x.device, stream)
     head = (*sizes, _b._dtype_code(g["dx"]), *rows, at_w, 0, dout.data_ptr(), *[_at(t) for t in g.values()])
     tail = (eps, bool(gate_first), per_head, 0)
     pack = _PACKED[10].pack
@@ -191,12 +191,14 @@ def ssm_block_norm_bwd(y, x, dout, dx_out=None, *, w=None, post=False, w_post=No
     _one_device(y, x, dout, dx_out, w, w_post, gate, workspace)
     D, dev = sizes[2], y.device
 
-    def new(wanted, shape):
-        return _b._result(shape, torch.float32, dev, stream) if wanted else None
-
-    g = dict(dy=_new(y, grad_dtype or torch.float32, stream), dx=None if x is None else _new(x, res, stream),
-             dw=new(want_dw, (D,)), dw_post=new(want_dw and post, (D,)),
-             dgate=new(want_dw and gate is not None, () if gate is None else gate.shape))
+    g = dict(dy=_new(y, grad_dtype or torch.float32, stream), dx=None if x is None else _new(x, res, stream), dw=None,
+             dw_post=None, dgate=None)
+    if want_dw:
+        g["dw"] = _sum(w, (D,), dev, stream)
+        if post:
+            g["dw_post"] = _sum(w_post, (D,), dev, stream)
+        if gate is not None:
+            g["dgate"] = _sum(gate, None, dev, stream)
     head = (*sizes, _b._dtype_code(g["dy"]), *inputs, 0, 0, dout.data_ptr(), _at(dx_out), *[_at(t) for t in g.values()])
     tail = (eps, scale, bool(post), 0)
     pack = _PACKED[11].pack

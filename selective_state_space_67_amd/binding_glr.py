@@ -110,6 +110,15 @@ def _new(t, dtype, stream):
     return _b._result(t.shape, dtype, t.device, stream)
 
 
+def _sum(like, shape, device, stream):
+    """A float32 output of this shape, which `like` has if there is one."""
+    import torch
+
+    if like is not None:
+        return _new(like, torch.float32, stream)
+    return _b._result(shape, torch.float32, device, stream)
+
+
 def _space(size_fn, packed, workspace, device, stream):
     """(workspace, its address and bytes) of what a call needs."""
     import torch
@@ -285,7 +294,9 @@ def ssm_glr_bwd(u, dt_raw, A, dout, *, dt_bias=None, in_raw=None, in_bias=None, 
     gate = in_raw is not None
     g = dict(du=_new(u, gd, stream), d_dt_raw=_new(u, gd, stream), din_raw=_new(u, gd, stream) if gate else None,
              dz=None if z is None else _new(u, gd, stream), dA=_new(A, f32, stream), d_dt_bias=_new(A, f32, stream),
-             din_bias=_new(A, f32, stream) if gate else None, dh0=_b._result((B, D), f32, dev, stream) if want_dh0 else None)
+             din_bias=_new(A, f32, stream) if gate else None, dh0=None)
+    if want_dh0:
+        g["dh0"] = _sum(h0 if dh_last is None else dh_last, (B, D), dev, stream)
     head = (*sizes, _b._dtype_code(g["du"]), *fields, *_sequence(sizes, reset, h0), 0, 0, dout.data_ptr(), _at(dh_last),
             *[_at(t) for t in g.values()])
     pack = _PACKED[8].pack
