@@ -690,7 +690,7 @@ ssm_status ssm_qk_norm_bwd(const ssm_qk_norm_params* p, void* hip_stream);
  *   dA       (D) float32, required; d_dt_bias, din_bias (D), dh0 (B,D) float32, NULL => not
  *            written. Sums go in a fixed order: repeated calls give identical bits.
  *   workspace, workspace_bytes : at least ssm_glr_bwd_workspace_size() bytes, aligned to
- *            256: 32 bytes for every 32 steps of a channel.
+ *            256: some 32 bytes for every 32 steps of a channel.
  * Arithmetic is float32 whatever in_dtype is; only results are rounded. Outputs must not
  * overlap inputs, each other or the workspace. A non-finite input stays within its
  * channel and document (the sums over tokens aside).

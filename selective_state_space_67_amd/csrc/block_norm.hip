@@ -9,7 +9,11 @@
 //   dy = dm, or back through the post norm
 //
 // One pass over the data each way: a token's row is read once, kept in registers
-// and written once, so memory bounds both. out is the norm of x' before x' is
+// and written once, so memory bounds both: 8192 rows of 2560, bfloat16 with a float32
+// stream, 45.8 us for 252 MB, 5.5 TB/s (x' partly stays in the last-level cache; a large
+// copy reaches 5.2), backward 74.5 us for 377 MB, 5.1, and 4.8 for the sums. Rows above
+// 8192 entries, or odd above 4096, outgrow the backward's registers: 250 to 365 us for
+// as many elements. out is the norm of x' before x' is
 // rounded to the residual stream's type, and the backward works x' out again from
 // x and y, so that neither sees that rounding.
 #include <utility>

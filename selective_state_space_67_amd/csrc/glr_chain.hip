@@ -20,6 +20,12 @@
 // clearing launch has left in it, and no order between words is relied on. Should a
 // word never come (the workspace overwritten by somebody else's work), a wait gives
 // up after kPolls looks and takes NaN.
+//
+// Bound by memory where the columns are many (8 x 2048 x 1536 channels, 192 columns: 52
+// us for 201 MB, 3.9 of a large copy's 5.2 TB/s, with the vector ALU busy for half of it),
+// and by the latency of looks and tickets where they are few (1 x 131072 x 256, 4 columns:
+// 92 us for 268 MB, waves waiting for 60% of their time). Waves of 16 or 32 channels with
+// more rows each, and workgroups that stay for another piece, were slower at both.
 #include "glr_device.h"
 #include "glr_launch.h"
 

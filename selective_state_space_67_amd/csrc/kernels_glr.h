@@ -1,7 +1,6 @@
 // Host-side interface between the front end of the gated linear recurrence
 // (api_glr.cpp) and its kernels (glr_fwd.hip, glr_chain.hip, glr_pieces.hip,
-// glr_bwd.hip). Not
-// installed; not part of the ABI.
+// glr_bwd.hip). Not installed; not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>

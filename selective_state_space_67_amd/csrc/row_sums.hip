@@ -15,7 +15,7 @@ struct SumsArgs {
   int size, columns;
 };
 
-constexpr int kCols = 32, kBy = 32;  // threads a column
+constexpr int kCols = 32, kBy = 32;  // columns, threads a column
 
 __global__ __launch_bounds__(kCols * kBy) void row_sums(const float* __restrict__ part, const SumsArgs a) {
   constexpr int kAhead = 8;
