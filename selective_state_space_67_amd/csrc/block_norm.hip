@@ -12,8 +12,8 @@
 // and written once, so memory bounds both: 8192 rows of 2560, bfloat16 with a float32
 // stream, 45.8 us for 252 MB, 5.5 TB/s (x' partly stays in the last-level cache; a large
 // copy reaches 5.2), backward 74.5 us for 377 MB, 5.1, and 4.8 for the sums. Rows above
-// 8192 entries, or odd above 4096, outgrow the backward's registers: 250 to 365 us for
-// as many elements. out is the norm of x' before x' is
+// 8192 entries outgrow the backward's registers (250 to 365 us for as many elements), odd
+// ones above 4096 take 120 to 196. out is the norm of x' before x' is
 // rounded to the residual stream's type, and the backward works x' out again from
 // x and y, so that neither sees that rounding.
 #include <utility>
@@ -243,6 +243,7 @@ BlockArgs block_args(const BlockPlan& p) {
 
 template <typename InT, typename ResT>
 struct Forward {
+  static constexpr bool kMany = false;
   template <int V, int TR, int NV, int MOST>
   static hipError_t run(int threads, BlockArgs a, hipStream_t stream) {
     a.g.parts = row_parts(a.g, threads, TR ? threads / (TR ? TR : 1) : 1);
@@ -256,6 +257,7 @@ struct Forward {
 
 template <typename InT, typename ResT>
 struct Backward {
+  static constexpr bool kMany = true;
   template <int V, int TR, int NV, int MOST>
   static hipError_t run(int threads, BlockArgs a, int parts, hipStream_t stream) {
     a.g.parts = parts;

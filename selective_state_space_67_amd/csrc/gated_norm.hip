@@ -188,6 +188,7 @@ GatedArgs gated_args(const GatedPlan& p) {
 
 template <typename InT>
 struct Forward {
+  static constexpr bool kMany = false;
   template <int V, int TR, int NV, int MOST>
   static hipError_t run(int threads, GatedArgs a, hipStream_t stream) {
     a.g.parts = row_parts(a.g, threads, TR ? threads / (TR ? TR : 1) : 1);
@@ -201,6 +202,7 @@ struct Forward {
 
 template <typename InT>
 struct Backward {
+  static constexpr bool kMany = false;
   template <int V, int TR, int NV, int MOST>
   static hipError_t run(int threads, GatedArgs a, int parts, hipStream_t stream) {
     a.g.parts = parts;
