@@ -213,7 +213,10 @@ bool glr_steps_fit(int64_t B, int64_t D) { return fits_launch(B * tiles_of(D), k
 // workgroups) 68.5 and 71.5; 16 x 2048 x 1280 (320) 121 and 85; 16 x 1024 x 2048 (512) 68.6 and 75.6.
 GlrPieces plan_glr(int64_t B, int64_t L, int64_t D) {
   const int64_t groups = B * tiles_of(D), rounds = (groups + 255) / 256;
-  if (groups < int64_t{1} << 22 && (30000 * rounds - 119 * groups) * L >= 7000000) return plan_glr_chain(B, L, D);
+  if (groups < int64_t{1} << 22 && (30000 * rounds - 119 * groups) * L >= 7000000) {
+    const GlrPieces chain = plan_glr_chain(B, L, D);
+    if (glr_grids_fit(B, D, chain)) return chain;  // (of very many rows of few channels it may need too large a launch)
+  }
   GlrPieces p{};
   p.pieces = 1;
   p.rows = L;

@@ -127,8 +127,10 @@ def test_more_than_a_launch_allows(lib):  # noqa: F811
     # 512 threads a piece, and none of the sizes is multiplied past 64 bits
     assert ok(batch=(1 << 23) - 1, seqlen=128) == 0
     assert ok(batch=1 << 23, seqlen=128) == SHAPE
-    assert ok(batch=65, seqlen=(1 << 27) - 1) == SHAPE  # pieces of a chain, 256 threads each
-    assert ok(batch=7, seqlen=(1 << 27) - 1) == 0
+    # pieces of a chain, 256 threads each; where they are too many, a walk (which has no workspace)
+    assert ok(batch=7, seqlen=(1 << 27) - 1) == 0 and n.value > 0
+    assert ok(batch=65, seqlen=(1 << 27) - 1) == 0 and n.value == 0
+    assert ok(batch=128, seqlen=1 << 23) == 0 and n.value == 0
     assert lib.ssm_glr_bwd_workspace_size(ctypes.byref(seq(batch=1 << 20, seqlen=1 << 20, dim=1)), ctypes.byref(n)) == SHAPE
     assert lib.ssm_glr_bwd_workspace_size(ctypes.byref(seq(batch=1 << 57, seqlen=1, dim=1)), ctypes.byref(n)) == SHAPE
 

@@ -99,6 +99,28 @@ def test_pieces(L, D, cuts):
         compare_bwd(x, t, "sigmoid", "unit", False)
 
 
+@pytest.mark.parametrize("L", [5, 100, 1500])
+def test_every_token_a_document(L):
+    """Nothing is handed from one token to the next: out = i u silu(z), no gradient of the decay, dh0 0."""
+    import torch
+
+    from selective_state_space_67_amd import ssm_glr_bwd
+
+    x = glr_inputs(2, L, 66, wl.F32, seed=L, z=True, state=True, resets=[(b, t) for b in range(2) for t in range(L)])
+    t = on_device(x, device())
+    print(L, flush=True)
+    out, last = forward(x, t, "sigmoid", "unit")
+    ref, rh = og.glr_fwd(**wide(x))
+    check(out, ref, STATE, "out")
+    check(last, rh, STATE, "h_last")
+    compare_bwd(x, t, "sigmoid", "unit", False)
+    a, k = call(t)
+    g = ssm_glr_bwd(*a, t["dout"], reset=t["reset"], h0=t["h0"], dh_last=t["dh_last"], **k)
+    torch.cuda.synchronize()
+    for n in ("d_dt_raw", "dA", "d_dt_bias", "dh0"):
+        assert not g[n].any(), n
+
+
 # 768 pieces of 32 rows and more are joined in segments of 64 (2048 rows)
 @pytest.mark.parametrize("B,L,D", [(1, 24544, 64), (1, 24545, 3), (2, 28700, 66)])
 @pytest.mark.parametrize("cuts", [False, True])
