@@ -58,7 +58,7 @@ def _gated(x, z, w):
     shape, dt = x.shape, x.dtype
     B, L, H, d = shape
     xs = H * d if x.is_contiguous() else _head_tokens(x, shape, "x", dt)
-    zs = _head_tokens(z, shape, "z", dt)
+    zs = xs if z.is_contiguous() and z.dtype is dt and z.shape == shape and xs == H * d else _head_tokens(z, shape, "z", dt)
     per_head = w is not None and w.dim() == 2
     if w is not None:
         _need(w, (H, d) if per_head else (d,), "w", torch.float32)
@@ -80,9 +80,9 @@ def ssm_gated_norm_fwd(x, z, *, w=None, eps=1e-6, gate_first=False, out=None, ou
         out = _new(x, out_dtype or torch.float32, stream)
     else:
         _need(out, x.shape, "out", out.dtype)
-    _one_device(x, z, w, out)
+    d = _one_device(x, z, w, out)
     _call(lib.ssm_gated_norm_fwd, _PACKED[10].pack(*sizes, _b._dtype_code(out), *rows, at_w, out.data_ptr(), 0, 0, 0, 0,
-                                                   0, 0, eps, bool(gate_first), per_head, 0), stream, x.device)
+                                                   0, 0, eps, bool(gate_first), per_head, 0), stream, d)
     return out
 
 
@@ -97,7 +97,7 @@ def ssm_gated_norm_bwd(x, z, dout, *, w=None, eps=1e-6, gate_first=False, grad_d
     dt = grad_dtype or torch.float32
     sizes, rows, at_w, per_head = _gated(x, z, w)
     _need(dout, x.shape, "dout", x.dtype)
-    _one_device(x, z, dout, w, workspace)
+    d = _one_device(x, z, dout, w, workspace)
     g = dict(dx=_new(x, dt, stream), dz=_new(z, dt, stream), dw=None)
     if want_dw:
         g["dw"] = _sum(w, x.shape[3:], x.device, stream)
@@ -106,7 +106,7 @@ def ssm_gated_norm_bwd(x, z, dout, *, w=None, eps=1e-6, gate_first=False, grad_d
     pack = _PACKED[10].pack
     workspace, at, n = _space(lib.ssm_gated_norm_bwd_workspace_size, pack(*head, 0, 0, *tail), workspace, x.device,
                               stream)
-    _call(lib.ssm_gated_norm_bwd, pack(*head, at, n, *tail), stream, x.device)
+    _call(lib.ssm_gated_norm_bwd, pack(*head, at, n, *tail), stream, d)
     return g
 
 
@@ -165,9 +165,9 @@ def ssm_block_norm_fwd(y, x=None, *, w=None, post=False, w_post=None, gate=None,
         _need(x_out, y.shape, "x_out", res)
     elif want_x:
         x_out = _new(y, res, stream)
-    _one_device(y, x, w, w_post, gate, out, x_out)
+    d = _one_device(y, x, w, w_post, gate, out, x_out)
     _call(lib.ssm_block_norm_fwd, _PACKED[11].pack(*sizes, _b._dtype_code(out), *inputs, out.data_ptr(), _at(x_out), 0, 0,
-                                                   0, 0, 0, 0, 0, 0, 0, eps, scale, bool(post), 0), stream, y.device)
+                                                   0, 0, 0, 0, 0, 0, 0, eps, scale, bool(post), 0), stream, d)
     return out, x_out
 
 
@@ -188,7 +188,7 @@ def ssm_block_norm_bwd(y, x, dout, dx_out=None, *, w=None, post=False, w_post=No
     _need(dout, y.shape, "dout", y.dtype)
     if dx_out is not None:
         _need(dx_out, y.shape, "dx_out", res)
-    _one_device(y, x, dout, dx_out, w, w_post, gate, workspace)
+    d = _one_device(y, x, dout, dx_out, w, w_post, gate, workspace)
     D, dev = sizes[2], y.device
 
     g = dict(dy=_new(y, grad_dtype or torch.float32, stream), dx=None if x is None else _new(x, res, stream), dw=None,
@@ -203,5 +203,5 @@ def ssm_block_norm_bwd(y, x, dout, dx_out=None, *, w=None, post=False, w_post=No
     tail = (eps, scale, bool(post), 0)
     pack = _PACKED[11].pack
     workspace, at, n = _space(lib.ssm_block_norm_bwd_workspace_size, pack(*head, 0, 0, *tail), workspace, dev, stream)
-    _call(lib.ssm_block_norm_bwd, pack(*head, at, n, *tail), stream, dev)
+    _call(lib.ssm_block_norm_bwd, pack(*head, at, n, *tail), stream, d)
     return g

@@ -16,7 +16,7 @@ import ctypes
 import struct
 
 from . import binding as _b
-from .binding_delta import _need, _stream
+from .binding_delta import _need
 
 _i64, _i32, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
 
@@ -74,25 +74,30 @@ def check_layouts(lib, structs, packed):
 
 
 def _one_device(first, *others):
-    """Everything lies where the call runs (an address on another device would fault there)."""
+    """Everything lies where the call runs (an address on another device would fault there): its number."""
     d = first.get_device()
     for t in others:
         if t is not None and t.get_device() != d:
             raise ValueError("tensors on %s and %s in one call" % (first.device, t.device))
+    return d
 
 
 def _call(fn, packed, stream, device):
-    """Enqueue on the stream, with its device current."""
+    """Enqueue on the stream, with its device (a number) current."""
     import torch
 
-    if device.type != "cuda" and isinstance(fn, ctypes._CFuncPtr):  # (a stand-in may have them anywhere)
-        raise ValueError("tensors on %s: the operators run on a GPU" % device)
-    st = _stream(stream, device)
-    if device.type != "cuda" or device.index == torch._C._cuda_getDevice():
-        status = fn(packed, st)
+    c = torch._C
+    if device < 0:
+        if isinstance(fn, ctypes._CFuncPtr):  # (a stand-in may have them anywhere)
+            raise ValueError("tensors on cpu: the operators run on a GPU")
+        status = fn(packed, 0 if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
+        st = c._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+        if device == c._cuda_getDevice():
             status = fn(packed, st)
+        else:
+            with torch.cuda.device(device):
+                status = fn(packed, st)
     if status != 0:
         _b._check(status)
 
@@ -106,6 +111,8 @@ def _new(t, dtype, stream):
     import torch
 
     if stream is None:
+        if t.dtype is dtype and t.is_contiguous():
+            return torch.empty_like(t)
         return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
     return _b._result(t.shape, dtype, t.device, stream)
 
@@ -163,22 +170,25 @@ def _inputs(u, dt_raw, A, dt_bias, in_raw, in_bias, z, decay, mix):
     shape, dt = u.shape, u.dtype
     B, L, D = shape
     us = D if u.is_contiguous() else _tokens(u, shape, "u", dt)
-    ds = _tokens(dt_raw, shape, "dt_raw", dt)
-    ins = zs = 0
+    ds = D if dt_raw.is_contiguous() and dt_raw.dtype is dt and dt_raw.shape == shape else _tokens(dt_raw, shape, "dt_raw", dt)
+    ins = zs = at_in = at_z = at_dt_bias = at_in_bias = 0
     if in_raw is not None:
-        ins = _tokens(in_raw, shape, "in_raw", dt)
+        ins = D if in_raw.is_contiguous() and in_raw.dtype is dt and in_raw.shape == shape else _tokens(in_raw, shape, "in_raw", dt)
+        at_in = in_raw.data_ptr()
     elif in_bias is not None:
         raise ValueError("in_bias comes with in_raw")
     if z is not None:
-        zs = _tokens(z, shape, "z", dt)
+        zs = D if z.is_contiguous() and z.dtype is dt and z.shape == shape else _tokens(z, shape, "z", dt)
+        at_z = z.data_ptr()
     size = (D,)
     _need(A, size, "A", f32)
     if dt_bias is not None:
         _need(dt_bias, size, "dt_bias", f32)
+        at_dt_bias = dt_bias.data_ptr()
     if in_bias is not None:
         _need(in_bias, size, "in_bias", f32)
-    fields = (u.data_ptr(), dt_raw.data_ptr(), _at(in_raw), _at(z), us, ds, ins, zs, A.data_ptr(), _at(dt_bias),
-              _at(in_bias))
+        at_in_bias = in_bias.data_ptr()
+    fields = (u.data_ptr(), dt_raw.data_ptr(), at_in, at_z, us, ds, ins, zs, A.data_ptr(), at_dt_bias, at_in_bias)
     return (B, L, D, _b._dtype_code(u)), fields, (p_decay, p_mix)
 
 
@@ -217,17 +227,17 @@ def ssm_glr_fwd(u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=None, z=None
         _need(out, u.shape, "out", out.dtype)
     if h_last is not None:
         _need(h_last, (sizes[0], sizes[2]), "h_last", torch.float32)
-    _one_device(u, dt_raw, A, dt_bias, in_raw, in_bias, z, reset, h0, out, h_last, workspace)
+    d = _one_device(u, dt_raw, A, dt_bias, in_raw, in_bias, z, reset, h0, out, h_last, workspace)
     head = (*sizes, _b._dtype_code(out), *fields, *_sequence(sizes, reset, h0), out.data_ptr(), _at(h_last), *_NO_GRADS)
     pack = _PACKED[8].pack
     workspace, at, n = _space(lib.ssm_glr_workspace_size, pack(*head, 0, 0, *kinds), workspace,
                               u.device, stream)
-    _call(lib.ssm_glr_fwd, pack(*head, at, n, *kinds), stream, u.device)
+    _call(lib.ssm_glr_fwd, pack(*head, at, n, *kinds), stream, d)
     return out
 
 
 def _update(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, out_dtype, decay, mix, stream):
-    """(packed struct, out) of a decode window."""
+    """(packed struct, out, device) of a decode window."""
     import torch
 
     sizes, fields, kinds = _inputs(u, dt_raw, A, dt_bias, in_raw, in_bias, z, decay, mix)
@@ -236,8 +246,8 @@ def _update(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, out_dtype, decay,
     else:
         _need(out, u.shape, "out", out.dtype)
     _need(h, (sizes[0], sizes[2]), "h", torch.float32)
-    _one_device(u, h, dt_raw, A, dt_bias, in_raw, in_bias, z, out)
-    return _PACKED[9].pack(*sizes, _b._dtype_code(out), h.data_ptr(), *fields, out.data_ptr(), *kinds), out
+    d = _one_device(u, h, dt_raw, A, dt_bias, in_raw, in_bias, z, out)
+    return _PACKED[9].pack(*sizes, _b._dtype_code(out), h.data_ptr(), *fields, out.data_ptr(), *kinds), out, d
 
 
 def ssm_glr_update(h, u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=None, z=None, out=None, out_dtype=None,
@@ -245,8 +255,8 @@ def ssm_glr_update(h, u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=None, 
     """Decode window of T tokens: updates h (B, D) float32 in place and returns out
     (B, T, D). Arguments as for ssm_glr_fwd with L = T."""
     lib = _b.load_library()
-    packed, out = _update(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, out_dtype, decay, mix, stream)
-    _call(lib.ssm_glr_update, packed, stream, u.device)
+    packed, out, d = _update(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, out_dtype, decay, mix, stream)
+    _call(lib.ssm_glr_update, packed, stream, d)
     return out
 
 
@@ -257,13 +267,13 @@ def prepare_glr_update(h, u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=No
     import torch
 
     lib = _b.load_library()
-    packed, out = _update(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, out_dtype, decay, mix, stream)
-    fn, dev = lib.ssm_glr_update, u.device
-    if stream is None and dev.type == "cuda":
-        stream = torch.cuda.current_stream(dev)
+    packed, out, d = _update(h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out, out_dtype, decay, mix, stream)
+    fn = lib.ssm_glr_update
+    if stream is None and d >= 0:
+        stream = torch.cuda.current_stream(d)
 
     def call():
-        _call(fn, packed, stream, dev)
+        _call(fn, packed, stream, d)
         return out
 
     call.keep = (h, u, dt_raw, A, dt_bias, in_raw, in_bias, z, out)
@@ -290,7 +300,7 @@ def ssm_glr_bwd(u, dt_raw, A, dout, *, dt_bias=None, in_raw=None, in_bias=None, 
     _need(dout, u.shape, "dout", u.dtype)
     if dh_last is not None:
         _need(dh_last, (B, D), "dh_last", f32)
-    _one_device(u, dt_raw, A, dout, dt_bias, in_raw, in_bias, z, reset, h0, dh_last, workspace)
+    d = _one_device(u, dt_raw, A, dout, dt_bias, in_raw, in_bias, z, reset, h0, dh_last, workspace)
     gate = in_raw is not None
     g = dict(du=_new(u, gd, stream), d_dt_raw=_new(u, gd, stream), din_raw=_new(u, gd, stream) if gate else None,
              dz=None if z is None else _new(u, gd, stream), dA=_new(A, f32, stream), d_dt_bias=_new(A, f32, stream),
@@ -301,5 +311,5 @@ def ssm_glr_bwd(u, dt_raw, A, dout, *, dt_bias=None, in_raw=None, in_bias=None, 
             *[_at(t) for t in g.values()])
     pack = _PACKED[8].pack
     workspace, at, n = _space(lib.ssm_glr_bwd_workspace_size, pack(*head, 0, 0, *kinds), workspace, dev, stream)
-    _call(lib.ssm_glr_bwd, pack(*head, at, n, *kinds), stream, dev)
+    _call(lib.ssm_glr_bwd, pack(*head, at, n, *kinds), stream, d)
     return g
