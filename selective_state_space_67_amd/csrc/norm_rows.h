@@ -292,11 +292,12 @@ inline int row_parts(const RowGroups& g, int threads, int teams) {
 
 // Workgroups of a backward, each of which leaves a row of sums for the weights: the least whole
 // number for every CU that gives it `per_cu` threads (a part more on some CUs makes the others
-// wait: 4096 rows of 5120 of the block norm 85 us with 256 workgroups, 115 with 307).
+// wait: 4096 rows of 5120 of the block norm 85 us with 256 workgroups, 115 with 307). Few rows:
+// one for 8192 entries or 8 rows (a row after another takes a team 0.6 us and more).
 inline int64_t row_sum_blocks(int64_t groups, int64_t rows, int size, int64_t per_cu) {
   const int64_t threads = size <= 512 ? 256 : (size + 511) / 512 * 64;
   const int64_t most = std::max<int64_t>(1, 256 * ((per_cu + threads - 1) / threads) / groups);
-  const int64_t want = std::min<int64_t>((rows * size + 8191) / 8192, most);
+  const int64_t want = std::min(std::max((rows * size + 8191) / 8192, rows / 8), most);
   return groups * std::max<int64_t>(1, std::min(want, rows));
 }
 
