@@ -127,7 +127,7 @@ ssm_status check_block(const ssm_block_norm_params* p, BlockSizes* s) {
       !span(s->tokens, s->ys, p->dim, &s->y) || s->y > kLim || !mul_ok(p->batch, p->dim, &s->gate) || s->gate > kLim)
     return fail(SSM_ERR_BAD_SHAPE, "element count overflows");
   if (!p->gate_rows) s->gate = p->dim;
-  // a gate for each sequence: a workgroup of up to 1024 threads at least for each
+  // a gate for each sequence: a workgroup of up to 1024 threads at least for each, and one of 1024 for 32 elements of dgate
   if (p->gate_rows && !s->empty() &&
       (!fits_launch(p->batch, 1024) || !fits_launch(p->batch * ((p->dim + 31) / 32), 1024)))
     return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
