@@ -833,6 +833,7 @@ ssm_status ssm_gated_norm_bwd(const ssm_gated_norm_params* p, void* hip_stream);
  *   x        (B,L,D) res_dtype, dense, NULL => 0 (the stream starts here)
  *   w, w_post (D) float32, NULL => 1 (w_post only with post)
  *   gate     float32, NULL => 1: (D), or (B,D) with gate_rows (a gate for each sequence)
+ *            for B below 2^22 (backward: B ceil(D / 32) below 2^22)
  *   out      (B,L,D) dense, out_dtype, required; x_out (B,L,D) dense, res_dtype, NULL =>
  *            not written
  * ssm_block_norm_bwd, gradients of  loss = sum dout * out + sum dx_out * x_out  for the

@@ -127,11 +127,17 @@ ssm_status check_block(const ssm_block_norm_params* p, BlockSizes* s) {
       !span(s->tokens, s->ys, p->dim, &s->y) || s->y > kLim || !mul_ok(p->batch, p->dim, &s->gate) || s->gate > kLim)
     return fail(SSM_ERR_BAD_SHAPE, "element count overflows");
   if (!p->gate_rows) s->gate = p->dim;
-  // a gate for each sequence: a workgroup of up to 1024 threads at least for each, and one of 1024 for 32 elements of dgate
-  if (p->gate_rows && !s->empty() &&
-      (!fits_launch(p->batch, 1024) || !fits_launch(p->batch * ((p->dim + 31) / 32), 1024)))
+  // a gate for each sequence: a workgroup of up to 1024 threads at least for each
+  if (p->gate_rows && !s->empty() && !fits_launch(p->batch, 1024))
     return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
   return SSM_OK;
+}
+
+// dgate's sums over the workgroups' rows: a workgroup of 1024 threads for 32 of its elements.
+ssm_status check_block_bwd(const ssm_block_norm_params* p, BlockSizes* s) {
+  const ssm_status st = check_block(p, s);
+  if (st != SSM_OK || !p->gate_rows || s->empty() || fits_launch(p->batch * ((p->dim + 31) / 32), 1024)) return st;
+  return fail(SSM_ERR_BAD_SHAPE, "problem needs more workgroups than one launch allows");
 }
 
 // Weights and gradients that belong to an option which is off.
@@ -269,7 +275,7 @@ ssm_status ssm_block_norm_fwd(const ssm_block_norm_params* p, void* hip_stream) 
 ssm_status ssm_block_norm_bwd_workspace_size(const ssm_block_norm_params* p, size_t* bytes) {
   if (!p || !bytes) return fail(SSM_ERR_NULL_POINTER, "params or bytes is NULL");
   BlockSizes s;
-  const ssm_status st = check_block(p, &s);
+  const ssm_status st = check_block_bwd(p, &s);
   if (st != SSM_OK) return st;
   *bytes = block_bytes(p, s);
   return ok();
@@ -278,7 +284,7 @@ ssm_status ssm_block_norm_bwd_workspace_size(const ssm_block_norm_params* p, siz
 ssm_status ssm_block_norm_bwd(const ssm_block_norm_params* p, void* hip_stream) {
   if (!p) return fail(SSM_ERR_NULL_POINTER, "params is NULL");
   BlockSizes s;
-  ssm_status st = check_block(p, &s);
+  ssm_status st = check_block_bwd(p, &s);
   if (st != SSM_OK) return st;
   const size_t si = dtype_size(p->in_dtype), so = dtype_size(p->out_dtype), sr = dtype_size(p->res_dtype);
   const size_t ws = block_bytes(p, s);

@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 from test_block_abi_cpu import block
-from test_delta_abi_cpu import SHAPE, lib, refused  # noqa: F401
+from test_delta_abi_cpu import ALIGN, SHAPE, lib, refused  # noqa: F401
 
 
 @pytest.mark.parametrize("batch,dim,status", [(8191, 16384, 0), (8192, 16384, SHAPE), (16383, 8192, 0), (16384, 8192, SHAPE),
@@ -20,3 +20,9 @@ def test_sums_of_many_gates(lib, batch, dim, status):  # noqa: F811
             refused(lib, "ssm_block_norm_bwd", p, SHAPE, "workgroups")
         else:
             assert n.value == 3 * batch * dim * 4
+
+
+@pytest.mark.parametrize("batch,dim,status", [(8192, 16384, ALIGN), ((1 << 22) - 1, 64, ALIGN), (1 << 22, 64, SHAPE)])
+def test_a_forward_is_not_refused_for_sums_that_it_does_not_make(lib, batch, dim, status):  # noqa: F811
+    """(A misaligned pointer stops what passes the checks of sizes, so that nothing runs.)"""
+    refused(lib, "ssm_block_norm_fwd", block(batch=batch, seqlen=1, dim=dim, gate_rows=1, x=0x50000002), status)

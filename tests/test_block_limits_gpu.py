@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from delta_helpers import device
-from test_block_norm_gpu import GRAD, SUM
+from test_block_norm_gpu import FWD, GRAD, SUM
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,23 @@ def test_sums_of_many_gates(B, D, post):
     close(g["dw"], dw, SUM, "dw")
     if post:
         close(g["dw_post"], dwp, SUM, "dw_post")
+
+
+def test_forward_of_more_gates_than_the_backward_sums():
+    import torch
+
+    from selective_state_space_67_amd import ssm_block_norm_fwd
+
+    B, D, dev = 8192, 16384, device()
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(1)
+    y = torch.randn(B, 1, D, generator=gen, device=dev, dtype=torch.bfloat16)
+    gate = torch.randn(B, D, generator=gen, device=dev)
+    print(B, D, flush=True)
+    out, x = ssm_block_norm_fwd(y, None, gate=gate, scale=0.5)
+    torch.cuda.synchronize()
+    for i in range(0, B, 1024):
+        s = 0.5 * gate[i:i + 1024].double() * y[i:i + 1024, 0].double()
+        close(x[i:i + 1024, 0], s, FWD, "x_out of rows from %d" % i)
+        close(out[i:i + 1024, 0], s * torch.rsqrt(s.square().mean(-1, keepdim=True) + float(np.float32(1e-6))), FWD,
+              "out of rows from %d" % i)
