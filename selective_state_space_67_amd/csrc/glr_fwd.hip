@@ -162,11 +162,12 @@ __global__ __launch_bounds__(kLanes) void glr_steps(const GlrArgs g) {
   if (g.h_last && on) g.h_last[state] = h;
 }
 
-// Few workgroups, none of which shares its CU with another, take 16 rows a wave: with half the
-// barriers and folds an element their waves wait less (8 x 2048 x 1536 channels, 192 workgroups:
-// 65 us, with 8 rows 71; with 16 waves of 16 rows 63). Many take 8, and so does what 8 rows a
-// wave cover in a few tiles: 1 x 37 x 1536 4.8 us, with 16 rows 6.7.
-bool wide_tiles(int64_t blocks, int64_t rows) { return blocks <= 384 && rows >= 8 * kTile; }
+// Up to 256 workgroups, one on a CU, take 16 rows a wave: with half the barriers and folds an
+// element their waves wait less (8 x 2048 x 1536 channels, 192 workgroups: 65 us, with 8 rows 71;
+// with 16 waves of 16 rows 63). More of them take 8 (of the sequences that long, plan_glr leaves
+// the walk those of more than 400 workgroups), and so does what 8 rows a wave cover in a few
+// tiles: 1 x 37 x 1536 4.8 us, with 16 rows 6.7.
+bool wide_tiles(int64_t blocks, int64_t rows) { return blocks <= 256 && rows >= 8 * kTile; }
 
 struct Walk {
   template <typename InT, int DECAY, int MIX, bool IN, bool Z>
