@@ -63,8 +63,14 @@ __global__ __launch_bounds__(kLanes * W) void glr_grads(const GlrArgs g) {
   const Channel<DECAY> chn(g, ch);
   const uint32_t cuts = static_cast<uint32_t>(__builtin_amdgcn_ballot_w64(reset != 0));
 
-  float a[K], c[K], x[K], i[K], s[K], dy[K], b[K];  // x = i u, b = c x
-  decays<InT, DECAY, MIX, K>(chn, rdt, s, a, c);
+  float a[K], c[K], s[K], e[K], dy[K], b[K];  // b = c i u
+  decays<InT, DECAY, MIX, K>(chn, rdt, s, e, a, c);
+  // s' = s (1 - s). Of the two factors the smaller one is kept, which gives the other one and the
+  // product to full precision: s up to 1/2, else 1 - s with its sign turned.
+  if (DECAY == kGlrSigmoid) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k] = s[k] > 0.5f ? -(e[k] * s[k]) : s[k];
+  }
   const bool plain = rows == K && cuts == 0;
   if (cuts) {
     keep_branch();
@@ -72,15 +78,23 @@ __global__ __launch_bounds__(kLanes * W) void glr_grads(const GlrArgs g) {
     for (int k = 0; k < K; ++k)
       if ((cuts >> k) & 1) c[k] = 1.0f;
   }
+  // what the adjoint is multiplied by: c i for du, b (1 - i) for d in_raw, A s' for d dt_raw, and i u dc/da
+  float ci[K], in_slope[K], xdc[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    x[k] = widen<InT>(ru[k]);
-    i[k] = 1.0f;
+    float x = widen<InT>(ru[k]), i_rest = 0.0f;
+    ci[k] = c[k];
     if (IN) {
-      i[k] = biased_sigmoid(widen<InT>(rin[k]), chn.in);
-      x[k] *= i[k];
+      const Sigmoid i(__builtin_fmaf(widen<InT>(rin[k]), -kLog2e, chn.in));
+      i_rest = fminf(i.e, 3.4e38f) * i.value;
+      x *= i.value;
+      ci[k] = MIX == kGlrOne ? i.value : c[k] * i.value;
     }
-    b[k] = MIX == kGlrOne ? x[k] : c[k] * x[k];
+    b[k] = MIX == kGlrOne ? x : c[k] * x;
+    if (IN) in_slope[k] = b[k] * i_rest;
+    // where a rounds to 1, c is 0 and its slope infinite, but what the gate and A get tends to 0
+    if (MIX == kGlrUnit) xdc[k] = c[k] == 0.0f ? 0.0f : -a[k] * fast_rcp(c[k]) * x;
+    if (MIX == kGlrRest) xdc[k] = -x;
     dy[k] = Z ? widen<InT>(rdy[k]) * silu_f32(widen<InT>(rz[k])) : widen<InT>(rdy[k]);
   }
   float P = 1.0f, H = 0.0f, G = 0.0f;
@@ -110,34 +124,35 @@ __global__ __launch_bounds__(kLanes * W) void glr_grads(const GlrArgs g) {
       }
     }
     if (Z && on) store_rows<PLAIN, K>(g.dz, row, g.D, rows, ch, g.out_bf16, b);
-    float d_in[K];
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
       if (!PLAIN && k >= rows) continue;
-      const float lam = dy[k] + m, lc = MIX == kGlrOne ? lam : lam * c[k];
-      b[k] = IN ? lc * i[k] : lc;  // du
+      const float lam = dy[k] + m;
+      b[k] = lam * ci[k];  // du
       if (IN) {
-        d_in[k] = lc * x[k] * (1.0f - i[k]);
-        sum_in += d_in[k];
+        in_slope[k] *= lam;  // d in_raw
+        sum_in += in_slope[k];
       }
       if (!PLAIN && ((cuts >> k) & 1)) {
         m = dy[k] = 0.0f;
         continue;
       }
       m = a[k] * lam;
-      // where a rounds to 1, c is 0 and its slope infinite, but what the gate and A get tends to 0
-      float dc = 0.0f;
-      if (MIX == kGlrUnit) dc = c[k] == 0.0f ? 0.0f : -a[k] * fast_rcp(c[k]);
-      if (MIX == kGlrRest) dc = -1.0f;
-      const float dg = m * (MIX == kGlrOne ? before[k] : __builtin_fmaf(x[k], dc, before[k]));
-      sum_A = __builtin_fmaf(dg, s[k], sum_A);
-      const float slope = DECAY == kGlrSigmoid ? s[k] * (1.0f - s[k]) : sigmoid_f32(widen<InT>(rdt[k]) + chn.dt);
+      const float dg = m * (MIX == kGlrOne ? before[k] : before[k] + xdc[k]);
+      float gate = s[k], slope;
+      if (DECAY == kGlrSigmoid) {
+        gate = __float_as_int(s[k]) < 0 ? 1.0f + s[k] : s[k];
+        slope = __builtin_fmaf(-fabsf(s[k]), fabsf(s[k]), fabsf(s[k]));
+      } else {
+        slope = sigmoid_f32(widen<InT>(rdt[k]) + chn.dt);
+      }
+      sum_A = __builtin_fmaf(dg, gate, sum_A);
       dy[k] = dg * chn.A * slope;  // d dt_raw
       sum_dt += dy[k];
     }
     if (on) {
       store_rows<PLAIN, K>(g.du, row, g.D, rows, ch, g.out_bf16, b);
-      if (IN) store_rows<PLAIN, K>(g.d_in, row, g.D, rows, ch, g.out_bf16, d_in);
+      if (IN) store_rows<PLAIN, K>(g.d_in, row, g.D, rows, ch, g.out_bf16, in_slope);
       store_rows<PLAIN, K>(g.d_dt, row, g.D, rows, ch, g.out_bf16, dy);
     }
   };

@@ -158,9 +158,21 @@ __device__ __forceinline__ float biased_sigmoid(float x, float bias) {
   return fast_rcp(1.0f + fast_exp2(__builtin_fmaf(x, -kLog2e, bias)));
 }
 
+// sigmoid(x) from -x log2 e, and e^-x. 1 - sigmoid(x) is their product, which keeps its digits where
+// the sigmoid is near 1: taken from the rounded sigmoid it would be off by up to 2^-25, all of it from
+// x = 17 on. (An infinite e^-x belongs to a sigmoid of 0.)
+struct Sigmoid {
+  float e, value;
+  __device__ __forceinline__ explicit Sigmoid(float x) : e(fast_exp2(x)), value(fast_rcp(1.0f + e)) {}
+};
+
+// The gate s, and (sigmoid) the e that makes e s = 1 - s.
 template <int DECAY>
-__device__ __forceinline__ float decay_gate(float raw, const Channel<DECAY>& c) {
-  return DECAY == kGlrSigmoid ? biased_sigmoid(raw, c.dt) : softplus_f32(raw + c.dt);
+__device__ __forceinline__ float decay_gate(float raw, const Channel<DECAY>& c, float& e) {
+  if (DECAY == kGlrSoftplus) return softplus_f32(raw + c.dt);
+  const Sigmoid s(__builtin_fmaf(raw, -kLog2e, c.dt));
+  e = s.e;
+  return s.value;
 }
 
 // a = e^g and c. Near g = 0, where long memories live, 1 - a comes from the series of
@@ -190,10 +202,10 @@ __device__ __forceinline__ void decay_terms(float g, float& a, float& c) {
 // Gate, decay and multiplier of K rows. Whether the exponential is needed at all is the same
 // for the wave: from its channels' A, or (softplus) from these rows' largest |g|.
 template <typename T, int DECAY, int MIX, int K>
-__device__ __forceinline__ void decays(const Channel<DECAY>& ch, const uint32_t (&dt)[K], float (&s)[K], float (&a)[K],
-                                       float (&c)[K]) {
+__device__ __forceinline__ void decays(const Channel<DECAY>& ch, const uint32_t (&dt)[K], float (&s)[K], float (&e)[K],
+                                       float (&a)[K], float (&c)[K]) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) s[k] = decay_gate<DECAY>(widen<T>(dt[k]), ch);
+  for (int k = 0; k < K; ++k) s[k] = decay_gate<DECAY>(widen<T>(dt[k]), ch, e[k]);
   bool far = ch.far;
   if (DECAY == kGlrSoftplus) {
     float most = 0.0f;
@@ -214,8 +226,8 @@ __device__ __forceinline__ void decays(const Channel<DECAY>& ch, const uint32_t 
 template <typename T, int DECAY, int MIX, bool IN, int K>
 __device__ __forceinline__ void terms(const Channel<DECAY>& ch, const uint32_t (&u)[K], const uint32_t (&dt)[K],
                                       const uint32_t (&in)[K], uint32_t cuts, float (&a)[K], float (&b)[K]) {
-  float s[K], c[K];
-  decays<T, DECAY, MIX, K>(ch, dt, s, a, c);
+  float s[K], e[K], c[K];
+  decays<T, DECAY, MIX, K>(ch, dt, s, e, a, c);
 #pragma unroll
   for (int k = 0; k < K; ++k) b[k] = IN ? widen<T>(u[k]) * biased_sigmoid(widen<T>(in[k]), ch.in) : widen<T>(u[k]);
   if (MIX == kGlrOne) return;
