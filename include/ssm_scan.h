@@ -669,14 +669,20 @@ ssm_status ssm_qk_norm_bwd(const ssm_qk_norm_params* p, void* hip_stream);
  *            2^24; 0 = D), with batch rows L tokens apart, so slices of one packed
  *            projection can be passed as they lie.
  *   A        (D) float32, required. Any real value is accepted by SSM_GLR_REST and
- *            SSM_GLR_ONE; a_t above 1 (A > 0) makes SSM_GLR_UNIT's root NaN.
+ *            SSM_GLR_ONE, where a_t above 1 (A > 0) makes a state grow: sequences go in runs of
+ *            up to some 16384 steps, and where the product of a run's decays passes float32's
+ *            largest value, a state or adjoint that enters the run leaves it infinite, or NaN if
+ *            it was 0. With SSM_GLR_UNIT a_t above 1 makes the root NaN.
  *   dt_bias, in_bias (D) float32, NULL => 0 (in_bias only with in_raw)
  *   reset    (B,L) uint8, NULL => none; h0 (B,D) float32, NULL => 0
  * ssm_glr_fwd:
  *   out      (B,L,D) required, dense, out_dtype; h_last (B,D) float32, NULL => not written
  *   workspace, workspace_bytes : at least ssm_glr_workspace_size() bytes, aligned to
  *            256 (none where batch rows and channels fill the device by themselves);
- *            contents on entry ignored. Calls that may run at the same time need one each.
+ *            contents on entry ignored. Calls that may run at the same time need one each:
+ *            where something else writes the workspace while a call runs, its waits still
+ *            end (after 2^20 looks each), its results are then NaN or wrong, and no error
+ *            is reported.
  * ssm_glr_bwd, gradients of  loss = sum dout * out + sum dh_last * h_last  for the
  * same inputs (no intermediate of the forward is needed). With lam_t the adjoint of h_t:
  *   dy = dout silu(z),  dz = dout h silu'(z),  lam_t = dy_t + a_{t+1} lam_{t+1}
@@ -786,7 +792,8 @@ ssm_status ssm_glr_update(const ssm_glr_update_params* p, void* hip_stream);
  *   dw       as w, float32, NULL => not written: a sum in a fixed order
  *   workspace, workspace_bytes : at least ssm_gated_norm_bwd_workspace_size() bytes,
  *            aligned to 16 (the forward needs none)
- * Sums and factors are float32; only results are rounded.
+ * Sums and factors are float32; only results are rounded. Outputs must not overlap inputs,
+ * each other or the workspace.
  */
 #define SSM_MAX_NORM_DIM 16384
 
@@ -844,7 +851,8 @@ ssm_status ssm_gated_norm_bwd(const ssm_gated_norm_params* p, void* hip_stream);
  *            dgate only with gate): sums in a fixed order
  *   workspace, workspace_bytes : at least ssm_block_norm_bwd_workspace_size() bytes,
  *            aligned to 16 (the forward needs none)
- * Sums and factors are float32; only results are rounded.
+ * Sums and factors are float32; only results are rounded. Outputs must not overlap inputs,
+ * each other or the workspace.
  */
 typedef struct {
   int64_t batch, seqlen, dim;

@@ -12,8 +12,8 @@
 // and written once, so memory bounds both: 8192 rows of 2560, bfloat16 with a float32
 // stream, 45.8 us for 252 MB, 5.5 TB/s (x' partly stays in the last-level cache; a large
 // copy reaches 5.2), backward 74.5 us for 377 MB, 5.1, and 4.8 for the sums. Rows above
-// 8192 entries outgrow the backward's registers (250 to 365 us for as many elements), odd
-// ones above 4096 take 120 to 196. out is the norm of x' before x' is
+// 8192 entries outgrow the backward's registers: 206 to 286 us for as many elements, odd ones
+// 377 to 699; of odd ones above 4096 it takes 120 to 196, with a bfloat16 stream 166 to 277. out is the norm of x' before x' is
 // rounded to the residual stream's type, and the backward works x' out again from
 // x and y, so that neither sees that rounding.
 #include <utility>

@@ -11,8 +11,8 @@
 // One barrier a tile; the next tile's rows are loaded meanwhile. An element is
 // read once and written once. What bounds it is the tile's chain of dependent steps
 // (decays, recurrence, barrier, fold, recurrence) on the CUs that have a workgroup:
-// 64 channels go 30 ns a row, 8 x 2048 x 2048 channels (256 workgroups) 68.5 us, 3.9 of
-// the 5.2 TB/s of a large copy; 1 x 37 x 1536 4.6 us.
+// 64 channels go 30 ns a row, 8 x 2048 x 2048 channels (256 workgroups) 69 us, 3.9 of
+// the 5.2 TB/s of a large copy; 1 x 37 x 1536 4.7 us.
 #include "glr_device.h"
 #include "glr_launch.h"
 
@@ -207,11 +207,14 @@ bool glr_steps_fit(int64_t B, int64_t D) { return fits_launch(B * tiles_of(D), k
 
 // The walk gives 64 channels of a batch row to one workgroup, in rounds of one for every CU: 30 ns a
 // row and round, however little of the chip a round fills. The chain fills it whatever the shape
-// is (0.119 ns a row and 64 channels), for a launch and a workspace more. It is taken where that
-// saves 7 us. us of walk and chain, bfloat16 with the sigmoid gates: 1 x 256 x 256 channels 14.0 and
-// 18.3, 1 x 2048 x 1536 65 (by its 30 ns a row) and 18.7, 2 x 4096 x 2048 121 and 41; 8 x 512 x 1536 18.8
-// and 20.5, 8 x 1024 x 1536 34.7 and 32.5, 8 x 2048 x 1536 64.4 and 55.8; 8 x 2048 x 2048 (256
-// workgroups) 68.5 and 71.5; 16 x 2048 x 1280 (320) 121 and 85; 16 x 1024 x 2048 (512) 68.6 and 75.6.
+// is (0.119 ns a row and 64 channels), but has some 5 us more that do not depend on the shape: a clearing
+// launch, tickets, looks. It is taken where the two figures are 7 us apart. us of walk and chain by
+// themselves (the launches of a graph; bfloat16, sigmoid gates): 1 x 256 x 256 channels 10.0 and 7.7,
+// 1 x 2048 x 1536 57 and 13.6, 2 x 4096 x 2048 118 and 43; 8 x 512 x 1536 17.6 and 18.9, 8 x 1024 x 1536
+// 31.5 and 28.7, 8 x 2048 x 1536 65 and 57; 8 x 2048 x 2048 (256 workgroups) 70 and 72; 16 x 2048 x 1280
+// (320) 121 and 87; 16 x 1024 x 2048 (512) 67 and 73. Up to some 400 rows the host is slower than either
+// where one call follows another, and the chain with its workspace takes it 4 us more: 1 x 256 x 256 12.1
+// and 16.8 us a call, 1 x 400 x 256 16.1 and 16.3; a call that is waited for 28.3 and 28.4, 34.5 and 28.9.
 GlrPieces plan_glr(int64_t B, int64_t L, int64_t D) {
   const int64_t groups = B * tiles_of(D), rounds = (groups + 255) / 256;
   if (groups < int64_t{1} << 22 && (30000 * rounds - 119 * groups) * L >= 7000000) {

@@ -6,8 +6,10 @@
 // from behind to P m + G, with P the product of its decays and
 //   H = the state it leaves from zero,   G = sum_t (prod_{r <= t} a_r) dout_t silu(z_t)
 // A workgroup makes a piece's three values for 64 channels, each of its waves those of
-// 8 rows: 8 x 2048 x 1536 channels 48.5 us for 201 MB, 4.1 TB/s, which is what reading
-// alone reaches here. The fold runs the same scheme over the pieces that the walk runs
+// 8 rows: 8 x 2048 x 1536 channels 48.8 us for 201 MB, 4.1 TB/s. Reading them alone takes
+// 37 us (5.5 TB/s) by the same loads of two bytes a lane as by those of 16; the rest is the
+// gates and the recurrence on top (278 vector instructions a wave, the ALU busy for half of
+// the time), which a workgroup begins when its loads are there, and after which it ends. The fold runs the same scheme over the pieces that the walk runs
 // over rows. A workgroup of it gets through 128 pieces in 2.7 us, which is what its CU
 // draws from memory; many pieces (plan_glr_bwd) go in segments, first for what each
 // segment does, and again once the states and adjoints at its ends are known.
