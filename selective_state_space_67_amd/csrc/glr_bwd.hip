@@ -18,8 +18,8 @@
 // are summed over a wave's rows in registers, over the waves in LDS, and over the
 // pieces by row_sums, always in the same order.
 //
-// Bound by memory, the vector ALU close behind: 8 x 2048 x 1536 channels 73 to 77 us for 352 MB
-// (4.6 to 4.8 TB/s), 70 vector instructions an element, the ALU busy for 64% of the time. Two passes over the inputs are the price of a
+// Bound by memory, the vector ALU close behind: 8 x 2048 x 1536 channels 73 to 79 us for 352 MB
+// (4.5 to 4.8 TB/s), 70 vector instructions an element, the ALU busy for 64% of the time. Two passes over the inputs are the price of a
 // state that comes from the front and an adjoint that comes from behind. With a first pass
 // for the adjoints alone and this one getting its states from a chain of workgroups (as in
 // glr_chain.hip), u and in_raw are read only once, but this pass then waits: 29 and 95 us
