@@ -263,7 +263,7 @@ def ssm_glr_update(h, u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=None, 
 def prepare_glr_update(h, u, dt_raw, A, *, dt_bias=None, in_raw=None, in_bias=None, z=None, out=None, out_dtype=None,
                        decay="sigmoid", mix="unit", stream=None):
     """Marshal the arguments of ssm_glr_update once; returns a no-argument callable
-    that enqueues the same window again (updating h every time)."""
+    that enqueues the same window again on the same stream (updating h every time)."""
     import torch
 
     lib = _b.load_library()
